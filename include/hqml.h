@@ -187,11 +187,127 @@ int hqml_train_step_f64(hqml_ctx *ctx, int B, const double *x, const double *the
 int hqml_train_step_noalloc(const hqml_config *cfg, int B, const float *x, const float *theta,
                             const float *y, float *expz, float *loss, float *grad);
 
+/* ---- dense layers and their optimiser, around the circuits ----
+ *
+ * A dense layer maps a sample's features to encoding angles in front of a circuit, or
+ * reads expectation values out behind it; hqml_adamw_step updates circuit angles and
+ * dense weights together.  The conventions at the top hold here too, with row strides
+ * where an argument has one, and every call leaves the calling thread's current HIP device
+ * as it was. */
+
+typedef enum {
+    HQML_DTYPE_FP32 = 0,
+    HQML_DTYPE_BF16 = 1,
+    HQML_DTYPE_FP64 = 2         /* hqml_adamw_step only */
+} hqml_dtype;
+
+typedef enum {
+    HQML_ACT_NONE = 0,          /* z */
+    HQML_ACT_RELU = 1,          /* z < 0 ? 0 : z; slope 0 at 0 */
+    HQML_ACT_GELU = 2,          /* z Phi(z), Phi the normal distribution function (by erf) */
+    HQML_ACT_SILU = 3,          /* z / (1 + exp(-z)) */
+    HQML_ACT_TANH = 4,
+    HQML_ACT_SIGMOID = 5        /* 1 / (1 + exp(-z)); alpha = pi gives encoding angles */
+} hqml_activation;
+
+/* Largest in_features, out_features and row stride (elements), and largest batch. */
+#define HQML_DENSE_MAX_FEATURES (1 << 20)
+#define HQML_DENSE_MAX_BATCH (1 << 24)
+
+typedef struct hqml_dense hqml_dense;
+
+typedef struct {
+    int in_features;   /* K, 1..HQML_DENSE_MAX_FEATURES */
+    int out_features;  /* N, 1..HQML_DENSE_MAX_FEATURES */
+    int max_batch;     /* 1..HQML_DENSE_MAX_BATCH: the largest M of a call */
+    int dtype;         /* hqml_dtype of every array: HQML_DTYPE_FP32 or HQML_DTYPE_BF16 */
+    int activation;    /* hqml_activation */
+    float alpha;       /* finite factor of the activation */
+    int device;        /* HIP device ordinal */
+    void *stream;      /* hipStream_t to queue work on; NULL = the null stream */
+} hqml_dense_config;
+
+/* Device bytes hqml_dense_create reserves for cfg (partial products and row sums; the
+ * gradient at z).  Host-only.  Returns 0 for an invalid cfg. */
+size_t hqml_dense_workspace_bytes(const hqml_dense_config *cfg);
+
+/* Validate cfg, reserve the workspace and return a handle in *out.  Nothing is allocated
+ * later, and a handle keeps nothing of a call for the next.  Errors: hqml_last_error(NULL). */
+int hqml_dense_create(const hqml_dense_config *cfg, hqml_dense **out);
+
+/* Release the handle and its workspace (waits for its stream).  NULL is a no-op. */
+int hqml_dense_destroy(hqml_dense *h);
+
+/* Text of the last error on h ("" if none). */
+const char *hqml_dense_last_error(const hqml_dense *h);
+
+/* z = x w^T + bias, y = alpha act(z) + residual for a batch of M rows (0 <= M <= max_batch;
+ * M == 0 queues nothing).  x [M][K], w [N][K], residual and y [M][N] with row strides ldx,
+ * ldw, ldr, ldy in elements (at least the row's length); bias [N]; z [M][N] without gaps.
+ * bias, residual and z may be NULL; z is what hqml_dense_backward needs, rounded to dtype
+ * (with HQML_ACT_NONE it is not needed and not written).  y may be the residual itself
+ * (same stride); otherwise outputs overlap no other argument.  Sums are held in fp32; with
+ * HQML_DTYPE_BF16 y and z are rounded once, to nearest even. */
+int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw,
+                       const void *bias, const void *residual, long long ldr, void *y, long long ldy,
+                       void *z);
+
+/* Gradients of a forward call for dy = dL/dy [M][N] (row stride lddy):
+ * dz = alpha act'(z) dy, dx = dz w [M][K] (row stride lddx), dw = dz^T x [N][K],
+ * db = sum over rows of dz [N]; the residual's gradient is dy itself.  dw and db have no
+ * gaps.  Each of dx, dw, db may be NULL (not formed).  z is the forward call's (ignored with
+ * HQML_ACT_NONE).  M == 0 writes zeros to dw and db. */
+int hqml_dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx,
+                        const void *w, long long ldw, const void *z, void *dx, long long lddx, void *dw,
+                        void *db);
+
+/* How the moments of hqml_adamw_step are held. */
+typedef enum {
+    HQML_MOMENTS_32 = 0,        /* m and v in fp32 (fp64 for fp64 parameters) */
+    HQML_MOMENTS_8 = 1          /* m and sqrt(v), each as OCP e4m3 codes [numel] times one fp32
+                                   scale per HQML_ADAMW_BLOCK elements
+                                   [ceil(numel / HQML_ADAMW_BLOCK)].  scale = max(largest
+                                   magnitude of the block / 448, 2^-100); the code is the nearest
+                                   to x / scale (ties to even), at least the smallest one, 2^-9,
+                                   for x != 0: a root that became 0 under a moment that did not
+                                   would divide by eps.  A NaN or infinite gradient makes its
+                                   whole block's moments NaN.  fp32 and bf16 parameters */
+} hqml_moments;
+#define HQML_ADAMW_BLOCK 256
+
+typedef struct {
+    void *param;            /* [numel], updated */
+    const void *grad;       /* [numel] */
+    void *m;                /* [numel] first moment, updated */
+    void *v;                /* [numel] second moment (HQML_MOMENTS_8: its root), updated */
+    float *m_scale;         /* HQML_MOMENTS_8 only: scales, updated */
+    float *v_scale;
+    long long numel;        /* >= 0; 0 skips the tensor */
+} hqml_adamw_tensor;
+
+typedef struct {
+    int param_dtype;   /* hqml_dtype of param */
+    int grad_dtype;    /* hqml_dtype of grad: param_dtype, or fp32 and bf16 mixed */
+    int moments;       /* hqml_moments */
+    long long step;    /* number of this step, from 1 */
+    double lr, beta1, beta2, eps, weight_decay;   /* lr, eps, weight_decay >= 0; betas in [0, 1) */
+    int device;
+    void *stream;
+} hqml_adamw_config;
+
+/* One AdamW step (decoupled weight decay) over n_tensors tensors:
+ *   m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = p (1 - lr weight_decay) - (m / (sqrt(v) / sqrt(1 - beta2^step) + eps)) lr / (1 - beta1^step)
+ * in fp32 (fp64 for fp64 parameters); bf16 parameters are rounded once, to nearest even.
+ * Tensors must not overlap.  The step number is a host value, so a stream under graph capture
+ * is refused (HQML_ERR_UNSUPPORTED).  Errors: hqml_last_error(NULL). */
+int hqml_adamw_step(const hqml_adamw_config *cfg, int n_tensors, const hqml_adamw_tensor *tensors);
+
 /* Static text for a status code. */
 const char *hqml_status_str(int status);
 
 /* Text of the last error on ctx ("" if none); with ctx == NULL, the last error of
- * hqml_create or hqml_train_step_noalloc on this thread. */
+ * hqml_create, hqml_train_step_noalloc, hqml_dense_create or hqml_adamw_step on this thread. */
 const char *hqml_last_error(const hqml_ctx *ctx);
 
 /* ---- instrumentation (benchmarking; not needed for training) ---- */

@@ -30,6 +30,13 @@ HQML_FUSED = 0
 HQML_GATE_BY_GATE = 1
 HQML_ENT_CZ = 0
 HQML_ENT_CNOT = 1
+HQML_DTYPE_FP32, HQML_DTYPE_BF16, HQML_DTYPE_FP64 = range(3)
+HQML_ACT_NONE, HQML_ACT_RELU, HQML_ACT_GELU, HQML_ACT_SILU, HQML_ACT_TANH, HQML_ACT_SIGMOID = range(6)
+HQML_DENSE_MAX_FEATURES = 1 << 20
+HQML_DENSE_MAX_BATCH = 1 << 24
+HQML_MOMENTS_32 = 0
+HQML_MOMENTS_8 = 1
+HQML_ADAMW_BLOCK = 256
 HQML_K_FWD_PASS, HQML_K_BWD_PASS, HQML_K_SMALL, HQML_K_OTHER, HQML_K_GATE, HQML_K_COUNT = range(6)
 
 
@@ -47,6 +54,47 @@ class hqml_config(ctypes.Structure):
         ("obs_mask", ctypes.c_int),
         ("obs_x_mask", ctypes.c_int),
         ("entangler", ctypes.c_int),
+    ]
+
+
+class hqml_dense_config(ctypes.Structure):
+    _fields_ = [
+        ("in_features", ctypes.c_int),
+        ("out_features", ctypes.c_int),
+        ("max_batch", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("activation", ctypes.c_int),
+        ("alpha", ctypes.c_float),
+        ("device", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class hqml_adamw_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("m", ctypes.c_void_p),
+        ("v", ctypes.c_void_p),
+        ("m_scale", ctypes.c_void_p),
+        ("v_scale", ctypes.c_void_p),
+        ("numel", ctypes.c_longlong),
+    ]
+
+
+class hqml_adamw_config(ctypes.Structure):
+    _fields_ = [
+        ("param_dtype", ctypes.c_int),
+        ("grad_dtype", ctypes.c_int),
+        ("moments", ctypes.c_int),
+        ("step", ctypes.c_longlong),
+        ("lr", ctypes.c_double),
+        ("beta1", ctypes.c_double),
+        ("beta2", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("device", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
     ]
 
 
@@ -70,7 +118,9 @@ def load() -> ctypes.CDLL:
     lib = ctypes.CDLL(LIB_PATH)
     P = ctypes.c_void_p
     i = ctypes.c_int
+    ll = ctypes.c_longlong
     cfgp = ctypes.POINTER(hqml_config)
+    densep = ctypes.POINTER(hqml_dense_config)
     sig = {
         "hqml_workspace_bytes": (ctypes.c_size_t, [cfgp]),
         "hqml_create": (i, [cfgp, ctypes.POINTER(P)]),
@@ -90,6 +140,13 @@ def load() -> ctypes.CDLL:
                               ctypes.POINTER(ctypes.c_size_t)]),
         "hqml_describe_plan": (ctypes.c_longlong, [cfgp, ctypes.c_char_p, ctypes.c_size_t]),
         "hqml_train_step_noalloc": (i, [cfgp, i, P, P, P, P, P, P]),
+        "hqml_dense_workspace_bytes": (ctypes.c_size_t, [densep]),
+        "hqml_dense_create": (i, [densep, ctypes.POINTER(P)]),
+        "hqml_dense_destroy": (i, [P]),
+        "hqml_dense_last_error": (ctypes.c_char_p, [P]),
+        "hqml_dense_forward": (i, [P, i, P, ll, P, ll, P, P, ll, P, ll, P]),
+        "hqml_dense_backward": (i, [P, i, P, ll, P, ll, P, ll, P, P, ll, P, P]),
+        "hqml_adamw_step": (i, [ctypes.POINTER(hqml_adamw_config), i, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -102,7 +159,8 @@ def load() -> ctypes.CDLL:
 EXPORTED = ("hqml_workspace_bytes", "hqml_create", "hqml_destroy", "hqml_forward", "hqml_backward",
             "hqml_train_step", "hqml_forward_f64", "hqml_backward_f64", "hqml_train_step_f64", "hqml_status_str", "hqml_last_error", "hqml_set_timing",
             "hqml_set_overlap", "hqml_kernel_times", "hqml_plan_info", "hqml_describe_plan",
-            "hqml_train_step_noalloc")
+            "hqml_train_step_noalloc", "hqml_dense_workspace_bytes", "hqml_dense_create", "hqml_dense_destroy",
+            "hqml_dense_last_error", "hqml_dense_forward", "hqml_dense_backward", "hqml_adamw_step")
 
 
 def make_config(n_qubits, n_layers, max_batch, storage="fp32", ckpt_block=0, device=0, stream=None,
@@ -114,6 +172,18 @@ def make_config(n_qubits, n_layers, max_batch, storage="fp32", ckpt_block=0, dev
     return hqml_config(int(n_qubits), int(n_layers), int(max_batch), int(st), int(ckpt_block),
                        int(device), ctypes.c_void_p(stream or 0), int(fu), int(co), int(obs_mask),
                        int(obs_x_mask), int(en))
+
+
+DENSE_DTYPES = {"fp32": HQML_DTYPE_FP32, "bf16": HQML_DTYPE_BF16}
+ACTIVATIONS = {"none": HQML_ACT_NONE, "relu": HQML_ACT_RELU, "gelu": HQML_ACT_GELU, "silu": HQML_ACT_SILU,
+               "tanh": HQML_ACT_TANH, "sigmoid": HQML_ACT_SIGMOID}
+
+
+def make_dense_config(in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0, device=0,
+                      stream=None):
+    return hqml_dense_config(int(in_features), int(out_features), int(max_batch), int(DENSE_DTYPES.get(dtype, dtype)),
+                             int(ACTIVATIONS.get(activation, activation)), float(alpha), int(device),
+                             ctypes.c_void_p(stream or 0))
 
 
 # ---- the C entry points, same names, argument marshalling only ----
@@ -177,6 +247,47 @@ def hqml_train_step_f64(ctx, B, x_ptr, theta_ptr, y_ptr, expz_ptr, loss_ptr, gra
 def hqml_train_step_noalloc(cfg: hqml_config, B, x_ptr, theta_ptr, y_ptr, expz_ptr, loss_ptr, grad_ptr) -> None:
     lib = load()
     rc = lib.hqml_train_step_noalloc(ctypes.byref(cfg), int(B), x_ptr, theta_ptr, y_ptr, expz_ptr, loss_ptr, grad_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, lib.hqml_last_error(None).decode())
+
+
+def hqml_dense_workspace_bytes(cfg: hqml_dense_config) -> int:
+    return int(load().hqml_dense_workspace_bytes(ctypes.byref(cfg)))
+
+
+def hqml_dense_create(cfg: hqml_dense_config) -> ctypes.c_void_p:
+    lib = load()
+    h = ctypes.c_void_p()
+    rc = lib.hqml_dense_create(ctypes.byref(cfg), ctypes.byref(h))
+    if rc != HQML_OK:
+        raise HqmlError(rc, lib.hqml_last_error(None).decode())
+    return h
+
+
+def hqml_dense_destroy(h) -> None:
+    load().hqml_dense_destroy(h)
+
+
+def hqml_dense_last_error(h) -> str:
+    return load().hqml_dense_last_error(h).decode()
+
+
+def hqml_dense_forward(h, M, x_ptr, ldx, w_ptr, ldw, bias_ptr, residual_ptr, ldr, y_ptr, ldy, z_ptr) -> None:
+    rc = load().hqml_dense_forward(h, M, x_ptr, ldx, w_ptr, ldw, bias_ptr, residual_ptr, ldr, y_ptr, ldy, z_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, hqml_dense_last_error(h))
+
+
+def hqml_dense_backward(h, M, dy_ptr, lddy, x_ptr, ldx, w_ptr, ldw, z_ptr, dx_ptr, lddx, dw_ptr, db_ptr) -> None:
+    rc = load().hqml_dense_backward(h, M, dy_ptr, lddy, x_ptr, ldx, w_ptr, ldw, z_ptr, dx_ptr, lddx, dw_ptr, db_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, hqml_dense_last_error(h))
+
+
+def hqml_adamw_step(cfg: hqml_adamw_config, n_tensors, tensors) -> None:
+    """tensors: a ctypes array of hqml_adamw_tensor, or of as many 64-bit words."""
+    lib = load()
+    rc = lib.hqml_adamw_step(ctypes.byref(cfg), int(n_tensors), tensors)
     if rc != HQML_OK:
         raise HqmlError(rc, lib.hqml_last_error(None).decode())
 
@@ -296,3 +407,123 @@ class Context:
 
     def plan_info(self):
         return hqml_plan_info(self.handle)
+
+
+class Dense:
+    """One dense layer's handle: y = alpha act(x w^T + bias) + residual and its gradients.
+
+    Tensors are torch CUDA tensors of the handle's device and dtype ("fp32" or "bf16"):
+    x [M][in_features], w [out_features][in_features], bias [out_features], residual and y
+    [M][out_features], M <= max_batch.  Rows may be strided (a slice of columns is used in
+    place); other layouts are copied.  Work is queued on the stream the handle was made on (or
+    `stream`); a call from another current stream waits for that one and is waited for by it.
+    """
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0,
+                 device=None, stream=None):
+        import torch
+        if not torch.cuda.is_available():
+            raise RuntimeError("hqml needs a GPU (torch.cuda.is_available() is False)")
+        dev = torch.cuda.current_device() if device is None else int(device)
+        self.torch = torch
+        self.device = torch.device("cuda", dev)
+        self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream)
+        self.K, self.N, self.max_batch = int(in_features), int(out_features), int(max_batch)
+        self.cfg = make_dense_config(in_features, out_features, max_batch, dtype, activation, alpha, dev, self.stream)
+        self.dtype = torch.bfloat16 if self.cfg.dtype == HQML_DTYPE_BF16 else torch.float32
+        self.plain = self.cfg.activation == HQML_ACT_NONE   # the gradient needs no z
+        self._current_stream = torch._C._cuda_getCurrentRawStream
+        self.handle = None
+        self.handle = hqml_dense_create(self.cfg)
+
+    def close(self):
+        if self.handle is not None:
+            hqml_dense_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+    def _check(self, t, shape, name):
+        if t.dtype is not self.dtype or t.device != self.device:
+            raise TypeError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
+        if tuple(t.shape) != shape:
+            raise ValueError(f"expected shape {shape} for {name}, got {tuple(t.shape)}")
+
+    def _rows(self, t, shape, name):
+        """t, with rows the kernels can walk, and its row stride."""
+        self._check(t, shape, name)
+        rows, length = shape
+        if not t.is_contiguous():
+            ld = t.stride(0)
+            if (length == 1 or t.stride(1) == 1) and (rows == 1 or length <= ld <= HQML_DENSE_MAX_FEATURES):
+                return t, ld if rows > 1 else length
+            t = t.contiguous()
+        return t, length
+
+    def _queue(self, call, *args):
+        if self._current_stream(self.device.index) == self.stream:
+            return call(self.handle, *args)
+        cuda = self.torch.cuda
+        here = cuda.current_stream(self.device)
+        own = cuda.ExternalStream(self.stream, device=self.device) if self.stream else cuda.default_stream(self.device)
+        own.wait_stream(here)
+        call(self.handle, *args)
+        here.wait_stream(own)
+
+    def _forward(self, x, w, bias, residual, out, keep):
+        t = self.torch
+        M = x.shape[0]
+        x, ldx = self._rows(x, (M, self.K), "x")
+        w, ldw = self._rows(w, (self.N, self.K), "w")
+        if bias is not None:
+            self._check(bias, (self.N,), "bias")
+            bias = bias.contiguous()
+        ldr = 0
+        if residual is not None:
+            residual, ldr = self._rows(residual, (M, self.N), "residual")
+        if out is None:
+            y, ldy = t.empty((M, self.N), dtype=self.dtype, device=self.device), self.N
+        else:
+            y, ldy = self._rows(out, (M, self.N), "out")
+            if y is not out:
+                raise ValueError("out must have rows without gaps between their elements")
+        z = None
+        if keep and not self.plain:
+            z = t.empty((M, self.N), dtype=self.dtype, device=self.device)
+        self._queue(hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                    None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
+                    y.data_ptr(), ldy, None if z is None else z.data_ptr())
+        return y if out is None else out, z
+
+    def forward(self, x, w, bias=None, residual=None, out=None):
+        """y.  `out` may be the residual itself."""
+        return self._forward(x, w, bias, residual, out, False)[0]
+
+    def forward_train(self, x, w, bias=None, residual=None, out=None):
+        """(y, z): z is what backward needs (None without an activation)."""
+        return self._forward(x, w, bias, residual, out, True)
+
+    def backward(self, dy, x, w, z=None, input=True, weight=True, bias=True):
+        """(dx, dw, db) for dy = dL/dy and the arguments and z of a forward call; those not
+        asked for are None.  The residual's gradient is dy."""
+        t = self.torch
+        M = dy.shape[0]
+        dy, lddy = self._rows(dy, (M, self.N), "dy")
+        x, ldx = self._rows(x, (M, self.K), "x")
+        w, ldw = self._rows(w, (self.N, self.K), "w")
+        if not self.plain:
+            if z is None:
+                raise ValueError("the gradient of an activation needs the forward call's z")
+            self._check(z, (M, self.N), "z")
+            z = z.contiguous()
+        dx = t.empty((M, self.K), dtype=self.dtype, device=self.device) if input else None
+        dw = t.empty((self.N, self.K), dtype=self.dtype, device=self.device) if weight else None
+        db = t.empty((self.N,), dtype=self.dtype, device=self.device) if bias else None
+        self._queue(hqml_dense_backward, M, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
+                    None if self.plain else z.data_ptr(), dx.data_ptr() if input else None, self.K,
+                    dw.data_ptr() if weight else None, db.data_ptr() if bias else None)
+        return dx, dw, db

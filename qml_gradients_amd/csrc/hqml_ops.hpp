@@ -1,0 +1,56 @@
+// Internal interface between the entry points of the dense layer and AdamW (hqml_ops.cpp)
+// and their kernels (hqml_dense.hip, hqml_adamw.hip).  Not part of the public ABI.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+
+#include "../../include/hqml.h"
+
+namespace hqml {
+
+struct DenseForward {
+    int M, K, N;
+    const void *x, *w, *bias, *residual;
+    long long ldx, ldw, ldr, ldy;
+    void *y, *z;
+    int act;
+    float alpha;
+};
+
+struct DenseBackward {
+    int M, K, N;
+    const void *dy, *x, *w, *z;
+    long long lddy, ldx, ldw, lddx;
+    void *dx, *dw, *db;
+    int act;
+    float alpha;
+};
+
+// Parts of a handle's workspace (byte counts and, once reserved, addresses).
+struct DenseWorkspace {
+    size_t dz_bytes = 0;     // gradient at z, [M][N] in dtype
+    size_t rows_bytes = 0;   // partial row sums of dz, fp32
+    void *dz = nullptr;
+    float *rows = nullptr;
+};
+
+DenseWorkspace dense_workspace(const hqml_dense_config &cfg);
+hipError_t launch_dense_forward(const DenseForward &a, int dtype, const DenseWorkspace &ws, hipStream_t s);
+hipError_t launch_dense_backward(const DenseBackward &a, int dtype, const DenseWorkspace &ws, hipStream_t s);
+
+// One AdamW launch takes this many tensors in its kernel arguments.
+constexpr int kAdamwTensors = 48;
+
+struct AdamwScalars {
+    double decay;     // lr weight_decay
+    double b1, c1;    // beta1, 1 - beta1
+    double b2, c2;
+    double inv_root;  // 1 / sqrt(1 - beta2^step)
+    double eps;
+    double size;      // lr / (1 - beta1^step)
+};
+
+hipError_t launch_adamw(const hqml_adamw_config &cfg, const AdamwScalars &k, int n, const hqml_adamw_tensor *t,
+                        hipStream_t s);
+
+}  // namespace hqml

@@ -5,8 +5,8 @@ summary, section 3.3).  This module plays that role over the C ABI: the forward
 runs ``hqml_forward`` (keeping the fused-pass outputs), the backward runs
 ``hqml_backward`` with the incoming dL/dE, so any loss built from the
 expectation values gets its gradient from the fused adjoint kernels.  Gradients
-flow to theta only; the encoding angles x are data.  Marshalling only: no
-arithmetic of the method runs here.
+flow to theta only; the encoding angles x are data.  DenseLayer does the same for the
+dense layers around the circuits.  Marshalling only: no arithmetic of the method runs here.
 """
 from __future__ import annotations
 
@@ -14,7 +14,7 @@ import math
 
 import torch
 
-from . import Context
+from . import Context, Dense
 
 
 class HEAExpectation(torch.autograd.Function):
@@ -59,3 +59,58 @@ class HEALayer(torch.nn.Module):
 
     def forward(self, x):
         return HEAExpectation.apply(self.theta, x, self.hq)
+
+
+class DenseFunction(torch.autograd.Function):
+    """y = alpha act(x w^T + bias) + residual, differentiable in all four."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, dense):
+        ctx.dense = dense
+        y, z = dense.forward_train(x, weight, bias, residual)
+        ctx.save_for_backward(x, weight, z)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        x, weight, z = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            dx, dw, db = ctx.dense.backward(dy, x, weight, z, input=need[0], weight=need[1], bias=need[2])
+        return dx, dw, db, dy if need[3] else None, None
+
+
+class DenseLayer(torch.nn.Module):
+    """Dense layer y = alpha act(x weight^T + bias) + residual over the last axis of x, with
+    weight [out_features][in_features] and bias [out_features] as trainable parameters
+    (initialised uniformly within 1/sqrt(in_features)).  max_batch bounds the product of x's
+    other axes.  activation="sigmoid" with alpha=pi maps features to encoding angles."""
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0, bias=True,
+                 device=None):
+        super().__init__()
+        self.dense = Dense(in_features, out_features, max_batch, dtype=dtype, activation=activation, alpha=alpha,
+                           device=device)
+        bound = 1.0 / math.sqrt(in_features)
+
+        def parameter(*shape):
+            v = (torch.rand(*shape, dtype=torch.float64) * 2.0 - 1.0) * bound
+            return torch.nn.Parameter(v.to(self.dense.device, self.dense.dtype))
+
+        self.weight = parameter(out_features, in_features)
+        self.bias = parameter(out_features) if bias else None
+
+    def forward(self, x, residual=None):
+        lead = x.shape[:-1]
+        x = x.reshape(-1, x.shape[-1])
+        if residual is not None:
+            residual = residual.reshape(-1, residual.shape[-1])
+        grads = torch.is_grad_enabled() and any(
+            t is not None and t.requires_grad for t in (x, self.weight, self.bias, residual))
+        if grads:
+            y = DenseFunction.apply(x, self.weight, self.bias, residual, self.dense)
+        else:
+            y = self.dense.forward(x, self.weight, self.bias, residual)
+        return y.reshape(*lead, y.shape[-1])
