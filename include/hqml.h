@@ -243,14 +243,15 @@ const char *hqml_dense_last_error(const hqml_dense *h);
 
 /* z = x w^T + bias, y = alpha act(z) + residual for a batch of M rows (0 <= M <= max_batch;
  * M == 0 queues nothing).  x [M][K], w [N][K], residual and y [M][N] with row strides ldx,
- * ldw, ldr, ldy in elements (at least the row's length); bias [N]; z [M][N] without gaps.
- * bias, residual and z may be NULL; z is what hqml_dense_backward needs, rounded to dtype
- * (with HQML_ACT_NONE it is not needed and not written).  y may be the residual itself
- * (same stride); otherwise outputs overlap no other argument.  Sums are held in fp32; with
- * HQML_DTYPE_BF16 y and z are rounded once, to nearest even. */
+ * ldw, ldr, ldy in elements (at least the row's length); bias [N]; z [M][N] without gaps,
+ * fp32 with either dtype (held in bf16 it would cost a gradient half as much precision again
+ * as the gradient's own rounding, where the activation bends most).  bias, residual and z may
+ * be NULL; z is what hqml_dense_backward needs (with HQML_ACT_NONE it is not needed and not
+ * written).  y may be the residual itself (same stride); otherwise outputs overlap no other
+ * argument.  Sums are held in fp32; with HQML_DTYPE_BF16 y is rounded once, to nearest even. */
 int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw,
                        const void *bias, const void *residual, long long ldr, void *y, long long ldy,
-                       void *z);
+                       float *z);
 
 /* Gradients of a forward call for dy = dL/dy [M][N] (row stride lddy):
  * dz = alpha act'(z) dy, dx = dz w [M][K] (row stride lddx), dw = dz^T x [N][K],
@@ -258,7 +259,7 @@ int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const
  * gaps.  Each of dx, dw, db may be NULL (not formed).  z is the forward call's (ignored with
  * HQML_ACT_NONE).  M == 0 writes zeros to dw and db. */
 int hqml_dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx,
-                        const void *w, long long ldw, const void *z, void *dx, long long lddx, void *dw,
+                        const void *w, long long ldw, const float *z, void *dx, long long lddx, void *dw,
                         void *db);
 
 /* How the moments of hqml_adamw_step are held. */

@@ -447,9 +447,10 @@ class Dense:
         except Exception:
             pass
 
-    def _check(self, t, shape, name):
-        if t.dtype is not self.dtype or t.device != self.device:
-            raise TypeError(f"{name} must be {self.dtype} on {self.device}, got {t.dtype} on {t.device}")
+    def _check(self, t, shape, name, dtype=None):
+        dtype = dtype or self.dtype
+        if t.dtype is not dtype or t.device != self.device:
+            raise TypeError(f"{name} must be {dtype} on {self.device}, got {t.dtype} on {t.device}")
         if tuple(t.shape) != shape:
             raise ValueError(f"expected shape {shape} for {name}, got {tuple(t.shape)}")
 
@@ -493,7 +494,7 @@ class Dense:
                 raise ValueError("out must have rows without gaps between their elements")
         z = None
         if keep and not self.plain:
-            z = t.empty((M, self.N), dtype=self.dtype, device=self.device)
+            z = t.empty((M, self.N), dtype=t.float32, device=self.device)
         self._queue(hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
                     y.data_ptr(), ldy, None if z is None else z.data_ptr())
@@ -504,7 +505,7 @@ class Dense:
         return self._forward(x, w, bias, residual, out, False)[0]
 
     def forward_train(self, x, w, bias=None, residual=None, out=None):
-        """(y, z): z is what backward needs (None without an activation)."""
+        """(y, z): z, in fp32, is what backward needs (None without an activation)."""
         return self._forward(x, w, bias, residual, out, True)
 
     def backward(self, dy, x, w, z=None, input=True, weight=True, bias=True):
@@ -518,7 +519,7 @@ class Dense:
         if not self.plain:
             if z is None:
                 raise ValueError("the gradient of an activation needs the forward call's z")
-            self._check(z, (M, self.N), "z")
+            self._check(z, (M, self.N), "z", t.float32)
             z = z.contiguous()
         dx = t.empty((M, self.K), dtype=self.dtype, device=self.device) if input else None
         dw = t.empty((self.N, self.K), dtype=self.dtype, device=self.device) if weight else None

@@ -1,49 +1,20 @@
 // Dense layer: y = alpha act(x w^T + bias) + residual and its gradients.
 //
-// All three products of the layer are one tile kernel, C(i, j) = sum_k A(i, k) B(k, j), with
-// the operands addressed by two strides each:
+// All three products of the layer are one kernel family (hqml_gemm.hpp):
 //   forward  C = x w^T      dx = dz w      dw = dz^T x
-// and an epilogue that finishes the value where the sum ends.
+// This file chooses their tiles and splits, and forms dz = alpha act'(z) dy with its row sums.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
 
-#include "hqml_ops.hpp"
+#include "hqml_gemm.hpp"
 
 namespace hqml {
 namespace {
 
-struct bf16 {
-    uint16_t u;
-};
-
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(bf16 x) { return __builtin_bit_cast(float, (uint32_t)x.u << 16); }
-__device__ __forceinline__ void narrow(float x, float &o) { o = x; }
-// round to nearest even; a NaN stays one
-__device__ __forceinline__ void narrow(float x, bf16 &o)
-{
-    const uint32_t b = __builtin_bit_cast(uint32_t, x);
-    o.u = x != x ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFF + ((b >> 16) & 1)) >> 16);
-}
-
-// Phi(z), the normal distribution function.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
-__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
-
-__device__ __forceinline__ float activate(float z, int act)
-{
-    switch (act) {
-    case HQML_ACT_RELU: return z < 0.0f ? 0.0f : z;
-    case HQML_ACT_GELU: return z * normal_cdf(z);
-    case HQML_ACT_SILU: return z * logistic(z);
-    case HQML_ACT_TANH: return tanhf(z);
-    case HQML_ACT_SIGMOID: return logistic(z);
-    default: return z;
-    }
-}
+using namespace gemm;
 
 __device__ __forceinline__ float slope(float z, int act)
 {
@@ -66,64 +37,59 @@ __device__ __forceinline__ float slope(float z, int act)
     }
 }
 
-template <typename T>
-struct Product {
-    const T *a, *b;          // A(i, k) = a[i * ai + k * ak], B(k, j) = b[k * bk + j * bj]
-    long long ai, ak, bk, bj;
-    int I, J, K;
-    T *c;                    // C(i, j) at c[i * ci + j]
-    long long ci;
-    // epilogue
-    const T *bias, *residual;
-    long long ri;
-    T *z;                    // [I][J]
-    int act;
-    float alpha;
+constexpr size_t kPartBytes = 64u << 20;   // most that partial sums take
+constexpr int kMostParts = 64;
+
+// How a product is cut up.
+struct Cut {
+    Shape shape;
+    int parts, k_part;
 };
 
-constexpr int kTile = 64, kStep = 16;
+int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// A 64 x 64 tile of C by 256 threads, 4 x 4 sums a thread.
-template <typename T>
-__global__ __launch_bounds__(256) void k_product(Product<T> P)
+Cut cut(int I, int J, int K, bool wide_bf16, size_t part_bytes)
 {
-    __shared__ float as[kStep][kTile + 1], bs[kStep][kTile + 1];
-    const int ti = (P.I + kTile - 1) / kTile;
-    const int i0 = (int)(blockIdx.x % ti) * kTile, j0 = (int)(blockIdx.x / ti) * kTile;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < P.K; k0 += kStep) {
-        for (int e = threadIdx.x; e < kTile * kStep; e += 256) {
-            // consecutive threads along whichever index is contiguous
-            const int ia = P.ak == 1 ? e / kStep : e % kTile, ka = P.ak == 1 ? e % kStep : e / kTile;
-            const int jb = P.bk == 1 ? e / kStep : e % kTile, kb = P.bk == 1 ? e % kStep : e / kTile;
-            as[ka][ia] = i0 + ia < P.I && k0 + ka < P.K ? widen(P.a[(i0 + ia) * P.ai + (k0 + ka) * P.ak]) : 0.0f;
-            bs[kb][jb] = j0 + jb < P.J && k0 + kb < P.K ? widen(P.b[(k0 + kb) * P.bk + (j0 + jb) * P.bj]) : 0.0f;
+    auto tiles = [&](int n) { return (long long)ceil_div(I, n) * ceil_div(J, n); };
+    Cut c{TILE_64, 1, (K + 63) / 64 * 64};
+    if (wide_bf16 && tiles(256) >= 192) c.shape = TILE_256;
+    else if (tiles(128) >= 256) c.shape = TILE_128;
+    if (c.shape == TILE_64 && tiles(64) < 256) {
+        long long parts = std::min<long long>(512 / tiles(64), K / 128);
+        parts = std::min<long long>(parts, kMostParts);
+        parts = std::min<long long>(parts, (long long)(part_bytes / ((size_t)I * J * 4)));
+        if (parts > 1) {
+            c.k_part = ceil_div(ceil_div(K, (int)parts), 64) * 64;
+            c.parts = ceil_div(K, c.k_part);
         }
-        __syncthreads();
-        for (int k = 0; k < kStep; ++k)
-            for (int r = 0; r < 4; ++r)
-                for (int c = 0; c < 4; ++c) acc[r][c] += as[k][ty + 16 * r] * bs[k][tx + 16 * c];
-        __syncthreads();
     }
-    for (int r = 0; r < 4; ++r)
-        for (int c = 0; c < 4; ++c) {
-            const int i = i0 + ty + 16 * r, j = j0 + tx + 16 * c;
-            if (i >= P.I || j >= P.J) continue;
-            float z = acc[r][c];
-            if (P.bias) z += widen(P.bias[j]);
-            if (P.z) narrow(z, P.z[(long long)i * P.J + j]);
-            float y = P.alpha * activate(z, P.act);
-            if (P.residual) y += widen(P.residual[i * P.ri + j]);
-            narrow(y, P.c[i * P.ci + j]);
-        }
+    return c;
 }
 
-template <typename T>
-hipError_t run_product(const Product<T> &P, hipStream_t s)
+bool aligned(const void *p, long long ld, size_t elem)
 {
-    const unsigned tiles = (unsigned)((P.I + kTile - 1) / kTile) * (unsigned)((P.J + kTile - 1) / kTile);
-    k_product<T><<<tiles, 256, 0, s>>>(P);
+    return (uintptr_t)p % 16 == 0 && ld * (long long)elem % 16 == 0;
+}
+
+// Runs one product; P holds everything but its cut.
+template <typename T>
+hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStream_t s)
+{
+    const int per = 16 / (int)sizeof(T);
+    const bool wide = aligned(P.a, P.lda, sizeof(T)) && aligned(P.b, P.ldb, sizeof(T)) &&
+                      ((la == K_COLS && lb == K_COLS) || P.K % per == 0);
+    P.wide = aligned(P.c, P.ldc, sizeof(T)) && P.J % 8 == 0 && (!P.bias || aligned(P.bias, 0, sizeof(T))) &&
+             (!P.residual || aligned(P.residual, P.ldr, sizeof(T))) && (!P.z || aligned(P.z, 0, 4));
+    const Cut c = cut(P.I, P.J, P.K, sizeof(T) == 2 && wide, ws.part_bytes);
+    const int side = c.shape == TILE_64 ? 64 : c.shape == TILE_128 ? 128 : 256;
+    P.tiles_i = ceil_div(P.I, side), P.tiles_j = ceil_div(P.J, side);
+    P.k_part = c.k_part;
+    P.part = c.parts > 1 ? ws.part : nullptr;
+    const hipError_t e = sizeof(T) == 2 ? launch_bf16(P, la, lb, wide, c.shape, c.parts, s)
+                                        : launch_fp32(P, la, lb, wide, c.shape, c.parts, s);
+    if (e != hipSuccess || c.parts == 1) return e;
+    const long long all = (long long)P.I * P.J;
+    k_join<T><<<(unsigned)std::min<long long>((all + 255) / 256, 4096), 256, 0, s>>>(P, c.parts);
     return hipGetLastError();
 }
 
@@ -131,7 +97,7 @@ constexpr int kRowChunk = 64;    // rows whose dz one workgroup forms and sums
 
 // dz = alpha act'(z) dy (written if dz is not null) and its sums over kRowChunk rows.
 template <typename T>
-__global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const T *z, T *dz, float *rows, int M,
+__global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, float *rows, int M,
                                                int N, int act, float alpha)
 {
     const int col = blockIdx.x * 256 + threadIdx.x;
@@ -140,7 +106,7 @@ __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, cons
     float sum = 0.0f;
     for (int r = r0; r < r1; ++r) {
         float d = alpha * widen(dy[r * lddy + col]);
-        if (act != HQML_ACT_NONE) d *= slope(widen(z[(long long)r * N + col]), act);
+        if (act != HQML_ACT_NONE) d *= slope(z[(long long)r * N + col], act);
         if (dz) narrow(d, dz[(long long)r * N + col]);
         sum += d;
     }
@@ -173,17 +139,17 @@ hipError_t zero(void *p, long long n, hipStream_t s)
 }
 
 template <typename T>
-hipError_t forward(const DenseForward &a, hipStream_t s)
+hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t s)
 {
-    Product<T> P{};
-    P.a = (const T *)a.x, P.ai = a.ldx, P.ak = 1;
-    P.b = (const T *)a.w, P.bk = 1, P.bj = a.ldw;
+    Args P{};
+    P.a = a.x, P.lda = a.ldx;
+    P.b = a.w, P.ldb = a.ldw;
     P.I = a.M, P.J = a.N, P.K = a.K;
-    P.c = (T *)a.y, P.ci = a.ldy;
-    P.bias = (const T *)a.bias, P.residual = (const T *)a.residual, P.ri = a.ldr;
-    P.z = a.act == HQML_ACT_NONE ? nullptr : (T *)a.z;
+    P.c = a.y, P.ldc = a.ldy;
+    P.bias = a.bias, P.residual = a.residual, P.ldr = a.ldr;
+    P.z = a.act == HQML_ACT_NONE ? nullptr : (float *)a.z;
     P.act = a.act, P.alpha = a.alpha;
-    return run_product(P, s);
+    return run_product<T>(P, K_ROWS, K_ROWS, ws, s);
 }
 
 template <typename T>
@@ -204,7 +170,7 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
             const int n = std::min(65535, chunks - c0);
             const long long r0 = (long long)c0 * kRowChunk;
             k_slope<T><<<dim3((unsigned)((a.N + 255) / 256), (unsigned)n), 256, 0, s>>>(
-                (const T *)a.dy + r0 * a.lddy, a.lddy, a.z ? (const T *)a.z + r0 * a.N : nullptr,
+                (const T *)a.dy + r0 * a.lddy, a.lddy, a.z ? (const float *)a.z + r0 * a.N : nullptr,
                 form ? (T *)ws.dz + r0 * a.N : nullptr, a.db ? ws.rows + (long long)c0 * a.N : nullptr,
                 (int)std::min<long long>(a.M - r0, (long long)n * kRowChunk), a.N, a.act, a.alpha);
             if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -215,21 +181,20 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         }
         if (form) dz = (const T *)ws.dz, lddz = a.N, alpha = 1.0f;
     }
-    Product<T> P{};
+    Args P{};
+    P.a = dz, P.lda = lddz;
     P.act = HQML_ACT_NONE, P.alpha = alpha;
     if (a.dx) {
-        P.a = dz, P.ai = lddz, P.ak = 1;
-        P.b = (const T *)a.w, P.bk = a.ldw, P.bj = 1;
+        P.b = a.w, P.ldb = a.ldw;
         P.I = a.M, P.J = a.K, P.K = a.N;
-        P.c = (T *)a.dx, P.ci = a.lddx;
-        if ((e = run_product(P, s)) != hipSuccess) return e;
+        P.c = a.dx, P.ldc = a.lddx;
+        if ((e = run_product<T>(P, K_ROWS, K_COLS, ws, s)) != hipSuccess) return e;
     }
     if (a.dw) {
-        P.a = dz, P.ai = 1, P.ak = lddz;
-        P.b = (const T *)a.x, P.bk = a.ldx, P.bj = 1;
+        P.b = a.x, P.ldb = a.ldx;
         P.I = a.N, P.J = a.K, P.K = a.M;
-        P.c = (T *)a.dw, P.ci = a.K;
-        if ((e = run_product(P, s)) != hipSuccess) return e;
+        P.c = a.dw, P.ldc = a.K;
+        if ((e = run_product<T>(P, K_COLS, K_COLS, ws, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -242,12 +207,15 @@ DenseWorkspace dense_workspace(const hqml_dense_config &cfg)
     const size_t M = (size_t)cfg.max_batch, N = (size_t)cfg.out_features;
     if (cfg.activation != HQML_ACT_NONE) ws.dz_bytes = M * N * (cfg.dtype == HQML_DTYPE_BF16 ? 2 : 4);
     ws.rows_bytes = (M + kRowChunk - 1) / kRowChunk * N * 4;
+    // partial sums: up to kMostParts of the largest result
+    const size_t K = (size_t)cfg.in_features, most = std::max({M * N, M * K, N * K});
+    ws.part_bytes = std::min(kPartBytes, most * 4 * kMostParts);
     return ws;
 }
 
-hipError_t launch_dense_forward(const DenseForward &a, int dtype, const DenseWorkspace &, hipStream_t s)
+hipError_t launch_dense_forward(const DenseForward &a, int dtype, const DenseWorkspace &ws, hipStream_t s)
 {
-    return dtype == HQML_DTYPE_BF16 ? forward<bf16>(a, s) : forward<float>(a, s);
+    return dtype == HQML_DTYPE_BF16 ? forward<bf16>(a, ws, s) : forward<float>(a, ws, s);
 }
 
 hipError_t launch_dense_backward(const DenseBackward &a, int dtype, const DenseWorkspace &ws, hipStream_t s)

@@ -1,0 +1,617 @@
+// The matrix product under the dense layer, on the matrix cores.
+//
+//   C(i, j) = sum_k A(i, k) B(j, k)
+//
+// An operand is stored with k along its rows (K_ROWS: x and w of the forward product) or with
+// k across them (K_COLS: w of dx = dz w, both operands of dw = dz^T x).  A workgroup forms a
+// BM x BN tile of C; each of its waves a TI x TJ part of it as 16 x 16 blocks
+// (v_mfma_f32_16x16x32_bf16, sums in fp32 registers).  Tiles of the operands go through LDS:
+//   K_ROWS  [row][BK], 16-byte chunks permuted by the row so that eight lanes reading one
+//           chunk of eight rows meet eight different banks; a fragment is one 16-byte read
+//   K_COLS  [k][rows], a fragment is two transposing reads (ds_read_b64_tr_b16), each of which
+//           hands a lane four k of its own column; 32-byte units permuted by k for the banks
+// The block of C is handed to the matrix core transposed (B's rows as its rows), so a lane
+// ends with four neighbouring j of one row i.  The epilogue turns a wave's part around in
+// LDS and works on eight neighbouring values of a row: one 16-byte access in bf16.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "hqml_ops.hpp"
+
+namespace hqml {
+namespace gemm {
+
+struct bf16 {
+    uint16_t u;
+};
+
+__device__ __forceinline__ float widen(float x) { return x; }
+__device__ __forceinline__ float widen(bf16 x) { return __builtin_bit_cast(float, (uint32_t)x.u << 16); }
+__device__ __forceinline__ void narrow(float x, float &o) { o = x; }
+// round to nearest even; a NaN stays one
+__device__ __forceinline__ void narrow(float x, bf16 &o)
+{
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    o.u = x != x ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFF + ((b >> 16) & 1)) >> 16);
+}
+
+// Phi(z), the normal distribution function.
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
+__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
+
+// n values through one activation.
+template <int n>
+__device__ __forceinline__ void activate(float (&z)[n], int act)
+{
+    switch (act) {
+    case HQML_ACT_RELU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] = z[k] < 0.0f ? 0.0f : z[k];
+        break;
+    case HQML_ACT_GELU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] *= normal_cdf(z[k]);
+        break;
+    case HQML_ACT_SILU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] *= logistic(z[k]);
+        break;
+    case HQML_ACT_TANH:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] = tanhf(z[k]);
+        break;
+    case HQML_ACT_SIGMOID:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] = logistic(z[k]);
+        break;
+    default: break;
+    }
+}
+
+using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using s16x4 = __attribute__((ext_vector_type(4))) short;
+using f32x4 = __attribute__((ext_vector_type(4))) float;
+using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+using lds_char = __attribute__((address_space(3))) char;
+
+enum Layout { K_ROWS = 0, K_COLS = 1 };
+
+struct Args {
+    const void *a, *b;
+    long long lda, ldb;      // elements from one stored row to the next
+    int I, J, K;
+    int tiles_i, tiles_j;
+    // epilogue: y = alpha act(sum + bias) + residual
+    void *c;
+    long long ldc;
+    const void *bias, *residual;
+    long long ldr;
+    float *z;                // [I][J], sum + bias
+    int act;
+    float alpha;
+    int wide;                // every row of c, residual and z, and bias, allows 16-byte access
+    // work split over k
+    int k_part;              // k of one part, a multiple of BK
+    float *part;             // [parts][I][J]: sums of one part, no epilogue; null: whole sums
+};
+
+// Tile of a workgroup.  Workgroups go round the eight XCDs in turn; each XCD takes a run of
+// neighbouring tiles, and the run walks bands of eight tile rows, so that the tiles an XCD
+// works on together share operand rows in its L2.
+__device__ __forceinline__ void tile_of(int id, int ti, int tj, int &i, int &j)
+{
+    const int all = ti * tj, xcd = id & 7, q = all >> 3, r = all & 7;
+    const int t = xcd * q + (xcd < r ? xcd : r) + (id >> 3);
+    const int band = t / (8 * tj), first = band * 8;
+    const int rows = ti - first < 8 ? ti - first : 8;
+    const int in = t - band * 8 * tj;
+    i = first + in % rows;
+    j = in / rows;
+}
+
+// vmcnt(n): at most n of this wave's loads are still under way.
+template <int n>
+__device__ __forceinline__ void wait_loads()
+{
+    __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
+}
+
+__device__ __forceinline__ void barrier()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
+// One bf16 operand tile of R rows (i or j) and BK k, loaded straight into LDS.
+// Loads go through a buffer resource that ends with the operand's last element: rows past
+// the end read as zero by themselves; k past the end of a row is sent past the end of the buffer.
+template <int L, int R, int BK, int WAVES>
+struct DirectTile {
+    static constexpr int kBytes = R * BK * 2;
+    static constexpr int kLoads = kBytes / (WAVES * 1024);   // 16-byte loads of a lane
+    static_assert(kBytes % (WAVES * 1024) == 0, "whole loads");
+    static constexpr int kRow = (L == K_ROWS ? BK : R) * 2;   // bytes of an LDS row
+    static constexpr int kChunks = kRow / 16;
+
+    const char *base;
+    long long ld;      // bytes
+    int rows, K;
+    int off[kLoads];   // byte offset of a lane's chunk in the tile; K_COLS: past the end if its rows are
+    int at;            // K_ROWS: first k of a lane's chunk (the same in all its rows: they are 8 n apart)
+    int frag;          // byte of a lane's part of the fragment at row 0, k 0
+
+    static __device__ __forceinline__ int key(int r)
+    {
+        if (L == K_ROWS) return kChunks == 4 ? (r >> 1) & 3 : r & 7;
+        return (((r & 3) | ((r >> 1) & 12)) << 1) & (kChunks - 1);
+    }
+
+    __device__ __forceinline__ void init(const void *p, long long ld_elems, int row0, int n_rows, int n_k, int k0)
+    {
+        ld = ld_elems * 2;
+        rows = n_rows - row0;
+        K = n_k;
+        base = (const char *)p + (L == K_ROWS ? row0 * ld + k0 * 2ll : k0 * ld + row0 * 2ll);
+        const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            const int slot = (n * WAVES + wave) * 64 + lane;
+            const int r = slot / kChunks, c = (slot % kChunks) ^ key(r);
+            if (L == K_ROWS) {
+                off[n] = (int)(r * ld) + c * 16;
+                at = c * 8;
+            } else {
+                off[n] = c * 8 < rows ? (int)(r * ld) + c * 16 : 0x7FFFFFF0;
+            }
+        }
+        init_fragment();
+    }
+
+    __device__ __forceinline__ void init_fragment()
+    {
+        const int lane = threadIdx.x & 63;
+        if (L == K_ROWS) {
+            frag = (lane & 15) * kRow + (((lane >> 4) ^ key(lane & 15)) << 4);
+        } else {
+            const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
+            frag = k * kRow + (key(k) << 4) + (lane & 3) * 8;
+        }
+    }
+
+    // Queue the loads of the tile at k (relative to init's k0, which left n_k).
+    __device__ __forceinline__ void load(lds_char *to, int k) const
+    {
+        const int left = K - k;
+        long long bytes;
+        const char *p;
+        if (L == K_ROWS) {
+            p = base + 2ll * k;
+            bytes = (long long)(rows - 1) * ld + 2ll * left;
+        } else {
+            p = base + k * ld;
+            bytes = (long long)(left - 1) * ld + 2ll * rows;
+        }
+        const int end = left <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
+        const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) {
+            int o = off[n];
+            if (L == K_ROWS && left < BK) o = at < left ? o : 0x7FFFFFF0;
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(
+                rsrc, (__attribute__((address_space(3))) void *)(to + (n * WAVES + wave) * 1024), 16, o, 0, 0, 0);
+        }
+    }
+
+    // Fragment of 16 rows from row r0 (a multiple of 16), 32 k from k0 (of 32).  Neither changes a
+    // row's or k's key, so both enter the lane's byte as a sum or one exclusive or.
+    __device__ __forceinline__ bf16x8 fragment(const lds_char *t, int r0, int k0) const
+    {
+        if (L == K_ROWS)
+            return *(const __attribute__((address_space(3))) bf16x8 *)(t + (frag ^ (k0 << 1)) + r0 * kRow);
+        union {
+            s16x4 s[2];
+            bf16x8 v;
+        } u;
+        // sixteen lanes read four k rows of sixteen values and receive them transposed
+        const lds_char *p = t + (frag ^ (r0 << 1)) + k0 * kRow;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            u.s[h] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4 *)(p + h * 4 * kRow));
+        return u.v;
+    }
+};
+
+// Epilogue of a wave's TI x TJ part (16 x 16 blocks acc[FI][FJ], four j of row lane % 16 a lane)
+// that begins at (i0, j0) of C; buf: this wave's own LDS, PR rows of TJ floats, whose 16-byte
+// chunks are permuted by the row (a lane writes one chunk of its row).
+// Only a forward product has more to finish than alpha.  again(i, j): the sum at (i, j) formed anew where it is not finite (kAgain).
+template <typename TC, int FI, int FJ, int PR, bool kForward, bool kAgain, typename F>
+__device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int i0, int j0, int part, lds_char *buf,
+                                       F again)
+{
+    constexpr int TJ = FJ * 16, kRow = TJ * 4, kMask = TJ / 4 - 1;
+    static_assert((TJ & (TJ - 1)) == 0, "chunk permutation");
+    constexpr int kPer = PR / 16;   // block rows of a turn
+    const int lane = threadIdx.x & 63;
+    float *out = P.part ? P.part + (long long)part * P.I * P.J : nullptr;
+#pragma unroll
+    for (int f0 = 0; f0 < FI; f0 += kPer) {
+#pragma unroll
+        for (int f = 0; f < kPer; ++f)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g)
+                *(__attribute__((address_space(3))) f32x4 *)(buf + (f * 16 + (lane & 15)) * kRow +
+                                                             (((g * 4 + (lane >> 4)) ^ (lane & kMask & 15)) << 4)) =
+                    acc[f0 + f][g];
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own writes, read by its other lanes
+        for (int e = lane; e < PR * (TJ / 8); e += 64) {
+            const int r = e / (TJ / 8), c = (e % (TJ / 8)) * 8;
+            const int i = i0 + f0 * 16 + r, j = j0 + c;
+            float v[8];
+            const auto *src = (const __attribute__((address_space(3))) f32x4 *)(buf + r * kRow);
+            const int key = r & kMask & 15;
+            const f32x4 lo = src[(c >> 2) ^ key], hi = src[((c >> 2) + 1) ^ key];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
+            if (i >= P.I || j >= P.J) continue;
+            const int n = P.J - j < 8 ? P.J - j : 8;
+            if (kAgain) {
+                float worst = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) worst += v[k] * 0.0f;
+                if (worst != worst)
+                    for (int k = 0; k < n; ++k) {
+                        const float s = again(i, j + k);
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) v[q] = q == k ? s : v[q];
+                    }
+            }
+            if (P.wide) {   // J is a multiple of 8 then
+                if (out) {
+                    f32x4 *o = (f32x4 *)(out + (long long)i * P.J + j);
+                    o[0] = f32x4{v[0], v[1], v[2], v[3]}, o[1] = f32x4{v[4], v[5], v[6], v[7]};
+                    continue;
+                }
+                TC t[8];
+                constexpr int kV = (int)sizeof(t) / 16;
+                u32x4 w[kV];
+                if (kForward && P.bias) {
+#pragma unroll
+                    for (int k = 0; k < kV; ++k) w[k] = ((const u32x4 *)((const TC *)P.bias + j))[k];
+                    __builtin_memcpy(t, w, sizeof t);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += widen(t[k]);
+                }
+                if (kForward && P.z) {
+                    f32x4 *o = (f32x4 *)(P.z + (long long)i * P.J + j);
+                    o[0] = f32x4{v[0], v[1], v[2], v[3]}, o[1] = f32x4{v[4], v[5], v[6], v[7]};
+                }
+                if (kForward) activate(v, P.act);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[k] *= P.alpha;
+                if (kForward && P.residual) {
+#pragma unroll
+                    for (int k = 0; k < kV; ++k) w[k] = ((const u32x4 *)((const TC *)P.residual + i * P.ldr + j))[k];
+                    __builtin_memcpy(t, w, sizeof t);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) v[k] += widen(t[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) narrow(v[k], t[k]);
+                __builtin_memcpy(w, t, sizeof t);
+#pragma unroll
+                for (int k = 0; k < kV; ++k) ((u32x4 *)((TC *)P.c + i * P.ldc + j))[k] = w[k];
+            } else if (out) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < n) out[(long long)i * P.J + j + k] = v[k];
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (kForward && P.bias && k < n) v[k] += widen(((const TC *)P.bias)[j + k]);
+                    if (kForward && P.z && k < n) P.z[(long long)i * P.J + j + k] = v[k];
+                }
+                if (kForward) activate(v, P.act);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (k >= n) continue;
+                    float y = v[k] * P.alpha;
+                    if (kForward && P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j + k]);
+                    narrow(y, ((TC *)P.c)[i * P.ldc + j + k]);
+                }
+            }
+        }
+        asm volatile("" ::: "memory");
+    }
+}
+
+// bf16 operands whose rows allow 16-byte access.  Two LDS buffers: the loads of step t + 1 are
+// under way while step t is computed; one barrier a step.
+template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
+__global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
+{
+    constexpr int kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
+    using TA = DirectTile<LA, BM, BK, kWaves>;
+    using TB = DirectTile<LB, BN, BK, kWaves>;
+    __shared__ __attribute__((aligned(1024))) char a0[TA::kBytes], a1[TA::kBytes], b0[TB::kBytes], b1[TB::kBytes];
+
+    int ti, tj;
+    tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
+    const int kb = blockIdx.y * P.k_part;
+    const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
+    TA ta;
+    TB tb;
+    ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
+    tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
+    const int wave = threadIdx.x >> 6, wi = wave / WJ, wj = wave % WJ;
+    f32x4 acc[FI][FJ] = {};
+
+    auto compute = [&](const char *A, const char *B) {
+#pragma unroll
+        for (int k = 0; k < BK; k += 32) {
+            bf16x8 fb[FJ];
+#pragma unroll
+            for (int g = 0; g < FJ; ++g) fb[g] = tb.fragment((const lds_char *)B, wj * TJ + g * 16, k);
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                const bf16x8 fa = ta.fragment((const lds_char *)A, wi * TI + f * 16, k);
+#pragma unroll
+                for (int g = 0; g < FJ; ++g)
+                    acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[g], fa, acc[f][g], 0, 0, 0);
+            }
+        }
+    };
+    const int steps = (kn + BK - 1) / BK;
+    ta.load((lds_char *)a0, 0);
+    tb.load((lds_char *)b0, 0);
+    for (int t = 0; t + 1 < steps; t += 2) {
+        wait_loads<0>();
+        barrier();
+        ta.load((lds_char *)a1, (t + 1) * BK);
+        tb.load((lds_char *)b1, (t + 1) * BK);
+        compute(a0, b0);
+        wait_loads<0>();
+        barrier();
+        ta.load((lds_char *)a0, (t + 2) * BK);   // past the last step: an empty buffer, nothing is read
+        tb.load((lds_char *)b0, (t + 2) * BK);
+        compute(a1, b1);
+    }
+    wait_loads<0>();
+    barrier();
+    if (steps & 1) {
+        compute(a0, b0);
+        barrier();
+    }
+    // each buffer serves a quarter of the waves
+    constexpr int kOwn = (TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes) * 4 / kWaves;
+    constexpr int kFit = kOwn / (TJ * 4);
+    static_assert(kWaves % 4 == 0 && kFit >= 16, "room for one block row");
+    constexpr int PR = kFit >= TI ? TI : kFit;
+    const int which = wave & 3;
+    lds_char *const own = (which == 0 ? (lds_char *)a0 : which == 1 ? (lds_char *)a1 : which == 2 ? (lds_char *)b0
+                                                                                      : (lds_char *)b1) +
+                          (wave >> 2) * kOwn;
+    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, own,
+                                    [](int, int) { return 0.0f; });
+}
+
+// One operand tile that goes through registers on its way to LDS: 32-bit operands, which are
+// split there, and rows that do not allow 16-byte access.  The LDS layout is DirectTile's,
+// PLANES times.  A 32-bit value is the sum of PLANES bf16 values to 8 PLANES + 1 bits or so
+// (exactly, with three, where none underflows): x = h + m + l, each the rounding of what the
+// ones before leave.
+template <typename T, int PLANES, int L, int R, int BK, int THREADS, bool WIDE>
+struct StagedTile {
+    using Tile = DirectTile<L, R, BK, THREADS / 64>;
+    static constexpr int kPlane = R * BK * 2, kBytes = kPlane * PLANES;
+    static constexpr int kN = R * BK / 8 / THREADS;   // 8-value chunks of a lane
+    static_assert(kN >= 1 && R * BK / 8 % THREADS == 0, "whole chunks");
+    static constexpr int kSize = (int)sizeof(T), kWords = WIDE ? kSize * 2 : 8;   // registers of a chunk
+
+    const char *base;
+    long long ld;   // bytes
+    int rows, K;
+    int off[kN];
+    int at[kN];     // first k (K_COLS: first row) of a lane's chunk in the tile
+    int put;        // its LDS byte; chunk n lies n * THREADS * 16 further
+    uint32_t reg[kN][kWords];
+
+    __device__ __forceinline__ void init(const void *p, long long ld_elems, int row0, int n_rows, int n_k, int k0)
+    {
+        ld = ld_elems * kSize;
+        rows = n_rows - row0;
+        K = n_k;
+        base = (const char *)p + (L == K_ROWS ? row0 * ld + (long long)k0 * kSize : k0 * ld + (long long)row0 * kSize);
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            const int slot = n * THREADS + threadIdx.x;
+            const int r = slot / Tile::kChunks, c = (slot % Tile::kChunks) ^ Tile::key(r);
+            off[n] = (int)(r * ld) + c * 8 * kSize;
+            at[n] = c * 8;
+        }
+        put = threadIdx.x * 16;
+    }
+
+    // Load the tile at k into registers.
+    __device__ __forceinline__ void load(int k)
+    {
+        const int left = K - k;
+        long long bytes;
+        const char *p;
+        if (L == K_ROWS) {
+            p = base + (long long)k * kSize;
+            bytes = (long long)(rows - 1) * ld + (long long)left * kSize;
+        } else {
+            p = base + k * ld;
+            bytes = (long long)(left - 1) * ld + (long long)rows * kSize;
+        }
+        const int end = left <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
+        const int stop = L == K_ROWS ? left : rows;   // values of the chunk's direction that exist
+        const bool tail = L == K_ROWS ? left < BK : rows < R;
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            if (WIDE) {
+#pragma unroll
+                for (int h = 0; h < kWords / 4; ++h) {
+                    int o = off[n] + h * 16;
+                    if (tail) o = at[n] + h * (16 / kSize) < stop ? o : 0x7FFFFFF0;
+                    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rsrc, o, 0, 0);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) reg[n][h * 4 + q] = w[q];
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    int o = off[n] + e * kSize;
+                    if (tail) o = at[n] + e < stop ? o : 0x7FFFFFF0;
+                    if (kSize == 4) reg[n][e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
+                    else reg[n][e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
+                }
+            }
+        }
+    }
+
+    // Split what load() brought and write it to LDS.
+    __device__ __forceinline__ void store(lds_char *to) const
+    {
+#pragma unroll
+        for (int n = 0; n < kN; ++n) {
+            lds_char *dst = to + put + n * THREADS * 16;
+            if (kSize == 2) {
+                u32x4 w;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) w[q] = WIDE ? reg[n][q] : reg[n][2 * q % kWords] | reg[n][(2 * q + 1) % kWords] << 16;
+                *(__attribute__((address_space(3))) u32x4 *)dst = w;
+            } else {
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(float, reg[n][e % kWords]);
+#pragma unroll
+                for (int p = 0; p < PLANES; ++p) {
+                    bf16x8 h;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        h[e] = (__bf16)x[e];
+                        if (p + 1 < PLANES) x[e] -= (float)h[e];
+                    }
+                    *(__attribute__((address_space(3))) bf16x8 *)(dst + p * kPlane) = h;
+                }
+            }
+        }
+    }
+};
+
+// The sum at (i, j) by itself, in fp32: for values whose split does not hold (infinities, and
+// magnitudes that round up to one).
+template <typename T, typename U, int LA, int LB>
+__device__ __attribute__((noinline)) float plain_sum(const T *a, const U *b, long long lda, long long ldb, int i, int j, int k0, int n)
+{
+    float s = 0.0f;
+    for (int k = k0; k < k0 + n; ++k)
+        s += widen(LA == K_ROWS ? a[i * lda + k] : a[k * lda + i]) * widen(LB == K_ROWS ? b[j * ldb + k] : b[k * ldb + j]);
+    return s;
+}
+
+// Operands of type T and U held as PA and PB bf16 planes; of the products of planes those are
+// formed that reach the sum's 24 bits: 6 for 3 x 3 planes, whose left-out ones are below 2^-24 of the
+// product of magnitudes.  One LDS buffer: step t + 1 is loaded into registers while step t is
+// computed, and two workgroups share a compute unit, so that one computes while the other stores.
+template <typename T, int PA, int LA, typename U, int PB, int LB, typename TC, int BM, int BN, int BK, int WI, int WJ,
+          bool WIDE>
+__global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
+{
+    constexpr int kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
+    using TA = StagedTile<T, PA, LA, BM, BK, kThreads, WIDE>;
+    using TB = StagedTile<U, PB, LB, BN, BK, kThreads, WIDE>;
+    constexpr int kTurn = TI * TJ * 4 < 16 * TJ * 4 * 2 ? TI : 32;   // rows of a wave's part turned at once
+    constexpr int kTurnBytes = kTurn * TJ * 4;
+    constexpr int kTiles = TA::kBytes + TB::kBytes;
+    constexpr int kLds = kTiles > kWaves * kTurnBytes ? kTiles : kWaves * kTurnBytes;
+    __shared__ __attribute__((aligned(1024))) char lds[kLds];
+    lds_char *const A = (lds_char *)lds, *const B = A + TA::kBytes;
+
+    int ti, tj;
+    tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
+    const int kb = blockIdx.y * P.k_part;
+    const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
+    TA ta;
+    TB tb;
+    ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
+    tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
+    typename TA::Tile fa_of;   // where a lane's fragments begin
+    typename TB::Tile fb_of;
+    fa_of.init_fragment();
+    fb_of.init_fragment();
+    const int wave = threadIdx.x >> 6, wi = wave / WJ, wj = wave % WJ;
+    f32x4 acc[FI][FJ] = {};
+    ta.load(0);
+    tb.load(0);
+    for (int k0 = 0; k0 < kn; k0 += BK) {
+        ta.store(A);
+        tb.store(B);
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
+        barrier();
+        ta.load(k0 + BK);   // past the last step: an empty buffer, nothing is read
+        tb.load(k0 + BK);
+#pragma unroll
+        for (int k = 0; k < BK; k += 32) {
+            bf16x8 fb[PB][FJ];
+#pragma unroll
+            for (int p = 0; p < PB; ++p)
+#pragma unroll
+                for (int g = 0; g < FJ; ++g) fb[p][g] = fb_of.fragment(B + p * TB::kPlane, wj * TJ + g * 16, k);
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+#pragma unroll
+                for (int p = PA - 1; p >= 0; --p) {
+                    const bf16x8 fa = fa_of.fragment(A + p * TA::kPlane, wi * TI + f * 16, k);
+#pragma unroll
+                    for (int q = PB - 1; q >= 0; --q) {
+                        if (p + q >= (PA > PB ? PA : PB)) continue;
+#pragma unroll
+                        for (int g = 0; g < FJ; ++g)
+                            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa, acc[f][g], 0, 0, 0);
+                    }
+                }
+        }
+        barrier();
+    }
+    finish<TC, FI, FJ, kTurn, LA == K_ROWS && LB == K_ROWS, (PA > 1 || PB > 1)>(
+        P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, A + wave * kTurnBytes, [&](int i, int j) {
+            return plain_sum<T, U, LA, LB>((const T *)P.a, (const U *)P.b, P.lda, P.ldb, i, j, kb, kn);
+        });
+}
+
+// y of summed parts: the join after work split over k.
+template <typename TC>
+__global__ __launch_bounds__(256) void k_join(Args P, int parts)
+{
+    const long long all = (long long)P.I * P.J;
+    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < all; e += (long long)gridDim.x * 256) {
+        const int i = (int)(e / P.J), j = (int)(e % P.J);
+        float v[1] = {0.0f};
+        for (int p = 0; p < parts; ++p) v[0] += P.part[p * all + e];
+        if (P.bias) v[0] += widen(((const TC *)P.bias)[j]);
+        if (P.z) P.z[e] = v[0];
+        activate(v, P.act);
+        float y = v[0] * P.alpha;
+        if (P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j]);
+        narrow(y, ((TC *)P.c)[i * P.ldc + j]);
+    }
+}
+
+// Tile shapes a product can be run with.
+enum Shape { TILE_64 = 0, TILE_128 = 1, TILE_256 = 2 };
+
+// The kernels of one operand type, for a layout pair (K_ROWS, K_ROWS), (K_ROWS, K_COLS) or
+// (K_COLS, K_COLS); wide: both operands' rows allow 16-byte access.  TILE_256 is for wide bf16.
+hipError_t launch_bf16(const Args &a, int la, int lb, bool wide, Shape shape, int parts, hipStream_t s);
+hipError_t launch_fp32(const Args &a, int la, int lb, bool wide, Shape shape, int parts, hipStream_t s);
+
+}  // namespace gemm
+}  // namespace hqml

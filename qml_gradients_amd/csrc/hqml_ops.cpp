@@ -64,7 +64,7 @@ size_t up256(size_t b)
 
 size_t total_bytes(const DenseWorkspace &ws)
 {
-    return up256(ws.dz_bytes) + up256(ws.rows_bytes);
+    return up256(ws.dz_bytes) + up256(ws.rows_bytes) + up256(ws.part_bytes);
 }
 
 int check_dense_config(const hqml_dense_config *c, std::string *err)
@@ -90,11 +90,13 @@ struct Arg {
     const void *p;
     long long rows, len, ld;
     bool optional;
+    size_t elem = 0;   // bytes of an element; 0: the handle's
 };
 
-int check_args(int device, size_t elem, const Arg *a, int n, std::string *err)
+int check_args(int device, size_t dtype, const Arg *a, int n, std::string *err)
 {
     for (int i = 0; i < n; ++i) {
+        const size_t elem = a[i].elem ? a[i].elem : dtype;
         if (!a[i].p && a[i].optional) continue;
         if (a[i].ld < a[i].len || (a[i].rows > 1 && a[i].ld > HQML_DENSE_MAX_FEATURES)) {
             *err = std::string("row stride of ") + a[i].name + " must be at least its row's length and at most 2^20";
@@ -131,7 +133,7 @@ int thread_error(int code, const std::string &msg)
 }
 
 int dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw, const void *bias,
-                  const void *residual, long long ldr, void *y, long long ldy, void *z)
+                  const void *residual, long long ldr, void *y, long long ldy, float *z)
 {
     const hqml_dense_config &c = h->cfg;
     int rc = check_batch(h, M);
@@ -141,7 +143,7 @@ int dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void
     if (on.error() != hipSuccess) return dense_error(h, HQML_ERR_HIP, hip_text("device", on.error()));
     const Arg args[] = {{"x", x, M, K, ldx, false},        {"w", w, N, K, ldw, false},
                         {"bias", bias, 1, N, N, true},     {"residual", residual, M, N, ldr, true},
-                        {"y", y, M, N, ldy, false},        {"z", z, M, N, N, true}};
+                        {"y", y, M, N, ldy, false},        {"z", z, M, N, N, true, 4}};
     std::string err;
     rc = check_args(c.device, dtype_bytes(c.dtype), args, 6, &err);
     if (rc != HQML_OK) return dense_error(h, rc, err);
@@ -151,7 +153,7 @@ int dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void
 }
 
 int dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx, const void *w,
-                   long long ldw, const void *z, void *dx, long long lddx, void *dw, void *db)
+                   long long ldw, const float *z, void *dx, long long lddx, void *dw, void *db)
 {
     const hqml_dense_config &c = h->cfg;
     int rc = check_batch(h, M);
@@ -162,7 +164,7 @@ int dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const v
     std::string err;
     if (M > 0) {
         const Arg args[] = {{"dy", dy, M, N, lddy, false},     {"x", x, M, K, ldx, !dw},
-                            {"w", w, N, K, ldw, !dx},          {"z", z, M, N, N, c.activation == HQML_ACT_NONE},
+                            {"w", w, N, K, ldw, !dx},          {"z", z, M, N, N, c.activation == HQML_ACT_NONE, 4},
                             {"dx", dx, M, K, lddx, true},      {"dw", dw, N, K, K, true},
                             {"db", db, 1, N, N, true}};
         rc = check_args(c.device, dtype_bytes(c.dtype), args, 7, &err);
@@ -208,6 +210,7 @@ int dense_create(const hqml_dense_config *cfg, hqml_dense **out)
     h->reserved = p;
     ws.dz = p;
     ws.rows = reinterpret_cast<float *>(p + up256(ws.dz_bytes));
+    ws.part = reinterpret_cast<float *>(p + up256(ws.dz_bytes) + up256(ws.rows_bytes));
     h->ws = ws;
     *out = h;
     return HQML_OK;
@@ -339,14 +342,14 @@ const char *hqml_dense_last_error(const hqml_dense *h)
 }
 
 int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw,
-                       const void *bias, const void *residual, long long ldr, void *y, long long ldy, void *z)
+                       const void *bias, const void *residual, long long ldr, void *y, long long ldy, float *z)
 {
     if (!h) return HQML_ERR_ARG;
     return guarded([&] { return dense_forward(h, M, x, ldx, w, ldw, bias, residual, ldr, y, ldy, z); });
 }
 
 int hqml_dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx,
-                        const void *w, long long ldw, const void *z, void *dx, long long lddx, void *dw, void *db)
+                        const void *w, long long ldw, const float *z, void *dx, long long lddx, void *dw, void *db)
 {
     if (!h) return HQML_ERR_ARG;
     return guarded([&] { return dense_backward(h, M, dy, lddy, x, ldx, w, ldw, z, dx, lddx, dw, db); });

@@ -12,14 +12,16 @@ struct DenseForward {
     int M, K, N;
     const void *x, *w, *bias, *residual;
     long long ldx, ldw, ldr, ldy;
-    void *y, *z;
+    void *y;
+    float *z;
     int act;
     float alpha;
 };
 
 struct DenseBackward {
     int M, K, N;
-    const void *dy, *x, *w, *z;
+    const void *dy, *x, *w;
+    const float *z;
     long long lddy, ldx, ldw, lddx;
     void *dx, *dw, *db;
     int act;
@@ -30,8 +32,10 @@ struct DenseBackward {
 struct DenseWorkspace {
     size_t dz_bytes = 0;     // gradient at z, [M][N] in dtype
     size_t rows_bytes = 0;   // partial row sums of dz, fp32
+    size_t part_bytes = 0;   // partial sums of products split over k, fp32
     void *dz = nullptr;
     float *rows = nullptr;
+    float *part = nullptr;
 };
 
 DenseWorkspace dense_workspace(const hqml_dense_config &cfg);
