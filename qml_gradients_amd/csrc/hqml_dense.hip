@@ -16,24 +16,41 @@ namespace {
 
 using namespace gemm;
 
-__device__ __forceinline__ float slope(float z, int act)
+// z becomes d act / dz.
+template <int n>
+__device__ __forceinline__ void slope(float (&z)[n], int act)
 {
     switch (act) {
-    case HQML_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case HQML_ACT_GELU: return normal_cdf(z) + z * expf(-0.5f * z * z) * 0.39894228f;
-    case HQML_ACT_SILU: {
-        const float f = logistic(z);
-        return f * (1.0f + z * (1.0f - f));
-    }
-    case HQML_ACT_TANH: {
-        const float t = tanhf(z);
-        return 1.0f - t * t;
-    }
-    case HQML_ACT_SIGMOID: {
-        const float f = logistic(z);
-        return f * (1.0f - f);
-    }
-    default: return 1.0f;
+    case HQML_ACT_RELU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] = z[k] > 0.0f ? 1.0f : 0.0f;
+        break;
+    case HQML_ACT_GELU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) z[k] = normal_cdf(z[k]) + z[k] * expf(-0.5f * z[k] * z[k]) * 0.39894228f;
+        break;
+    case HQML_ACT_SILU:
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float f = logistic(z[k]);
+            z[k] = f * (1.0f + z[k] * (1.0f - f));
+        }
+        break;
+    case HQML_ACT_TANH:
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float t = tanhf(z[k]);
+            z[k] = 1.0f - t * t;
+        }
+        break;
+    case HQML_ACT_SIGMOID:
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float f = logistic(z[k]);
+            z[k] = f * (1.0f - f);
+        }
+        break;
+    default: break;
     }
 }
 
@@ -48,11 +65,11 @@ struct Cut {
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-Cut cut(int I, int J, int K, bool wide_bf16, size_t part_bytes)
+Cut cut(int I, int J, int K, bool direct, size_t part_bytes)
 {
     auto tiles = [&](int n) { return (long long)ceil_div(I, n) * ceil_div(J, n); };
     Cut c{TILE_64, 1, (K + 63) / 64 * 64};
-    if (wide_bf16 && tiles(256) >= 192) c.shape = TILE_256;
+    if (direct && tiles(256) >= 192) c.shape = TILE_256;
     else if (tiles(128) >= 256) c.shape = TILE_128;
     if (c.shape == TILE_64 && tiles(64) < 256) {
         long long parts = std::min<long long>(512 / tiles(64), K / 128);
@@ -75,18 +92,17 @@ bool aligned(const void *p, long long ld, size_t elem)
 template <typename T>
 hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStream_t s)
 {
-    const int per = 16 / (int)sizeof(T);
-    const bool wide = aligned(P.a, P.lda, sizeof(T)) && aligned(P.b, P.ldb, sizeof(T)) &&
-                      ((la == K_COLS && lb == K_COLS) || P.K % per == 0);
+    const bool direct = sizeof(T) == 2 && aligned(P.a, P.lda, 2) && aligned(P.b, P.ldb, 2) &&
+                        ((la == K_COLS && lb == K_COLS) || P.K % 8 == 0);
     P.wide = aligned(P.c, P.ldc, sizeof(T)) && P.J % 8 == 0 && (!P.bias || aligned(P.bias, 0, sizeof(T))) &&
              (!P.residual || aligned(P.residual, P.ldr, sizeof(T))) && (!P.z || aligned(P.z, 0, 4));
-    const Cut c = cut(P.I, P.J, P.K, sizeof(T) == 2 && wide, ws.part_bytes);
+    const Cut c = cut(P.I, P.J, P.K, direct, ws.part_bytes);
     const int side = c.shape == TILE_64 ? 64 : c.shape == TILE_128 ? 128 : 256;
     P.tiles_i = ceil_div(P.I, side), P.tiles_j = ceil_div(P.J, side);
     P.k_part = c.k_part;
     P.part = c.parts > 1 ? ws.part : nullptr;
-    const hipError_t e = sizeof(T) == 2 ? launch_bf16(P, la, lb, wide, c.shape, c.parts, s)
-                                        : launch_fp32(P, la, lb, wide, c.shape, c.parts, s);
+    const hipError_t e = sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, c.shape, c.parts, s)
+                                        : launch_fp32(P, la, lb, c.shape, c.parts, s);
     if (e != hipSuccess || c.parts == 1) return e;
     const long long all = (long long)P.I * P.J;
     k_join<T><<<(unsigned)std::min<long long>((all + 255) / 256, 4096), 256, 0, s>>>(P, c.parts);
@@ -94,33 +110,88 @@ hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStre
 }
 
 constexpr int kRowChunk = 64;    // rows whose dz one workgroup forms and sums
+constexpr int kSlopeCols = 256;  // and columns: 32 lanes of eight; eight threads go down the rows
 
-// dz = alpha act'(z) dy (written if dz is not null) and its sums over kRowChunk rows.
-template <typename T>
+// dz = alpha act'(z) dy (written if dz is not null) and its sums over kRowChunk rows.  Bound by
+// memory.  VEC: the rows allow 16-byte access and a lane's eight columns are neighbours; otherwise
+// they are 32 apart, so that a row is still read in runs.
+template <typename T, bool VEC>
 __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, float *rows, int M,
                                                int N, int act, float alpha)
 {
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= N) return;
+    __shared__ float part[8][kSlopeCols];
+    const int lane = threadIdx.x & 31, down = threadIdx.x >> 5;
+    const int c0 = blockIdx.x * kSlopeCols;
     const int r0 = blockIdx.y * kRowChunk, r1 = min(M, r0 + kRowChunk);
-    float sum = 0.0f;
-    for (int r = r0; r < r1; ++r) {
-        float d = alpha * widen(dy[r * lddy + col]);
-        if (act != HQML_ACT_NONE) d *= slope(z[(long long)r * N + col], act);
-        if (dz) narrow(d, dz[(long long)r * N + col]);
-        sum += d;
+    float sum[8] = {};
+    for (int r = r0 + down; r < r1; r += 8) {
+        float d[8], f[8];
+        if (VEC) {
+            const int c = c0 + lane * 8;
+            if (c >= N) break;
+            T t[8];
+            __builtin_memcpy(t, __builtin_assume_aligned(dy + r * lddy + c, 16), sizeof t);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] = alpha * widen(t[k]);
+            if (act != HQML_ACT_NONE) __builtin_memcpy(f, __builtin_assume_aligned(z + (long long)r * N + c, 16), sizeof f);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = c0 + lane + 32 * k;
+                d[k] = c < N ? alpha * widen(dy[r * lddy + c]) : 0.0f;
+                f[k] = c < N && act != HQML_ACT_NONE ? z[(long long)r * N + c] : 0.0f;
+            }
+        }
+        if (act != HQML_ACT_NONE) {
+            slope(f, act);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) d[k] *= f[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += d[k];
+        if (!dz) continue;
+        if (VEC) {
+            T t[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) narrow(d[k], t[k]);
+            __builtin_memcpy(__builtin_assume_aligned(dz + (long long)r * N + c0 + lane * 8, 16), t, sizeof t);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int c = c0 + lane + 32 * k;
+                if (c < N) narrow(d[k], dz[(long long)r * N + c]);
+            }
+        }
     }
-    if (rows) rows[(long long)blockIdx.y * N + col] = sum;
+    if (!rows) return;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) part[down][VEC ? lane * 8 + k : lane + 32 * k] = sum[k];
+    __syncthreads();
+    const int c = c0 + threadIdx.x;
+    if (c >= N) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s += part[q][threadIdx.x];
+    rows[(long long)blockIdx.y * N + c] = s;
 }
 
+// db: the sums of all row chunks, 32 columns a workgroup, eight threads down the chunks.
 template <typename T>
 __global__ __launch_bounds__(256) void k_row_sum(const float *rows, int chunks, int N, T *db)
 {
-    const int col = blockIdx.x * 256 + threadIdx.x;
-    if (col >= N) return;
-    float sum = 0.0f;
-    for (int c = 0; c < chunks; ++c) sum += rows[(long long)c * N + col];
-    narrow(sum, db[col]);
+    __shared__ float part[8][32];
+    const int lane = threadIdx.x & 31, down = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
+    float s = 0.0f;
+    if (c < N)
+#pragma unroll 4
+        for (int q = down; q < chunks; q += 8) s += rows[(long long)q * N + c];
+    part[down][lane] = s;
+    __syncthreads();
+    if (down || c >= N) return;
+#pragma unroll
+    for (int q = 1; q < 8; ++q) s += part[q][lane];
+    narrow(s, db[c]);
 }
 
 template <typename T>
@@ -169,14 +240,19 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         for (int c0 = 0; c0 < chunks; c0 += 65535) {   // grid limit in y
             const int n = std::min(65535, chunks - c0);
             const long long r0 = (long long)c0 * kRowChunk;
-            k_slope<T><<<dim3((unsigned)((a.N + 255) / 256), (unsigned)n), 256, 0, s>>>(
-                (const T *)a.dy + r0 * a.lddy, a.lddy, a.z ? (const float *)a.z + r0 * a.N : nullptr,
-                form ? (T *)ws.dz + r0 * a.N : nullptr, a.db ? ws.rows + (long long)c0 * a.N : nullptr,
-                (int)std::min<long long>(a.M - r0, (long long)n * kRowChunk), a.N, a.act, a.alpha);
+            const dim3 grid((unsigned)ceil_div(a.N, kSlopeCols), (unsigned)n);
+            const T *dy = (const T *)a.dy + r0 * a.lddy;
+            const float *z = a.act != HQML_ACT_NONE ? a.z + r0 * a.N : nullptr;
+            T *to = form ? (T *)ws.dz + r0 * a.N : nullptr;
+            float *rows = a.db ? ws.rows + (long long)c0 * a.N : nullptr;
+            const int m = (int)std::min<long long>(a.M - r0, (long long)n * kRowChunk);
+            if (a.N % 8 == 0 && aligned(a.dy, a.lddy, sizeof(T)) && aligned(a.z, 0, 4))
+                k_slope<T, true><<<grid, 256, 0, s>>>(dy, a.lddy, z, to, rows, m, a.N, a.act, a.alpha);
+            else k_slope<T, false><<<grid, 256, 0, s>>>(dy, a.lddy, z, to, rows, m, a.N, a.act, a.alpha);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (a.db) {
-            k_row_sum<T><<<(unsigned)((a.N + 255) / 256), 256, 0, s>>>(ws.rows, chunks, a.N, (T *)a.db);
+            k_row_sum<T><<<(unsigned)ceil_div(a.N, 32), 256, 0, s>>>(ws.rows, chunks, a.N, (T *)a.db);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (form) dz = (const T *)ws.dz, lddz = a.N, alpha = 1.0f;

@@ -181,8 +181,14 @@ struct DirectTile {
         }
     }
 
-    // Queue the loads of the tile at k (relative to init's k0, which left n_k).
-    __device__ __forceinline__ void load(lds_char *to, int k) const
+    // What the loads of one step share.
+    struct Step {
+        const char *p;
+        int end, left;
+    };
+
+    // The tile at k (relative to init's k0, which left n_k); past the end: an empty buffer, nothing is read.
+    __device__ __forceinline__ Step begin(int k) const
     {
         const int left = K - k;
         long long bytes;
@@ -195,15 +201,18 @@ struct DirectTile {
             bytes = (long long)(left - 1) * ld + 2ll * rows;
         }
         const int end = left <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
-        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
+        return {p, end, left};
+    }
+
+    // Queue load n of kLoads.
+    __device__ __forceinline__ void load(const Step &st, lds_char *to, int n) const
+    {
         const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-#pragma unroll
-        for (int n = 0; n < kLoads; ++n) {
-            int o = off[n];
-            if (L == K_ROWS && left < BK) o = at < left ? o : 0x7FFFFFF0;
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(
-                rsrc, (__attribute__((address_space(3))) void *)(to + (n * WAVES + wave) * 1024), 16, o, 0, 0, 0);
-        }
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)st.p, 0, st.end, 0x00027000);
+        int o = off[n];
+        if (L == K_ROWS) o = at < st.left ? o : 0x7FFFFFF0;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            rsrc, (__attribute__((address_space(3))) void *)(to + (n * WAVES + wave) * 1024), 16, o, 0, 0, 0);
     }
 
     // Fragment of 16 rows from row r0 (a multiple of 16), 32 k from k0 (of 32).  Neither changes a
@@ -329,88 +338,162 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
     }
 }
 
-// bf16 operands whose rows allow 16-byte access.  Two LDS buffers: the loads of step t + 1 are
-// under way while step t is computed; one barrier a step.
+// bf16 operands whose rows allow 16-byte access, loaded straight into LDS.  Four LDS buffers of
+// a step (32 k) each: the loads of two to three steps are under way while one is computed.  A
+// wave reads fragments ahead of the matrix instructions that take them: row blocks of A by
+// kAhead, the next step's column blocks of B during the second half of a step.  So the one
+// barrier of a step stands in its middle: it makes step t + 1 readable and frees the
+// buffer of step t - 1, into which the loads of step t + 3 go out one after each row block (all
+// at once, they would hold up the wave's matrix instructions behind them).
+// 8192 x 4096 x 4096 at 256 x 256 tiles, by layout pair: 218, 206 and 200 us (1264, 1332 and
+// 1377 TFLOP/s), with two buffers of 64 k 228-257; the matrix instructions alone take 135.
+
+// What a wave of k_product_direct holds.
+template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
+struct Direct {
+    static constexpr int kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
+    using TA = DirectTile<LA, BM, BK, kWaves>;
+    using TB = DirectTile<LB, BN, BK, kWaves>;
+    static constexpr int kLoads = TA::kLoads + TB::kLoads;
+    TA ta;
+    TB tb;
+    int wi, wj;
+    f32x4 acc[FI][FJ];
+    static constexpr int kAhead = FI >= 4 ? 2 : 1, kMid = FI / 2, kPer = FJ / (FI - kMid);
+    bf16x8 fa[FI], fb[FJ];
+
+    // Queue all loads of step t.
+    __device__ __forceinline__ void load(char *A, char *B, int t) const
+    {
+        const auto sa = ta.begin(t * BK);
+        const auto sb = tb.begin(t * BK);
+#pragma unroll
+        for (int n = 0; n < TA::kLoads; ++n) ta.load(sa, (lds_char *)A, n);
+#pragma unroll
+        for (int n = 0; n < TB::kLoads; ++n) tb.load(sb, (lds_char *)B, n);
+    }
+
+    __device__ __forceinline__ void first(const char *A, const char *B)
+    {
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) fa[f] = ta.fragment((const lds_char *)A, wi * TI + f * 16, 0);
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) fb[g] = tb.fragment((const lds_char *)B, wj * TJ + g * 16, 0);
+    }
+    __device__ __forceinline__ void step(const char *A, const char *A1, const char *B1, char *A3, char *B3, int t)
+    {
+        const auto sa = ta.begin((t + 3) * BK);
+        const auto sb = tb.begin((t + 3) * BK);
+        bf16x8 na[kAhead], nb[FJ];
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            if (f == kMid) {
+                wait_loads<kLoads>();
+                barrier();
+            }
+            if (f + kAhead < FI) fa[f + kAhead] = ta.fragment((const lds_char *)A, wi * TI + (f + kAhead) * 16, 0);
+            else na[f + kAhead - FI] = ta.fragment((const lds_char *)A1, wi * TI + (f + kAhead - FI) * 16, 0);
+            if (f >= kMid) {
+#pragma unroll
+                for (int g = (f - kMid) * kPer; g < (f - kMid + 1) * kPer; ++g)
+                    nb[g] = tb.fragment((const lds_char *)B1, wj * TJ + g * 16, 0);
+            }
+#pragma unroll
+            for (int g = 0; g < FJ; ++g)
+                acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[g], fa[f], acc[f][g], 0, 0, 0);
+            if (f >= kMid) {
+                constexpr int kH = FI - kMid;
+#pragma unroll
+                for (int n = (f - kMid) * kLoads / kH; n < (f - kMid + 1) * kLoads / kH; ++n) {
+                    if (n < TA::kLoads) ta.load(sa, (lds_char *)A3, n);
+                    else tb.load(sb, (lds_char *)B3, n - TA::kLoads);
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) fa[f] = na[f];
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) fb[g] = nb[g];
+    }
+
+    // Step t is in LDS for every wave, and every wave is done with the buffer of step t - 1.
+    __device__ __forceinline__ void ready() const
+    {
+        wait_loads<2 * kLoads>();
+        barrier();
+    }
+};
+
 template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
 {
-    constexpr int kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
-    using TA = DirectTile<LA, BM, BK, kWaves>;
-    using TB = DirectTile<LB, BN, BK, kWaves>;
-    __shared__ __attribute__((aligned(1024))) char a0[TA::kBytes], a1[TA::kBytes], b0[TB::kBytes], b1[TB::kBytes];
+    using D = Direct<LA, LB, BM, BN, BK, WI, WJ>;
+    using TA = typename D::TA;
+    using TB = typename D::TB;
+    constexpr int kWaves = D::kWaves, TI = D::TI, TJ = D::TJ, FI = D::FI, FJ = D::FJ;
+    __shared__ __attribute__((aligned(1024))) char a0[TA::kBytes], a1[TA::kBytes], a2[TA::kBytes], a3[TA::kBytes];
+    __shared__ __attribute__((aligned(1024))) char b0[TB::kBytes], b1[TB::kBytes], b2[TB::kBytes], b3[TB::kBytes];
 
     int ti, tj;
     tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
     const int kb = blockIdx.y * P.k_part;
     const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
-    TA ta;
-    TB tb;
-    ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
-    tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
-    const int wave = threadIdx.x >> 6, wi = wave / WJ, wj = wave % WJ;
-    f32x4 acc[FI][FJ] = {};
+    const int wave = threadIdx.x >> 6;
+    D d;
+    d.ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
+    d.tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
+    d.wi = wave / WJ, d.wj = wave % WJ;
+#pragma unroll
+    for (int f = 0; f < FI; ++f)
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) d.acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
-    auto compute = [&](const char *A, const char *B) {
-#pragma unroll
-        for (int k = 0; k < BK; k += 32) {
-            bf16x8 fb[FJ];
-#pragma unroll
-            for (int g = 0; g < FJ; ++g) fb[g] = tb.fragment((const lds_char *)B, wj * TJ + g * 16, k);
-#pragma unroll
-            for (int f = 0; f < FI; ++f) {
-                const bf16x8 fa = ta.fragment((const lds_char *)A, wi * TI + f * 16, k);
-#pragma unroll
-                for (int g = 0; g < FJ; ++g)
-                    acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[g], fa, acc[f][g], 0, 0, 0);
-            }
-        }
-    };
     const int steps = (kn + BK - 1) / BK;
-    ta.load((lds_char *)a0, 0);
-    tb.load((lds_char *)b0, 0);
-    for (int t = 0; t + 1 < steps; t += 2) {
-        wait_loads<0>();
-        barrier();
-        ta.load((lds_char *)a1, (t + 1) * BK);
-        tb.load((lds_char *)b1, (t + 1) * BK);
-        compute(a0, b0);
-        wait_loads<0>();
-        barrier();
-        ta.load((lds_char *)a0, (t + 2) * BK);   // past the last step: an empty buffer, nothing is read
-        tb.load((lds_char *)b0, (t + 2) * BK);
-        compute(a1, b1);
+    d.load(a0, b0, 0);
+    d.load(a1, b1, 1);
+    d.load(a2, b2, 2);
+    d.ready();
+    d.first(a0, b0);
+    int t = 0;
+    for (; t + 4 <= steps; t += 4) {
+        d.step(a0, a1, b1, a3, b3, t);
+        d.step(a1, a2, b2, a0, b0, t + 1);
+        d.step(a2, a3, b3, a1, b1, t + 2);
+        d.step(a3, a0, b0, a2, b2, t + 3);
+    }
+    if (t < steps) {
+        d.step(a0, a1, b1, a3, b3, t);
+        if (t + 1 < steps) {
+            d.step(a1, a2, b2, a0, b0, t + 1);
+            if (t + 2 < steps) d.step(a2, a3, b3, a1, b1, t + 2);
+        }
     }
     wait_loads<0>();
     barrier();
-    if (steps & 1) {
-        compute(a0, b0);
-        barrier();
-    }
     // each buffer serves a quarter of the waves
-    constexpr int kOwn = (TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes) * 4 / kWaves;
+    constexpr int kOwn = (TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes);
     constexpr int kFit = kOwn / (TJ * 4);
-    static_assert(kWaves % 4 == 0 && kFit >= 16, "room for one block row");
+    static_assert(kWaves % 4 == 0 && kWaves <= 8 && kFit >= 16, "room for one block row");
     constexpr int PR = kFit >= TI ? TI : kFit;
-    const int which = wave & 3;
-    lds_char *const own = (which == 0 ? (lds_char *)a0 : which == 1 ? (lds_char *)a1 : which == 2 ? (lds_char *)b0
-                                                                                      : (lds_char *)b1) +
-                          (wave >> 2) * kOwn;
-    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, own,
+    lds_char *const own = wave == 0 ? (lds_char *)a0 : wave == 1 ? (lds_char *)a1 : wave == 2 ? (lds_char *)a2 : wave==3 ? (lds_char *)a3 : wave==4 ? (lds_char*)b0 : wave==5?(lds_char*)b1:wave==6?(lds_char*)b2:(lds_char*)b3;
+    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, d.acc, ti * BM + d.wi * TI, tj * BN + d.wj * TJ, blockIdx.y, own,
                                     [](int, int) { return 0.0f; });
 }
 
 // One operand tile that goes through registers on its way to LDS: 32-bit operands, which are
-// split there, and rows that do not allow 16-byte access.  The LDS layout is DirectTile's,
-// PLANES times.  A 32-bit value is the sum of PLANES bf16 values to 8 PLANES + 1 bits or so
+// split there, and bf16 rows that do not allow 16-byte access to LDS.  The LDS layout is
+// DirectTile's, PLANES times.  Loads into registers take 16 bytes at any alignment of the element;
+// where a chunk may pass the end of its row, its values are loaded one by one.  A 32-bit value is the sum of PLANES bf16 values to 8 PLANES + 1 bits or so
 // (exactly, with three, where none underflows): x = h + m + l, each the rounding of what the
 // ones before leave.
-template <typename T, int PLANES, int L, int R, int BK, int THREADS, bool WIDE>
+template <typename T, int PLANES, int L, int R, int BK, int THREADS>
 struct StagedTile {
     using Tile = DirectTile<L, R, BK, THREADS / 64>;
     static constexpr int kPlane = R * BK * 2, kBytes = kPlane * PLANES;
     static constexpr int kN = R * BK / 8 / THREADS;   // 8-value chunks of a lane
     static_assert(kN >= 1 && R * BK / 8 % THREADS == 0, "whole chunks");
-    static constexpr int kSize = (int)sizeof(T), kWords = WIDE ? kSize * 2 : 8;   // registers of a chunk
+    static constexpr int kSize = (int)sizeof(T), kWords = kSize * 2;   // registers of a chunk
 
     const char *base;
     long long ld;   // bytes
@@ -455,22 +538,24 @@ struct StagedTile {
         const bool tail = L == K_ROWS ? left < BK : rows < R;
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
-            if (WIDE) {
+            if (!tail) {
 #pragma unroll
                 for (int h = 0; h < kWords / 4; ++h) {
-                    int o = off[n] + h * 16;
-                    if (tail) o = at[n] + h * (16 / kSize) < stop ? o : 0x7FFFFFF0;
-                    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rsrc, o, 0, 0);
+                    const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off[n] + h * 16, 0, 0);
 #pragma unroll
                     for (int q = 0; q < 4; ++q) reg[n][h * 4 + q] = w[q];
                 }
-            } else {
+                continue;
+            }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    int o = off[n] + e * kSize;
-                    if (tail) o = at[n] + e < stop ? o : 0x7FFFFFF0;
-                    if (kSize == 4) reg[n][e] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
-                    else reg[n][e] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
+            for (int e = 0; e < 8; ++e) {
+                const int o = at[n] + e < stop ? off[n] + e * kSize : 0x7FFFFFF0;
+                if (kSize == 4) {
+                    reg[n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
+                } else {
+                    const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
+                    if (e & 1) reg[n][e / 2] |= v << 16;
+                    else reg[n][e / 2] = v;
                 }
             }
         }
@@ -483,10 +568,7 @@ struct StagedTile {
         for (int n = 0; n < kN; ++n) {
             lds_char *dst = to + put + n * THREADS * 16;
             if (kSize == 2) {
-                u32x4 w;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) w[q] = WIDE ? reg[n][q] : reg[n][2 * q % kWords] | reg[n][(2 * q + 1) % kWords] << 16;
-                *(__attribute__((address_space(3))) u32x4 *)dst = w;
+                *(__attribute__((address_space(3))) u32x4 *)dst = u32x4{reg[n][0], reg[n][1], reg[n][2], reg[n][3]};
             } else {
                 float x[8];
 #pragma unroll
@@ -519,21 +601,24 @@ __device__ __attribute__((noinline)) float plain_sum(const T *a, const U *b, lon
 
 // Operands of type T and U held as PA and PB bf16 planes; of the products of planes those are
 // formed that reach the sum's 24 bits: 6 for 3 x 3 planes, whose left-out ones are below 2^-24 of the
-// product of magnitudes.  One LDS buffer: step t + 1 is loaded into registers while step t is
-// computed, and two workgroups share a compute unit, so that one computes while the other stores.
-template <typename T, int PA, int LA, typename U, int PB, int LB, typename TC, int BM, int BN, int BK, int WI, int WJ,
-          bool WIDE>
+// product of magnitudes.  Step t + 1 is loaded into registers while step t is computed.  With
+// BUF = 2 its split and its way to LDS fall between step t's matrix instructions, at one barrier
+// a step; with BUF = 1 they come after, and two workgroups share a compute unit, so that one
+// computes while the other stores.  2048^3 in fp32 (256 tiles, one a compute unit): 91 us with
+// two buffers, 102 with one; 4096^3 (1024 tiles): 693 and 640.
+template <typename T, int PA, int LA, typename U, int PB, int LB, typename TC, int BM, int BN, int WI, int WJ, int BUF>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
 {
-    constexpr int kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
-    using TA = StagedTile<T, PA, LA, BM, BK, kThreads, WIDE>;
-    using TB = StagedTile<U, PB, LB, BN, BK, kThreads, WIDE>;
-    constexpr int kTurn = TI * TJ * 4 < 16 * TJ * 4 * 2 ? TI : 32;   // rows of a wave's part turned at once
+    constexpr int BK = 32, kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16,
+                  FJ = TJ / 16;
+    using TA = StagedTile<T, PA, LA, BM, BK, kThreads>;
+    using TB = StagedTile<U, PB, LB, BN, BK, kThreads>;
+    constexpr int kTurn = TI < 32 ? TI : 32;   // rows of a wave's part turned at once
     constexpr int kTurnBytes = kTurn * TJ * 4;
     constexpr int kTiles = TA::kBytes + TB::kBytes;
-    constexpr int kLds = kTiles > kWaves * kTurnBytes ? kTiles : kWaves * kTurnBytes;
+    constexpr int kLds = kTiles * BUF > kWaves * kTurnBytes ? kTiles * BUF : kWaves * kTurnBytes;
     __shared__ __attribute__((aligned(1024))) char lds[kLds];
-    lds_char *const A = (lds_char *)lds, *const B = A + TA::kBytes;
+    lds_char *here = (lds_char *)lds, *next = here + (BUF - 1) * kTiles;
 
     int ti, tj;
     tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
@@ -551,38 +636,57 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
     f32x4 acc[FI][FJ] = {};
     ta.load(0);
     tb.load(0);
+    ta.store(here);
+    tb.store(here + TA::kBytes);
+    ta.load(BK);   // past the last step: an empty buffer, nothing is read
+    tb.load(BK);
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
+    barrier();
     for (int k0 = 0; k0 < kn; k0 += BK) {
-        ta.store(A);
-        tb.store(B);
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
-        barrier();
-        ta.load(k0 + BK);   // past the last step: an empty buffer, nothing is read
-        tb.load(k0 + BK);
+        bf16x8 fb[PB][FJ];
 #pragma unroll
-        for (int k = 0; k < BK; k += 32) {
-            bf16x8 fb[PB][FJ];
+        for (int p = 0; p < PB; ++p)
 #pragma unroll
-            for (int p = 0; p < PB; ++p)
+            for (int g = 0; g < FJ; ++g)
+                fb[p][g] = fb_of.fragment(here + TA::kBytes + p * TB::kPlane, wj * TJ + g * 16, 0);
 #pragma unroll
-                for (int g = 0; g < FJ; ++g) fb[p][g] = fb_of.fragment(B + p * TB::kPlane, wj * TJ + g * 16, k);
+        for (int f = 0; f < FI; ++f) {
 #pragma unroll
-            for (int f = 0; f < FI; ++f)
+            for (int p = PA - 1; p >= 0; --p) {
+                const bf16x8 fa = fa_of.fragment(here + p * TA::kPlane, wi * TI + f * 16, 0);
 #pragma unroll
-                for (int p = PA - 1; p >= 0; --p) {
-                    const bf16x8 fa = fa_of.fragment(A + p * TA::kPlane, wi * TI + f * 16, k);
+                for (int q = PB - 1; q >= 0; --q) {
+                    if (p + q >= (PA > PB ? PA : PB)) continue;
 #pragma unroll
-                    for (int q = PB - 1; q >= 0; --q) {
-                        if (p + q >= (PA > PB ? PA : PB)) continue;
-#pragma unroll
-                        for (int g = 0; g < FJ; ++g)
-                            acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa, acc[f][g], 0, 0, 0);
-                    }
+                    for (int g = 0; g < FJ; ++g)
+                        acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa, acc[f][g], 0, 0, 0);
                 }
+            }
+            if (BUF == 2 && f == FI / 2 - 1) {
+                ta.store(next);
+                ta.load(k0 + 2 * BK);
+            }
+            if (BUF == 2 && f == FI - 1) {
+                tb.store(next + TA::kBytes);
+                tb.load(k0 + 2 * BK);
+            }
         }
+        if (BUF == 1) {
+            barrier();
+            ta.store(here);
+            tb.store(here + TA::kBytes);
+            ta.load(k0 + 2 * BK);
+            tb.load(k0 + 2 * BK);
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);
         barrier();
+        lds_char *const swap = here;
+        here = next;
+        next = swap;
     }
     finish<TC, FI, FJ, kTurn, LA == K_ROWS && LB == K_ROWS, (PA > 1 || PB > 1)>(
-        P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, A + wave * kTurnBytes, [&](int i, int j) {
+        P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, (lds_char *)lds + wave * kTurnBytes,
+        [&](int i, int j) {
             return plain_sum<T, U, LA, LB>((const T *)P.a, (const U *)P.b, P.lda, P.ldb, i, j, kb, kn);
         });
 }
@@ -609,9 +713,9 @@ __global__ __launch_bounds__(256) void k_join(Args P, int parts)
 enum Shape { TILE_64 = 0, TILE_128 = 1, TILE_256 = 2 };
 
 // The kernels of one operand type, for a layout pair (K_ROWS, K_ROWS), (K_ROWS, K_COLS) or
-// (K_COLS, K_COLS); wide: both operands' rows allow 16-byte access.  TILE_256 is for wide bf16.
-hipError_t launch_bf16(const Args &a, int la, int lb, bool wide, Shape shape, int parts, hipStream_t s);
-hipError_t launch_fp32(const Args &a, int la, int lb, bool wide, Shape shape, int parts, hipStream_t s);
+// (K_COLS, K_COLS).  direct: both bf16 operands' rows allow 16-byte access to LDS; TILE_256 needs it.
+hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, int parts, hipStream_t s);
+hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, int parts, hipStream_t s);
 
 }  // namespace gemm
 }  // namespace hqml
