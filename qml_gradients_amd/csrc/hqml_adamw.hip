@@ -31,7 +31,6 @@ struct AdamwTensor {
 
 struct AdamwBatch {
     int count;
-    int wide;                        // 1 bit would do: every array of every tensor allows 16-byte access
     unsigned first[kAdamwTensors];   // first workgroup of each tensor
     AdamwTensor t[kAdamwTensors];
 };
@@ -47,10 +46,37 @@ __device__ __forceinline__ float widen(bf16 x) { return __builtin_bit_cast(float
 __device__ __forceinline__ void narrow(float x, float &o) { o = x; }
 __device__ __forceinline__ void narrow(double x, double &o) { o = x; }
 // round to nearest even; a NaN stays one
-__device__ __forceinline__ void narrow(float x, bf16 &o)
+__device__ __forceinline__ void narrow(float x, bf16 &o) { o.u = __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// n neighbouring values in one access.
+template <int n, typename T>
+__device__ __forceinline__ void get(T (&to)[n], const T *from)
 {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x);
-    o.u = x != x ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFF + ((b >> 16) & 1)) >> 16);
+    struct alignas(sizeof(T) * n) All {
+        T t[n];
+    };
+    const All a = *(const All *)from;
+#pragma unroll
+    for (int k = 0; k < n; ++k) to[k] = a.t[k];
+}
+
+template <int n, typename T>
+__device__ __forceinline__ void put(T *to, const T (&from)[n])
+{
+    struct alignas(sizeof(T) * n) All {
+        T t[n];
+    };
+    All a;
+#pragma unroll
+    for (int k = 0; k < n; ++k) a.t[k] = from[k];
+    *(All *)to = a;
+}
+
+// Whether n values from p on can be one access.
+template <int n, typename T>
+__device__ __forceinline__ bool fits(const T *p)
+{
+    return ((uintptr_t)p & (sizeof(T) * n - 1)) == 0;
 }
 
 template <typename R>
@@ -87,7 +113,9 @@ __device__ __forceinline__ int tensor_of(const AdamwBatch &b, unsigned wg)
     return lo;
 }
 
-// Moments in 32 bits (fp64 for fp64 parameters).
+// Moments in 32 bits (fp64 for fp64 parameters).  A thread takes four neighbouring elements at a
+// time, kAt of them loaded before the first is computed; where the tensor ends or its arrays do not
+// allow it, one at a time.
 template <typename P, typename G, typename R>
 __global__ __launch_bounds__(kThreadsA) void k_adamw(AdamwBatch batch, AdamwScalars sc)
 {
@@ -95,99 +123,178 @@ __global__ __launch_bounds__(kThreadsA) void k_adamw(AdamwBatch batch, AdamwScal
     const AdamwTensor t = batch.t[ti];
     const long long base = (long long)(blockIdx.x - batch.first[ti]) * kChunk;
     const Coef<R> k(sc);
-    P *p = (P *)t.p;
-    const G *g = (const G *)t.g;
-    R *m = (R *)t.m, *v = (R *)t.v;
-    for (int i = threadIdx.x; i < kChunk; i += kThreadsA) {
-        const long long at = base + i;
-        if (at >= t.n) break;
-        R pe = widen(p[at]), me = m[at], vn, root;
-        element<R>(k, pe, (R)widen(g[at]), me, v[at], vn, root);
-        narrow(pe, p[at]);
-        m[at] = me;
-        v[at] = vn;
+    P *p = (P *)t.p + base;
+    const G *g = (const G *)t.g + base;
+    R *m = (R *)t.m + base, *v = (R *)t.v + base;
+    const long long left = t.n - base;
+    constexpr int kN = sizeof(R) == 8 ? 2 : 4;   // neighbours
+    constexpr int kAt = kChunk / kThreadsA / kN / (sizeof(R) == 8 ? 4 : 2);
+    if (left >= kChunk && fits<kN>(p) && fits<kN>(g) && fits<kN>(m) && fits<kN>(v)) {
+#pragma unroll 1
+        for (int i = threadIdx.x * kN; i < kChunk; i += kThreadsA * kN * kAt) {
+            P pe[kAt][kN];
+            G ge[kAt][kN];
+            R me[kAt][kN], ve[kAt][kN];
+#pragma unroll
+            for (int a = 0; a < kAt; ++a) {
+                const int at = i + a * kThreadsA * kN;
+                get(pe[a], p + at), get(ge[a], g + at), get(me[a], m + at), get(ve[a], v + at);
+            }
+#pragma unroll
+            for (int a = 0; a < kAt; ++a) {
+                const int at = i + a * kThreadsA * kN;
+#pragma unroll
+                for (int e = 0; e < kN; ++e) {
+                    R x = widen(pe[a][e]), vn, root;
+                    element<R>(k, x, (R)widen(ge[a][e]), me[a][e], ve[a][e], vn, root);
+                    narrow(x, pe[a][e]);
+                    ve[a][e] = vn;
+                }
+                put(p + at, pe[a]), put(m + at, me[a]), put(v + at, ve[a]);
+            }
+        }
+        return;
+    }
+    const int end = left < kChunk ? (int)left : kChunk;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < end; i += kThreadsA) {
+        R x = widen(p[i]), me = m[i], vn, root;
+        element<R>(k, x, (R)widen(g[i]), me, v[i], vn, root);
+        narrow(x, p[i]);
+        m[i] = me;
+        v[i] = vn;
     }
 }
 
-__device__ __forceinline__ float from_e4m3(uint32_t code)
+using f32x2 = __attribute__((ext_vector_type(2))) float;
+
+// Largest magnitude of a half wave, as bits: magnitudes order as integers and a NaN is above them
+// all, so it is kept.  Within sixteen lanes by DPP, then once across.
+__device__ __forceinline__ uint32_t half_wave_max(uint32_t b)
 {
-    return __builtin_amdgcn_cvt_f32_fp8(code, 0);
+    auto with = [&](uint32_t other) { b = b > other ? b : other; };
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x141, 0xF, 0xF, true));   // mirrored in eight
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x140, 0xF, 0xF, true));   // mirrored in sixteen
+    with((uint32_t)__shfl_xor((int)b, 16, 64));
+    return b;
 }
 
-__device__ __forceinline__ uint32_t to_e4m3(float x)
+__device__ __forceinline__ float block_scale(uint32_t amax)
 {
-    return __builtin_amdgcn_cvt_pk_fp8_f32(x, 0.0f, 0, false) & 0xFF;
-}
-
-// Largest magnitude of a block over the wave, as bits: magnitudes order as integers and a
-// NaN is above them all, so it is kept.
-__device__ __forceinline__ float wave_max(uint32_t b)
-{
-    for (int o = 32; o; o >>= 1) {
-        const uint32_t other = __shfl_xor(b, o, 64);
-        b = b > other ? b : other;
-    }
-    return __builtin_bit_cast(float, b);
-}
-
-__device__ __forceinline__ float block_scale(float amax)
-{
-    const float s = amax * (1.0f / 448.0f);
+    const float s = __builtin_bit_cast(float, amax) * (1.0f / 448.0f);
     return s < 0x1p-100f ? 0x1p-100f : s;   // a NaN stays
 }
 
+// What is rounded to a code: not zero where x is not.
 __device__ __forceinline__ float scaled(float x, float inv)
 {
     const float u = x * inv;
     return u > 0.0f && u < 0x1p-9f ? 0x1p-9f : u < 0.0f && u > -0x1p-9f ? -0x1p-9f : u;
 }
 
-// Moments in 8 bits.  A wave takes one block of 256 elements at a time, four a lane.
+__device__ __forceinline__ void from_codes(float (&x)[8], const uint32_t (&w)[2], float scale)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], false), b = __builtin_amdgcn_cvt_pk_f32_fp8(w[h], true);
+        x[h * 4] = a.x * scale, x[h * 4 + 1] = a.y * scale;
+        x[h * 4 + 2] = b.x * scale, x[h * 4 + 3] = b.y * scale;
+    }
+}
+
+__device__ __forceinline__ void to_codes(uint32_t (&w)[2], const float (&x)[8], float inv)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int lo = __builtin_amdgcn_cvt_pk_fp8_f32(scaled(x[h * 4], inv), scaled(x[h * 4 + 1], inv), 0, false);
+        w[h] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(scaled(x[h * 4 + 2], inv), scaled(x[h * 4 + 3], inv), lo, true);
+    }
+}
+
+// Moments in 8 bits.  Half a wave takes a block of 256 elements, eight a lane, so a wave's
+// two blocks share its reductions; kAt pairs of blocks are loaded before the first is computed.
 template <typename P, typename G>
 __global__ __launch_bounds__(kThreadsA) void k_adamw8(AdamwBatch batch, AdamwScalars sc)
 {
+    static_assert(HQML_ADAMW_BLOCK == 256, "32 lanes of eight");
+    constexpr int kAt = 2, kPer = kThreadsA * 8;   // elements the workgroup takes at once
     const int ti = tensor_of(batch, blockIdx.x);
     const AdamwTensor t = batch.t[ti];
     const long long base = (long long)(blockIdx.x - batch.first[ti]) * kChunk;
     const Coef<float> k(sc);
-    P *p = (P *)t.p;
-    const G *g = (const G *)t.g;
-    uint8_t *m = (uint8_t *)t.m, *v = (uint8_t *)t.v;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int b = wave; b < kChunk / HQML_ADAMW_BLOCK; b += kThreadsA / 64) {
-        const long long at0 = base + b * HQML_ADAMW_BLOCK;
-        if (at0 >= t.n) break;
-        const long long blk = at0 / HQML_ADAMW_BLOCK;
-        const float ms = t.ms[blk], vs = t.vs[blk];
-        float me[4], ro[4];
-        uint32_t mb = 0, vb = 0;
-        for (int j = 0; j < 4; ++j) {
-            const long long at = at0 + lane * 4 + j;
-            me[j] = ro[j] = 0.0f;
-            if (at < t.n) {
-                float pe = widen(p[at]), vn;
-                me[j] = from_e4m3(m[at]) * ms;
-                const float r = from_e4m3(v[at]) * vs;
-                element<float>(k, pe, widen(g[at]), me[j], r * r, vn, ro[j]);
-                narrow(pe, p[at]);
-                const uint32_t a = __builtin_bit_cast(uint32_t, me[j]) & 0x7FFFFFFF;
-                const uint32_t c = __builtin_bit_cast(uint32_t, ro[j]) & 0x7FFFFFFF;
-                mb = a > mb ? a : mb;
-                vb = c > vb ? c : vb;
+    P *p = (P *)t.p + base;
+    const G *g = (const G *)t.g + base;
+    uint8_t *m = (uint8_t *)t.m + base, *v = (uint8_t *)t.v + base;
+    float *ms = t.ms + base / HQML_ADAMW_BLOCK, *vs = t.vs + base / HQML_ADAMW_BLOCK;
+    const long long left = t.n - base;
+    const bool wide = left >= kChunk && fits<8>(p) && fits<8>(g) && fits<8>(m) && fits<8>(v);
+    const int end = left < kChunk ? (int)left : kChunk;
+#pragma unroll 1
+    for (int i0 = threadIdx.x * 8; i0 < kChunk; i0 += kPer * kAt) {
+        P pe[kAt][8];
+        G ge[kAt][8];
+        uint32_t mw[kAt][2], vw[kAt][2];
+        float sm[kAt], sv[kAt];
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            const int i = i0 + a * kPer;
+            if (wide) {
+                get(pe[a], p + i), get(ge[a], g + i);
+                get(mw[a], (const uint32_t *)(m + i)), get(vw[a], (const uint32_t *)(v + i));
+            } else {
+                mw[a][0] = mw[a][1] = vw[a][0] = vw[a][1] = 0;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    pe[a][e] = P{}, ge[a][e] = G{};
+                    if (i + e >= end) continue;
+                    pe[a][e] = p[i + e], ge[a][e] = g[i + e];
+                    mw[a][e / 4] |= (uint32_t)m[i + e] << (e % 4 * 8);
+                    vw[a][e / 4] |= (uint32_t)v[i + e] << (e % 4 * 8);
+                }
             }
+            const bool some = (i & ~255) < end;   // the block holds elements
+            sm[a] = some ? ms[i >> 8] : 0.0f;
+            sv[a] = some ? vs[i >> 8] : 0.0f;
         }
-        const float sm = block_scale(wave_max(mb)), sv = block_scale(wave_max(vb));
-        const float im = 1.0f / sm, iv = 1.0f / sv;
-        for (int j = 0; j < 4; ++j) {
-            const long long at = at0 + lane * 4 + j;
-            if (at < t.n) {
-                m[at] = (uint8_t)to_e4m3(scaled(me[j], im));
-                v[at] = (uint8_t)to_e4m3(scaled(ro[j], iv));
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            const int i = i0 + a * kPer;
+            float me[8], ro[8];
+            from_codes(me, mw[a], sm[a]);
+            from_codes(ro, vw[a], sv[a]);
+            uint32_t mb = 0, vb = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                float x = widen(pe[a][e]), vn;
+                const float r = ro[e];
+                element<float>(k, x, widen(ge[a][e]), me[e], r * r, vn, ro[e]);
+                narrow(x, pe[a][e]);
+                const uint32_t am = __builtin_bit_cast(uint32_t, me[e]) & 0x7FFFFFFF;
+                const uint32_t ar = __builtin_bit_cast(uint32_t, ro[e]) & 0x7FFFFFFF;
+                mb = am > mb ? am : mb;
+                vb = ar > vb ? ar : vb;
             }
-        }
-        if (lane == 0) {
-            t.ms[blk] = sm;
-            t.vs[blk] = sv;
+            const float nm = block_scale(half_wave_max(mb)), nv = block_scale(half_wave_max(vb));
+            to_codes(mw[a], me, 1.0f / nm);
+            to_codes(vw[a], ro, 1.0f / nv);
+            if (wide) {
+                put(p + i, pe[a]);
+                put((uint32_t *)(m + i), mw[a]), put((uint32_t *)(v + i), vw[a]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (i + e >= end) continue;
+                    p[i + e] = pe[a][e];
+                    m[i + e] = (uint8_t)(mw[a][e / 4] >> (e % 4 * 8));
+                    v[i + e] = (uint8_t)(vw[a][e / 4] >> (e % 4 * 8));
+                }
+            }
+            if ((threadIdx.x & 31) == 0 && (i & ~255) < end) {
+                ms[i >> 8] = nm;
+                vs[i >> 8] = nv;
+            }
         }
     }
 }
@@ -199,7 +306,6 @@ hipError_t each_batch(int n, const hqml_adamw_tensor *t, F launch)
     while (i < n) {
         AdamwBatch b;
         b.count = 0;
-        b.wide = 1;
         unsigned long long wgs = 0;
         for (; i < n && b.count < kAdamwTensors; ++i) {
             if (t[i].numel == 0) continue;

@@ -17,7 +17,7 @@ namespace {
 using namespace gemm;
 
 // z becomes d act / dz.
-template <int n>
+template <bool FAST, int n>
 __device__ __forceinline__ void slope(float (&z)[n], int act)
 {
     switch (act) {
@@ -27,26 +27,30 @@ __device__ __forceinline__ void slope(float (&z)[n], int act)
         break;
     case HQML_ACT_GELU:
 #pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = normal_cdf(z[k]) + z[k] * expf(-0.5f * z[k] * z[k]) * 0.39894228f;
+        for (int k = 0; k < n; ++k) {
+            float e;
+            const float f = normal_cdf(z[k], e);
+            z[k] = f + z[k] * e * 0.39894228f;
+        }
         break;
     case HQML_ACT_SILU:
 #pragma unroll
         for (int k = 0; k < n; ++k) {
-            const float f = logistic(z[k]);
+            const float f = logistic<FAST>(z[k]);
             z[k] = f * (1.0f + z[k] * (1.0f - f));
         }
         break;
     case HQML_ACT_TANH:
 #pragma unroll
         for (int k = 0; k < n; ++k) {
-            const float t = tanhf(z[k]);
+            const float t = tanh_of<FAST>(z[k]);
             z[k] = 1.0f - t * t;
         }
         break;
     case HQML_ACT_SIGMOID:
 #pragma unroll
         for (int k = 0; k < n; ++k) {
-            const float f = logistic(z[k]);
+            const float f = logistic<FAST>(z[k]);
             z[k] = f * (1.0f - f);
         }
         break;
@@ -143,7 +147,7 @@ __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, cons
             }
         }
         if (act != HQML_ACT_NONE) {
-            slope(f, act);
+            slope<sizeof(T) == 2>(f, act);
 #pragma unroll
             for (int k = 0; k < 8; ++k) d[k] *= f[k];
         }

@@ -31,18 +31,50 @@ __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(bf16 x) { return __builtin_bit_cast(float, (uint32_t)x.u << 16); }
 __device__ __forceinline__ void narrow(float x, float &o) { o = x; }
 // round to nearest even; a NaN stays one
-__device__ __forceinline__ void narrow(float x, bf16 &o)
+__device__ __forceinline__ void narrow(float x, bf16 &o) { o.u = __builtin_bit_cast(uint16_t, (__bf16)x); }
+
+// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  With t = 1 / (1 + 0.3 |z|),
+// Phi(-|z|) exp(z^2 / 2) / t is smooth in t on (0, 1]; the polynomial is its least largest relative
+// error there, 1.5e-7 (weighted least squares, reweighted to the largest error), and 2e-7 is what fp32
+// adds.  So the tail keeps its relative precision.  An eighth of erff and expf's instructions.
+__device__ __forceinline__ float normal_cdf(float z, float &e)
 {
-    const uint32_t b = __builtin_bit_cast(uint32_t, x);
-    o.u = x != x ? (uint16_t)((b >> 16) | 0x40) : (uint16_t)((b + 0x7FFF + ((b >> 16) & 1)) >> 16);
+    const float a = __builtin_fabsf(z);
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
+    e = __builtin_amdgcn_exp2f(a * a * -0.72134752f);
+    float p = 0.0356756443f;
+    p = __builtin_fmaf(p, t, -0.157206790f);
+    p = __builtin_fmaf(p, t, 0.206360008f);
+    p = __builtin_fmaf(p, t, -0.0536897052f);
+    p = __builtin_fmaf(p, t, 0.128564859f);
+    p = __builtin_fmaf(p, t, 0.0999125095f);
+    p = __builtin_fmaf(p, t, 0.120754113f);
+    p = __builtin_fmaf(p, t, 0.119629289f);
+    const float q = p * t * e;
+    return z < 0.0f ? q : 1.0f - q;
 }
 
-// Phi(z), the normal distribution function.
-__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * (1.0f + erff(z * 0.70710678f)); }
-__device__ __forceinline__ float logistic(float z) { return 1.0f / (1.0f + expf(-z)); }
+// 1 / (1 + exp(-z)) and tanh.  FAST, for results held in bf16: the hardware's exp2 and reciprocal, good to
+// (1 + |z|) 2^-23 or so against bf16's 2^-9.
+template <bool FAST>
+__device__ __forceinline__ float logistic(float z)
+{
+    if (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
+    return 1.0f / (1.0f + expf(-z));
+}
+
+template <bool FAST>
+__device__ __forceinline__ float tanh_of(float z)
+{
+    if (!FAST) return tanhf(z);
+    // near 0 the quotient would cancel: two more terms of the series, off by z^6 17/315 below 0.1
+    const float s = z * z, near = z * __builtin_fmaf(s, __builtin_fmaf(s, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
+    const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * 2.88539008f));
+    return s < 0.01f ? near : far;
+}
 
 // n values through one activation.
-template <int n>
+template <bool FAST, int n>
 __device__ __forceinline__ void activate(float (&z)[n], int act)
 {
     switch (act) {
@@ -52,19 +84,22 @@ __device__ __forceinline__ void activate(float (&z)[n], int act)
         break;
     case HQML_ACT_GELU:
 #pragma unroll
-        for (int k = 0; k < n; ++k) z[k] *= normal_cdf(z[k]);
+        for (int k = 0; k < n; ++k) {
+            float e;
+            z[k] *= normal_cdf(z[k], e);
+        }
         break;
     case HQML_ACT_SILU:
 #pragma unroll
-        for (int k = 0; k < n; ++k) z[k] *= logistic(z[k]);
+        for (int k = 0; k < n; ++k) z[k] *= logistic<FAST>(z[k]);
         break;
     case HQML_ACT_TANH:
 #pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = tanhf(z[k]);
+        for (int k = 0; k < n; ++k) z[k] = tanh_of<FAST>(z[k]);
         break;
     case HQML_ACT_SIGMOID:
 #pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = logistic(z[k]);
+        for (int k = 0; k < n; ++k) z[k] = logistic<FAST>(z[k]);
         break;
     default: break;
     }
@@ -244,93 +279,126 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
 {
     constexpr int TJ = FJ * 16, kRow = TJ * 4, kMask = TJ / 4 - 1;
     static_assert((TJ & (TJ - 1)) == 0, "chunk permutation");
-    constexpr int kPer = PR / 16;   // block rows of a turn
+    constexpr int kGroups = TJ / 8, kRows = 64 / kGroups;   // a wave takes kRows rows of kGroups values of eight at once
+    constexpr int kRounds = PR / kRows, kU = kRounds % 4 == 0 ? 4 : kRounds % 2 == 0 ? 2 : 1;
+    constexpr int kV = (int)sizeof(TC) / 2;                 // 16-byte words of eight values
+    static_assert(PR % kRows == 0 && FI * 16 % PR == 0, "whole turns");
+    constexpr bool kFast = sizeof(TC) == 2;
     const int lane = threadIdx.x & 63;
+    const int c = lane % kGroups * 8, j = j0 + c, n = P.J - j < 8 ? P.J - j : 8;
     float *out = P.part ? P.part + (long long)part * P.I * P.J : nullptr;
+    float bias[8] = {};
+    if (kForward && P.bias && !out)
 #pragma unroll
-    for (int f0 = 0; f0 < FI; f0 += kPer) {
+        for (int k = 0; k < 8; ++k)
+            if (k < n) bias[k] = widen(((const TC *)P.bias)[j + k]);
 #pragma unroll
-        for (int f = 0; f < kPer; ++f)
+    for (int f0 = 0; f0 < FI; f0 += PR / 16) {
+#pragma unroll
+        for (int f = 0; f < PR / 16; ++f)
 #pragma unroll
             for (int g = 0; g < FJ; ++g)
                 *(__attribute__((address_space(3))) f32x4 *)(buf + (f * 16 + (lane & 15)) * kRow +
                                                              (((g * 4 + (lane >> 4)) ^ (lane & kMask & 15)) << 4)) =
                     acc[f0 + f][g];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own writes, read by its other lanes
-        for (int e = lane; e < PR * (TJ / 8); e += 64) {
-            const int r = e / (TJ / 8), c = (e % (TJ / 8)) * 8;
-            const int i = i0 + f0 * 16 + r, j = j0 + c;
-            float v[8];
-            const auto *src = (const __attribute__((address_space(3))) f32x4 *)(buf + r * kRow);
-            const int key = r & kMask & 15;
-            const f32x4 lo = src[(c >> 2) ^ key], hi = src[((c >> 2) + 1) ^ key];
+        for (int round = 0; round < kRounds; round += kU) {
+            const int r0 = round * kRows + lane / kGroups, i_of = i0 + f0 * 16 + r0;
+            const bool wide = P.wide && j < P.J;   // J is a multiple of 8 then
+            u32x4 res[kU][kV];
+            if (kForward && wide && P.residual && !out)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[k] = lo[k], v[4 + k] = hi[k];
-            if (i >= P.I || j >= P.J) continue;
-            const int n = P.J - j < 8 ? P.J - j : 8;
-            if (kAgain) {
-                float worst = 0.0f;
+                for (int u = 0; u < kU; ++u)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) worst += v[k] * 0.0f;
-                if (worst != worst)
-                    for (int k = 0; k < n; ++k) {
-                        const float s = again(i, j + k);
+                    for (int k = 0; k < kV; ++k)
+                        if (i_of + u * kRows < P.I)
+                            res[u][k] = ((const u32x4 *)((const TC *)P.residual + (i_of + u * kRows) * P.ldr + j))[k];
+            float v[kU * 8];
 #pragma unroll
-                        for (int q = 0; q < 8; ++q) v[q] = q == k ? s : v[q];
-                    }
+            for (int u = 0; u < kU; ++u) {
+                const int r = r0 + u * kRows, key = r & kMask & 15;
+                const auto *src = (const __attribute__((address_space(3))) f32x4 *)(buf + r * kRow);
+                const f32x4 lo = src[(c >> 2) ^ key], hi = src[((c >> 2) + 1) ^ key];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[u * 8 + k] = lo[k], v[u * 8 + 4 + k] = hi[k];
+                if (kAgain && i_of + u * kRows < P.I) {
+                    float worst = 0.0f;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) worst += k < n ? v[u * 8 + k] * 0.0f : 0.0f;
+                    if (worst != worst)
+                        for (int k = 0; k < n; ++k) {
+                            const float s = again(i_of + u * kRows, j + k);
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) v[u * 8 + q] = q == k ? s : v[u * 8 + q];
+                        }
+                }
             }
-            if (P.wide) {   // J is a multiple of 8 then
-                if (out) {
-                    f32x4 *o = (f32x4 *)(out + (long long)i * P.J + j);
-                    o[0] = f32x4{v[0], v[1], v[2], v[3]}, o[1] = f32x4{v[4], v[5], v[6], v[7]};
-                    continue;
+            if (out) {
+#pragma unroll
+                for (int u = 0; u < kU; ++u) {
+                    const int i = i_of + u * kRows;
+                    if (i >= P.I) continue;
+                    float *o = out + (long long)i * P.J + j;
+                    if (wide) {
+                        ((f32x4 *)o)[0] = f32x4{v[u * 8], v[u * 8 + 1], v[u * 8 + 2], v[u * 8 + 3]};
+                        ((f32x4 *)o)[1] = f32x4{v[u * 8 + 4], v[u * 8 + 5], v[u * 8 + 6], v[u * 8 + 7]};
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            if (k < n) o[k] = v[u * 8 + k];
+                    }
                 }
-                TC t[8];
-                constexpr int kV = (int)sizeof(t) / 16;
-                u32x4 w[kV];
-                if (kForward && P.bias) {
+                continue;
+            }
+            if (kForward) {
 #pragma unroll
-                    for (int k = 0; k < kV; ++k) w[k] = ((const u32x4 *)((const TC *)P.bias + j))[k];
-                    __builtin_memcpy(t, w, sizeof t);
+                for (int u = 0; u < kU; ++u)
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += widen(t[k]);
-                }
-                if (kForward && P.z) {
-                    f32x4 *o = (f32x4 *)(P.z + (long long)i * P.J + j);
-                    o[0] = f32x4{v[0], v[1], v[2], v[3]}, o[1] = f32x4{v[4], v[5], v[6], v[7]};
-                }
-                if (kForward) activate(v, P.act);
+                    for (int k = 0; k < 8; ++k) v[u * 8 + k] += bias[k];
+                if (P.z)
 #pragma unroll
-                for (int k = 0; k < 8; ++k) v[k] *= P.alpha;
-                if (kForward && P.residual) {
+                    for (int u = 0; u < kU; ++u) {
+                        const int i = i_of + u * kRows;
+                        if (i >= P.I) continue;
+                        float *o = P.z + (long long)i * P.J + j;
+                        if (wide) {
+                            ((f32x4 *)o)[0] = f32x4{v[u * 8], v[u * 8 + 1], v[u * 8 + 2], v[u * 8 + 3]};
+                            ((f32x4 *)o)[1] = f32x4{v[u * 8 + 4], v[u * 8 + 5], v[u * 8 + 6], v[u * 8 + 7]};
+                        } else {
 #pragma unroll
-                    for (int k = 0; k < kV; ++k) w[k] = ((const u32x4 *)((const TC *)P.residual + i * P.ldr + j))[k];
-                    __builtin_memcpy(t, w, sizeof t);
+                            for (int k = 0; k < 8; ++k)
+                                if (k < n) o[k] = v[u * 8 + k];
+                        }
+                    }
+                activate<kFast>(v, P.act);
+            }
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) v[k] += widen(t[k]);
-                }
+            for (int u = 0; u < kU; ++u) {
+                const int i = i_of + u * kRows;
+                if (i >= P.I) continue;
+                TC *o = (TC *)P.c + i * P.ldc + j;
+                if (wide) {
+                    TC t[8];
+                    if (kForward && P.residual) {
+                        __builtin_memcpy(t, res[u], sizeof t);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) narrow(v[k], t[k]);
-                __builtin_memcpy(w, t, sizeof t);
+                        for (int k = 0; k < 8; ++k) narrow(v[u * 8 + k] * P.alpha + widen(t[k]), t[k]);
+                    } else {
 #pragma unroll
-                for (int k = 0; k < kV; ++k) ((u32x4 *)((TC *)P.c + i * P.ldc + j))[k] = w[k];
-            } else if (out) {
+                        for (int k = 0; k < 8; ++k) narrow(v[u * 8 + k] * P.alpha, t[k]);
+                    }
+                    u32x4 w[kV];
+                    __builtin_memcpy(w, t, sizeof t);
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < n) out[(long long)i * P.J + j + k] = v[k];
-            } else {
+                    for (int k = 0; k < kV; ++k) ((u32x4 *)o)[k] = w[k];
+                } else {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (kForward && P.bias && k < n) v[k] += widen(((const TC *)P.bias)[j + k]);
-                    if (kForward && P.z && k < n) P.z[(long long)i * P.J + j + k] = v[k];
-                }
-                if (kForward) activate(v, P.act);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    if (k >= n) continue;
-                    float y = v[k] * P.alpha;
-                    if (kForward && P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j + k]);
-                    narrow(y, ((TC *)P.c)[i * P.ldc + j + k]);
+                    for (int k = 0; k < 8; ++k) {
+                        if (k >= n) continue;
+                        float y = v[u * 8 + k] * P.alpha;
+                        if (kForward && P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j + k]);
+                        narrow(y, o[k]);
+                    }
                 }
             }
         }
@@ -702,7 +770,7 @@ __global__ __launch_bounds__(256) void k_join(Args P, int parts)
         for (int p = 0; p < parts; ++p) v[0] += P.part[p * all + e];
         if (P.bias) v[0] += widen(((const TC *)P.bias)[j]);
         if (P.z) P.z[e] = v[0];
-        activate(v, P.act);
+        activate<sizeof(TC) == 2>(v, P.act);
         float y = v[0] * P.alpha;
         if (P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j]);
         narrow(y, ((TC *)P.c)[i * P.ldc + j]);
