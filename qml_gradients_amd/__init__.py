@@ -432,6 +432,7 @@ class Dense:
         self.cfg = make_dense_config(in_features, out_features, max_batch, dtype, activation, alpha, dev, self.stream)
         self.dtype = torch.bfloat16 if self.cfg.dtype == HQML_DTYPE_BF16 else torch.float32
         self.plain = self.cfg.activation == HQML_ACT_NONE   # the gradient needs no z
+        self._index, self._lib = dev, load()
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self.handle = None
         self.handle = hqml_dense_create(self.cfg)
@@ -447,17 +448,16 @@ class Dense:
         except Exception:
             pass
 
-    def _check(self, t, shape, name, dtype=None):
-        dtype = dtype or self.dtype
-        if t.dtype is not dtype or t.device != self.device:
+    def _check(self, t, shape, name, dtype):
+        if t.dtype is not dtype or t.get_device() != self._index:
             raise TypeError(f"{name} must be {dtype} on {self.device}, got {t.dtype} on {t.device}")
-        if tuple(t.shape) != shape:
+        if t.shape != shape:
             raise ValueError(f"expected shape {shape} for {name}, got {tuple(t.shape)}")
 
-    def _rows(self, t, shape, name):
+    def _rows(self, t, rows, length, name):
         """t, with rows the kernels can walk, and its row stride."""
-        self._check(t, shape, name)
-        rows, length = shape
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (rows, length):
+            self._check(t, (rows, length), name, self.dtype)
         if not t.is_contiguous():
             ld = t.stride(0)
             if (length == 1 or t.stride(1) == 1) and (rows == 1 or length <= ld <= HQML_DENSE_MAX_FEATURES):
@@ -466,39 +466,42 @@ class Dense:
         return t, length
 
     def _queue(self, call, *args):
-        if self._current_stream(self.device.index) == self.stream:
-            return call(self.handle, *args)
-        cuda = self.torch.cuda
-        here = cuda.current_stream(self.device)
-        own = cuda.ExternalStream(self.stream, device=self.device) if self.stream else cuda.default_stream(self.device)
-        own.wait_stream(here)
-        call(self.handle, *args)
-        here.wait_stream(own)
+        if self._current_stream(self._index) == self.stream:
+            rc = call(self.handle, *args)
+        else:
+            cuda = self.torch.cuda
+            here = cuda.current_stream(self.device)
+            own = (cuda.ExternalStream(self.stream, device=self.device) if self.stream
+                   else cuda.default_stream(self.device))
+            own.wait_stream(here)
+            rc = call(self.handle, *args)
+            here.wait_stream(own)
+        if rc != HQML_OK:
+            raise HqmlError(rc, hqml_dense_last_error(self.handle))
 
     def _forward(self, x, w, bias, residual, out, keep):
-        t = self.torch
-        M = x.shape[0]
-        x, ldx = self._rows(x, (M, self.K), "x")
-        w, ldw = self._rows(w, (self.N, self.K), "w")
+        empty, M = self.torch.empty, x.shape[0]
+        x, ldx = self._rows(x, M, self.K, "x")
+        w, ldw = self._rows(w, self.N, self.K, "w")
         if bias is not None:
-            self._check(bias, (self.N,), "bias")
+            self._check(bias, (self.N,), "bias", self.dtype)
             bias = bias.contiguous()
         ldr = 0
         if residual is not None:
-            residual, ldr = self._rows(residual, (M, self.N), "residual")
+            residual, ldr = self._rows(residual, M, self.N, "residual")
         if out is None:
-            y, ldy = t.empty((M, self.N), dtype=self.dtype, device=self.device), self.N
+            y, ldy = empty((M, self.N), dtype=self.dtype, device=self.device), self.N
         else:
-            y, ldy = self._rows(out, (M, self.N), "out")
+            y, ldy = self._rows(out, M, self.N, "out")
             if y is not out:
                 raise ValueError("out must have rows without gaps between their elements")
         z = None
         if keep and not self.plain:
-            z = t.empty((M, self.N), dtype=t.float32, device=self.device)
-        self._queue(hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
+            z = empty((M, self.N), dtype=self.torch.float32, device=self.device)
+        self._queue(self._lib.hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
                     y.data_ptr(), ldy, None if z is None else z.data_ptr())
-        return y if out is None else out, z
+        return y, z
 
     def forward(self, x, w, bias=None, residual=None, out=None):
         """y.  `out` may be the residual itself."""
@@ -511,20 +514,19 @@ class Dense:
     def backward(self, dy, x, w, z=None, input=True, weight=True, bias=True):
         """(dx, dw, db) for dy = dL/dy and the arguments and z of a forward call; those not
         asked for are None.  The residual's gradient is dy."""
-        t = self.torch
-        M = dy.shape[0]
-        dy, lddy = self._rows(dy, (M, self.N), "dy")
-        x, ldx = self._rows(x, (M, self.K), "x")
-        w, ldw = self._rows(w, (self.N, self.K), "w")
+        empty, M = self.torch.empty, dy.shape[0]
+        dy, lddy = self._rows(dy, M, self.N, "dy")
+        x, ldx = self._rows(x, M, self.K, "x")
+        w, ldw = self._rows(w, self.N, self.K, "w")
         if not self.plain:
             if z is None:
                 raise ValueError("the gradient of an activation needs the forward call's z")
-            self._check(z, (M, self.N), "z", t.float32)
+            self._check(z, (M, self.N), "z", self.torch.float32)
             z = z.contiguous()
-        dx = t.empty((M, self.K), dtype=self.dtype, device=self.device) if input else None
-        dw = t.empty((self.N, self.K), dtype=self.dtype, device=self.device) if weight else None
-        db = t.empty((self.N,), dtype=self.dtype, device=self.device) if bias else None
-        self._queue(hqml_dense_backward, M, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
+        dx = empty((M, self.K), dtype=self.dtype, device=self.device) if input else None
+        dw = empty((self.N, self.K), dtype=self.dtype, device=self.device) if weight else None
+        db = empty((self.N,), dtype=self.dtype, device=self.device) if bias else None
+        self._queue(self._lib.hqml_dense_backward, M, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if self.plain else z.data_ptr(), dx.data_ptr() if input else None, self.K,
                     dw.data_ptr() if weight else None, db.data_ptr() if bias else None)
         return dx, dw, db

@@ -10,86 +10,48 @@
 #include <algorithm>
 
 #include "hqml_gemm.hpp"
+#include "hqml_ops.hpp"
 
 namespace hqml {
 namespace {
 
 using namespace gemm;
 
-// z becomes d act / dz.
-template <bool FAST, int n>
-__device__ __forceinline__ void slope(float (&z)[n], int act)
-{
-    switch (act) {
-    case HQML_ACT_RELU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = z[k] > 0.0f ? 1.0f : 0.0f;
-        break;
-    case HQML_ACT_GELU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            float e;
-            const float f = normal_cdf(z[k], e);
-            z[k] = f + z[k] * e * 0.39894228f;
-        }
-        break;
-    case HQML_ACT_SILU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const float f = logistic<FAST>(z[k]);
-            z[k] = f * (1.0f + z[k] * (1.0f - f));
-        }
-        break;
-    case HQML_ACT_TANH:
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const float t = tanh_of<FAST>(z[k]);
-            z[k] = 1.0f - t * t;
-        }
-        break;
-    case HQML_ACT_SIGMOID:
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            const float f = logistic<FAST>(z[k]);
-            z[k] = f * (1.0f - f);
-        }
-        break;
-    default: break;
-    }
-}
-
-constexpr size_t kPartBytes = 64u << 20;   // most that partial sums take
-constexpr int kMostParts = 64;
-
-// How a product is cut up.
-struct Cut {
-    Shape shape;
-    int parts, k_part;
-};
+// Work is split over k where a product has fewer tiles than kFewTiles: into parts of kPartK at least, as many
+// as make kPartTiles of them.
+constexpr int kFewTiles = 256, kPartTiles = 512, kPartK = 128;
 
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-Cut cut(int I, int J, int K, bool direct, size_t part_bytes)
+// The most tiles of partial sums that products of up to I rows leave.
+size_t part_tiles(size_t I, size_t J, size_t K)
 {
-    auto tiles = [&](int n) { return (long long)ceil_div(I, n) * ceil_div(J, n); };
-    Cut c{TILE_64, 1, (K + 63) / 64 * 64};
-    if (direct && tiles(256) >= 192) c.shape = TILE_256;
-    else if (tiles(128) >= 256) c.shape = TILE_128;
-    if (c.shape == TILE_64 && tiles(64) < 256) {
-        long long parts = std::min<long long>(512 / tiles(64), K / 128);
-        parts = std::min<long long>(parts, kMostParts);
-        parts = std::min<long long>(parts, (long long)(part_bytes / ((size_t)I * J * 4)));
-        if (parts > 1) {
-            c.k_part = ceil_div(ceil_div(K, (int)parts), 64) * 64;
-            c.parts = ceil_div(K, c.k_part);
-        }
-    }
-    return c;
+    if (K < 2 * kPartK) return 0;
+    const size_t tiles = ((I + 63) / 64) * ((J + 63) / 64);
+    return std::min<size_t>(kPartTiles, tiles * (K / kPartK));
 }
 
 bool aligned(const void *p, long long ld, size_t elem)
 {
     return (uintptr_t)p % 16 == 0 && ld * (long long)elem % 16 == 0;
+}
+
+// Cuts a product into tiles of `side` and, if they are the 64 x 64 ones and few, its k into parts, whose
+// sums go to the workspace.
+void cut(Args &P, int side, const DenseWorkspace &ws)
+{
+    P.tiles_i = ceil_div(P.I, side);
+    P.tiles_j = ceil_div(P.J, side);
+    P.parts = 1;
+    P.k_part = ceil_div(P.K, 32) * 32;
+    const long long tiles = (long long)P.tiles_i * P.tiles_j;
+    if (side != 64 || tiles >= kFewTiles) return;
+    const int parts = std::min((int)(kPartTiles / tiles), P.K / kPartK);
+    if (parts < 2) return;
+    P.k_part = ceil_div(ceil_div(P.K, parts), 32) * 32;
+    P.parts = ceil_div(P.K, P.k_part);
+    P.part = ws.part;
+    P.ticket = ws.ticket;
 }
 
 // Runs one product; P holds everything but its cut.
@@ -98,19 +60,12 @@ hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStre
 {
     const bool direct = sizeof(T) == 2 && aligned(P.a, P.lda, 2) && aligned(P.b, P.ldb, 2) &&
                         ((la == K_COLS && lb == K_COLS) || P.K % 8 == 0);
-    P.wide = aligned(P.c, P.ldc, sizeof(T)) && P.J % 8 == 0 && (!P.bias || aligned(P.bias, 0, sizeof(T))) &&
+    P.wide = aligned(P.c, P.ldc, sizeof(T)) && P.J % 8 == 0 &&
              (!P.residual || aligned(P.residual, P.ldr, sizeof(T))) && (!P.z || aligned(P.z, 0, 4));
-    const Cut c = cut(P.I, P.J, P.K, direct, ws.part_bytes);
-    const int side = c.shape == TILE_64 ? 64 : c.shape == TILE_128 ? 128 : 256;
-    P.tiles_i = ceil_div(P.I, side), P.tiles_j = ceil_div(P.J, side);
-    P.k_part = c.k_part;
-    P.part = c.parts > 1 ? ws.part : nullptr;
-    const hipError_t e = sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, c.shape, c.parts, s)
-                                        : launch_fp32(P, la, lb, c.shape, c.parts, s);
-    if (e != hipSuccess || c.parts == 1) return e;
-    const long long all = (long long)P.I * P.J;
-    k_join<T><<<(unsigned)std::min<long long>((all + 255) / 256, 4096), 256, 0, s>>>(P, c.parts);
-    return hipGetLastError();
+    auto tiles = [&](int n) { return (long long)ceil_div(P.I, n) * ceil_div(P.J, n); };
+    const Shape shape = direct && tiles(256) >= 192 ? TILE_256 : tiles(128) >= 256 ? TILE_128 : TILE_64;
+    cut(P, shape == TILE_64 ? 64 : shape == TILE_128 ? 128 : 256, ws);
+    return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, shape, s) : launch_fp32(P, la, lb, shape, s);
 }
 
 constexpr int kRowChunk = 64;    // rows whose dz one workgroup forms and sums
@@ -213,6 +168,30 @@ hipError_t zero(void *p, long long n, hipStream_t s)
     return hipGetLastError();
 }
 
+// Tiles and waves of a small product or two.
+void cut_small(Args &P, int fi)
+{
+    P.tiles_i = ceil_div(P.I, 16 * fi);
+    P.tiles_j = ceil_div(P.J + (P.ones ? 1 : 0), 16);
+}
+
+long long small_tiles(const Args &P, int fi)
+{
+    return (long long)ceil_div(P.I, 16 * fi) * ceil_div(P.J + (P.ones ? 1 : 0), 16);
+}
+
+int small_waves(int K, long long tiles, int most)
+{
+    int waves = 1;
+    while (waves < most && waves * 2 <= ceil_div(K, 32) && tiles * waves < 4096) waves *= 2;
+    return waves;
+}
+
+bool small(int M, int N, int K)
+{
+    return (long long)M * N * K <= 1ll << 27;
+}
+
 template <typename T>
 hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t s)
 {
@@ -224,7 +203,37 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
     P.bias = a.bias, P.residual = a.residual, P.ldr = a.ldr;
     P.z = a.act == HQML_ACT_NONE ? nullptr : (float *)a.z;
     P.act = a.act, P.alpha = a.alpha;
+    if (small(a.M, a.N, a.K)) {
+        const int fi = small_tiles(P, 4) >= 512 ? 4 : 1;
+        cut_small(P, fi);
+        return launch_small_forward(P, sizeof(T) == 2, fi, small_waves(P.K, small_tiles(P, fi), fi == 1 ? 16 : 8), s);
+    }
     return run_product<T>(P, K_ROWS, K_ROWS, ws, s);
+}
+
+template <typename T>
+hipError_t gradients(const DenseBackward &a, hipStream_t s)
+{
+    Args X{}, W{};
+    X.a = W.a = a.dy, X.lda = W.lda = a.lddy;
+    X.z = W.z = const_cast<float *>(a.z);
+    X.act = W.act = a.act, X.alpha = W.alpha = a.alpha;
+    if (a.dx) {
+        X.b = a.w, X.ldb = a.ldw;
+        X.I = a.M, X.J = a.K, X.K = a.N;
+        X.c = a.dx, X.ldc = a.lddx;
+    }
+    if (a.dw || a.db) {
+        W.b = a.x, W.ldb = a.ldx;
+        W.I = a.N, W.J = a.dw ? a.K : 0, W.K = a.M;
+        W.c = a.dw, W.ldc = a.K;
+        W.ones = a.db;
+    }
+    const int fi = small_tiles(X, 4) + small_tiles(W, 4) >= 512 ? 4 : 1;
+    cut_small(X, fi);
+    cut_small(W, fi);
+    const int waves = small_waves(std::max(X.K, W.K), small_tiles(X, fi) + small_tiles(W, fi), 8);
+    return launch_small_gradients(X, W, sizeof(T) == 2, fi, waves, s);
 }
 
 template <typename T>
@@ -235,6 +244,7 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         e = zero<T>(a.dw, (long long)a.N * a.K, s);
         return e != hipSuccess ? e : zero<T>(a.db, a.N, s);
     }
+    if (small(a.M, a.N, a.K)) return gradients<T>(a, s);
     const T *dz = (const T *)a.dy;
     long long lddz = a.lddy;
     float alpha = a.alpha;
@@ -287,9 +297,10 @@ DenseWorkspace dense_workspace(const hqml_dense_config &cfg)
     const size_t M = (size_t)cfg.max_batch, N = (size_t)cfg.out_features;
     if (cfg.activation != HQML_ACT_NONE) ws.dz_bytes = M * N * (cfg.dtype == HQML_DTYPE_BF16 ? 2 : 4);
     ws.rows_bytes = (M + kRowChunk - 1) / kRowChunk * N * 4;
-    // partial sums: up to kMostParts of the largest result
-    const size_t K = (size_t)cfg.in_features, most = std::max({M * N, M * K, N * K});
-    ws.part_bytes = std::min(kPartBytes, most * 4 * kMostParts);
+    const size_t K = (size_t)cfg.in_features;
+    const size_t tiles = std::max({part_tiles(M, N, K), part_tiles(M, K, N), part_tiles(N, K, M)});
+    ws.part_bytes = tiles * 64 * 64 * 4;
+    ws.ticket_bytes = tiles * sizeof(unsigned);
     return ws;
 }
 

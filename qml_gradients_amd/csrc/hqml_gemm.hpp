@@ -15,98 +15,16 @@
 // LDS and works on eight neighbouring values of a row: one 16-byte access in bf16.
 #pragma once
 #include <hip/hip_runtime.h>
-#include <math.h>
 #include <stdint.h>
 
-#include "hqml_ops.hpp"
+#include "hqml_act.hpp"
 
 namespace hqml {
 namespace gemm {
 
-struct bf16 {
-    uint16_t u;
-};
-
-__device__ __forceinline__ float widen(float x) { return x; }
-__device__ __forceinline__ float widen(bf16 x) { return __builtin_bit_cast(float, (uint32_t)x.u << 16); }
-__device__ __forceinline__ void narrow(float x, float &o) { o = x; }
-// round to nearest even; a NaN stays one
-__device__ __forceinline__ void narrow(float x, bf16 &o) { o.u = __builtin_bit_cast(uint16_t, (__bf16)x); }
-
-// Phi(z), the normal distribution function, and e = exp(-z^2 / 2).  With t = 1 / (1 + 0.3 |z|),
-// Phi(-|z|) exp(z^2 / 2) / t is smooth in t on (0, 1]; the polynomial is its least largest relative
-// error there, 1.5e-7 (weighted least squares, reweighted to the largest error), and 2e-7 is what fp32
-// adds.  So the tail keeps its relative precision.  An eighth of erff and expf's instructions.
-__device__ __forceinline__ float normal_cdf(float z, float &e)
-{
-    const float a = __builtin_fabsf(z);
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, a, 1.0f));
-    e = __builtin_amdgcn_exp2f(a * a * -0.72134752f);
-    float p = 0.0356756443f;
-    p = __builtin_fmaf(p, t, -0.157206790f);
-    p = __builtin_fmaf(p, t, 0.206360008f);
-    p = __builtin_fmaf(p, t, -0.0536897052f);
-    p = __builtin_fmaf(p, t, 0.128564859f);
-    p = __builtin_fmaf(p, t, 0.0999125095f);
-    p = __builtin_fmaf(p, t, 0.120754113f);
-    p = __builtin_fmaf(p, t, 0.119629289f);
-    const float q = p * t * e;
-    return z < 0.0f ? q : 1.0f - q;
-}
-
-// 1 / (1 + exp(-z)) and tanh.  FAST, for results held in bf16: the hardware's exp2 and reciprocal, good to
-// (1 + |z|) 2^-23 or so against bf16's 2^-9.
-template <bool FAST>
-__device__ __forceinline__ float logistic(float z)
-{
-    if (FAST) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
-    return 1.0f / (1.0f + expf(-z));
-}
-
-template <bool FAST>
-__device__ __forceinline__ float tanh_of(float z)
-{
-    if (!FAST) return tanhf(z);
-    // near 0 the quotient would cancel: two more terms of the series, off by z^6 17/315 below 0.1
-    const float s = z * z, near = z * __builtin_fmaf(s, __builtin_fmaf(s, 2.0f / 15.0f, -1.0f / 3.0f), 1.0f);
-    const float far = 1.0f - 2.0f * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * 2.88539008f));
-    return s < 0.01f ? near : far;
-}
-
-// n values through one activation.
-template <bool FAST, int n>
-__device__ __forceinline__ void activate(float (&z)[n], int act)
-{
-    switch (act) {
-    case HQML_ACT_RELU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = z[k] < 0.0f ? 0.0f : z[k];
-        break;
-    case HQML_ACT_GELU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) {
-            float e;
-            z[k] *= normal_cdf(z[k], e);
-        }
-        break;
-    case HQML_ACT_SILU:
-#pragma unroll
-        for (int k = 0; k < n; ++k) z[k] *= logistic<FAST>(z[k]);
-        break;
-    case HQML_ACT_TANH:
-#pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = tanh_of<FAST>(z[k]);
-        break;
-    case HQML_ACT_SIGMOID:
-#pragma unroll
-        for (int k = 0; k < n; ++k) z[k] = logistic<FAST>(z[k]);
-        break;
-    default: break;
-    }
-}
-
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
+using f32x2 = __attribute__((ext_vector_type(2))) float;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 using lds_char = __attribute__((address_space(3))) char;
@@ -126,10 +44,12 @@ struct Args {
     float *z;                // [I][J], sum + bias
     int act;
     float alpha;
-    int wide;                // every row of c, residual and z, and bias, allows 16-byte access
-    // work split over k
-    int k_part;              // k of one part, a multiple of BK
-    float *part;             // [parts][I][J]: sums of one part, no epilogue; null: whole sums
+    int wide;                // J, and every row of c, residual and z, allow 16-byte access
+    void *ones;              // [I]: the sums of A's rows, as a column J of B that is all ones; or null
+    // work split over k: every part leaves its sums, the last one of a tile to finish adds them up
+    int parts, k_part;       // k of one part, a multiple of 32
+    float *part;             // [tiles][parts][BM * BN]
+    unsigned *ticket;        // [tiles], 0 between calls
 };
 
 // Tile of a workgroup.  Workgroups go round the eight XCDs in turn; each XCD takes a run of
@@ -269,13 +189,65 @@ struct DirectTile {
     }
 };
 
+// Work split over k.  A workgroup leaves its sums in the workspace and takes a ticket; the one that
+// takes a tile's last adds all parts in their order (the result does not depend on who came
+// last) and finishes the tile.  Says whether this workgroup is the one.  The sums are written
+// and read as device-scope atomics, past the caches that the XCDs do not share, and have
+// arrived when the ticket is taken: a fence would write back a whole L2 for each of them (serve
+// 4096 -> 4096: 32 us with fences).
+template <int FI, int FJ, int THREADS>
+__device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int tile, int part, int i0)
+{
+    __shared__ unsigned taken;
+    constexpr int kWords = FI * FJ * 2;   // pairs of sums of a lane
+    unsigned long long *all = (unsigned long long *)P.part + (long long)tile * P.parts * (kWords * THREADS) + threadIdx.x;
+    unsigned long long *own = all + (long long)part * (kWords * THREADS);
+    const int rows = P.I - i0 - (threadIdx.x & 15);   // a lane's row of block f exists if 16 f < rows
+#pragma unroll
+    for (int f = 0; f < FI; ++f) {
+        if (f * 16 >= rows) continue;
+#pragma unroll
+        for (int g = 0; g < FJ; ++g)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const f32x2 pair = {acc[f][g][2 * h], acc[f][g][2 * h + 1]};
+                __hip_atomic_store(own + ((f * FJ + g) * 2 + h) * THREADS, __builtin_bit_cast(unsigned long long, pair),
+                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+    }
+    wait_loads<0>();   // and stores: this wave's have arrived
+    __syncthreads();   // every wave's have
+    if (threadIdx.x == 0)
+        taken = __hip_atomic_fetch_add(P.ticket + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (taken != (unsigned)P.parts - 1) return false;
+#pragma unroll
+    for (int f = 0; f < FI; ++f) {
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (f * 16 >= rows) continue;
+        for (int p = 0; p < P.parts; ++p)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const unsigned long long w =
+                        __hip_atomic_load(all + ((long long)p * kWords + (f * FJ + g) * 2 + h) * THREADS,
+                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                    acc[f][g][2 * h] += __builtin_bit_cast(float, (uint32_t)w);
+                    acc[f][g][2 * h + 1] += __builtin_bit_cast(float, (uint32_t)(w >> 32));
+                }
+    }
+    if (threadIdx.x == 0) __hip_atomic_store(P.ticket + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return true;
+}
+
 // Epilogue of a wave's TI x TJ part (16 x 16 blocks acc[FI][FJ], four j of row lane % 16 a lane)
 // that begins at (i0, j0) of C; buf: this wave's own LDS, PR rows of TJ floats, whose 16-byte
 // chunks are permuted by the row (a lane writes one chunk of its row).
 // Only a forward product has more to finish than alpha.  again(i, j): the sum at (i, j) formed anew where it is not finite (kAgain).
 template <typename TC, int FI, int FJ, int PR, bool kForward, bool kAgain, typename F>
-__device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int i0, int j0, int part, lds_char *buf,
-                                       F again)
+__device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int i0, int j0, lds_char *buf, F again)
 {
     constexpr int TJ = FJ * 16, kRow = TJ * 4, kMask = TJ / 4 - 1;
     static_assert((TJ & (TJ - 1)) == 0, "chunk permutation");
@@ -286,9 +258,19 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
     constexpr bool kFast = sizeof(TC) == 2;
     const int lane = threadIdx.x & 63;
     const int c = lane % kGroups * 8, j = j0 + c, n = P.J - j < 8 ? P.J - j : 8;
-    float *out = P.part ? P.part + (long long)part * P.I * P.J : nullptr;
+    bool bad = false;   // a sum of this wave is not finite
+    if (kAgain) {
+        float worst = 0.0f;
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) worst = __builtin_fmaf(acc[f][g][k], 0.0f, worst);
+        bad = __any(worst != 0.0f);
+    }
     float bias[8] = {};
-    if (kForward && P.bias && !out)
+    if (kForward && P.bias)
 #pragma unroll
         for (int k = 0; k < 8; ++k)
             if (k < n) bias[k] = widen(((const TC *)P.bias)[j + k]);
@@ -302,11 +284,20 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
                                                              (((g * 4 + (lane >> 4)) ^ (lane & kMask & 15)) << 4)) =
                     acc[f0 + f][g];
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // the wave's own writes, read by its other lanes
+        if (kAgain && bad) {
+#pragma unroll 1
+            for (int e = lane; e < PR * TJ; e += 64) {
+                const int r = e / TJ, q = e % TJ, i = i0 + f0 * 16 + r, col = j0 + q;
+                auto *at = (__attribute__((address_space(3))) float *)(buf + r * kRow + (((q >> 2) ^ (r & kMask & 15)) << 4)) + (q & 3);
+                if (i < P.I && col < P.J && *at * 0.0f != 0.0f) *at = again(i, col);
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        }
         for (int round = 0; round < kRounds; round += kU) {
             const int r0 = round * kRows + lane / kGroups, i_of = i0 + f0 * 16 + r0;
             const bool wide = P.wide && j < P.J;   // J is a multiple of 8 then
             u32x4 res[kU][kV];
-            if (kForward && wide && P.residual && !out)
+            if (kForward && wide && P.residual)
 #pragma unroll
                 for (int u = 0; u < kU; ++u)
 #pragma unroll
@@ -321,34 +312,6 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
                 const f32x4 lo = src[(c >> 2) ^ key], hi = src[((c >> 2) + 1) ^ key];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) v[u * 8 + k] = lo[k], v[u * 8 + 4 + k] = hi[k];
-                if (kAgain && i_of + u * kRows < P.I) {
-                    float worst = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) worst += k < n ? v[u * 8 + k] * 0.0f : 0.0f;
-                    if (worst != worst)
-                        for (int k = 0; k < n; ++k) {
-                            const float s = again(i_of + u * kRows, j + k);
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) v[u * 8 + q] = q == k ? s : v[u * 8 + q];
-                        }
-                }
-            }
-            if (out) {
-#pragma unroll
-                for (int u = 0; u < kU; ++u) {
-                    const int i = i_of + u * kRows;
-                    if (i >= P.I) continue;
-                    float *o = out + (long long)i * P.J + j;
-                    if (wide) {
-                        ((f32x4 *)o)[0] = f32x4{v[u * 8], v[u * 8 + 1], v[u * 8 + 2], v[u * 8 + 3]};
-                        ((f32x4 *)o)[1] = f32x4{v[u * 8 + 4], v[u * 8 + 5], v[u * 8 + 6], v[u * 8 + 7]};
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            if (k < n) o[k] = v[u * 8 + k];
-                    }
-                }
-                continue;
             }
             if (kForward) {
 #pragma unroll
@@ -505,7 +468,7 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
 
     int ti, tj;
     tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
-    const int kb = blockIdx.y * P.k_part;
+    const int part = blockIdx.y, kb = part * P.k_part;
     const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
     const int wave = threadIdx.x >> 6;
     D d;
@@ -539,27 +502,32 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
     }
     wait_loads<0>();
     barrier();
-    // each buffer serves a quarter of the waves
-    constexpr int kOwn = (TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes);
-    constexpr int kFit = kOwn / (TJ * 4);
-    static_assert(kWaves % 4 == 0 && kWaves <= 8 && kFit >= 16, "room for one block row");
+    if (P.parts > 1 && !joined<FI, FJ, 64 * kWaves>(P, d.acc, ti * P.tiles_j + tj, part, ti * BM + d.wi * TI)) return;
+    // each wave has a buffer of its own
+    constexpr int kOwn = TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes, kFit = kOwn / (TJ * 4);
+    static_assert(kWaves <= 8 && kFit >= 16, "room for one block row");
     constexpr int PR = kFit >= TI ? TI : kFit;
-    lds_char *const own = wave == 0 ? (lds_char *)a0 : wave == 1 ? (lds_char *)a1 : wave == 2 ? (lds_char *)a2 : wave==3 ? (lds_char *)a3 : wave==4 ? (lds_char*)b0 : wave==5?(lds_char*)b1:wave==6?(lds_char*)b2:(lds_char*)b3;
-    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, d.acc, ti * BM + d.wi * TI, tj * BN + d.wj * TJ, blockIdx.y, own,
-                                    [](int, int) { return 0.0f; });
+    lds_char *const own = wave == 0   ? (lds_char *)a0
+                          : wave == 1 ? (lds_char *)a1
+                          : wave == 2 ? (lds_char *)a2
+                          : wave == 3 ? (lds_char *)a3
+                          : wave == 4 ? (lds_char *)b0
+                          : wave == 5 ? (lds_char *)b1
+                          : wave == 6 ? (lds_char *)b2
+                                      : (lds_char *)b3;
+    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, d.acc, ti * BM + d.wi * TI, tj * BN + d.wj * TJ,
+                                                                  own, [](int, int) { return 0.0f; });
 }
 
-// One operand tile that goes through registers on its way to LDS: 32-bit operands, which are
-// split there, and bf16 rows that do not allow 16-byte access to LDS.  The LDS layout is
-// DirectTile's, PLANES times.  Loads into registers take 16 bytes at any alignment of the element;
-// where a chunk may pass the end of its row, its values are loaded one by one.  A 32-bit value is the sum of PLANES bf16 values to 8 PLANES + 1 bits or so
-// (exactly, with three, where none underflows): x = h + m + l, each the rounding of what the
-// ones before leave.
-template <typename T, int PLANES, int L, int R, int BK, int THREADS>
-struct StagedTile {
-    using Tile = DirectTile<L, R, BK, THREADS / 64>;
-    static constexpr int kPlane = R * BK * 2, kBytes = kPlane * PLANES;
-    static constexpr int kN = R * BK / 8 / THREADS;   // 8-value chunks of a lane
+// One operand tile on its way through registers: kSets steps of it, 8-value chunks, loaded 16 bytes
+// at a time at any alignment of the element; where a chunk may pass the end of its row (K_ROWS:
+// the last k; K_COLS: the last row of the operand), one value at a time.
+constexpr int kSets = 2;
+
+template <typename T, int L, int R, int BK, int THREADS>
+struct Chunks {
+    using Tile = DirectTile<L, R, BK, THREADS / 64>;   // whose LDS layout the chunks follow
+    static constexpr int kN = R * BK / 8 / THREADS;    // chunks of a lane
     static_assert(kN >= 1 && R * BK / 8 % THREADS == 0, "whole chunks");
     static constexpr int kSize = (int)sizeof(T), kWords = kSize * 2;   // registers of a chunk
 
@@ -568,8 +536,7 @@ struct StagedTile {
     int rows, K;
     int off[kN];
     int at[kN];     // first k (K_COLS: first row) of a lane's chunk in the tile
-    int put;        // its LDS byte; chunk n lies n * THREADS * 16 further
-    uint32_t reg[kN][kWords];
+    uint32_t reg[kSets][kN][kWords];
 
     __device__ __forceinline__ void init(const void *p, long long ld_elems, int row0, int n_rows, int n_k, int k0)
     {
@@ -584,10 +551,10 @@ struct StagedTile {
             off[n] = (int)(r * ld) + c * 8 * kSize;
             at[n] = c * 8;
         }
-        put = threadIdx.x * 16;
     }
 
-    // Load the tile at k into registers.
+    // Load the tile at k into set SET; past the end: an empty buffer, nothing is read.
+    template <int SET>
     __device__ __forceinline__ void load(int k)
     {
         const int left = K - k;
@@ -600,7 +567,7 @@ struct StagedTile {
             p = base + k * ld;
             bytes = (long long)(left - 1) * ld + (long long)rows * kSize;
         }
-        const int end = left <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
+        const int end = left <= 0 || rows <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
         const int stop = L == K_ROWS ? left : rows;   // values of the chunk's direction that exist
         const bool tail = L == K_ROWS ? left < BK : rows < R;
@@ -611,7 +578,7 @@ struct StagedTile {
                 for (int h = 0; h < kWords / 4; ++h) {
                     const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off[n] + h * 16, 0, 0);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) reg[n][h * 4 + q] = w[q];
+                    for (int q = 0; q < 4; ++q) reg[SET][n][h * 4 + q] = w[q];
                 }
                 continue;
             }
@@ -619,162 +586,423 @@ struct StagedTile {
             for (int e = 0; e < 8; ++e) {
                 const int o = at[n] + e < stop ? off[n] + e * kSize : 0x7FFFFFF0;
                 if (kSize == 4) {
-                    reg[n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
+                    reg[SET][n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
                 } else {
                     const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
-                    if (e & 1) reg[n][e / 2] |= v << 16;
-                    else reg[n][e / 2] = v;
+                    if (e & 1) reg[SET][n][e / 2] |= v << 16;
+                    else reg[SET][n][e / 2] = v;
                 }
             }
         }
     }
 
-    // Split what load() brought and write it to LDS.
+    template <int SET>
+    __device__ __forceinline__ void values(float (&x)[8], int n) const
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (kSize == 4) x[e] = __builtin_bit_cast(float, reg[SET][n][e % kWords]);
+            else x[e] = __builtin_bit_cast(float, e & 1 ? reg[SET][n][e / 2] & 0xFFFF0000u : reg[SET][n][e / 2] << 16);
+        }
+    }
+};
+
+// x as PLANES bf16 values each, chunk by chunk into LDS planes kPlane bytes apart.  A 32-bit value is the
+// sum of its planes to 8 bits and a rounding a plane (exactly, with three, where none
+// underflows): x = h + m + l, each the rounding of what the ones before leave.
+template <int PLANES, int kPlane>
+__device__ __forceinline__ void split(lds_char *dst, float (&x)[8])
+{
+#pragma unroll
+    for (int p = 0; p < PLANES; ++p) {
+        bf16x8 h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            h[e] = (__bf16)x[e];
+            if (p + 1 < PLANES) x[e] -= (float)h[e];
+        }
+        *(__attribute__((address_space(3))) bf16x8 *)(dst + p * kPlane) = h;
+    }
+}
+
+// A stored operand as planes.
+template <typename T, int PLANES_, int L_, int R, int THREADS>
+struct Stored {
+    static constexpr int PLANES = PLANES_, L = L_, BK = 32, kPlane = R * BK * 2, kBytes = kPlane * PLANES;
+    using C = Chunks<T, L, R, BK, THREADS>;
+    using Tile = typename C::Tile;
+    C c;
+
+    __device__ __forceinline__ void init(const Args &P, bool second, int row0, int n_k, int k0)
+    {
+        if (second) c.init(P.b, P.ldb, row0, P.J, n_k, k0);
+        else c.init(P.a, P.lda, row0, P.I, n_k, k0);
+    }
+    template <int SET>
+    __device__ __forceinline__ void load(int k)
+    {
+        c.template load<SET>(k);
+    }
+    template <int SET>
     __device__ __forceinline__ void store(lds_char *to) const
     {
 #pragma unroll
-        for (int n = 0; n < kN; ++n) {
-            lds_char *dst = to + put + n * THREADS * 16;
-            if (kSize == 2) {
-                *(__attribute__((address_space(3))) u32x4 *)dst = u32x4{reg[n][0], reg[n][1], reg[n][2], reg[n][3]};
+        for (int n = 0; n < C::kN; ++n) {
+            lds_char *dst = to + (n * THREADS + threadIdx.x) * 16;
+            if (C::kSize == 2) {
+                *(__attribute__((address_space(3))) u32x4 *)dst =
+                    u32x4{c.reg[SET][n][0], c.reg[SET][n][1], c.reg[SET][n][2], c.reg[SET][n][3]};
             } else {
                 float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = __builtin_bit_cast(float, reg[n][e % kWords]);
-#pragma unroll
-                for (int p = 0; p < PLANES; ++p) {
-                    bf16x8 h;
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        h[e] = (__bf16)x[e];
-                        if (p + 1 < PLANES) x[e] -= (float)h[e];
-                    }
-                    *(__attribute__((address_space(3))) bf16x8 *)(dst + p * kPlane) = h;
-                }
+                c.template values<SET>(x, n);
+                split<PLANES, kPlane>(dst, x);
             }
         }
+    }
+    // One value: row r, k.
+    static __device__ __forceinline__ float value(const Args &P, bool second, int r, int k)
+    {
+        const T *p = (const T *)(second ? P.b : P.a);
+        const long long ld = second ? P.ldb : P.lda;
+        return widen(p[L == K_ROWS ? r * ld + k : k * ld + r]);
     }
 };
 
 // The sum at (i, j) by itself, in fp32: for values whose split does not hold (infinities, and
 // magnitudes that round up to one).
-template <typename T, typename U, int LA, int LB>
-__device__ __attribute__((noinline)) float plain_sum(const T *a, const U *b, long long lda, long long ldb, int i, int j, int k0, int n)
+template <class A, class B>
+__device__ __forceinline__ float plain_sum(const Args &P, int i, int j)
 {
     float s = 0.0f;
-    for (int k = k0; k < k0 + n; ++k)
-        s += widen(LA == K_ROWS ? a[i * lda + k] : a[k * lda + i]) * widen(LB == K_ROWS ? b[j * ldb + k] : b[k * ldb + j]);
+    for (int k = 0; k < P.K; ++k) s += A::value(P, false, i, k) * B::value(P, true, j, k);
     return s;
 }
 
-// Operands of type T and U held as PA and PB bf16 planes; of the products of planes those are
-// formed that reach the sum's 24 bits: 6 for 3 x 3 planes, whose left-out ones are below 2^-24 of the
-// product of magnitudes.  Step t + 1 is loaded into registers while step t is computed.  With
-// BUF = 2 its split and its way to LDS fall between step t's matrix instructions, at one barrier
-// a step; with BUF = 1 they come after, and two workgroups share a compute unit, so that one
-// computes while the other stores.  2048^3 in fp32 (256 tiles, one a compute unit): 91 us with
-// two buffers, 102 with one; 4096^3 (1024 tiles): 693 and 640.
-template <typename T, int PA, int LA, typename U, int PB, int LB, typename TC, int BM, int BN, int WI, int WJ, int BUF>
-__global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
-{
-    constexpr int BK = 32, kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16,
-                  FJ = TJ / 16;
-    using TA = StagedTile<T, PA, LA, BM, BK, kThreads>;
-    using TB = StagedTile<U, PB, LB, BN, BK, kThreads>;
-    constexpr int kTurn = TI < 32 ? TI : 32;   // rows of a wave's part turned at once
-    constexpr int kTurnBytes = kTurn * TJ * 4;
-    constexpr int kTiles = TA::kBytes + TB::kBytes;
-    constexpr int kLds = kTiles * BUF > kWaves * kTurnBytes ? kTiles * BUF : kWaves * kTurnBytes;
-    __shared__ __attribute__((aligned(1024))) char lds[kLds];
-    lds_char *here = (lds_char *)lds, *next = here + (BUF - 1) * kTiles;
+// A product whose operands A and B go through registers and are held in LDS as bf16 planes; of the
+// products of planes those are formed that reach the sum's 24 bits: 6 for 3 x 3 planes, whose
+// left-out ones are below 2^-24 of the product of magnitudes.  Steps t + 2 and t + 3 are on their way
+// into registers while step t is computed.  With BUF = 2 the split of step t + 1 and its way to
+// LDS fall between step t's matrix instructions, at one barrier a step; with BUF = 1 they come
+// after, and two workgroups share a compute unit, so that one computes while the other
+// stores.
+template <class A, class B, typename TC, int BM, int BN, int WI, int WJ, int BUF, bool kForward>
+struct Staged {
+    static constexpr int BK = 32, kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16,
+                         FJ = TJ / 16, PA = A::PLANES, PB = B::PLANES, kMost = PA > PB ? PA : PB;
+    static constexpr int kTurn = TI < 32 ? TI : 32;   // rows of a wave's part turned at once
+    static constexpr int kTurnBytes = kTurn * TJ * 4, kTiles = A::kBytes + B::kBytes;
+    static constexpr int kLds = kTiles * BUF > kWaves * kTurnBytes ? kTiles * BUF : kWaves * kTurnBytes;
 
-    int ti, tj;
-    tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
-    const int kb = blockIdx.y * P.k_part;
-    const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
-    TA ta;
-    TB tb;
-    ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
-    tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
-    typename TA::Tile fa_of;   // where a lane's fragments begin
-    typename TB::Tile fb_of;
-    fa_of.init_fragment();
-    fb_of.init_fragment();
-    const int wave = threadIdx.x >> 6, wi = wave / WJ, wj = wave % WJ;
-    f32x4 acc[FI][FJ] = {};
-    ta.load(0);
-    tb.load(0);
-    ta.store(here);
-    tb.store(here + TA::kBytes);
-    ta.load(BK);   // past the last step: an empty buffer, nothing is read
-    tb.load(BK);
-    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
-    barrier();
-    for (int k0 = 0; k0 < kn; k0 += BK) {
-        bf16x8 fb[PB][FJ];
+    A ta;
+    B tb;
+    typename A::Tile fa_of;   // where a lane's fragments begin
+    typename B::Tile fb_of;
+    int wi, wj;
+    f32x4 acc[FI][FJ];
+
+    // Compute step t from here; set SET holds step t + 1.
+    template <int SET>
+    __device__ __forceinline__ void step(lds_char *here, lds_char *next, int t)
+    {
+        bf16x8 fa[PA][FI], fb[PB][FJ];
 #pragma unroll
-        for (int p = 0; p < PB; ++p)
+        for (int p = PB - 1; p >= 0; --p)
 #pragma unroll
             for (int g = 0; g < FJ; ++g)
-                fb[p][g] = fb_of.fragment(here + TA::kBytes + p * TB::kPlane, wj * TJ + g * 16, 0);
+                fb[p][g] = fb_of.fragment(here + A::kBytes + p * B::kPlane, wj * TJ + g * 16, 0);
 #pragma unroll
-        for (int f = 0; f < FI; ++f) {
+        for (int p = PA - 1; p >= 0; --p)
 #pragma unroll
-            for (int p = PA - 1; p >= 0; --p) {
-                const bf16x8 fa = fa_of.fragment(here + p * TA::kPlane, wi * TI + f * 16, 0);
+            for (int f = 0; f < FI; ++f) fa[p][f] = fa_of.fragment(here + p * A::kPlane, wi * TI + f * 16, 0);
+        // small products first
+        constexpr int kPairs = kMost == 3 ? 6 : PA * PB, kFirst = (kPairs - 1) / 3, kSecond = (kPairs - 1) * 2 / 3;
+        int pair = 0;
 #pragma unroll
-                for (int q = PB - 1; q >= 0; --q) {
-                    if (p + q >= (PA > PB ? PA : PB)) continue;
+        for (int sum = kMost - 1; sum >= 0; --sum)
+#pragma unroll
+            for (int p = 0; p < PA; ++p) {
+                const int q = sum - p;
+                if (q < 0 || q >= PB) continue;
+#pragma unroll
+                for (int f = 0; f < FI; ++f)
 #pragma unroll
                     for (int g = 0; g < FJ; ++g)
-                        acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa, acc[f][g], 0, 0, 0);
+                        acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa[p][f], acc[f][g], 0, 0, 0);
+                if (BUF == 2 && pair == kFirst) {
+                    ta.template store<SET>(next);
+                    ta.template load<SET>((t + 1 + kSets) * BK);
                 }
+                if (BUF == 2 && pair == kSecond) {
+                    tb.template store<SET>(next + A::kBytes);
+                    tb.template load<SET>((t + 1 + kSets) * BK);
+                }
+                ++pair;
             }
-            if (BUF == 2 && f == FI / 2 - 1) {
-                ta.store(next);
-                ta.load(k0 + 2 * BK);
-            }
-            if (BUF == 2 && f == FI - 1) {
-                tb.store(next + TA::kBytes);
-                tb.load(k0 + 2 * BK);
-            }
-        }
         if (BUF == 1) {
             barrier();
-            ta.store(here);
-            tb.store(here + TA::kBytes);
-            ta.load(k0 + 2 * BK);
-            tb.load(k0 + 2 * BK);
+            ta.template store<SET>(here);
+            tb.template store<SET>(here + A::kBytes);
+            ta.template load<SET>((t + 1 + kSets) * BK);
+            tb.template load<SET>((t + 1 + kSets) * BK);
         }
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
+        barrier();
+    }
+
+    __device__ __forceinline__ void run(const Args &P, int id, int part, lds_char *lds)
+    {
+        int ti, tj;
+        tile_of(id, P.tiles_i, P.tiles_j, ti, tj);
+        const int kb = part * P.k_part, kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
+        ta.init(P, false, ti * BM, kn, kb);
+        tb.init(P, true, tj * BN, kn, kb);
+        fa_of.init_fragment();
+        fb_of.init_fragment();
+        const int wave = threadIdx.x >> 6;
+        wi = wave / WJ, wj = wave % WJ;
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        lds_char *const other = lds + (BUF - 1) * kTiles;
+        ta.template load<0>(0);
+        tb.template load<0>(0);
+        ta.template load<1>(BK);
+        tb.template load<1>(BK);
+        ta.template store<0>(lds);
+        tb.template store<0>(lds + A::kBytes);
+        ta.template load<0>(2 * BK);
+        tb.template load<0>(2 * BK);
         __builtin_amdgcn_s_waitcnt(0xC07F);
         barrier();
-        lds_char *const swap = here;
-        here = next;
-        next = swap;
+        const int steps = (kn + BK - 1) / BK;
+        int t = 0;
+        for (; t + 1 < steps; t += 2) {
+            step<1>(lds, other, t);
+            step<0>(other, lds, t + 1);
+        }
+        if (t < steps) step<1>(lds, other, t);
+        if (P.parts > 1 && !joined<FI, FJ, kThreads>(P, acc, ti * P.tiles_j + tj, part, ti * BM + wi * TI)) return;
+        finish<TC, FI, FJ, kTurn, kForward, (PA > 1 || PB > 1)>(P, acc, ti * BM + wi * TI, tj * BN + wj * TJ,
+                                                                lds + wave * kTurnBytes,
+                                                                [&](int i, int j) { return plain_sum<A, B>(P, i, j); });
     }
-    finish<TC, FI, FJ, kTurn, LA == K_ROWS && LB == K_ROWS, (PA > 1 || PB > 1)>(
-        P, acc, ti * BM + wi * TI, tj * BN + wj * TJ, blockIdx.y, (lds_char *)lds + wave * kTurnBytes,
-        [&](int i, int j) {
-            return plain_sum<T, U, LA, LB>((const T *)P.a, (const U *)P.b, P.lda, P.ldb, i, j, kb, kn);
-        });
+};
+
+// 2048^3 in fp32 (256 tiles of 128 x 128, one a compute unit): 91 us with two buffers, 102 with
+// one; 4096^3 (1024 tiles): 693 and 640.
+template <typename T, int PLANES, int LA, int LB, int BM, int BN, int WI, int WJ, int BUF>
+__global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
+{
+    using S = Staged<Stored<T, PLANES, LA, BM, 64 * WI * WJ>, Stored<T, PLANES, LB, BN, 64 * WI * WJ>, T, BM, BN, WI, WJ,
+                     BUF, LA == K_ROWS && LB == K_ROWS>;
+    __shared__ __attribute__((aligned(1024))) char lds[S::kLds];
+    S s;
+    s.run(P, blockIdx.x, blockIdx.y, (lds_char *)lds);
 }
 
-// y of summed parts: the join after work split over k.
-template <typename TC>
-__global__ __launch_bounds__(256) void k_join(Args P, int parts)
-{
-    const long long all = (long long)P.I * P.J;
-    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < all; e += (long long)gridDim.x * 256) {
-        const int i = (int)(e / P.J), j = (int)(e % P.J);
-        float v[1] = {0.0f};
-        for (int p = 0; p < parts; ++p) v[0] += P.part[p * all + e];
-        if (P.bias) v[0] += widen(((const TC *)P.bias)[j]);
-        if (P.z) P.z[e] = v[0];
-        activate<sizeof(TC) == 2>(v, P.act);
-        float y = v[0] * P.alpha;
-        if (P.residual) y += widen(((const TC *)P.residual)[i * P.ldr + j]);
-        narrow(y, ((TC *)P.c)[i * P.ldc + j]);
+// ---- small products ----
+//
+// Where latency counts, or one operand has few rows: tiles of 16 FI x 16, whose k the waves of
+// a workgroup share out.  Fragments come straight from memory (each value is used by one or FI
+// matrix instructions only, so LDS would add a trip and save nothing), kAt steps of 32 k
+// before the first is used; the waves' sums meet in LDS and are added in their order.
+// fp32, and dz formed in fp32, use the fp32 matrix instruction: nothing is rounded or split.
+
+// Eight k of one row: k0 + 8 (lane / 16) + 0..7 of row0 + lane % 16.
+template <typename T, int L>
+struct Piece {
+    static constexpr int kSize = (int)sizeof(T), kWords = kSize * 2;
+    uint32_t w[kWords];
+
+    // rows and K: those of the operand.
+    __device__ __forceinline__ void load(const void *p, long long ld_elems, int row0, int rows, int k0, int K)
+    {
+        const int lane = threadIdx.x & 63, r = lane & 15, q = (lane >> 4) * 8;
+        const long long ld = ld_elems * kSize;
+        const int left = K - k0, more = rows - row0;
+        const char *base = (const char *)p + (L == K_ROWS ? row0 * ld + (long long)k0 * kSize : k0 * ld + (long long)row0 * kSize);
+        const long long bytes = L == K_ROWS ? (more - 1) * ld + (long long)left * kSize : (left - 1) * ld + (long long)more * kSize;
+        const int end = left <= 0 || more <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
+        const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)base, 0, end, 0x00027000);
+        if (L == K_ROWS && left >= 32) {
+            const int off = (int)(r * ld) + q * kSize;
+#pragma unroll
+            for (int h = 0; h < kWords / 4; ++h) {
+                const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off + h * 16, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[h * 4 + e] = v[e];
+            }
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int off = L == K_ROWS ? (q + e < left ? (int)(r * ld) + (q + e) * kSize : 0x7FFFFFF0)
+                                        : (r < more ? (int)((q + e) * ld) + r * kSize : 0x7FFFFFF0);
+            if (kSize == 4) {
+                w[e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, off, 0, 0);
+            } else {
+                const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, off, 0, 0);
+                if (e & 1) w[e / 2] |= v << 16;
+                else w[e / 2] = v;
+            }
+        }
     }
+    __device__ __forceinline__ float value(int e) const
+    {
+        if (kSize == 4) return __builtin_bit_cast(float, w[e % kWords]);
+        return __builtin_bit_cast(float, e & 1 ? w[e / 2] & 0xFFFF0000u : w[e / 2] << 16);
+    }
+};
+
+// dz of a piece: dy, scaled by act'(z) (alpha is the epilogue's); without an activation, dy alone.
+template <typename T, int L>
+struct SlopePiece {
+    Piece<T, L> d;
+    Piece<float, L> z;
+    float x[8];
+
+    __device__ __forceinline__ void load(const Args &P, int row0, int k0)
+    {
+        d.load(P.a, P.lda, row0, P.I, k0, P.K);
+        if (P.act != HQML_ACT_NONE) z.load(P.z, L == K_ROWS ? P.K : P.I, row0, P.I, k0, P.K);
+    }
+    __device__ __forceinline__ void form(int act)
+    {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = z.value(e);
+        if (act != HQML_ACT_NONE) {
+            slope<sizeof(T) == 2>(x, act);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= d.value(e);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = d.value(e);
+        }
+    }
+    __device__ __forceinline__ float value(int e) const { return x[e]; }
+};
+
+// The waves' sums of a 16 FI x 16 tile, added and finished.
+template <typename T, int FI, bool kForward>
+__device__ __forceinline__ void small_finish(const Args &P, f32x4 (&acc)[FI], int i0, int j0, float *lds)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
+#pragma unroll
+    for (int f = 0; f < FI; ++f)   // [wave][row][16 columns]
+        *(f32x4 *)(lds + (wave * FI * 16 + f * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) = acc[f];
+    __syncthreads();
+    for (int e = threadIdx.x; e < FI * 256; e += blockDim.x) {
+        const int i = i0 + (e >> 4), j = j0 + (e & 15);
+        if (i >= P.I) continue;
+        float v[1] = {0.0f};
+        for (int q = 0; q < waves; ++q) v[0] += lds[q * FI * 256 + e];
+        if (!kForward) {
+            if (j < P.J) narrow(v[0] * P.alpha, ((T *)P.c)[i * P.ldc + j]);
+            else if (j == P.J && P.ones) narrow(v[0] * P.alpha, ((T *)P.ones)[i]);
+            continue;
+        }
+        if (j >= P.J) continue;
+        if (P.bias) v[0] += widen(((const T *)P.bias)[j]);
+        if (P.z) P.z[(long long)i * P.J + j] = v[0];
+        activate<sizeof(T) == 2>(v, P.act);
+        float y = v[0] * P.alpha;
+        if (P.residual) y += widen(((const T *)P.residual)[i * P.ldr + j]);
+        narrow(y, ((T *)P.c)[i * P.ldc + j]);
+    }
+}
+
+// k of this wave: [first, last), a multiple of 32 long unless it ends with K.
+__device__ __forceinline__ void small_share(int K, int &first, int &last)
+{
+    const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int steps = (K + 31) >> 5, q = steps / waves, r = steps % waves;
+    first = (wave * q + (wave < r ? wave : r)) * 32;
+    last = first + (q + (wave < r ? 1 : 0)) * 32;
+    if (last > K) last = K;
+}
+
+// Forward: C = A B^T, both with k along their rows.
+template <typename T, int FI>
+__global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small_forward(Args P)
+{
+    extern __shared__ float small_lds[];
+    constexpr int kAt = FI == 1 ? 4 : 2;
+    const int i0 = blockIdx.x % P.tiles_i * (16 * FI), j0 = blockIdx.x / P.tiles_i * 16;
+    f32x4 acc[FI] = {};
+    int first, last;
+    small_share(P.K, first, last);
+    for (int k0 = first; k0 < last; k0 += 32 * kAt) {
+        Piece<T, K_ROWS> a[kAt][FI], b[kAt];
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) {   // steps past the share: empty buffers, nothing is read
+            const int k = k0 + 32 * n < last ? k0 + 32 * n : P.K;
+            b[n].load(P.b, P.ldb, j0, P.J, k, P.K);
+#pragma unroll
+            for (int f = 0; f < FI; ++f) a[n][f].load(P.a, P.lda, i0 + f * 16, P.I, k, P.K);
+        }
+#pragma unroll
+        for (int n = 0; n < kAt; ++n)
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                if (sizeof(T) == 2) {
+                    bf16x8 va, vb;
+                    __builtin_memcpy(&va, a[n][f].w, 16);
+                    __builtin_memcpy(&vb, b[n].w, 16);
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, va, acc[f], 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
+                }
+            }
+    }
+    small_finish<T, FI, true>(P, acc, i0, j0, small_lds);
+}
+
+// One gradient product: C = dz B with B's k across its rows; dz's layout L.  A column of ones after B's
+// last gives dz's row sums.
+template <typename T, int FI, int L>
+__device__ __forceinline__ void small_gradient(const Args &P, int id, float *lds)
+{
+    constexpr int kAt = FI == 1 ? 2 : 1;
+    const int i0 = id % P.tiles_i * (16 * FI), j0 = id / P.tiles_i * 16;
+    const bool one = P.ones && j0 + (int)(threadIdx.x & 15) == P.J;
+    f32x4 acc[FI] = {};
+    int first, last;
+    small_share(P.K, first, last);
+    for (int k0 = first; k0 < last; k0 += 32 * kAt) {
+        SlopePiece<T, L> a[kAt][FI];
+        Piece<T, K_COLS> b[kAt];
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) {
+            const int k = k0 + 32 * n < last ? k0 + 32 * n : P.K;
+            b[n].load(P.b, P.ldb, j0, P.J, k, P.K);
+#pragma unroll
+            for (int f = 0; f < FI; ++f) a[n][f].load(P, i0 + f * 16, k);
+        }
+#pragma unroll
+        for (int n = 0; n < kAt; ++n)
+#pragma unroll
+            for (int f = 0; f < FI; ++f) {
+                a[n][f].form(P.act);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(one ? 1.0f : b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
+            }
+    }
+    small_finish<T, FI, false>(P, acc, i0, j0, lds);
+}
+
+// Small gradients in one launch: dx = dz w from the first workgroups, dw = dz^T x with db as a column
+// of ones from the others.  dz is formed anew by every tile that takes it, and never rounded.
+template <typename T, int FI>
+__global__ __launch_bounds__(512) void k_small_gradients(Args dx, Args dw)
+{
+    extern __shared__ float small_lds[];
+    const int tx = dx.tiles_i * dx.tiles_j, id = blockIdx.x;
+    if (id < tx) small_gradient<T, FI, K_ROWS>(dx, id, small_lds);
+    else small_gradient<T, FI, K_COLS>(dw, id - tx, small_lds);
 }
 
 // Tile shapes a product can be run with.
@@ -782,8 +1010,11 @@ enum Shape { TILE_64 = 0, TILE_128 = 1, TILE_256 = 2 };
 
 // The kernels of one operand type, for a layout pair (K_ROWS, K_ROWS), (K_ROWS, K_COLS) or
 // (K_COLS, K_COLS).  direct: both bf16 operands' rows allow 16-byte access to LDS; TILE_256 needs it.
-hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, int parts, hipStream_t s);
-hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, int parts, hipStream_t s);
+hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, hipStream_t s);
+hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, hipStream_t s);
+// Small products, in tiles of 16 fi x 16 (fi = 1 or 4) by `waves` waves; either gradient may have no tiles.
+hipError_t launch_small_forward(const Args &a, bool is_bf16, int fi, int waves, hipStream_t s);
+hipError_t launch_small_gradients(const Args &dx, const Args &dw, bool is_bf16, int fi, int waves, hipStream_t s);
 
 }  // namespace gemm
 }  // namespace hqml

@@ -9,8 +9,8 @@ template <int LA, int LB>
 void run(const Args &a, bool direct, Shape shape, dim3 grid, hipStream_t s)
 {
     if (!direct) {
-        if (shape == TILE_64) k_product_staged<bf16, 1, LA, bf16, 1, LB, bf16, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
-        else k_product_staged<bf16, 1, LA, bf16, 1, LB, bf16, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a);
+        if (shape == TILE_64) k_product_staged<bf16, 1, LA, LB, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
+        else k_product_staged<bf16, 1, LA, LB, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a);
         return;
     }
     // 256 x 256: waves of 64 x 128 where both operands lie along k (218 us against 231 for
@@ -23,9 +23,9 @@ void run(const Args &a, bool direct, Shape shape, dim3 grid, hipStream_t s)
 
 }  // namespace
 
-hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, int parts, hipStream_t s)
+hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.tiles_i * (unsigned)a.tiles_j, (unsigned)parts);
+    const dim3 grid((unsigned)a.tiles_i * (unsigned)a.tiles_j, (unsigned)a.parts);
     if (la == K_ROWS && lb == K_ROWS) run<K_ROWS, K_ROWS>(a, direct, shape, grid, s);
     else if (la == K_ROWS) run<K_ROWS, K_COLS>(a, direct, shape, grid, s);
     else run<K_COLS, K_COLS>(a, direct, shape, grid, s);

@@ -9,16 +9,16 @@ namespace {
 template <int LA, int LB>
 void run(const Args &a, Shape shape, dim3 grid, hipStream_t s)
 {
-    if (shape == TILE_64) k_product_staged<float, 3, LA, float, 3, LB, float, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
-    else if (grid.x < 512) k_product_staged<float, 3, LA, float, 3, LB, float, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a);
-    else k_product_staged<float, 3, LA, float, 3, LB, float, 128, 128, 2, 4, 1><<<grid, 512, 0, s>>>(a);
+    if (shape == TILE_64) k_product_staged<float, 3, LA, LB, 64, 64, 2, 2, 2><<<grid, 256, 0, s>>>(a);
+    else if (grid.x < 512) k_product_staged<float, 3, LA, LB, 128, 128, 2, 4, 2><<<grid, 512, 0, s>>>(a);
+    else k_product_staged<float, 3, LA, LB, 128, 128, 2, 4, 1><<<grid, 512, 0, s>>>(a);
 }
 
 }  // namespace
 
-hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, int parts, hipStream_t s)
+hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, hipStream_t s)
 {
-    const dim3 grid((unsigned)a.tiles_i * (unsigned)a.tiles_j, (unsigned)parts);
+    const dim3 grid((unsigned)a.tiles_i * (unsigned)a.tiles_j, (unsigned)a.parts);
     if (la == K_ROWS && lb == K_ROWS) run<K_ROWS, K_ROWS>(a, shape, grid, s);
     else if (la == K_ROWS) run<K_ROWS, K_COLS>(a, shape, grid, s);
     else run<K_COLS, K_COLS>(a, shape, grid, s);

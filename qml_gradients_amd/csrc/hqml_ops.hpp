@@ -33,9 +33,11 @@ struct DenseWorkspace {
     size_t dz_bytes = 0;     // gradient at z, [M][N] in dtype
     size_t rows_bytes = 0;   // partial row sums of dz, fp32
     size_t part_bytes = 0;   // partial sums of products split over k, fp32
+    size_t ticket_bytes = 0; // one counter a tile of them, 0 between calls
     void *dz = nullptr;
     float *rows = nullptr;
     float *part = nullptr;
+    unsigned *ticket = nullptr;
 };
 
 DenseWorkspace dense_workspace(const hqml_dense_config &cfg);

@@ -15,7 +15,7 @@ from . import (HQML_ADAMW_BLOCK, HQML_DTYPE_BF16, HQML_DTYPE_FP32, HQML_DTYPE_FP
                hqml_adamw_config, hqml_adamw_step)
 
 _DTYPES = {torch.float32: HQML_DTYPE_FP32, torch.bfloat16: HQML_DTYPE_BF16, torch.float64: HQML_DTYPE_FP64}
-_WORDS = 7   # 64-bit words of an hqml_adamw_tensor
+_current_stream = torch._C._cuda_getCurrentRawStream
 
 
 class AdamW(torch.optim.Optimizer):
@@ -58,46 +58,60 @@ class AdamW(torch.optim.Optimizer):
             state[name + "_scale"] = torch.zeros(blocks, dtype=torch.float32, device=p.device)
         return state
 
-    @torch.no_grad()
     def step(self, closure=None):
+        for hook in tuple(self._optimizer_step_pre_hooks.values()):
+            hook(self, (), {})
         loss = None
         if closure is not None:
             with torch.enable_grad():
                 loss = closure()
+        state = self.state
         for group in self.param_groups:
-            bits = group["state_bits"]
+            eight = group["state_bits"] == 8
             calls = {}   # tensors that one call can take
             for p in group["params"]:
                 g = p.grad
                 if g is None:
                     continue
-                if g.is_sparse or g.dtype not in _DTYPES or g.device != p.device:
-                    raise ValueError("gradients must be dense, on their parameter's device, in fp32, bf16 or fp64")
+                if g.layout is not torch.strided or g.dtype not in _DTYPES:
+                    raise ValueError("gradients must be dense, in fp32, bf16 or fp64")
                 if not p.is_contiguous():
                     raise ValueError("parameters must be contiguous")
-                s = self.state[p]
+                if not g.is_contiguous():
+                    g = g.detach().contiguous()
+                s = state[p]
                 if not s:
-                    s.update(self._begin(p, bits))
-                g = g if g.is_contiguous() else g.contiguous()
-                key = (p.dtype, g.dtype, p.device.index, s["step"])
-                words, kept = calls.setdefault(key, ([], []))
-                if bits == 32:
-                    words += (p.data_ptr(), g.data_ptr(), s["exp_avg"].data_ptr(), s["exp_avg_sq"].data_ptr(), 0, 0,
-                              p.numel())
-                else:
+                    s.update(self._begin(p, group["state_bits"]))
+                key = (p.dtype, g.dtype, p.get_device(), s["step"])
+                call = calls.get(key)
+                if call is None:
+                    call = calls[key] = ([], [], [], [])
+                words, params, grads, states = call
+                if eight:
                     words += (p.data_ptr(), g.data_ptr(), s["exp_avg"].data_ptr(), s["exp_avg_sq_root"].data_ptr(),
                               s["exp_avg_scale"].data_ptr(), s["exp_avg_sq_root_scale"].data_ptr(), p.numel())
-                kept.append((p, g, s))
-            for (pd, gd, device, before), (words, kept) in calls.items():
-                cfg = hqml_adamw_config(_DTYPES[pd], _DTYPES[gd], HQML_MOMENTS_32 if bits == 32 else HQML_MOMENTS_8,
+                else:
+                    words += (p.data_ptr(), g.data_ptr(), s["exp_avg"].data_ptr(), s["exp_avg_sq"].data_ptr(), 0, 0,
+                              p.numel())
+                params.append(p)
+                grads.append(g)    # kept until its kernel is queued
+                states.append(s)
+            for (pd, gd, device, before), (words, params, grads, states) in calls.items():
+                cfg = hqml_adamw_config(_DTYPES[pd], _DTYPES[gd], HQML_MOMENTS_8 if eight else HQML_MOMENTS_32,
                                         before + 1, group["lr"], *group["betas"], group["eps"], group["weight_decay"],
-                                        device, torch._C._cuda_getCurrentRawStream(device))
-                hqml_adamw_step(cfg, len(kept), (ctypes.c_longlong * len(words))(*words))
-                for _, _, s in kept:
+                                        device, _current_stream(device))
+                hqml_adamw_step(cfg, len(params), (ctypes.c_longlong * len(words))(*words))
+                for s in states:
                     s["step"] = before + 1
                 # a backward pass that saved a parameter from before this step has to refuse it
-                torch.autograd.graph.increment_version([p for p, _, _ in kept])
+                torch.autograd.graph.increment_version(params)
+        for hook in tuple(self._optimizer_step_post_hooks.values()):
+            hook(self, (), {})
         return loss
+
+    # torch wraps a step that does not say this in a profiler range and the hooks, which cost four times the
+    # launch; the optimiser's own hooks run above
+    step.hooked = True
 
     def load_state_dict(self, state_dict):
         """As torch's, but the moments keep the types they were saved in."""

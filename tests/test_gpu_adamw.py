@@ -284,6 +284,37 @@ def test_step_marks_parameters_changed():
         loss.backward()
 
 
+def test_hooks_run_once():
+    p = torch.nn.Parameter(torch.ones(4, device="cuda"))
+    p.grad = torch.ones(4, device="cuda")
+    opt, seen = optimiser([p]), []
+    opt.register_step_pre_hook(lambda o, a, k: seen.append(("before", float(p[0]))))
+    opt.register_step_post_hook(lambda o, a, k: seen.append(("after", float(p[0]))))
+    opt.step()
+    assert [s[0] for s in seen] == ["before", "after"] and seen[0][1] == 1.0 and seen[1][1] < 1.0
+
+
+def test_learning_rate_schedule_and_closure():
+    p = torch.nn.Parameter(torch.ones(4, device="cuda"))
+    opt = optimiser([p], weight_decay=0.0)
+    schedule = torch.optim.lr_scheduler.StepLR(opt, step_size=1, gamma=0.1)
+
+    def closure():
+        opt.zero_grad()
+        loss = p.sum()
+        loss.backward()
+        return loss
+
+    moves = []
+    for _ in range(3):
+        before = float(p[0])
+        assert float(opt.step(closure)) == pytest.approx(4 * before, rel=1e-6)
+        moves.append(before - float(p[0]))
+        schedule.step()
+    for k, move in enumerate(moves):   # equal gradients: each step is lr itself
+        assert move == pytest.approx(LR * 0.1 ** k, rel=1e-2)
+
+
 def test_parameters_without_gradient_wait():
     a, b = (torch.nn.Parameter(torch.ones(4, device="cuda")) for _ in range(2))
     opt = optimiser([a, b])
