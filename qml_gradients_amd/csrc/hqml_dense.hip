@@ -17,18 +17,114 @@ namespace {
 
 using namespace gemm;
 
-// Work is split over k where a product has fewer tiles than kFewTiles: into parts of kPartK at least, as many
-// as make kPartTiles of them.
-constexpr int kFewTiles = 256, kPartTiles = 512, kPartK = 128;
-
 int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
-// The most tiles of partial sums that products of up to I rows leave.
+// ---- how a product is run: the estimate that is least ----
+//
+// Times in us, fitted to a sweep of every shape over 13 products from 64 x 64 x 256 to 2048^3 and
+// 200 x 200 x 16000; the choice was within 15 % of the best one at each of them.
+
+constexpr int kUnits = 256;    // compute units
+constexpr int kPartTiles = 1024, kMostParts = 64;
+constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, kMostParts};
+
+// A tile kernel: a workgroup spends `step` on 32 k when alone on its compute unit, n of them n * share; fixed:
+// launch, first loads, epilogue; work split over k costs join + parts * join_part.
+struct TileCost {
+    int side;
+    float fixed, step, share, join, join_part;
+};
+constexpr TileCost kFp32Cost[] = {{64, 4.0f, 0.70f, 0.55f, 1.5f, 0.4f}, {128, 5.0f, 1.20f, 1.42f, 4.0f, 1.0f}};
+constexpr TileCost kStagedCost[] = {{64, 4.0f, 0.27f, 0.16f, 2.0f, 0.4f}, {128, 4.0f, 0.36f, 0.47f, 4.0f, 1.0f}};
+constexpr TileCost kDirectCost[] = {{64, 3.0f, 0.12f, 0.135f, 2.0f, 0.4f},
+                                    {128, 4.0f, 0.22f, 0.32f, 4.0f, 1.0f},
+                                    {256, 7.0f, 0.57f, 0.82f, 7.0f, 2.0f}};
+
+struct Cut {
+    int side, parts;
+    float us;
+};
+
+Cut best_cut(int I, int J, int K, const TileCost *cost, int n)
+{
+    const int steps = ceil_div(K, 32);
+    Cut best{0, 1, 0.0f};
+    for (int c = 0; c < n; ++c) {
+        const long long tiles = (long long)ceil_div(I, cost[c].side) * ceil_div(J, cost[c].side);
+        for (int parts : kParts) {
+            if (parts > 1 && (tiles * parts > kPartTiles * 64 * 64 / (cost[c].side * cost[c].side) || parts * 2 > steps)) break;
+            const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
+            float us = cost[c].fixed + ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share);
+            if (parts > 1) us += cost[c].join + parts * cost[c].join_part;
+            if (!best.side || us < best.us) best = {cost[c].side, parts, us};
+        }
+    }
+    return best;
+}
+
+Cut best_cut(int I, int J, int K, size_t elem, bool direct)
+{
+    if (elem == 4) return best_cut(I, J, K, kFp32Cost, 2);
+    return direct ? best_cut(I, J, K, kDirectCost, 3) : best_cut(I, J, K, kStagedCost, 2);
+}
+
+// A small forward product: every tile reads its own rows, at 40 bytes a cycle and compute unit; the fp32 matrix
+// instruction takes 8 x 32 cycles for 16 x 16 x 32; a wave waits for its loads once in kAt steps.
+struct SmallCut {
+    int fi, waves;
+    float us;
+};
+
+SmallCut small_cut(int I, int J, int K, size_t elem)
+{
+    SmallCut best{0, 1, 0.0f};
+    const int steps = ceil_div(K, 32);
+    for (int fi : {1, 4})
+        for (int waves : {1, 2, 4, 8, 16}) {
+            if (waves > 1 && (waves > steps || (waves == 16 && fi == 4))) break;
+            const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
+            const float each = (float)((tiles + kUnits - 1) / kUnits);
+            const float load = each * steps * (16 * 32 * elem * (fi + 1)) / 84e3f;
+            const float mul = elem == 2 ? 0.0f : each * steps * fi * 0.03f;
+            const float wait = ceil_div(steps, waves * (fi == 1 ? 4 : 2)) * 1.2f * std::max(1.0f, each * waves / 16);
+            const float us = 3.5f + std::max(load + mul, wait) + 0.05f * waves;
+            if (!best.fi || us < best.us) best = {fi, waves, us};
+        }
+    return best;
+}
+
+// Small gradients in one launch.  What counts is forming dz anew in every tile (1,500 cycles of a SIMD for 16
+// rows and 32 k, the matrix instructions with them) and the waits of the longer product's waves.
+SmallCut small_gradients_cut(int M, int N, int K)
+{
+    SmallCut best{0, 1, 0.0f};
+    const int steps = std::max(ceil_div(N, 32), ceil_div(M, 32));
+    for (int fi : {1, 4})
+        for (int waves : {1, 2, 4, 8}) {
+            if (waves > 1 && waves > steps) break;
+            const long long tx = (long long)ceil_div(M, 16 * fi) * ceil_div(K, 16);
+            const long long tw = (long long)ceil_div(N, 16 * fi) * ceil_div(K + 1, 16);
+            const float work = (tx * ceil_div(N, 32) + tw * ceil_div(M, 32)) * (fi * 1500.0f + 400.0f) / 2.15e6f;
+            const int at = fi == 1 ? 2 : 1;   // steps a wave loads together
+            const float wait = ceil_div(steps, waves * at) * (1.2f + 0.7f * fi * at);
+            const float us = 3.5f + std::max(work, wait) + (tx + tw) * waves * 1e-4f;
+            if (!best.fi || us < best.us) best = {fi, waves, us};
+        }
+    return best;
+}
+
+// dz and its row sums by themselves.
+float slope_us(int M, int N, size_t elem)
+{
+    return 6.0f + (float)M * N * (4 + 2 * elem) / 5e6f;
+}
+
+// The most 64 x 64 tiles of partial sums that a product of up to these sizes leaves.
 size_t part_tiles(size_t I, size_t J, size_t K)
 {
-    if (K < 2 * kPartK) return 0;
-    const size_t tiles = ((I + 63) / 64) * ((J + 63) / 64);
-    return std::min<size_t>(kPartTiles, tiles * (K / kPartK));
+    if (K <= 96) return 0;   // three steps: never split
+    const size_t tiles = ((I + 255) / 256) * ((J + 255) / 256) * 16;   // whole tiles of any shape
+    return std::min<size_t>(kPartTiles, tiles * kMostParts);
 }
 
 bool aligned(const void *p, long long ld, size_t elem)
@@ -36,102 +132,99 @@ bool aligned(const void *p, long long ld, size_t elem)
     return (uintptr_t)p % 16 == 0 && ld * (long long)elem % 16 == 0;
 }
 
-// Cuts a product into tiles of `side` and, if they are the 64 x 64 ones and few, its k into parts, whose
-// sums go to the workspace.
-void cut(Args &P, int side, const DenseWorkspace &ws)
+// Whether bf16 operands can be loaded straight into LDS.
+bool direct_bf16(const Args &P, int la, int lb)
 {
-    P.tiles_i = ceil_div(P.I, side);
-    P.tiles_j = ceil_div(P.J, side);
-    P.parts = 1;
-    P.k_part = ceil_div(P.K, 32) * 32;
-    const long long tiles = (long long)P.tiles_i * P.tiles_j;
-    if (side != 64 || tiles >= kFewTiles) return;
-    const int parts = std::min((int)(kPartTiles / tiles), P.K / kPartK);
-    if (parts < 2) return;
-    P.k_part = ceil_div(ceil_div(P.K, parts), 32) * 32;
-    P.parts = ceil_div(P.K, P.k_part);
-    P.part = ws.part;
-    P.ticket = ws.ticket;
+    return aligned(P.a, P.lda, 2) && aligned(P.b, P.ldb, 2) && ((la == K_COLS && lb == K_COLS) || P.K % 8 == 0);
 }
 
-// Runs one product; P holds everything but its cut.
+// Runs one product on tiles; P holds everything but its cut.
 template <typename T>
 hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStream_t s)
 {
-    const bool direct = sizeof(T) == 2 && aligned(P.a, P.lda, 2) && aligned(P.b, P.ldb, 2) &&
-                        ((la == K_COLS && lb == K_COLS) || P.K % 8 == 0);
-    P.wide = aligned(P.c, P.ldc, sizeof(T)) && P.J % 8 == 0 &&
-             (!P.residual || aligned(P.residual, P.ldr, sizeof(T))) && (!P.z || aligned(P.z, 0, 4));
-    auto tiles = [&](int n) { return (long long)ceil_div(P.I, n) * ceil_div(P.J, n); };
-    const Shape shape = direct && tiles(256) >= 192 ? TILE_256 : tiles(128) >= 256 ? TILE_128 : TILE_64;
-    cut(P, shape == TILE_64 ? 64 : shape == TILE_128 ? 128 : 256, ws);
+    const bool direct = sizeof(T) == 2 && direct_bf16(P, la, lb);
+    const Cut c = best_cut(P.I, P.J, P.K, sizeof(T), direct);
+    P.tiles_i = ceil_div(P.I, c.side);
+    P.tiles_j = ceil_div(P.J, c.side);
+    P.k_part = ceil_div(ceil_div(P.K, c.parts), 32) * 32;
+    P.parts = ceil_div(P.K, P.k_part);
+    P.part = ws.part;
+    P.ticket = ws.ticket;
+    const Shape shape = c.side == 64 ? TILE_64 : c.side == 128 ? TILE_128 : TILE_256;
     return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, shape, s) : launch_fp32(P, la, lb, shape, s);
 }
 
-constexpr int kRowChunk = 64;    // rows whose dz one workgroup forms and sums
-constexpr int kSlopeCols = 256;  // and columns: 32 lanes of eight; eight threads go down the rows
+constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; eight threads go down the rows
 
-// dz = alpha act'(z) dy (written if dz is not null) and its sums over kRowChunk rows.  Bound by
-// memory.  VEC: the rows allow 16-byte access and a lane's eight columns are neighbours; otherwise
-// they are 32 apart, so that a row is still read in runs.
-template <typename T, bool VEC>
+// dz = alpha act'(z) dy (written if dz is not null) and its sums over `chunk` rows.  Bound by memory;
+// 16 bytes at any alignment, single values where a row ends.
+template <typename T>
 __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, float *rows, int M,
-                                               int N, int act, float alpha)
+                                               int N, int chunk, int act, float alpha)
 {
     __shared__ float part[8][kSlopeCols];
     const int lane = threadIdx.x & 31, down = threadIdx.x >> 5;
-    const int c0 = blockIdx.x * kSlopeCols;
-    const int r0 = blockIdx.y * kRowChunk, r1 = min(M, r0 + kRowChunk);
+    const int c0 = blockIdx.x * kSlopeCols, c = c0 + lane * 8, n = min(8, N - c);
+    const int r0 = blockIdx.y * chunk, r1 = min(M, r0 + chunk);
+    constexpr int kV = (int)sizeof(T) / 2;   // 16-byte words of eight values
     float sum[8] = {};
+#pragma unroll 2
     for (int r = r0 + down; r < r1; r += 8) {
-        float d[8], f[8];
-        if (VEC) {
-            const int c = c0 + lane * 8;
-            if (c >= N) break;
-            T t[8];
-            __builtin_memcpy(t, __builtin_assume_aligned(dy + r * lddy + c, 16), sizeof t);
+        if (n <= 0) break;
+        float d[8], f[8] = {};
+        T t[8] = {};
+        if (n == 8) {
+            u32x4 w[kV];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = alpha * widen(t[k]);
-            if (act != HQML_ACT_NONE) __builtin_memcpy(f, __builtin_assume_aligned(z + (long long)r * N + c, 16), sizeof f);
+            for (int k = 0; k < kV; ++k) w[k] = ((const u32x4_any *)(dy + r * lddy + c))[k];
+            __builtin_memcpy(t, w, sizeof t);
+            if (act != HQML_ACT_NONE) {
+                const f32x4_any *from = (const f32x4_any *)(z + (long long)r * N + c);
+                const f32x4 lo = from[0], hi = from[1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) f[k] = lo[k], f[4 + k] = hi[k];
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                const int c = c0 + lane + 32 * k;
-                d[k] = c < N ? alpha * widen(dy[r * lddy + c]) : 0.0f;
-                f[k] = c < N && act != HQML_ACT_NONE ? z[(long long)r * N + c] : 0.0f;
+                if (k >= n) continue;
+                t[k] = dy[r * lddy + c + k];
+                if (act != HQML_ACT_NONE) f[k] = z[(long long)r * N + c + k];
             }
         }
         if (act != HQML_ACT_NONE) {
             slope<sizeof(T) == 2>(f, act);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] *= f[k];
-        }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) sum[k] += d[k];
-        if (!dz) continue;
-        if (VEC) {
-            T t[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k) narrow(d[k], t[k]);
-            __builtin_memcpy(__builtin_assume_aligned(dz + (long long)r * N + c0 + lane * 8, 16), t, sizeof t);
+            for (int k = 0; k < 8; ++k) d[k] = alpha * widen(t[k]) * f[k];
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int c = c0 + lane + 32 * k;
-                if (c < N) narrow(d[k], dz[(long long)r * N + c]);
-            }
+            for (int k = 0; k < 8; ++k) d[k] = alpha * widen(t[k]);
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) sum[k] += d[k], narrow(d[k], t[k]);
+        if (!dz) continue;
+        T *to = dz + (long long)r * N + c;
+        if (n == 8) {
+            u32x4 w[kV];
+            __builtin_memcpy(w, t, sizeof t);
+#pragma unroll
+            for (int k = 0; k < kV; ++k) ((u32x4_any *)to)[k] = w[k];
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) to[k] = t[k];
         }
     }
     if (!rows) return;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) part[down][VEC ? lane * 8 + k : lane + 32 * k] = sum[k];
+    for (int k = 0; k < 8; ++k) part[down][lane * 8 + k] = sum[k];
     __syncthreads();
-    const int c = c0 + threadIdx.x;
-    if (c >= N) return;
+    const int col = c0 + threadIdx.x;
+    if (col >= N) return;
     float s = 0.0f;
 #pragma unroll
     for (int q = 0; q < 8; ++q) s += part[q][threadIdx.x];
-    rows[(long long)blockIdx.y * N + c] = s;
+    rows[(long long)blockIdx.y * N + col] = s;
 }
 
 // db: the sums of all row chunks, 32 columns a workgroup, eight threads down the chunks.
@@ -153,6 +246,14 @@ __global__ __launch_bounds__(256) void k_row_sum(const float *rows, int chunks, 
     narrow(s, db[c]);
 }
 
+// Rows that a workgroup of k_slope sums: 16, or 64 where that leaves enough of them.
+constexpr int kFewRows = 64 * 1024;
+
+int row_chunk(int M, int N)
+{
+    return M <= kFewRows && (long long)ceil_div(M, 64) * ceil_div(N, kSlopeCols) < 1024 ? 16 : 64;
+}
+
 template <typename T>
 __global__ void k_zero(T *p, long long n)
 {
@@ -168,28 +269,10 @@ hipError_t zero(void *p, long long n, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles and waves of a small product or two.
 void cut_small(Args &P, int fi)
 {
     P.tiles_i = ceil_div(P.I, 16 * fi);
     P.tiles_j = ceil_div(P.J + (P.ones ? 1 : 0), 16);
-}
-
-long long small_tiles(const Args &P, int fi)
-{
-    return (long long)ceil_div(P.I, 16 * fi) * ceil_div(P.J + (P.ones ? 1 : 0), 16);
-}
-
-int small_waves(int K, long long tiles, int most)
-{
-    int waves = 1;
-    while (waves < most && waves * 2 <= ceil_div(K, 32) && tiles * waves < 4096) waves *= 2;
-    return waves;
-}
-
-bool small(int M, int N, int K)
-{
-    return (long long)M * N * K <= 1ll << 27;
 }
 
 template <typename T>
@@ -203,16 +286,17 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
     P.bias = a.bias, P.residual = a.residual, P.ldr = a.ldr;
     P.z = a.act == HQML_ACT_NONE ? nullptr : (float *)a.z;
     P.act = a.act, P.alpha = a.alpha;
-    if (small(a.M, a.N, a.K)) {
-        const int fi = small_tiles(P, 4) >= 512 ? 4 : 1;
-        cut_small(P, fi);
-        return launch_small_forward(P, sizeof(T) == 2, fi, small_waves(P.K, small_tiles(P, fi), fi == 1 ? 16 : 8), s);
+    const SmallCut c = small_cut(P.I, P.J, P.K, sizeof(T));
+    if (c.us <= best_cut(P.I, P.J, P.K, sizeof(T), sizeof(T) == 2 && direct_bf16(P, K_ROWS, K_ROWS)).us) {
+        cut_small(P, c.fi);
+        return launch_small_forward(P, sizeof(T) == 2, c.fi, c.waves, s);
     }
     return run_product<T>(P, K_ROWS, K_ROWS, ws, s);
 }
 
+// dx, dw and db in one launch.
 template <typename T>
-hipError_t gradients(const DenseBackward &a, hipStream_t s)
+hipError_t gradients(const DenseBackward &a, const SmallCut &c, hipStream_t s)
 {
     Args X{}, W{};
     X.a = W.a = a.dy, X.lda = W.lda = a.lddy;
@@ -229,11 +313,9 @@ hipError_t gradients(const DenseBackward &a, hipStream_t s)
         W.c = a.dw, W.ldc = a.K;
         W.ones = a.db;
     }
-    const int fi = small_tiles(X, 4) + small_tiles(W, 4) >= 512 ? 4 : 1;
-    cut_small(X, fi);
-    cut_small(W, fi);
-    const int waves = small_waves(std::max(X.K, W.K), small_tiles(X, fi) + small_tiles(W, fi), 8);
-    return launch_small_gradients(X, W, sizeof(T) == 2, fi, waves, s);
+    cut_small(X, c.fi);
+    cut_small(W, c.fi);
+    return launch_small_gradients(X, W, sizeof(T) == 2, c.fi, c.waves, s);
 }
 
 template <typename T>
@@ -244,25 +326,27 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         e = zero<T>(a.dw, (long long)a.N * a.K, s);
         return e != hipSuccess ? e : zero<T>(a.db, a.N, s);
     }
-    if (small(a.M, a.N, a.K)) return gradients<T>(a, s);
+    const SmallCut c = small_gradients_cut(a.M, a.N, a.K);
+    const bool two = sizeof(T) == 2;
+    const float apart = slope_us(a.M, a.N, sizeof(T)) + best_cut(a.M, a.K, a.N, sizeof(T), two).us +
+                        best_cut(a.N, a.K, a.M, sizeof(T), two).us;
+    if (c.us <= apart) return gradients<T>(a, c, s);
     const T *dz = (const T *)a.dy;
     long long lddz = a.lddy;
     float alpha = a.alpha;
     const bool form = a.act != HQML_ACT_NONE && (a.dx || a.dw);
-    const int chunks = (a.M + kRowChunk - 1) / kRowChunk;
     if (form || a.db) {
+        const int chunk = row_chunk(a.M, a.N), chunks = ceil_div(a.M, chunk);
         for (int c0 = 0; c0 < chunks; c0 += 65535) {   // grid limit in y
             const int n = std::min(65535, chunks - c0);
-            const long long r0 = (long long)c0 * kRowChunk;
+            const long long r0 = (long long)c0 * chunk;
             const dim3 grid((unsigned)ceil_div(a.N, kSlopeCols), (unsigned)n);
-            const T *dy = (const T *)a.dy + r0 * a.lddy;
-            const float *z = a.act != HQML_ACT_NONE ? a.z + r0 * a.N : nullptr;
-            T *to = form ? (T *)ws.dz + r0 * a.N : nullptr;
-            float *rows = a.db ? ws.rows + (long long)c0 * a.N : nullptr;
-            const int m = (int)std::min<long long>(a.M - r0, (long long)n * kRowChunk);
-            if (a.N % 8 == 0 && aligned(a.dy, a.lddy, sizeof(T)) && aligned(a.z, 0, 4))
-                k_slope<T, true><<<grid, 256, 0, s>>>(dy, a.lddy, z, to, rows, m, a.N, a.act, a.alpha);
-            else k_slope<T, false><<<grid, 256, 0, s>>>(dy, a.lddy, z, to, rows, m, a.N, a.act, a.alpha);
+            k_slope<T><<<grid, 256, 0, s>>>((const T *)a.dy + r0 * a.lddy, a.lddy,
+                                            a.act != HQML_ACT_NONE ? a.z + r0 * a.N : nullptr,
+                                            form ? (T *)ws.dz + r0 * a.N : nullptr,
+                                            a.db ? ws.rows + (long long)c0 * a.N : nullptr,
+                                            (int)std::min<long long>(a.M - r0, (long long)n * chunk), a.N, chunk, a.act,
+                                            a.alpha);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (a.db) {
@@ -296,7 +380,9 @@ DenseWorkspace dense_workspace(const hqml_dense_config &cfg)
     DenseWorkspace ws;
     const size_t M = (size_t)cfg.max_batch, N = (size_t)cfg.out_features;
     if (cfg.activation != HQML_ACT_NONE) ws.dz_bytes = M * N * (cfg.dtype == HQML_DTYPE_BF16 ? 2 : 4);
-    ws.rows_bytes = (M + kRowChunk - 1) / kRowChunk * N * 4;
+    // a smaller batch may have more chunks of fewer rows
+    const size_t chunk = (size_t)row_chunk(cfg.max_batch, cfg.out_features);
+    ws.rows_bytes = std::max((M + chunk - 1) / chunk, (std::min(M, (size_t)kFewRows) + 15) / 16) * N * 4;
     const size_t K = (size_t)cfg.in_features;
     const size_t tiles = std::max({part_tiles(M, N, K), part_tiles(M, K, N), part_tiles(N, K, M)});
     ws.part_bytes = tiles * 64 * 64 * 4;

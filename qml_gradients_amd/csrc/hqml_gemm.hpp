@@ -27,6 +27,9 @@ using s16x4 = __attribute__((ext_vector_type(4))) short;
 using f32x2 = __attribute__((ext_vector_type(2))) float;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
+// 16 bytes at any alignment of an element: the hardware takes them so
+using u32x4_any = __attribute__((ext_vector_type(4), aligned(2))) uint32_t;
+using f32x4_any = __attribute__((ext_vector_type(4), aligned(4))) float;
 using lds_char = __attribute__((address_space(3))) char;
 
 enum Layout { K_ROWS = 0, K_COLS = 1 };
@@ -44,7 +47,6 @@ struct Args {
     float *z;                // [I][J], sum + bias
     int act;
     float alpha;
-    int wide;                // J, and every row of c, residual and z, allow 16-byte access
     void *ones;              // [I]: the sums of A's rows, as a column J of B that is all ones; or null
     // work split over k: every part leaves its sums, the last one of a tile to finish adds them up
     int parts, k_part;       // k of one part, a multiple of 32
@@ -221,22 +223,28 @@ __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int 
         taken = __hip_atomic_fetch_add(P.ticket + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (taken != (unsigned)P.parts - 1) return false;
+    constexpr int kAtOnce = kWords <= 8 ? 4 : kWords <= 16 ? 2 : 1;   // parts whose loads are under way together
 #pragma unroll
-    for (int f = 0; f < FI; ++f) {
+    for (int f = 0; f < FI; ++f)
 #pragma unroll
         for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (f * 16 >= rows) continue;
-        for (int p = 0; p < P.parts; ++p)
+    for (int p0 = 0; p0 < P.parts; p0 += kAtOnce) {
+        unsigned long long w[kAtOnce][kWords];
 #pragma unroll
-            for (int g = 0; g < FJ; ++g)
+        for (int p = 0; p < kAtOnce; ++p)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const unsigned long long w =
-                        __hip_atomic_load(all + ((long long)p * kWords + (f * FJ + g) * 2 + h) * THREADS,
-                                          __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-                    acc[f][g][2 * h] += __builtin_bit_cast(float, (uint32_t)w);
-                    acc[f][g][2 * h + 1] += __builtin_bit_cast(float, (uint32_t)(w >> 32));
-                }
+            for (int e = 0; e < kWords; ++e)
+                w[p][e] = p0 + p < P.parts && e / (FJ * 2) * 16 < rows
+                              ? __hip_atomic_load(all + ((long long)(p0 + p) * kWords + e) * THREADS, __ATOMIC_RELAXED,
+                                                  __HIP_MEMORY_SCOPE_AGENT)
+                              : 0;
+#pragma unroll
+        for (int p = 0; p < kAtOnce; ++p)
+#pragma unroll
+            for (int e = 0; e < kWords; ++e) {
+                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2] += __builtin_bit_cast(float, (uint32_t)w[p][e]);
+                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2 + 1] += __builtin_bit_cast(float, (uint32_t)(w[p][e] >> 32));
+            }
     }
     if (threadIdx.x == 0) __hip_atomic_store(P.ticket + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
@@ -295,7 +303,7 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
         }
         for (int round = 0; round < kRounds; round += kU) {
             const int r0 = round * kRows + lane / kGroups, i_of = i0 + f0 * 16 + r0;
-            const bool wide = P.wide && j < P.J;   // J is a multiple of 8 then
+            const bool wide = n == 8;
             u32x4 res[kU][kV];
             if (kForward && wide && P.residual)
 #pragma unroll
@@ -303,7 +311,7 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
 #pragma unroll
                     for (int k = 0; k < kV; ++k)
                         if (i_of + u * kRows < P.I)
-                            res[u][k] = ((const u32x4 *)((const TC *)P.residual + (i_of + u * kRows) * P.ldr + j))[k];
+                            res[u][k] = ((const u32x4_any *)((const TC *)P.residual + (i_of + u * kRows) * P.ldr + j))[k];
             float v[kU * 8];
 #pragma unroll
             for (int u = 0; u < kU; ++u) {
@@ -325,8 +333,8 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
                         if (i >= P.I) continue;
                         float *o = P.z + (long long)i * P.J + j;
                         if (wide) {
-                            ((f32x4 *)o)[0] = f32x4{v[u * 8], v[u * 8 + 1], v[u * 8 + 2], v[u * 8 + 3]};
-                            ((f32x4 *)o)[1] = f32x4{v[u * 8 + 4], v[u * 8 + 5], v[u * 8 + 6], v[u * 8 + 7]};
+                            ((f32x4_any *)o)[0] = f32x4{v[u * 8], v[u * 8 + 1], v[u * 8 + 2], v[u * 8 + 3]};
+                            ((f32x4_any *)o)[1] = f32x4{v[u * 8 + 4], v[u * 8 + 5], v[u * 8 + 6], v[u * 8 + 7]};
                         } else {
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
@@ -353,7 +361,7 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
                     u32x4 w[kV];
                     __builtin_memcpy(w, t, sizeof t);
 #pragma unroll
-                    for (int k = 0; k < kV; ++k) ((u32x4 *)o)[k] = w[k];
+                    for (int k = 0; k < kV; ++k) ((u32x4_any *)o)[k] = w[k];
                 } else {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
@@ -519,11 +527,11 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
                                                                   own, [](int, int) { return 0.0f; });
 }
 
-// One operand tile on its way through registers: kSets steps of it, 8-value chunks, loaded 16 bytes
-// at a time at any alignment of the element; where a chunk may pass the end of its row (K_ROWS:
-// the last k; K_COLS: the last row of the operand), one value at a time.
-constexpr int kSets = 2;
-
+// One operand tile on its way through registers: 8-value chunks, loaded 16 bytes at a time at any
+// alignment of the element.  Where a chunk may pass the end of its row (K_ROWS:
+// the last k; K_COLS: the last row of the operand), bf16 values are loaded one at a time, as a word
+// that is half in the buffer would read as zero; of 32-bit values those past the last k are
+// masked afterwards, and those past the last row reach only sums that are not stored.
 template <typename T, int L, int R, int BK, int THREADS>
 struct Chunks {
     using Tile = DirectTile<L, R, BK, THREADS / 64>;   // whose LDS layout the chunks follow
@@ -536,7 +544,7 @@ struct Chunks {
     int rows, K;
     int off[kN];
     int at[kN];     // first k (K_COLS: first row) of a lane's chunk in the tile
-    uint32_t reg[kSets][kN][kWords];
+    uint32_t reg[kN][kWords];
 
     __device__ __forceinline__ void init(const void *p, long long ld_elems, int row0, int n_rows, int n_k, int k0)
     {
@@ -553,8 +561,7 @@ struct Chunks {
         }
     }
 
-    // Load the tile at k into set SET; past the end: an empty buffer, nothing is read.
-    template <int SET>
+    // Load the tile at k; past the end: an empty buffer, nothing is read.
     __device__ __forceinline__ void load(int k)
     {
         const int left = K - k;
@@ -570,7 +577,7 @@ struct Chunks {
         const int end = left <= 0 || rows <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
         const int stop = L == K_ROWS ? left : rows;   // values of the chunk's direction that exist
-        const bool tail = L == K_ROWS ? left < BK : rows < R;
+        const bool tail = kSize == 2 && (L == K_ROWS ? left < BK : rows < R);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             if (!tail) {
@@ -578,7 +585,7 @@ struct Chunks {
                 for (int h = 0; h < kWords / 4; ++h) {
                     const u32x4 w = __builtin_amdgcn_raw_buffer_load_b128(rsrc, off[n] + h * 16, 0, 0);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) reg[SET][n][h * 4 + q] = w[q];
+                    for (int q = 0; q < 4; ++q) reg[n][h * 4 + q] = w[q];
                 }
                 continue;
             }
@@ -586,23 +593,32 @@ struct Chunks {
             for (int e = 0; e < 8; ++e) {
                 const int o = at[n] + e < stop ? off[n] + e * kSize : 0x7FFFFFF0;
                 if (kSize == 4) {
-                    reg[SET][n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
+                    reg[n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
                 } else {
                     const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
-                    if (e & 1) reg[SET][n][e / 2] |= v << 16;
-                    else reg[SET][n][e / 2] = v;
+                    if (e & 1) reg[n][e / 2] |= v << 16;
+                    else reg[n][e / 2] = v;
                 }
             }
         }
     }
 
-    template <int SET>
+    // What a 32-bit chunk of the tile at k read past its row's last k becomes 0.
+    __device__ __forceinline__ void mask(int k)
+    {
+        if (kSize == 2 || L == K_COLS || K - k >= BK) return;
+#pragma unroll
+        for (int n = 0; n < kN; ++n)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) reg[n][e % kWords] = at[n] + e < K - k ? reg[n][e % kWords] : 0;
+    }
+
     __device__ __forceinline__ void values(float (&x)[8], int n) const
     {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            if (kSize == 4) x[e] = __builtin_bit_cast(float, reg[SET][n][e % kWords]);
-            else x[e] = __builtin_bit_cast(float, e & 1 ? reg[SET][n][e / 2] & 0xFFFF0000u : reg[SET][n][e / 2] << 16);
+            if (kSize == 4) x[e] = __builtin_bit_cast(float, reg[n][e % kWords]);
+            else x[e] = __builtin_bit_cast(float, e & 1 ? reg[n][e / 2] & 0xFFFF0000u : reg[n][e / 2] << 16);
         }
     }
 };
@@ -638,12 +654,14 @@ struct Stored {
         if (second) c.init(P.b, P.ldb, row0, P.J, n_k, k0);
         else c.init(P.a, P.lda, row0, P.I, n_k, k0);
     }
-    template <int SET>
     __device__ __forceinline__ void load(int k)
     {
-        c.template load<SET>(k);
+        c.load(k);
     }
-    template <int SET>
+    __device__ __forceinline__ void mask(int k)
+    {
+        c.mask(k);
+    }
     __device__ __forceinline__ void store(lds_char *to) const
     {
 #pragma unroll
@@ -651,10 +669,10 @@ struct Stored {
             lds_char *dst = to + (n * THREADS + threadIdx.x) * 16;
             if (C::kSize == 2) {
                 *(__attribute__((address_space(3))) u32x4 *)dst =
-                    u32x4{c.reg[SET][n][0], c.reg[SET][n][1], c.reg[SET][n][2], c.reg[SET][n][3]};
+                    u32x4{c.reg[n][0], c.reg[n][1], c.reg[n][2], c.reg[n][3]};
             } else {
                 float x[8];
-                c.template values<SET>(x, n);
+                c.values(x, n);
                 split<PLANES, kPlane>(dst, x);
             }
         }
@@ -680,11 +698,11 @@ __device__ __forceinline__ float plain_sum(const Args &P, int i, int j)
 
 // A product whose operands A and B go through registers and are held in LDS as bf16 planes; of the
 // products of planes those are formed that reach the sum's 24 bits: 6 for 3 x 3 planes, whose
-// left-out ones are below 2^-24 of the product of magnitudes.  Steps t + 2 and t + 3 are on their way
-// into registers while step t is computed.  With BUF = 2 the split of step t + 1 and its way to
-// LDS fall between step t's matrix instructions, at one barrier a step; with BUF = 1 they come
-// after, and two workgroups share a compute unit, so that one computes while the other
-// stores.
+// left-out ones are below 2^-24 of the product of magnitudes.  With BUF = 2 the split of step t + 1 and
+// its way to LDS fall between step t's matrix instructions, at one barrier a step, and step t + 2 is
+// on its way into registers; with BUF = 1 they come after, and two workgroups share a compute
+// unit, so that one computes while the other stores.  (Two steps in registers instead of one
+// gave nothing: 90 us for 2048^3 either way.)
 template <class A, class B, typename TC, int BM, int BN, int WI, int WJ, int BUF, bool kForward>
 struct Staged {
     static constexpr int BK = 32, kWaves = WI * WJ, kThreads = 64 * kWaves, TI = BM / WI, TJ = BN / WJ, FI = TI / 16,
@@ -700,50 +718,45 @@ struct Staged {
     int wi, wj;
     f32x4 acc[FI][FJ];
 
-    // Compute step t from here; set SET holds step t + 1.
-    template <int SET>
+    // Compute step t from here; step t + 1 is in the registers.
     __device__ __forceinline__ void step(lds_char *here, lds_char *next, int t)
     {
-        bf16x8 fa[PA][FI], fb[PB][FJ];
+        ta.mask((t + 1) * BK);
+        tb.mask((t + 1) * BK);
+        bf16x8 fb[PB][FJ];
 #pragma unroll
-        for (int p = PB - 1; p >= 0; --p)
+        for (int p = 0; p < PB; ++p)
 #pragma unroll
             for (int g = 0; g < FJ; ++g)
                 fb[p][g] = fb_of.fragment(here + A::kBytes + p * B::kPlane, wj * TJ + g * 16, 0);
 #pragma unroll
-        for (int p = PA - 1; p >= 0; --p)
+        for (int f = 0; f < FI; ++f) {
 #pragma unroll
-            for (int f = 0; f < FI; ++f) fa[p][f] = fa_of.fragment(here + p * A::kPlane, wi * TI + f * 16, 0);
-        // small products first
-        constexpr int kPairs = kMost == 3 ? 6 : PA * PB, kFirst = (kPairs - 1) / 3, kSecond = (kPairs - 1) * 2 / 3;
-        int pair = 0;
+            for (int p = PA - 1; p >= 0; --p) {   // small products first
+                const bf16x8 fa = fa_of.fragment(here + p * A::kPlane, wi * TI + f * 16, 0);
 #pragma unroll
-        for (int sum = kMost - 1; sum >= 0; --sum)
-#pragma unroll
-            for (int p = 0; p < PA; ++p) {
-                const int q = sum - p;
-                if (q < 0 || q >= PB) continue;
-#pragma unroll
-                for (int f = 0; f < FI; ++f)
+                for (int q = PB - 1; q >= 0; --q) {
+                    if (p + q >= kMost) continue;
 #pragma unroll
                     for (int g = 0; g < FJ; ++g)
-                        acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa[p][f], acc[f][g], 0, 0, 0);
-                if (BUF == 2 && pair == kFirst) {
-                    ta.template store<SET>(next);
-                    ta.template load<SET>((t + 1 + kSets) * BK);
+                        acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[q][g], fa, acc[f][g], 0, 0, 0);
                 }
-                if (BUF == 2 && pair == kSecond) {
-                    tb.template store<SET>(next + A::kBytes);
-                    tb.template load<SET>((t + 1 + kSets) * BK);
-                }
-                ++pair;
             }
+            if (BUF == 2 && f == FI / 2 - 1) {
+                ta.store(next);
+                ta.load((t + 2) * BK);
+            }
+            if (BUF == 2 && f == FI - 1) {
+                tb.store(next + A::kBytes);
+                tb.load((t + 2) * BK);
+            }
+        }
         if (BUF == 1) {
             barrier();
-            ta.template store<SET>(here);
-            tb.template store<SET>(here + A::kBytes);
-            ta.template load<SET>((t + 1 + kSets) * BK);
-            tb.template load<SET>((t + 1 + kSets) * BK);
+            ta.store(here);
+            tb.store(here + A::kBytes);
+            ta.load((t + 2) * BK);
+            tb.load((t + 2) * BK);
         }
         __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
         barrier();
@@ -765,23 +778,18 @@ struct Staged {
 #pragma unroll
             for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         lds_char *const other = lds + (BUF - 1) * kTiles;
-        ta.template load<0>(0);
-        tb.template load<0>(0);
-        ta.template load<1>(BK);
-        tb.template load<1>(BK);
-        ta.template store<0>(lds);
-        tb.template store<0>(lds + A::kBytes);
-        ta.template load<0>(2 * BK);
-        tb.template load<0>(2 * BK);
+        ta.load(0);
+        tb.load(0);
+        ta.mask(0);
+        tb.mask(0);
+        ta.store(lds);
+        tb.store(lds + A::kBytes);
+        ta.load(BK);
+        tb.load(BK);
         __builtin_amdgcn_s_waitcnt(0xC07F);
         barrier();
         const int steps = (kn + BK - 1) / BK;
-        int t = 0;
-        for (; t + 1 < steps; t += 2) {
-            step<1>(lds, other, t);
-            step<0>(other, lds, t + 1);
-        }
-        if (t < steps) step<1>(lds, other, t);
+        for (int t = 0; t < steps; ++t) step(t & 1 ? other : lds, t & 1 ? lds : other, t);
         if (P.parts > 1 && !joined<FI, FJ, kThreads>(P, acc, ti * P.tiles_j + tj, part, ti * BM + wi * TI)) return;
         finish<TC, FI, FJ, kTurn, kForward, (PA > 1 || PB > 1)>(P, acc, ti * BM + wi * TI, tj * BN + wj * TJ,
                                                                 lds + wave * kTurnBytes,
@@ -789,8 +797,8 @@ struct Staged {
     }
 };
 
-// 2048^3 in fp32 (256 tiles of 128 x 128, one a compute unit): 91 us with two buffers, 102 with
-// one; 4096^3 (1024 tiles): 693 and 640.
+// 2048^3 in fp32 (256 tiles of 128 x 128, one a compute unit): 92 us with two buffers, 104 with
+// one; 4096^3 (1024 tiles): 693 and 649, 212 TFLOP/s.
 template <typename T, int PLANES, int LA, int LB, int BM, int BN, int WI, int WJ, int BUF>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
 {
