@@ -106,8 +106,9 @@ SmallCut small_gradients_cut(int M, int N, int K)
             const long long tw = (long long)ceil_div(N, 16 * fi) * ceil_div(K + 1, 16);
             const float work = (tx * ceil_div(N, 32) + tw * ceil_div(M, 32)) * (fi * 1500.0f + 400.0f) / 2.15e6f;
             const int at = fi == 1 ? 2 : 1;   // steps a wave loads together
-            const float wait = ceil_div(steps, waves * at) * (1.2f + 0.7f * fi * at);
-            const float us = 3.5f + std::max(work, wait) + (tx + tw) * waves * 1e-4f;
+            const float wait = ceil_div(steps, waves * at) * (1.8f + 0.8f * fi * at);
+            const float ends = (tx + tw) * waves * 2.5f / (kUnits * 32);   // workgroups' starts and epilogues
+            const float us = 3.5f + std::max(work, wait) + ends;
             if (!best.fi || us < best.us) best = {fi, waves, us};
         }
     return best;
@@ -132,18 +133,16 @@ bool aligned(const void *p, long long ld, size_t elem)
     return (uintptr_t)p % 16 == 0 && ld * (long long)elem % 16 == 0;
 }
 
-// Whether bf16 operands can be loaded straight into LDS.
-bool direct_bf16(const Args &P, int la, int lb)
+// Whether a bf16 operand can be loaded straight into LDS: 16-byte rows, and zeros (or nothing) after the last k.
+bool straight(const void *p, long long ld, int layout, int K)
 {
-    return aligned(P.a, P.lda, 2) && aligned(P.b, P.ldb, 2) && ((la == K_COLS && lb == K_COLS) || P.K % 8 == 0);
+    return aligned(p, ld, 2) && (layout == K_COLS || K % 8 == 0);
 }
 
 // Runs one product on tiles; P holds everything but its cut.
 template <typename T>
-hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStream_t s)
+hipError_t run_product(Args P, int la, int lb, const Cut &c, bool direct, const DenseWorkspace &ws, hipStream_t s)
 {
-    const bool direct = sizeof(T) == 2 && direct_bf16(P, la, lb);
-    const Cut c = best_cut(P.I, P.J, P.K, sizeof(T), direct);
     P.tiles_i = ceil_div(P.I, c.side);
     P.tiles_j = ceil_div(P.J, c.side);
     P.k_part = ceil_div(ceil_div(P.K, c.parts), 32) * 32;
@@ -154,13 +153,68 @@ hipError_t run_product(Args P, int la, int lb, const DenseWorkspace &ws, hipStre
     return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, shape, s) : launch_fp32(P, la, lb, shape, s);
 }
 
+// ---- bf16 rows that cannot be loaded straight into LDS ----
+//
+// Their products run at about half the rate (2049 x 2051 x 2047: 57 us; 2048^3: 24).  Where that costs more than a copy
+// in rows of a multiple of eight, zeros after the last value, the copy is made first.
+
+int pad8(int n) { return (n + 7) & ~7; }
+
+// Up to two arrays [rows][K] copied into rows of Kp.
+__global__ __launch_bounds__(256) void k_pad(const uint16_t *a, long long lda, int rows_a, const uint16_t *b, long long ldb,
+                                             int rows_b, int K, int Kp, uint16_t *to_a, uint16_t *to_b)
+{
+    const int chunks = Kp / 8;
+    const long long all = (long long)(rows_a + rows_b) * chunks;
+    for (long long e = (long long)blockIdx.x * 256 + threadIdx.x; e < all; e += (long long)gridDim.x * 256) {
+        const long long row = e / chunks;
+        const int c = (int)(e % chunks) * 8, n = min(8, K - c);
+        const bool second = row >= rows_a;
+        const uint16_t *from = second ? b + (row - rows_a) * ldb + c : a + row * lda + c;
+        uint16_t *to = (second ? to_b + (row - rows_a) * Kp : to_a + row * Kp) + c;
+        u32x4 w;
+        if (n == 8) {
+            w = *(const u32x4_any *)from;
+        } else {
+            uint16_t t[8] = {};
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (k < n) t[k] = from[k];
+            __builtin_memcpy(&w, t, 16);
+        }
+        *(u32x4 *)to = w;
+    }
+}
+
+// Copies of x and w; an array that is not wanted has no rows.
+struct Padded {
+    const void *x, *w;
+    hipError_t e;
+};
+
+Padded pad(const void *x, long long ldx, int rows_x, const void *w, long long ldw, int rows_w, int K,
+           const DenseWorkspace &ws, hipStream_t s)
+{
+    const int Kp = pad8(K);
+    uint16_t *to_x = (uint16_t *)ws.pad, *to_w = to_x + (size_t)rows_x * Kp;
+    const long long chunks = (long long)(rows_x + rows_w) * (Kp / 8);
+    k_pad<<<(unsigned)std::min<long long>((chunks + 255) / 256, 8192), 256, 0, s>>>(
+        (const uint16_t *)x, ldx, rows_x, (const uint16_t *)w, ldw, rows_w, K, Kp, to_x, to_w);
+    return {to_x, to_w, hipGetLastError()};
+}
+
+float pad_us(int rows, int K)
+{
+    return rows ? 4.0f + (float)rows * K * 4 / 4.5e6f : 0.0f;
+}
+
 constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; eight threads go down the rows
 
-// dz = alpha act'(z) dy (written if dz is not null) and its sums over `chunk` rows.  Bound by memory;
+// dz = alpha act'(z) dy (written, if dz is not null, in rows of lddz: N, or the next multiple of eight) and its sums over `chunk` rows.  Bound by memory;
 // 16 bytes at any alignment, single values where a row ends.
 template <typename T>
-__global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, float *rows, int M,
-                                               int N, int chunk, int act, float alpha)
+__global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, int lddz, float *rows,
+                                               int M, int N, int chunk, int act, float alpha)
 {
     __shared__ float part[8][kSlopeCols];
     const int lane = threadIdx.x & 31, down = threadIdx.x >> 5;
@@ -203,8 +257,8 @@ __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, cons
 #pragma unroll
         for (int k = 0; k < 8; ++k) sum[k] += d[k], narrow(d[k], t[k]);
         if (!dz) continue;
-        T *to = dz + (long long)r * N + c;
-        if (n == 8) {
+        T *to = dz + (long long)r * lddz + c;
+        if (n == 8 || lddz != N) {   // rows of a multiple of eight end with zeros
             u32x4 w[kV];
             __builtin_memcpy(w, t, sizeof t);
 #pragma unroll
@@ -286,12 +340,28 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
     P.bias = a.bias, P.residual = a.residual, P.ldr = a.ldr;
     P.z = a.act == HQML_ACT_NONE ? nullptr : (float *)a.z;
     P.act = a.act, P.alpha = a.alpha;
-    const SmallCut c = small_cut(P.I, P.J, P.K, sizeof(T));
-    if (c.us <= best_cut(P.I, P.J, P.K, sizeof(T), sizeof(T) == 2 && direct_bf16(P, K_ROWS, K_ROWS)).us) {
-        cut_small(P, c.fi);
-        return launch_small_forward(P, sizeof(T) == 2, c.fi, c.waves, s);
+    bool direct = false;
+    int copy_x = 0, copy_w = 0;   // rows to copy
+    Cut c = best_cut(P.I, P.J, P.K, sizeof(T), false);
+    if (sizeof(T) == 2) {
+        if (!straight(a.x, a.ldx, K_ROWS, a.K)) copy_x = a.M;
+        if (!straight(a.w, a.ldw, K_ROWS, a.K)) copy_w = a.N;
+        const Cut d = best_cut(P.I, P.J, P.K, 2, true);
+        direct = !(copy_x + copy_w) || (ws.pad && d.us + pad_us(copy_x + copy_w, a.K) < c.us);
+        if (direct) c = d, c.us += pad_us(copy_x + copy_w, a.K);
     }
-    return run_product<T>(P, K_ROWS, K_ROWS, ws, s);
+    const SmallCut sc = small_cut(P.I, P.J, P.K, sizeof(T));
+    if (sc.us <= c.us) {
+        cut_small(P, sc.fi);
+        return launch_small_forward(P, sizeof(T) == 2, sc.fi, sc.waves, s);
+    }
+    if (direct && copy_x + copy_w) {
+        const Padded p = pad(a.x, a.ldx, copy_x, a.w, a.ldw, copy_w, a.K, ws, s);
+        if (p.e != hipSuccess) return p.e;
+        if (copy_x) P.a = p.x, P.lda = pad8(a.K);
+        if (copy_w) P.b = p.w, P.ldb = pad8(a.K);
+    }
+    return run_product<T>(P, K_ROWS, K_ROWS, c, direct, ws, s);
 }
 
 // dx, dw and db in one launch.
@@ -326,15 +396,29 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         e = zero<T>(a.dw, (long long)a.N * a.K, s);
         return e != hipSuccess ? e : zero<T>(a.db, a.N, s);
     }
+    // dx = dz w and dw = dz^T x: the cuts, and for bf16 whether to copy what cannot be loaded straight
+    Cut cx = best_cut(a.M, a.K, a.N, sizeof(T), false), cw = best_cut(a.N, a.K, a.M, sizeof(T), false);
+    bool form = a.act != HQML_ACT_NONE, direct = false;
+    int copy_x = 0, copy_w = 0;   // rows to copy
+    if (sizeof(T) == 2) {
+        if (!straight(a.x, a.ldx, K_COLS, 0) && a.dw) copy_x = a.M;
+        if (!straight(a.w, a.ldw, K_COLS, 0) && a.dx) copy_w = a.N;
+        const bool dy_straight = straight(a.dy, a.lddy, K_ROWS, a.N);
+        const Cut dx = best_cut(a.M, a.K, a.N, 2, true), dw = best_cut(a.N, a.K, a.M, 2, true);
+        const float copies = pad_us(copy_x + copy_w, a.K) + (form || dy_straight ? 0.0f : pad_us(a.M, a.N));
+        direct = (form || dy_straight || ws.dz) && (!(copy_x + copy_w) || ws.pad) && dx.us + dw.us + copies < cx.us + cw.us;
+        if (direct) {
+            cx = dx, cw = dw, cx.us += copies;
+            form = form || !dy_straight;   // dz in rows of a multiple of eight
+        }
+    }
     const SmallCut c = small_gradients_cut(a.M, a.N, a.K);
-    const bool two = sizeof(T) == 2;
-    const float apart = slope_us(a.M, a.N, sizeof(T)) + best_cut(a.M, a.K, a.N, sizeof(T), two).us +
-                        best_cut(a.N, a.K, a.M, sizeof(T), two).us;
-    if (c.us <= apart) return gradients<T>(a, c, s);
+    if (c.us <= slope_us(a.M, a.N, sizeof(T)) + cx.us + cw.us) return gradients<T>(a, c, s);
     const T *dz = (const T *)a.dy;
     long long lddz = a.lddy;
     float alpha = a.alpha;
-    const bool form = a.act != HQML_ACT_NONE && (a.dx || a.dw);
+    form = form && (a.dx || a.dw);
+    const int Np = sizeof(T) == 2 ? pad8(a.N) : a.N;   // a row of dz in the workspace
     if (form || a.db) {
         const int chunk = row_chunk(a.M, a.N), chunks = ceil_div(a.M, chunk);
         for (int c0 = 0; c0 < chunks; c0 += 65535) {   // grid limit in y
@@ -343,7 +427,7 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
             const dim3 grid((unsigned)ceil_div(a.N, kSlopeCols), (unsigned)n);
             k_slope<T><<<grid, 256, 0, s>>>((const T *)a.dy + r0 * a.lddy, a.lddy,
                                             a.act != HQML_ACT_NONE ? a.z + r0 * a.N : nullptr,
-                                            form ? (T *)ws.dz + r0 * a.N : nullptr,
+                                            form ? (T *)ws.dz + r0 * Np : nullptr, Np,
                                             a.db ? ws.rows + (long long)c0 * a.N : nullptr,
                                             (int)std::min<long long>(a.M - r0, (long long)n * chunk), a.N, chunk, a.act,
                                             a.alpha);
@@ -353,22 +437,30 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
             k_row_sum<T><<<(unsigned)ceil_div(a.N, 32), 256, 0, s>>>(ws.rows, chunks, a.N, (T *)a.db);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
-        if (form) dz = (const T *)ws.dz, lddz = a.N, alpha = 1.0f;
+        if (form) dz = (const T *)ws.dz, lddz = Np, alpha = 1.0f;
+    }
+    const void *x = a.x, *w = a.w;
+    long long ldx = a.ldx, ldw = a.ldw;
+    if (direct && copy_x + copy_w) {
+        const Padded p = pad(a.x, a.ldx, copy_x, a.w, a.ldw, copy_w, a.K, ws, s);
+        if (p.e != hipSuccess) return p.e;
+        if (copy_x) x = p.x, ldx = pad8(a.K);
+        if (copy_w) w = p.w, ldw = pad8(a.K);
     }
     Args P{};
     P.a = dz, P.lda = lddz;
     P.act = HQML_ACT_NONE, P.alpha = alpha;
     if (a.dx) {
-        P.b = a.w, P.ldb = a.ldw;
+        P.b = w, P.ldb = ldw;
         P.I = a.M, P.J = a.K, P.K = a.N;
         P.c = a.dx, P.ldc = a.lddx;
-        if ((e = run_product<T>(P, K_ROWS, K_COLS, ws, s)) != hipSuccess) return e;
+        if ((e = run_product<T>(P, K_ROWS, K_COLS, cx, direct, ws, s)) != hipSuccess) return e;
     }
     if (a.dw) {
-        P.b = a.x, P.ldb = a.ldx;
+        P.b = x, P.ldb = ldx;
         P.I = a.N, P.J = a.K, P.K = a.M;
         P.c = a.dw, P.ldc = a.K;
-        if ((e = run_product<T>(P, K_COLS, K_COLS, ws, s)) != hipSuccess) return e;
+        if ((e = run_product<T>(P, K_COLS, K_COLS, cw, direct, ws, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -379,7 +471,9 @@ DenseWorkspace dense_workspace(const hqml_dense_config &cfg)
 {
     DenseWorkspace ws;
     const size_t M = (size_t)cfg.max_batch, N = (size_t)cfg.out_features;
-    if (cfg.activation != HQML_ACT_NONE) ws.dz_bytes = M * N * (cfg.dtype == HQML_DTYPE_BF16 ? 2 : 4);
+    const bool two = cfg.dtype == HQML_DTYPE_BF16;
+    if (cfg.activation != HQML_ACT_NONE || (two && N % 8)) ws.dz_bytes = M * (two ? pad8(cfg.out_features) * 2 : N * 4);
+    if (two && cfg.in_features % 8) ws.pad_bytes = (M + N) * (size_t)pad8(cfg.in_features) * 2;
     // a smaller batch may have more chunks of fewer rows
     const size_t chunk = (size_t)row_chunk(cfg.max_batch, cfg.out_features);
     ws.rows_bytes = std::max((M + chunk - 1) / chunk, (std::min(M, (size_t)kFewRows) + 15) / 16) * N * 4;

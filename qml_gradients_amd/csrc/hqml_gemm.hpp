@@ -96,6 +96,7 @@ struct DirectTile {
     const char *base;
     long long ld;      // bytes
     int rows, K;
+    int span;          // bytes of the buffer: of the rows before the tile's last one (K_ROWS), of one k (K_COLS)
     int off[kLoads];   // byte offset of a lane's chunk in the tile; K_COLS: past the end if its rows are
     int at;            // K_ROWS: first k of a lane's chunk (the same in all its rows: they are 8 n apart)
     int frag;          // byte of a lane's part of the fragment at row 0, k 0
@@ -111,6 +112,9 @@ struct DirectTile {
         ld = ld_elems * 2;
         rows = n_rows - row0;
         K = n_k;
+        // an odd number of rows (K_COLS) ends in the middle of a word, which would read as zero: the whole
+        // aligned word is let in, and its other half reaches only sums that are not stored
+        span = L == K_ROWS ? ((rows < R ? rows : R) - 1) * (int)ld : (2 * rows + 3) & ~3;
         base = (const char *)p + (L == K_ROWS ? row0 * ld + k0 * 2ll : k0 * ld + row0 * 2ll);
         const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
@@ -148,17 +152,10 @@ struct DirectTile {
     __device__ __forceinline__ Step begin(int k) const
     {
         const int left = K - k;
-        long long bytes;
-        const char *p;
-        if (L == K_ROWS) {
-            p = base + 2ll * k;
-            bytes = (long long)(rows - 1) * ld + 2ll * left;
-        } else {
-            p = base + k * ld;
-            bytes = (long long)(left - 1) * ld + 2ll * rows;
-        }
-        const int end = left <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
-        return {p, end, left};
+        const char *p = L == K_ROWS ? base + 2ll * k : base + k * ld;
+        // K_ROWS: rows end with zeros up to a multiple of eight
+        const int end = L == K_ROWS ? span + ((2 * left + 15) & ~15) : (left < BK ? left - 1 : BK - 1) * (int)ld + span;
+        return {p, left <= 0 ? 0 : end, left};
     }
 
     // Queue load n of kLoads.
@@ -542,6 +539,7 @@ struct Chunks {
     const char *base;
     long long ld;   // bytes
     int rows, K;
+    int span;       // bytes of the buffer: of the rows before the tile's last one (K_ROWS), of one k (K_COLS)
     int off[kN];
     int at[kN];     // first k (K_COLS: first row) of a lane's chunk in the tile
     uint32_t reg[kN][kWords];
@@ -551,6 +549,7 @@ struct Chunks {
         ld = ld_elems * kSize;
         rows = n_rows - row0;
         K = n_k;
+        span = L == K_ROWS ? ((rows < R ? rows : R) - 1) * (int)ld : rows * kSize;
         base = (const char *)p + (L == K_ROWS ? row0 * ld + (long long)k0 * kSize : k0 * ld + (long long)row0 * kSize);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
@@ -565,16 +564,9 @@ struct Chunks {
     __device__ __forceinline__ void load(int k)
     {
         const int left = K - k;
-        long long bytes;
-        const char *p;
-        if (L == K_ROWS) {
-            p = base + (long long)k * kSize;
-            bytes = (long long)(rows - 1) * ld + (long long)left * kSize;
-        } else {
-            p = base + k * ld;
-            bytes = (long long)(left - 1) * ld + (long long)rows * kSize;
-        }
-        const int end = left <= 0 || rows <= 0 ? 0 : bytes > 0x7FFFFFE0 ? 0x7FFFFFE0 : (int)bytes;
+        const char *p = L == K_ROWS ? base + (long long)k * kSize : base + k * ld;
+        const int bytes = L == K_ROWS ? span + left * kSize : (left < BK ? left - 1 : BK - 1) * (int)ld + span;
+        const int end = left <= 0 ? 0 : bytes;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
         const int stop = L == K_ROWS ? left : rows;   // values of the chunk's direction that exist
         const bool tail = kSize == 2 && (L == K_ROWS ? left < BK : rows < R);

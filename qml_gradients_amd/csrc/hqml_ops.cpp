@@ -64,7 +64,8 @@ size_t up256(size_t b)
 
 size_t total_bytes(const DenseWorkspace &ws)
 {
-    return up256(ws.dz_bytes) + up256(ws.rows_bytes) + up256(ws.part_bytes) + up256(ws.ticket_bytes);
+    return up256(ws.dz_bytes) + up256(ws.rows_bytes) + up256(ws.part_bytes) +
+           up256(ws.ticket_bytes) + up256(ws.pad_bytes);
 }
 
 int check_dense_config(const hqml_dense_config *c, std::string *err)
@@ -189,7 +190,7 @@ int dense_create(const hqml_dense_config *cfg, hqml_dense **out)
     size_t free_b = 0, all_b = 0;
     hipError_t e = hipMemGetInfo(&free_b, &all_b);
     if (e != hipSuccess) return thread_error(HQML_ERR_HIP, hip_text("hipMemGetInfo", e));
-    const size_t need = total_bytes(ws) > 0 ? total_bytes(ws) : 256;
+    const size_t need = total_bytes(ws);
     if (need > free_b) {
         char msg[160];
         std::snprintf(msg, sizeof msg, "workspace needs %zu bytes, device has %zu free", need, free_b);
@@ -208,10 +209,17 @@ int dense_create(const hqml_dense_config *cfg, hqml_dense **out)
     h->cfg = *cfg;
     h->stream = reinterpret_cast<hipStream_t>(cfg->stream);
     h->reserved = p;
-    ws.dz = p;
-    ws.rows = reinterpret_cast<float *>(p + up256(ws.dz_bytes));
-    ws.part = reinterpret_cast<float *>(p + up256(ws.dz_bytes) + up256(ws.rows_bytes));
-    ws.ticket = reinterpret_cast<unsigned *>(reinterpret_cast<char *>(ws.part) + up256(ws.part_bytes));
+    char *at = p;
+    auto take = [&](size_t bytes) -> void * {
+        char *here = at;
+        at += up256(bytes);
+        return bytes ? here : nullptr;
+    };
+    ws.dz = take(ws.dz_bytes);
+    ws.rows = static_cast<float *>(take(ws.rows_bytes));
+    ws.part = static_cast<float *>(take(ws.part_bytes));
+    ws.ticket = static_cast<unsigned *>(take(ws.ticket_bytes));
+    ws.pad = take(ws.pad_bytes);
     if (ws.ticket_bytes) {
         e = hipMemsetAsync(ws.ticket, 0, ws.ticket_bytes, h->stream);
         if (e == hipSuccess) e = hipStreamSynchronize(h->stream);

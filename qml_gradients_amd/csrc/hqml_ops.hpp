@@ -30,11 +30,12 @@ struct DenseBackward {
 
 // Parts of a handle's workspace (byte counts and, once reserved, addresses).
 struct DenseWorkspace {
-    size_t dz_bytes = 0;     // gradient at z, [M][N] in dtype
+    size_t dz_bytes = 0;     // gradient at z in dtype, rows of N (bf16: the next multiple of eight)
     size_t rows_bytes = 0;   // partial row sums of dz, fp32
     size_t part_bytes = 0;   // partial sums of products split over k, fp32
     size_t ticket_bytes = 0; // one counter a tile of them, 0 between calls
-    void *dz = nullptr;
+    size_t pad_bytes = 0;    // bf16 copies of x and w in aligned rows, where in_features does not allow 16-byte ones
+    void *dz = nullptr, *pad = nullptr;
     float *rows = nullptr;
     float *part = nullptr;
     unsigned *ticket = nullptr;

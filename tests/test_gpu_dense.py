@@ -157,6 +157,31 @@ def test_strided_and_misaligned_rows(shape, offset, pad, dtype):
     assert int(torch.isnan(whole).sum()) == M * (offset + pad)
 
 
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(700, 333, 501), (333, 1021, 517), (1001, 520, 263), (515, 1029, 1024), (61, 2500, 3001)])
+@pytest.mark.parametrize("pad", [0, 16])
+def test_odd_lengths_of_large_products(shape, pad, dtype):
+    """Odd lengths in every direction at sizes that go to the large tiles; with `pad`, rows that
+    begin 16-byte aligned all the same, NaN between them."""
+    M, K, N = shape
+    say(f"[gpu] dense odd {shape} pad {pad} {dtype}")
+    d = make(M, K, N, dtype, 37)
+    want = expect(d, dtype, "silu", 1.0)
+    if pad:
+        for k in ("x", "w", "residual", "dy"):
+            t = d[k]
+            wide = torch.full((t.shape[0], (t.shape[1] + pad) // 8 * 8), float("nan"), dtype=t.dtype, device="cuda")
+            wide[:, :t.shape[1]] = t
+            d[k] = wide[:, :t.shape[1]]
+    got = run(d, dtype, "silu", 1.0)
+    for name in want:
+        check(name, got[name], want[name])
+    plain = expect(d, dtype, "none", 1.0)   # no activation: dy itself is an operand
+    got = run(d, dtype, "none", 1.0)
+    for name in plain:
+        check(name, got[name], plain[name])
+
+
 def test_transposed_weights_are_copied():
     d = make(40, 56, 24, "fp32", 3)
     d["w"] = d["w"].t().contiguous().t()
