@@ -35,7 +35,7 @@ struct TileCost {
     float fixed, step, share, join, join_part;
 };
 constexpr TileCost kFp32Cost[] = {{64, 4.0f, 0.70f, 0.55f, 1.5f, 0.4f}, {128, 5.0f, 1.20f, 1.42f, 4.0f, 1.0f}};
-constexpr TileCost kStagedCost[] = {{64, 4.0f, 0.27f, 0.16f, 2.0f, 0.4f}, {128, 4.0f, 0.36f, 0.47f, 4.0f, 1.0f}};
+constexpr TileCost kStagedCost[] = {{64, 4.0f, 0.30f, 0.21f, 2.0f, 0.4f}, {128, 4.0f, 0.45f, 0.50f, 4.0f, 1.0f}};
 constexpr TileCost kDirectCost[] = {{64, 3.0f, 0.12f, 0.135f, 2.0f, 0.4f},
                                     {128, 4.0f, 0.22f, 0.32f, 4.0f, 1.0f},
                                     {256, 7.0f, 0.57f, 0.82f, 7.0f, 2.0f}};
@@ -45,16 +45,17 @@ struct Cut {
     float us;
 };
 
-Cut best_cut(int I, int J, int K, const TileCost *cost, int n)
+Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n)
 {
     const int steps = ceil_div(K, 32);
+    const float memory = ((float)I * K + (float)J * K + (float)I * J) * elem / 4.6e6f;
     Cut best{0, 1, 0.0f};
     for (int c = 0; c < n; ++c) {
         const long long tiles = (long long)ceil_div(I, cost[c].side) * ceil_div(J, cost[c].side);
         for (int parts : kParts) {
             if (parts > 1 && (tiles * parts > kPartTiles * 64 * 64 / (cost[c].side * cost[c].side) || parts * 2 > steps)) break;
             const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
-            float us = cost[c].fixed + ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share);
+            float us = cost[c].fixed + std::max(memory, ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share));
             if (parts > 1) us += cost[c].join + parts * cost[c].join_part;
             if (!best.side || us < best.us) best = {cost[c].side, parts, us};
         }
@@ -64,32 +65,43 @@ Cut best_cut(int I, int J, int K, const TileCost *cost, int n)
 
 Cut best_cut(int I, int J, int K, size_t elem, bool direct)
 {
-    if (elem == 4) return best_cut(I, J, K, kFp32Cost, 2);
-    return direct ? best_cut(I, J, K, kDirectCost, 3) : best_cut(I, J, K, kStagedCost, 2);
+    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 2);
+    return direct ? best_cut(I, J, K, elem, kDirectCost, 3) : best_cut(I, J, K, elem, kStagedCost, 2);
 }
 
 // A small forward product: every tile reads its own rows, at 40 bytes a cycle and compute unit; the fp32 matrix
-// instruction takes 8 x 32 cycles for 16 x 16 x 32; a wave waits for its loads once in kAt steps.
+// instruction takes 8 x 32 cycles for 16 x 16 x 32; a wave waits for its loads once in a few steps.
 struct SmallCut {
-    int fi, waves;
+    int fi, waves, parts;
     float us;
 };
 
 SmallCut small_cut(int I, int J, int K, size_t elem)
 {
-    SmallCut best{0, 1, 0.0f};
+    SmallCut best{0, 1, 1, 0.0f};
     const int steps = ceil_div(K, 32);
-    for (int fi : {1, 4})
+    const float bytes = ((float)I * K + (float)J * K + (float)I * J) * elem;
+    for (int fi : {1, 2, 4}) {
+        if (fi > 1 && I <= 8 * fi) break;
+        const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
         for (int waves : {1, 2, 4, 8, 16}) {
-            if (waves > 1 && (waves > steps || (waves == 16 && fi == 4))) break;
-            const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
-            const float each = (float)((tiles + kUnits - 1) / kUnits);
-            const float load = each * steps * (16 * 32 * elem * (fi + 1)) / 84e3f;
-            const float mul = elem == 2 ? 0.0f : each * steps * fi * 0.03f;
-            const float wait = ceil_div(steps, waves * (fi == 1 ? 4 : 2)) * 1.2f * std::max(1.0f, each * waves / 16);
-            const float us = 3.5f + std::max(load + mul, wait) + 0.05f * waves;
-            if (!best.fi || us < best.us) best = {fi, waves, us};
+            if (waves > 1 && (waves > steps || (waves == 16 && fi > 1))) break;
+            for (int parts : {1, 2, 3, 4, 6, 8}) {
+                if (parts > 1 && (tiles * parts > kUnits || parts * waves * 4 > steps)) break;
+                const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
+                const int own = ceil_div(steps, parts);   // of one workgroup
+                const float load = each * own * (16 * 32 * elem * (fi + 1)) / 65e3f;
+                const float mul = elem == 2 ? 0.0f : each * own * fi * 0.04f;
+                const float wait = ceil_div(own, waves * (fi == 4 ? 2 : 4)) * 1.2f * std::max(1.0f, each * waves / 16);
+                // memory's rate needs about 40 KB under way on a compute unit
+                const float under_way = each * waves * (fi == 4 ? 2 : 4) * 16 * 32 * elem;
+                const float memory = bytes / (4.6e6f * std::min(1.0f, under_way / 40e3f));
+                const float us = 3.5f + std::max({load + mul, wait, memory}) + 0.05f * waves +
+                                 (parts > 1 ? 2.0f + 0.2f * parts : 0.0f);
+                if (!best.fi || us < best.us) best = {fi, waves, parts, us};
+            }
         }
+    }
     return best;
 }
 
@@ -97,7 +109,7 @@ SmallCut small_cut(int I, int J, int K, size_t elem)
 // rows and 32 k, the matrix instructions with them) and the waits of the longer product's waves.
 SmallCut small_gradients_cut(int M, int N, int K)
 {
-    SmallCut best{0, 1, 0.0f};
+    SmallCut best{0, 1, 1, 0.0f};
     const int steps = std::max(ceil_div(N, 32), ceil_div(M, 32));
     for (int fi : {1, 4})
         for (int waves : {1, 2, 4, 8}) {
@@ -109,7 +121,7 @@ SmallCut small_gradients_cut(int M, int N, int K)
             const float wait = ceil_div(steps, waves * at) * (1.8f + 0.8f * fi * at);
             const float ends = (tx + tw) * waves * 2.5f / (kUnits * 32);   // workgroups' starts and epilogues
             const float us = 3.5f + std::max(work, wait) + ends;
-            if (!best.fi || us < best.us) best = {fi, waves, us};
+            if (!best.fi || us < best.us) best = {fi, waves, 1, us};
         }
     return best;
 }
@@ -281,22 +293,22 @@ __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, cons
     rows[(long long)blockIdx.y * N + col] = s;
 }
 
-// db: the sums of all row chunks, 32 columns a workgroup, eight threads down the chunks.
+// db: the sums of all row chunks, eight columns a workgroup, 32 threads down the chunks.
 template <typename T>
 __global__ __launch_bounds__(256) void k_row_sum(const float *rows, int chunks, int N, T *db)
 {
-    __shared__ float part[8][32];
-    const int lane = threadIdx.x & 31, down = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
+    __shared__ float part[32][8];
+    const int lane = threadIdx.x & 7, down = threadIdx.x >> 3;
+    const int c = blockIdx.x * 8 + lane;
     float s = 0.0f;
     if (c < N)
 #pragma unroll 4
-        for (int q = down; q < chunks; q += 8) s += rows[(long long)q * N + c];
+        for (int q = down; q < chunks; q += 32) s += rows[(long long)q * N + c];
     part[down][lane] = s;
     __syncthreads();
     if (down || c >= N) return;
 #pragma unroll
-    for (int q = 1; q < 8; ++q) s += part[q][lane];
+    for (int q = 1; q < 32; ++q) s += part[q][lane];
     narrow(s, db[c]);
 }
 
@@ -325,6 +337,7 @@ hipError_t zero(void *p, long long n, hipStream_t s)
 
 void cut_small(Args &P, int fi)
 {
+    P.parts = 1;
     P.tiles_i = ceil_div(P.I, 16 * fi);
     P.tiles_j = ceil_div(P.J + (P.ones ? 1 : 0), 16);
 }
@@ -353,6 +366,10 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
     const SmallCut sc = small_cut(P.I, P.J, P.K, sizeof(T));
     if (sc.us <= c.us) {
         cut_small(P, sc.fi);
+        P.k_part = ceil_div(ceil_div(a.K, sc.parts), 32) * 32;
+        P.parts = ceil_div(a.K, P.k_part);
+        P.part = ws.part;
+        P.ticket = ws.ticket;
         return launch_small_forward(P, sizeof(T) == 2, sc.fi, sc.waves, s);
     }
     if (direct && copy_x + copy_w) {
@@ -434,7 +451,7 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (a.db) {
-            k_row_sum<T><<<(unsigned)ceil_div(a.N, 32), 256, 0, s>>>(ws.rows, chunks, a.N, (T *)a.db);
+            k_row_sum<T><<<(unsigned)ceil_div(a.N, 8), 256, 0, s>>>(ws.rows, chunks, a.N, (T *)a.db);
             if ((e = hipGetLastError()) != hipSuccess) return e;
         }
         if (form) dz = (const T *)ws.dz, lddz = Np, alpha = 1.0f;

@@ -526,8 +526,8 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
 
 // One operand tile on its way through registers: 8-value chunks, loaded 16 bytes at a time at any
 // alignment of the element.  Where a chunk may pass the end of its row (K_ROWS:
-// the last k; K_COLS: the last row of the operand), bf16 values are loaded one at a time, as a word
-// that is half in the buffer would read as zero; of 32-bit values those past the last k are
+// the last k; K_COLS: the last row of the operand), bf16 values are loaded one at a time where the buffer ends too, as a
+// word that is half in it would read as zero; of 32-bit values those past the last k are
 // masked afterwards, and those past the last row reach only sums that are not stored.
 template <typename T, int L, int R, int BK, int THREADS>
 struct Chunks {
@@ -555,8 +555,8 @@ struct Chunks {
         for (int n = 0; n < kN; ++n) {
             const int slot = n * THREADS + threadIdx.x;
             const int r = slot / Tile::kChunks, c = (slot % Tile::kChunks) ^ Tile::key(r);
-            off[n] = (int)(r * ld) + c * 8 * kSize;
             at[n] = c * 8;
+            off[n] = L == K_ROWS || at[n] < rows ? (int)(r * ld) + c * 8 * kSize : 0x7FFFFFF0;
         }
     }
 
@@ -565,11 +565,12 @@ struct Chunks {
     {
         const int left = K - k;
         const char *p = L == K_ROWS ? base + (long long)k * kSize : base + k * ld;
-        const int bytes = L == K_ROWS ? span + left * kSize : (left < BK ? left - 1 : BK - 1) * (int)ld + span;
+        const int bytes = L == K_ROWS ? span + left * kSize : (left <= BK ? left - 1 : BK) * (int)ld + span;
         const int end = left <= 0 ? 0 : bytes;
         const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void *)p, 0, end, 0x00027000);
         const int stop = L == K_ROWS ? left : rows;   // values of the chunk's direction that exist
-        const bool tail = kSize == 2 && (L == K_ROWS ? left < BK : rows < R);
+        // a K_COLS chunk that passes its row's end reads into the next k's row, until there is none
+        const bool tail = kSize == 2 && (L == K_ROWS ? left < BK : rows < R && left <= BK);
 #pragma unroll
         for (int n = 0; n < kN; ++n) {
             if (!tail) {
@@ -883,43 +884,70 @@ struct SlopePiece {
     __device__ __forceinline__ float value(int e) const { return x[e]; }
 };
 
-// The waves' sums of a 16 FI x 16 tile, added and finished.
-template <typename T, int FI, bool kForward>
-__device__ __forceinline__ void small_finish(const Args &P, f32x4 (&acc)[FI], int i0, int j0, float *lds)
+// One value of a small product, finished.
+template <typename T, bool kForward>
+__device__ __forceinline__ void small_value(const Args &P, float sum, int i, int j)
 {
+    if (i >= P.I) return;
+    if (!kForward) {
+        if (j < P.J) narrow(sum * P.alpha, ((T *)P.c)[i * P.ldc + j]);
+        else if (j == P.J && P.ones) narrow(sum * P.alpha, ((T *)P.ones)[i]);
+        return;
+    }
+    if (j >= P.J) return;
+    float v[1] = {sum};
+    if (P.bias) v[0] += widen(((const T *)P.bias)[j]);
+    if (P.z) P.z[(long long)i * P.J + j] = v[0];
+    activate<sizeof(T) == 2>(v, P.act);
+    float y = v[0] * P.alpha;
+    if (P.residual) y += widen(((const T *)P.residual)[i * P.ldr + j]);
+    narrow(y, ((T *)P.c)[i * P.ldc + j]);
+}
+
+// The waves' sums of a 16 FI x 16 tile, added and finished; split over k, parts meet as joined()'s do.
+template <typename T, int FI, bool kForward>
+__device__ __forceinline__ void small_finish(const Args &P, f32x4 (&acc)[FI], int tile, int i0, int j0, float *lds)
+{
+    __shared__ unsigned taken;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
 #pragma unroll
     for (int f = 0; f < FI; ++f)   // [wave][row][16 columns]
         *(f32x4 *)(lds + (wave * FI * 16 + f * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) = acc[f];
     __syncthreads();
+    float *all = P.part + (long long)tile * P.parts * (FI * 256);
     for (int e = threadIdx.x; e < FI * 256; e += blockDim.x) {
-        const int i = i0 + (e >> 4), j = j0 + (e & 15);
-        if (i >= P.I) continue;
-        float v[1] = {0.0f};
-        for (int q = 0; q < waves; ++q) v[0] += lds[q * FI * 256 + e];
-        if (!kForward) {
-            if (j < P.J) narrow(v[0] * P.alpha, ((T *)P.c)[i * P.ldc + j]);
-            else if (j == P.J && P.ones) narrow(v[0] * P.alpha, ((T *)P.ones)[i]);
-            continue;
-        }
-        if (j >= P.J) continue;
-        if (P.bias) v[0] += widen(((const T *)P.bias)[j]);
-        if (P.z) P.z[(long long)i * P.J + j] = v[0];
-        activate<sizeof(T) == 2>(v, P.act);
-        float y = v[0] * P.alpha;
-        if (P.residual) y += widen(((const T *)P.residual)[i * P.ldr + j]);
-        narrow(y, ((T *)P.c)[i * P.ldc + j]);
+        float sum = 0.0f;
+        for (int q = 0; q < waves; ++q) sum += lds[q * FI * 256 + e];
+        if (P.parts == 1) small_value<T, kForward>(P, sum, i0 + (e >> 4), j0 + (e & 15));
+        else if (i0 + (e >> 4) < P.I)
+            __hip_atomic_store(all + blockIdx.y * (FI * 256) + e, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
+    if (P.parts == 1) return;
+    wait_loads<0>();   // and stores: this wave's have arrived
+    __syncthreads();   // every wave's have
+    if (threadIdx.x == 0)
+        taken = __hip_atomic_fetch_add(P.ticket + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __syncthreads();
+    if (taken != (unsigned)P.parts - 1) return;
+    for (int e = threadIdx.x; e < FI * 256; e += blockDim.x) {
+        if (i0 + (e >> 4) >= P.I) break;
+        float sum = 0.0f;
+#pragma unroll 4
+        for (int p = 0; p < P.parts; ++p)
+            sum += __hip_atomic_load(all + p * (FI * 256) + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        small_value<T, kForward>(P, sum, i0 + (e >> 4), j0 + (e & 15));
+    }
+    if (threadIdx.x == 0) __hip_atomic_store(P.ticket + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-// k of this wave: [first, last), a multiple of 32 long unless it ends with K.
-__device__ __forceinline__ void small_share(int K, int &first, int &last)
+// k of this wave in [begin, end): [first, last), a multiple of 32 long unless it ends with the range.
+__device__ __forceinline__ void small_share(int begin, int end, int &first, int &last)
 {
     const int waves = blockDim.x >> 6, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int steps = (K + 31) >> 5, q = steps / waves, r = steps % waves;
-    first = (wave * q + (wave < r ? wave : r)) * 32;
+    const int steps = (end - begin + 31) >> 5, q = steps / waves, r = steps % waves;
+    first = begin + (wave * q + (wave < r ? wave : r)) * 32;
     last = first + (q + (wave < r ? 1 : 0)) * 32;
-    if (last > K) last = K;
+    if (last > end) last = end;
 }
 
 // Forward: C = A B^T, both with k along their rows.
@@ -927,11 +955,12 @@ template <typename T, int FI>
 __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small_forward(Args P)
 {
     extern __shared__ float small_lds[];
-    constexpr int kAt = FI == 1 ? 4 : 2;
+    constexpr int kAt = FI == 4 ? 2 : 4;
     const int i0 = blockIdx.x % P.tiles_i * (16 * FI), j0 = blockIdx.x / P.tiles_i * 16;
     f32x4 acc[FI] = {};
     int first, last;
-    small_share(P.K, first, last);
+    const int begin = blockIdx.y * P.k_part;
+    small_share(begin, P.K - begin < P.k_part ? P.K : begin + P.k_part, first, last);
     for (int k0 = first; k0 < last; k0 += 32 * kAt) {
         Piece<T, K_ROWS> a[kAt][FI], b[kAt];
 #pragma unroll
@@ -942,22 +971,25 @@ __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small_forward(Args P)
             for (int f = 0; f < FI; ++f) a[n][f].load(P.a, P.lda, i0 + f * 16, P.I, k, P.K);
         }
 #pragma unroll
-        for (int n = 0; n < kAt; ++n)
+        for (int n = 0; n < kAt; ++n) {
+            if (sizeof(T) == 2) {
 #pragma unroll
-            for (int f = 0; f < FI; ++f) {
-                if (sizeof(T) == 2) {
+                for (int f = 0; f < FI; ++f) {
                     bf16x8 va, vb;
                     __builtin_memcpy(&va, a[n][f].w, 16);
                     __builtin_memcpy(&vb, b[n].w, 16);
                     acc[f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(vb, va, acc[f], 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
                 }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+#pragma unroll
+                    for (int f = 0; f < FI; ++f)
+                        acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
             }
+        }
     }
-    small_finish<T, FI, true>(P, acc, i0, j0, small_lds);
+    small_finish<T, FI, true>(P, acc, blockIdx.x, i0, j0, small_lds);
 }
 
 // One gradient product: C = dz B with B's k across its rows; dz's layout L.  A column of ones after B's
@@ -970,7 +1002,7 @@ __device__ __forceinline__ void small_gradient(const Args &P, int id, float *lds
     const bool one = P.ones && j0 + (int)(threadIdx.x & 15) == P.J;
     f32x4 acc[FI] = {};
     int first, last;
-    small_share(P.K, first, last);
+    small_share(0, P.K, first, last);
     for (int k0 = first; k0 < last; k0 += 32 * kAt) {
         SlopePiece<T, L> a[kAt][FI];
         Piece<T, K_COLS> b[kAt];
@@ -991,7 +1023,7 @@ __device__ __forceinline__ void small_gradient(const Args &P, int id, float *lds
                     acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(one ? 1.0f : b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
             }
     }
-    small_finish<T, FI, false>(P, acc, i0, j0, lds);
+    small_finish<T, FI, false>(P, acc, id, i0, j0, lds);
 }
 
 // Small gradients in one launch: dx = dz w from the first workgroups, dw = dz^T x with db as a column
@@ -1012,7 +1044,8 @@ enum Shape { TILE_64 = 0, TILE_128 = 1, TILE_256 = 2 };
 // (K_COLS, K_COLS).  direct: both bf16 operands' rows allow 16-byte access to LDS; TILE_256 needs it.
 hipError_t launch_bf16(const Args &a, int la, int lb, bool direct, Shape shape, hipStream_t s);
 hipError_t launch_fp32(const Args &a, int la, int lb, Shape shape, hipStream_t s);
-// Small products, in tiles of 16 fi x 16 (fi = 1 or 4) by `waves` waves; either gradient may have no tiles.
+// Small products, in tiles of 16 fi x 16 by `waves` waves (fi = 1 or 4; forward also 2); either gradient may have
+// no tiles.
 hipError_t launch_small_forward(const Args &a, bool is_bf16, int fi, int waves, hipStream_t s);
 hipError_t launch_small_gradients(const Args &dx, const Args &dw, bool is_bf16, int fi, int waves, hipStream_t s);
 
