@@ -48,11 +48,12 @@ __device__ __forceinline__ void narrow(double x, double &o) { o = x; }
 // round to nearest even; a NaN stays one
 __device__ __forceinline__ void narrow(float x, bf16 &o) { o.u = __builtin_bit_cast(uint16_t, (__bf16)x); }
 
-// n neighbouring values in one access.
+// n neighbouring values, 16 bytes or fewer at a time and at any alignment of the element: the hardware
+// takes them so.
 template <int n, typename T>
 __device__ __forceinline__ void get(T (&to)[n], const T *from)
 {
-    struct alignas(sizeof(T) * n) All {
+    struct __attribute__((packed)) All {
         T t[n];
     };
     const All a = *(const All *)from;
@@ -63,20 +64,13 @@ __device__ __forceinline__ void get(T (&to)[n], const T *from)
 template <int n, typename T>
 __device__ __forceinline__ void put(T *to, const T (&from)[n])
 {
-    struct alignas(sizeof(T) * n) All {
+    struct __attribute__((packed)) All {
         T t[n];
     };
     All a;
 #pragma unroll
     for (int k = 0; k < n; ++k) a.t[k] = from[k];
     *(All *)to = a;
-}
-
-// Whether n values from p on can be one access.
-template <int n, typename T>
-__device__ __forceinline__ bool fits(const T *p)
-{
-    return ((uintptr_t)p & (sizeof(T) * n - 1)) == 0;
 }
 
 template <typename R>
@@ -113,36 +107,26 @@ __device__ __forceinline__ int tensor_of(const AdamwBatch &b, unsigned wg)
     return lo;
 }
 
-// Moments in 32 bits (fp64 for fp64 parameters).  A thread takes four neighbouring elements at a
-// time, kAt of them loaded before the first is computed; where the tensor ends or its arrays do not
-// allow it, one at a time.
-template <typename P, typename G, typename R>
-__global__ __launch_bounds__(kThreadsA) void k_adamw(AdamwBatch batch, AdamwScalars sc)
+// `end` elements of a tensor by the workgroup: a thread takes kN neighbours at a time, kAt times before the
+// first is computed; the last ones of a tensor (not WHOLE) one at a time.
+template <bool WHOLE, typename P, typename G, typename R>
+__device__ __forceinline__ void run_chunk(const Coef<R> &k, P *p, const G *g, R *m, R *v, int end)
 {
-    const int ti = tensor_of(batch, blockIdx.x);
-    const AdamwTensor t = batch.t[ti];
-    const long long base = (long long)(blockIdx.x - batch.first[ti]) * kChunk;
-    const Coef<R> k(sc);
-    P *p = (P *)t.p + base;
-    const G *g = (const G *)t.g + base;
-    R *m = (R *)t.m + base, *v = (R *)t.v + base;
-    const long long left = t.n - base;
-    constexpr int kN = sizeof(R) == 8 ? 2 : 4;   // neighbours
-    constexpr int kAt = kChunk / kThreadsA / kN / (sizeof(R) == 8 ? 4 : 2);
-    if (left >= kChunk && fits<kN>(p) && fits<kN>(g) && fits<kN>(m) && fits<kN>(v)) {
+    constexpr int kN = sizeof(R) == 8 ? 2 : 4, kAt = 2;
 #pragma unroll 1
-        for (int i = threadIdx.x * kN; i < kChunk; i += kThreadsA * kN * kAt) {
-            P pe[kAt][kN];
-            G ge[kAt][kN];
-            R me[kAt][kN], ve[kAt][kN];
+    for (int i = threadIdx.x * kN; i < end; i += kThreadsA * kN * kAt) {
+        P pe[kAt][kN];
+        G ge[kAt][kN];
+        R me[kAt][kN], ve[kAt][kN];
 #pragma unroll
-            for (int a = 0; a < kAt; ++a) {
-                const int at = i + a * kThreadsA * kN;
-                get(pe[a], p + at), get(ge[a], g + at), get(me[a], m + at), get(ve[a], v + at);
-            }
+        for (int a = 0; a < kAt; ++a) {
+            const int at = i + a * kThreadsA * kN;
+            if (WHOLE || at + kN <= end) get(pe[a], p + at), get(ge[a], g + at), get(me[a], m + at), get(ve[a], v + at);
+        }
 #pragma unroll
-            for (int a = 0; a < kAt; ++a) {
-                const int at = i + a * kThreadsA * kN;
+        for (int a = 0; a < kAt; ++a) {
+            const int at = i + a * kThreadsA * kN;
+            if (WHOLE || at + kN <= end) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e) {
                     R x = widen(pe[a][e]), vn, root;
@@ -151,19 +135,32 @@ __global__ __launch_bounds__(kThreadsA) void k_adamw(AdamwBatch batch, AdamwScal
                     ve[a][e] = vn;
                 }
                 put(p + at, pe[a]), put(m + at, me[a]), put(v + at, ve[a]);
+            } else {
+                for (int j = at; j < end; ++j) {
+                    R x = widen(p[j]), mj = m[j], vn, root;
+                    element<R>(k, x, (R)widen(g[j]), mj, v[j], vn, root);
+                    narrow(x, p[j]);
+                    m[j] = mj;
+                    v[j] = vn;
+                }
             }
         }
-        return;
     }
-    const int end = left < kChunk ? (int)left : kChunk;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < end; i += kThreadsA) {
-        R x = widen(p[i]), me = m[i], vn, root;
-        element<R>(k, x, (R)widen(g[i]), me, v[i], vn, root);
-        narrow(x, p[i]);
-        m[i] = me;
-        v[i] = vn;
-    }
+}
+
+// Moments in 32 bits (fp64 for fp64 parameters).
+template <typename P, typename G, typename R>
+__global__ __launch_bounds__(kThreadsA) void k_adamw(AdamwBatch batch, AdamwScalars sc)
+{
+    const int ti = tensor_of(batch, blockIdx.x);
+    const AdamwTensor t = batch.t[ti];
+    const long long base = (long long)(blockIdx.x - batch.first[ti]) * kChunk, left = t.n - base;
+    const Coef<R> k(sc);
+    P *p = (P *)t.p + base;
+    const G *g = (const G *)t.g + base;
+    R *m = (R *)t.m + base, *v = (R *)t.v + base;
+    if (left >= kChunk) run_chunk<true>(k, p, g, m, v, kChunk);
+    else run_chunk<false>(k, p, g, m, v, (int)left);
 }
 
 using f32x2 = __attribute__((ext_vector_type(2))) float;
@@ -229,10 +226,9 @@ __global__ __launch_bounds__(kThreadsA) void k_adamw8(AdamwBatch batch, AdamwSca
     uint8_t *m = (uint8_t *)t.m + base, *v = (uint8_t *)t.v + base;
     float *ms = t.ms + base / HQML_ADAMW_BLOCK, *vs = t.vs + base / HQML_ADAMW_BLOCK;
     const long long left = t.n - base;
-    const bool wide = left >= kChunk && fits<8>(p) && fits<8>(g) && fits<8>(m) && fits<8>(v);
     const int end = left < kChunk ? (int)left : kChunk;
 #pragma unroll 1
-    for (int i0 = threadIdx.x * 8; i0 < kChunk; i0 += kPer * kAt) {
+    for (int i0 = threadIdx.x * 8; (i0 & ~511) < end; i0 += kPer * kAt) {   // whole waves: their halves reduce
         P pe[kAt][8];
         G ge[kAt][8];
         uint32_t mw[kAt][2], vw[kAt][2];
@@ -240,7 +236,7 @@ __global__ __launch_bounds__(kThreadsA) void k_adamw8(AdamwBatch batch, AdamwSca
 #pragma unroll
         for (int a = 0; a < kAt; ++a) {
             const int i = i0 + a * kPer;
-            if (wide) {
+            if (i + 8 <= end) {
                 get(pe[a], p + i), get(ge[a], g + i);
                 get(mw[a], (const uint32_t *)(m + i)), get(vw[a], (const uint32_t *)(v + i));
             } else {
@@ -279,7 +275,7 @@ __global__ __launch_bounds__(kThreadsA) void k_adamw8(AdamwBatch batch, AdamwSca
             const float nm = block_scale(half_wave_max(mb)), nv = block_scale(half_wave_max(vb));
             to_codes(mw[a], me, 1.0f / nm);
             to_codes(vw[a], ro, 1.0f / nv);
-            if (wide) {
+            if (i + 8 <= end) {
                 put(p + i, pe[a]);
                 put((uint32_t *)(m + i), mw[a]), put((uint32_t *)(v + i), vw[a]);
             } else {

@@ -174,6 +174,7 @@ int dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const v
         rc = check_args(c.device, dtype_bytes(c.dtype), args, 2, &err);
     }
     if (rc != HQML_OK) return dense_error(h, rc, err);
+    if (!dx && !dw && !db) return HQML_OK;
     DenseBackward a{M, (int)K, (int)N, dy, x, w, z, lddy, ldx, ldw, lddx, dx, dw, db, c.activation, c.alpha};
     const hipError_t e = launch_dense_backward(a, c.dtype, h->ws, h->stream);
     return e == hipSuccess ? HQML_OK : dense_error(h, HQML_ERR_HIP, hip_text("dense backward", e));

@@ -209,6 +209,37 @@ def test_residual_in_place_and_smaller_batches(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(40, 24, 36), (700, 520, 1024), (513, 333, 1025)])
+def test_each_gradient_alone(shape, dtype):
+    """Gradients asked for one by one are the ones of the joint call, to the bounds; none is a no-op."""
+    import qml_gradients_amd as hq
+    M, K, N = shape
+    for act in ("none", "gelu"):
+        d = make(M, K, N, dtype, 23)
+        want = expect(d, dtype, act, 1.25)
+        layer = hq.Dense(K, N, M, dtype=dtype, activation=act, alpha=1.25)
+        _, z = layer.forward_train(d["x"], d["w"], d["bias"], d["residual"])
+        for k, name in enumerate(("dx", "dw", "db")):
+            ask = [i == k for i in range(3)]
+            got = layer.backward(d["dy"], d["x"], d["w"], z, *ask)
+            assert [g is not None for g in got] == ask
+            check(name, got[k], want[name])
+        assert layer.backward(d["dy"], d["x"], d["w"], z, False, False, False) == (None, None, None)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(1, 4096, 300), (24, 6766, 583), (7, 9000, 33), (64, 2111, 64), (4000, 37, 9), (9000, 24, 300)])
+def test_long_and_narrow(shape, dtype):
+    """Few rows or columns against a long sum: the products that are split over k."""
+    M, K, N = shape
+    say(f"[gpu] dense long and narrow {shape} {dtype}")
+    d = make(M, K, N, dtype, 51)
+    got = run(d, dtype, "tanh", 1.0)
+    for name, want in expect(d, dtype, "tanh", 1.0).items():
+        check(name, got[name], want)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_empty_batch(act, dtype):
     import qml_gradients_amd as hq
