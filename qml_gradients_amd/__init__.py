@@ -465,6 +465,12 @@ class Dense:
             t = t.contiguous()
         return t, length
 
+    def _new(self, rows, length, like, ld):
+        """An array [rows][length]; `like`, if its rows have no gaps, is the quicker way to one."""
+        if ld == length:
+            return self.torch.empty_like(like)
+        return self.torch.empty((rows, length), dtype=self.dtype, device=self.device)
+
     def _queue(self, call, *args):
         if self._current_stream(self._index) == self.stream:
             rc = call(self.handle, *args)
@@ -480,7 +486,7 @@ class Dense:
             raise HqmlError(rc, hqml_dense_last_error(self.handle))
 
     def _forward(self, x, w, bias, residual, out, keep):
-        empty, M = self.torch.empty, x.shape[0]
+        M = x.shape[0]
         x, ldx = self._rows(x, M, self.K, "x")
         w, ldw = self._rows(w, self.N, self.K, "w")
         if bias is not None:
@@ -490,14 +496,14 @@ class Dense:
         if residual is not None:
             residual, ldr = self._rows(residual, M, self.N, "residual")
         if out is None:
-            y, ldy = empty((M, self.N), dtype=self.dtype, device=self.device), self.N
+            y, ldy = self._new(M, self.N, residual, ldr), self.N
         else:
             y, ldy = self._rows(out, M, self.N, "out")
             if y is not out:
                 raise ValueError("out must have rows without gaps between their elements")
         z = None
         if keep and not self.plain:
-            z = empty((M, self.N), dtype=self.torch.float32, device=self.device)
+            z = self.torch.empty((M, self.N), dtype=self.torch.float32, device=self.device)
         self._queue(self._lib.hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
                     y.data_ptr(), ldy, None if z is None else z.data_ptr())
@@ -514,7 +520,7 @@ class Dense:
     def backward(self, dy, x, w, z=None, input=True, weight=True, bias=True):
         """(dx, dw, db) for dy = dL/dy and the arguments and z of a forward call; those not
         asked for are None.  The residual's gradient is dy."""
-        empty, M = self.torch.empty, dy.shape[0]
+        M = dy.shape[0]
         dy, lddy = self._rows(dy, M, self.N, "dy")
         x, ldx = self._rows(x, M, self.K, "x")
         w, ldw = self._rows(w, self.N, self.K, "w")
@@ -523,9 +529,9 @@ class Dense:
                 raise ValueError("the gradient of an activation needs the forward call's z")
             self._check(z, (M, self.N), "z", self.torch.float32)
             z = z.contiguous()
-        dx = empty((M, self.K), dtype=self.dtype, device=self.device) if input else None
-        dw = empty((self.N, self.K), dtype=self.dtype, device=self.device) if weight else None
-        db = empty((self.N,), dtype=self.dtype, device=self.device) if bias else None
+        dx = self._new(M, self.K, x, ldx) if input else None
+        dw = self._new(self.N, self.K, w, ldw) if weight else None
+        db = self.torch.empty(self.N, dtype=self.dtype, device=self.device) if bias else None
         self._queue(self._lib.hqml_dense_backward, M, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if self.plain else z.data_ptr(), dx.data_ptr() if input else None, self.K,
                     dw.data_ptr() if weight else None, db.data_ptr() if bias else None)
