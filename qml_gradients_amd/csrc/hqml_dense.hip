@@ -21,8 +21,8 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---- how a product is run: the estimate that is least ----
 //
-// Times in us, fitted to a sweep of every shape over 13 products from 64 x 64 x 256 to 2048^3 and
-// 200 x 200 x 16000; the choice was within 15 % of the best one at each of them.
+// Times in us, fitted to sweeps of every cut over 26 set and 90 drawn products (rows 1 to 16384, 8 to 8192 columns,
+// k 16 to 11000) of each type; the cut chosen took 4 % more than the fastest one in the mean, a third more at worst.
 
 constexpr int kUnits = 256;    // compute units
 constexpr int kPartTiles = 1024, kMostParts = 64;
@@ -69,35 +69,39 @@ Cut best_cut(int I, int J, int K, size_t elem, bool direct)
     return direct ? best_cut(I, J, K, elem, kDirectCost, 3) : best_cut(I, J, K, elem, kStagedCost, 2);
 }
 
-// A small forward product: every tile reads its own rows, at 40 bytes a cycle and compute unit; the fp32 matrix
-// instruction takes 8 x 32 cycles for 16 x 16 x 32; a wave waits for its loads once in a few steps.
+// A small forward product: every tile reads its own rows, at `rate` bytes a us and compute unit (bf16 rows whose
+// elements straddle words: a sixth of fp32's rate); the fp32 matrix instruction takes 8 x 32 cycles and more for
+// 16 x 16 x 32; a wave waits for its loads once in a few steps.
 struct SmallCut {
     int fi, waves, parts;
     float us;
 };
 
-SmallCut small_cut(int I, int J, int K, size_t elem)
+SmallCut small_cut(int I, int J, int K, size_t elem, bool words)
 {
     SmallCut best{0, 1, 1, 0.0f};
     const int steps = ceil_div(K, 32);
     const float bytes = ((float)I * K + (float)J * K + (float)I * J) * elem;
+    const float rate = elem == 4 ? 81e3f : words ? 51e3f : 14.3e3f;
     for (int fi : {1, 2, 4}) {
         if (fi > 1 && I <= 8 * fi) break;
         const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
-        for (int waves : {1, 2, 4, 8, 16}) {
-            if (waves > 1 && (waves > steps || (waves == 16 && fi > 1))) break;
-            for (int parts : {1, 2, 3, 4, 6, 8}) {
-                if (parts > 1 && (tiles * parts > kUnits || parts * waves * 4 > steps)) break;
-                const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
-                const int own = ceil_div(steps, parts);   // of one workgroup
-                const float load = each * own * (16 * 32 * elem * (fi + 1)) / 65e3f;
-                const float mul = elem == 2 ? 0.0f : each * own * fi * 0.04f;
-                const float wait = ceil_div(own, waves * (fi == 4 ? 2 : 4)) * 1.2f * std::max(1.0f, each * waves / 16);
+        const int rows = std::min(16 * fi, I) + std::min(16, J), at = fi == 4 ? 2 : 4;   // steps a wave loads together
+        for (int parts : {1, 2, 3, 4, 6, 8}) {
+            const int own = ceil_div(steps, parts);   // of one workgroup
+            if (parts > 1 && (tiles * parts > kUnits || own < 4)) break;
+            const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
+            for (int waves : {1, 2, 4, 8, 16}) {
+                if (waves > 1 && (waves > own || (waves == 16 && fi > 1))) break;
+                const float load = each * own * (32 * elem * rows) / rate;
+                const float mul = elem == 2 ? 0.0f : each * own * fi * 0.037f, work = load + mul;
+                const float wait = ceil_div(own, waves * at) * (elem == 4 ? 0.3f + 0.63f * fi : 0.14f + 0.45f * fi) *
+                                   std::max(1.0f, each * waves / 16);
                 // memory's rate needs about 40 KB under way on a compute unit
-                const float under_way = each * waves * (fi == 4 ? 2 : 4) * 16 * 32 * elem;
+                const float under_way = each * waves * at * (16 * 16 * elem * (fi + 1));
                 const float memory = bytes / (4.6e6f * std::min(1.0f, under_way / 40e3f));
-                const float us = 3.5f + std::max({load + mul, wait, memory}) + 0.05f * waves +
-                                 (parts > 1 ? 2.0f + 0.2f * parts : 0.0f);
+                const float us = 2.9f + std::max(std::max(work, wait) + 0.3f * std::min(work, wait), memory) +
+                                 each * (0.35f + 0.065f * waves) + (parts > 1 ? 1.65f + 0.07f * parts : 0.0f);
                 if (!best.fi || us < best.us) best = {fi, waves, parts, us};
             }
         }
@@ -149,6 +153,12 @@ bool aligned(const void *p, long long ld, size_t elem)
 bool straight(const void *p, long long ld, int layout, int K)
 {
     return aligned(p, ld, 2) && (layout == K_COLS || K % 8 == 0);
+}
+
+// Whether the rows of a bf16 operand begin on whole words.
+bool whole_words(const void *p, long long ld)
+{
+    return (uintptr_t)p % 4 == 0 && ld % 2 == 0;
 }
 
 // Runs one product on tiles; P holds everything but its cut.
@@ -363,7 +373,7 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
         direct = !(copy_x + copy_w) || (ws.pad && d.us + pad_us(copy_x + copy_w, a.K) < c.us);
         if (direct) c = d, c.us += pad_us(copy_x + copy_w, a.K);
     }
-    const SmallCut sc = small_cut(P.I, P.J, P.K, sizeof(T));
+    const SmallCut sc = small_cut(P.I, P.J, P.K, sizeof(T), whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw));
     if (sc.us <= c.us) {
         cut_small(P, sc.fi);
         P.k_part = ceil_div(ceil_div(a.K, sc.parts), 32) * 32;
