@@ -21,43 +21,55 @@ int ceil_div(int a, int b) { return (a + b - 1) / b; }
 
 // ---- how a product is run: the estimate that is least ----
 //
-// Times in us, fitted to sweeps of every cut over 26 set and 90 drawn products (rows 1 to 16384, 8 to 8192 columns,
-// k 16 to 11000) of each type; the cut chosen took 4 % more than the fastest one in the mean, a third more at worst.
+// Times in us, fitted to sweeps of every cut over 71 products of 64 to 16384 rows, 7 to 8192 columns and k 7 to 16384 and
+// 90 smaller ones, of each type and layout: the cut chosen took 2 to 5 % more than the fastest in the mean, 40 % at worst.
 
 constexpr int kUnits = 256;    // compute units
-constexpr int kPartTiles = 1024, kMostParts = 64;
+constexpr int kPartTiles = 4096, kMostParts = 64;
 constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, kMostParts};
 
 // A tile kernel: a workgroup spends `step` on 32 k when alone on its compute unit, n of them n * share; fixed:
-// launch, first loads, epilogue; work split over k costs join + parts * join_part.
+// launch, first loads, epilogue; work split over k costs join + parts * join_part and the way of its sums to memory and
+// back (9 TB/s: most stay in the caches).  Memory gives `rate` bytes a us where a compute unit's workgroups, up to
+// `most` together, have `enough` bytes under way; the result's bytes count `out` times as much again.
 struct TileCost {
-    int side;
+    int side, most;
     float fixed, step, share, join, join_part;
 };
-constexpr TileCost kFp32Cost[] = {{64, 4.0f, 0.70f, 0.55f, 1.5f, 0.4f}, {128, 5.0f, 1.20f, 1.42f, 4.0f, 1.0f}};
-constexpr TileCost kStagedCost[] = {{64, 4.0f, 0.30f, 0.21f, 2.0f, 0.4f}, {128, 4.0f, 0.45f, 0.50f, 4.0f, 1.0f}};
-constexpr TileCost kDirectCost[] = {{64, 3.0f, 0.12f, 0.135f, 2.0f, 0.4f},
-                                    {128, 4.0f, 0.22f, 0.32f, 4.0f, 1.0f},
-                                    {256, 7.0f, 0.57f, 0.82f, 7.0f, 2.0f}};
+struct MemoryCost {
+    float rate, enough, out;
+};
+constexpr TileCost kFp32Cost[] = {{64, 4, 4.6f, 0.65f, 0.45f, 0.3f, 0.23f}, {128, 2, 5.0f, 1.18f, 1.25f, 0.1f, 1.0f}};
+constexpr TileCost kStagedCost[] = {{64, 4, 4.5f, 0.27f, 0.184f, 0.6f, 0.4f}, {128, 2, 4.5f, 0.435f, 0.35f, 0.8f, 1.0f}};
+constexpr TileCost kDirectCost[] = {{64, 4, 2.6f, 0.18f, 0.137f, 0.65f, 0.42f},
+                                    {128, 2, 4.6f, 0.2f, 0.24f, 2.0f, 1.06f},
+                                    {256, 1, 8.6f, 0.45f, 0.525f, 4.6f, 4.0f}};
+constexpr MemoryCost kFp32Memory{4.2e6f, 1e3f, 0.0f}, kStagedMemory{5e6f, 29e3f, 2.0f}, kDirectMemory{5e6f, 18e3f, 1.0f};
 
 struct Cut {
     int side, parts;
     float us;
 };
 
-Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n)
+Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n, const MemoryCost &m)
 {
     const int steps = ceil_div(K, 32);
-    const float memory = ((float)I * K + (float)J * K + (float)I * J) * elem / 4.6e6f;
+    const float out = (float)I * J * elem, bytes = ((float)I * K + (float)J * K) * elem + out;
     Cut best{0, 1, 0.0f};
     for (int c = 0; c < n; ++c) {
-        const long long tiles = (long long)ceil_div(I, cost[c].side) * ceil_div(J, cost[c].side);
+        const int side = cost[c].side;
+        const long long tiles = (long long)ceil_div(I, side) * ceil_div(J, side);
+        const float step_bytes = 32.0f * elem * (std::min(side, I) + std::min(side, J));
         for (int parts : kParts) {
-            if (parts > 1 && (tiles * parts > kPartTiles * 64 * 64 / (cost[c].side * cost[c].side) || parts * 2 > steps)) break;
-            const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
+            const long long groups = tiles * parts;
+            if (parts > 1 && (groups > kPartTiles * 64 * 64 / (side * side) || parts * 2 > steps)) break;
+            const float each = (float)((groups + kUnits - 1) / kUnits);
+            // three steps of a workgroup are under way
+            const float under_way = std::min((float)groups / kUnits, (float)cost[c].most) * 3 * step_bytes;
+            const float memory = bytes / (m.rate * std::min(1.0f, under_way / m.enough)) + out * m.out / m.rate;
             float us = cost[c].fixed + std::max(memory, ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share));
-            if (parts > 1) us += cost[c].join + parts * cost[c].join_part;
-            if (!best.side || us < best.us) best = {cost[c].side, parts, us};
+            if (parts > 1) us += cost[c].join + parts * cost[c].join_part + (float)groups * (side * side * 8) / 9e6f;
+            if (!best.side || us < best.us) best = {side, parts, us};
         }
     }
     return best;
@@ -65,8 +77,9 @@ Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n)
 
 Cut best_cut(int I, int J, int K, size_t elem, bool direct)
 {
-    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 2);
-    return direct ? best_cut(I, J, K, elem, kDirectCost, 3) : best_cut(I, J, K, elem, kStagedCost, 2);
+    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 2, kFp32Memory);
+    return direct ? best_cut(I, J, K, elem, kDirectCost, 3, kDirectMemory)
+                  : best_cut(I, J, K, elem, kStagedCost, 2, kStagedMemory);
 }
 
 // A small forward product: every tile reads its own rows, at `rate` bytes a us and compute unit (bf16 rows whose
@@ -141,7 +154,7 @@ size_t part_tiles(size_t I, size_t J, size_t K)
 {
     if (K <= 96) return 0;   // three steps: never split
     const size_t tiles = ((I + 255) / 256) * ((J + 255) / 256) * 16;   // whole tiles of any shape
-    return std::min<size_t>(kPartTiles, tiles * kMostParts);
+    return std::min<size_t>(kPartTiles, tiles * std::min<size_t>(kMostParts, (K + 31) / 64));
 }
 
 bool aligned(const void *p, long long ld, size_t elem)
