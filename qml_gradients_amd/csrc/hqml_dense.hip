@@ -122,24 +122,28 @@ SmallCut small_cut(int I, int J, int K, size_t elem, bool words)
     return best;
 }
 
-// Small gradients in one launch.  What counts is forming dz anew in every tile (1,500 cycles of a SIMD for 16
-// rows and 32 k, the matrix instructions with them) and the waits of the longer product's waves.
-SmallCut small_gradients_cut(int M, int N, int K)
+// Small gradients in one launch.  What counts is forming dz anew in every tile (1,300 to 1,770 cycles of a SIMD for
+// 16 rows and 32 k, the matrix instructions with them) and the waits
+// of the longer product's waves.  Over 70 products of each type the choice took 2 % more than the best in the mean.
+SmallCut small_gradients_cut(int M, int N, int K, size_t elem, bool words)
 {
     SmallCut best{0, 1, 1, 0.0f};
-    const int steps = std::max(ceil_div(N, 32), ceil_div(M, 32));
-    for (int fi : {1, 4})
+    const int steps_x = ceil_div(N, 32), steps_w = ceil_div(M, 32), steps = std::max(steps_x, steps_w);
+    for (int fi : {1, 4}) {
+        const float block_us = ((elem == 4 ? 1420.0f : words ? 1300.0f : 1570.0f) + (fi == 4 ? 200.0f : 0.0f)) / 2.15e6f;
         for (int waves : {1, 2, 4, 8}) {
             if (waves > 1 && waves > steps) break;
             const long long tx = (long long)ceil_div(M, 16 * fi) * ceil_div(K, 16);
             const long long tw = (long long)ceil_div(N, 16 * fi) * ceil_div(K + 1, 16);
-            const float work = (tx * ceil_div(N, 32) + tw * ceil_div(M, 32)) * (fi * 1500.0f + 400.0f) / 2.15e6f;
+            const float work = ((float)tx * steps_x * std::min(M, 16 * fi) + (float)tw * steps_w * std::min(N, 16 * fi)) /
+                               16 * block_us;
             const int at = fi == 1 ? 2 : 1;   // steps a wave loads together
-            const float wait = ceil_div(steps, waves * at) * (1.8f + 0.8f * fi * at);
-            const float ends = (tx + tw) * waves * 2.5f / (kUnits * 32);   // workgroups' starts and epilogues
-            const float us = 3.5f + std::max(work, wait) + ends;
+            const float wait = ceil_div(steps, waves * at) * (fi == 1 ? 1.55f : 2.9f);
+            const float ends = (tx + tw) * waves * 4.4f / (kUnits * 32);   // workgroups' starts and epilogues
+            const float us = 3.6f + std::max(work, wait) + 0.37f * std::min(work, wait) + ends;
             if (!best.fi || us < best.us) best = {fi, waves, 1, us};
         }
+    }
     return best;
 }
 
@@ -452,7 +456,8 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
             form = form || !dy_straight;   // dz in rows of a multiple of eight
         }
     }
-    const SmallCut c = small_gradients_cut(a.M, a.N, a.K);
+    const bool words = whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw) && whole_words(a.dy, a.lddy);
+    const SmallCut c = small_gradients_cut(a.M, a.N, a.K, sizeof(T), words);
     if (c.us <= slope_us(a.M, a.N, sizeof(T)) + cx.us + cw.us) return gradients<T>(a, c, s);
     const T *dz = (const T *)a.dy;
     long long lddz = a.lddy;
