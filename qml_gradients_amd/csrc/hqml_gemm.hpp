@@ -75,6 +75,13 @@ __device__ __forceinline__ void wait_loads()
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// This wave's LDS reads and writes are done.
+__device__ __forceinline__ void wait_lds()
+{
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+}
+
 __device__ __forceinline__ void barrier()
 {
     asm volatile("" ::: "memory");
@@ -745,13 +752,14 @@ struct Staged {
             }
         }
         if (BUF == 1) {
+            wait_lds();   // the fragments have arrived: the matrix instructions that take them may come after the barrier
             barrier();
             ta.store(here);
             tb.store(here + A::kBytes);
             ta.load((t + 2) * BK);
             tb.load((t + 2) * BK);
         }
-        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the stores are done
+        wait_lds();
         barrier();
     }
 
@@ -779,7 +787,7 @@ struct Staged {
         tb.store(lds + A::kBytes);
         ta.load(BK);
         tb.load(BK);
-        __builtin_amdgcn_s_waitcnt(0xC07F);
+        wait_lds();
         barrier();
         const int steps = (kn + BK - 1) / BK;
         for (int t = 0; t < steps; ++t) step(t & 1 ? other : lds, t & 1 ? lds : other, t);

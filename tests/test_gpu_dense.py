@@ -239,6 +239,23 @@ def test_long_and_narrow(shape, dtype):
         check(name, got[name], want)
 
 
+# More than 512 tiles of 128 x 128 in every product: two workgroups share a compute unit, and in fp32 one LDS buffer
+# a workgroup is read and refilled in turn.
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_products_of_many_tiles(dtype):
+    import qml_gradients_amd as hq
+    M, K, N = 2990, 2950, 3001
+    say(f"[gpu] dense {M} x {K} -> {N} {dtype}")
+    d = make(M, K, N, dtype, 77)
+    layer = hq.Dense(K, N, M, dtype=dtype, activation="silu")
+    got = run(d, dtype, "silu", 1.0, layer)
+    for _ in range(5):
+        again = run(d, dtype, "silu", 1.0, layer)
+        assert all(torch.equal(got[k], again[k]) for k in got)
+    for name, want in expect(d, dtype, "silu", 1.0).items():
+        check(name, got[name], want)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_empty_batch(act, dtype):
