@@ -178,6 +178,14 @@ bool whole_words(const void *p, long long ld)
     return (uintptr_t)p % 4 == 0 && ld % 2 == 0;
 }
 
+// Whether a product's partial sums and tickets fit the workspace.
+bool fits(const Args &P, int tile_values, const DenseWorkspace &ws)
+{
+    const size_t tiles = (size_t)P.tiles_i * P.tiles_j;
+    return P.parts == 1 ||
+           (tiles * P.parts * tile_values * 4 <= ws.part_bytes && tiles * sizeof(unsigned) <= ws.ticket_bytes);
+}
+
 // Runs one product on tiles; P holds everything but its cut.
 template <typename T>
 hipError_t run_product(Args P, int la, int lb, const Cut &c, bool direct, const DenseWorkspace &ws, hipStream_t s)
@@ -188,6 +196,7 @@ hipError_t run_product(Args P, int la, int lb, const Cut &c, bool direct, const 
     P.parts = ceil_div(P.K, P.k_part);
     P.part = ws.part;
     P.ticket = ws.ticket;
+    if (!fits(P, c.side * c.side, ws)) return hipErrorInvalidValue;
     const Shape shape = c.side == 64 ? TILE_64 : c.side == 128 ? TILE_128 : TILE_256;
     return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, shape, s) : launch_fp32(P, la, lb, shape, s);
 }
@@ -397,6 +406,7 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
         P.parts = ceil_div(a.K, P.k_part);
         P.part = ws.part;
         P.ticket = ws.ticket;
+        if (!fits(P, sc.fi * 16 * 16, ws)) return hipErrorInvalidValue;
         return launch_small_forward(P, sizeof(T) == 2, sc.fi, sc.waves, s);
     }
     if (direct && copy_x + copy_w) {
@@ -524,8 +534,9 @@ DenseWorkspace dense_workspace(const hqml_dense_config &cfg)
     ws.rows_bytes = std::max((M + chunk - 1) / chunk, (std::min(M, (size_t)kFewRows) + 15) / 16) * N * 4;
     const size_t K = (size_t)cfg.in_features;
     const size_t tiles = std::max({part_tiles(M, N, K), part_tiles(M, K, N), part_tiles(N, K, M)});
-    ws.part_bytes = tiles * 64 * 64 * 4;
-    ws.ticket_bytes = tiles * sizeof(unsigned);
+    // small products split over k: up to one workgroup a compute unit, of tiles of up to 64 x 16
+    ws.part_bytes = tiles ? std::max(tiles * 64 * 64, (size_t)kUnits * 64 * 16) * 4 : 0;
+    ws.ticket_bytes = tiles ? std::max(tiles, (size_t)kUnits) * sizeof(unsigned) : 0;
     return ws;
 }
 

@@ -256,6 +256,23 @@ def test_products_of_many_tiles(dtype):
         check(name, got[name], want)
 
 
+# Forward products split over k whose tiles outnumber 64 x 64 ones, with the copies of odd rows beside their counters.
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(128, 256, 249), (100, 1001, 130), (64, 2047, 64), (16, 5001, 60), (240, 301, 250)])
+def test_small_products_split_over_k(shape, dtype):
+    import qml_gradients_amd as hq
+    M, K, N = shape
+    say(f"[gpu] dense {M} x {K} -> {N} {dtype}")
+    d = make(M, K, N, dtype, 78)
+    layer = hq.Dense(K, N, M, dtype=dtype, activation="tanh")
+    got = run(d, dtype, "tanh", 1.0, layer)
+    for _ in range(3):
+        again = run(d, dtype, "tanh", 1.0, layer)
+        assert all(torch.equal(got[k], again[k]) for k in got)
+    for name, want in expect(d, dtype, "tanh", 1.0).items():
+        check(name, got[name], want)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_empty_batch(act, dtype):
