@@ -33,21 +33,25 @@ constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, kMostParts};
 // back (9 TB/s: most stay in the caches).  Memory gives `rate` bytes a us where a compute unit's workgroups, up to
 // `most` together, have `enough` bytes under way; the result's bytes count `out` times as much again.
 struct TileCost {
-    int side, most;
+    Shape shape;
+    int most;
     float fixed, step, share, join, join_part;
 };
 struct MemoryCost {
     float rate, enough, out;
 };
-constexpr TileCost kFp32Cost[] = {{64, 4, 4.6f, 0.65f, 0.45f, 0.3f, 0.23f}, {128, 2, 5.0f, 1.18f, 1.25f, 0.1f, 1.0f}};
-constexpr TileCost kStagedCost[] = {{64, 4, 4.5f, 0.27f, 0.184f, 0.6f, 0.4f}, {128, 2, 4.5f, 0.435f, 0.35f, 0.8f, 1.0f}};
-constexpr TileCost kDirectCost[] = {{64, 4, 2.6f, 0.18f, 0.137f, 0.65f, 0.42f},
-                                    {128, 2, 4.6f, 0.2f, 0.24f, 2.0f, 1.06f},
-                                    {256, 1, 8.6f, 0.45f, 0.525f, 4.6f, 4.0f}};
-constexpr MemoryCost kFp32Memory{4.2e6f, 1e3f, 0.0f}, kStagedMemory{5e6f, 29e3f, 2.0f}, kDirectMemory{5e6f, 18e3f, 1.0f};
+constexpr TileCost kFp32Cost[] = {{TILE_64, 4, 4.6f, 0.65f, 0.45f, 0.3f, 0.23f}, {TILE_128, 2, 5.0f, 1.18f, 1.25f, 0.1f, 1.0f},
+                                  {TILE_64x32, 6, 4.6f, 0.75f, 0.23f, 0.3f, 0.2f},
+                                  {TILE_32x64, 6, 4.6f, 0.75f, 0.23f, 0.3f, 0.2f}};
+constexpr TileCost kStagedCost[] = {{TILE_64, 4, 4.5f, 0.27f, 0.184f, 0.6f, 0.4f}, {TILE_128, 2, 4.5f, 0.435f, 0.35f, 0.8f, 1.0f}};
+constexpr TileCost kDirectCost[] = {{TILE_64, 4, 2.6f, 0.18f, 0.137f, 0.65f, 0.42f},
+                                    {TILE_128, 2, 4.6f, 0.2f, 0.24f, 2.0f, 1.06f},
+                                    {TILE_256, 1, 8.6f, 0.45f, 0.525f, 4.6f, 4.0f}};
+constexpr MemoryCost kFp32Memory{4.6e6f, 90e3f, 0.0f}, kStagedMemory{5e6f, 29e3f, 2.0f}, kDirectMemory{5e6f, 18e3f, 1.0f};
 
 struct Cut {
-    int side, parts;
+    Shape shape;
+    int parts;
     float us;
 };
 
@@ -55,21 +59,24 @@ Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n, cons
 {
     const int steps = ceil_div(K, 32);
     const float out = (float)I * J * elem, bytes = ((float)I * K + (float)J * K) * elem + out;
-    Cut best{0, 1, 0.0f};
+    Cut best{TILE_64, 0, 0.0f};
     for (int c = 0; c < n; ++c) {
-        const int side = cost[c].side;
-        const long long tiles = (long long)ceil_div(I, side) * ceil_div(J, side);
-        const float step_bytes = 32.0f * elem * (std::min(side, I) + std::min(side, J));
+        const int *side = kSides[cost[c].shape];
+        // narrow tiles are for operands that a wider one would not fill
+        if ((side[0] < side[1] && I > side[0]) || (side[1] < side[0] && J > side[1])) continue;
+        const long long tiles = (long long)ceil_div(I, side[0]) * ceil_div(J, side[1]);
+        const float step_bytes = 32.0f * elem * (std::min(side[0], I) + std::min(side[1], J));
         for (int parts : kParts) {
             const long long groups = tiles * parts;
-            if (parts > 1 && (groups > kPartTiles * 64 * 64 / (side * side) || parts * 2 > steps)) break;
+            if (parts > 1 && (groups > kPartTiles * 64 * 64 / (side[0] * side[1]) || parts * 2 > steps)) break;
             const float each = (float)((groups + kUnits - 1) / kUnits);
             // three steps of a workgroup are under way
             const float under_way = std::min((float)groups / kUnits, (float)cost[c].most) * 3 * step_bytes;
             const float memory = bytes / (m.rate * std::min(1.0f, under_way / m.enough)) + out * m.out / m.rate;
-            float us = cost[c].fixed + std::max(memory, ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share));
-            if (parts > 1) us += cost[c].join + parts * cost[c].join_part + (float)groups * (side * side * 8) / 9e6f;
-            if (!best.side || us < best.us) best = {side, parts, us};
+            float us = cost[c].fixed + std::max(memory, ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share)) +
+                       0.1f * each;   // starts and ends
+            if (parts > 1) us += cost[c].join + parts * cost[c].join_part + (float)groups * (side[0] * side[1] * 8) / 9e6f;
+            if (!best.parts || us < best.us) best = {cost[c].shape, parts, us};
         }
     }
     return best;
@@ -77,7 +84,7 @@ Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n, cons
 
 Cut best_cut(int I, int J, int K, size_t elem, bool direct)
 {
-    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 2, kFp32Memory);
+    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 4, kFp32Memory);
     return direct ? best_cut(I, J, K, elem, kDirectCost, 3, kDirectMemory)
                   : best_cut(I, J, K, elem, kStagedCost, 2, kStagedMemory);
 }
@@ -190,15 +197,14 @@ bool fits(const Args &P, int tile_values, const DenseWorkspace &ws)
 template <typename T>
 hipError_t run_product(Args P, int la, int lb, const Cut &c, bool direct, const DenseWorkspace &ws, hipStream_t s)
 {
-    P.tiles_i = ceil_div(P.I, c.side);
-    P.tiles_j = ceil_div(P.J, c.side);
+    P.tiles_i = ceil_div(P.I, kSides[c.shape][0]);
+    P.tiles_j = ceil_div(P.J, kSides[c.shape][1]);
     P.k_part = ceil_div(ceil_div(P.K, c.parts), 32) * 32;
     P.parts = ceil_div(P.K, P.k_part);
     P.part = ws.part;
     P.ticket = ws.ticket;
-    if (!fits(P, c.side * c.side, ws)) return hipErrorInvalidValue;
-    const Shape shape = c.side == 64 ? TILE_64 : c.side == 128 ? TILE_128 : TILE_256;
-    return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, shape, s) : launch_fp32(P, la, lb, shape, s);
+    if (!fits(P, kSides[c.shape][0] * kSides[c.shape][1], ws)) return hipErrorInvalidValue;
+    return sizeof(T) == 2 ? launch_bf16(P, la, lb, direct, c.shape, s) : launch_fp32(P, la, lb, c.shape, s);
 }
 
 // ---- bf16 rows that cannot be loaded straight into LDS ----

@@ -201,7 +201,8 @@ struct DirectTile {
 // and read as device-scope atomics, past the caches that the XCDs do not share, and have
 // arrived when the ticket is taken: a fence would write back a whole L2 for each of them (serve
 // 4096 -> 4096: 32 us with fences).
-template <int FI, int FJ, int THREADS>
+// MORE: twice the parts' loads under way, for kernels whose LDS leaves room in the registers.
+template <int FI, int FJ, int THREADS, bool MORE = false>
 __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int tile, int part, int i0)
 {
     __shared__ unsigned taken;
@@ -227,7 +228,7 @@ __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int 
         taken = __hip_atomic_fetch_add(P.ticket + tile, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (taken != (unsigned)P.parts - 1) return false;
-    constexpr int kAtOnce = kWords <= 8 ? 4 : kWords <= 16 ? 2 : 1;   // parts whose loads are under way together
+    constexpr int kAtOnce = kWords <= 8 ? (MORE ? 8 : 4) : kWords <= 16 ? 2 : 1;   // parts whose loads are under way together
 #pragma unroll
     for (int f = 0; f < FI; ++f)
 #pragma unroll
@@ -791,7 +792,7 @@ struct Staged {
         barrier();
         const int steps = (kn + BK - 1) / BK;
         for (int t = 0; t < steps; ++t) step(t & 1 ? other : lds, t & 1 ? lds : other, t);
-        if (P.parts > 1 && !joined<FI, FJ, kThreads>(P, acc, ti * P.tiles_j + tj, part, ti * BM + wi * TI)) return;
+        if (P.parts > 1 && !joined<FI, FJ, kThreads, (PA > 1 || PB > 1)>(P, acc, ti * P.tiles_j + tj, part, ti * BM + wi * TI)) return;
         finish<TC, FI, FJ, kTurn, kForward, (PA > 1 || PB > 1)>(P, acc, ti * BM + wi * TI, tj * BN + wj * TJ,
                                                                 lds + wave * kTurnBytes,
                                                                 [&](int i, int j) { return plain_sum<A, B>(P, i, j); });
@@ -1047,7 +1048,8 @@ __global__ __launch_bounds__(512) void k_small_gradients(Args dx, Args dw)
 }
 
 // Tile shapes a product can be run with.
-enum Shape { TILE_64 = 0, TILE_128 = 1, TILE_256 = 2 };
+enum Shape { TILE_64, TILE_128, TILE_256, TILE_64x32, TILE_32x64 };
+constexpr int kSides[][2] = {{64, 64}, {128, 128}, {256, 256}, {64, 32}, {32, 64}};   // rows, columns
 
 // The kernels of one operand type, for a layout pair (K_ROWS, K_ROWS), (K_ROWS, K_COLS) or
 // (K_COLS, K_COLS).  direct: both bf16 operands' rows allow 16-byte access to LDS; TILE_256 needs it.

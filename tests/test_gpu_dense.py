@@ -273,6 +273,18 @@ def test_small_products_split_over_k(shape, dtype):
         check(name, got[name], want)
 
 
+# At most 32 rows or columns against thousands, in each of the three products.
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("shape", [(4877, 1401, 30), (31, 2500, 3001), (9000, 29, 3001), (2500, 3000, 32), (32, 3000, 2500)])
+def test_narrow_products(shape, dtype):
+    M, K, N = shape
+    say(f"[gpu] dense {M} x {K} -> {N} {dtype}")
+    d = make(M, K, N, dtype, 79)
+    got = run(d, dtype, "gelu", -0.75)
+    for name, want in expect(d, dtype, "gelu", -0.75).items():
+        check(name, got[name], want)
+
+
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_empty_batch(act, dtype):
