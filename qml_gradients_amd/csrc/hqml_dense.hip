@@ -266,7 +266,8 @@ constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; 
 
 // dz = alpha act'(z) dy (written, if dz is not null, in rows of lddz: N, or the next multiple of eight) and its sums over `chunk` rows.  Bound by memory
 // (8192 x 4096 bf16: 268 MB in 55 us, 4.9 TB/s); 16 bytes at any alignment, single values where a row ends.  The sums
-// leave as one row a chunk, so that no atomic's order changes them.
+// take dz before it is rounded to its type (bf16: the matrix cores take it so) and leave as one row a chunk, so that no
+// atomic's order changes them.
 template <typename T>
 __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, int lddz, float *rows,
                                                int M, int N, int chunk, int act, float alpha)

@@ -820,7 +820,7 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
 // before the first is used; the waves' sums meet in LDS and are added in their order.
 // fp32, and dz formed in fp32, use the fp32 matrix instruction: nothing is rounded or split.
 // Bound by the waits for memory: fp32 1 x 64 -> 4 takes 3.5 us, 1000 x 784 -> 20 6.2, bf16 1 x 4096 -> 4096 8.4
-// (32 MB of weights from HBM, 4.0 TB/s); all gradients of 64 x 12 -> 64 7.4.
+// (32 MB of weights from HBM, 4.0 TB/s); all gradients of 64 x 12 -> 64 6.3.
 
 // Eight k of one row: k0 + 8 (lane / 16) + 0..7 of row0 + lane % 16.
 template <typename T, int L>
