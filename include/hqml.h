@@ -257,7 +257,8 @@ int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const
  * dz = alpha act'(z) dy, dx = dz w [M][K] (row stride lddx), dw = dz^T x [N][K],
  * db = sum over rows of dz [N]; the residual's gradient is dy itself.  dw and db have no
  * gaps.  Each of dx, dw, db may be NULL (not formed).  z is the forward call's (ignored with
- * HQML_ACT_NONE).  M == 0 writes zeros to dw and db. */
+ * HQML_ACT_NONE).  M == 0 writes zeros to dw and db.  Sums are held in fp32; with
+ * HQML_DTYPE_BF16 the results are rounded once, and before them dz, except in small products. */
 int hqml_dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx,
                         const void *w, long long ldw, const float *z, void *dx, long long lddx, void *dw,
                         void *db);

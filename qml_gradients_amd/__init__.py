@@ -501,6 +501,8 @@ class Dense:
             y, ldy = self._rows(out, M, self.N, "out")
             if y is not out:
                 raise ValueError("out must have rows without gaps between their elements")
+            if M and y.data_ptr() in (x.data_ptr(), w.data_ptr()):
+                raise ValueError("out must not overlap x or w")
         z = None
         if keep and not self.plain:
             z = self.torch.empty((M, self.N), dtype=self.torch.float32, device=self.device)
@@ -510,7 +512,7 @@ class Dense:
         return y, z
 
     def forward(self, x, w, bias=None, residual=None, out=None):
-        """y.  `out` may be the residual itself."""
+        """y.  `out` may be the residual itself; it must not overlap another argument."""
         return self._forward(x, w, bias, residual, out, False)[0]
 
     def forward_train(self, x, w, bias=None, residual=None, out=None):

@@ -468,6 +468,20 @@ def test_refusals():
     assert e.value.status == hq.HQML_ERR_OOM
 
 
+def test_out_must_not_be_an_operand():
+    import qml_gradients_amd as hq
+    layer = hq.Dense(16, 16, 16)
+    x, w = torch.randn(16, 16, device="cuda"), torch.randn(16, 16, device="cuda")
+    with pytest.raises(ValueError):
+        layer.forward(x, w, out=x)
+    with pytest.raises(ValueError):
+        layer.forward(x, w, out=w)
+    y = layer.forward(x, w)
+    both = torch.cat((x, torch.zeros_like(x)), 1)   # neighbouring columns do not overlap
+    assert torch.equal(layer.forward(both[:, :16], w, out=both[:, 16:]), y)
+    assert torch.equal(both[:, :16], x)
+
+
 def test_layer_gradients_reach_every_argument():
     from qml_gradients_amd.torch_layer import DenseLayer
     torch.manual_seed(4)
