@@ -130,8 +130,8 @@ SmallCut small_cut(int I, int J, int K, size_t elem, bool words)
 }
 
 // Small gradients in one launch.  What counts is forming dz anew in every tile (1,300 to 1,770 cycles of a SIMD for
-// 16 rows and 32 k, the matrix instructions with them) and the waits
-// of the longer product's waves.  Over 70 products of each type the choice took 2 % more than the best in the mean.
+// 16 rows and 32 k, the matrix instructions with them) and the waits of the longer product's waves.  Over 70 products
+// of each type the choice took 1 to 3 % more than the best in the mean.
 SmallCut small_gradients_cut(int M, int N, int K, size_t elem, bool words)
 {
     SmallCut best{0, 1, 1, 0.0f};
@@ -264,10 +264,10 @@ float pad_us(int rows, int K)
 
 constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; eight threads go down the rows
 
-// dz = alpha act'(z) dy (written, if dz is not null, in rows of lddz: N, or the next multiple of eight) and its sums over `chunk` rows.  Bound by memory
-// (8192 x 4096 bf16: 268 MB in 55 us, 4.9 TB/s); 16 bytes at any alignment, single values where a row ends.  The sums
-// take dz before it is rounded to its type (bf16: the matrix cores take it so) and leave as one row a chunk, so that no
-// atomic's order changes them.
+// dz = alpha act'(z) dy (written, if dz is not null, in rows of lddz: N, or the next multiple of eight) and its sums
+// over `chunk` rows.  Bound by memory (8192 x 4096 bf16: 268 MB in 55 us, 4.9 TB/s); 16 bytes at any alignment, single
+// values where a row ends.  The sums take dz before it is rounded to its type (bf16: the matrix cores take it so) and
+// leave as one row a chunk, so that no atomic's order changes them.
 template <typename T>
 __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, int lddz, float *rows,
                                                int M, int N, int chunk, int act, float alpha)
