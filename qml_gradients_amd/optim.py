@@ -15,6 +15,8 @@ from . import (HQML_ADAMW_BLOCK, HQML_DTYPE_BF16, HQML_DTYPE_FP32, HQML_DTYPE_FP
                hqml_adamw_config, hqml_adamw_step)
 
 _DTYPES = {torch.float32: HQML_DTYPE_FP32, torch.bfloat16: HQML_DTYPE_BF16, torch.float64: HQML_DTYPE_FP64}
+_WIDE = {torch.float32: torch.float32, torch.bfloat16: torch.float32, torch.float64: torch.float64}
+_CODES = torch.float8_e4m3fn
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -58,6 +60,26 @@ class AdamW(torch.optim.Optimizer):
             state[name + "_scale"] = torch.zeros(blocks, dtype=torch.float32, device=p.device)
         return state
 
+    def _fit(self, p, s, bits):
+        """Moments in 32 or 64 bits take p's type; what else of a state s of p is not of the type and size that the
+        step takes is refused."""
+        wide = torch.float64 if p.dtype is torch.float64 else torch.float32
+        if bits == 32:
+            need = (("exp_avg", wide, p.shape), ("exp_avg_sq", wide, p.shape))
+        else:
+            codes, blocks = torch.float8_e4m3fn, (-(-p.numel() // HQML_ADAMW_BLOCK),)
+            need = (("exp_avg", codes, p.shape), ("exp_avg_sq_root", codes, p.shape),
+                    ("exp_avg_scale", torch.float32, blocks), ("exp_avg_sq_root_scale", torch.float32, blocks))
+        for name, dtype, shape in need:
+            t = s.get(name)
+            if t is None or t.shape != shape or t.device != p.device or not t.is_contiguous():
+                raise ValueError(f"{name} of a parameter {tuple(p.shape)} on {p.device} must be a contiguous tensor "
+                                 f"{tuple(shape)} there")
+            if t.dtype is not dtype:
+                if bits != 32 or t.dtype not in (torch.float32, torch.float64):
+                    raise ValueError(f"{name} of a parameter in {p.dtype} must be {dtype}, not {t.dtype}")
+                s[name] = t.to(dtype)
+
     def step(self, closure=None):
         for hook in tuple(self._optimizer_step_pre_hooks.values()):
             hook(self, (), {})
@@ -67,7 +89,7 @@ class AdamW(torch.optim.Optimizer):
                 loss = closure()
         state = self.state
         for group in self.param_groups:
-            eight = group["state_bits"] == 8
+            bits = group["state_bits"]
             calls = {}   # tensors that one call can take
             for p in group["params"]:
                 g = p.grad
@@ -75,29 +97,40 @@ class AdamW(torch.optim.Optimizer):
                     continue
                 if g.layout is not torch.strided or g.dtype not in _DTYPES:
                     raise ValueError("gradients must be dense, in fp32, bf16 or fp64")
-                if not p.is_contiguous():
-                    raise ValueError("parameters must be contiguous")
+                n, dtype = p.numel(), p.dtype
+                if not p.is_contiguous() or dtype not in _DTYPES:
+                    raise ValueError("parameters must be contiguous, in fp32, bf16 or fp64")
+                if g.numel() != n:
+                    raise ValueError(f"a parameter of {n} elements has a gradient of {g.numel()}")
                 if not g.is_contiguous():
                     g = g.detach().contiguous()
                 s = state[p]
                 if not s:
-                    s.update(self._begin(p, group["state_bits"]))
-                key = (p.dtype, g.dtype, p.get_device(), s["step"])
+                    s.update(self._begin(p, bits))
+                # the kernel walks a state by its parameter's type and size, and nothing behind the addresses says
+                # how large it is; that it is on the device is the entry point's to check
+                m, v = s.get("exp_avg"), s.get("exp_avg_sq_root" if bits == 8 else "exp_avg_sq")
+                fits = (m is not None and v is not None and m.dtype is v.dtype is (_CODES if bits == 8 else _WIDE[dtype])
+                        and m.numel() == n == v.numel() and m.is_contiguous() and v.is_contiguous())
+                if bits == 8 and fits:
+                    ms, vs, blocks = s.get("exp_avg_scale"), s.get("exp_avg_sq_root_scale"), -(-n // HQML_ADAMW_BLOCK)
+                    fits = (ms is not None and vs is not None and ms.dtype is vs.dtype is torch.float32
+                            and ms.numel() == blocks == vs.numel() and ms.is_contiguous() and vs.is_contiguous())
+                if not fits:
+                    self._fit(p, s, bits)   # or an error; with 8 bits always one
+                    m, v = s["exp_avg"], s["exp_avg_sq"]
+                key = (dtype, g.dtype, p.get_device(), s["step"])
                 call = calls.get(key)
                 if call is None:
                     call = calls[key] = ([], [], [], [])
                 words, params, grads, states = call
-                if eight:
-                    words += (p.data_ptr(), g.data_ptr(), s["exp_avg"].data_ptr(), s["exp_avg_sq_root"].data_ptr(),
-                              s["exp_avg_scale"].data_ptr(), s["exp_avg_sq_root_scale"].data_ptr(), p.numel())
-                else:
-                    words += (p.data_ptr(), g.data_ptr(), s["exp_avg"].data_ptr(), s["exp_avg_sq"].data_ptr(), 0, 0,
-                              p.numel())
+                words += (p.data_ptr(), g.data_ptr(), m.data_ptr(), v.data_ptr(), ms.data_ptr() if bits == 8 else 0,
+                          vs.data_ptr() if bits == 8 else 0, n)
                 params.append(p)
                 grads.append(g)    # kept until its kernel is queued
                 states.append(s)
             for (pd, gd, device, before), (words, params, grads, states) in calls.items():
-                cfg = hqml_adamw_config(_DTYPES[pd], _DTYPES[gd], HQML_MOMENTS_8 if eight else HQML_MOMENTS_32,
+                cfg = hqml_adamw_config(_DTYPES[pd], _DTYPES[gd], HQML_MOMENTS_8 if bits == 8 else HQML_MOMENTS_32,
                                         before + 1, group["lr"], *group["betas"], group["eps"], group["weight_decay"],
                                         device, _current_stream(device))
                 hqml_adamw_step(cfg, len(params), (ctypes.c_longlong * len(words))(*words))
@@ -114,12 +147,22 @@ class AdamW(torch.optim.Optimizer):
     step.hooked = True
 
     def load_state_dict(self, state_dict):
-        """As torch's, but the moments keep the types they were saved in."""
+        """As torch's, but the moments keep the precision they were saved in (32 and 64 bits follow the parameter's
+        type).  A state that does not fit its parameter is refused before anything is taken over."""
+        saved, held = state_dict["state"], []
+        for own, group in zip(self.param_groups, state_dict["param_groups"]):
+            bits = group.get("state_bits")
+            if bits not in (8, 32):
+                raise ValueError("state_bits must be 8 or 32")
+            for i, p in zip(group["params"], own["params"]):
+                if p.dtype is torch.float64 and bits == 8:
+                    raise ValueError("8-bit moments are for fp32 and bf16 parameters")
+                if not saved.get(i):
+                    continue
+                s = {k: v.detach().to(p.device, copy=True).contiguous() if isinstance(v, torch.Tensor)
+                     else copy.deepcopy(v) for k, v in saved[i].items()}
+                self._fit(p, s, bits)
+                held.append((p, s))
         super().load_state_dict(state_dict)
-        saved = state_dict["state"]
-        ids = [i for g in state_dict["param_groups"] for i in g["params"]]
-        params = [p for g in self.param_groups for p in g["params"]]
-        for i, p in zip(ids, params):
-            if i in saved:
-                self.state[p] = {k: v.detach().to(p.device, copy=True).contiguous() if isinstance(v, torch.Tensor)
-                                 else copy.deepcopy(v) for k, v in saved[i].items()}
+        for p, s in held:
+            self.state[p] = s
