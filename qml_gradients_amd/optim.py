@@ -10,6 +10,7 @@ import copy
 import ctypes
 
 import torch
+from torch.optim.optimizer import _global_optimizer_post_hooks, _global_optimizer_pre_hooks
 
 from . import (HQML_ADAMW_BLOCK, HQML_DTYPE_BF16, HQML_DTYPE_FP32, HQML_DTYPE_FP64, HQML_MOMENTS_8, HQML_MOMENTS_32,
                hqml_adamw_config, hqml_adamw_step)
@@ -80,9 +81,7 @@ class AdamW(torch.optim.Optimizer):
                     raise ValueError(f"{name} of a parameter in {p.dtype} must be {dtype}, not {t.dtype}")
                 s[name] = t.to(dtype)
 
-    def step(self, closure=None):
-        for hook in tuple(self._optimizer_step_pre_hooks.values()):
-            hook(self, (), {})
+    def _step(self, closure=None):
         loss = None
         if closure is not None:
             with torch.enable_grad():
@@ -138,13 +137,19 @@ class AdamW(torch.optim.Optimizer):
                     s["step"] = before + 1
                 # a backward pass that saved a parameter from before this step has to refuse it
                 torch.autograd.graph.increment_version(params)
-        for hook in tuple(self._optimizer_step_post_hooks.values()):
-            hook(self, (), {})
         return loss
 
-    # torch wraps a step that does not say this in a profiler range and the hooks, which cost four times the
-    # launch; the optimiser's own hooks run above
-    step.hooked = True
+    _hooked_step = torch.optim.Optimizer.profile_hook_step(_step)
+
+    def step(self, closure=None):
+        """One step of every parameter that has a gradient; what `closure` returns, called first with gradients on."""
+        # torch's hooks and profiler range cost four times the launch: taken where somebody asked for one
+        if (_global_optimizer_pre_hooks or _global_optimizer_post_hooks or self._optimizer_step_pre_hooks
+                or self._optimizer_step_post_hooks or torch.autograd._profiler_enabled()):
+            return self._hooked_step() if closure is None else self._hooked_step(closure)
+        return self._step(closure)
+
+    step.hooked = True   # torch wraps a step that does not say so itself
 
     def load_state_dict(self, state_dict):
         """As torch's, but the moments keep the precision they were saved in (32 and 64 bits follow the parameter's

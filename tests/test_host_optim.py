@@ -163,3 +163,56 @@ def test_plain_steps_pass_what_they_hold(bits, calls):
     other.step()
     assert_in_range(other, calls)
     assert calls[-1][0].step == 3
+
+
+def test_step_hooks_are_called_as_torch_calls_them(calls):
+    """Global and own hooks, in torch's order, with the step's arguments; as for one of torch's own optimisers."""
+    from torch.optim.optimizer import register_optimizer_step_post_hook, register_optimizer_step_pre_hook
+
+    def run(make):
+        seen = []
+
+        def note(name):
+            return lambda o, args, kwargs: seen.append((name, args[1:] == (closure,) or kwargs == {"closure": closure}))
+
+        def closure():
+            seen.append("closure")
+            return torch.tensor(2.0)
+
+        p = parameter()
+        opt = make([p])
+        handles = [register_optimizer_step_pre_hook(note("global before")),
+                   register_optimizer_step_post_hook(note("global after")),
+                   opt.register_step_pre_hook(note("before")), opt.register_step_post_hook(note("after"))]
+        try:
+            assert float(opt.step(closure)) == 2.0
+            opt.step()
+        finally:
+            for h in handles:
+                h.remove()
+        opt.step()
+        return seen
+
+    got = run(optim.AdamW)
+    assert got == run(lambda params: torch.optim.SGD(params, lr=0.1))
+    assert len(got) == 9 and got[2] == "closure" and all(e[1] for e in got[:5] if e != "closure")
+    assert len(calls) == 3
+
+
+def test_a_hook_may_replace_the_closure(calls):
+    opt = optim.AdamW([parameter()])
+
+    def other(o, args, kwargs):
+        return (o, lambda: torch.tensor(5.0)), {}
+
+    handle = opt.register_step_pre_hook(other)
+    assert float(opt.step(lambda: torch.tensor(2.0))) == 5.0
+    handle.remove()
+    assert float(opt.step(lambda: torch.tensor(2.0))) == 2.0 and opt.step() is None
+
+
+def test_a_profile_shows_the_step(calls):
+    opt = optim.AdamW([parameter()])
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
+        opt.step()
+    assert any("Optimizer.step#AdamW" in e.key for e in prof.key_averages())
