@@ -154,7 +154,19 @@ class AdamW(torch.optim.Optimizer):
     def load_state_dict(self, state_dict):
         """As torch's, but the moments keep the precision they were saved in (32 and 64 bits follow the parameter's
         type).  A state that does not fit its parameter is refused before anything is taken over."""
-        saved, held = state_dict["state"], []
+        # as the last hook before the load, it sees what the others made of state_dict
+        last = self.register_load_state_dict_pre_hook(AdamW._keep)
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            last.remove()
+            self._kept = ()
+
+    _kept = ()
+
+    def _keep(self, state_dict):
+        """The states to load, as they were saved and checked: torch casts its own copies to the parameters' types."""
+        saved, kept = state_dict["state"], []
         for own, group in zip(self.param_groups, state_dict["param_groups"]):
             bits = group.get("state_bits")
             if bits not in (8, 32):
@@ -167,7 +179,10 @@ class AdamW(torch.optim.Optimizer):
                 s = {k: v.detach().to(p.device, copy=True).contiguous() if isinstance(v, torch.Tensor)
                      else copy.deepcopy(v) for k, v in saved[i].items()}
                 self._fit(p, s, bits)
-                held.append((p, s))
-        super().load_state_dict(state_dict)
-        for p, s in held:
+                kept.append((p, s))
+        self._kept = kept
+
+    def __setstate__(self, state):   # during a load: before the hooks that follow it
+        super().__setstate__(state)
+        for p, s in self._kept:
             self.state[p] = s

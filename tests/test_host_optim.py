@@ -216,3 +216,46 @@ def test_a_profile_shows_the_step(calls):
     with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CPU]) as prof:
         opt.step()
     assert any("Optimizer.step#AdamW" in e.key for e in prof.key_averages())
+
+
+def test_load_hooks_see_and_change_what_is_loaded(calls):
+    a = optim.AdamW([parameter(300)], state_bits=8)
+    a.step()
+    p = parameter(300)
+    b = optim.AdamW([p], state_bits=8)
+    seen = []
+
+    def before(o, state_dict):   # what a hook returns is loaded in its place
+        changed = {**state_dict, "state": {0: {**state_dict["state"][0], "step": 41}}}
+        changed["state"][0]["exp_avg_scale"] = torch.full((2,), 0.5)
+        return changed
+
+    def after(o):                # the moments are in place, in their types, and may be changed
+        seen.append((o.state[p]["step"], o.state[p]["exp_avg"].dtype))
+        o.state[p]["exp_avg_sq_root_scale"].fill_(0.25)
+
+    b.register_load_state_dict_pre_hook(before)
+    b.register_load_state_dict_post_hook(after)
+    b.load_state_dict(a.state_dict())
+    assert seen == [(41, torch.float8_e4m3fn)]
+    assert bool((b.state[p]["exp_avg_scale"] == 0.5).all()) and bool((b.state[p]["exp_avg_sq_root_scale"] == 0.25).all())
+    assert a.state_dict()["state"][0]["step"] == 1   # the caller's own stays
+    b.step()
+    assert_in_range(b, calls)
+    assert calls[-1][0].step == 42
+
+
+def test_saved_and_copied_optimisers_keep_their_moments(calls):
+    import copy
+    import io
+    a = optim.AdamW([parameter(300)], state_bits=8)
+    a.step()
+    file = io.BytesIO()
+    torch.save(a, file)
+    file.seek(0)
+    for b in (copy.deepcopy(a), torch.load(file, weights_only=False)):
+        q = b.param_groups[0]["params"][0]
+        q.grad = torch.ones(300)
+        b.step()
+        assert_in_range(b, calls)
+        assert b.state[q]["step"] == 2 and b.state[q]["exp_avg"].dtype is torch.float8_e4m3fn
