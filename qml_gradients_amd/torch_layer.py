@@ -65,8 +65,10 @@ class DenseFunction(torch.autograd.Function):
     """y = alpha act(x w^T + bias) + residual, differentiable in all four."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, dense):
+    def forward(ctx, x, weight, bias, residual, dense, gradients):
         ctx.dense = dense
+        if not gradients or not any(ctx.needs_input_grad[:3]):   # the residual's needs nothing kept
+            return dense.forward(x, weight, bias, residual)
         y, z = dense.forward_train(x, weight, bias, residual)
         ctx.save_for_backward(x, weight, z)
         return y
@@ -74,12 +76,12 @@ class DenseFunction(torch.autograd.Function):
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dy):
-        x, weight, z = ctx.saved_tensors
         need = ctx.needs_input_grad
         dx = dw = db = None
         if any(need[:3]):
+            x, weight, z = ctx.saved_tensors
             dx, dw, db = ctx.dense.backward(dy, x, weight, z, input=need[0], weight=need[1], bias=need[2])
-        return dx, dw, db, dy if need[3] else None, None
+        return dx, dw, db, dy if need[3] else None, None, None
 
 
 class DenseLayer(torch.nn.Module):
@@ -107,10 +109,7 @@ class DenseLayer(torch.nn.Module):
         x = x.reshape(-1, x.shape[-1])
         if residual is not None:
             residual = residual.reshape(-1, residual.shape[-1])
-        grads = torch.is_grad_enabled() and any(
-            t is not None and t.requires_grad for t in (x, self.weight, self.bias, residual))
-        if grads:
-            y = DenseFunction.apply(x, self.weight, self.bias, residual, self.dense)
-        else:
-            y = self.dense.forward(x, self.weight, self.bias, residual)
+        # through the function whether or not a gradient is wanted: it refuses a tangent that it would lose, and a trace
+        # shows it
+        y = DenseFunction.apply(x, self.weight, self.bias, residual, self.dense, torch.is_grad_enabled())
         return y.reshape(*lead, y.shape[-1])
