@@ -248,7 +248,8 @@ const char *hqml_dense_last_error(const hqml_dense *h);
  * as the gradient's own rounding, where the activation bends most).  bias, residual and z may
  * be NULL; z is what hqml_dense_backward needs (with HQML_ACT_NONE it is not needed and not
  * written).  y may be the residual itself (same stride); otherwise outputs overlap no other
- * argument.  Sums are held in fp32; with HQML_DTYPE_BF16 y is rounded once, to nearest even. */
+ * argument (HQML_ERR_ARG; neighbouring columns of one array do not overlap).  Sums are held in
+ * fp32; with HQML_DTYPE_BF16 y is rounded once, to nearest even. */
 int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw,
                        const void *bias, const void *residual, long long ldr, void *y, long long ldy,
                        float *z);
@@ -256,9 +257,10 @@ int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const
 /* Gradients of a forward call for dy = dL/dy [M][N] (row stride lddy):
  * dz = alpha act'(z) dy, dx = dz w [M][K] (row stride lddx), dw = dz^T x [N][K],
  * db = sum over rows of dz [N]; the residual's gradient is dy itself.  dw and db have no
- * gaps.  Each of dx, dw, db may be NULL (not formed).  z is the forward call's (ignored with
- * HQML_ACT_NONE).  M == 0 writes zeros to dw and db.  Sums are held in fp32; with
- * HQML_DTYPE_BF16 the results are rounded once, and before them dz, except in small products. */
+ * gaps, and outputs overlap no other argument (HQML_ERR_ARG).  Each of dx, dw, db may be NULL
+ * (not formed).  z is the forward call's (ignored with HQML_ACT_NONE).  M == 0 writes zeros to dw
+ * and db.  Sums are held in fp32; with HQML_DTYPE_BF16 the results are rounded once, and before
+ * them dz, except in small products. */
 int hqml_dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const void *x, long long ldx,
                         const void *w, long long ldw, const float *z, void *dx, long long lddx, void *dw,
                         void *db);

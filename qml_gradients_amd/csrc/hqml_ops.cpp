@@ -92,7 +92,30 @@ struct Arg {
     long long rows, len, ld;
     bool optional;
     size_t elem = 0;   // bytes of an element; 0: the handle's
+    bool output = false;
+    int itself = -1;   // the argument that an output may be
 };
+
+// Whether two arrays share bytes.  Where neither lies before the other they may still be columns of one array: rows the
+// same distance apart, and the columns apart within it.  Rows at other distances count as shared.
+bool overlap(const Arg &a, size_t ea, const Arg &b, size_t eb)
+{
+    struct Bytes {
+        size_t at, rows, len, step;
+    };
+    auto bytes = [](const Arg &g, size_t e) {
+        Bytes r{(size_t)g.p, (size_t)g.rows, e * (size_t)g.len, e * (size_t)g.ld};
+        if (r.rows > 1 && r.step == r.len) r.len *= r.rows, r.rows = 1;   // no gaps
+        return r;
+    };
+    const Bytes p = bytes(a, ea), q = bytes(b, eb);
+    if (p.at + (p.rows - 1) * p.step + p.len <= q.at || q.at + (q.rows - 1) * q.step + q.len <= p.at) return false;
+    if (p.rows == 1 && q.rows == 1) return true;
+    if (p.rows > 1 && q.rows > 1 && p.step != q.step) return true;
+    const size_t step = p.rows > 1 ? p.step : q.step;
+    const size_t from = q.at >= p.at ? (q.at - p.at) % step : (step - (p.at - q.at) % step) % step;
+    return p.len > from || from + q.len > step;
+}
 
 int check_args(int device, size_t dtype, const Arg *a, int n, std::string *err)
 {
@@ -112,6 +135,15 @@ int check_args(int device, size_t dtype, const Arg *a, int n, std::string *err)
         const int rc = check_device_array(device, a[i].p, bytes, a[i].name, err);
         if (rc != HQML_OK) return rc;
     }
+    // workgroups write rows of an output while others still read their operands
+    for (int i = 0; i < n; ++i)
+        for (int j = 0; j < n; ++j) {
+            if (!a[i].output || i == j || (a[j].output && j > i) || !a[i].p || !a[j].p) continue;
+            if (j == a[i].itself && a[i].p == a[j].p && a[i].ld == a[j].ld) continue;
+            if (!overlap(a[i], a[i].elem ? a[i].elem : dtype, a[j], a[j].elem ? a[j].elem : dtype)) continue;
+            *err = std::string(a[i].name) + " must not overlap " + a[j].name;
+            return HQML_ERR_ARG;
+        }
     return HQML_OK;
 }
 
@@ -142,9 +174,10 @@ int dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void
     const long long K = c.in_features, N = c.out_features;
     const OnDevice on(c.device);
     if (on.error() != hipSuccess) return dense_error(h, HQML_ERR_HIP, hip_text("device", on.error()));
-    const Arg args[] = {{"x", x, M, K, ldx, false},        {"w", w, N, K, ldw, false},
-                        {"bias", bias, 1, N, N, true},     {"residual", residual, M, N, ldr, true},
-                        {"y", y, M, N, ldy, false},        {"z", z, M, N, N, true, 4}};
+    if (c.activation == HQML_ACT_NONE) z = nullptr;
+    const Arg args[] = {{"x", x, M, K, ldx, false},         {"w", w, N, K, ldw, false},
+                        {"bias", bias, 1, N, N, true},      {"residual", residual, M, N, ldr, true},
+                        {"y", y, M, N, ldy, false, 0, true, 3}, {"z", z, M, N, N, true, 4, true}};
     std::string err;
     rc = check_args(c.device, dtype_bytes(c.dtype), args, 6, &err);
     if (rc != HQML_OK) return dense_error(h, rc, err);
@@ -164,13 +197,14 @@ int dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const v
     if (on.error() != hipSuccess) return dense_error(h, HQML_ERR_HIP, hip_text("device", on.error()));
     std::string err;
     if (M > 0) {
-        const Arg args[] = {{"dy", dy, M, N, lddy, false},     {"x", x, M, K, ldx, !dw},
-                            {"w", w, N, K, ldw, !dx},          {"z", z, M, N, N, c.activation == HQML_ACT_NONE, 4},
-                            {"dx", dx, M, K, lddx, true},      {"dw", dw, N, K, K, true},
-                            {"db", db, 1, N, N, true}};
+        if (c.activation == HQML_ACT_NONE) z = nullptr;
+        const Arg args[] = {{"dy", dy, M, N, lddy, false},           {"x", x, M, K, ldx, !dw},
+                            {"w", w, N, K, ldw, !dx},                {"z", z, M, N, N, c.activation == HQML_ACT_NONE, 4},
+                            {"dx", dx, M, K, lddx, true, 0, true},   {"dw", dw, N, K, K, true, 0, true},
+                            {"db", db, 1, N, N, true, 0, true}};
         rc = check_args(c.device, dtype_bytes(c.dtype), args, 7, &err);
     } else {
-        const Arg args[] = {{"dw", dw, N, K, K, true}, {"db", db, 1, N, N, true}};
+        const Arg args[] = {{"dw", dw, N, K, K, true, 0, true}, {"db", db, 1, N, N, true, 0, true}};
         rc = check_args(c.device, dtype_bytes(c.dtype), args, 2, &err);
     }
     if (rc != HQML_OK) return dense_error(h, rc, err);

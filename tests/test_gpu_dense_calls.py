@@ -1,0 +1,69 @@
+"""Calls of the dense layer at the edges of its arguments: arrays that overlap, row strides of a single row, outputs that
+autograd has seen, layers of more than 2^32 weights."""
+import pytest
+
+from gpu_util import say
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+def refused(call, *args):
+    import qml_gradients_amd as hq
+    with pytest.raises(hq.HqmlError) as e:
+        call(*args)
+    assert e.value.status == hq.HQML_ERR_ARG and "overlap" in str(e.value)
+
+
+def test_outputs_that_overlap_an_argument_are_refused():
+    """Workgroups write some rows of an output while others still read theirs."""
+    import qml_gradients_amd as hq
+    M, K, N = 12, 16, 16
+    layer = hq.Dense(K, N, M, activation="tanh")
+    buf = torch.randn(4 * M, K, device="cuda")
+    x, w, bias, r = buf[:M], torch.randn(N, K, device="cuda"), torch.randn(N, device="cuda"), torch.randn(M, N, device="cuda")
+    before = buf.clone()
+    refused(lambda: layer.forward(x, w, out=buf[1:M + 1]))              # a row on
+    refused(lambda: layer.forward(buf[3:M + 3], w, out=buf[:M]))        # from behind
+    both = torch.randn(M, K + N, device="cuda")
+    refused(lambda: layer.forward(both[:, :K], w, out=both[:, K - 1:-1]))   # one column in common
+    refused(lambda: layer.forward(x, w, both.view(-1)[K + N:K + 2 * N], out=both[:, :N]))   # the bias is a row of it
+    refused(lambda: layer.forward(x, w, residual=buf[2 * M:3 * M], out=buf[2 * M + 1:3 * M + 1]))
+    refused(lambda: layer.forward(x.clone(), w, residual=buf.view(-1, 2 * K)[:M, :K], out=buf[:M]))   # another row stride
+    weights = torch.randn(M + N, K, device="cuda")
+    refused(lambda: layer.forward(x, weights[M - 1:M - 1 + N], out=weights[:M]))
+    y, z = layer.forward_train(x, w, bias, r)
+    p = [t.data_ptr() for t in (x, w, z, r)]
+    refused(hq.hqml_dense_forward, layer.handle, M, p[0], K, p[1], K, None, None, 0, y.data_ptr(), N, y.data_ptr() + 64)
+    refused(hq.hqml_dense_backward, layer.handle, M, p[3], N, p[0], K, p[1], K, p[2], p[0], K, None, None)
+    refused(hq.hqml_dense_backward, layer.handle, M, p[3], N, p[0], K, p[1], K, p[2], None, K, p[1], None)
+    refused(hq.hqml_dense_backward, layer.handle, M, p[3], N, p[0], K, p[1], K, p[2], None, K, None, p[2] + 4)
+    dw = torch.zeros(N, K, device="cuda")
+    refused(hq.hqml_dense_backward, layer.handle, M, p[3], N, p[0], K, p[1], K, p[2], None, K, dw.data_ptr(),
+            dw.data_ptr() + 8)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, before) and not dw.any()
+
+
+def test_outputs_beside_their_arguments_are_taken():
+    """Columns of one array, rows that follow one another, a bias in the gap between output rows, the residual itself."""
+    import qml_gradients_amd as hq
+    M, K, N = 12, 16, 24
+    layer = hq.Dense(K, N, M, activation="tanh")
+    x, w, bias, r = (torch.randn(*s, device="cuda") for s in ((M, K), (N, K), (N,), (M, N)))
+    want = layer.forward(x, w, bias, r)
+    wide = torch.randn(M, K + 3 * N, device="cuda")
+    wide[:, :K], wide[:, K:K + N], wide[3, -N:] = x, r, bias
+    keep = wide.clone()
+    got = layer.forward(wide[:, :K], w, wide[3, -N:], wide[:, K:K + N], out=wide[:, K + N:K + 2 * N])
+    assert torch.equal(got, want)
+    keep[:, K + N:K + 2 * N] = want
+    assert torch.equal(wide, keep)
+    rows = torch.zeros(2 * M, N, device="cuda")
+    rows[:M] = r
+    assert torch.equal(layer.forward(x, w, bias, rows[:M], out=rows[M:]), want)
+    assert torch.equal(layer.forward(x, w, bias, rows[:M], out=rows[:M]), want)
+    one = rows[M - 1:M].clone()   # one row's stride means nothing
+    one.copy_(r[:1])
+    assert torch.allclose(layer.forward(x[:1], w, bias, one, out=one), want[:1], atol=1e-5)
