@@ -139,12 +139,19 @@ int check_args(int device, size_t dtype, const Arg *a, int n, std::string *err)
     for (int i = 0; i < n; ++i)
         for (int j = 0; j < n; ++j) {
             if (!a[i].output || i == j || (a[j].output && j > i) || !a[i].p || !a[j].p) continue;
-            if (j == a[i].itself && a[i].p == a[j].p && a[i].ld == a[j].ld) continue;
+            if (j == a[i].itself && a[i].p == a[j].p && (a[i].ld == a[j].ld || a[i].rows == 1)) continue;
             if (!overlap(a[i], a[i].elem ? a[i].elem : dtype, a[j], a[j].elem ? a[j].elem : dtype)) continue;
             *err = std::string(a[i].name) + " must not overlap " + a[j].name;
             return HQML_ERR_ARG;
         }
     return HQML_OK;
+}
+
+// The stride that the kernels take.  They form it for rows past the last one too, and hold it in 32 bits of bytes: that of
+// a single row, which may be anything, would bring those back onto the row itself.
+long long stride(long long rows, long long len, long long ld)
+{
+    return rows > 1 ? ld : len;
 }
 
 int dense_error(hqml_dense *h, int code, const std::string &msg)
@@ -181,7 +188,8 @@ int dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void
     std::string err;
     rc = check_args(c.device, dtype_bytes(c.dtype), args, 6, &err);
     if (rc != HQML_OK) return dense_error(h, rc, err);
-    DenseForward a{M, (int)K, (int)N, x, w, bias, residual, ldx, ldw, ldr, ldy, y, z, c.activation, c.alpha};
+    DenseForward a{M, (int)K, (int)N, x, w, bias, residual, stride(M, K, ldx), stride(N, K, ldw), stride(M, N, ldr),
+                   stride(M, N, ldy), y, z, c.activation, c.alpha};
     const hipError_t e = launch_dense_forward(a, c.dtype, h->ws, h->stream);
     return e == hipSuccess ? HQML_OK : dense_error(h, HQML_ERR_HIP, hip_text("dense forward", e));
 }
@@ -209,7 +217,8 @@ int dense_backward(hqml_dense *h, int M, const void *dy, long long lddy, const v
     }
     if (rc != HQML_OK) return dense_error(h, rc, err);
     if (!dx && !dw && !db) return HQML_OK;
-    DenseBackward a{M, (int)K, (int)N, dy, x, w, z, lddy, ldx, ldw, lddx, dx, dw, db, c.activation, c.alpha};
+    DenseBackward a{M, (int)K, (int)N, dy, x, w, z, stride(M, N, lddy), stride(M, K, ldx), stride(N, K, ldw),
+                    stride(M, K, lddx), dx, dw, db, c.activation, c.alpha};
     const hipError_t e = launch_dense_backward(a, c.dtype, h->ws, h->stream);
     return e == hipSuccess ? HQML_OK : dense_error(h, HQML_ERR_HIP, hip_text("dense backward", e));
 }

@@ -67,3 +67,33 @@ def test_outputs_beside_their_arguments_are_taken():
     one = rows[M - 1:M].clone()   # one row's stride means nothing
     one.copy_(r[:1])
     assert torch.allclose(layer.forward(x[:1], w, bias, one, out=one), want[:1], atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("act", ["none", "tanh"])
+def test_stride_of_a_single_row_means_nothing(act, dtype):
+    """Of an array of one row any stride is as good as another, 2^30 elements (2^32 bytes) too."""
+    import qml_gradients_amd as hq
+    for M, K, N in ((1, 40, 24), (1, 300, 1), (7, 33, 1)):
+        say(f"[gpu] dense {M} x {K} -> {N} {dtype} {act}")
+        dt = torch.float32 if dtype == "fp32" else torch.bfloat16
+        x, w, r, dy = (torch.randn(*s, device="cuda").to(dt) for s in ((M, K), (N, K), (M, N), (M, N)))
+        layer = hq.Dense(K, N, M, dtype=dtype, activation=act)
+        want, z = layer.forward_train(x, w, None, r)
+        grads = layer.backward(dy, x, w, z)
+        zp = None if z is None else z.data_ptr()
+        for far in (1 << 20, 1 << 30, (1 << 30) + 8, 1 << 31, 1 << 40):
+            lx, lw, ly = far if M == 1 else K, far if N == 1 else K, far if M == 1 else N
+            y = torch.zeros_like(r)
+            hq.hqml_dense_forward(layer.handle, M, x.data_ptr(), lx, w.data_ptr(), lw, None, r.data_ptr(), ly,
+                                  y.data_ptr(), ly, zp)
+            assert torch.equal(y, want)
+            got = torch.zeros_like(x), torch.zeros_like(w), torch.zeros(N, dtype=dt, device="cuda")
+            hq.hqml_dense_backward(layer.handle, M, dy.data_ptr(), ly, x.data_ptr(), lx, w.data_ptr(), lw, zp,
+                                   got[0].data_ptr(), lx, got[1].data_ptr(), got[2].data_ptr())
+            assert all(torch.equal(a, b) for a, b in zip(got, grads)), far
+        same = r[:1].clone()
+        if M == 1:   # the residual itself, whatever the strides say
+            hq.hqml_dense_forward(layer.handle, 1, x.data_ptr(), K, w.data_ptr(), K, None, same.data_ptr(), N,
+                                  same.data_ptr(), N + 8, None)
+            assert torch.equal(same, want)
