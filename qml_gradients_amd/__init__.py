@@ -509,6 +509,8 @@ class Dense:
         self._queue(self._lib.hqml_dense_forward, M, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
                     y.data_ptr(), ldy, None if z is None else z.data_ptr())
+        if out is not None:   # a backward pass that saved it from before has to refuse it
+            self.torch.autograd.graph.increment_version(out)
         return y, z
 
     def forward(self, x, w, bias=None, residual=None, out=None):

@@ -97,3 +97,15 @@ def test_stride_of_a_single_row_means_nothing(act, dtype):
             hq.hqml_dense_forward(layer.handle, 1, x.data_ptr(), K, w.data_ptr(), K, None, same.data_ptr(), N,
                                   same.data_ptr(), N + 8, None)
             assert torch.equal(same, want)
+
+
+def test_out_marks_its_array_changed():
+    """A backward pass that saved the array from before the call has to refuse it."""
+    import qml_gradients_amd as hq
+    layer = hq.Dense(8, 6, 4)
+    x, w, out = (torch.randn(*s, device="cuda") for s in ((4, 8), (6, 8), (4, 6)))
+    a = torch.ones(4, 6, device="cuda", requires_grad=True)
+    loss = (a * out).sum()
+    layer.forward(x, w, out=out)
+    with pytest.raises(RuntimeError):
+        loss.backward()
