@@ -2,13 +2,14 @@
 //
 // All three products of the layer are one kernel family (hqml_gemm.hpp):
 //   forward  C = x w^T      dx = dz w      dw = dz^T x
-// This file chooses their tiles and splits, and forms dz = alpha act'(z) dy with its row sums.
+// hqml_dense_cut.hpp chooses their tiles and splits; this file runs them and forms dz = alpha act'(z) dy with its row sums.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
 
+#include "hqml_dense_cut.hpp"
 #include "hqml_gemm.hpp"
 #include "hqml_ops.hpp"
 
@@ -16,149 +17,6 @@ namespace hqml {
 namespace {
 
 using namespace gemm;
-
-int ceil_div(int a, int b) { return (a + b - 1) / b; }
-
-// ---- how a product is run: the estimate that is least ----
-//
-// Times in us, fitted to sweeps of every cut over 71 products of 64 to 16384 rows, 7 to 8192 columns and k 7 to 16384 and
-// 90 smaller ones, of each type and layout: the cut chosen took 2 to 5 % more than the fastest in the mean, 40 % at worst.
-
-constexpr int kUnits = 256;    // compute units
-constexpr int kPartTiles = 4096, kMostParts = 64;
-constexpr int kParts[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, kMostParts};
-
-// A tile kernel: a workgroup spends `step` on 32 k when alone on its compute unit, n of them n * share; fixed:
-// launch, first loads, epilogue; work split over k costs join + parts * join_part and the way of its sums to memory and
-// back (9 TB/s: most stay in the caches).  Memory gives `rate` bytes a us where a compute unit's workgroups, up to
-// `most` together, have `enough` bytes under way; the result's bytes count `out` times as much again.
-struct TileCost {
-    Shape shape;
-    int most;
-    float fixed, step, share, join, join_part;
-};
-struct MemoryCost {
-    float rate, enough, out;
-};
-constexpr TileCost kFp32Cost[] = {{TILE_64, 4, 4.6f, 0.65f, 0.45f, 0.3f, 0.23f}, {TILE_128, 2, 5.0f, 1.18f, 1.25f, 0.1f, 1.0f},
-                                  {TILE_64x32, 6, 4.6f, 0.75f, 0.23f, 0.3f, 0.2f},
-                                  {TILE_32x64, 6, 4.6f, 0.75f, 0.23f, 0.3f, 0.2f}};
-constexpr TileCost kStagedCost[] = {{TILE_64, 4, 4.5f, 0.27f, 0.184f, 0.6f, 0.4f}, {TILE_128, 2, 4.5f, 0.435f, 0.35f, 0.8f, 1.0f}};
-constexpr TileCost kDirectCost[] = {{TILE_64, 4, 2.6f, 0.18f, 0.137f, 0.65f, 0.42f},
-                                    {TILE_128, 2, 4.6f, 0.2f, 0.24f, 2.0f, 1.06f},
-                                    {TILE_256, 1, 8.6f, 0.45f, 0.525f, 4.6f, 4.0f}};
-constexpr MemoryCost kFp32Memory{4.6e6f, 90e3f, 0.0f}, kStagedMemory{5e6f, 29e3f, 2.0f}, kDirectMemory{5e6f, 18e3f, 1.0f};
-
-struct Cut {
-    Shape shape;
-    int parts;
-    float us;
-};
-
-Cut best_cut(int I, int J, int K, size_t elem, const TileCost *cost, int n, const MemoryCost &m)
-{
-    const int steps = ceil_div(K, 32);
-    const float out = (float)I * J * elem, bytes = ((float)I * K + (float)J * K) * elem + out;
-    Cut best{TILE_64, 0, 0.0f};
-    for (int c = 0; c < n; ++c) {
-        const int *side = kSides[cost[c].shape];
-        // narrow tiles are for operands that a wider one would not fill
-        if ((side[0] < side[1] && I > side[0]) || (side[1] < side[0] && J > side[1])) continue;
-        const long long tiles = (long long)ceil_div(I, side[0]) * ceil_div(J, side[1]);
-        const float step_bytes = 32.0f * elem * (std::min(side[0], I) + std::min(side[1], J));
-        for (int parts : kParts) {
-            const long long groups = tiles * parts;
-            if (parts > 1 && (groups > kPartTiles * 64 * 64 / (side[0] * side[1]) || parts * 2 > steps)) break;
-            const float each = (float)((groups + kUnits - 1) / kUnits);
-            // three steps of a workgroup are under way
-            const float under_way = std::min((float)groups / kUnits, (float)cost[c].most) * 3 * step_bytes;
-            const float memory = bytes / (m.rate * std::min(1.0f, under_way / m.enough)) + out * m.out / m.rate;
-            float us = cost[c].fixed + std::max(memory, ceil_div(steps, parts) * std::max(cost[c].step, each * cost[c].share)) +
-                       0.1f * each;   // starts and ends
-            if (parts > 1) us += cost[c].join + parts * cost[c].join_part + (float)groups * (side[0] * side[1] * 8) / 9e6f;
-            if (!best.parts || us < best.us) best = {cost[c].shape, parts, us};
-        }
-    }
-    return best;
-}
-
-Cut best_cut(int I, int J, int K, size_t elem, bool direct)
-{
-    if (elem == 4) return best_cut(I, J, K, elem, kFp32Cost, 4, kFp32Memory);
-    return direct ? best_cut(I, J, K, elem, kDirectCost, 3, kDirectMemory)
-                  : best_cut(I, J, K, elem, kStagedCost, 2, kStagedMemory);
-}
-
-// A small forward product: every tile reads its own rows, at `rate` bytes a us and compute unit (bf16 rows whose
-// elements straddle words: a sixth of fp32's rate); the fp32 matrix instruction takes 8 x 32 cycles and more for
-// 16 x 16 x 32; a wave waits for its loads once in a few steps.
-struct SmallCut {
-    int fi, waves, parts;
-    float us;
-};
-
-SmallCut small_cut(int I, int J, int K, size_t elem, bool words)
-{
-    SmallCut best{0, 1, 1, 0.0f};
-    const int steps = ceil_div(K, 32);
-    const float bytes = ((float)I * K + (float)J * K + (float)I * J) * elem;
-    const float rate = elem == 4 ? 81e3f : words ? 51e3f : 14.3e3f;
-    for (int fi : {1, 2, 4}) {
-        if (fi > 1 && I <= 8 * fi) break;
-        const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
-        const int rows = std::min(16 * fi, I) + std::min(16, J), at = fi == 4 ? 2 : 4;   // steps a wave loads together
-        for (int parts : {1, 2, 3, 4, 6, 8}) {
-            const int own = ceil_div(steps, parts);   // of one workgroup
-            if (parts > 1 && (tiles * parts > kUnits || own < 4)) break;
-            const float each = (float)((tiles * parts + kUnits - 1) / kUnits);
-            for (int waves : {1, 2, 4, 8, 16}) {
-                if (waves > 1 && (waves > own || (waves == 16 && fi > 1))) break;
-                const float load = each * own * (32 * elem * rows) / rate;
-                const float mul = elem == 2 ? 0.0f : each * own * fi * 0.037f, work = load + mul;
-                const float wait = ceil_div(own, waves * at) * (elem == 4 ? 0.3f + 0.63f * fi : 0.14f + 0.45f * fi) *
-                                   std::max(1.0f, each * waves / 16);
-                // memory's rate needs about 40 KB under way on a compute unit
-                const float under_way = each * waves * at * (16 * 16 * elem * (fi + 1));
-                const float memory = bytes / (4.6e6f * std::min(1.0f, under_way / 40e3f));
-                const float us = 2.9f + std::max(std::max(work, wait) + 0.3f * std::min(work, wait), memory) +
-                                 each * (0.35f + 0.065f * waves) + (parts > 1 ? 1.65f + 0.07f * parts : 0.0f);
-                if (!best.fi || us < best.us) best = {fi, waves, parts, us};
-            }
-        }
-    }
-    return best;
-}
-
-// Small gradients in one launch.  What counts is forming dz anew in every tile (1,300 to 1,770 cycles of a SIMD for
-// 16 rows and 32 k, the matrix instructions with them) and the waits of the longer product's waves.  Over 70 products
-// of each type the choice took 1 to 3 % more than the best in the mean.
-SmallCut small_gradients_cut(int M, int N, int K, size_t elem, bool words)
-{
-    SmallCut best{0, 1, 1, 0.0f};
-    const int steps_x = ceil_div(N, 32), steps_w = ceil_div(M, 32), steps = std::max(steps_x, steps_w);
-    for (int fi : {1, 4}) {
-        const float block_us = ((elem == 4 ? 1420.0f : words ? 1300.0f : 1570.0f) + (fi == 4 ? 200.0f : 0.0f)) / 2.15e6f;
-        for (int waves : {1, 2, 4, 8}) {
-            if (waves > 1 && waves > steps) break;
-            const long long tx = (long long)ceil_div(M, 16 * fi) * ceil_div(K, 16);
-            const long long tw = (long long)ceil_div(N, 16 * fi) * ceil_div(K + 1, 16);
-            const float work = ((float)tx * steps_x * std::min(M, 16 * fi) + (float)tw * steps_w * std::min(N, 16 * fi)) /
-                               16 * block_us;
-            const int at = fi == 1 ? 2 : 1;   // steps a wave loads together
-            const float wait = ceil_div(steps, waves * at) * (fi == 1 ? 1.55f : 2.9f);
-            const float ends = (tx + tw) * waves * 4.4f / (kUnits * 32);   // workgroups' starts and epilogues
-            const float us = 3.6f + std::max(work, wait) + 0.37f * std::min(work, wait) + ends;
-            if (!best.fi || us < best.us) best = {fi, waves, 1, us};
-        }
-    }
-    return best;
-}
-
-// dz and its row sums by themselves.
-float slope_us(int M, int N, size_t elem)
-{
-    return 6.0f + (float)M * N * (4 + 2 * elem) / 5e6f;
-}
 
 // The most 64 x 64 tiles of partial sums that a product of up to these sizes leaves, 64 MB of them.
 size_t part_tiles(size_t I, size_t J, size_t K)
@@ -255,11 +113,6 @@ Padded pad(const void *x, long long ldx, int rows_x, const void *w, long long ld
     k_pad<<<(unsigned)std::min<long long>((chunks + 255) / 256, 8192), 256, 0, s>>>(
         (const uint16_t *)x, ldx, rows_x, (const uint16_t *)w, ldw, rows_w, K, Kp, to_x, to_w);
     return {to_x, to_w, hipGetLastError()};
-}
-
-float pad_us(int rows, int K)
-{
-    return rows ? 4.0f + (float)rows * K * 4 / 4.5e6f : 0.0f;
 }
 
 constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; eight threads go down the rows
@@ -397,33 +250,25 @@ hipError_t forward(const DenseForward &a, const DenseWorkspace &ws, hipStream_t 
     P.bias = a.bias, P.residual = a.residual, P.ldr = a.ldr;
     P.z = a.act == HQML_ACT_NONE ? nullptr : (float *)a.z;
     P.act = a.act, P.alpha = a.alpha;
-    bool direct = false;
-    int copy_x = 0, copy_w = 0;   // rows to copy
-    Cut c = best_cut(P.I, P.J, P.K, sizeof(T), false);
-    if (sizeof(T) == 2) {
-        if (!straight(a.x, a.ldx, K_ROWS, a.K)) copy_x = a.M;
-        if (!straight(a.w, a.ldw, K_ROWS, a.K)) copy_w = a.N;
-        const Cut d = best_cut(P.I, P.J, P.K, 2, true);
-        direct = !(copy_x + copy_w) || (ws.pad && d.us + pad_us(copy_x + copy_w, a.K) < c.us);
-        if (direct) c = d, c.us += pad_us(copy_x + copy_w, a.K);
-    }
-    const SmallCut sc = small_cut(P.I, P.J, P.K, sizeof(T), whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw));
-    if (sc.us <= c.us) {
-        cut_small(P, sc.fi);
-        P.k_part = ceil_div(ceil_div(a.K, sc.parts), 32) * 32;
+    const ForwardChoice f = choose_forward(a.M, a.K, a.N, sizeof(T), straight(a.x, a.ldx, K_ROWS, a.K),
+                                           straight(a.w, a.ldw, K_ROWS, a.K),
+                                           whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw), ws.pad);
+    if (f.small) {
+        cut_small(P, f.few.fi);
+        P.k_part = ceil_div(ceil_div(a.K, f.few.parts), 32) * 32;
         P.parts = ceil_div(a.K, P.k_part);
         P.part = ws.part;
         P.ticket = ws.ticket;
-        if (!fits(P, sc.fi * 16 * 16, ws)) return hipErrorInvalidValue;
-        return launch_small_forward(P, sizeof(T) == 2, sc.fi, sc.waves, s);
+        if (!fits(P, f.few.fi * 16 * 16, ws)) return hipErrorInvalidValue;
+        return launch_small_forward(P, sizeof(T) == 2, f.few.fi, f.few.waves, s);
     }
-    if (direct && copy_x + copy_w) {
-        const Padded p = pad(a.x, a.ldx, copy_x, a.w, a.ldw, copy_w, a.K, ws, s);
+    if (f.copy_x || f.copy_w) {
+        const Padded p = pad(a.x, a.ldx, f.copy_x ? a.M : 0, a.w, a.ldw, f.copy_w ? a.N : 0, a.K, ws, s);
         if (p.e != hipSuccess) return p.e;
-        if (copy_x) P.a = p.x, P.lda = pad8(a.K);
-        if (copy_w) P.b = p.w, P.ldb = pad8(a.K);
+        if (f.copy_x) P.a = p.x, P.lda = pad8(a.K);
+        if (f.copy_w) P.b = p.w, P.ldb = pad8(a.K);
     }
-    return run_product<T>(P, K_ROWS, K_ROWS, c, direct, ws, s);
+    return run_product<T>(P, K_ROWS, K_ROWS, f.tiles, f.direct, ws, s);
 }
 
 // dx, dw and db in one launch.
@@ -458,29 +303,15 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         e = zero<T>(a.dw, (long long)a.N * a.K, s);
         return e != hipSuccess ? e : zero<T>(a.db, a.N, s);
     }
-    // dx = dz w and dw = dz^T x: the cuts, and for bf16 whether to copy what cannot be loaded straight
-    Cut cx = best_cut(a.M, a.K, a.N, sizeof(T), false), cw = best_cut(a.N, a.K, a.M, sizeof(T), false);
-    bool form = a.act != HQML_ACT_NONE, direct = false;
-    int copy_x = 0, copy_w = 0;   // rows to copy
-    if (sizeof(T) == 2) {
-        if (!straight(a.x, a.ldx, K_COLS, 0) && a.dw) copy_x = a.M;
-        if (!straight(a.w, a.ldw, K_COLS, 0) && a.dx) copy_w = a.N;
-        const bool dy_straight = straight(a.dy, a.lddy, K_ROWS, a.N);
-        const Cut dx = best_cut(a.M, a.K, a.N, 2, true), dw = best_cut(a.N, a.K, a.M, 2, true);
-        const float copies = pad_us(copy_x + copy_w, a.K) + (form || dy_straight ? 0.0f : pad_us(a.M, a.N));
-        direct = (form || dy_straight || ws.dz) && (!(copy_x + copy_w) || ws.pad) && dx.us + dw.us + copies < cx.us + cw.us;
-        if (direct) {
-            cx = dx, cw = dw, cx.us += copies;
-            form = form || !dy_straight;   // dz in rows of a multiple of eight
-        }
-    }
-    const bool words = whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw) && whole_words(a.dy, a.lddy);
-    const SmallCut c = small_gradients_cut(a.M, a.N, a.K, sizeof(T), words);
-    if (c.us <= slope_us(a.M, a.N, sizeof(T)) + cx.us + cw.us) return gradients<T>(a, c, s);
+    const BackwardChoice b =
+        choose_backward(a.M, a.K, a.N, sizeof(T), a.act != HQML_ACT_NONE, a.dx, a.dw, straight(a.dy, a.lddy, K_ROWS, a.N),
+                        straight(a.x, a.ldx, K_COLS, 0), straight(a.w, a.ldw, K_COLS, 0),
+                        whole_words(a.x, a.ldx) && whole_words(a.w, a.ldw) && whole_words(a.dy, a.lddy), ws.dz, ws.pad);
+    if (b.small) return gradients<T>(a, b.few, s);
     const T *dz = (const T *)a.dy;
     long long lddz = a.lddy;
     float alpha = a.alpha;
-    form = form && (a.dx || a.dw);
+    const bool form = b.form && (a.dx || a.dw);
     const int Np = sizeof(T) == 2 ? pad8(a.N) : a.N;   // a row of dz in the workspace
     if (form || a.db) {
         const int chunk = row_chunk(a.M, a.N), chunks = ceil_div(a.M, chunk);
@@ -504,11 +335,11 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
     }
     const void *x = a.x, *w = a.w;
     long long ldx = a.ldx, ldw = a.ldw;
-    if (direct && copy_x + copy_w) {
-        const Padded p = pad(a.x, a.ldx, copy_x, a.w, a.ldw, copy_w, a.K, ws, s);
+    if (b.copy_x || b.copy_w) {
+        const Padded p = pad(a.x, a.ldx, b.copy_x ? a.M : 0, a.w, a.ldw, b.copy_w ? a.N : 0, a.K, ws, s);
         if (p.e != hipSuccess) return p.e;
-        if (copy_x) x = p.x, ldx = pad8(a.K);
-        if (copy_w) w = p.w, ldw = pad8(a.K);
+        if (b.copy_x) x = p.x, ldx = pad8(a.K);
+        if (b.copy_w) w = p.w, ldw = pad8(a.K);
     }
     Args P{};
     P.a = dz, P.lda = lddz;
@@ -517,13 +348,13 @@ hipError_t backward(const DenseBackward &a, const DenseWorkspace &ws, hipStream_
         P.b = w, P.ldb = ldw;
         P.I = a.M, P.J = a.K, P.K = a.N;
         P.c = a.dx, P.ldc = a.lddx;
-        if ((e = run_product<T>(P, K_ROWS, K_COLS, cx, direct, ws, s)) != hipSuccess) return e;
+        if ((e = run_product<T>(P, K_ROWS, K_COLS, b.dx, b.direct, ws, s)) != hipSuccess) return e;
     }
     if (a.dw) {
         P.b = x, P.ldb = ldx;
         P.I = a.N, P.J = a.K, P.K = a.M;
         P.c = a.dw, P.ldc = a.K;
-        if ((e = run_product<T>(P, K_COLS, K_COLS, cw, direct, ws, s)) != hipSuccess) return e;
+        if ((e = run_product<T>(P, K_COLS, K_COLS, b.dw, b.direct, ws, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }

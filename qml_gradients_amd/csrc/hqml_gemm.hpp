@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "hqml_act.hpp"
+#include "hqml_dense_cut.hpp"
 
 namespace hqml {
 namespace gemm {
@@ -1048,10 +1049,6 @@ __global__ __launch_bounds__(512) void k_small_gradients(Args dx, Args dw)
     if (id < tx) small_gradient<T, FI, K_ROWS>(dx, id, small_lds);
     else small_gradient<T, FI, K_COLS>(dw, id - tx, small_lds);
 }
-
-// Tile shapes a product can be run with.
-enum Shape { TILE_64, TILE_128, TILE_256, TILE_64x32, TILE_32x64 };
-constexpr int kSides[][2] = {{64, 64}, {128, 128}, {256, 256}, {64, 32}, {32, 64}};   // rows, columns
 
 // The kernels of one operand type, for a layout pair (K_ROWS, K_ROWS), (K_ROWS, K_COLS) or
 // (K_COLS, K_COLS).  direct: both bf16 operands' rows allow 16-byte access to LDS; TILE_256 needs it.
