@@ -220,15 +220,14 @@ int row_chunk(int M, int N)
 template <typename T>
 __global__ void k_zero(T *p, long long n)
 {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i < n) p[i] = T{};
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256) p[i] = T{};
 }
 
 template <typename T>
 hipError_t zero(void *p, long long n, hipStream_t s)
 {
     if (!p) return hipSuccess;
-    k_zero<T><<<(unsigned)((n + 255) / 256), 256, 0, s>>>((T *)p, n);
+    k_zero<T><<<(unsigned)std::min<long long>((n + 255) / 256, 1 << 16), 256, 0, s>>>((T *)p, n);   // a grid has fewer than 2^32 threads
     return hipGetLastError();
 }
 

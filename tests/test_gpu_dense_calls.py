@@ -109,3 +109,19 @@ def test_out_marks_its_array_changed():
     layer.forward(x, w, out=out)
     with pytest.raises(RuntimeError):
         loss.backward()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_empty_batch_of_a_layer_of_2_to_the_32_weights(dtype):
+    """Its dw is zeros like any other's."""
+    import qml_gradients_amd as hq
+    K = N = 1 << 16
+    free, _ = torch.cuda.mem_get_info()
+    if free < 24 << 30:
+        pytest.skip("needs 24 GiB of free device memory")
+    layer = hq.Dense(K, N, 4, dtype=dtype)
+    dw = torch.ones(N, K, dtype=layer.dtype, device="cuda")
+    db = torch.ones(N, dtype=layer.dtype, device="cuda")
+    hq.hqml_dense_backward(layer.handle, 0, None, N, None, K, None, K, None, None, K, dw.data_ptr(), db.data_ptr())
+    assert not db.any() and int(torch.count_nonzero(dw[:2])) == 0 and int(torch.count_nonzero(dw[-2:])) == 0
+    assert int(sum(torch.count_nonzero(part) for part in dw.split(1 << 12))) == 0
