@@ -249,7 +249,8 @@ const char *hqml_dense_last_error(const hqml_dense *h);
  * be NULL; z is what hqml_dense_backward needs (with HQML_ACT_NONE it is not needed and not
  * written).  y may be the residual itself (same stride); otherwise outputs overlap no other
  * argument (HQML_ERR_ARG; neighbouring columns of one array do not overlap).  Sums are held in
- * fp32; with HQML_DTYPE_BF16 y is rounded once, to nearest even. */
+ * fp32, of operands exact from 1.5e-33 up and to 2^-134 below; with HQML_DTYPE_BF16 y is rounded
+ * once, to nearest even. */
 int hqml_dense_forward(hqml_dense *h, int M, const void *x, long long ldx, const void *w, long long ldw,
                        const void *bias, const void *residual, long long ldr, void *y, long long ldy,
                        float *z);

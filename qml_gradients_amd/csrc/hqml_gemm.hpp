@@ -639,8 +639,9 @@ struct Chunks {
 };
 
 // x as PLANES bf16 values each, chunk by chunk into LDS planes kPlane bytes apart.  A 32-bit value is the
-// sum of its planes to 8 bits and a rounding a plane (exactly, with three, where none
-// underflows): x = h + m + l, each the rounding of what the ones before leave.
+// sum of its planes to 8 bits and a rounding a plane: x = h + m + l, each the rounding of what the
+// ones before leave; exactly, with three, from 2^-109 (1.5e-33) up.  Below, the last planes fall under bf16's
+// smallest magnitude, 2^-133, and x is off by up to 2^-134.
 template <int PLANES, int kPlane>
 __device__ __forceinline__ void split(lds_char *dst, float (&x)[8])
 {

@@ -101,3 +101,18 @@ def test_a_diverged_layer_keeps_its_speed():
     for name, got in (("one sample", sample), ("one weight", weight), ("all", whole)):
         say(f"[gpu] dense 2048^3 fp32, {name} NaN: {got[0] / plain[0]:.1f} and {got[1] / plain[1]:.1f} times the finite step")
         assert got[0] <= 12 * plain[0] and got[1] <= 12 * plain[1], name
+
+
+@pytest.mark.parametrize("size", [1e-30, 1e-33, 1e-35, 1e-37, 1e-40])
+def test_operands_near_the_smallest(size):
+    """Planes end at bf16's smallest magnitude, 2^-133, so on tiles an operand is off by up to 2^-134: nothing to one of
+    2^-109 (1.5e-33) or more, whose three planes hold all its bits."""
+    import qml_gradients_amd as hq
+    M, K, N = 2048, 512, 1030
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.rand(M, K, generator=g, device="cuda") + 0.5) * size
+    w = (torch.rand(N, K, generator=g, device="cuda") - 0.5) * 1e20
+    y = hq.Dense(K, N, M).forward(x, w).double()
+    a, b = x.double(), w.double().t().contiguous()
+    bound = (K + 8) * E * (a.abs() @ b.abs()) + (2.0 ** -134 if size < 2e-33 else 0.0) * b.abs().sum(0)
+    assert bool(((y - a @ b).abs() <= bound).all())
