@@ -607,13 +607,9 @@ struct Chunks {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int o = at[n] + e < stop ? off[n] + e * kSize : 0x7FFFFFF0;
-                if (kSize == 4) {
-                    reg[n][e % kWords] = __builtin_amdgcn_raw_buffer_load_b32(rsrc, o, 0, 0);
-                } else {
-                    const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
-                    if (e & 1) reg[n][e / 2] |= v << 16;
-                    else reg[n][e / 2] = v;
-                }
+                const uint32_t v = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rsrc, o, 0, 0);
+                if (e & 1) reg[n][e / 2] |= v << 16;
+                else reg[n][e / 2] = v;
             }
         }
     }
@@ -895,8 +891,9 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
 // matrix instructions only, so LDS would add a trip and save nothing), kAt steps of 32 k
 // before the first is used; the waves' sums meet in LDS and are added in their order.
 // fp32, and dz formed in fp32, use the fp32 matrix instruction: nothing is rounded or split.
-// Bound by the waits for memory: fp32 1 x 64 -> 4 takes 3.5 us, 1000 x 784 -> 20 6.2, bf16 1 x 4096 -> 4096 8.4
-// (32 MB of weights from HBM, 4.0 TB/s); all gradients of 64 x 12 -> 64 6.3.
+// Bound by the waits for memory: fp32 1 x 64 -> 4 takes 3.5 us, 1000 x 784 -> 20 6.2, bf16 1 x 4096 -> 4096 in a loop
+// of calls 8.0 with its 32 MB of weights in the last-level cache (4.2 TB/s) and 10.1 from HBM (3.3; 24 such weights in turn);
+// all gradients of 64 x 12 -> 64 6.3.
 
 // dz of a piece: dy, scaled by act'(z) (alpha is the epilogue's); without an activation, dy alone.
 template <typename T, int L>
