@@ -417,6 +417,7 @@ class Dense:
     [M][out_features], M <= max_batch.  Rows may be strided (a slice of columns is used in
     place); other layouts are copied.  Work is queued on the stream the handle was made on (or
     `stream`); a call from another current stream waits for that one and is waited for by it.
+    A graph can capture calls of a handle made on any stream but the default one.
     """
 
     def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0,
@@ -476,6 +477,10 @@ class Dense:
             rc = call(self.handle, *args)
         else:
             cuda = self.torch.cuda
+            if not self.stream and cuda.is_current_stream_capturing():
+                # the default stream takes no part in a capture, and must not wait for a stream that does
+                raise RuntimeError("a handle made on the default stream cannot be captured: make it on the stream of "
+                                   "the capture, or on any but the default one")
             here = cuda.current_stream(self.device)
             own = (cuda.ExternalStream(self.stream, device=self.device) if self.stream
                    else cuda.default_stream(self.device))

@@ -125,3 +125,20 @@ def test_empty_batch_of_a_layer_of_2_to_the_32_weights(dtype):
     hq.hqml_dense_backward(layer.handle, 0, None, N, None, K, None, K, None, None, K, dw.data_ptr(), db.data_ptr())
     assert not db.any() and int(torch.count_nonzero(dw[:2])) == 0 and int(torch.count_nonzero(dw[-2:])) == 0
     assert int(sum(torch.count_nonzero(part) for part in dw.split(1 << 12))) == 0
+
+
+def test_capture_of_a_handle_on_the_default_stream_is_refused():
+    """Before anything is queued: the capture goes on, and so does the handle."""
+    import qml_gradients_amd as hq
+    x, w = torch.randn(8, 16, device="cuda"), torch.randn(12, 16, device="cuda")
+    layer = hq.Dense(16, 12, 8, stream=0)
+    want = layer.forward(x, w)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph, stream=side):
+        twice = x * 2.0
+        with pytest.raises(RuntimeError, match="default stream"):
+            layer.forward(x, w)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(twice, x * 2.0) and torch.equal(layer.forward(x, w), want)
