@@ -142,3 +142,28 @@ def test_capture_of_a_handle_on_the_default_stream_is_refused():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(twice, x * 2.0) and torch.equal(layer.forward(x, w), want)
+
+
+def test_capture_of_a_handle_on_another_stream():
+    """Its stream joins the capture; replays, with eager work between, match eager calls."""
+    import qml_gradients_amd as hq
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+    M, K, N = 130, 300, 70
+    layer = hq.Dense(K, N, M, activation="gelu", stream=own.cuda_stream)
+    x, w, dy = (torch.randn(*s, device="cuda") for s in ((M, K), (N, K), (M, N)))
+    layer.forward(x, w)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y, z = layer.forward_train(x, w)
+        held = (y, *layer.backward(dy, x, w, z))
+    for seed in (1, 2, 3):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for t in (x, w, dy):
+            t.copy_(torch.randn(t.shape, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        y, z = layer.forward_train(x, w)
+        assert all(torch.equal(a, b) for a, b in zip(got, (y, *layer.backward(dy, x, w, z))))
+        torch.cuda.synchronize()
