@@ -436,7 +436,13 @@ class Dense:
         self._index, self._lib = dev, load()
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self.handle = None
-        self.handle = hqml_dense_create(self.cfg)
+        try:
+            self.handle = hqml_dense_create(self.cfg)
+        except HqmlError as e:
+            if e.status != HQML_ERR_OOM:
+                raise
+            torch.cuda.empty_cache()   # torch may hold what the workspace needs, unused
+            self.handle = hqml_dense_create(self.cfg)
 
     def close(self):
         if self.handle is not None:

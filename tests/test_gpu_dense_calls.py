@@ -167,3 +167,29 @@ def test_capture_of_a_handle_on_another_stream():
         y, z = layer.forward_train(x, w)
         assert all(torch.equal(a, b) for a, b in zip(got, (y, *layer.backward(dy, x, w, z))))
         torch.cuda.synchronize()
+
+
+def test_workspace_takes_what_torch_keeps_unused(monkeypatch):
+    """Memory that torch's allocator holds and nobody uses is given back before a layer is refused for want of it."""
+    import qml_gradients_amd as hq
+    create, freed, fail = hq.hqml_dense_create, [], [1]
+
+    def short(cfg):
+        if fail[0]:
+            fail[0] -= 1
+            raise hq.HqmlError(hq.HQML_ERR_OOM, "workspace")
+        return create(cfg)
+
+    monkeypatch.setattr(hq, "hqml_dense_create", short)
+    empty = torch.cuda.empty_cache
+    monkeypatch.setattr(torch.cuda, "empty_cache", lambda: (freed.append(1), empty()))
+    layer = hq.Dense(16, 12, 8)
+    assert freed and layer.forward(torch.ones(8, 16, device="cuda"), torch.ones(12, 16, device="cuda"))[0, 0] == 16
+    fail[0] = 2     # still none: refused
+    with pytest.raises(hq.HqmlError) as e:
+        hq.Dense(16, 12, 8)
+    assert e.value.status == hq.HQML_ERR_OOM and not fail[0]
+    with pytest.raises(hq.HqmlError):   # other errors are not tried again
+        freed.clear()
+        hq.Dense(0, 12, 8)
+    assert not freed
