@@ -69,10 +69,12 @@ __device__ __forceinline__ void tile_of(int id, int ti, int tj, int &i, int &j)
     j = in / rows;
 }
 
-// vmcnt(n): at most n of this wave's loads are still under way.
+// vmcnt(n): at most n of this wave's loads and stores are still under way.  The builtin alone says nothing of memory: the
+// compiler might move one past it.
 template <int n>
 __device__ __forceinline__ void wait_loads()
 {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt((n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
