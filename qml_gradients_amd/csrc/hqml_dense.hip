@@ -119,8 +119,10 @@ constexpr int kSlopeCols = 256;   // columns of a workgroup: 32 lanes of eight; 
 
 // dz = alpha act'(z) dy (written, if dz is not null, in rows of lddz: N, or the next multiple of eight) and its sums
 // over `chunk` rows.  Bound by memory (8192 x 4096 bf16: 268 MB in 55 us, 4.9 TB/s); 16 bytes at any alignment, single
-// values where a row ends.  The sums take dz before it is rounded to its type (bf16: the matrix cores take it so) and
-// leave as one row a chunk, so that no atomic's order changes them.
+// values where a row ends.  The sums take dz before it is rounded to its type and leave as one row a chunk, so that no
+// atomic's order changes them.  In bf16 that is the one rounding that a form in 32 bits has not: the matrix cores take
+// bf16, and a second plane for the rest of dz would double both products (196 and 184 us at that size).  It makes dx and dw
+// 0.0024 off in the norm where the results' own rounding makes them 0.0017.
 template <typename T>
 __global__ __launch_bounds__(256) void k_slope(const T *dy, long long lddy, const float *z, T *dz, int lddz, float *rows,
                                                int M, int N, int chunk, int act, float alpha)

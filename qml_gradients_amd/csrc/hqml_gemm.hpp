@@ -405,8 +405,9 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
 // barrier of a step stands in its middle: it makes step t + 1 readable and frees the
 // buffer of step t - 1, into which the loads of step t + 3 go out one after each row block (all
 // at once, they would hold up the wave's matrix instructions behind them).
-// 8192 x 4096 x 4096 at 256 x 256 tiles, by layout pair: 218, 206 and 200 us (1264, 1332 and
-// 1377 TFLOP/s), with two buffers of 64 k 228-257; the matrix instructions alone take 135.
+// 8192 x 4096 x 4096 at 256 x 256 tiles, by layout pair: 201-218, 196-206 and 182-200 us, card to
+// card (1264-1370, 1332-1403 and 1377-1510 TFLOP/s), with two buffers of 64 k 228-257; the matrix
+// instructions alone take 135.
 
 // What a wave of k_product_direct holds.
 template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
@@ -874,8 +875,9 @@ struct Staged {
 };
 
 // Bound by LDS, the matrix cores and the split's arithmetic about equally (a step of two workgroups on a compute unit:
-// 2.5 us; its LDS traffic alone 1.4, its matrix instructions 1.4, its split 0.9).  2048^3 in fp32: 94 us, 183 TFLOP/s;
-// 4096^3: 655 us, 210 TFLOP/s.
+// 2.5 us; its LDS traffic alone 1.4, its matrix instructions 1.4, its split 0.9).  2048^3 in fp32, each product alone in
+// a loop: forward 95 to 100 us, dx and dw 88 to 90 (171 to 193 TFLOP/s); one after another in a training step's kernel
+// trace, with bias, residual and z: 109 to 111, 98 to 100 and 101 to 103.  4096^3: 640 to 655 us, 210 TFLOP/s.
 template <typename T, int PLANES, int LA, int LB, int BM, int BN, int WI, int WJ, int BUF>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_staged(Args P)
 {
