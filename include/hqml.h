@@ -274,14 +274,15 @@ typedef enum {
                                    [ceil(numel / HQML_ADAMW_BLOCK)].  scale = max(largest
                                    magnitude of the block / 448, 2^-100); the code is the nearest
                                    to x / scale (ties to even), at least the smallest one, 2^-9,
-                                   for x != 0: a root that became 0 under a moment that did not
-                                   would divide by eps.  A NaN or infinite gradient makes its
-                                   whole block's moments NaN.  Nearest codes do not creep: with
-                                   beta2 = 0.999 a root loses 0.05 % a step, less than half a code's
-                                   distance, so one that is not its block's largest stays where it is
-                                   until the block's scale moves (gradients that fall a hundredfold under a
-                                   largest that does not: after 5,000 steps the kept roots are 9 times
-                                   too large, after 8,000 38 times).  fp32 and bf16 parameters */
+                                   where x / scale != 0 in fp32: a root that became 0 under a moment
+                                   that did not would divide by eps.  A NaN or infinite gradient
+                                   makes its whole block's moments NaN.  Nearest codes do not creep:
+                                   with beta2 = 0.999 a root loses 0.05 % a step, less than half a
+                                   code's distance, so one that is not its block's largest stays
+                                   until the block's scale moves (gradients that fall a hundredfold
+                                   beside one that does not: the kept roots are 9 times too large
+                                   after 5,000 steps, 38 times after 8,000).  fp32 and bf16
+                                   parameters */
 } hqml_moments;
 #define HQML_ADAMW_BLOCK 256
 

@@ -229,7 +229,8 @@ template <typename T>
 hipError_t zero(void *p, long long n, hipStream_t s)
 {
     if (!p) return hipSuccess;
-    k_zero<T><<<(unsigned)std::min<long long>((n + 255) / 256, 1 << 16), 256, 0, s>>>((T *)p, n);   // a grid has fewer than 2^32 threads
+    // a grid has fewer than 2^32 threads
+    k_zero<T><<<(unsigned)std::min<long long>((n + 255) / 256, 1 << 16), 256, 0, s>>>((T *)p, n);
     return hipGetLastError();
 }
 

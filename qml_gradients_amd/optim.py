@@ -26,9 +26,10 @@ class AdamW(torch.optim.Optimizer):
     (state_bits=32 only) fp64; a gradient may be bf16 for an fp32 parameter and the other way
     round.  state[p] holds "step" and, with state_bits=32, "exp_avg" and "exp_avg_sq"; with
     state_bits=8, "exp_avg" and "exp_avg_sq_root" (torch.float8_e4m3fn) and their scales under
-    the same names with "_scale" appended: value = code * scale of its 256 elements.  A root in 8 bits
-    falls only with its block's largest (its decay of a step is less than half a code), so parameters whose
-    gradients fade while others' of the same 256 do not keep too small a step: use 32 bits there.
+    the same names with "_scale" appended: value = code * scale of its 256 elements.  A root in 8
+    bits falls only with its block's largest (its decay in a step is less than half a code):
+    elements whose gradients fade while others' of the same 256 do not keep too small a step, and
+    are for 32 bits.
     The step runs on each device's current stream, which must not be under graph capture."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, state_bits=32):
