@@ -314,11 +314,129 @@ typedef struct {
  * is refused (HQML_ERR_UNSUPPORTED).  Errors: hqml_last_error(NULL). */
 int hqml_adamw_step(const hqml_adamw_config *cfg, int n_tensors, const hqml_adamw_tensor *tensors);
 
+/* ---- a dense layer in 8-bit integers, for serving ----
+ *
+ * Weights and inputs are held as codes of -127..127 times a scale for each row (output channel,
+ * sample): scale = max(largest magnitude of the row / 127, 2^-100), code = the nearest integer to
+ * x / scale (scale before it is rounded to fp32), ties to even.  A row with an infinity or a NaN
+ * gets the scale NaN and codes 0. */
+
+/* Largest in_features of the 8-bit layer: sums of 2^17 products of codes fit 32 bits. */
+#define HQML_DENSE8_MAX_IN (1 << 17)
+
+/* Codes [rows][K] (row stride ldc: a multiple of 16 of at least K, and codes 16-byte aligned) and
+ * scales [rows] of x [rows][K] (row stride ldx; dtype fp32 or bf16), queued on stream.  Codes past
+ * a row's last one, up to the next multiple of 16, are written as zeros.  1 <= K <= 2^20; rows == 0
+ * queues nothing.  Errors: hqml_last_error(NULL). */
+int hqml_quantise_rows(int device, void *stream, int dtype, long long rows, int K, const void *x,
+                       long long ldx, signed char *codes, long long ldc, float *scales);
+
+typedef struct hqml_dense8 hqml_dense8;
+
+/* As hqml_dense_workspace_bytes, _create, _destroy and _last_error; in_features up to
+ * HQML_DENSE8_MAX_IN.  The workspace holds x's codes and partial sums. */
+size_t hqml_dense8_workspace_bytes(const hqml_dense_config *cfg);
+int hqml_dense8_create(const hqml_dense_config *cfg, hqml_dense8 **out);
+int hqml_dense8_destroy(hqml_dense8 *h);
+const char *hqml_dense8_last_error(const hqml_dense8 *h);
+
+/* y = alpha act(x w^T + bias) + residual with x rounded to codes for each row and w given as
+ * codes [N][K] with row stride ldw as hqml_quantise_rows takes it (what its rows hold past K does
+ * not count, up to the next multiple of 16 it is read) and scales [N].  Everything else as
+ * hqml_dense_forward; there is no gradient.  Sums of products of codes are exact.  A row of
+ * x that is not finite gives a row of NaN. */
+int hqml_dense8_forward(hqml_dense8 *h, int M, const void *x, long long ldx, const signed char *codes,
+                        long long ldw, const float *scales, const void *bias, const void *residual,
+                        long long ldr, void *y, long long ldy);
+
+/* ---- group norm with an activation ---- */
+
+#define HQML_NORM_MAX_CHANNELS 4096
+#define HQML_NORM_MAX_ROWS (1 << 30)
+
+typedef struct hqml_norm hqml_norm;
+
+typedef struct {
+    int channels;      /* C, 1..HQML_NORM_MAX_CHANNELS */
+    int groups;        /* G, divides channels: groups of C / G neighbouring channels */
+    int max_rows;      /* 1..HQML_NORM_MAX_ROWS: the most positions of a call, over all its samples */
+    int dtype;         /* hqml_dtype of x, y, gamma, beta and the gradients: fp32 or bf16 */
+    int activation;    /* hqml_activation */
+    float eps;         /* finite, > 0 */
+    int device;
+    void *stream;
+} hqml_norm_config;
+
+/* As the dense layer's.  The workspace holds partial sums. */
+size_t hqml_norm_workspace_bytes(const hqml_norm_config *cfg);
+int hqml_norm_create(const hqml_norm_config *cfg, hqml_norm **out);
+int hqml_norm_destroy(hqml_norm *h);
+const char *hqml_norm_last_error(const hqml_norm *h);
+
+/* xhat = (x - mean) rstd, y = act(gamma xhat + beta), for B samples of S positions (B, S >= 0,
+ * B S <= max_rows; none queues nothing): x and y [B][S][C] with ldx and ldy elements from one
+ * position to the next, samples following each other without a gap; gamma and beta [C], NULL
+ * for 1 and 0.  mean and rstd = 1 / sqrt(var + eps), var the mean squared distance from the mean,
+ * are those of a sample's group over all its positions.  mean and rstd [B][G], fp32, are written
+ * unless both are NULL; hqml_norm_backward needs them.  y may be x itself (same stride);
+ * otherwise outputs overlap no other argument (HQML_ERR_ARG).  Statistics are held in fp32, the
+ * variance as the sum of squared distances from the mean; bf16 results are rounded once. */
+int hqml_norm_forward(hqml_norm *h, int B, int S, const void *x, long long ldx, const void *gamma,
+                      const void *beta, void *y, long long ldy, float *mean, float *rstd);
+
+/* Gradients of a forward call for dy = dL/dy: with z = gamma xhat + beta and dz = dy act'(z),
+ * dx = rstd (gamma dz - m1 - xhat m2), m1 and m2 the means over the group of gamma dz and
+ * gamma dz xhat; dgamma = sum of dz xhat, dbeta = sum of dz over samples and positions.  Each of dx,
+ * dgamma, dbeta may be NULL (not formed).  x, gamma, beta, mean and rstd are the forward call's.
+ * No positions: zeros to dgamma and dbeta.  Sums are held in fp32; bf16 results are rounded once. */
+int hqml_norm_backward(hqml_norm *h, int B, int S, const void *dy, long long lddy, const void *x,
+                       long long ldx, const void *gamma, const void *beta, const float *mean,
+                       const float *rstd, void *dx, long long lddx, void *dgamma, void *dbeta);
+
+/* ---- Muon: momentum and orthogonalised updates of weight matrices ---- */
+
+#define HQML_MUON_MAX_SIDE (1 << 16)
+#define HQML_MUON_MAX_STEPS 100
+
+typedef struct {
+    void *param;            /* [rows][cols], updated */
+    const void *grad;       /* [rows][cols] */
+    float *momentum;        /* [rows][cols], updated */
+    int rows, cols;         /* 0..HQML_MUON_MAX_SIDE; a matrix without elements is skipped */
+    double scale;           /* f: this matrix's factor of lr, finite, >= 0 */
+} hqml_muon_tensor;
+
+typedef struct {
+    int param_dtype;   /* hqml_dtype of param: fp32 or bf16 */
+    int grad_dtype;    /* hqml_dtype of grad: fp32 or bf16 */
+    int nesterov;
+    int steps;         /* 1..HQML_MUON_MAX_STEPS */
+    double lr, momentum, weight_decay, eps;   /* lr, weight_decay >= 0; momentum in [0, 1); eps > 0 */
+    double a, b, c;    /* coefficients of the polynomial, magnitudes up to 16 */
+    int device;
+    void *stream;
+} hqml_muon_config;
+
+/* Device bytes that hqml_muon_step needs at `workspace` (256-byte aligned).  Host-only; looks at the
+ * matrices' sizes alone.  Returns 0 for invalid arguments and where nothing is needed. */
+size_t hqml_muon_workspace_bytes(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors);
+
+/* One step over n_tensors matrices (mu = momentum):
+ *   m = mu m + (1 - mu) g,  u = nesterov ? mu m + (1 - mu) g : m,  X = u / max(|u|, eps) (Frobenius norm);
+ *   `steps` times, with A = X X^T:  X = a X + (b A + c A^2) X;  p = p (1 - lr weight_decay) - lr f X
+ * m in fp32.  The products take operands in fp16: one for each value where the parameters are bf16 (11
+ * bits), two for fp32 parameters (22 bits), sums in fp32; values of X, A or b A + c A^2 beyond 63
+ * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Matrices
+ * must not overlap.  The workspace is used until the step has run.  Errors: hqml_last_error(NULL). */
+int hqml_muon_step(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors,
+                   void *workspace, size_t workspace_bytes);
+
 /* Static text for a status code. */
 const char *hqml_status_str(int status);
 
 /* Text of the last error on ctx ("" if none); with ctx == NULL, the last error of
- * hqml_create, hqml_train_step_noalloc, hqml_dense_create or hqml_adamw_step on this thread. */
+ * hqml_create, hqml_train_step_noalloc, hqml_dense_create, hqml_dense8_create, hqml_norm_create,
+ * hqml_quantise_rows, hqml_adamw_step or hqml_muon_step on this thread. */
 const char *hqml_last_error(const hqml_ctx *ctx);
 
 /* ---- instrumentation (benchmarking; not needed for training) ---- */

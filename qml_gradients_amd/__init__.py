@@ -37,6 +37,11 @@ HQML_DENSE_MAX_BATCH = 1 << 24
 HQML_MOMENTS_32 = 0
 HQML_MOMENTS_8 = 1
 HQML_ADAMW_BLOCK = 256
+HQML_DENSE8_MAX_IN = 1 << 17
+HQML_NORM_MAX_CHANNELS = 4096
+HQML_NORM_MAX_ROWS = 1 << 30
+HQML_MUON_MAX_SIDE = 1 << 16
+HQML_MUON_MAX_STEPS = 100
 HQML_K_FWD_PASS, HQML_K_BWD_PASS, HQML_K_SMALL, HQML_K_OTHER, HQML_K_GATE, HQML_K_COUNT = range(6)
 
 
@@ -98,6 +103,48 @@ class hqml_adamw_config(ctypes.Structure):
     ]
 
 
+class hqml_norm_config(ctypes.Structure):
+    _fields_ = [
+        ("channels", ctypes.c_int),
+        ("groups", ctypes.c_int),
+        ("max_rows", ctypes.c_int),
+        ("dtype", ctypes.c_int),
+        ("activation", ctypes.c_int),
+        ("eps", ctypes.c_float),
+        ("device", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class hqml_muon_tensor(ctypes.Structure):
+    _fields_ = [
+        ("param", ctypes.c_void_p),
+        ("grad", ctypes.c_void_p),
+        ("momentum", ctypes.c_void_p),
+        ("rows", ctypes.c_int),
+        ("cols", ctypes.c_int),
+        ("scale", ctypes.c_double),
+    ]
+
+
+class hqml_muon_config(ctypes.Structure):
+    _fields_ = [
+        ("param_dtype", ctypes.c_int),
+        ("grad_dtype", ctypes.c_int),
+        ("nesterov", ctypes.c_int),
+        ("steps", ctypes.c_int),
+        ("lr", ctypes.c_double),
+        ("momentum", ctypes.c_double),
+        ("weight_decay", ctypes.c_double),
+        ("eps", ctypes.c_double),
+        ("a", ctypes.c_double),
+        ("b", ctypes.c_double),
+        ("c", ctypes.c_double),
+        ("device", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
 class HqmlError(RuntimeError):
     def __init__(self, status: int, message: str):
         super().__init__(f"hqml status {status}: {message}")
@@ -121,6 +168,8 @@ def load() -> ctypes.CDLL:
     ll = ctypes.c_longlong
     cfgp = ctypes.POINTER(hqml_config)
     densep = ctypes.POINTER(hqml_dense_config)
+    normp = ctypes.POINTER(hqml_norm_config)
+    muonp, matrixp = ctypes.POINTER(hqml_muon_config), ctypes.POINTER(hqml_muon_tensor)
     sig = {
         "hqml_workspace_bytes": (ctypes.c_size_t, [cfgp]),
         "hqml_create": (i, [cfgp, ctypes.POINTER(P)]),
@@ -147,6 +196,20 @@ def load() -> ctypes.CDLL:
         "hqml_dense_forward": (i, [P, i, P, ll, P, ll, P, P, ll, P, ll, P]),
         "hqml_dense_backward": (i, [P, i, P, ll, P, ll, P, ll, P, P, ll, P, P]),
         "hqml_adamw_step": (i, [ctypes.POINTER(hqml_adamw_config), i, P]),
+        "hqml_quantise_rows": (i, [i, P, i, ll, i, P, ll, P, ll, P]),
+        "hqml_dense8_workspace_bytes": (ctypes.c_size_t, [densep]),
+        "hqml_dense8_create": (i, [densep, ctypes.POINTER(P)]),
+        "hqml_dense8_destroy": (i, [P]),
+        "hqml_dense8_last_error": (ctypes.c_char_p, [P]),
+        "hqml_dense8_forward": (i, [P, i, P, ll, P, ll, P, P, P, ll, P, ll]),
+        "hqml_norm_workspace_bytes": (ctypes.c_size_t, [normp]),
+        "hqml_norm_create": (i, [normp, ctypes.POINTER(P)]),
+        "hqml_norm_destroy": (i, [P]),
+        "hqml_norm_last_error": (ctypes.c_char_p, [P]),
+        "hqml_norm_forward": (i, [P, i, i, P, ll, P, P, P, ll, P, P]),
+        "hqml_norm_backward": (i, [P, i, i, P, ll, P, ll, P, P, P, P, P, ll, P, P]),
+        "hqml_muon_workspace_bytes": (ctypes.c_size_t, [muonp, i, matrixp]),
+        "hqml_muon_step": (i, [muonp, i, matrixp, P, ctypes.c_size_t]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -160,7 +223,11 @@ EXPORTED = ("hqml_workspace_bytes", "hqml_create", "hqml_destroy", "hqml_forward
             "hqml_train_step", "hqml_forward_f64", "hqml_backward_f64", "hqml_train_step_f64", "hqml_status_str", "hqml_last_error", "hqml_set_timing",
             "hqml_set_overlap", "hqml_kernel_times", "hqml_plan_info", "hqml_describe_plan",
             "hqml_train_step_noalloc", "hqml_dense_workspace_bytes", "hqml_dense_create", "hqml_dense_destroy",
-            "hqml_dense_last_error", "hqml_dense_forward", "hqml_dense_backward", "hqml_adamw_step")
+            "hqml_dense_last_error", "hqml_dense_forward", "hqml_dense_backward", "hqml_adamw_step",
+            "hqml_quantise_rows", "hqml_dense8_workspace_bytes", "hqml_dense8_create", "hqml_dense8_destroy",
+            "hqml_dense8_last_error", "hqml_dense8_forward", "hqml_norm_workspace_bytes", "hqml_norm_create",
+            "hqml_norm_destroy", "hqml_norm_last_error", "hqml_norm_forward", "hqml_norm_backward",
+            "hqml_muon_workspace_bytes", "hqml_muon_step")
 
 
 def make_config(n_qubits, n_layers, max_batch, storage="fp32", ckpt_block=0, device=0, stream=None,
@@ -184,6 +251,12 @@ def make_dense_config(in_features, out_features, max_batch, dtype="fp32", activa
     return hqml_dense_config(int(in_features), int(out_features), int(max_batch), int(DENSE_DTYPES.get(dtype, dtype)),
                              int(ACTIVATIONS.get(activation, activation)), float(alpha), int(device),
                              ctypes.c_void_p(stream or 0))
+
+
+def make_norm_config(channels, groups, max_rows, dtype="fp32", activation="none", eps=1e-5, device=0, stream=None):
+    return hqml_norm_config(int(channels), int(groups), int(max_rows), int(DENSE_DTYPES.get(dtype, dtype)),
+                            int(ACTIVATIONS.get(activation, activation)), float(eps), int(device),
+                            ctypes.c_void_p(stream or 0))
 
 
 # ---- the C entry points, same names, argument marshalling only ----
@@ -288,6 +361,85 @@ def hqml_adamw_step(cfg: hqml_adamw_config, n_tensors, tensors) -> None:
     """tensors: a ctypes array of hqml_adamw_tensor, or of as many 64-bit words."""
     lib = load()
     rc = lib.hqml_adamw_step(ctypes.byref(cfg), int(n_tensors), tensors)
+    if rc != HQML_OK:
+        raise HqmlError(rc, lib.hqml_last_error(None).decode())
+
+
+def hqml_quantise_rows(device, stream, dtype, rows, K, x_ptr, ldx, codes_ptr, ldc, scales_ptr) -> None:
+    lib = load()
+    rc = lib.hqml_quantise_rows(device, stream, dtype, rows, K, x_ptr, ldx, codes_ptr, ldc, scales_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, lib.hqml_last_error(None).decode())
+
+
+def _created(create, cfg) -> ctypes.c_void_p:
+    h = ctypes.c_void_p()
+    rc = create(ctypes.byref(cfg), ctypes.byref(h))
+    if rc != HQML_OK:
+        raise HqmlError(rc, load().hqml_last_error(None).decode())
+    return h
+
+
+def hqml_dense8_workspace_bytes(cfg: hqml_dense_config) -> int:
+    return int(load().hqml_dense8_workspace_bytes(ctypes.byref(cfg)))
+
+
+def hqml_dense8_create(cfg: hqml_dense_config) -> ctypes.c_void_p:
+    return _created(load().hqml_dense8_create, cfg)
+
+
+def hqml_dense8_destroy(h) -> None:
+    load().hqml_dense8_destroy(h)
+
+
+def hqml_dense8_last_error(h) -> str:
+    return load().hqml_dense8_last_error(h).decode()
+
+
+def hqml_dense8_forward(h, M, x_ptr, ldx, codes_ptr, ldw, scales_ptr, bias_ptr, residual_ptr, ldr, y_ptr, ldy) -> None:
+    rc = load().hqml_dense8_forward(h, M, x_ptr, ldx, codes_ptr, ldw, scales_ptr, bias_ptr, residual_ptr, ldr, y_ptr, ldy)
+    if rc != HQML_OK:
+        raise HqmlError(rc, hqml_dense8_last_error(h))
+
+
+def hqml_norm_workspace_bytes(cfg: hqml_norm_config) -> int:
+    return int(load().hqml_norm_workspace_bytes(ctypes.byref(cfg)))
+
+
+def hqml_norm_create(cfg: hqml_norm_config) -> ctypes.c_void_p:
+    return _created(load().hqml_norm_create, cfg)
+
+
+def hqml_norm_destroy(h) -> None:
+    load().hqml_norm_destroy(h)
+
+
+def hqml_norm_last_error(h) -> str:
+    return load().hqml_norm_last_error(h).decode()
+
+
+def hqml_norm_forward(h, B, S, x_ptr, ldx, gamma_ptr, beta_ptr, y_ptr, ldy, mean_ptr, rstd_ptr) -> None:
+    rc = load().hqml_norm_forward(h, B, S, x_ptr, ldx, gamma_ptr, beta_ptr, y_ptr, ldy, mean_ptr, rstd_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, hqml_norm_last_error(h))
+
+
+def hqml_norm_backward(h, B, S, dy_ptr, lddy, x_ptr, ldx, gamma_ptr, beta_ptr, mean_ptr, rstd_ptr, dx_ptr, lddx, dgamma_ptr,
+                       dbeta_ptr) -> None:
+    rc = load().hqml_norm_backward(h, B, S, dy_ptr, lddy, x_ptr, ldx, gamma_ptr, beta_ptr, mean_ptr, rstd_ptr, dx_ptr, lddx,
+                                   dgamma_ptr, dbeta_ptr)
+    if rc != HQML_OK:
+        raise HqmlError(rc, hqml_norm_last_error(h))
+
+
+def hqml_muon_workspace_bytes(cfg: hqml_muon_config, n_tensors, tensors) -> int:
+    """tensors: a ctypes array of hqml_muon_tensor."""
+    return int(load().hqml_muon_workspace_bytes(ctypes.byref(cfg), int(n_tensors), tensors))
+
+
+def hqml_muon_step(cfg: hqml_muon_config, n_tensors, tensors, workspace_ptr, workspace_bytes) -> None:
+    lib = load()
+    rc = lib.hqml_muon_step(ctypes.byref(cfg), int(n_tensors), tensors, workspace_ptr, int(workspace_bytes))
     if rc != HQML_OK:
         raise HqmlError(rc, lib.hqml_last_error(None).decode())
 
@@ -409,19 +561,11 @@ class Context:
         return hqml_plan_info(self.handle)
 
 
-class Dense:
-    """One dense layer's handle: y = alpha act(x w^T + bias) + residual and its gradients.
+class _Layer:
+    """What the handles of dense layers and norms share: the device, the stream, the call's queueing and its arrays."""
 
-    Tensors are torch CUDA tensors of the handle's device and dtype ("fp32" or "bf16"):
-    x [M][in_features], w [out_features][in_features], bias [out_features], residual and y
-    [M][out_features], M <= max_batch.  Rows may be strided (a slice of columns is used in
-    place); other layouts are copied.  Work is queued on the stream the handle was made on (or
-    `stream`); a call from another current stream waits for that one and is waited for by it.
-    A graph can capture calls of a handle made on any stream but the default one.
-    """
-
-    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0,
-                 device=None, stream=None):
+    def _open(self, device, stream):
+        """The handle's device, and the stream it is made on."""
         import torch
         if not torch.cuda.is_available():
             raise RuntimeError("hqml needs a GPU (torch.cuda.is_available() is False)")
@@ -429,24 +573,24 @@ class Dense:
         self.torch = torch
         self.device = torch.device("cuda", dev)
         self.stream = torch.cuda.current_stream(dev).cuda_stream if stream is None else int(stream)
-        self.K, self.N, self.max_batch = int(in_features), int(out_features), int(max_batch)
-        self.cfg = make_dense_config(in_features, out_features, max_batch, dtype, activation, alpha, dev, self.stream)
-        self.dtype = torch.bfloat16 if self.cfg.dtype == HQML_DTYPE_BF16 else torch.float32
-        self.plain = self.cfg.activation == HQML_ACT_NONE   # the gradient needs no z
         self._index, self._lib = dev, load()
         self._current_stream = torch._C._cuda_getCurrentRawStream
         self.handle = None
+        return dev
+
+    def _make(self, create):
+        self.dtype = self.torch.bfloat16 if self.cfg.dtype == HQML_DTYPE_BF16 else self.torch.float32
         try:
-            self.handle = hqml_dense_create(self.cfg)
+            self.handle = create(self.cfg)
         except HqmlError as e:
             if e.status != HQML_ERR_OOM:
                 raise
-            torch.cuda.empty_cache()   # torch may hold what the workspace needs, unused
-            self.handle = hqml_dense_create(self.cfg)
+            self.torch.cuda.empty_cache()   # torch may hold what the workspace needs, unused
+            self.handle = create(self.cfg)
 
     def close(self):
         if self.handle is not None:
-            hqml_dense_destroy(self.handle)
+            self._destroy(self.handle)
             self.handle = None
 
     def __del__(self):
@@ -494,7 +638,29 @@ class Dense:
             rc = call(self.handle, *args)
             here.wait_stream(own)
         if rc != HQML_OK:
-            raise HqmlError(rc, hqml_dense_last_error(self.handle))
+            raise HqmlError(rc, self._error(self.handle))
+
+
+class Dense(_Layer):
+    """One dense layer's handle: y = alpha act(x w^T + bias) + residual and its gradients.
+
+    Tensors are torch CUDA tensors of the handle's device and dtype ("fp32" or "bf16"):
+    x [M][in_features], w [out_features][in_features], bias [out_features], residual and y
+    [M][out_features], M <= max_batch.  Rows may be strided (a slice of columns is used in
+    place); other layouts are copied.  Work is queued on the stream the handle was made on (or
+    `stream`); a call from another current stream waits for that one and is waited for by it.
+    A graph can capture calls of a handle made on any stream but the default one.
+    """
+
+    _destroy, _error = staticmethod(hqml_dense_destroy), staticmethod(hqml_dense_last_error)
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0,
+                 device=None, stream=None):
+        dev = self._open(device, stream)
+        self.K, self.N, self.max_batch = int(in_features), int(out_features), int(max_batch)
+        self.cfg = make_dense_config(in_features, out_features, max_batch, dtype, activation, alpha, dev, self.stream)
+        self.plain = self.cfg.activation == HQML_ACT_NONE   # the gradient needs no z
+        self._make(hqml_dense_create)
 
     def _forward(self, x, w, bias, residual, out, keep):
         M = x.shape[0]
@@ -550,4 +716,179 @@ class Dense:
         self._queue(self._lib.hqml_dense_backward, M, dy.data_ptr(), lddy, x.data_ptr(), ldx, w.data_ptr(), ldw,
                     None if self.plain else z.data_ptr(), dx.data_ptr() if input else None, self.K,
                     dw.data_ptr() if weight else None, db.data_ptr() if bias else None)
+        return dx, dw, db
+
+
+def quantise_rows(x):
+    """(codes, scales) of the rows of x, a CUDA tensor [rows][K] in fp32 or bf16: x ~ codes * scales[:, None], codes of
+    -127..127 in int8, scales in fp32.  The codes' rows are a multiple of 16 apart, as DenseInt8 takes them.  Runs on the
+    current stream of x's device."""
+    import torch
+    if x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16) or not x.is_cuda:
+        raise TypeError(f"x must be a CUDA matrix in fp32 or bf16, got {x.dtype} {tuple(x.shape)} on {x.device}")
+    rows, K = x.shape
+    if K < 1:
+        raise ValueError("rows must not be empty")
+    x = x.detach()
+    ldx = x.stride(0)
+    if (K > 1 and x.stride(1) != 1) or (rows > 1 and not K <= ldx <= HQML_DENSE_MAX_FEATURES):
+        x = x.contiguous()
+        ldx = K
+    Kp = -(-K // 16) * 16
+    codes = torch.empty((rows, Kp), dtype=torch.int8, device=x.device)
+    scales = torch.empty(rows, dtype=torch.float32, device=x.device)
+    dtype = HQML_DTYPE_BF16 if x.dtype is torch.bfloat16 else HQML_DTYPE_FP32
+    device = x.get_device()
+    hqml_quantise_rows(device, torch._C._cuda_getCurrentRawStream(device), dtype, rows, K, x.data_ptr(),
+                       ldx if rows > 1 else K, codes.data_ptr(), Kp, scales.data_ptr())
+    return codes[:, :K], scales
+
+
+class DenseInt8(_Layer):
+    """A dense layer served in 8-bit integers: y = alpha act(x w^T + bias) + residual with w given as codes and scales
+    (quantise_rows) and x rounded to codes within the call, a scale for each of its rows.
+
+    x, bias, residual and y as Dense's, in fp32 or bf16; codes [out_features][in_features] in int8, rows a multiple
+    of 16 apart (others are copied), scales [out_features] in fp32.  Streams and graphs as Dense's.  There is no gradient."""
+
+    _destroy, _error = staticmethod(hqml_dense8_destroy), staticmethod(hqml_dense8_last_error)
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0,
+                 device=None, stream=None):
+        dev = self._open(device, stream)
+        self.K, self.N, self.max_batch = int(in_features), int(out_features), int(max_batch)
+        self.cfg = make_dense_config(in_features, out_features, max_batch, dtype, activation, alpha, dev, self.stream)
+        self._make(hqml_dense8_create)
+
+    def _codes(self, codes):
+        """codes in rows that the kernels can load sixteen at a time, and the rows' distance."""
+        N, K, Kp = self.N, self.K, -(-self.K // 16) * 16
+        self._check(codes, (N, K), "codes", self.torch.int8)
+        ld = codes.stride(0) if N > 1 else Kp
+        if ((K == 1 or codes.stride(1) == 1) and ld % 16 == 0 and Kp <= ld <= HQML_DENSE_MAX_FEATURES
+                and codes.data_ptr() % 16 == 0
+                and codes.storage_offset() + (N - 1) * ld + Kp <= codes.untyped_storage().nbytes()):
+            return codes, ld
+        held = self.torch.zeros((N, Kp), dtype=self.torch.int8, device=self.device)
+        held[:, :K] = codes
+        return held, Kp
+
+    def forward(self, x, codes, scales, bias=None, residual=None, out=None):
+        """y.  `out` may be the residual itself; it must not overlap another argument."""
+        M = x.shape[0]
+        x, ldx = self._rows(x, M, self.K, "x")
+        codes, ldw = self._codes(codes)
+        self._check(scales, (self.N,), "scales", self.torch.float32)
+        scales = scales.contiguous()
+        if bias is not None:
+            self._check(bias, (self.N,), "bias", self.dtype)
+            bias = bias.contiguous()
+        ldr = 0
+        if residual is not None:
+            residual, ldr = self._rows(residual, M, self.N, "residual")
+        if out is None:
+            y, ldy = self._new(M, self.N, residual, ldr), self.N
+        else:
+            y, ldy = self._rows(out, M, self.N, "out")
+            if y is not out:
+                raise ValueError("out must have rows without gaps between their elements")
+        self._queue(self._lib.hqml_dense8_forward, M, x.data_ptr(), ldx, codes.data_ptr(), ldw, scales.data_ptr(),
+                    None if bias is None else bias.data_ptr(), None if residual is None else residual.data_ptr(), ldr,
+                    y.data_ptr(), ldy)
+        if out is not None:   # a backward pass that saved it from before has to refuse it
+            self.torch.autograd.graph.increment_version(out)
+        return y
+
+
+class GroupNorm(_Layer):
+    """Group norm with an activation, channels last: y = act(weight xhat + bias), xhat = (x - mean) rstd over a sample's
+    group of channels / groups neighbouring channels and all its positions.
+
+    x [samples][...positions][channels] in fp32 or bf16 (the handle's dtype), samples times positions up to max_rows;
+    weight and bias [channels] or None.  Positions may be strided evenly (a slice of channels is used in place); other
+    layouts are copied.  Streams and graphs as Dense's."""
+
+    _destroy, _error = staticmethod(hqml_norm_destroy), staticmethod(hqml_norm_last_error)
+
+    def __init__(self, channels, groups, max_rows, dtype="fp32", activation="none", eps=1e-5, device=None, stream=None):
+        dev = self._open(device, stream)
+        self.C, self.G, self.max_rows = int(channels), int(groups), int(max_rows)
+        self.cfg = make_norm_config(channels, groups, max_rows, dtype, activation, eps, dev, self.stream)
+        self._make(hqml_norm_create)
+
+    def _positions(self, t, shape, name):
+        """t with positions the kernels can walk, and their distance."""
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != shape:
+            self._check(t, tuple(shape), name, self.dtype)
+        if not t.is_contiguous():
+            rows = [(n, s) for n, s in zip(t.shape[:-1], t.stride()[:-1]) if n > 1]   # from the outermost in
+            ld = rows[-1][1] if rows else self.C
+            even = all(a[1] == b[0] * b[1] for a, b in zip(rows, rows[1:]))
+            if (self.C == 1 or t.stride(-1) == 1) and even and self.C <= ld <= HQML_DENSE_MAX_FEATURES:
+                return t, ld
+            t = t.contiguous()
+        return t, self.C
+
+    def _sizes(self, x):
+        if x.dim() < 2:
+            raise ValueError(f"expected [samples][...][{self.C}], got {tuple(x.shape)}")
+        shape, S = x.shape, 1
+        for n in shape[1:-1]:
+            S *= n
+        if shape[-1] != self.C:
+            raise ValueError(f"expected {self.C} channels, got {tuple(shape)}")
+        return shape, shape[0], S
+
+    def _parameter(self, t, name):
+        if t is None:
+            return None
+        self._check(t, (self.C,), name, self.dtype)
+        return t.contiguous()
+
+    def _forward(self, x, weight, bias, out, keep):
+        shape, B, S = self._sizes(x)
+        x, ldx = self._positions(x, shape, "x")
+        weight, bias = self._parameter(weight, "weight"), self._parameter(bias, "bias")
+        if out is None:
+            y, ldy = self.torch.empty(shape, dtype=self.dtype, device=self.device), self.C
+        else:
+            y, ldy = self._positions(out, shape, "out")
+            if y is not out:
+                raise ValueError("out must have evenly strided positions")
+        mean = rstd = None
+        if keep:
+            mean, rstd = self.torch.empty((2, B, self.G), dtype=self.torch.float32, device=self.device)
+        self._queue(self._lib.hqml_norm_forward, B, S, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(),
+                    None if bias is None else bias.data_ptr(), y.data_ptr(), ldy, mean.data_ptr() if keep else None,
+                    rstd.data_ptr() if keep else None)
+        if out is not None:   # a backward pass that saved it from before has to refuse it
+            self.torch.autograd.graph.increment_version(out)
+        return y, mean, rstd
+
+    def forward(self, x, weight=None, bias=None, out=None):
+        """y.  `out` may be x itself; it must not overlap another argument."""
+        return self._forward(x, weight, bias, out, False)[0]
+
+    def forward_train(self, x, weight=None, bias=None):
+        """(y, mean, rstd): mean and rstd [samples][groups], in fp32, are what backward needs."""
+        return self._forward(x, weight, bias, None, True)
+
+    def backward(self, dy, x, weight, bias, mean, rstd, input=True, parameters=True):
+        """(dx, dweight, dbias) for dy = dL/dy and the arguments and statistics of a forward_train call; those not asked
+        for are None."""
+        shape, B, S = self._sizes(x)
+        x, ldx = self._positions(x, shape, "x")
+        dy, lddy = self._positions(dy, shape, "dy")
+        weight, bias = self._parameter(weight, "weight"), self._parameter(bias, "bias")
+        for t, name in ((mean, "mean"), (rstd, "rstd")):
+            self._check(t, (B, self.G), name, self.torch.float32)
+        mean, rstd = mean.contiguous(), rstd.contiguous()
+        dx = self.torch.empty(shape, dtype=self.dtype, device=self.device) if input else None
+        dw = db = None
+        if parameters:
+            dw, db = self.torch.empty((2, self.C), dtype=self.dtype, device=self.device)
+        self._queue(self._lib.hqml_norm_backward, B, S, dy.data_ptr(), lddy, x.data_ptr(), ldx,
+                    None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
+                    mean.data_ptr(), rstd.data_ptr(), dx.data_ptr() if input else None, self.C,
+                    dw.data_ptr() if parameters else None, db.data_ptr() if parameters else None)
         return dx, dw, db

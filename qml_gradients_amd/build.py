@@ -17,7 +17,8 @@ ROOT = os.path.dirname(HERE)
 LIB = os.path.join(HERE, "libhqml.so")
 SOURCES = ["hqml_kernels.hip", "hqml_small.hip", "hqml_small12.hip", "hqml_gbg.hip", "hqml_noalloc.hip",
            "hqml_dense.hip", "hqml_gemm_bf16.hip", "hqml_gemm_fp32.hip", "hqml_gemm_small.hip",
-           "hqml_adamw.hip", "hqml_abi.cpp", "hqml_plan.cpp", "hqml_ops.cpp"]
+           "hqml_adamw.hip", "hqml_dense8.hip", "hqml_norm.hip", "hqml_muon.hip", "hqml_abi.cpp", "hqml_plan.cpp",
+           "hqml_ops.cpp", "hqml_layers.cpp"]
 # Compilation units: (source, extra flags).  hqml_kernels.hip is compiled a second time
 # for the fp32 adjoint launches alone, with the backend's max-ilp instruction schedule;
 # the whole-circuit kernel takes the iterative-maxocc schedule (measured 1.5-2 % faster

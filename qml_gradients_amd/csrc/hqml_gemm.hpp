@@ -17,6 +17,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "hqml_act.hpp"
 #include "hqml_dense_cut.hpp"
 
@@ -24,8 +26,9 @@ namespace hqml {
 namespace gemm {
 
 using bf16x8 = __attribute__((ext_vector_type(8))) __bf16;
+using f16x8 = __attribute__((ext_vector_type(8))) _Float16;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
-using f32x2 = __attribute__((ext_vector_type(2))) float;
+using i32x4 = __attribute__((ext_vector_type(4))) int;
 using f32x4 = __attribute__((ext_vector_type(4))) float;
 using u32x4 = __attribute__((ext_vector_type(4))) uint32_t;
 // 16 bytes at any alignment of an element: the hardware takes them so
@@ -205,9 +208,11 @@ struct DirectTile {
 // arrived when the ticket is taken: a fence would write back a whole L2 for each of them (serve
 // 4096 -> 4096: 32 us with fences).
 // MORE: twice the parts' loads under way, for kernels whose LDS leaves room in the registers.
-template <int FI, int FJ, int THREADS, bool MORE = false>
-__device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int tile, int part, int i0)
+template <int FI, int FJ, int THREADS, bool MORE = false, class Sum = f32x4>
+__device__ __forceinline__ bool joined(const Args &P, Sum (&acc)[FI][FJ], int tile, int part, int i0)
 {
+    using E = std::decay_t<decltype(acc[0][0][0])>;
+    using Pair = __attribute__((ext_vector_type(2))) E;
     __shared__ unsigned taken;
     constexpr int kWords = FI * FJ * 2;   // pairs of sums of a lane
     unsigned long long *all = (unsigned long long *)P.part + (long long)tile * P.parts * (kWords * THREADS) + threadIdx.x;
@@ -220,7 +225,7 @@ __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int 
         for (int g = 0; g < FJ; ++g)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const f32x2 pair = {acc[f][g][2 * h], acc[f][g][2 * h + 1]};
+                const Pair pair = {acc[f][g][2 * h], acc[f][g][2 * h + 1]};
                 __hip_atomic_store(own + ((f * FJ + g) * 2 + h) * THREADS, __builtin_bit_cast(unsigned long long, pair),
                                    __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
@@ -235,7 +240,7 @@ __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int 
 #pragma unroll
     for (int f = 0; f < FI; ++f)
 #pragma unroll
-        for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int g = 0; g < FJ; ++g) acc[f][g] = Sum{};
     for (int p0 = 0; p0 < P.parts; p0 += kAtOnce) {
         unsigned long long w[kAtOnce][kWords];
 #pragma unroll
@@ -250,8 +255,8 @@ __device__ __forceinline__ bool joined(const Args &P, f32x4 (&acc)[FI][FJ], int 
         for (int p = 0; p < kAtOnce; ++p)
 #pragma unroll
             for (int e = 0; e < kWords; ++e) {
-                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2] += __builtin_bit_cast(float, (uint32_t)w[p][e]);
-                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2 + 1] += __builtin_bit_cast(float, (uint32_t)(w[p][e] >> 32));
+                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2] += __builtin_bit_cast(E, (uint32_t)w[p][e]);
+                acc[e / (FJ * 2)][e / 2 % FJ][e % 2 * 2 + 1] += __builtin_bit_cast(E, (uint32_t)(w[p][e] >> 32));
             }
     }
     if (threadIdx.x == 0) __hip_atomic_store(P.ticket + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -409,8 +414,41 @@ __device__ __forceinline__ void finish(const Args &P, f32x4 (&acc)[FI][FJ], int 
 // card (1264-1370, 1332-1403 and 1377-1510 TFLOP/s), with two buffers of 64 k 228-257; the matrix
 // instructions alone take 135.
 
+// The matrix instruction of 16-byte fragments: 32 k of two-byte values, or 64 of integers, two of which take one bf16's
+// place in every tile, length and stride here.
+struct MulBf16 {
+    using Sum = f32x4;
+    static __device__ __forceinline__ Sum mul(bf16x8 b, bf16x8 a, Sum c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, a, c, 0, 0, 0);
+    }
+};
+struct MulF16 {
+    using Sum = f32x4;
+    static __device__ __forceinline__ Sum mul(bf16x8 b, bf16x8 a, Sum c)
+    {
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, b), __builtin_bit_cast(f16x8, a), c, 0, 0, 0);
+    }
+};
+struct MulI8 {
+    using Sum = i32x4;
+    static __device__ __forceinline__ Sum mul(bf16x8 b, bf16x8 a, Sum c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, b), __builtin_bit_cast(i32x4, a), c, 0, 0, 0);
+    }
+};
+
+// Where the operands' tiles of step t lie: one after the other along k.
+struct AlongK {
+    template <bool kSecond, class Tile>
+    __device__ __forceinline__ typename Tile::Step begin(const Tile &tile, int t, int bk) const
+    {
+        return tile.begin(t * bk);
+    }
+};
+
 // What a wave of k_product_direct holds.
-template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
+template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ, class Mul = MulBf16, class Steps = AlongK>
 struct Direct {
     static constexpr int kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
     using TA = DirectTile<LA, BM, BK, kWaves>;
@@ -418,16 +456,17 @@ struct Direct {
     static constexpr int kLoads = TA::kLoads + TB::kLoads;
     TA ta;
     TB tb;
+    Steps steps;
     int wi, wj;
-    f32x4 acc[FI][FJ];
+    typename Mul::Sum acc[FI][FJ];
     static constexpr int kAhead = FI >= 4 ? 2 : 1, kMid = FI / 2, kPer = FJ / (FI - kMid);
     bf16x8 fa[FI], fb[FJ];
 
     // Queue all loads of step t.
     __device__ __forceinline__ void load(char *A, char *B, int t) const
     {
-        const auto sa = ta.begin(t * BK);
-        const auto sb = tb.begin(t * BK);
+        const auto sa = steps.template begin<false>(ta, t, BK);
+        const auto sb = steps.template begin<true>(tb, t, BK);
 #pragma unroll
         for (int n = 0; n < TA::kLoads; ++n) ta.load(sa, (lds_char *)A, n);
 #pragma unroll
@@ -443,8 +482,8 @@ struct Direct {
     }
     __device__ __forceinline__ void step(const char *A, const char *A1, const char *B1, char *A3, char *B3, int t)
     {
-        const auto sa = ta.begin((t + 3) * BK);
-        const auto sb = tb.begin((t + 3) * BK);
+        const auto sa = steps.template begin<false>(ta, t + 3, BK);
+        const auto sb = steps.template begin<true>(tb, t + 3, BK);
         bf16x8 na[kAhead], nb[FJ];
 #pragma unroll
         for (int f = 0; f < FI; ++f) {
@@ -460,8 +499,7 @@ struct Direct {
                     nb[g] = tb.fragment((const lds_char *)B1, wj * TJ + g * 16, 0);
             }
 #pragma unroll
-            for (int g = 0; g < FJ; ++g)
-                acc[f][g] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[g], fa[f], acc[f][g], 0, 0, 0);
+            for (int g = 0; g < FJ; ++g) acc[f][g] = Mul::mul(fb[g], fa[f], acc[f][g]);
             if (f >= kMid) {
                 constexpr int kH = FI - kMid;
 #pragma unroll
@@ -484,7 +522,58 @@ struct Direct {
         wait_loads<2 * kLoads>();
         barrier();
     }
+
+    // All `n` steps, from tiles that are set up; the buffers of LDS are free afterwards.
+    __device__ __forceinline__ void run(int n, char *a0, char *a1, char *a2, char *a3, char *b0, char *b1, char *b2, char *b3)
+    {
+        const int wave = threadIdx.x >> 6;
+        wi = wave / WJ, wj = wave % WJ;
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g) acc[f][g] = typename Mul::Sum{};
+        load(a0, b0, 0);
+        load(a1, b1, 1);
+        load(a2, b2, 2);
+        ready();
+        first(a0, b0);
+        int t = 0;
+        for (; t + 4 <= n; t += 4) {
+            step(a0, a1, b1, a3, b3, t);
+            step(a1, a2, b2, a0, b0, t + 1);
+            step(a2, a3, b3, a1, b1, t + 2);
+            step(a3, a0, b0, a2, b2, t + 3);
+        }
+        if (t < n) {
+            step(a0, a1, b1, a3, b3, t);
+            if (t + 1 < n) {
+                step(a1, a2, b2, a0, b0, t + 1);
+                if (t + 2 < n) step(a2, a3, b3, a1, b1, t + 2);
+            }
+        }
+        wait_loads<0>();
+        barrier();
+    }
+
+    // Rows of TJ floats that a wave's own buffer holds in the epilogue, of those that divide its part.
+    static constexpr int kOwn = TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes, kFit = kOwn / (TJ * 4);
+    static_assert(kWaves <= 8 && kFit >= 16, "room for one block row");
+    static constexpr int PR = kFit >= TI ? TI : kFit;
 };
+
+// The buffer that is a wave's own in the epilogue.
+__device__ __forceinline__ lds_char *own_buffer(char *a0, char *a1, char *a2, char *a3, char *b0, char *b1, char *b2, char *b3)
+{
+    const int wave = threadIdx.x >> 6;
+    return wave == 0   ? (lds_char *)a0
+           : wave == 1 ? (lds_char *)a1
+           : wave == 2 ? (lds_char *)a2
+           : wave == 3 ? (lds_char *)a3
+           : wave == 4 ? (lds_char *)b0
+           : wave == 5 ? (lds_char *)b1
+           : wave == 6 ? (lds_char *)b2
+                       : (lds_char *)b3;
+}
 
 template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
@@ -492,7 +581,6 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
     using D = Direct<LA, LB, BM, BN, BK, WI, WJ>;
     using TA = typename D::TA;
     using TB = typename D::TB;
-    constexpr int kWaves = D::kWaves, TI = D::TI, TJ = D::TJ, FI = D::FI, FJ = D::FJ;
     __shared__ __attribute__((aligned(1024))) char a0[TA::kBytes], a1[TA::kBytes], a2[TA::kBytes], a3[TA::kBytes];
     __shared__ __attribute__((aligned(1024))) char b0[TB::kBytes], b1[TB::kBytes], b2[TB::kBytes], b3[TB::kBytes];
 
@@ -500,53 +588,14 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product_direct(Args P)
     tile_of(blockIdx.x, P.tiles_i, P.tiles_j, ti, tj);
     const int part = blockIdx.y, kb = part * P.k_part;
     const int kn = P.K - kb < P.k_part ? P.K - kb : P.k_part;
-    const int wave = threadIdx.x >> 6;
     D d;
     d.ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
     d.tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
-    d.wi = wave / WJ, d.wj = wave % WJ;
-#pragma unroll
-    for (int f = 0; f < FI; ++f)
-#pragma unroll
-        for (int g = 0; g < FJ; ++g) d.acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const int steps = (kn + BK - 1) / BK;
-    d.load(a0, b0, 0);
-    d.load(a1, b1, 1);
-    d.load(a2, b2, 2);
-    d.ready();
-    d.first(a0, b0);
-    int t = 0;
-    for (; t + 4 <= steps; t += 4) {
-        d.step(a0, a1, b1, a3, b3, t);
-        d.step(a1, a2, b2, a0, b0, t + 1);
-        d.step(a2, a3, b3, a1, b1, t + 2);
-        d.step(a3, a0, b0, a2, b2, t + 3);
-    }
-    if (t < steps) {
-        d.step(a0, a1, b1, a3, b3, t);
-        if (t + 1 < steps) {
-            d.step(a1, a2, b2, a0, b0, t + 1);
-            if (t + 2 < steps) d.step(a2, a3, b3, a1, b1, t + 2);
-        }
-    }
-    wait_loads<0>();
-    barrier();
-    if (P.parts > 1 && !joined<FI, FJ, 64 * kWaves>(P, d.acc, ti * P.tiles_j + tj, part, ti * BM + d.wi * TI)) return;
-    // each wave has a buffer of its own
-    constexpr int kOwn = TA::kBytes < TB::kBytes ? TA::kBytes : TB::kBytes, kFit = kOwn / (TJ * 4);
-    static_assert(kWaves <= 8 && kFit >= 16, "room for one block row");
-    constexpr int PR = kFit >= TI ? TI : kFit;
-    lds_char *const own = wave == 0   ? (lds_char *)a0
-                          : wave == 1 ? (lds_char *)a1
-                          : wave == 2 ? (lds_char *)a2
-                          : wave == 3 ? (lds_char *)a3
-                          : wave == 4 ? (lds_char *)b0
-                          : wave == 5 ? (lds_char *)b1
-                          : wave == 6 ? (lds_char *)b2
-                                      : (lds_char *)b3;
-    finish<bf16, FI, FJ, PR, LA == K_ROWS && LB == K_ROWS, false>(P, d.acc, ti * BM + d.wi * TI, tj * BN + d.wj * TJ,
-                                                                  own, [](int, int, const bool (&)[4]) { return f32x4{}; });
+    d.run((kn + BK - 1) / BK, a0, a1, a2, a3, b0, b1, b2, b3);
+    const int i0 = ti * BM + d.wi * D::TI, j0 = tj * BN + d.wj * D::TJ;
+    if (P.parts > 1 && !joined<D::FI, D::FJ, 64 * D::kWaves>(P, d.acc, ti * P.tiles_j + tj, part, i0)) return;
+    finish<bf16, D::FI, D::FJ, D::PR, LA == K_ROWS && LB == K_ROWS, false>(
+        P, d.acc, i0, j0, own_buffer(a0, a1, a2, a3, b0, b1, b2, b3), [](int, int, const bool (&)[4]) { return f32x4{}; });
 }
 
 // One operand tile on its way through registers: 8-value chunks, loaded 16 bytes at a time at any
@@ -947,21 +996,27 @@ __device__ __forceinline__ void small_value(const Args &P, float sum, int i, int
     narrow(y, ((T *)P.c)[i * P.ldc + j]);
 }
 
-// The waves' sums of a 16 FI x 16 tile, added and finished; split over k, parts meet as joined()'s do.
-template <typename T, int FI, bool kForward>
-__device__ __forceinline__ void small_finish(const Args &P, f32x4 (&acc)[FI], int tile, int i0, int j0, float *lds)
+// The waves' sums of a 16 FI x 16 tile, added and finished; split over k, parts meet as joined()'s do.  value(sum, i, j): what
+// a sum becomes before the epilogue, of i and j that exist (j may be the column of ones).
+template <typename T, int FI, bool kForward, class Sum, class F>
+__device__ __forceinline__ void small_finish(const Args &P, Sum (&acc)[FI], int tile, int i0, int j0, float *lds, F value)
 {
+    using E = std::decay_t<decltype(acc[0][0])>;
     __shared__ unsigned taken;
+    E *held = (E *)lds;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, waves = blockDim.x >> 6;
 #pragma unroll
     for (int f = 0; f < FI; ++f)   // [wave][row][16 columns]
-        *(f32x4 *)(lds + (wave * FI * 16 + f * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) = acc[f];
+        *(Sum *)(held + (wave * FI * 16 + f * 16 + (lane & 15)) * 16 + (lane >> 4) * 4) = acc[f];
     __syncthreads();
-    float *all = P.part + (long long)tile * P.parts * (FI * 256);
+    auto finished = [&](E sum, int i, int j) {
+        if (i < P.I && j < P.J + (kForward ? 0 : 1)) small_value<T, kForward>(P, value(sum, i, j), i, j);
+    };
+    E *all = (E *)P.part + (long long)tile * P.parts * (FI * 256);
     for (int e = threadIdx.x; e < FI * 256; e += blockDim.x) {
-        float sum = 0.0f;
-        for (int q = 0; q < waves; ++q) sum += lds[q * FI * 256 + e];
-        if (P.parts == 1) small_value<T, kForward>(P, sum, i0 + (e >> 4), j0 + (e & 15));
+        E sum = 0;
+        for (int q = 0; q < waves; ++q) sum += held[q * FI * 256 + e];
+        if (P.parts == 1) finished(sum, i0 + (e >> 4), j0 + (e & 15));
         else if (i0 + (e >> 4) < P.I)
             __hip_atomic_store(all + blockIdx.y * (FI * 256) + e, sum, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
@@ -974,11 +1029,11 @@ __device__ __forceinline__ void small_finish(const Args &P, f32x4 (&acc)[FI], in
     if (taken != (unsigned)P.parts - 1) return;
     for (int e = threadIdx.x; e < FI * 256; e += blockDim.x) {
         if (i0 + (e >> 4) >= P.I) break;
-        float sum = 0.0f;
+        E sum = 0;
 #pragma unroll 4
         for (int p = 0; p < P.parts; ++p)
             sum += __hip_atomic_load(all + p * (FI * 256) + e, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        small_value<T, kForward>(P, sum, i0 + (e >> 4), j0 + (e & 15));
+        finished(sum, i0 + (e >> 4), j0 + (e & 15));
     }
     if (threadIdx.x == 0) __hip_atomic_store(P.ticket + tile, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
@@ -1032,7 +1087,7 @@ __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small_forward(Args P)
             }
         }
     }
-    small_finish<T, FI, true>(P, acc, blockIdx.x, i0, j0, small_lds);
+    small_finish<T, FI, true>(P, acc, blockIdx.x, i0, j0, small_lds, [](float sum, int, int) { return sum; });
 }
 
 // One gradient product: C = dz B with B's k across its rows; dz's layout L.  A column of ones after B's
@@ -1066,7 +1121,7 @@ __device__ __forceinline__ void small_gradient(const Args &P, int id, float *lds
                     acc[f] = __builtin_amdgcn_mfma_f32_16x16x4f32(one ? 1.0f : b[n].value(e), a[n][f].value(e), acc[f], 0, 0, 0);
             }
     }
-    small_finish<T, FI, false>(P, acc, id, i0, j0, lds);
+    small_finish<T, FI, false>(P, acc, id, i0, j0, lds, [](float sum, int, int) { return sum; });
 }
 
 // Small gradients in one launch: dx = dz w from the first workgroups, dw = dz^T x with db as a column

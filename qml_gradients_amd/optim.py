@@ -1,23 +1,27 @@
-"""AdamW over all of a model's tensors in one launch: circuit angles and dense weights alike.
+"""The optimisers of a model around circuits.
 
-Marshalling only: the step runs in ``hqml_adamw_step``.  The moments are torch tensors in the
-optimiser's state, held in 32 bits (64 for 64-bit parameters) or in 8 bits: e4m3 codes and one
-32-bit scale per 256 elements, the second moment as its square root.
+AdamW takes all of its tensors in one launch, circuit angles and dense weights alike; Muon takes weight matrices, whose
+updates it orthogonalises.  Marshalling only: the steps run in ``hqml_adamw_step`` and ``hqml_muon_step``.  AdamW's moments
+are torch tensors in the optimiser's state, held in 32 bits (64 for 64-bit parameters) or in 8 bits: e4m3 codes and one
+32-bit scale per 256 elements, the second moment as its square root.  Muon's momentum is held in 32 bits.
 """
 from __future__ import annotations
 
 import copy
 import ctypes
+import math
 
 import torch
 from torch.optim.optimizer import _global_optimizer_post_hooks, _global_optimizer_pre_hooks
 
 from . import (HQML_ADAMW_BLOCK, HQML_DTYPE_BF16, HQML_DTYPE_FP32, HQML_DTYPE_FP64, HQML_MOMENTS_8, HQML_MOMENTS_32,
-               hqml_adamw_config, hqml_adamw_step)
+               HQML_MUON_MAX_SIDE, HQML_MUON_MAX_STEPS, hqml_adamw_config, hqml_adamw_step, hqml_muon_config,
+               hqml_muon_step, hqml_muon_tensor, hqml_muon_workspace_bytes)
 
 _DTYPES = {torch.float32: HQML_DTYPE_FP32, torch.bfloat16: HQML_DTYPE_BF16, torch.float64: HQML_DTYPE_FP64}
 _WIDE = {torch.float32: torch.float32, torch.bfloat16: torch.float32, torch.float64: torch.float64}
 _CODES = torch.float8_e4m3fn
+_MATRIX = (torch.float32, torch.bfloat16)   # Muon's types
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -182,6 +186,151 @@ class AdamW(torch.optim.Optimizer):
                 s = {k: v.detach().to(p.device, copy=True).contiguous() if isinstance(v, torch.Tensor)
                      else copy.deepcopy(v) for k, v in saved[i].items()}
                 self._fit(p, s, bits)
+                kept.append((p, s))
+        self._kept = kept
+
+    def __setstate__(self, state):   # during a load: before the hooks that follow it
+        super().__setstate__(state)
+        for p, s in self._kept:
+            self.state[p] = s
+
+
+def _rms(rows, cols):
+    return 0.2 * math.sqrt(max(rows, cols))
+
+
+def _spectral(rows, cols):
+    return math.sqrt(max(1.0, rows / cols))
+
+
+class Muon(torch.optim.Optimizer):
+    """Momentum and orthogonalised updates (K. Jordan et al., 2024) for weight matrices:
+      m = momentum m + (1 - momentum) g,  u = momentum m + (1 - momentum) g (nesterov) or m,
+      X = u / max(|u|, eps);  `steps` times, with A = X X^T:  X = a X + (b A + c A^2) X,
+      p = p (1 - lr weight_decay) - lr f X
+    with (a, b, c) = coefficients.  f by `adjust`: "spectral", sqrt(max(1, rows / cols)); "rms", 0.2 sqrt(max(rows,
+    cols)), which gives updates the size of AdamW's; "none", 1.  Parameters: contiguous CUDA matrices in fp32 or bf16
+    (vectors, angles and the like are AdamW's); a gradient may be bf16 for an fp32 parameter and the other way round.
+    state[p]["momentum"] is m, in fp32.  The step runs on each device's current stream and can be captured into a graph,
+    which then repeats it with the lr it was captured with."""
+
+    def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True,
+                 coefficients=(3.4445, -4.7750, 2.0315), steps=5, eps=1e-7, adjust="spectral"):
+        super().__init__(params, dict(lr=lr, momentum=momentum, weight_decay=weight_decay, nesterov=nesterov,
+                                      coefficients=tuple(coefficients), steps=steps, eps=eps, adjust=adjust))
+
+    _adjust = {"spectral": _spectral, "rms": _rms, "none": lambda rows, cols: 1.0}
+
+    def add_param_group(self, param_group):
+        super().add_param_group(param_group)
+        group = self.param_groups[-1]
+        if not group["lr"] >= 0.0 or not group["weight_decay"] >= 0.0:
+            raise ValueError("lr and weight_decay must be >= 0")
+        if not 0.0 <= group["momentum"] < 1.0 or not group["eps"] > 0.0:
+            raise ValueError("momentum must be in [0, 1), eps > 0")
+        if len(group["coefficients"]) != 3 or not 1 <= group["steps"] <= HQML_MUON_MAX_STEPS:
+            raise ValueError(f"there are three coefficients and 1 to {HQML_MUON_MAX_STEPS} steps")
+        if group["adjust"] not in self._adjust:
+            raise ValueError(f"adjust must be one of {', '.join(self._adjust)}")
+        for p in group["params"]:
+            self._accept(p)
+
+    @staticmethod
+    def _accept(p):
+        if not p.is_cuda:
+            raise ValueError("parameters must be CUDA tensors")
+        Muon._fits(p)
+
+    @staticmethod
+    def _fits(p):
+        if p.dim() != 2 or p.dtype not in _MATRIX or not p.is_contiguous() or max(p.shape) > HQML_MUON_MAX_SIDE:
+            raise ValueError("parameters must be contiguous matrices in fp32 or bf16, of up to 2^16 rows and columns")
+
+    @staticmethod
+    def _momentum(p, s):
+        """The momentum of a state s of p, checked: the kernel walks it by its parameter's size."""
+        m = s.get("momentum")
+        if m is None:
+            m = s["momentum"] = torch.zeros_like(p, dtype=torch.float32)
+        elif m.shape != p.shape or m.dtype is not torch.float32 or m.device != p.device or not m.is_contiguous():
+            raise ValueError(f"the momentum of a parameter {tuple(p.shape)} on {p.device} must be a contiguous fp32 "
+                             "tensor of its shape there")
+        return m
+
+    def _step(self, closure=None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            size_of = self._adjust[group["adjust"]]
+            calls = {}   # matrices that one call can take
+            for p in group["params"]:
+                g = p.grad
+                if g is None:
+                    continue
+                if g.layout is not torch.strided or g.dtype not in _MATRIX:
+                    raise ValueError("gradients must be dense, in fp32 or bf16")
+                self._fits(p)
+                if g.shape != p.shape:
+                    raise ValueError(f"a parameter {tuple(p.shape)} has a gradient {tuple(g.shape)}")
+                if not g.is_contiguous():
+                    g = g.detach().contiguous()
+                m = self._momentum(p, self.state[p])
+                tensors, params, kept = calls.setdefault((p.dtype, g.dtype, p.get_device()), ([], [], []))
+                rows, cols = p.shape
+                tensors.append(hqml_muon_tensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), rows, cols, size_of(rows, cols)
+                                                if rows and cols else 0.0))
+                params.append(p)
+                kept.append(g)    # until its kernels are queued
+            for (pd, gd, device), (tensors, params, kept) in calls.items():
+                cfg = hqml_muon_config(_DTYPES[pd], _DTYPES[gd], bool(group["nesterov"]), group["steps"], group["lr"],
+                                       group["momentum"], group["weight_decay"], group["eps"], *group["coefficients"],
+                                       device, _current_stream(device))
+                array = (hqml_muon_tensor * len(tensors))(*tensors)
+                need = hqml_muon_workspace_bytes(cfg, len(tensors), array)
+                # torch's memory: freed at once, it is handed out again only to what the stream runs later
+                work = torch.empty(need, dtype=torch.uint8, device=params[0].device)
+                hqml_muon_step(cfg, len(tensors), array, work.data_ptr(), need)
+                # a backward pass that saved a parameter from before this step has to refuse it
+                torch.autograd.graph.increment_version(params)
+        return loss
+
+    _hooked_step = torch.optim.Optimizer.profile_hook_step(_step)
+
+    def step(self, closure=None):
+        """One step of every parameter that has a gradient; what `closure` returns, called first with gradients on."""
+        # torch's hooks and profiler range cost time: taken where somebody asked for one
+        if (_global_optimizer_post_hooks or _global_optimizer_pre_hooks or self._optimizer_step_pre_hooks
+                or self._optimizer_step_post_hooks or torch.autograd._profiler_enabled()):
+            return self._hooked_step() if closure is None else self._hooked_step(closure)
+        return self._step(closure)
+
+    step.hooked = True   # torch wraps a step that does not say so itself
+
+    def load_state_dict(self, state_dict):
+        """As torch's, but the momentum stays in fp32.  A state that does not fit its parameter is refused before anything
+        is taken over."""
+        # as the last hook before the load, it sees what the others made of state_dict
+        last = self.register_load_state_dict_pre_hook(Muon._keep)
+        try:
+            super().load_state_dict(state_dict)
+        finally:
+            last.remove()
+            self._kept = ()
+
+    _kept = ()
+
+    def _keep(self, state_dict):
+        """The states to load, as they were saved and checked: torch casts its own copies to the parameters' types."""
+        saved, kept = state_dict["state"], []
+        for own, group in zip(self.param_groups, state_dict["param_groups"]):
+            for i, p in zip(group["params"], own["params"]):
+                if not saved.get(i):
+                    continue
+                s = {k: v.detach().to(p.device, copy=True).contiguous() if isinstance(v, torch.Tensor)
+                     else copy.deepcopy(v) for k, v in saved[i].items()}
+                self._momentum(p, s)
                 kept.append((p, s))
         self._kept = kept
 

@@ -5,8 +5,9 @@ summary, section 3.3).  This module plays that role over the C ABI: the forward
 runs ``hqml_forward`` (keeping the fused-pass outputs), the backward runs
 ``hqml_backward`` with the incoming dL/dE, so any loss built from the
 expectation values gets its gradient from the fused adjoint kernels.  Gradients
-flow to theta only; the encoding angles x are data.  DenseLayer does the same for the
-dense layers around the circuits.  Marshalling only: no arithmetic of the method runs here.
+flow to theta only; the encoding angles x are data.  DenseLayer and GroupNormLayer do the
+same for the layers around the circuits, and DenseInt8Layer serves a trained dense layer in 8-bit
+integers.  Marshalling only: no arithmetic of the method runs here.
 """
 from __future__ import annotations
 
@@ -14,7 +15,7 @@ import math
 
 import torch
 
-from . import Context, Dense
+from . import Context, Dense, DenseInt8, GroupNorm, quantise_rows
 
 
 class HEAExpectation(torch.autograd.Function):
@@ -113,3 +114,84 @@ class DenseLayer(torch.nn.Module):
         # shows it
         y = DenseFunction.apply(x, self.weight, self.bias, residual, self.dense, torch.is_grad_enabled())
         return y.reshape(*lead, y.shape[-1])
+
+
+class DenseInt8Layer(torch.nn.Module):
+    """A dense layer served in 8-bit integers: y = alpha act(x w^T + bias) + residual over the last axis of x, with the
+    weights held as int8 codes [out_features][in_features] and a scale for each output channel.  `of` makes one of a
+    trained DenseLayer; codes, scales and bias are buffers.  There is no gradient: an input that wants one is refused."""
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0, bias=True,
+                 device=None):
+        super().__init__()
+        self.dense = DenseInt8(in_features, out_features, max_batch, dtype=dtype, activation=activation, alpha=alpha,
+                               device=device)
+        weight = torch.zeros(out_features, in_features, device=self.dense.device)
+        codes, scales = quantise_rows(weight)
+        self.register_buffer("codes", codes)
+        self.register_buffer("scales", scales)
+        self.register_buffer("bias", torch.zeros(out_features, dtype=self.dense.dtype, device=self.dense.device)
+                             if bias else None)
+
+    @classmethod
+    def of(cls, layer):
+        """The DenseLayer `layer` in 8-bit integers."""
+        c = layer.dense.cfg
+        made = cls(c.in_features, c.out_features, c.max_batch, dtype=c.dtype, activation=c.activation, alpha=c.alpha,
+                   bias=layer.bias is not None, device=c.device)
+        with torch.no_grad():
+            made.codes, made.scales = quantise_rows(layer.weight)
+            if layer.bias is not None:
+                made.bias.copy_(layer.bias)
+        return made
+
+    def forward(self, x, residual=None):
+        if torch.is_grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)):
+            raise RuntimeError("a dense layer in 8-bit integers has no gradient: call it under torch.no_grad()")
+        lead = x.shape[:-1]
+        x = x.reshape(-1, x.shape[-1])
+        if residual is not None:
+            residual = residual.reshape(-1, residual.shape[-1])
+        y = self.dense.forward(x, self.codes, self.scales, self.bias, residual)
+        return y.reshape(*lead, y.shape[-1])
+
+
+class GroupNormFunction(torch.autograd.Function):
+    """y = act(weight xhat + bias), differentiable in all three."""
+
+    @staticmethod
+    def forward(ctx, x, weight, bias, norm, gradients):
+        ctx.norm = norm
+        if not gradients or not any(ctx.needs_input_grad[:3]):
+            return norm.forward(x, weight, bias)
+        y, mean, rstd = norm.forward_train(x, weight, bias)
+        ctx.save_for_backward(x, weight, bias, mean, rstd)
+        return y
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dy):
+        need = ctx.needs_input_grad
+        dx = dw = db = None
+        if any(need[:3]):
+            x, weight, bias, mean, rstd = ctx.saved_tensors
+            dx, dw, db = ctx.norm.backward(dy, x, weight, bias, mean, rstd, input=need[0], parameters=need[1] or need[2])
+        return dx, dw if need[1] else None, db if need[2] else None, None, None
+
+
+class GroupNormLayer(torch.nn.Module):
+    """Group norm with an activation over channels-last arrays [samples][...positions][channels], with weight (1 at
+    first) and bias (0) [channels] as trainable parameters.  max_rows bounds samples times positions."""
+
+    def __init__(self, channels, groups, max_rows, dtype="fp32", activation="none", eps=1e-5, affine=True, device=None):
+        super().__init__()
+        self.norm = GroupNorm(channels, groups, max_rows, dtype=dtype, activation=activation, eps=eps, device=device)
+
+        def parameter(value):
+            return torch.nn.Parameter(torch.full((channels,), value, dtype=self.norm.dtype, device=self.norm.device))
+
+        self.weight = parameter(1.0) if affine else None
+        self.bias = parameter(0.0) if affine else None
+
+    def forward(self, x):
+        return GroupNormFunction.apply(x, self.weight, self.bias, self.norm, torch.is_grad_enabled())
