@@ -438,17 +438,8 @@ struct MulI8 {
     }
 };
 
-// Where the operands' tiles of step t lie: one after the other along k.
-struct AlongK {
-    template <bool kSecond, class Tile>
-    __device__ __forceinline__ typename Tile::Step begin(const Tile &tile, int t, int bk) const
-    {
-        return tile.begin(t * bk);
-    }
-};
-
 // What a wave of k_product_direct holds.
-template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ, class Mul = MulBf16, class Steps = AlongK>
+template <int LA, int LB, int BM, int BN, int BK, int WI, int WJ, class Mul = MulBf16>
 struct Direct {
     static constexpr int kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
     using TA = DirectTile<LA, BM, BK, kWaves>;
@@ -456,7 +447,6 @@ struct Direct {
     static constexpr int kLoads = TA::kLoads + TB::kLoads;
     TA ta;
     TB tb;
-    Steps steps;
     int wi, wj;
     typename Mul::Sum acc[FI][FJ];
     static constexpr int kAhead = FI >= 4 ? 2 : 1, kMid = FI / 2, kPer = FJ / (FI - kMid);
@@ -465,8 +455,8 @@ struct Direct {
     // Queue all loads of step t.
     __device__ __forceinline__ void load(char *A, char *B, int t) const
     {
-        const auto sa = steps.template begin<false>(ta, t, BK);
-        const auto sb = steps.template begin<true>(tb, t, BK);
+        const auto sa = ta.begin(t * BK);
+        const auto sb = tb.begin(t * BK);
 #pragma unroll
         for (int n = 0; n < TA::kLoads; ++n) ta.load(sa, (lds_char *)A, n);
 #pragma unroll
@@ -482,8 +472,8 @@ struct Direct {
     }
     __device__ __forceinline__ void step(const char *A, const char *A1, const char *B1, char *A3, char *B3, int t)
     {
-        const auto sa = steps.template begin<false>(ta, t + 3, BK);
-        const auto sb = steps.template begin<true>(tb, t + 3, BK);
+        const auto sa = ta.begin((t + 3) * BK);
+        const auto sb = tb.begin((t + 3) * BK);
         bf16x8 na[kAhead], nb[FJ];
 #pragma unroll
         for (int f = 0; f < FI; ++f) {

@@ -367,12 +367,17 @@ int muon_step(const hqml_muon_config *c, int n, const hqml_muon_tensor *t, void 
     std::string err;
     int rc = check_muon(c, n, t, &err);
     if (rc != HQML_OK) return thread_error(rc, err);
+    bool some = false;
+    for (int i = 0; i < n; ++i) some = some || (t[i].rows && t[i].cols);
+    if (!some) return HQML_OK;
     const size_t need = muon_workspace(*c, n, t);
-    if (!need) return HQML_OK;   // no elements
     const OnDevice on(c->device);
     if (on.error() != hipSuccess) return thread_error(HQML_ERR_HIP, hip_text("device", on.error()));
-    if (bytes < need || (size_t)workspace % 256) return thread_error(HQML_ERR_ARG, "workspace is too small or not 256-byte aligned");
-    rc = check_device_array(c->device, workspace, need, "workspace", &err);
+    if (need) {
+        if (bytes < need || (size_t)workspace % 256)
+            return thread_error(HQML_ERR_ARG, "workspace is too small or not 256-byte aligned");
+        rc = check_device_array(c->device, workspace, need, "workspace", &err);
+    }
     for (int i = 0; rc == HQML_OK && i < n; ++i) {
         const size_t k = (size_t)t[i].rows * t[i].cols;
         if (!k) continue;

@@ -29,8 +29,8 @@ namespace {
 using namespace gemm;
 
 constexpr float kScale = 1024.0f, kUnscale = 1.0f / kScale;
-constexpr int kMatrices = 32;              // of one launch
-constexpr long long kChunk = 16384;        // values of a workgroup of the momentum kernel
+constexpr int kMatrices = 24;              // of one launch
+constexpr long long kChunk = 8192;         // values of a workgroup of the momentum kernel
 constexpr size_t kBatchBytes = 1ull << 30; // workspace from which matrices go in several rounds
 
 int pad8(int n) { return (n + 7) & ~7; }
@@ -78,22 +78,75 @@ __device__ __forceinline__ int matrix_of(const unsigned *first, int count, unsig
 
 __device__ __forceinline__ float update_of(const Scalars &k, float m, float g) { return k.nesterov ? m * k.mu + g * k.nu : m; }
 
+// n neighbouring values, 16 bytes or fewer at a time and at any alignment of the element: the hardware takes them so.
+template <int n, typename T>
+__device__ __forceinline__ void get(T (&to)[n], const T *from)
+{
+    struct __attribute__((packed)) All {
+        T t[n];
+    };
+    const All a = *(const All *)from;
+#pragma unroll
+    for (int k = 0; k < n; ++k) to[k] = a.t[k];
+}
+
+template <int n, typename T>
+__device__ __forceinline__ void put(T *to, const T (&from)[n])
+{
+    struct __attribute__((packed)) All {
+        T t[n];
+    };
+    All a;
+#pragma unroll
+    for (int k = 0; k < n; ++k) a.t[k] = from[k];
+    *(All *)to = a;
+}
+
 // m, and the sums of u^2 of each chunk, in 64 bits: they neither overflow nor lose a small chunk beside a large one.
+// The first workgroup clears the tickets of the products that follow.
 template <typename G>
-__global__ __launch_bounds__(256) void k_momentum(Batch batch, Scalars k)
+__global__ __launch_bounds__(256) void k_momentum(Batch batch, Scalars k, unsigned *tickets, int n_tickets)
 {
     __shared__ double part[4];
+    if (blockIdx.x == 0)
+        for (int i = threadIdx.x; i < n_tickets; i += 256) tickets[i] = 0;
     const int ti = matrix_of(batch.first, batch.count, blockIdx.x);
     const Matrix &t = batch.t[ti];
     const long long chunk = blockIdx.x - batch.first[ti], n = (long long)t.rows * t.cols, base = chunk * kChunk;
-    const long long end = n - base < kChunk ? n : base + kChunk;
-    const G *g = (const G *)t.g;
+    const int end = n - base < kChunk ? (int)(n - base) : (int)kChunk;
+    const G *g = (const G *)t.g + base;
+    float *m = t.m + base;
     double sum = 0.0;
-    for (long long i = base + threadIdx.x; i < end; i += 256) {
-        const float gi = widen(g[i]), m = t.m[i] * k.mu + gi * k.nu;
-        t.m[i] = m;
-        const double u = update_of(k, m, gi);
-        sum += u * u;
+    constexpr int kV = 4, kAt = 4;   // values of a thread at once, and how often before the first is used
+    for (int i0 = threadIdx.x * kV; i0 < end; i0 += 256 * kV * kAt) {
+        float mv[kAt][kV];
+        G gv[kAt][kV];
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            const int i = i0 + a * 256 * kV;
+            if (i + kV <= end) get(mv[a], m + i), get(gv[a], g + i);
+        }
+#pragma unroll
+        for (int a = 0; a < kAt; ++a) {
+            const int i = i0 + a * 256 * kV;
+            if (i + kV <= end) {
+#pragma unroll
+                for (int e = 0; e < kV; ++e) {
+                    const float gi = widen(gv[a][e]);
+                    mv[a][e] = mv[a][e] * k.mu + gi * k.nu;
+                    const double u = update_of(k, mv[a][e], gi);
+                    sum += u * u;
+                }
+                put(m + i, mv[a]);
+            } else {
+                for (int j = i; j < end; ++j) {
+                    const float gi = widen(g[j]), mj = m[j] * k.mu + gi * k.nu;
+                    m[j] = mj;
+                    const double u = update_of(k, mj, gi);
+                    sum += u * u;
+                }
+            }
+        }
     }
 #pragma unroll
     for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
@@ -141,17 +194,27 @@ __global__ __launch_bounds__(256) void k_begin(Batch batch, Scalars k)
         const int row = (int)(i / eights), c = (int)(i - (long long)row * eights) * 8;
         const long long at = (long long)row * t.cols + c;
         Half hi[8], lo[8];
+        float mv[8] = {};
+        G gv[8] = {};
+        if (c + 8 <= t.cols) {
+            get(mv, t.m + at);
+            if (k.nesterov) get(gv, g + at);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float u = c + e < t.cols ? update_of(k, t.m[at + e], widen(g[at + e])) : 0.0f;
-            to_planes(c + e < t.cols ? u * inv : 0.0f, hi[e], lo[e]);
+            for (int e = 0; e < 8; ++e)
+                if (c + e < t.cols) mv[e] = t.m[at + e], gv[e] = g[at + e];
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to_planes(c + e < t.cols ? update_of(k, mv[e], widen(gv[e])) * inv : 0.0f, hi[e], lo[e]);
         *(u32x4 *)(t.x[0] + (long long)row * ld + c) = __builtin_bit_cast(u32x4, hi);
         if (PLANES == 2) *(u32x4 *)(t.x[0] + plane + (long long)row * ld + c) = __builtin_bit_cast(u32x4, lo);
     }
 }
 
 // ---- the products ----
+//
+// A product's tiles, for few of them each in several parts along k, are the workgroups.  A and B are symmetric: of their tiles
+// those on and below the diagonal are formed, and each is written to its mirrored place too.
 
 enum Stage { GRAM, POLY, APPLY };
 
@@ -160,10 +223,15 @@ struct Product {
     const Half *a, *b, *with;   // with: what a multiple of is added, laid out as C
     Half *c;
     void *p;                    // the last step's: the parameter
+    float *part;                // partial sums
+    unsigned *ticket;
     long long plane_a, plane_b, plane_c;   // values from one plane to the next
     int lda, ldb, ldc, I, J, K;
-    int cols;                   // A and B across k (GRAM), B across k (APPLY)
     int tiles_i, tiles_j;
+    int tiles, skip;            // of this launch; tiles of twice the side that another one took
+    int parts, steps;           // steps of a part
+    short cols;                 // A and B across k (GRAM), B across k (APPLY)
+    short mirrored;
     float size;
 };
 
@@ -180,42 +248,191 @@ struct Finish {
 };
 static_assert(sizeof(Products) + sizeof(Finish) <= 4096, "kernel arguments");
 
-// The operands' tiles along k: with two planes, the small products first: lo hi, hi lo, hi hi.
-template <int PLANES>
-struct Planes {
-    int per;                     // steps of a plane
-    long long plane_a, plane_b;  // bytes
-    template <bool kSecond, class Tile>
-    __device__ __forceinline__ typename Tile::Step begin(const Tile &tile, int t, int bk) const
+// Operands of two planes: gemm::Direct with both planes of a step's tiles in a buffer, and three matrix instructions for its one:
+// lo hi, hi lo and hi hi.  A step has 4/3 of the loads and barriers of three steps of one plane (1024 x 4096, X X^T: 56 us so).
+template <int LA, int LB, int BM, int BN, int WI, int WJ>
+struct DirectPair {
+    static constexpr int BK = 32, kWaves = WI * WJ, TI = BM / WI, TJ = BN / WJ, FI = TI / 16, FJ = TJ / 16;
+    using TA = DirectTile<LA, BM, BK, kWaves>;
+    using TB = DirectTile<LB, BN, BK, kWaves>;
+    static constexpr int kPlaneA = TA::kBytes, kPlaneB = TB::kBytes, kLoads = 2 * (TA::kLoads + TB::kLoads);
+    TA ta;
+    TB tb;
+    long long plane_a, plane_b;   // bytes
+    int wi, wj;
+    f32x4 acc[FI][FJ];
+    static constexpr int kAhead = 1, kMid = FI / 2, kPer = FJ / (FI - kMid);
+    bf16x8 fa[FI][2], fb[FJ][2];
+
+    // Queue load n of kLoads.
+    __device__ __forceinline__ void load_one(const typename TA::Step &sa, const typename TB::Step &sb, char *A, char *B, int n) const
     {
-        if (PLANES == 1) return tile.begin(t * bk);
-        const int turn = t >= 2 * per ? 2 : t >= per ? 1 : 0;
-        auto st = tile.begin((t - turn * per) * bk);
-        if (turn == (kSecond ? 1 : 0)) st.p += kSecond ? plane_b : plane_a;
-        return st;
+        const int plane = n & 1;
+        n >>= 1;
+        if (n < TA::kLoads) {
+            auto st = sa;
+            st.p += plane * plane_a;
+            ta.load(st, (lds_char *)A + plane * kPlaneA, n);
+        } else {
+            auto st = sb;
+            st.p += plane * plane_b;
+            tb.load(st, (lds_char *)B + plane * kPlaneB, n - TA::kLoads);
+        }
     }
+    __device__ __forceinline__ void load(char *A, char *B, int t) const
+    {
+        const auto sa = ta.begin(t * BK);
+        const auto sb = tb.begin(t * BK);
+#pragma unroll
+        for (int n = 0; n < kLoads; ++n) load_one(sa, sb, A, B, n);
+    }
+    __device__ __forceinline__ void get_a(bf16x8 (&to)[2], const char *A, int f) const
+    {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) to[p] = ta.fragment((const lds_char *)A + p * kPlaneA, wi * TI + f * 16, 0);
+    }
+    __device__ __forceinline__ void get_b(bf16x8 (&to)[2], const char *B, int g) const
+    {
+#pragma unroll
+        for (int p = 0; p < 2; ++p) to[p] = tb.fragment((const lds_char *)B + p * kPlaneB, wj * TJ + g * 16, 0);
+    }
+    __device__ __forceinline__ void step(const char *A, const char *A1, const char *B1, char *A3, char *B3, int t)
+    {
+        const auto sa = ta.begin((t + 3) * BK);
+        const auto sb = tb.begin((t + 3) * BK);
+        bf16x8 na[kAhead][2], nb[FJ][2];
+        wait_loads<kLoads>();   // step t + 1 is there, and every wave is done with step t - 1
+        barrier();
+#pragma unroll
+        for (int f = 0; f < FI; ++f) {
+            if (f + kAhead < FI) get_a(fa[f + kAhead], A, f + kAhead);
+            else get_a(na[f + kAhead - FI], A1, f + kAhead - FI);
+            if (f >= kMid) {
+#pragma unroll
+                for (int g = (f - kMid) * kPer; g < (f - kMid + 1) * kPer; ++g) get_b(nb[g], B1, g);
+            }
+            // a wave's loads among its matrix instructions, a few at a time: more would hold those up behind them
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {   // small products first
+#pragma unroll
+                for (int g = 0; g < FJ; ++g) acc[f][g] = MulF16::mul(fb[g][c == 1], fa[f][c == 0], acc[f][g]);
+                constexpr int kSlots = FI * 3;
+                const int slot = f * 3 + c;
+#pragma unroll
+                for (int n = slot * kLoads / kSlots; n < (slot + 1) * kLoads / kSlots; ++n) load_one(sa, sb, A3, B3, n);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 2; ++p) {
+#pragma unroll
+            for (int f = 0; f < kAhead; ++f) fa[f][p] = na[f][p];
+#pragma unroll
+            for (int g = 0; g < FJ; ++g) fb[g][p] = nb[g][p];
+        }
+    }
+    __device__ __forceinline__ void run(int n, char *a0, char *a1, char *a2, char *a3, char *b0, char *b1, char *b2, char *b3)
+    {
+        const int wave = threadIdx.x >> 6;
+        wi = wave / WJ, wj = wave % WJ;
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int g = 0; g < FJ; ++g) acc[f][g] = f32x4{};
+        load(a0, b0, 0);
+        load(a1, b1, 1);
+        load(a2, b2, 2);
+        wait_loads<2 * kLoads>();
+        barrier();
+#pragma unroll
+        for (int f = 0; f < kAhead; ++f) get_a(fa[f], a0, f);
+#pragma unroll
+        for (int g = 0; g < FJ; ++g) get_b(fb[g], b0, g);
+        int t = 0;
+        for (; t + 4 <= n; t += 4) {
+            step(a0, a1, b1, a3, b3, t);
+            step(a1, a2, b2, a0, b0, t + 1);
+            step(a2, a3, b3, a1, b1, t + 2);
+            step(a3, a0, b0, a2, b2, t + 3);
+        }
+        if (t < n) {
+            step(a0, a1, b1, a3, b3, t);
+            if (t + 1 < n) {
+                step(a1, a2, b2, a0, b0, t + 1);
+                if (t + 2 < n) step(a2, a3, b3, a1, b1, t + 2);
+            }
+        }
+        wait_loads<0>();
+        barrier();
+    }
+    static constexpr int kFit = 2 * (kPlaneA < kPlaneB ? kPlaneA : kPlaneB) / (TJ * 4), PR = kFit >= TI ? TI : kFit;
 };
 
-template <int LA, int LB, int PLANES, int BM, int BN, int WI, int WJ>
-__device__ __forceinline__ void product(const Product &P, const Finish &F, int id, char *a0, char *a1, char *a2, char *a3, char *b0,
-                                        char *b1, char *b2, char *b3)
+// Tile t of a lower triangle, in rows.
+__device__ __forceinline__ void triangle(int t, int &i, int &j)
 {
-    using D = Direct<LA, LB, BM, BN, 32, WI, WJ, MulF16, Planes<PLANES>>;
-    int ti, tj;
-    tile_of(id, P.tiles_i, P.tiles_j, ti, tj);
+    i = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+    while (i * (i + 1) / 2 > t) --i;
+    while ((i + 1) * (i + 2) / 2 <= t) ++i;
+    j = t - i * (i + 1) / 2;
+}
+
+// Tile t of ti x tj, in bands of eight rows.
+__device__ __forceinline__ void banded(int t, int ti, int tj, int &i, int &j)
+{
+    const int band = t / (8 * tj), first = band * 8, rows = ti - first < 8 ? ti - first : 8, in = t - band * 8 * tj;
+    i = first + in % rows;
+    j = in / rows;
+}
+
+template <int PLANES>
+__device__ __forceinline__ void read_planes(float (&x)[8], const Half *from, long long plane)
+{
+    Half h[8];
+    u32x4 w = *(const u32x4 *)from;
+    __builtin_memcpy(h, &w, 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = from_half(h[e]);
+    if (PLANES == 1) return;
+    w = *(const u32x4 *)(from + plane);
+    __builtin_memcpy(h, &w, 16);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] += from_half(h[e]);
+}
+
+template <int PLANES>
+__device__ __forceinline__ void write_planes(Half *to, long long plane, const float (&v)[8])
+{
+    Half hi[8], lo[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) to_planes(v[e], hi[e], lo[e]);
+    *(u32x4 *)to = __builtin_bit_cast(u32x4, hi);
+    if (PLANES == 2) *(u32x4 *)(to + plane) = __builtin_bit_cast(u32x4, lo);
+}
+
+template <int STAGE, int LA, int LB, int PLANES, int BM, int BN, int WI, int WJ>
+__device__ __forceinline__ void product(const Product &P, const Finish &F, int ti, int tj, int tile, int part, char *a0, char *a1,
+                                        char *a2, char *a3, char *b0, char *b1, char *b2, char *b3)
+{
+    using D = std::conditional_t<PLANES == 2, DirectPair<LA, LB, BM, BN, WI, WJ>, Direct<LA, LB, BM, BN, 32, WI, WJ, MulF16>>;
     D d;
-    d.ta.init(P.a, P.lda, ti * BM, P.I, P.K, 0);
-    d.tb.init(P.b, P.ldb, tj * BN, P.J, P.K, 0);
-    d.steps.per = (P.K + 31) / 32;
-    d.steps.plane_a = P.plane_a * 2;
-    d.steps.plane_b = P.plane_b * 2;
-    d.run(d.steps.per * (PLANES == 2 ? 3 : 1), a0, a1, a2, a3, b0, b1, b2, b3);
+    const int kb = part * P.steps * 32, kn = P.K - kb < P.steps * 32 ? P.K - kb : P.steps * 32;
+    d.ta.init(P.a, P.lda, ti * BM, P.I, kn, kb);
+    d.tb.init(P.b, P.ldb, tj * BN, P.J, kn, kb);
+    if constexpr (PLANES == 2) d.plane_a = P.plane_a * 2, d.plane_b = P.plane_b * 2;
+    d.run((kn + 31) / 32, a0, a1, a2, a3, b0, b1, b2, b3);
+    constexpr int TJ = D::TJ, FI = D::FI, FJ = D::FJ, PR = D::PR, kRow = TJ * 4, kMask = TJ / 4 - 1;
+    const int lane = threadIdx.x & 63, i0 = ti * BM + d.wi * D::TI, j0 = tj * BN + d.wj * TJ;
+    if (P.parts > 1) {
+        Args at{};
+        at.I = P.I, at.parts = P.parts, at.part = P.part, at.ticket = P.ticket;
+        if (!joined<FI, FJ, 64 * D::kWaves>(at, d.acc, tile, part, i0)) return;
+    }
 
     // a wave's part is turned around in LDS, so that a lane ends with eight neighbouring j of a row
-    constexpr int TJ = D::TJ, FI = D::FI, FJ = D::FJ, PR = D::PR, kRow = TJ * 4, kMask = TJ / 4 - 1;
     constexpr int kGroups = TJ / 8, kRows = 64 / kGroups, kRounds = PR / kRows;
-    const int lane = threadIdx.x & 63, i0 = ti * BM + d.wi * D::TI, j0 = tj * BN + d.wj * TJ;
     const int c = lane % kGroups * 8, j = j0 + c;
+    const bool mirror = STAGE != APPLY && ti != tj;
     lds_char *const buf = own_buffer(a0, a1, a2, a3, b0, b1, b2, b3);
 #pragma unroll
     for (int f0 = 0; f0 < FI; f0 += PR / 16) {
@@ -232,64 +449,231 @@ __device__ __forceinline__ void product(const Product &P, const Finish &F, int i
             const auto *src = (const __attribute__((address_space(3))) f32x4 *)(buf + r * kRow);
             const f32x4 lo4 = src[(c >> 2) ^ key], hi4 = src[((c >> 2) + 1) ^ key];
             if (i >= P.I || j >= P.J) continue;
-            float v[8];
+            float v[8], x[8];
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = lo4[e] * F.one, v[4 + e] = hi4[e] * F.one;
             const long long at = (long long)i * P.ldc + j;
-            if (P.with) {   // rows end with zeros, and so do sums over them
-                Half h[8];
-                u32x4 w = *(const u32x4 *)(P.with + at);
-                __builtin_memcpy(h, &w, 16);
-                float x[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = from_half(h[e]);
-                if (PLANES == 2) {
-                    w = *(const u32x4 *)(P.with + P.plane_c + at);
-                    __builtin_memcpy(h, &w, 16);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) x[e] += from_half(h[e]);
-                }
+            if (STAGE != GRAM) {   // rows end with zeros, and so do sums over them
+                read_planes<PLANES>(x, P.with + at, P.plane_c);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) v[e] = __builtin_fmaf(x[e], F.two, v[e]);
             }
-            if (!F.last) {
-                Half hi[8], lo[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) to_planes(v[e], hi[e], lo[e]);
-                *(u32x4 *)(P.c + at) = __builtin_bit_cast(u32x4, hi);
-                if (PLANES == 2) *(u32x4 *)(P.c + P.plane_c + at) = __builtin_bit_cast(u32x4, lo);
+            if (STAGE != APPLY || !F.last) {
+                write_planes<PLANES>(P.c + at, P.plane_c, v);
+                if (mirror) {   // finished, for the mirrored place
+                    auto *back = (__attribute__((address_space(3))) f32x4 *)(buf + r * kRow);
+                    back[(c >> 2) ^ key] = f32x4{v[0], v[1], v[2], v[3]};
+                    back[((c >> 2) + 1) ^ key] = f32x4{v[4], v[5], v[6], v[7]};
+                }
                 continue;
             }
             using T = std::conditional_t<PLANES == 2, float, bf16>;
-            T *p = (T *)P.p + (long long)i * P.J + j;
+            T *p = (T *)P.p + (long long)i * P.J + j, t[8];
             const float size = P.size * kUnscale;
+            if (j + 8 <= P.J) {
+                get(t, p);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                if (j + e >= P.J) continue;
-                const float x = widen(p[e]);
-                // one rounding for the decayed parameter: 1 - lr wd, held in 32 bits, would add its own
-                narrow(__builtin_fmaf(x, -F.decay, x) - size * v[e], p[e]);
+                for (int e = 0; e < 8; ++e) {
+                    const float y = widen(t[e]);
+                    // one rounding for the decayed parameter: 1 - lr wd, held in 32 bits, would add its own
+                    narrow(__builtin_fmaf(y, -F.decay, y) - size * v[e], t[e]);
+                }
+                put(p, t);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (j + e >= P.J) continue;
+                    const float y = widen(p[e]);
+                    narrow(__builtin_fmaf(y, -F.decay, y) - size * v[e], p[e]);
+                }
+            }
+        }
+        if (mirror) {   // eight rows of a column are eight neighbours of a row there; lanes beside each other take its next ones
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            constexpr int kDown = PR / 8, kAcross = 64 / kDown;
+            const int r0 = lane % kDown * 8, i = i0 + f0 * 16 + r0;
+#pragma unroll 2
+            for (int cj = lane / kDown; cj < TJ; cj += kAcross) {
+                const int jj = j0 + cj;
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    v[e] = *(const __attribute__((address_space(3))) float *)(buf + (r0 + e) * kRow +
+                                                                              (((cj >> 2) ^ ((r0 + e) & kMask & 15)) << 4) + (cj & 3) * 4);
+                if (jj < P.J && i < P.I) write_planes<PLANES>(P.c + (long long)jj * P.ldc + i, P.plane_c, v);
             }
         }
         asm volatile("" ::: "memory");
     }
 }
 
-template <int STAGE, int PLANES, int SIDE>
-__global__ __launch_bounds__(SIDE == 256 ? 512 : 256, 2) void k_product(Products G, Finish F)
+template <int STAGE, int PLANES, int SIDE, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 4 ? 1 : 2) void k_product(Products G, Finish F)
 {
-    constexpr int kBytes = SIDE * 64;
+    constexpr int kBytes = SIDE * 64 * PLANES;
+    static_assert(PLANES == 1 || SIDE <= 128, "room for two planes");
     __shared__ __attribute__((aligned(1024))) char a0[kBytes], a1[kBytes], a2[kBytes], a3[kBytes];
     __shared__ __attribute__((aligned(1024))) char b0[kBytes], b1[kBytes], b2[kBytes], b3[kBytes];
-    const int ti = matrix_of(G.first, G.count, blockIdx.x), id = blockIdx.x - G.first[ti];
-    const Product &P = G.t[ti];
-    if (id >= P.tiles_i * P.tiles_j) return;
+    const int m = matrix_of(G.first, G.count, blockIdx.x);
+    const Product &P = G.t[m];
+    // Workgroups go round the eight XCDs in turn; each XCD takes a run of the product's tiles, part by part, so that what it
+    // works on together shares rows and k in its L2.
+    const int id = blockIdx.x - G.first[m], units = P.tiles * P.parts, xcd = id & 7, q = units >> 3, r = units & 7;
+    if ((id >> 3) >= q + (xcd < r ? 1 : 0)) return;
+    const int unit = xcd * q + (xcd < r ? xcd : r) + (id >> 3), part = unit / P.tiles, tile = unit - part * P.tiles;
+    int ti, tj;
+    if (P.skip < 0) {
+        if (STAGE != APPLY) triangle(tile, ti, tj);
+        else banded(tile, P.tiles_i, P.tiles_j, ti, tj);
+    } else {   // quarters of larger tiles
+        const int large = P.skip + (tile >> 2);
+        if (STAGE != APPLY) triangle(large, ti, tj);
+        else banded(large, (P.tiles_i + 1) >> 1, (P.tiles_j + 1) >> 1, ti, tj);
+        ti = ti * 2 + ((tile >> 1) & 1), tj = tj * 2 + (tile & 1);
+        if (ti >= P.tiles_i || tj >= P.tiles_j || (STAGE != APPLY && tj > ti)) return;
+    }
     // 256 x 256: waves of 64 x 128 where both operands lie along k, of 128 x 64 elsewhere, as the dense layer's
-    constexpr int WI = 2, WJ = SIDE == 256 ? 4 : 2, WIR = SIDE == 256 ? 4 : 2, WJR = 2;
-    if (STAGE == POLY || (STAGE == GRAM && !P.cols) || (STAGE == APPLY && !P.cols))
-        product<K_ROWS, K_ROWS, PLANES, SIDE, SIDE, WIR, WJR>(P, F, id, a0, a1, a2, a3, b0, b1, b2, b3);
-    else if (STAGE == GRAM) product<K_COLS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, id, a0, a1, a2, a3, b0, b1, b2, b3);
-    else product<K_ROWS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, id, a0, a1, a2, a3, b0, b1, b2, b3);
+    constexpr int WI = 2, WJ = WAVES / 2, WIR = WAVES / 2, WJR = 2;
+    if (STAGE == POLY || !P.cols)
+        product<STAGE, K_ROWS, K_ROWS, PLANES, SIDE, SIDE, WIR, WJR>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+    else if (STAGE == GRAM)
+        product<STAGE, K_COLS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+    else
+        product<STAGE, K_ROWS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+}
+
+// ---- small matrices ----
+//
+// A workgroup takes a whole matrix through the whole step: X (the smaller side as rows), A and B in fp32 in LDS, products by the
+// fp32 matrix instruction, nothing rounded to fewer bits.  What counts is latency: three products and as many barriers a
+// step, one launch instead of 2 + 3 for each step.
+
+constexpr int kSmallSide = 64, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallLds = 160 * 1024 - 1024;
+constexpr long long kSmallWork = 1 << 20;   // multiply-adds of X X^T
+
+__host__ __device__ inline int pad16(int n) { return (n + 15) & ~15; }
+
+struct SmallSize {
+    int n, m, ldx, lda;   // sides, padded; floats from a row to the next, four more than they hold: other banks
+    __host__ __device__ SmallSize(int rows, int cols)
+        : n(pad16(rows < cols ? rows : cols)), m(pad16(rows < cols ? cols : rows)), ldx(m + 4), lda(n + 4)
+    {
+    }
+    __host__ __device__ size_t bytes() const { return ((size_t)n * ldx + 2 * (size_t)n * lda + kSmallWaves * 256) * 4; }
+};
+
+bool is_small(int rows, int cols)
+{
+    const SmallSize z(rows, cols);
+    return z.n <= kSmallSide && z.bytes() <= (size_t)kSmallLds && (long long)z.n * z.n * z.m <= kSmallWork;
+}
+
+// Four k of a 16 x 16 block: lane % 16 is the row of either operand, lane / 16 its k.
+__device__ __forceinline__ f32x4 multiply(float b, float a, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(b, a, c, 0, 0, 0); }
+
+template <typename T, typename G>
+__global__ __launch_bounds__(kSmallThreads) void k_small(Batch batch, Scalars k, int steps)
+{
+    extern __shared__ float small_lds[];
+    __shared__ double part[kSmallWaves];
+    const Matrix &t = batch.t[blockIdx.x];
+    const SmallSize z(t.rows, t.cols);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4, nt = z.n / 16;
+    const bool tall = t.rows > t.cols;
+    float *X = small_lds, *A = X + z.n * z.ldx, *B = A + z.n * z.lda, *P = B + z.n * z.lda;
+    const G *g = (const G *)t.g;
+    T *p = (T *)t.p;
+    const int all = t.rows * t.cols;
+    for (int i = threadIdx.x; i < z.n * z.ldx; i += kSmallThreads) X[i] = 0.0f;
+    __syncthreads();
+    double sum = 0.0;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < all; i += kSmallThreads) {
+        const float gi = widen(g[i]), m = t.m[i] * k.mu + gi * k.nu, u = update_of(k, m, gi);
+        t.m[i] = m;
+        const int r = i / t.cols, c = i - r * t.cols;
+        X[tall ? c * z.ldx + r : r * z.ldx + c] = u;
+        sum += (double)u * u;
+    }
+#pragma unroll
+    for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
+    if (lane == 0) part[wave] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSmallWaves; ++w) sum += part[w];
+    const double norm = sqrt(sum);
+    const float inv = (float)(1.0 / (norm <= (double)k.eps ? (double)k.eps : norm));
+    for (int i = threadIdx.x; i < z.n * z.ldx; i += kSmallThreads) X[i] *= inv;
+    __syncthreads();
+    const int tiles = nt * (nt + 1) / 2, parts = kSmallWaves / tiles;   // of A; each wave a tile's part of k
+    int ti = 0, tj = wave % tiles;
+    while (tj > ti) tj -= ++ti;   // tile of a lower triangle, in rows
+    const int kp = wave / tiles, fours = z.m / 4, each = (fours + parts - 1) / parts;
+    for (int step = 0; step < steps; ++step) {
+        if (kp < parts) {   // A = X X^T
+            f32x4 s[2] = {};
+            const float *a = X + (ti * 16 + row) * z.ldx + quad, *b = X + (tj * 16 + row) * z.ldx + quad;
+            const int last = (kp + 1) * each < fours ? (kp + 1) * each : fours;
+            int f = kp * each;
+            for (; f + 2 <= last; f += 2) {
+                s[0] = multiply(b[f * 4], a[f * 4], s[0]);
+                s[1] = multiply(b[f * 4 + 4], a[f * 4 + 4], s[1]);
+            }
+            if (f < last) s[0] = multiply(b[f * 4], a[f * 4], s[0]);
+            *(f32x4 *)(P + wave * 256 + row * 16 + quad * 4) = s[0] + s[1];
+        }
+        __syncthreads();
+        for (int i = threadIdx.x; i < tiles * 256; i += kSmallThreads) {
+            const int tile = i >> 8, r = (i >> 4) & 15, c = i & 15;
+            int bi = 0, bj = tile;
+            while (bj > bi) bj -= ++bi;
+            float s = 0.0f;
+            for (int q = 0; q < parts; ++q) s += P[(q * tiles + tile) * 256 + (i & 255)];
+            A[(bi * 16 + r) * z.lda + bj * 16 + c] = s;
+            if (bi != bj) A[(bj * 16 + c) * z.lda + bi * 16 + r] = s;
+        }
+        __syncthreads();
+        if (kp == 0) {   // B = b A + c A^2
+            f32x4 s = {};
+            const float *a = A + (ti * 16 + row) * z.lda + quad, *b = A + (tj * 16 + row) * z.lda + quad;
+#pragma unroll 4
+            for (int f = 0; f < nt * 4; ++f) s = multiply(b[f * 4], a[f * 4], s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = ti * 16 + row, j = tj * 16 + quad * 4 + e;
+                const float v = __builtin_fmaf(k.b, A[i * z.lda + j], k.c * s[e]);
+                B[i * z.lda + j] = v;
+                if (ti != tj) B[j * z.lda + i] = v;
+            }
+        }
+        __syncthreads();
+        for (int cb = wave; cb < z.m / 16; cb += kSmallWaves) {   // X = a X + B X, sixteen columns a wave: no other reads them
+            f32x4 s[kSmallSide / 16] = {};
+            for (int f = 0; f < nt * 4; ++f) {
+                const float x = X[(f * 4 + quad) * z.ldx + cb * 16 + row];
+#pragma unroll
+                for (int it = 0; it < kSmallSide / 16; ++it)
+                    if (it < nt) s[it] = multiply(x, B[(it * 16 + row) * z.lda + f * 4 + quad], s[it]);
+            }
+#pragma unroll
+            for (int it = 0; it < kSmallSide / 16; ++it) {
+                if (it >= nt) continue;
+                f32x4 *at = (f32x4 *)(X + (it * 16 + row) * z.ldx + cb * 16 + quad * 4);
+                const f32x4 x = *at;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[it][e] = __builtin_fmaf(k.a, x[e], s[it][e]);
+                *at = s[it];
+            }
+        }
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < all; i += kSmallThreads) {
+        const int r = i / t.cols, c = i - r * t.cols;
+        const float y = widen(p[i]);
+        narrow(__builtin_fmaf(y, -k.decay, y) - t.size * X[tall ? c * z.ldx + r : r * z.ldx + c], p[i]);
+    }
 }
 
 // ---- a call ----
@@ -311,6 +695,11 @@ Bytes bytes_of(const hqml_muon_tensor &t, int planes)
     return b;
 }
 
+// Partial sums of a launch: at most this much, in tiles that at most so many tickets count.
+constexpr size_t kPartBytes = 64ull << 20;
+constexpr int kTickets = 4096;
+constexpr size_t kJoinBytes = kPartBytes + kTickets * sizeof(unsigned);
+
 int planes_of(const hqml_muon_config &cfg) { return cfg.param_dtype == HQML_DTYPE_FP32 ? 2 : 1; }
 
 // Calls f(first, last, bytes) for each round of matrices that go together.
@@ -319,57 +708,167 @@ void rounds(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, F f)
 {
     for (int i = 0; i < n;) {
         size_t bytes = 0;
-        int last = i, count = 0;
-        for (; last < n && count < kMatrices; ++last) {
+        int last = i, large = 0, small = 0;
+        for (; last < n && large < kMatrices && small < kMatrices; ++last) {
             if (!t[last].rows || !t[last].cols) continue;
+            if (is_small(t[last].rows, t[last].cols)) {
+                ++small;
+                continue;
+            }
             const size_t here = bytes_of(t[last], planes_of(cfg)).all();
-            if (count && bytes + here > kBatchBytes) break;
+            if (large && bytes + here > kBatchBytes) break;
             bytes += here;
-            ++count;
+            ++large;
         }
-        if (count) f(i, last, bytes);
+        if (large || small) f(i, last, large ? bytes + kJoinBytes : 0);
         i = last;
     }
 }
 
-// Tile side of a launch: times in us as the dense layer's estimate has them.
-int side_of(const Products &G, int planes)
+// All tiles of a product.
+int tiles_of(const Product &P, int side)
 {
-    static constexpr struct {
-        int side, most;
-        float fixed, step, share;
-    } kCost[] = {{64, 4, 2.6f, 0.18f, 0.137f}, {128, 2, 4.6f, 0.2f, 0.24f}, {256, 1, 8.6f, 0.45f, 0.525f}};
-    int best = 64;
-    float least = 0.0f;
-    for (const auto &c : kCost) {
-        float steps = 0.0f, longest = 0.0f;
-        for (int i = 0; i < G.count; ++i) {
-            const Product &P = G.t[i];
-            const float own = (float)(ceil_div(P.K, 32) * (planes == 2 ? 3 : 1));
-            steps += own * (float)ceil_div(P.I, c.side) * (float)ceil_div(P.J, c.side);
-            longest = std::max(longest, own);
+    const int i = ceil_div(P.I, side), j = ceil_div(P.J, side);
+    return P.mirrored ? i * (i + 1) / 2 : i * j;
+}
+
+int steps_of(const Product &P) { return ceil_div(P.K, 32); }
+
+// A kernel's times in us, as the dense layer's TileCost: a step of a workgroup alone on its compute unit, and of n of them
+// n share; launch and epilogue; joining parts.  Fitted to sweeps of sides and parts over the three products of matrices of 300 x
+// 200 to 4096 x 4096.
+constexpr TileCost kOneCost[] = {{TILE_64, 4, 3.0f, 0.2f, 0.165f, 0.65f, 0.42f},
+                                 {TILE_128, 2, 5.0f, 0.32f, 0.36f, 2.0f, 1.06f},
+                                 {TILE_256, 1, 10.0f, 0.66f, 0.88f, 4.6f, 4.0f}};
+constexpr TileCost kPairCost[] = {{TILE_64, 2, 4.5f, 0.33f, 0.43f, 0.65f, 0.42f}, {TILE_128, 1, 10.0f, 0.52f, 0.7f, 2.0f, 1.06f}};
+
+struct Pieces {
+    int side, steps;   // tile side, steps of a part
+    float us;
+};
+
+// How tiles[i] tiles of side `side` of the products are cut best, with kernels of up to that side.  A tile makes four of half
+// its side.
+Pieces cut_of(const Products &G, const int *tiles, int side, int planes, bool smaller)
+{
+    Pieces best{0, 1 << 30, 0.0f};
+    int most = 0;
+    for (int i = 0; i < G.count; ++i)
+        if (tiles[i]) most = std::max(most, steps_of(G.t[i]));
+    const TileCost *cost = planes == 2 ? kPairCost : kOneCost;
+    for (int n_cost = planes == 2 ? 2 : 3; n_cost > 0; --n_cost, ++cost) {
+        const TileCost &c = *cost;
+        const int own = kSides[c.shape][0];
+        if (own != (smaller ? side / 2 : side)) continue;
+        int last = 0;
+        for (int parts : kParts) {
+            const int u = ceil_div(most, parts);
+            if (u == last || (parts > 1 && u < 4)) continue;
+            last = u;
+            long long groups = 0, split = 0, joins = 0;
+            float work = 0.0f;
+            for (int i = 0; i < G.count; ++i) {
+                const int steps = steps_of(G.t[i]), n = ceil_div(steps, u);
+                const long long t = smaller ? tiles[i] * 4 : tiles[i];
+                groups += t * n;
+                work += (float)t * (float)steps;
+                if (n > 1) split += t * n, joins += t;
+            }
+            if (split * own * own * 4 > (long long)kPartBytes || joins > kTickets) continue;
+            // a compute unit's workgroups share it, or, of the largest tiles, come one after the other; shorter ones than the
+            // longest fill in
+            const float each = (float)groups / kUnits, even = std::min(each, work / kUnits / (float)u + 1.0f);
+            const float whole = floorf(even), last_round = even - whole;
+            const float busy = c.most > 1 ? std::max(c.step, even * c.share)
+                                          : whole * c.share + (last_round > 0.0f ? std::max(c.step, last_round * c.share) : 0.0f);
+            float us = c.fixed + (float)u * busy + (float)own / 160 * each;
+            if (split) us += c.join + (float)parts * c.join_part + (float)split * (own * own * 8) / 9e6f;
+            if (!best.side || us < best.us) best = {own, u, us};
         }
-        const float us = c.fixed + std::max(longest * c.step, steps * c.share / kUnits);
-        if (c.side == 64 || us < least) least = us, best = c.side;
+    }
+    return best;
+}
+
+// How a stage runs: `first` tiles of a side, the rest, if any, as quarters of them in a second launch.
+struct Plan {
+    Pieces main, rest;
+    int first;
+};
+
+// A compute unit holds one workgroup of the largest tiles, so those that go beyond whole rounds of all compute units would take
+// a round of their own: quarters of them, split along k, take less.  Two 4096 x 4096, X X^T of one plane: 272 tiles of 256 in two
+// rounds 206 us.
+Plan plan_of(const Products &G, int planes)
+{
+    Plan best{{0, 0, 0.0f}, {0, 0, 0.0f}, 0};
+    int tiles[kMatrices], rest[kMatrices];
+    for (int side : {64, 128, 256}) {
+        long long all = 0;
+        for (int i = 0; i < G.count; ++i) all += tiles[i] = tiles_of(G.t[i], side);
+        if (all > 1 << 28) continue;   // tiles in 32 bits, quarters among them
+        const Pieces whole = cut_of(G, tiles, side, planes, false);
+        if (whole.side && (!best.main.side || whole.us < best.main.us + best.rest.us)) best = {whole, {0, 0, 0.0f}, (int)all};
+        const int first = (int)(all / kUnits) * kUnits;
+        if (side < (planes == 2 ? 128 : 256) || !first || first == all) continue;
+        int left = first;
+        for (int i = 0; i < G.count; ++i) {
+            const int here = std::min(left, tiles[i]);
+            left -= here;
+            rest[i] = tiles[i] - here, tiles[i] = here;
+        }
+        const Pieces rounds = cut_of(G, tiles, side, planes, false), quarters = cut_of(G, rest, side, planes, true);
+        if (rounds.side && quarters.side && rounds.us + quarters.us < best.main.us + best.rest.us) best = {rounds, quarters, first};
     }
     return best;
 }
 
 template <int STAGE, int PLANES>
-hipError_t run_stage(Products &G, const Finish &F, hipStream_t s)
+hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *tiles, const int *skip, float *part, unsigned *ticket,
+                   hipStream_t s)
 {
-    const int side = side_of(G, PLANES);
     unsigned at = 0;
+    float *part_end = part + kPartBytes / 4;
+    unsigned *ticket_end = ticket + kTickets;
     for (int i = 0; i < G.count; ++i) {
         Product &P = G.t[i];
-        P.tiles_i = ceil_div(P.I, side), P.tiles_j = ceil_div(P.J, side);
+        P.tiles_i = ceil_div(P.I, cut.side), P.tiles_j = ceil_div(P.J, cut.side);
+        P.skip = skip ? skip[i] : -1;
+        P.tiles = skip ? tiles[i] * 4 : tiles[i];
+        P.steps = std::min(cut.steps, steps_of(P));
+        P.parts = ceil_div(steps_of(P), P.steps);
+        if (P.parts > 1 && P.tiles) {
+            P.part = part, P.ticket = ticket;
+            if ((long long)P.tiles * P.parts * cut.side * cut.side > part_end - part || P.tiles > ticket_end - ticket)
+                return hipErrorInvalidValue;
+            part += (size_t)P.tiles * P.parts * cut.side * cut.side;
+            ticket += P.tiles;
+        }
         G.first[i] = at;
-        at += ((unsigned)P.tiles_i * (unsigned)P.tiles_j + 7) & ~7u;
+        at += ((unsigned)P.tiles * (unsigned)P.parts + 7) & ~7u;
     }
-    if (side == 64) k_product<STAGE, PLANES, 64><<<at, 256, 0, s>>>(G, F);
-    else if (side == 128) k_product<STAGE, PLANES, 128><<<at, 256, 0, s>>>(G, F);
-    else k_product<STAGE, PLANES, 256><<<at, 512, 0, s>>>(G, F);
+    if (cut.side == 64) k_product<STAGE, PLANES, 64, 4><<<at, 256, 0, s>>>(G, F);
+    else if (PLANES == 1 && cut.side == 128) k_product<STAGE, 1, 128, 4><<<at, 256, 0, s>>>(G, F);
+    else if (PLANES == 2) k_product<STAGE, 2, 128, 8><<<at, 512, 0, s>>>(G, F);
+    else k_product<STAGE, 1, 256, 8><<<at, 512, 0, s>>>(G, F);
     return hipGetLastError();
+}
+
+template <int STAGE, int PLANES>
+hipError_t run_stage(Products &G, const Finish &F, float *part, unsigned *ticket, hipStream_t s)
+{
+    const Plan plan = plan_of(G, PLANES);
+    if (!plan.main.side) return hipErrorInvalidValue;
+    int tiles[kMatrices], skip[kMatrices], left = plan.first;
+    for (int i = 0; i < G.count; ++i) {
+        const int all = tiles_of(G.t[i], plan.main.side);
+        tiles[i] = std::min(left, all);
+        left -= tiles[i];
+        skip[i] = tiles[i];
+    }
+    hipError_t e = run_cut<STAGE, PLANES>(G, F, plan.main, tiles, nullptr, part, ticket, s);
+    if (e != hipSuccess || !plan.rest.side) return e;
+    for (int i = 0; i < G.count; ++i) tiles[i] = tiles_of(G.t[i], plan.main.side) - skip[i];
+    return run_cut<STAGE, PLANES>(G, F, plan.rest, tiles, skip, part, ticket, s);
 }
 
 template <typename G, int PLANES>
@@ -381,7 +880,7 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     k.eps = (float)cfg.eps;
     k.decay = (float)(cfg.lr * cfg.weight_decay);
     k.a = (float)cfg.a, k.b = (float)cfg.b, k.c = (float)cfg.c;
-    Batch b{};
+    Batch b{}, few{};   // large matrices, small ones
     unsigned groups = 0;
     auto each = [&](auto count_of) {   // first workgroups
         groups = 0;
@@ -392,11 +891,13 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     };
     for (int i = 0; i < n; ++i) {
         if (!t[i].rows || !t[i].cols) continue;
+        const bool small = is_small(t[i].rows, t[i].cols);
         const Bytes z = bytes_of(t[i], PLANES);
-        Matrix &m = b.t[b.count++];
+        Matrix &m = small ? few.t[few.count++] : b.t[b.count++];
         m.p = t[i].param, m.g = t[i].grad, m.m = t[i].momentum;
         m.rows = t[i].rows, m.cols = t[i].cols;
         m.size = (float)(cfg.lr * t[i].scale);
+        if (small) continue;
         auto take = [&](size_t bytes) {
             char *here = work;
             work += bytes;
@@ -406,10 +907,23 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
         m.a = (Half *)take(z.gram), m.b = (Half *)take(z.gram);
         m.sums = (double *)take(z.sums);
     }
+    hipError_t e = hipSuccess;
+    if (few.count) {
+        using T = std::conditional_t<PLANES == 2, float, bf16>;
+        size_t lds = 0;
+        for (int i = 0; i < few.count; ++i) lds = std::max(lds, SmallSize(few.t[i].rows, few.t[i].cols).bytes());
+        if (lds > 32 * 1024) {   // with what the kernel holds besides, more than a launch may take unasked
+            e = hipFuncSetAttribute((const void *)k_small<T, G>, hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+            if (e != hipSuccess) return e;
+        }
+        k_small<T, G><<<few.count, kSmallThreads, lds, s>>>(few, k, cfg.steps);
+        if ((e = hipGetLastError()) != hipSuccess || !b.count) return e;
+    }
+    float *const part = (float *)work;
+    unsigned *const ticket = (unsigned *)(work + kPartBytes);
     each([](const Matrix &m) { return (unsigned)(((long long)m.rows * m.cols + kChunk - 1) / kChunk); });
-    k_momentum<G><<<groups, 256, 0, s>>>(b, k);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+    k_momentum<G><<<groups, 256, 0, s>>>(b, k, ticket, kTickets);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
     each([](const Matrix &m) { return (unsigned)std::min<long long>(((long long)m.rows * pad8(m.cols) / 8 + 255) / 256, 4096); });
     k_begin<G, PLANES><<<groups, 256, 0, s>>>(b, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
@@ -427,12 +941,12 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
             A.a = A.b = x, A.c = m.a;
             A.lda = A.ldb = ldx, A.ldc = lda;
             A.plane_a = A.plane_b = plane_x, A.plane_c = plane_a;
-            A.I = A.J = small, A.K = tall ? m.rows : m.cols, A.cols = tall;
+            A.I = A.J = small, A.K = tall ? m.rows : m.cols, A.cols = tall, A.mirrored = true;
             Product &B = poly.t[i];
             B.a = B.b = B.with = m.a, B.c = m.b;
             B.lda = B.ldb = B.ldc = lda;
             B.plane_a = B.plane_b = B.plane_c = plane_a;
-            B.I = B.J = B.K = small;
+            B.I = B.J = B.K = small, B.mirrored = true;
             Product &X = apply.t[i];
             X.a = tall ? x : m.b, X.b = tall ? m.b : x, X.with = x, X.c = m.x[1 - (step & 1)];
             X.lda = tall ? ldx : lda, X.ldb = tall ? lda : ldx, X.ldc = ldx;
@@ -440,9 +954,9 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
             X.I = m.rows, X.J = m.cols, X.K = small, X.cols = !tall;
             X.p = m.p, X.size = m.size;
         }
-        if ((e = run_stage<GRAM, PLANES>(gram, {kUnscale, 0.0f, 0.0f, 0}, s)) != hipSuccess) return e;
-        if ((e = run_stage<POLY, PLANES>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, s)) != hipSuccess) return e;
-        if ((e = run_stage<APPLY, PLANES>(apply, {kUnscale, k.a, k.decay, last}, s)) != hipSuccess) return e;
+        if ((e = run_stage<GRAM, PLANES>(gram, {kUnscale, 0.0f, 0.0f, 0}, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<POLY, PLANES>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<APPLY, PLANES>(apply, {kUnscale, k.a, k.decay, last}, part, ticket, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }

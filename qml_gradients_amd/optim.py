@@ -290,8 +290,8 @@ class Muon(torch.optim.Optimizer):
                 array = (hqml_muon_tensor * len(tensors))(*tensors)
                 need = hqml_muon_workspace_bytes(cfg, len(tensors), array)
                 # torch's memory: freed at once, it is handed out again only to what the stream runs later
-                work = torch.empty(need, dtype=torch.uint8, device=params[0].device)
-                hqml_muon_step(cfg, len(tensors), array, work.data_ptr(), need)
+                work = torch.empty(need, dtype=torch.uint8, device=params[0].device) if need else None
+                hqml_muon_step(cfg, len(tensors), array, work.data_ptr() if need else None, need)
                 # a backward pass that saved a parameter from before this step has to refuse it
                 torch.autograd.graph.increment_version(params)
         return loss

@@ -231,11 +231,11 @@ def test_saved_and_loaded():
 def test_refusals():
     import qml_gradients_amd as hq
     from qml_gradients_amd.optim import Muon
-    p = torch.nn.Parameter(torch.randn(16, 8, device="cuda"))
-    p.grad = torch.randn(16, 8, device="cuda")
-    m = torch.zeros(16, 8, device="cuda")
+    p = torch.nn.Parameter(torch.randn(160, 80, device="cuda"))
+    p.grad = torch.randn(160, 80, device="cuda")
+    m = torch.zeros(160, 80, device="cuda")
     cfg = hq.hqml_muon_config(0, 0, 1, 5, 0.1, 0.9, 0.0, 1e-7, *COEFFICIENTS, 0, None)
-    t = hq.hqml_muon_tensor(p.data_ptr(), p.grad.data_ptr(), m.data_ptr(), 16, 8, 1.0)
+    t = hq.hqml_muon_tensor(p.data_ptr(), p.grad.data_ptr(), m.data_ptr(), 160, 80, 1.0)
     need = hq.hqml_muon_workspace_bytes(cfg, 1, (hq.hqml_muon_tensor * 1)(t))
     work = torch.empty(need, dtype=torch.uint8, device="cuda")
 
@@ -257,6 +257,6 @@ def test_refusals():
         with pytest.raises(ValueError):
             Muon([torch.nn.Parameter(bad)])
     opt = Muon([p])
-    opt.state[p]["momentum"] = torch.zeros(8, 16, device="cuda")
+    opt.state[p]["momentum"] = torch.zeros(80, 160, device="cuda")
     with pytest.raises(ValueError):
         opt.step()

@@ -62,7 +62,7 @@ def _muon(**change):
                                  dict(eps=math.inf), dict(a=17.0), dict(b=math.nan), dict(c=-math.inf), dict(device=-1)])
 def test_muon_configurations_refused(bad):
     _lib()
-    t = (hq.hqml_muon_tensor * 1)(hq.hqml_muon_tensor(None, None, None, 8, 8, 1.0))
+    t = (hq.hqml_muon_tensor * 1)(hq.hqml_muon_tensor(None, None, None, 100, 100, 1.0))
     assert hq.hqml_muon_workspace_bytes(_muon(), 1, t) > 0
     assert hq.hqml_muon_workspace_bytes(_muon(**bad), 1, t) == 0
     with pytest.raises(hq.HqmlError) as e:
@@ -71,16 +71,19 @@ def test_muon_configurations_refused(bad):
 
 
 def test_muon_workspace():
-    """Two X and two of the smaller side's square for each matrix, rounds of up to 1 GiB."""
+    """Two X and two of the smaller side's square for each matrix, rounds of up to 1 GiB, and 64 MiB and 16 KiB of partial sums
+    and counters; nothing for small matrices."""
     _lib()
+    joins = (64 << 20) + (16 << 10)
     array = lambda *sizes: (hq.hqml_muon_tensor * len(sizes))(*[hq.hqml_muon_tensor(None, None, None, r, c, 1.0) for r, c in sizes])
-    one = hq.hqml_muon_workspace_bytes(_muon(), 1, array((1024, 4096)))
+    one = hq.hqml_muon_workspace_bytes(_muon(), 1, array((1024, 4096))) - joins
     assert one >= 2 * 4 * (1024 * 4096 + 1024 * 1024)
-    assert hq.hqml_muon_workspace_bytes(_muon(param_dtype=1), 1, array((1024, 4096))) <= one // 2 + 4096
-    assert hq.hqml_muon_workspace_bytes(_muon(), 3, array((1024, 4096), (4096, 1024), (0, 7))) <= 2 * one + 4096
-    many = hq.hqml_muon_workspace_bytes(_muon(), 200, array(*[(1024, 4096)] * 200))
+    assert hq.hqml_muon_workspace_bytes(_muon(param_dtype=1), 1, array((1024, 4096))) - joins <= one // 2 + 8192
+    assert hq.hqml_muon_workspace_bytes(_muon(), 3, array((1024, 4096), (4096, 1024), (0, 7))) - joins <= 2 * one + 4096
+    many = hq.hqml_muon_workspace_bytes(_muon(), 200, array(*[(1024, 4096)] * 200)) - joins
     assert one < many <= (1 << 30)
     assert hq.hqml_muon_workspace_bytes(_muon(), 1, array((0, 7))) == 0
+    assert hq.hqml_muon_workspace_bytes(_muon(), 2, array((32, 64), (4, 64))) == 0
     assert hq.hqml_muon_workspace_bytes(_muon(), 0, None) == 0
     hq.hqml_muon_step(_muon(), 1, array((0, 7)), None, 0)   # no elements: nothing to do
     for bad in ((-1, 4), (4, -1), ((1 << 16) + 1, 4), (4, (1 << 16) + 1)):
