@@ -169,7 +169,7 @@ def load() -> ctypes.CDLL:
     cfgp = ctypes.POINTER(hqml_config)
     densep = ctypes.POINTER(hqml_dense_config)
     normp = ctypes.POINTER(hqml_norm_config)
-    muonp, matrixp = ctypes.POINTER(hqml_muon_config), ctypes.POINTER(hqml_muon_tensor)
+    muonp = ctypes.POINTER(hqml_muon_config)
     sig = {
         "hqml_workspace_bytes": (ctypes.c_size_t, [cfgp]),
         "hqml_create": (i, [cfgp, ctypes.POINTER(P)]),
@@ -208,8 +208,8 @@ def load() -> ctypes.CDLL:
         "hqml_norm_last_error": (ctypes.c_char_p, [P]),
         "hqml_norm_forward": (i, [P, i, i, P, ll, P, P, P, ll, P, P]),
         "hqml_norm_backward": (i, [P, i, i, P, ll, P, ll, P, P, P, P, P, ll, P, P]),
-        "hqml_muon_workspace_bytes": (ctypes.c_size_t, [muonp, i, matrixp]),
-        "hqml_muon_step": (i, [muonp, i, matrixp, P, ctypes.c_size_t]),
+        "hqml_muon_workspace_bytes": (ctypes.c_size_t, [muonp, i, P]),
+        "hqml_muon_step": (i, [muonp, i, P, P, ctypes.c_size_t]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -433,7 +433,7 @@ def hqml_norm_backward(h, B, S, dy_ptr, lddy, x_ptr, ldx, gamma_ptr, beta_ptr, m
 
 
 def hqml_muon_workspace_bytes(cfg: hqml_muon_config, n_tensors, tensors) -> int:
-    """tensors: a ctypes array of hqml_muon_tensor."""
+    """tensors: a ctypes array of hqml_muon_tensor, or their bytes."""
     return int(load().hqml_muon_workspace_bytes(ctypes.byref(cfg), int(n_tensors), tensors))
 
 
@@ -839,6 +839,12 @@ class GroupNorm(_Layer):
             raise ValueError(f"expected {self.C} channels, got {tuple(shape)}")
         return shape, shape[0], S
 
+    def _like(self, x, shape):
+        """An array without gaps; `x`, if it has none, is the quicker way to one."""
+        if x.is_contiguous():
+            return self.torch.empty_like(x)
+        return self.torch.empty(shape, dtype=self.dtype, device=self.device)
+
     def _parameter(self, t, name):
         if t is None:
             return None
@@ -850,14 +856,14 @@ class GroupNorm(_Layer):
         x, ldx = self._positions(x, shape, "x")
         weight, bias = self._parameter(weight, "weight"), self._parameter(bias, "bias")
         if out is None:
-            y, ldy = self.torch.empty(shape, dtype=self.dtype, device=self.device), self.C
+            y, ldy = self._like(x, shape), self.C
         else:
             y, ldy = self._positions(out, shape, "out")
             if y is not out:
                 raise ValueError("out must have evenly strided positions")
         mean = rstd = None
         if keep:
-            mean, rstd = self.torch.empty((2, B, self.G), dtype=self.torch.float32, device=self.device)
+            mean, rstd = self.torch.empty((2, B, self.G), dtype=self.torch.float32, device=self.device).unbind()
         self._queue(self._lib.hqml_norm_forward, B, S, x.data_ptr(), ldx, None if weight is None else weight.data_ptr(),
                     None if bias is None else bias.data_ptr(), y.data_ptr(), ldy, mean.data_ptr() if keep else None,
                     rstd.data_ptr() if keep else None)
@@ -883,10 +889,10 @@ class GroupNorm(_Layer):
         for t, name in ((mean, "mean"), (rstd, "rstd")):
             self._check(t, (B, self.G), name, self.torch.float32)
         mean, rstd = mean.contiguous(), rstd.contiguous()
-        dx = self.torch.empty(shape, dtype=self.dtype, device=self.device) if input else None
+        dx = self._like(x, shape) if input else None
         dw = db = None
         if parameters:
-            dw, db = self.torch.empty((2, self.C), dtype=self.dtype, device=self.device)
+            dw, db = self.torch.empty((2, self.C), dtype=self.dtype, device=self.device).unbind()
         self._queue(self._lib.hqml_norm_backward, B, S, dy.data_ptr(), lddy, x.data_ptr(), ldx,
                     None if weight is None else weight.data_ptr(), None if bias is None else bias.data_ptr(),
                     mean.data_ptr(), rstd.data_ptr(), dx.data_ptr() if input else None, self.C,

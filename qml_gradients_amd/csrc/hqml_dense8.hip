@@ -27,7 +27,7 @@ using namespace gemm;
 
 // What a row's codes are formed with: code = rint(x num / den).
 struct RowScale {
-    float num, den, inv;   // inv = num / den, rounded
+    float num, den, inv;   // inv = num / den, rounded; x num does not overflow
 };
 
 __device__ __forceinline__ RowScale row_scale(uint32_t bits, float &scale)
@@ -42,51 +42,72 @@ __device__ __forceinline__ RowScale row_scale(uint32_t bits, float &scale)
         return {0x1p100f, 1.0f, 0x1p100f};
     }
     scale = size / 127.0f;
-    return {127.0f, size, 127.0f / size};
+    const float less = size > 0x1p100f ? 0x1p-20f : 1.0f;
+    return {127.0f * less, size * less, 127.0f / size};
 }
 
-__device__ __forceinline__ int code_of(float x, const RowScale &s)
-{
-    if (s.num == 0.0f) return 0;
-    const float t = x * s.inv, k = __builtin_rintf(t);
-    // t is off by up to 2^-16: a quotient next to the middle of two codes is decided in 64 bits, where x num is exact and
-    // a quotient that is not a tie rounds to none (it is at least 2^-26 of itself away)
-    if (__builtin_fabsf(t - k) < 0.5f - 0x1p-13f) return (int)k;
-    return (int)__builtin_rint((double)x * (double)s.num / (double)s.den);
-}
-
-// Largest magnitude as bits: magnitudes order as integers, and a NaN is above them all.
+// The largest of a wave, in all its lanes; magnitudes as bits order as integers, and a NaN is above them all.
 __device__ __forceinline__ uint32_t wave_max(uint32_t b)
 {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)b, m, 64);
-        b = b > o ? b : o;
-    }
+    auto with = [&](uint32_t other) { b = b > other ? b : other; };
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x141, 0xF, 0xF, true));   // mirrored in eight
+    with((uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, 0x140, 0xF, 0xF, true));   // mirrored in sixteen
+    with((uint32_t)__shfl_xor((int)b, 16, 64));
+    with((uint32_t)__shfl_xor((int)b, 32, 64));
     return b;
 }
 
-// Sixteen values of a row from c on, zeros past its end.
+// Sixteen values of a row from c on, zeros past its end, as they are stored.
 template <typename T>
-__device__ __forceinline__ void get16(float (&x)[16], const T *row, int c, int K)
-{
-    constexpr int kV = (int)sizeof(T);   // 16-byte words of sixteen values
-    if (c + 16 <= K) {
-        T t[16];
-        u32x4 w[kV];
+struct Sixteen {
+    static constexpr int kV = (int)sizeof(T);   // 16-byte words
+    u32x4 w[kV];
+
+    __device__ __forceinline__ void load(const T *row, int c, int K)
+    {
+        if (c + 16 <= K) {
 #pragma unroll
-        for (int k = 0; k < kV; ++k) w[k] = ((const u32x4_any *)(row + c))[k];
+            for (int k = 0; k < kV; ++k) w[k] = ((const u32x4_any *)(row + c))[k];
+        } else {
+            T t[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) t[k] = c + k < K ? row[c + k] : T{};
+            __builtin_memcpy(w, t, sizeof t);
+        }
+    }
+    // The same through a buffer that ends with the row, or, for an odd number of bf16, with its last value's word, whose other
+    // half is cleared.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c, int K)
+    {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) w[k] = __builtin_amdgcn_raw_buffer_load_b128(row, c * (int)sizeof(T) + k * 16, 0, 0);
+        if (sizeof(T) == 2 && (K & 1))
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (c + 2 * k + 1 == K) w[k / 4][k % 4] &= 0xFFFFu;
+    }
+    __device__ __forceinline__ void values(float (&x)[16]) const
+    {
+        T t[16];
         __builtin_memcpy(t, w, sizeof t);
 #pragma unroll
         for (int k = 0; k < 16; ++k) x[k] = widen(t[k]);
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = c + k < K ? widen(row[c + k]) : 0.0f;
     }
-}
+    // What was formed of the values is not kept: the words are, which take half the registers in bf16.
+    __device__ __forceinline__ void keep()
+    {
+#pragma unroll
+        for (int k = 0; k < kV; ++k) asm volatile("" : "+v"(w[k]));
+    }
+};
 
-__device__ __forceinline__ uint32_t largest16(const float (&x)[16])
+template <typename T>
+__device__ __forceinline__ uint32_t largest16(const Sixteen<T> &v)
 {
+    float x[16];
+    v.values(x);
     uint32_t b = 0;
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
@@ -96,17 +117,52 @@ __device__ __forceinline__ uint32_t largest16(const float (&x)[16])
     return b;
 }
 
-__device__ __forceinline__ u32x4 codes16(const float (&x)[16], const RowScale &s)
+// The code of x where x num / den lies next to the middle h of two codes: x num and h den are compared exactly, each as the sum
+// of two values in 32 bits (they have 32 bits at most, 24 and 8).
+__device__ __forceinline__ float next_to_middle(float x, const RowScale &s, float h)
 {
-    u32x4 w = {0, 0, 0, 0};
+#pragma clang fp contract(off)
+    const float q = x * s.num, p = h * s.den;
+    const float r = (q - p) + (__builtin_fmaf(x, s.num, -q) - __builtin_fmaf(h, s.den, -p));
+    return r > 0.0f ? h + 0.5f : r < 0.0f ? h - 0.5f : __builtin_rintf(h);
+}
+
+// Adding 3 2^22 rounds to an integer, to nearest even, and leaves it in the low byte.  x num / den as x inv is off by up to
+// 2^-16: a quotient that is that near to the middle of two codes (one in 16,000) is looked at again.
+template <typename T>
+__device__ __forceinline__ u32x4 codes16(const Sixteen<T> &v, const RowScale &s)
+{
+    float x[16];
+    v.values(x);
+    if (s.num == 0.0f) return u32x4{0, 0, 0, 0};
+    constexpr float kRound = 12582912.0f;
+    float u[16], worst = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) w[k / 4] |= (uint32_t)(uint8_t)code_of(x[k], s) << (k % 4 * 8);
+    for (int k = 0; k < 16; ++k) {
+        const float t = x[k] * s.inv;
+        u[k] = t + kRound;
+        worst = fmaxf(worst, __builtin_fabsf(t - (u[k] - kRound)));
+    }
+    if (worst >= 0.5f - 0x1p-15f) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+            const float t = x[k] * s.inv, c = u[k] - kRound;
+            if (__builtin_fabsf(t - c) >= 0.5f - 0x1p-15f) u[k] = next_to_middle(x[k], s, c + (t > c ? 0.5f : -0.5f)) + kRound;
+        }
+    }
+    u32x4 w;
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint32_t lo = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, u[q * 4 + 1]), __builtin_bit_cast(uint32_t, u[q * 4]), 0x0C0C0400);
+        const uint32_t hi = __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, u[q * 4 + 3]), __builtin_bit_cast(uint32_t, u[q * 4 + 2]), 0x04000C0C);
+        w[q] = lo | hi;
+    }
     return w;
 }
 
-constexpr int kHeld = 2;   // sixteens of a thread that stay in registers between the two passes over a row
+constexpr int kHeld = 4;   // sixteens of a thread that stay in registers between the two passes over a row
 
-// kWaves waves a row, 4 / kWaves rows a workgroup; the codes' rows end with zeros.
+// kWaves waves a row, 4 / kWaves rows a workgroup; the codes' rows end with zeros.  Bound by memory.
 template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, long long rows, int K, int8_t *codes, long long ldc,
                                                   float *scales)
@@ -117,20 +173,22 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
     const int Kp = (K + 15) & ~15;
     const long long step = (long long)gridDim.x * (4 / kWaves);
     for (long long r0 = (long long)blockIdx.x * (4 / kWaves); r0 < rows; r0 += step) {
-        const long long r = r0 + (kWaves == 4 ? 0 : wave);
+        const long long r = r0 + (kWaves == 4 ? 0 : __builtin_amdgcn_readfirstlane(wave));
         const bool some = r < rows;   // the same in all threads of a row
-        const T *row = x + r * ldx;
-        float v[kHeld][16];
+        const auto row = __builtin_amdgcn_make_buffer_rsrc((void *)(x + (some ? r : 0) * ldx), 0, (K * (int)sizeof(T) + 3) & ~3, 0x00027000);
+        Sixteen<T> v[kHeld];
         uint32_t b = 0;
         if (some) {
 #pragma unroll
+            for (int h = 0; h < kHeld; ++h) v[h].load(row, (h * kThreads + lane) * 16, K);   // zeros past its end
+#pragma unroll
             for (int h = 0; h < kHeld; ++h) {
-                const int c = (h * kThreads + lane) * 16;
-                if (c < Kp) get16(v[h], row, c, K), b = max(b, largest16(v[h]));
+                b = max(b, largest16(v[h]));
+                __builtin_amdgcn_sched_barrier(0);
             }
             for (int c = (kHeld * kThreads + lane) * 16; c < Kp; c += kThreads * 16) {
-                float t[16];
-                get16(t, row, c, K);
+                Sixteen<T> t;
+                t.load(row, c, K);
                 b = max(b, largest16(t));
             }
         }
@@ -148,11 +206,14 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
 #pragma unroll
         for (int h = 0; h < kHeld; ++h) {
             const int c = (h * kThreads + lane) * 16;
-            if (c < Kp) *(u32x4 *)(to + c) = codes16(v[h], s);
+            if (c >= Kp) continue;
+            v[h].keep();
+            *(u32x4 *)(to + c) = codes16(v[h], s);
+            __builtin_amdgcn_sched_barrier(0);   // one at a time: registers for more waves
         }
         for (int c = (kHeld * kThreads + lane) * 16; c < Kp; c += kThreads * 16) {
-            float t[16];
-            get16(t, row, c, K);
+            Sixteen<T> t;
+            t.load(row, c, K);
             *(u32x4 *)(to + c) = codes16(t, s);
         }
         if (lane == 0) scales[r] = scale;
@@ -162,8 +223,8 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
 template <typename T>
 hipError_t quantise(const void *x, long long ldx, long long rows, int K, int8_t *codes, long long ldc, float *scales, hipStream_t s)
 {
-    // a wave a row up to two sixteens a lane
-    if (K <= 64 * 16 * kHeld) {
+    // a wave a row where its registers hold it and there are rows for all compute units' waves
+    if (K <= 64 * 16 * kHeld && (K <= 64 * 16 || rows >= 2048)) {
         const unsigned grid = (unsigned)std::min<long long>((rows + 3) / 4, 1 << 16);
         k_quantise<T, 1><<<grid, 256, 0, s>>>((const T *)x, ldx, rows, K, codes, ldc, scales);
     } else {
@@ -223,7 +284,7 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product8(Args P, Scales8 q)
                                                 [](int, int, const bool (&)[4]) { return f32x4{}; });
 }
 
-// Few rows of x: tiles of 16 FI x 16 straight from memory, as k_small_forward's.
+// Few rows of x: tiles of 16 FI x 16, codes of w straight from memory as k_small_forward's, x's codes from the workspace.
 template <typename T, int FI>
 __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small8(Args P, Scales8 q)
 {
@@ -257,6 +318,92 @@ __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small8(Args P, Scales8
                               [&](int sum, int i, int j) { return (float)sum * (q.x[i] * q.w[j]); });
 }
 
+constexpr int kOwnHeld = 2;   // sixteens of a thread's
+constexpr int kOwnLds = 40 * 1024;
+
+// Floats of LDS that a tile's own codes take: up to 16 rows, 16 bytes apart beyond their length, for the banks; their largest
+// magnitudes behind them.
+__host__ __device__ inline int own_pitch(int pairs) { return pairs * 2 + 16; }
+__host__ __device__ inline int own_bytes(int rows, int pairs) { return rows * own_pitch(pairs) + 64; }
+
+// As k_small8<T, 1>, and every workgroup rounds its tile's rows of x by itself, while its first codes of w are under way: one launch
+// instead of two.  P.a: x.
+template <typename T>
+__global__ __launch_bounds__(1024) void k_small8_own(Args P, Scales8 q, int K)
+{
+    extern __shared__ float small_lds[];
+    constexpr int kAt = 4;
+    const int i0 = blockIdx.x % P.tiles_i * 16, j0 = blockIdx.x / P.tiles_i * 16;
+    const int rows = P.I - i0 < 16 ? P.I - i0 : 16, pitch = own_pitch(P.K);
+    int8_t *codes = (int8_t *)small_lds;
+    uint32_t *largest = (uint32_t *)(codes + rows * pitch);
+    float *sums = (float *)(largest + 16);
+    int first, last;
+    const int begin = blockIdx.y * P.k_part;
+    small_share(begin, P.K - begin < P.k_part ? P.K : begin + P.k_part, first, last);
+    Piece<bf16, K_ROWS> b[kAt];
+    auto load = [&](int k0) {
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) b[n].load(P.b, P.ldb, j0, P.J, k0 + 32 * n < last ? k0 + 32 * n : P.K, P.K);
+    };
+    const int sixteens = P.K >> 3, all = rows * sixteens;   // of a row, of the tile
+    // x is asked for first: loads arrive in order, and it is needed before w
+    Sixteen<T> v[kOwnHeld];
+    int r_of[kOwnHeld];
+#pragma unroll
+    for (int h = 0; h < kOwnHeld; ++h) {
+        const int at = h * blockDim.x + threadIdx.x;
+        r_of[h] = rows == 1 ? 0 : at < all ? at / sixteens : rows - 1;
+        if (at < all) v[h].load((const T *)P.a + (i0 + r_of[h]) * P.lda, (at - r_of[h] * sixteens) * 16, K);
+    }
+    load(first);
+    if (threadIdx.x < 16) largest[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kOwnHeld; ++h) {
+        if (h * (int)blockDim.x >= all) continue;   // the same in the whole workgroup
+        const bool some = h * (int)blockDim.x + (int)threadIdx.x < all;
+        uint32_t most = some ? largest16(v[h]) : 0;
+        if (__builtin_amdgcn_readfirstlane(r_of[h]) == __builtin_amdgcn_readlane(r_of[h], 63)) {   // one row's
+            most = wave_max(most);
+            if ((threadIdx.x & 63) == 0 && some) atomicMax(largest + r_of[h], most);
+        } else if (some) {
+            atomicMax(largest + r_of[h], most);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int h = 0; h < kOwnHeld; ++h) {
+        const int at = h * blockDim.x + threadIdx.x;
+        if (at >= all) continue;
+        float scale;
+        *(u32x4 *)(codes + r_of[h] * pitch + (at - r_of[h] * sixteens) * 16) = codes16(v[h], row_scale(largest[r_of[h]], scale));
+    }
+    __syncthreads();
+    const int lane = threadIdx.x & 63, row = (lane & 15) < rows ? lane & 15 : rows - 1;
+    const int8_t *mine = codes + row * pitch + (lane >> 4) * 16;
+    i32x4 acc[1] = {};
+    for (int k0 = first; k0 < last; k0 += 32 * kAt) {
+        bf16x8 vb[kAt];
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) __builtin_memcpy(&vb[n], b[n].w, 16);
+        if (k0 + 32 * kAt < last) load(k0 + 32 * kAt);
+#pragma unroll
+        for (int n = 0; n < kAt; ++n) {
+            // past the share, or the row, w's codes are zeros
+            const int k = k0 + 32 * n;
+            const bool there = k < last && k * 2 + (lane >> 4) * 16 < P.K * 2;
+            const u32x4 a = *(const u32x4 *)(there ? mine + k * 2 : codes);
+            acc[0] = MulI8::mul(vb[n], __builtin_bit_cast(bf16x8, a), acc[0]);
+        }
+    }
+    small_finish<T, 1, true>(P, acc, blockIdx.x, i0, j0, sums, [&](int sum, int i, int j) {
+        float scale;
+        (void)row_scale(largest[i - i0], scale);
+        return (float)sum * (scale * q.w[j]);
+    });
+}
+
 template <typename T>
 hipError_t product8(const Args &P, const Scales8 &q, Shape shape, hipStream_t s)
 {
@@ -282,8 +429,6 @@ template <typename T>
 hipError_t forward(const Dense8Forward &a, const Dense8Workspace &ws, hipStream_t s)
 {
     const int pairs = (a.K + 15) / 16 * 8;
-    const hipError_t e = quantise<T>(a.x, a.ldx, a.M, a.K, ws.codes, 2ll * pairs, ws.scales, s);
-    if (e != hipSuccess) return e;
     Args P{};
     P.a = ws.codes, P.lda = pairs;
     P.b = a.codes, P.ldb = a.ldw / 2;
@@ -304,6 +449,16 @@ hipError_t forward(const Dense8Forward &a, const Dense8Workspace &ws, hipStream_
     const size_t all = (size_t)P.tiles_i * P.tiles_j;
     if (P.parts > 1 && (all * P.parts * side_i * side_j * 4 > ws.part_bytes || all * sizeof(unsigned) > ws.ticket_bytes))
         return hipErrorInvalidValue;
+    // a tile's rows of x in the registers of its workgroup, and their codes in its LDS
+    const int rows = std::min(a.M, 16);
+    if (small && few.fi == 1 && rows * (pairs / 8) <= kOwnHeld * 64 * few.waves && own_bytes(rows, pairs) <= kOwnLds) {
+        P.a = a.x, P.lda = a.ldx;
+        const dim3 grid((unsigned)all, (unsigned)P.parts);
+        k_small8_own<T><<<grid, 64 * few.waves, own_bytes(rows, pairs) + few.waves * 1024, s>>>(P, q, a.K);
+        return hipGetLastError();
+    }
+    const hipError_t e = quantise<T>(a.x, a.ldx, a.M, a.K, ws.codes, 2ll * pairs, ws.scales, s);
+    if (e != hipSuccess) return e;
     return small ? small8<T>(P, q, few.fi, few.waves, s) : product8<T>(P, q, tiles.shape, s);
 }
 

@@ -102,6 +102,23 @@ __device__ __forceinline__ void put(T *to, const T (&from)[n])
     *(All *)to = a;
 }
 
+// The sum over a wave, in all its lanes.
+__device__ __forceinline__ double wave_sum(double v)
+{
+    auto with = [&](auto move) {
+        const unsigned long long b = __builtin_bit_cast(unsigned long long, v);
+        const unsigned long long m = (unsigned)move((int)b) | (unsigned long long)(unsigned)move((int)(b >> 32)) << 32;
+        v += __builtin_bit_cast(double, m);
+    };
+    with([](int x) { return __builtin_amdgcn_update_dpp(0, x, 0xB1, 0xF, 0xF, true); });    // lane ^ 1
+    with([](int x) { return __builtin_amdgcn_update_dpp(0, x, 0x4E, 0xF, 0xF, true); });    // lane ^ 2
+    with([](int x) { return __builtin_amdgcn_update_dpp(0, x, 0x141, 0xF, 0xF, true); });   // mirrored in eight
+    with([](int x) { return __builtin_amdgcn_update_dpp(0, x, 0x140, 0xF, 0xF, true); });   // mirrored in sixteen
+    with([](int x) { return __shfl_xor(x, 16, 64); });
+    with([](int x) { return __shfl_xor(x, 32, 64); });
+    return v;
+}
+
 // m, and the sums of u^2 of each chunk, in 64 bits: they neither overflow nor lose a small chunk beside a large one.
 // The first workgroup clears the tickets of the products that follow.
 template <typename G>
@@ -148,8 +165,7 @@ __global__ __launch_bounds__(256) void k_momentum(Batch batch, Scalars k, unsign
             }
         }
     }
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
+    sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
     __syncthreads();
     if (threadIdx.x == 0) t.sums[chunk] = part[0] + part[1] + part[2] + part[3];
@@ -171,8 +187,7 @@ __device__ __forceinline__ float inverse_norm(const Matrix &t, float eps)
     const int chunks = (int)(((long long)t.rows * t.cols + kChunk - 1) / kChunk);
     double sum = 0.0;
     for (int i = threadIdx.x; i < chunks; i += 256) sum += t.sums[i];
-#pragma unroll
-    for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
+    sum = wave_sum(sum);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
     __syncthreads();
     const double norm = sqrt(part[0] + part[1] + part[2] + part[3]);
@@ -548,7 +563,7 @@ __global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 
 // fp32 matrix instruction, nothing rounded to fewer bits.  What counts is latency: three products and as many barriers a
 // step, one launch instead of 2 + 3 for each step.
 
-constexpr int kSmallSide = 64, kSmallThreads = 1024, kSmallWaves = kSmallThreads / 64;
+constexpr int kSmallSide = 64, kSmallWaves = 16, kTinyWaves = 4;
 constexpr int kSmallLds = 160 * 1024 - 1024;
 constexpr long long kSmallWork = 1 << 20;   // multiply-adds of X X^T
 
@@ -572,108 +587,181 @@ bool is_small(int rows, int cols)
 // Four k of a 16 x 16 block: lane % 16 is the row of either operand, lane / 16 its k.
 __device__ __forceinline__ f32x4 multiply(float b, float a, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x4f32(b, a, c, 0, 0, 0); }
 
-template <typename T, typename G>
-__global__ __launch_bounds__(kSmallThreads) void k_small(Batch batch, Scalars k, int steps)
+// The steps of a matrix of NT tiles of sixteen rows.  What counts is the way from LDS to the matrix instructions, so each loop
+// reads all its operands, or many, before it uses the first.
+template <int NT, int WAVES>
+__device__ __forceinline__ void small_steps(const SmallSize &z, const Scalars &k, int steps, float *X, float *A, float *B, float *P)
+{
+    constexpr int kThreads = 64 * WAVES, kTiles = NT * (NT + 1) / 2;
+    constexpr int kParts = kTiles < WAVES ? WAVES / kTiles : 1;   // of k, for A: a wave each
+    constexpr int kAt = 8;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4;
+    const int kp = wave / kTiles, fours = z.m / 4, share = (fours + kParts - 1) / kParts;
+    const int from = kp * share, to = from + share < fours ? from + share : fours;
+    auto tile_at = [](int tile, int &i, int &j) {   // of a lower triangle, in rows
+        i = 0, j = tile;
+        while (j > i) j -= ++i;
+    };
+    int wi, wj;
+    tile_at(wave % kTiles, wi, wj);
+    auto mirrored = [&](float *to, int i, int j, float v) {
+        to[i * z.lda + j] = v;
+        if (i >> 4 != j >> 4) to[j * z.lda + i] = v;
+    };
+    for (int step = 0; step < steps; ++step) {
+        if (kp < kParts) {   // A = X X^T
+            const float *a = X + (wi * 16 + row) * z.ldx + quad, *b = X + (wj * 16 + row) * z.ldx + quad;
+            f32x4 s[2] = {};
+            for (int f = from; f < to; f += kAt) {
+                float av[kAt], bv[kAt];
+#pragma unroll
+                for (int e = 0; e < kAt; ++e) {
+                    const int at = f + e < to ? f + e : from;
+                    av[e] = f + e < to ? a[at * 4] : 0.0f;
+                    bv[e] = b[at * 4];
+                }
+#pragma unroll
+                for (int e = 0; e < kAt; ++e) s[e & 1] = multiply(bv[e], av[e], s[e & 1]);
+            }
+            s[0] += s[1];
+            if (kParts > 1) {
+                *(f32x4 *)(P + wave * 256 + row * 16 + quad * 4) = s[0];
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mirrored(A, wi * 16 + row, wj * 16 + quad * 4 + e, s[0][e]);
+            }
+        }
+        __syncthreads();
+        if (kParts > 1) {
+            for (int i = threadIdx.x; i < kTiles * 256; i += kThreads) {
+                int bi, bj;
+                tile_at(i >> 8, bi, bj);
+                float s = 0.0f;
+#pragma unroll
+                for (int q = 0; q < kParts; ++q) s += P[q * kTiles * 256 + i];
+                mirrored(A, bi * 16 + ((i >> 4) & 15), bj * 16 + (i & 15), s);
+            }
+            __syncthreads();
+        }
+        for (int tile = wave; tile < kTiles; tile += WAVES) {   // B = b A + c A^2
+            int ti, tj;
+            tile_at(tile, ti, tj);
+            const float *a = A + (ti * 16 + row) * z.lda + quad, *b = A + (tj * 16 + row) * z.lda + quad;
+            float av[NT * 4], bv[NT * 4];
+#pragma unroll
+            for (int f = 0; f < NT * 4; ++f) av[f] = a[f * 4], bv[f] = b[f * 4];
+            const f32x4 own = *(const f32x4 *)(A + (ti * 16 + row) * z.lda + tj * 16 + quad * 4);
+            f32x4 s[2] = {};
+#pragma unroll
+            for (int f = 0; f < NT * 4; ++f) s[f & 1] = multiply(bv[f], av[f], s[f & 1]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                mirrored(B, ti * 16 + row, tj * 16 + quad * 4 + e, __builtin_fmaf(k.b, own[e], k.c * (s[0][e] + s[1][e])));
+        }
+        __syncthreads();
+        for (int cb = wave; cb < z.m / 16; cb += WAVES) {   // X = a X + B X, sixteen columns a wave: no other reads them
+            float x[NT * 4];
+            f32x4 own[NT], s[NT] = {};
+#pragma unroll
+            for (int f = 0; f < NT * 4; ++f) x[f] = X[(f * 4 + quad) * z.ldx + cb * 16 + row];
+#pragma unroll
+            for (int it = 0; it < NT; ++it) own[it] = *(const f32x4 *)(X + (it * 16 + row) * z.ldx + cb * 16 + quad * 4);
+#pragma unroll
+            for (int f0 = 0; f0 < NT * 4; f0 += 4) {
+                float b[4][NT];
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) b[f][it] = B[(it * 16 + row) * z.lda + (f0 + f) * 4 + quad];
+#pragma unroll
+                for (int f = 0; f < 4; ++f)
+#pragma unroll
+                    for (int it = 0; it < NT; ++it) s[it] = multiply(x[f0 + f], b[f][it], s[it]);
+            }
+#pragma unroll
+            for (int it = 0; it < NT; ++it) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[it][e] = __builtin_fmaf(k.a, own[it][e], s[it][e]);
+                *(f32x4 *)(X + (it * 16 + row) * z.ldx + cb * 16 + quad * 4) = s[it];
+            }
+        }
+        __syncthreads();
+    }
+}
+
+template <typename T, typename G, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_small(Batch batch, Scalars k, int steps)
 {
     extern __shared__ float small_lds[];
-    __shared__ double part[kSmallWaves];
+    constexpr int kThreads = 64 * WAVES;
+    __shared__ double part[WAVES];
     const Matrix &t = batch.t[blockIdx.x];
     const SmallSize z(t.rows, t.cols);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4, nt = z.n / 16;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const bool tall = t.rows > t.cols;
     float *X = small_lds, *A = X + z.n * z.ldx, *B = A + z.n * z.lda, *P = B + z.n * z.lda;
     const G *g = (const G *)t.g;
     T *p = (T *)t.p;
     const int all = t.rows * t.cols;
-    for (int i = threadIdx.x; i < z.n * z.ldx; i += kSmallThreads) X[i] = 0.0f;
+    // a thread's elements are kThreads apart: row and column go on by as much, without a division
+    const int dr = kThreads / t.cols, dc = kThreads - dr * t.cols;
+    const int r0 = (int)threadIdx.x / t.cols, c0 = (int)threadIdx.x - r0 * t.cols;
+    auto each = [&](auto f) {
+        int r = r0, c = c0;
+        for (int i = threadIdx.x; i < all; i += kThreads) {
+            f(i, X + (tall ? c * z.ldx + r : r * z.ldx + c));
+            r += dr, c += dc;
+            if (c >= t.cols) c -= t.cols, ++r;
+        }
+    };
+    for (int i = threadIdx.x; i < z.n * z.ldx; i += kThreads) X[i] = 0.0f;
     __syncthreads();
     double sum = 0.0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < all; i += kSmallThreads) {
-        const float gi = widen(g[i]), m = t.m[i] * k.mu + gi * k.nu, u = update_of(k, m, gi);
-        t.m[i] = m;
-        const int r = i / t.cols, c = i - r * t.cols;
-        X[tall ? c * z.ldx + r : r * z.ldx + c] = u;
-        sum += (double)u * u;
-    }
+    constexpr int kAt = 4;   // elements loaded before the first is used
+    {
+        int r = r0, c = c0;
+        for (int i0 = threadIdx.x; i0 < all; i0 += kThreads * kAt) {
+            float gv[kAt], mv[kAt];
 #pragma unroll
-    for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
+            for (int a = 0; a < kAt; ++a) {
+                const int i = i0 + a * kThreads;
+                gv[a] = i < all ? widen(g[i]) : 0.0f;
+                mv[a] = i < all ? t.m[i] : 0.0f;
+            }
+#pragma unroll
+            for (int a = 0; a < kAt; ++a) {
+                const int i = i0 + a * kThreads;
+                if (i < all) {
+                    const float m = mv[a] * k.mu + gv[a] * k.nu, u = update_of(k, m, gv[a]);
+                    t.m[i] = m;
+                    X[tall ? c * z.ldx + r : r * z.ldx + c] = u;
+                    sum += (double)u * u;
+                }
+                r += dr, c += dc;
+                if (c >= t.cols) c -= t.cols, ++r;
+            }
+        }
+    }
+    sum = wave_sum(sum);
     if (lane == 0) part[wave] = sum;
     __syncthreads();
     sum = 0.0;
 #pragma unroll
-    for (int w = 0; w < kSmallWaves; ++w) sum += part[w];
+    for (int w = 0; w < WAVES; ++w) sum += part[w];
     const double norm = sqrt(sum);
     const float inv = (float)(1.0 / (norm <= (double)k.eps ? (double)k.eps : norm));
-    for (int i = threadIdx.x; i < z.n * z.ldx; i += kSmallThreads) X[i] *= inv;
+    for (int i = threadIdx.x; i < z.n * z.ldx; i += kThreads) X[i] *= inv;
     __syncthreads();
-    const int tiles = nt * (nt + 1) / 2, parts = kSmallWaves / tiles;   // of A; each wave a tile's part of k
-    int ti = 0, tj = wave % tiles;
-    while (tj > ti) tj -= ++ti;   // tile of a lower triangle, in rows
-    const int kp = wave / tiles, fours = z.m / 4, each = (fours + parts - 1) / parts;
-    for (int step = 0; step < steps; ++step) {
-        if (kp < parts) {   // A = X X^T
-            f32x4 s[2] = {};
-            const float *a = X + (ti * 16 + row) * z.ldx + quad, *b = X + (tj * 16 + row) * z.ldx + quad;
-            const int last = (kp + 1) * each < fours ? (kp + 1) * each : fours;
-            int f = kp * each;
-            for (; f + 2 <= last; f += 2) {
-                s[0] = multiply(b[f * 4], a[f * 4], s[0]);
-                s[1] = multiply(b[f * 4 + 4], a[f * 4 + 4], s[1]);
-            }
-            if (f < last) s[0] = multiply(b[f * 4], a[f * 4], s[0]);
-            *(f32x4 *)(P + wave * 256 + row * 16 + quad * 4) = s[0] + s[1];
-        }
-        __syncthreads();
-        for (int i = threadIdx.x; i < tiles * 256; i += kSmallThreads) {
-            const int tile = i >> 8, r = (i >> 4) & 15, c = i & 15;
-            int bi = 0, bj = tile;
-            while (bj > bi) bj -= ++bi;
-            float s = 0.0f;
-            for (int q = 0; q < parts; ++q) s += P[(q * tiles + tile) * 256 + (i & 255)];
-            A[(bi * 16 + r) * z.lda + bj * 16 + c] = s;
-            if (bi != bj) A[(bj * 16 + c) * z.lda + bi * 16 + r] = s;
-        }
-        __syncthreads();
-        if (kp == 0) {   // B = b A + c A^2
-            f32x4 s = {};
-            const float *a = A + (ti * 16 + row) * z.lda + quad, *b = A + (tj * 16 + row) * z.lda + quad;
-#pragma unroll 4
-            for (int f = 0; f < nt * 4; ++f) s = multiply(b[f * 4], a[f * 4], s);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int i = ti * 16 + row, j = tj * 16 + quad * 4 + e;
-                const float v = __builtin_fmaf(k.b, A[i * z.lda + j], k.c * s[e]);
-                B[i * z.lda + j] = v;
-                if (ti != tj) B[j * z.lda + i] = v;
-            }
-        }
-        __syncthreads();
-        for (int cb = wave; cb < z.m / 16; cb += kSmallWaves) {   // X = a X + B X, sixteen columns a wave: no other reads them
-            f32x4 s[kSmallSide / 16] = {};
-            for (int f = 0; f < nt * 4; ++f) {
-                const float x = X[(f * 4 + quad) * z.ldx + cb * 16 + row];
-#pragma unroll
-                for (int it = 0; it < kSmallSide / 16; ++it)
-                    if (it < nt) s[it] = multiply(x, B[(it * 16 + row) * z.lda + f * 4 + quad], s[it]);
-            }
-#pragma unroll
-            for (int it = 0; it < kSmallSide / 16; ++it) {
-                if (it >= nt) continue;
-                f32x4 *at = (f32x4 *)(X + (it * 16 + row) * z.ldx + cb * 16 + quad * 4);
-                const f32x4 x = *at;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[it][e] = __builtin_fmaf(k.a, x[e], s[it][e]);
-                *at = s[it];
-            }
-        }
-        __syncthreads();
+    switch (z.n / 16) {
+    case 1: small_steps<1, WAVES>(z, k, steps, X, A, B, P); break;
+    case 2: small_steps<2, WAVES>(z, k, steps, X, A, B, P); break;
+    case 3: small_steps<3, WAVES>(z, k, steps, X, A, B, P); break;
+    default: small_steps<4, WAVES>(z, k, steps, X, A, B, P); break;
     }
-    for (int i = threadIdx.x; i < all; i += kSmallThreads) {
-        const int r = i / t.cols, c = i - r * t.cols;
+    each([&](int i, const float *x) {
         const float y = widen(p[i]);
-        narrow(__builtin_fmaf(y, -k.decay, y) - t.size * X[tall ? c * z.ldx + r : r * z.ldx + c], p[i]);
-    }
+        narrow(__builtin_fmaf(y, -k.decay, y) - t.size * *x, p[i]);
+    });
 }
 
 // ---- a call ----
@@ -911,12 +999,18 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     if (few.count) {
         using T = std::conditional_t<PLANES == 2, float, bf16>;
         size_t lds = 0;
-        for (int i = 0; i < few.count; ++i) lds = std::max(lds, SmallSize(few.t[i].rows, few.t[i].cols).bytes());
+        bool tiny = true;
+        for (int i = 0; i < few.count; ++i) {
+            const SmallSize z(few.t[i].rows, few.t[i].cols);
+            lds = std::max(lds, z.bytes());
+            tiny = tiny && z.n <= 32 && z.m <= 128;
+        }
         if (lds > 32 * 1024) {   // with what the kernel holds besides, more than a launch may take unasked
-            e = hipFuncSetAttribute((const void *)k_small<T, G>, hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
+            e = hipFuncSetAttribute((const void *)k_small<T, G, kSmallWaves>, hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);
             if (e != hipSuccess) return e;
         }
-        k_small<T, G><<<few.count, kSmallThreads, lds, s>>>(few, k, cfg.steps);
+        if (tiny) k_small<T, G, kTinyWaves><<<few.count, 64 * kTinyWaves, lds, s>>>(few, k, cfg.steps);
+        else k_small<T, G, kSmallWaves><<<few.count, 64 * kSmallWaves, lds, s>>>(few, k, cfg.steps);
         if ((e = hipGetLastError()) != hipSuccess || !b.count) return e;
     }
     float *const part = (float *)work;

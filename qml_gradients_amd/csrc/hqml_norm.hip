@@ -30,13 +30,28 @@ using u32x4_any = __attribute__((ext_vector_type(4), aligned(2))) uint32_t;
 template <typename T>
 constexpr int kVec = 16 / (int)sizeof(T);   // channels of a thread
 
-// How a workgroup's threads share `width` channels (a span of whole groups, or all) and the positions of `subs` samples.
+// Division of numbers below 2^16 by one of those, by the high half of a product (an integer division takes forty
+// instructions): with magic = ceil(2^32 / by), magic by is less than `by` above 2^32, and n times that less than 2^32.
+struct Div {
+    unsigned by, magic;
+    Div() = default;
+    explicit Div(int d) : by((unsigned)d), magic((unsigned)(((1ull << 32) + d - 1) / d)) {}   // 0 for 1
+    __device__ __forceinline__ int operator()(int n) const { return magic ? (int)__umulhi((unsigned)n, magic) : n; }
+};
+
+// How a workgroup's threads share `width` channels (a span of whole groups, or all) and the positions of `subs` samples.  Every
+// thread leaves one value for its groups' sums where all its channels are of one group, one for each of them otherwise; `each`
+// lanes (a power of two, up to a wave) put a group's together.
 struct Map {
     int width, vecs;    // channels, threads across them
     int lanes;          // threads down the positions of a sample
     int subs;
     int per;            // channels of a group
     int groups;         // of the span
+    int wide, pitch, mine;   // values of a thread, of a position; of a group in it
+    int sets, each;          // groups of all samples
+    float channels;          // that a value stands for
+    Div by_vecs, by_lanes, by_per, by_groups, by_mine;
 };
 
 struct Norm {
@@ -47,8 +62,9 @@ struct Norm {
     float *mean, *rstd;
     int act;
     float eps;
-    float *part;        // backward: [workgroups of a span][2][C], dgamma and dbeta
-    void *dgamma, *dbeta;   // written by the one workgroup of a span there is, or null
+    float *part;        // backward: partial sums [rows][2][C] of dbeta and dgamma; null: the only workgroup of a span writes those
+    void *dgamma, *dbeta;
+    int rows, extra;
     Map map;
     // split
     int chunk, chunks;      // positions of a chunk, chunks of a sample
@@ -68,9 +84,9 @@ template <int V>
 __device__ __forceinline__ Place place(const Map &m, int width)
 {
     Place p;
-    const int rl = (int)threadIdx.x / m.vecs, cv = (int)threadIdx.x - rl * m.vecs;
+    const int rl = m.by_vecs((int)threadIdx.x), cv = (int)threadIdx.x - rl * m.vecs;
     p.c = cv * V;
-    p.sub = rl / m.lanes;
+    p.sub = m.by_lanes(rl);
     p.row = rl - p.sub * m.lanes;
     p.on = p.sub < m.subs;
     p.n = !p.on || p.c >= width ? 0 : width - p.c < V ? width - p.c : V;
@@ -119,69 +135,133 @@ __device__ __forceinline__ void parameters(float (&v)[V], const void *from, int 
     for (int e = 0; e < V; ++e) v[e] = e < n && from ? widen(((const T *)from)[c + e]) : without;
 }
 
-// Sums over a group of Q values that every thread has for each of its channels: to LDS by channel and thread, summed down the
-// positions, then over the group's channels.  all: reduce_floats() of work.  Each quantity's sums end in
-// groups[q][sub][group].
+// The sum of n lanes beside each other (a power of two, the same in the whole wave), in all of them.
+__device__ __forceinline__ float lanes_sum(float v, int n)
+{
+    auto with = [&](int moved) { v += __builtin_bit_cast(float, moved); };
+    auto bits = [&] { return __builtin_bit_cast(int, v); };
+    if (n >= 2) with(__builtin_amdgcn_update_dpp(0, bits(), 0xB1, 0xF, 0xF, true));    // lane ^ 1
+    if (n >= 4) with(__builtin_amdgcn_update_dpp(0, bits(), 0x4E, 0xF, 0xF, true));    // lane ^ 2
+    if (n >= 8) with(__builtin_amdgcn_update_dpp(0, bits(), 0x141, 0xF, 0xF, true));   // mirrored in eight
+    if (n >= 16) with(__builtin_amdgcn_update_dpp(0, bits(), 0x140, 0xF, 0xF, true));  // mirrored in sixteen
+    if (n >= 32) v += __shfl_xor(v, 16, 64);
+    if (n >= 64) v += __shfl_xor(v, 32, 64);
+    return v;
+}
+
+// A thread's Q values for each of its channels, left for its workgroup.
+template <int V, int Q>
+__device__ __forceinline__ void leave_sums(const Map &m, const Place &p, const float (&s)[Q][V], float *all)
+{
+    const int T = blockDim.x;
+    if (!p.on) return;
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            if (m.wide == 1) sum += e < p.n ? s[q][e] : 0.0f;
+            else all[(q * T + (int)threadIdx.x) * V + e] = e < p.n ? s[q][e] : 0.0f;
+        }
+        if (m.wide == 1) all[q * T + (int)threadIdx.x] = sum;
+    }
+}
+
+// Calls f(at, l) for the values of a set that are this lane's: at is the value's place, l the thread down the positions.
+template <typename F>
+__device__ __forceinline__ void each_value(const Map &m, int set, int lane, F take)
+{
+    const int sub = m.by_groups(set), g = set - sub * m.groups;
+    const int from = sub * m.lanes * m.pitch + g * m.mine;
+    int l = m.by_mine(lane), k = lane - l * m.mine;
+    const int dl = m.by_mine(m.each), dk = m.each - dl * m.mine;
+    while (l < m.lanes) {
+        take(from + l * m.pitch + k, l);
+        l += dl, k += dk;
+        if (k >= m.mine) k -= m.mine, ++l;
+    }
+}
+
+// Sums over a group of Q values that every thread has for each of its channels; each quantity's end in groups[q][set].
 template <int V, int Q>
 __device__ __forceinline__ void group_sums(const Map &m, const Place &p, const float (&s)[Q][V], float *all, float *groups)
 {
-    const int T = blockDim.x, pitch = m.vecs * V, items = m.subs * pitch;
-    float *red = all, *col = all + Q * T * V;
-    if (p.on)
-#pragma unroll
-        for (int q = 0; q < Q; ++q)
-#pragma unroll
-            for (int e = 0; e < V; ++e) red[(q * T + (int)threadIdx.x) * V + e] = e < p.n ? s[q][e] : 0.0f;
+    const int T = blockDim.x;
+    leave_sums<V, Q>(m, p, s, all);
     __syncthreads();
-    // `parts` threads a channel where there are that many
-    int parts = T / items;
-    parts = parts < 1 ? 1 : parts > m.lanes ? m.lanes : parts;
-    for (int i = threadIdx.x; i < items * parts; i += T) {
-        const int part = i / items, at = i - part * items, sub = at / pitch, c = at - sub * pitch;
+    const int lane = threadIdx.x & (m.each - 1), stride = m.wide == 1 ? T : T * V;
+    for (int set = (int)(threadIdx.x >> __builtin_ctz(m.each)); set < m.sets; set += T >> __builtin_ctz(m.each)) {
+        float sum[Q] = {};
+        each_value(m, set, lane, [&](int at, int) {
+#pragma unroll
+            for (int q = 0; q < Q; ++q) sum[q] += all[q * stride + at];
+        });
 #pragma unroll
         for (int q = 0; q < Q; ++q) {
-            float sum = 0.0f;
-            for (int l = part; l < m.lanes; l += parts) sum += red[q * T * V + (sub * m.lanes + l) * pitch + c];
-            col[q * T * V + i] = sum;
-        }
-    }
-    __syncthreads();
-    const int sets = m.subs * m.groups, each = m.per * parts;
-    if (each <= 32) {
-        for (int i = threadIdx.x; i < sets * Q; i += T) {
-            const int q = i / sets, at = i - q * sets, sub = at / m.groups, g = at - sub * m.groups;
-            float sum = 0.0f;
-            for (int part = 0; part < parts; ++part)
-                for (int k = 0; k < m.per; ++k) sum += col[q * T * V + part * items + sub * pitch + g * m.per + k];
-            groups[q * sets + at] = sum;
-        }
-    } else {   // a wave a group
-        const int lane = threadIdx.x & 63;
-        for (int i = threadIdx.x >> 6; i < sets * Q; i += T >> 6) {
-            const int q = i / sets, at = i - q * sets, sub = at / m.groups, g = at - sub * m.groups;
-            float sum = 0.0f;
-            for (int part = 0; part < parts; ++part)
-                for (int k = lane; k < m.per; k += 64) sum += col[q * T * V + part * items + sub * pitch + g * m.per + k];
-#pragma unroll
-            for (int h = 1; h < 64; h <<= 1) sum += __shfl_xor(sum, h, 64);
-            if (lane == 0) groups[q * sets + at] = sum;
+            sum[q] = lanes_sum(sum[q], m.each);
+            if (lane == 0) groups[q * m.sets + set] = sum[q];
         }
     }
     __syncthreads();
 }
 
-// Floats of LDS that group_sums takes for its work.
-__host__ __device__ constexpr int reduce_floats(int threads, int V, int Q) { return 2 * Q * threads * V; }
-// At most: 512 threads of eight channels and two quantities, or 1024 of four, and two sums of each of 4096 groups.
-constexpr int kMostLds = (reduce_floats(512, 8, 2) + 2 * 4096) * 4;
-static_assert(reduce_floats(1024, 4, 2) <= reduce_floats(512, 8, 2), "either type");
+// Mean of a group, and the sum of squared distances from it, of what the threads have: the sum of each channel over the
+// thread's positions (count: positions), and the squared distances from its own mean.  Values that stand for several channels
+// (wide == 1) are joined in the thread first.  positions: of the sample or chunk.  The results end in groups[0][set],
+// groups[1][set].
+template <int V>
+__device__ __forceinline__ void group_moments(const Map &m, const Place &p, float (&sum)[V], float (&far)[V], float count,
+                                              int positions, float *all, float *groups)
+{
+    const int T = blockDim.x;
+    float s[2][V];
+    if (m.wide == 1) {
+        float total = 0.0f, squares = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) total += sum[e];
+        const float one = count > 0.0f ? 1.0f / count : 0.0f, mean = total * one * (1.0f / V);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float d = __builtin_fmaf(sum[e], one, -mean);
+            squares += __builtin_fmaf(d * d, count, far[e]);
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0][e] = e ? 0.0f : total, s[1][e] = e ? 0.0f : squares;
+    } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[0][e] = sum[e], s[1][e] = far[e];
+    }
+    leave_sums<V, 2>(m, p, s, all);
+    __syncthreads();
+    const int lane = threadIdx.x & (m.each - 1), stride = m.wide == 1 ? T : T * V;
+    const int some = positions / m.lanes, more = positions - some * m.lanes;   // positions of a thread: one more for the first ones
+    const float inv = 1.0f / ((float)positions * (float)m.per);
+    const float n0 = (float)some * m.channels, n1 = (float)(some + 1) * m.channels, i0 = some ? 1.0f / n0 : 0.0f, i1 = 1.0f / n1;
+    for (int set = (int)(threadIdx.x >> __builtin_ctz(m.each)); set < m.sets; set += T >> __builtin_ctz(m.each)) {
+        float total = 0.0f, squares = 0.0f;
+        each_value(m, set, lane, [&](int at, int) { total += all[at]; });
+        const float mean = lanes_sum(total, m.each) * inv;
+        each_value(m, set, lane, [&](int at, int l) {
+            const float d = __builtin_fmaf(all[at], l < more ? i1 : i0, -mean);
+            squares += l < more || some ? __builtin_fmaf(d * d, l < more ? n1 : n0, all[stride + at]) : 0.0f;
+        });
+        squares = lanes_sum(squares, m.each);
+        if (lane == 0) groups[set] = mean, groups[m.sets + set] = squares;
+    }
+    __syncthreads();
+}
+
+// Floats of LDS that these take for their work.
+__host__ __device__ constexpr int reduce_floats(int threads, int V) { return 2 * threads * V; }
+// At most: 1024 threads of eight channels, and two sums of each of their channels' groups.
+constexpr int kMostLds = 160 * 1024 - 4096;
 
 // A thread's group of each of its channels.
 template <int V>
 __device__ __forceinline__ void groups_of(int (&g)[V], const Map &m, const Place &p)
 {
 #pragma unroll
-    for (int e = 0; e < V; ++e) g[e] = e < p.n ? p.sub * m.groups + (p.c + e) / m.per : 0;
+    for (int e = 0; e < V; ++e) g[e] = e < p.n ? p.sub * m.groups + m.by_per(p.c + e) : 0;
 }
 
 // ---- all positions of a sample in registers ----
@@ -192,10 +272,10 @@ __global__ __launch_bounds__(MOST) void k_resident_forward(Norm P)
     extern __shared__ float norm_lds[];
     constexpr int V = kVec<T>;
     const Map &m = P.map;
-    const int c0 = blockIdx.y * m.width, width = P.C - c0 < m.width ? P.C - c0 : m.width, g0 = c0 / m.per;
-    const int groups = width / m.per, sets = m.subs * m.groups;
+    const int c0 = blockIdx.y * m.width, width = P.C - c0 < m.width ? P.C - c0 : m.width, g0 = m.by_per(c0);
+    const int groups = m.by_per(width), sets = m.sets;
     const Place p = place<V>(m, width);
-    float *first = norm_lds + reduce_floats(blockDim.x, V, 1), *second = first + sets;
+    float *first = norm_lds + reduce_floats(blockDim.x, V), *second = first + sets;
     float gamma[V], beta[V];
     int of[V];
     parameters<T, V>(gamma, P.gamma, c0 + p.c, p.n, 1.0f);
@@ -207,38 +287,43 @@ __global__ __launch_bounds__(MOST) void k_resident_forward(Norm P)
         const int S = b < P.B && p.n ? P.S : 0;   // positions of this thread's
         const T *x = (const T *)P.x + b * P.S * P.ldx + c0 + p.c;
         u32x4 w[ROWS];
-        float s[1][V] = {};
+        float sum[V] = {}, far[V] = {}, count = 0.0f;
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
             const int row = p.row + k * m.lanes;
             w[k] = u32x4{0, 0, 0, 0};
-            if (row < S) w[k] = get<T, V>(x + row * P.ldx, p.n);
+            if (row < S) w[k] = get<T, V>(x + row * P.ldx, p.n), count += 1.0f;
         }
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
             float v[V];
             widened<T, V>(v, w[k]);
 #pragma unroll
-            for (int e = 0; e < V; ++e) s[0][e] += v[e];
+            for (int e = 0; e < V; ++e) sum[e] += v[e];
         }
-        group_sums<V, 1>(m, p, s, norm_lds, first);
+        if (ROWS > 1) {
+            const float one = 1.0f / count;
+#pragma unroll
+            for (int k = 0; k < ROWS; ++k) {
+                if (p.row + k * m.lanes >= S) continue;
+                float v[V];
+                widened<T, V>(v, w[k]);
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    const float d = __builtin_fmaf(sum[e], -one, v[e]);
+                    far[e] = __builtin_fmaf(d, d, far[e]);
+                }
+            }
+        }
+        group_moments<V>(m, p, sum, far, count, P.S, norm_lds, first);
         float mean[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) mean[e] = first[of[e]] * inv, s[0][e] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            if (p.row + k * m.lanes >= S) continue;
-            float v[V];
-            widened<T, V>(v, w[k]);
-#pragma unroll
-            for (int e = 0; e < V; ++e) s[0][e] = __builtin_fmaf(v[e] - mean[e], v[e] - mean[e], s[0][e]);
-        }
-        group_sums<V, 1>(m, p, s, norm_lds, second);
+        for (int e = 0; e < V; ++e) mean[e] = first[of[e]];
         if (P.mean)
             for (int i = threadIdx.x; i < sets; i += blockDim.x) {
-                const int sub = i / m.groups, g = i - sub * m.groups;
+                const int sub = m.by_groups(i), g = i - sub * m.groups;
                 if (b0 + sub >= P.B || g >= groups) continue;
-                P.mean[(b0 + sub) * P.G + g0 + g] = first[i] * inv;
+                P.mean[(b0 + sub) * P.G + g0 + g] = first[i];
                 P.rstd[(b0 + sub) * P.G + g0 + g] = 1.0f / sqrtf(second[i] * inv + P.eps);
             }
         float a[V];
@@ -260,19 +345,19 @@ __global__ __launch_bounds__(MOST) void k_resident_forward(Norm P)
     }
 }
 
-// dz of a thread's channels at one position, and xhat.
+// dz of a thread's channels at one position, and x - mean; scale: rstd gamma.
 template <typename T, int V>
-__device__ __forceinline__ void gradient_at(float (&dz)[V], float (&hat)[V], const u32x4 &x, const u32x4 &dy, const float (&mean)[V],
-                                            const float (&rstd)[V], const float (&gamma)[V], const float (&beta)[V], int act)
+__device__ __forceinline__ void gradient_at(float (&dz)[V], float (&far)[V], const u32x4 &x, const u32x4 &dy, const float (&mean)[V],
+                                            const float (&scale)[V], const float (&beta)[V], int act)
 {
-    widened<T, V>(hat, x);
+    widened<T, V>(far, x);
     widened<T, V>(dz, dy);
 #pragma unroll
-    for (int e = 0; e < V; ++e) hat[e] = (hat[e] - mean[e]) * rstd[e];
+    for (int e = 0; e < V; ++e) far[e] -= mean[e];
     if (act == HQML_ACT_NONE) return;
     float z[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) z[e] = __builtin_fmaf(hat[e], gamma[e], beta[e]);
+    for (int e = 0; e < V; ++e) z[e] = __builtin_fmaf(far[e], scale[e], beta[e]);
     slope<sizeof(T) == 2>(z, act);
 #pragma unroll
     for (int e = 0; e < V; ++e) dz[e] *= z[e];
@@ -293,10 +378,16 @@ __device__ __forceinline__ void parameter_sums(const Norm &P, const Place &p, co
 #pragma unroll
             for (int e = 0; e < V; ++e) lds[(q * T_ + (int)threadIdx.x) * V + e] = s[q][e];
     __syncthreads();
-    for (int i = threadIdx.x; i < 2 * width; i += T_) {
+    int each = 1;   // lanes of a sum
+    while (each < 64 && each * 4 * width <= T_ && each < down) each <<= 1;
+    const int lane = threadIdx.x & (each - 1);
+    for (int i = (int)threadIdx.x / each; i < 2 * width; i += T_ / each) {
         const int q = i >= width, c = i - q * width;
         float sum = 0.0f;
-        for (int l = 0; l < down; ++l) sum += lds[q * T_ * V + l * pitch + c];
+#pragma unroll 4
+        for (int l = lane; l < down; l += each) sum += lds[q * T_ * V + l * pitch + c];
+        sum = lanes_sum(sum, each);
+        if (lane) continue;
         if (P.part) P.part[(row * 2 + q) * P.C + c0 + c] = sum;
         else if (q && P.dgamma) narrow(sum, ((T *)P.dgamma)[c0 + c]);
         else if (!q && P.dbeta) narrow(sum, ((T *)P.dbeta)[c0 + c]);
@@ -309,10 +400,10 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
     extern __shared__ float norm_lds[];
     constexpr int V = kVec<T>;
     const Map &m = P.map;
-    const int c0 = blockIdx.y * m.width, width = P.C - c0 < m.width ? P.C - c0 : m.width, g0 = c0 / m.per;
-    const int sets = m.subs * m.groups;
+    const int c0 = blockIdx.y * m.width, width = P.C - c0 < m.width ? P.C - c0 : m.width, g0 = m.by_per(c0);
+    const int sets = m.sets;
     const Place p = place<V>(m, width);
-    float *groups = norm_lds + reduce_floats(blockDim.x, V, 2);
+    float *groups = norm_lds + reduce_floats(blockDim.x, V);
     float gamma[V], beta[V], all[2][V] = {};
     int of[V];
     parameters<T, V>(gamma, P.gamma, c0 + p.c, p.n, 1.0f);
@@ -325,7 +416,7 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
         const T *x = (const T *)P.x + b * P.S * P.ldx + c0 + p.c;
         const T *dy = (const T *)P.dy + b * P.S * P.lddy + c0 + p.c;
         u32x4 w[ROWS];
-        float dz[ROWS][V], mean[V], rstd[V];
+        float dz[ROWS][V], mean[V], rstd[V], scale[V];
         u32x4 d[ROWS];
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
@@ -336,24 +427,26 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
 #pragma unroll
         for (int e = 0; e < V; ++e) {
             const bool some = S > 0 && e < p.n;
-            const long long g = b * P.G + g0 + (p.c + e) / m.per;
+            const long long g = b * P.G + g0 + m.by_per(p.c + e);
             mean[e] = some ? P.mean[g] : 0.0f;
             rstd[e] = some ? P.rstd[g] : 0.0f;
+            scale[e] = rstd[e] * gamma[e];
         }
         float s[2][V] = {};
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
-            float hat[V];
-            gradient_at<T, V>(dz[k], hat, w[k], d[k], mean, rstd, gamma, beta, P.act);
+            float far[V];
+            gradient_at<T, V>(dz[k], far, w[k], d[k], mean, scale, beta, P.act);
             const bool some = p.row + k * m.lanes < S;
 #pragma unroll
             for (int e = 0; e < V; ++e) {
                 s[0][e] += some ? dz[k][e] : 0.0f;
-                s[1][e] += some ? dz[k][e] * hat[e] : 0.0f;
+                s[1][e] += some ? dz[k][e] * far[e] : 0.0f;
             }
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
+            s[1][e] *= rstd[e];
             all[0][e] += s[0][e], all[1][e] += s[1][e];
             s[0][e] *= gamma[e], s[1][e] *= gamma[e];
         }
@@ -376,7 +469,7 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
             __syncthreads();   // the sums have been read
         }
     }
-    if (P.part || P.dgamma || P.dbeta) parameter_sums<T, V>(P, p, all, c0, width, blockIdx.x, norm_lds);
+    if (P.dgamma || P.dbeta) parameter_sums<T, V>(P, p, all, c0, width, blockIdx.x, norm_lds);
 }
 
 // ---- chunks of positions ----
@@ -427,7 +520,7 @@ __device__ __forceinline__ float over_chunks(const Norm &P, int n, float *lds, F
     return lds[(int)threadIdx.x < n ? threadIdx.x : 0];
 }
 
-constexpr int kStep = 8;   // positions of a thread under way together
+constexpr int kStep = 4;   // positions of a thread under way together
 
 // Mean and squared distance from it, of a chunk's groups; the sample's last workgroup joins them.
 template <typename T>
@@ -440,10 +533,8 @@ __global__ __launch_bounds__(1024) void k_stats(Norm P)
     const int b = blockIdx.x / P.chunks, chunk = blockIdx.x - b * P.chunks;
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
-    float *first = norm_lds + reduce_floats(blockDim.x, V, 1), *second = first + m.groups;
-    int of[V];
-    groups_of(of, m, p);
-    // by channel: mean and squared distance of the positions so far, joined eight at a time
+    float *first = norm_lds + reduce_floats(blockDim.x, V), *second = first + m.groups;
+    // by channel: mean and squared distance of the positions so far, joined kStep at a time
     float mean[V] = {}, far[V] = {};
     float count = 0.0f;
     for (int r0 = s0 + p.row; r0 < s1 && p.n; r0 += kStep * m.lanes) {
@@ -482,20 +573,13 @@ __global__ __launch_bounds__(1024) void k_stats(Norm P)
         }
         count = all;
     }
-    float s[1][V];
+    float sum[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) s[0][e] = mean[e] * count;
-    group_sums<V, 1>(m, p, s, norm_lds, first);
-    const float values = (float)(s1 - s0) * (float)m.per;
-#pragma unroll
-    for (int e = 0; e < V; ++e) {
-        const float d = mean[e] - first[of[e]] / values;
-        s[0][e] = count > 0.0f ? __builtin_fmaf(d * d, count, far[e]) : 0.0f;
-    }
-    group_sums<V, 1>(m, p, s, norm_lds, second);
+    for (int e = 0; e < V; ++e) sum[e] = mean[e] * count;
+    group_moments<V>(m, p, sum, far, count, s1 - s0, norm_lds, first);
     float *mine = P.stat + ((long long)b * P.chunks + chunk) * P.G * 2;
     for (int g = threadIdx.x; g < P.G; g += blockDim.x) {
-        leave(mine + g * 2, first[g] / values);
+        leave(mine + g * 2, first[g]);
         leave(mine + g * 2 + 1, second[g]);
     }
     if (!last_of(P, b)) return;
@@ -540,7 +624,7 @@ __global__ __launch_bounds__(1024) void k_apply_forward(Norm P)
     parameters<T, V>(beta, P.beta, p.c, p.n, 0.0f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const long long g = (long long)b * P.G + (p.c + (e < p.n ? e : 0)) / m.per;
+        const long long g = (long long)b * P.G + m.by_per(p.c + (e < p.n ? e : 0));
         mean[e] = P.mean[g];
         a[e] *= P.rstd[g];
     }
@@ -580,15 +664,16 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
     const T *dy = (const T *)P.dy + (long long)b * P.S * P.lddy + p.c;
-    float *groups = norm_lds + reduce_floats(blockDim.x, V, 2);
-    float gamma[V], beta[V], mean[V], rstd[V], s[2][V] = {};
+    float *groups = norm_lds + reduce_floats(blockDim.x, V);
+    float gamma[V], beta[V], mean[V], rstd[V], scale[V], s[2][V] = {};
     parameters<T, V>(gamma, P.gamma, p.c, p.n, 1.0f);
     parameters<T, V>(beta, P.beta, p.c, p.n, 0.0f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const long long g = (long long)b * P.G + (p.c + e) / m.per;
+        const long long g = (long long)b * P.G + m.by_per(p.c + e);
         mean[e] = e < p.n ? P.mean[g] : 0.0f;
         rstd[e] = e < p.n ? P.rstd[g] : 0.0f;
+        scale[e] = rstd[e] * gamma[e];
     }
     for (int r0 = s0 + p.row; r0 < s1 && p.n; r0 += kStepBack * m.lanes) {
         u32x4 w[kStepBack], d[kStepBack];
@@ -604,12 +689,14 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
 #pragma unroll
         for (int k = 0; k < kStepBack; ++k) {
             if (r0 + k * m.lanes >= s1) continue;
-            float dz[V], hat[V];
-            gradient_at<T, V>(dz, hat, w[k], d[k], mean, rstd, gamma, beta, P.act);
+            float dz[V], far[V];
+            gradient_at<T, V>(dz, far, w[k], d[k], mean, scale, beta, P.act);
 #pragma unroll
-            for (int e = 0; e < V; ++e) s[0][e] += dz[e], s[1][e] = __builtin_fmaf(dz[e], hat[e], s[1][e]);
+            for (int e = 0; e < V; ++e) s[0][e] += dz[e], s[1][e] = __builtin_fmaf(dz[e], far[e], s[1][e]);
         }
     }
+#pragma unroll
+    for (int e = 0; e < V; ++e) s[1][e] *= rstd[e];
     if (P.part) parameter_sums<T, V>(P, p, s, 0, P.C, (long long)b * P.chunks + chunk, norm_lds);
     if (!P.dx) return;
 #pragma unroll
@@ -632,9 +719,44 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
     }
 }
 
+// dgamma and dbeta: the sums over `rows` partial ones, eight channels of one of them a workgroup, its other threads down the
+// rows.
+template <typename T>
+__device__ __forceinline__ void reduce_parameters(const Norm &P, int block)
+{
+    __shared__ float held[128][8];
+    const int lane = threadIdx.x & 7, down = threadIdx.x >> 3, across = blockDim.x >> 3, blocks = (P.C + 7) / 8;
+    const int q = block / blocks, c = (block - q * blocks) * 8 + lane;
+    float s = 0.0f;
+    if (c < P.C)
+#pragma unroll 8
+        for (int r = down; r < P.rows; r += across) s += P.part[((long long)r * 2 + q) * P.C + c];
+    held[down][lane] = s;
+    int h = 64;   // the rows' threads, of which there are 32 to 128
+    while (h >= across) h >>= 1;
+    for (; h; h >>= 1) {
+        __syncthreads();
+        if (down < h && down + h < across) held[down][lane] += held[down + h][lane];
+    }
+    if (down || c >= P.C) return;
+    T *to = (T *)(q ? P.dgamma : P.dbeta);
+    if (to) narrow(held[0][lane], to[c]);
+}
+
+template <typename T>
+__global__ __launch_bounds__(1024) void k_parameters(Norm P)
+{
+    reduce_parameters<T>(P, blockIdx.x);
+}
+
+// dx by chunks; the first `extra` workgroups, if any, form dgamma and dbeta.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
 {
+    if ((int)blockIdx.x < P.extra) {
+        reduce_parameters<T>(P, blockIdx.x);
+        return;
+    }
     constexpr int V = kVec<T>;
     const Map &m = P.map;
     const Place p = place<V>(m, P.C);
@@ -644,14 +766,16 @@ __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
     const T *dy = (const T *)P.dy + (long long)b * P.S * P.lddy + p.c;
     T *dx = (T *)P.dx + (long long)b * P.S * P.lddx + p.c;
-    float gamma[V], beta[V], mean[V], rstd[V], one[V], two[V];
+    float gamma[V], beta[V], mean[V], scale[V], one[V], two[V];
     parameters<T, V>(gamma, P.gamma, p.c, p.n, 1.0f);
     parameters<T, V>(beta, P.beta, p.c, p.n, 0.0f);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const long long g = (long long)b * P.G + (p.c + (e < p.n ? e : 0)) / m.per;
-        mean[e] = P.mean[g], rstd[e] = P.rstd[g];
-        one[e] = P.group[g * 2], two[e] = P.group[g * 2 + 1];
+        const long long g = (long long)b * P.G + m.by_per(p.c + (e < p.n ? e : 0));
+        mean[e] = P.mean[g];
+        const float rstd = P.rstd[g];
+        scale[e] = rstd * gamma[e];   // dx = scale dz - one - (x - mean) two
+        one[e] = rstd * P.group[g * 2], two[e] = rstd * rstd * P.group[g * 2 + 1];
     }
     for (int r0 = s0 + p.row; r0 < s1; r0 += kStepBack * m.lanes) {
         u32x4 w[kStepBack], d[kStepBack];
@@ -668,32 +792,13 @@ __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
         for (int k = 0; k < kStepBack; ++k) {
             const int row = r0 + k * m.lanes;
             if (row >= s1) continue;
-            float dz[V], hat[V];
-            gradient_at<T, V>(dz, hat, w[k], d[k], mean, rstd, gamma, beta, P.act);
+            float dz[V], far[V];
+            gradient_at<T, V>(dz, far, w[k], d[k], mean, scale, beta, P.act);
 #pragma unroll
-            for (int e = 0; e < V; ++e) dz[e] = rstd[e] * (gamma[e] * dz[e] - (one[e] + hat[e] * two[e]));
+            for (int e = 0; e < V; ++e) dz[e] = __builtin_fmaf(scale[e], dz[e], -__builtin_fmaf(far[e], two[e], one[e]));
             put<T, V>(dx + (long long)row * P.lddx, dz, p.n);
         }
     }
-}
-
-// dgamma and dbeta: the sums over `rows` partial ones, eight channels a workgroup, 32 threads down the rows.
-template <typename T>
-__global__ __launch_bounds__(256) void k_parameters(const float *part, int rows, int C, T *dgamma, T *dbeta)
-{
-    __shared__ float held[32][8];
-    const int lane = threadIdx.x & 7, down = threadIdx.x >> 3, c = blockIdx.x * 8 + lane, q = blockIdx.y;
-    float s = 0.0f;
-    if (c < C)
-#pragma unroll 4
-        for (int r = down; r < rows; r += 32) s += part[((long long)r * 2 + q) * C + c];
-    held[down][lane] = s;
-    __syncthreads();
-    if (down || c >= C) return;
-#pragma unroll
-    for (int k = 1; k < 32; ++k) s += held[k][lane];
-    T *to = q ? dgamma : dbeta;
-    if (to) narrow(s, to[c]);
 }
 
 template <typename T>
@@ -707,7 +812,7 @@ __global__ void k_zero(T *a, T *b, int n)
 // ---- which runs, and how it is cut ----
 
 constexpr int kUnits = 256;          // compute units
-constexpr int kSplitGroups = 2048;   // workgroups that a split call aims at
+constexpr int kSplitGroups = 1024;   // workgroups that a split call aims at
 constexpr int kResidentMost = 1024;  // workgroups of a span in a resident backward pass
 constexpr int kMinSegment = 64;      // bytes of a row that a span has at least, unless the array is small
 constexpr long long kSmallArray = 1 << 20;
@@ -729,6 +834,24 @@ int split_lanes(int C)
 
 // The most positions of a thread: what its registers hold (backward: x, and dz in 32 bits), by the size of the workgroup.
 constexpr int kMostForward = 16, kMostBackward = 8, kMostOf1024 = 4;
+// Threads of the workgroups that small samples share: in the backward pass each leaves sums of all parameters.
+constexpr int kTogetherForward = 256, kTogetherBackward = 1024;
+
+// What follows from a map's widths, for workgroups of `threads`.
+template <typename T>
+void complete(Map &m, int threads)
+{
+    constexpr int V = kVec<T>;
+    const bool whole = m.per % V == 0;
+    m.wide = whole ? 1 : V;
+    m.pitch = m.vecs * m.wide;
+    m.mine = whole ? m.per / V : m.per;
+    m.channels = whole ? (float)V : 1.0f;
+    m.sets = m.subs * m.groups;
+    m.each = 1;
+    while (m.each < 64 && m.each * 2 * m.sets <= threads && m.each < m.mine * m.lanes) m.each <<= 1;
+    m.by_vecs = Div(m.vecs), m.by_lanes = Div(m.lanes), m.by_per = Div(m.per), m.by_groups = Div(m.groups), m.by_mine = Div(m.mine);
+}
 
 struct Resident {
     bool fits;
@@ -736,8 +859,9 @@ struct Resident {
     Map map;
 };
 
+// most: positions that a thread holds; together: threads that small samples share.
 template <typename T>
-Resident resident(int B, int S, int C, int G, int most)
+Resident resident(int B, int S, int C, int G, int most, int together)
 {
     constexpr int V = kVec<T>;
     const int per = C / G;
@@ -746,9 +870,12 @@ Resident resident(int B, int S, int C, int G, int most)
     // spans of whole groups: as many as give every compute unit one workgroup, of at least kMinSegment bytes of a row
     const bool small = (long long)B * S * C * (int)sizeof(T) <= kSmallArray;
     const int least = small ? per : std::max(1, ceil_div(kMinSegment / (int)sizeof(T), per)) * per;
-    int all = 0;   // threads down the positions that there can be
+    int unit = 1;   // groups that fill whole vectors
+    while (unit * per % V) ++unit;
+    int all = 0;    // threads down the positions that there can be
     for (int spans = std::min(ceil_div(kUnits, B), std::max(1, C / least));; ++spans) {
-        const int each = ceil_div(G, std::min(spans, G));   // groups of a span
+        int each = ceil_div(G, std::min(spans, G));   // groups of a span
+        if (each > unit) each = each / unit * unit;
         r.spans = ceil_div(G, each);
         m.width = each * per;
         m.groups = each;
@@ -763,9 +890,9 @@ Resident resident(int B, int S, int C, int G, int most)
     m.per = per;
     r.rows = ceil_div(S, all);
     m.lanes = ceil_div(S, r.rows);
-    // small samples share a workgroup of four waves
-    m.subs = std::max(1, std::min({all / m.lanes, 256 / (m.vecs * m.lanes), B}));
+    m.subs = std::max(1, std::min({r.rows == 1 ? together / (m.vecs * m.lanes) : 256 / (m.vecs * m.lanes), B}));
     r.threads = ceil_div(m.vecs * m.lanes * m.subs, 64) * 64;
+    complete<T>(m, r.threads);
     return r;
 }
 
@@ -792,6 +919,7 @@ int cut(Norm &P, const NormWorkspace &ws)
     m.subs = 1;
     m.per = P.C / P.G;
     m.groups = P.G;
+    complete<T>(m, split_threads<T>(P.C));
     const long long rows = (long long)P.B * P.S;
     P.chunk = (int)std::min<long long>(P.S, std::max<long long>(m.lanes * kStep, (rows + kSplitGroups - 1) / kSplitGroups));
     P.chunks = ceil_div(P.S, P.chunk);
@@ -817,19 +945,19 @@ bool fits(const Norm &P, const NormWorkspace &ws, bool parameters)
            (size_t)P.B * sizeof(unsigned) <= ws.ticket_bytes;
 }
 
-size_t lds_bytes(int threads, int V, int Q, int sets) { return (size_t)(reduce_floats(threads, V, Q) + 2 * sets) * 4; }
+size_t lds_bytes(int threads, int V, int sets) { return (size_t)(reduce_floats(threads, V) + 2 * sets) * 4; }
 
 template <typename T>
 hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 {
     Norm P = common(a);
-    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward);
+    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward, kTogetherForward);
     if (r.fits) {
         P.map = r.map;
         const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), 1 << 20), (unsigned)r.spans);
-        const size_t lds = lds_bytes(r.threads, kVec<T>, 1, r.map.subs * r.map.groups);
-        if (r.threads > 512) k_resident_forward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
-        else if (r.rows <= 1) k_resident_forward<T, 1, 512><<<grid, r.threads, lds, s>>>(P);
+        const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
+        if (r.rows <= 1) k_resident_forward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
+        else if (r.threads > 512) k_resident_forward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.rows <= 4) k_resident_forward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
         else k_resident_forward<T, kMostForward, 512><<<grid, r.threads, lds, s>>>(P);
         return hipGetLastError();
@@ -838,7 +966,7 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
     if (!fits(P, ws, false)) return hipErrorInvalidValue;
     if (!P.mean) P.mean = ws.group, P.rstd = ws.group + (size_t)a.B * a.G;
     const unsigned grid = (unsigned)a.B * (unsigned)P.chunks;
-    k_stats<T><<<grid, threads, lds_bytes(threads, kVec<T>, 1, a.G), s>>>(P);
+    k_stats<T><<<grid, threads, lds_bytes(threads, kVec<T>, a.G), s>>>(P);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     k_apply_forward<T><<<grid, threads, 0, s>>>(P);
@@ -849,37 +977,41 @@ template <typename T>
 hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 {
     Norm P = common(a);
+    P.dgamma = a.dgamma, P.dbeta = a.dbeta;
     const bool parameters = a.dgamma || a.dbeta;
-    int rows = 0;   // of partial sums
-    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward);
+    const int blocks = 2 * ceil_div(a.C, 8);   // of reduce_parameters
+    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward, kTogetherBackward);
     if (r.fits) {
         P.map = r.map;
         const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), kResidentMost), (unsigned)r.spans);
         if (parameters && grid.x > 1) {
-            rows = (int)grid.x;
+            P.rows = (int)grid.x;
             P.part = ws.part;
-            if ((size_t)rows * 2 * a.C * 4 > ws.part_bytes) return hipErrorInvalidValue;
-        } else {
-            P.dgamma = a.dgamma, P.dbeta = a.dbeta;
+            if ((size_t)P.rows * 2 * a.C * 4 > ws.part_bytes) return hipErrorInvalidValue;
         }
-        const size_t lds = lds_bytes(r.threads, kVec<T>, 2, r.map.subs * r.map.groups);
-        if (r.threads > 512) k_resident_backward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
-        else if (r.rows <= 1) k_resident_backward<T, 1, 512><<<grid, r.threads, lds, s>>>(P);
+        const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
+        if (r.rows <= 1) k_resident_backward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
+        else if (r.threads > 512) k_resident_backward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.rows <= 4) k_resident_backward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
         else k_resident_backward<T, kMostBackward, 512><<<grid, r.threads, lds, s>>>(P);
-    } else {
-        const int threads = cut<T>(P, ws);
-        if (!fits(P, ws, parameters)) return hipErrorInvalidValue;
-        const unsigned grid = (unsigned)a.B * (unsigned)P.chunks;
-        if (parameters) rows = (int)grid, P.part = ws.part + (size_t)grid * 2 * a.G;
-        k_sums<T><<<grid, threads, lds_bytes(threads, kVec<T>, 2, a.G), s>>>(P);
-        hipError_t e = hipGetLastError();
-        if (e != hipSuccess) return e;
-        if (a.dx) k_apply_backward<T><<<grid, threads, 0, s>>>(P);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || !P.rows) return e;
+        k_parameters<T><<<blocks, 512, 0, s>>>(P);
+        return hipGetLastError();
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || !rows) return e;
-    k_parameters<T><<<dim3((unsigned)ceil_div(a.C, 8), 2), 256, 0, s>>>(P.part, rows, a.C, (T *)a.dgamma, (T *)a.dbeta);
+    const int threads = cut<T>(P, ws);
+    if (!fits(P, ws, parameters)) return hipErrorInvalidValue;
+    const unsigned grid = (unsigned)a.B * (unsigned)P.chunks;
+    if (parameters) P.rows = (int)grid, P.part = ws.part + (size_t)grid * 2 * a.G;
+    k_sums<T><<<grid, threads, lds_bytes(threads, kVec<T>, a.G), s>>>(P);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if (a.dx) {
+        P.extra = parameters ? blocks : 0;
+        k_apply_backward<T><<<grid + P.extra, threads, 0, s>>>(P);
+    } else {   // as many threads: the sums' order, and so their last bit, is the same
+        k_parameters<T><<<blocks, threads, 0, s>>>(P);
+    }
     return hipGetLastError();
 }
 
@@ -887,9 +1019,9 @@ hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 template <typename T>
 hipError_t configure()
 {
-    const void *kernels[] = {(const void *)k_resident_forward<T, 1, 512>,          (const void *)k_resident_forward<T, 4, 512>,
+    const void *kernels[] = {(const void *)k_resident_forward<T, 1, 1024>,          (const void *)k_resident_forward<T, 4, 512>,
                              (const void *)k_resident_forward<T, kMostForward, 512>, (const void *)k_resident_forward<T, kMostOf1024, 1024>,
-                             (const void *)k_resident_backward<T, 1, 512>,         (const void *)k_resident_backward<T, 4, 512>,
+                             (const void *)k_resident_backward<T, 1, 1024>,         (const void *)k_resident_backward<T, 4, 512>,
                              (const void *)k_resident_backward<T, kMostBackward, 512>,
                              (const void *)k_resident_backward<T, kMostOf1024, 1024>, (const void *)k_stats<T>, (const void *)k_sums<T>};
     for (const void *k : kernels) {

@@ -10,18 +10,20 @@ from __future__ import annotations
 import copy
 import ctypes
 import math
+import struct
 
 import torch
 from torch.optim.optimizer import _global_optimizer_post_hooks, _global_optimizer_pre_hooks
 
 from . import (HQML_ADAMW_BLOCK, HQML_DTYPE_BF16, HQML_DTYPE_FP32, HQML_DTYPE_FP64, HQML_MOMENTS_8, HQML_MOMENTS_32,
                HQML_MUON_MAX_SIDE, HQML_MUON_MAX_STEPS, hqml_adamw_config, hqml_adamw_step, hqml_muon_config,
-               hqml_muon_step, hqml_muon_tensor, hqml_muon_workspace_bytes)
+               hqml_muon_step, hqml_muon_workspace_bytes)
 
 _DTYPES = {torch.float32: HQML_DTYPE_FP32, torch.bfloat16: HQML_DTYPE_BF16, torch.float64: HQML_DTYPE_FP64}
 _WIDE = {torch.float32: torch.float32, torch.bfloat16: torch.float32, torch.float64: torch.float64}
 _CODES = torch.float8_e4m3fn
 _MATRIX = (torch.float32, torch.bfloat16)   # Muon's types
+_TENSOR = "QQQiid"   # hqml_muon_tensor: three addresses, rows, columns, its factor of lr
 _current_stream = torch._C._cuda_getCurrentRawStream
 
 
@@ -265,33 +267,39 @@ class Muon(torch.optim.Optimizer):
         for group in self.param_groups:
             size_of = self._adjust[group["adjust"]]
             calls = {}   # matrices that one call can take
+            state = self.state
             for p in group["params"]:
                 g = p.grad
                 if g is None:
                     continue
-                if g.layout is not torch.strided or g.dtype not in _MATRIX:
-                    raise ValueError("gradients must be dense, in fp32 or bf16")
                 self._fits(p)
-                if g.shape != p.shape:
-                    raise ValueError(f"a parameter {tuple(p.shape)} has a gradient {tuple(g.shape)}")
+                shape, dtype = p.shape, g.dtype
+                if dtype not in _MATRIX or g.layout is not torch.strided:
+                    raise ValueError("gradients must be dense, in fp32 or bf16")
+                if g.shape != shape:
+                    raise ValueError(f"a parameter {tuple(shape)} has a gradient {tuple(g.shape)}")
                 if not g.is_contiguous():
                     g = g.detach().contiguous()
-                m = self._momentum(p, self.state[p])
-                tensors, params, kept = calls.setdefault((p.dtype, g.dtype, p.get_device()), ([], [], []))
-                rows, cols = p.shape
-                tensors.append(hqml_muon_tensor(p.data_ptr(), g.data_ptr(), m.data_ptr(), rows, cols, size_of(rows, cols)
-                                                if rows and cols else 0.0))
+                m = self._momentum(p, state[p])
+                key = (p.dtype, dtype, p.get_device())
+                call = calls.get(key)
+                if call is None:
+                    call = calls[key] = ([], [], [])
+                words, params, kept = call
+                rows, cols = shape
+                words += (p.data_ptr(), g.data_ptr(), m.data_ptr(), rows, cols, size_of(rows, cols) if rows and cols else 0.0)
                 params.append(p)
                 kept.append(g)    # until its kernels are queued
-            for (pd, gd, device), (tensors, params, kept) in calls.items():
+            for (pd, gd, device), (words, params, kept) in calls.items():
                 cfg = hqml_muon_config(_DTYPES[pd], _DTYPES[gd], bool(group["nesterov"]), group["steps"], group["lr"],
                                        group["momentum"], group["weight_decay"], group["eps"], *group["coefficients"],
                                        device, _current_stream(device))
-                array = (hqml_muon_tensor * len(tensors))(*tensors)
-                need = hqml_muon_workspace_bytes(cfg, len(tensors), array)
+                n = len(params)
+                tensors = struct.pack(_TENSOR * n, *words)   # n hqml_muon_tensor
+                need = hqml_muon_workspace_bytes(cfg, n, tensors)
                 # torch's memory: freed at once, it is handed out again only to what the stream runs later
                 work = torch.empty(need, dtype=torch.uint8, device=params[0].device) if need else None
-                hqml_muon_step(cfg, len(tensors), array, work.data_ptr() if need else None, need)
+                hqml_muon_step(cfg, n, tensors, work.data_ptr() if need else None, need)
                 # a backward pass that saved a parameter from before this step has to refuse it
                 torch.autograd.graph.increment_version(params)
         return loss

@@ -210,7 +210,8 @@ def calls(monkeypatch):
     seen = []
 
     def record(cfg, n, tensors, work, size):
-        seen.append((cfg, [(t.param, t.grad, t.momentum, t.rows, t.cols, t.scale) for t in tensors[:n]], size))
+        array = (hq.hqml_muon_tensor * n).from_buffer_copy(tensors)
+        seen.append((cfg, [(t.param, t.grad, t.momentum, t.rows, t.cols, t.scale) for t in array], size))
 
     monkeypatch.setattr(optim, "hqml_muon_step", record)
     monkeypatch.setattr(optim, "_current_stream", lambda device: 0)
