@@ -438,9 +438,17 @@ hipError_t forward(const Dense8Forward &a, const Dense8Workspace &ws, hipStream_
     P.act = a.act, P.alpha = a.alpha;
     P.part = ws.part, P.ticket = ws.ticket;
     const Scales8 q{ws.scales, a.scales};
+    // Codes of x by the workgroups that use them, or by a launch before: the least of estimates.  The launch takes 4.5 us and
+    // memory's time; a workgroup's own codes 1.2, and 0.6 for each sixteen values of a thread.
     const Cut tiles = best_cut(P.I, P.J, P.K, 2, true);
-    const SmallCut few = small_cut(P.I, P.J, P.K, 2, true);
-    const bool small = few.us <= tiles.us;
+    SmallCut few = small_cut(P.I, P.J, P.K, 2, true);
+    const SmallCut few16 = small_cut(P.I, P.J, P.K, 2, true, 1);
+    const int rows = std::min(a.M, 16), each = ceil_div(rows * (pairs / 8), 64 * few16.waves);
+    const float before = 4.5f + (float)a.M * a.K * (sizeof(T) + 1) / 3.5e6f;
+    const bool own = each <= kOwnHeld && own_bytes(rows, pairs) <= kOwnLds &&
+                     few16.us + 1.2f + 0.6f * (float)each <= before + std::min(few.us, tiles.us);
+    const bool small = own || few.us <= tiles.us;
+    if (own) few = few16;
     const int side_i = small ? 16 * few.fi : kSides[tiles.shape][0], side_j = small ? 16 : kSides[tiles.shape][1];
     const int parts = small ? few.parts : tiles.parts;
     P.tiles_i = ceil_div(P.I, side_i), P.tiles_j = ceil_div(P.J, side_j);
@@ -449,9 +457,7 @@ hipError_t forward(const Dense8Forward &a, const Dense8Workspace &ws, hipStream_
     const size_t all = (size_t)P.tiles_i * P.tiles_j;
     if (P.parts > 1 && (all * P.parts * side_i * side_j * 4 > ws.part_bytes || all * sizeof(unsigned) > ws.ticket_bytes))
         return hipErrorInvalidValue;
-    // a tile's rows of x in the registers of its workgroup, and their codes in its LDS
-    const int rows = std::min(a.M, 16);
-    if (small && few.fi == 1 && rows * (pairs / 8) <= kOwnHeld * 64 * few.waves && own_bytes(rows, pairs) <= kOwnLds) {
+    if (own) {
         P.a = a.x, P.lda = a.ldx;
         const dim3 grid((unsigned)all, (unsigned)P.parts);
         k_small8_own<T><<<grid, 64 * few.waves, own_bytes(rows, pairs) + few.waves * 1024, s>>>(P, q, a.K);

@@ -92,14 +92,15 @@ struct SmallCut {
     float us;
 };
 
-inline SmallCut small_cut(int I, int J, int K, size_t elem, bool words)
+// most: the largest fi.
+inline SmallCut small_cut(int I, int J, int K, size_t elem, bool words, int most = 4)
 {
     SmallCut best{0, 1, 1, 0.0f};
     const int steps = ceil_div(K, 32);
     const float bytes = ((float)I * K + (float)J * K + (float)I * J) * elem;
     const float rate = elem == 4 ? 81e3f : words ? 51e3f : 14.3e3f;
     for (int fi : {1, 2, 4}) {
-        if (fi > 1 && I <= 8 * fi) break;
+        if (fi > most || (fi > 1 && I <= 8 * fi)) break;
         const long long tiles = (long long)ceil_div(I, 16 * fi) * ceil_div(J, 16);
         const int rows = std::min(16 * fi, I) + std::min(16, J), at = fi == 4 ? 2 : 4;   // steps a wave loads together
         for (int parts : {1, 2, 3, 4, 6, 8}) {

@@ -174,8 +174,9 @@ __device__ __forceinline__ void each_value(const Map &m, int set, int lane, F ta
     const int sub = m.by_groups(set), g = set - sub * m.groups;
     const int from = sub * m.lanes * m.pitch + g * m.mine;
     int l = m.by_mine(lane), k = lane - l * m.mine;
-    const int dl = m.by_mine(m.each), dk = m.each - dl * m.mine;
-    while (l < m.lanes) {
+    const int dl = m.by_mine(m.each), dk = m.each - dl * m.mine, n = (m.mine * m.lanes - lane + m.each - 1) >> __builtin_ctz(m.each);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
         take(from + l * m.pitch + k, l);
         l += dl, k += dk;
         if (k >= m.mine) k -= m.mine, ++l;
@@ -890,7 +891,9 @@ Resident resident(int B, int S, int C, int G, int most, int together)
     m.per = per;
     r.rows = ceil_div(S, all);
     m.lanes = ceil_div(S, r.rows);
-    m.subs = std::max(1, std::min({r.rows == 1 ? together / (m.vecs * m.lanes) : 256 / (m.vecs * m.lanes), B}));
+    // but no fewer workgroups than half the compute units
+    const int most_subs = (int)std::min<long long>(B, std::max<long long>(1, 2 * (long long)B * r.spans / kUnits));
+    m.subs = std::max(1, std::min((r.rows == 1 ? together : 256) / (m.vecs * m.lanes), most_subs));
     r.threads = ceil_div(m.vecs * m.lanes * m.subs, 64) * 64;
     complete<T>(m, r.threads);
     return r;
