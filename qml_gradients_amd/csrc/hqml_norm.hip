@@ -65,6 +65,7 @@ struct Norm {
     float *part;        // backward: partial sums [rows][2][C] of dbeta and dgamma; null: the only workgroup of a span writes those
     void *dgamma, *dbeta;
     int rows, extra;
+    int ahead;          // rows that hold a thread's channels at least
     Map map;
     // split
     int chunk, chunks;      // positions of a chunk, chunks of a sample
@@ -93,10 +94,22 @@ __device__ __forceinline__ Place place(const Map &m, int width)
     return p;
 }
 
-template <typename T, int V>
-__device__ __forceinline__ u32x4 get(const T *from, int n)
+// Positions of sample b from which V channels may be read from channel c on, though they pass the row's end: all but the last
+// ones of the array.
+template <int V>
+__device__ __forceinline__ int rows_before_the_end(const Norm &P, long long b, int c)
 {
-    if (n == V) return *(const u32x4_any *)from;
+    if (c + V <= P.C) return P.S;
+    const long long left = (P.B - b) * (long long)P.S - P.ahead;
+    return left < P.S ? (int)left : P.S;
+}
+
+// A thread's channels at one position, of which n exist.  beyond: those that follow in memory may be read in their stead (they
+// are the row's next ones, or the next row's), which costs one load where n take one each.
+template <typename T, int V>
+__device__ __forceinline__ u32x4 get(const T *from, int n, bool beyond)
+{
+    if (n == V || beyond) return *(const u32x4_any *)from;
     T t[V] = {};
 #pragma unroll
     for (int e = 0; e < V; ++e)
@@ -107,16 +120,21 @@ __device__ __forceinline__ u32x4 get(const T *from, int n)
 template <typename T, int V>
 __device__ __forceinline__ void put(T *to, const float (&v)[V], int n)
 {
+    using u32x2_any = __attribute__((ext_vector_type(2), aligned(2))) uint32_t;
+    using u32_any = __attribute__((aligned(2))) uint32_t;
     T t[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) narrow(v[e], t[e]);
+    const u32x4 w = __builtin_bit_cast(u32x4, t);
     if (n == V) {
-        *(u32x4_any *)to = __builtin_bit_cast(u32x4, t);
+        *(u32x4_any *)to = w;
         return;
     }
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-        if (e < n) to[e] = t[e];
+    const int bytes = n * (int)sizeof(T);   // halves of what is left
+    char *at = (char *)to;
+    if (bytes & 8) *(u32x2_any *)at = u32x2_any{w[0], w[1]};
+    if (bytes & 4) *(u32_any *)(at + (bytes & 8)) = bytes & 8 ? w[2] : w[0];
+    if (bytes & 2) *(uint16_t *)(at + (bytes & 12)) = (uint16_t)(bytes & 8 ? bytes & 4 ? w[3] : w[2] : bytes & 4 ? w[1] : w[0]);
 }
 
 template <typename T, int V>
@@ -286,6 +304,7 @@ __global__ __launch_bounds__(MOST) void k_resident_forward(Norm P)
     for (long long b0 = (long long)blockIdx.x * m.subs; b0 < P.B; b0 += (long long)gridDim.x * m.subs) {
         const long long b = b0 + p.sub;
         const int S = b < P.B && p.n ? P.S : 0;   // positions of this thread's
+        const int beyond = rows_before_the_end<V>(P, b, c0 + p.c);
         const T *x = (const T *)P.x + b * P.S * P.ldx + c0 + p.c;
         u32x4 w[ROWS];
         float sum[V] = {}, far[V] = {}, count = 0.0f;
@@ -293,7 +312,7 @@ __global__ __launch_bounds__(MOST) void k_resident_forward(Norm P)
         for (int k = 0; k < ROWS; ++k) {
             const int row = p.row + k * m.lanes;
             w[k] = u32x4{0, 0, 0, 0};
-            if (row < S) w[k] = get<T, V>(x + row * P.ldx, p.n), count += 1.0f;
+            if (row < S) w[k] = get<T, V>(x + row * P.ldx, p.n, row < beyond), count += 1.0f;
         }
 #pragma unroll
         for (int k = 0; k < ROWS; ++k) {
@@ -414,6 +433,7 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
     for (long long b0 = (long long)blockIdx.x * m.subs; b0 < P.B; b0 += (long long)gridDim.x * m.subs) {
         const long long b = b0 + p.sub;
         const int S = b < P.B && p.n ? P.S : 0;
+        const int beyond = rows_before_the_end<V>(P, b, c0 + p.c);
         const T *x = (const T *)P.x + b * P.S * P.ldx + c0 + p.c;
         const T *dy = (const T *)P.dy + b * P.S * P.lddy + c0 + p.c;
         u32x4 w[ROWS];
@@ -423,7 +443,10 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
         for (int k = 0; k < ROWS; ++k) {
             const int row = p.row + k * m.lanes;
             w[k] = d[k] = u32x4{0, 0, 0, 0};
-            if (row < S) w[k] = get<T, V>(x + row * P.ldx, p.n), d[k] = get<T, V>(dy + row * P.lddy, p.n);
+            if (row < S) {
+                w[k] = get<T, V>(x + row * P.ldx, p.n, row < beyond);
+                d[k] = get<T, V>(dy + row * P.lddy, p.n, row < beyond);
+            }
         }
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -489,36 +512,64 @@ __device__ __forceinline__ bool last_of(const Norm &P, int b)
     return true;
 }
 
-__device__ __forceinline__ void leave(float *to, float v)
+using f32x2 = __attribute__((ext_vector_type(2))) float;
+
+__device__ __forceinline__ void leave(float *to, float a, float b)
 {
-    __hip_atomic_store(to, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    __hip_atomic_store((unsigned long long *)to, __builtin_bit_cast(unsigned long long, f32x2{a, b}), __ATOMIC_RELAXED,
+                       __HIP_MEMORY_SCOPE_AGENT);
 }
 
-__device__ __forceinline__ float fetch(const float *from)
+__device__ __forceinline__ f32x2 fetch(const float *from)
 {
-    return __hip_atomic_load(from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    return __builtin_bit_cast(f32x2, __hip_atomic_load((const unsigned long long *)from, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT));
 }
 
-// Sums over the chunks of a sample of f(chunk, group), for groups g0 .. g0 + n - 1: threads across the groups and down the
-// chunks, which meet in lds (a float a thread).  A thread below n receives its group's.
-template <typename F>
-__device__ __forceinline__ float over_chunks(const Norm &P, int n, float *lds, F f)
+// What the chunks of a sample left for n groups from g0 on, put together in their order: threads across the groups and down the
+// chunks.  take(value, pair, chunk) adds a chunk's to a thread's, join(value, other) one thread's to another's; a thread below n
+// receives its group's.  lds: a value a thread.
+template <class Value, class Take, class Join>
+__device__ __forceinline__ Value over_chunks(const Norm &P, const float *stat, int g0, int n, Value *lds, Take take, Join join)
 {
-    const int parts = blockDim.x / n, part = threadIdx.x / n, g = threadIdx.x - part * n;
-    float sum = 0.0f;
+    const int parts = blockDim.x / n, part = threadIdx.x / n, g = g0 + threadIdx.x - part * n;
+    constexpr int kAt = 8;   // loads under way together
+    Value v{};
     if (part < parts)
-#pragma unroll 4
-        for (int i = part; i < P.chunks; i += parts) sum += f(i, g);
+        for (int i0 = part; i0 < P.chunks; i0 += parts * kAt) {
+            f32x2 pair[kAt];
+#pragma unroll
+            for (int a = 0; a < kAt; ++a)
+                if (i0 + a * parts < P.chunks) pair[a] = fetch(stat + ((long long)(i0 + a * parts) * P.G + g) * 2);
+#pragma unroll
+            for (int a = 0; a < kAt; ++a)
+                if (i0 + a * parts < P.chunks) take(v, pair[a], i0 + a * parts);
+        }
     __syncthreads();   // lds is free
-    lds[threadIdx.x] = sum;
+    lds[threadIdx.x] = v;
     int h = 1;
     while (h < parts) h <<= 1;
     for (h >>= 1; h; h >>= 1) {
         __syncthreads();
-        if (part < h && part + h < parts) lds[threadIdx.x] += lds[threadIdx.x + h * n];
+        if (part < h && part + h < parts) {
+            join(v, lds[threadIdx.x + h * n]);
+            lds[threadIdx.x] = v;
+        }
     }
-    __syncthreads();
-    return lds[(int)threadIdx.x < n ? threadIdx.x : 0];
+    return v;
+}
+
+// Mean and squared distances from it of `count` values.
+struct Moments {
+    float count, mean, far;
+};
+
+__device__ __forceinline__ void join_moments(Moments &a, const Moments &b)
+{
+    if (b.count == 0.0f) return;
+    const float all = a.count + b.count, share = b.count / all, d = b.mean - a.mean;
+    a.far += __builtin_fmaf(d * d, a.count * share, b.far);
+    a.mean = __builtin_fmaf(d, share, a.mean);
+    a.count = all;
 }
 
 constexpr int kStep = 4;   // positions of a thread under way together
@@ -534,6 +585,7 @@ __global__ __launch_bounds__(1024) void k_stats(Norm P)
     const int b = blockIdx.x / P.chunks, chunk = blockIdx.x - b * P.chunks;
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
+    const int beyond = rows_before_the_end<V>(P, b, p.c);
     float *first = norm_lds + reduce_floats(blockDim.x, V), *second = first + m.groups;
     // by channel: mean and squared distance of the positions so far, joined kStep at a time
     float mean[V] = {}, far[V] = {};
@@ -545,7 +597,7 @@ __global__ __launch_bounds__(1024) void k_stats(Norm P)
         for (int k = 0; k < kStep; ++k) {
             const int row = r0 + k * m.lanes;
             w[k] = u32x4{0, 0, 0, 0};
-            if (row < s1) w[k] = get<T, V>(x + (long long)row * P.ldx, p.n), ++k_n;
+            if (row < s1) w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond), ++k_n;
         }
         const float n = (float)k_n, inv = 1.0f / n, all = count + n, share = n / all;
         float sum[V] = {}, sq[V] = {};
@@ -580,30 +632,23 @@ __global__ __launch_bounds__(1024) void k_stats(Norm P)
     group_moments<V>(m, p, sum, far, count, s1 - s0, norm_lds, first);
     float *mine = P.stat + ((long long)b * P.chunks + chunk) * P.G * 2;
     for (int g = threadIdx.x; g < P.G; g += blockDim.x) {
-        leave(mine + g * 2, first[g]);
-        leave(mine + g * 2 + 1, second[g]);
+        leave(mine + g * 2, first[g], second[g]);
     }
     if (!last_of(P, b)) return;
     const float *stat = P.stat + (long long)b * P.chunks * P.G * 2;
-    auto size = [&](int i) { return (float)((i + 1 == P.chunks ? P.S - i * P.chunk : P.chunk)); };   // positions of a chunk
-    const float inv = 1.0f / (float)P.S;
     for (int g0 = 0; g0 < P.G; g0 += blockDim.x) {
         const int n = P.G - g0 < (int)blockDim.x ? P.G - g0 : (int)blockDim.x;
-        float *held = norm_lds + blockDim.x;
-        const float sum = over_chunks(P, n, norm_lds, [&](int i, int g) {
-            return fetch(stat + ((long long)i * P.G + g0 + g) * 2) * (size(i) * inv);
-        });
-        if ((int)threadIdx.x < n) held[threadIdx.x] = sum;
-        __syncthreads();
-        const float sq = over_chunks(P, n, norm_lds, [&](int i, int g) {
-            const float *at = stat + ((long long)i * P.G + g0 + g) * 2;
-            const float d = fetch(at) - held[g];
-            return __builtin_fmaf(d * d, size(i) * (float)m.per, fetch(at + 1));
-        });
+        const Moments v = over_chunks(
+            P, stat, g0, n, (Moments *)norm_lds,
+            [&](Moments &to, f32x2 pair, int i) {
+                const int positions = i + 1 == P.chunks ? P.S - i * P.chunk : P.chunk;
+                join_moments(to, {(float)positions * (float)m.per, pair.x, pair.y});
+            },
+            [](Moments &to, const Moments &from) { join_moments(to, from); });
         if ((int)threadIdx.x < n) {
             const long long at = (long long)b * P.G + g0 + threadIdx.x;
-            P.mean[at] = held[threadIdx.x];
-            P.rstd[at] = 1.0f / sqrtf(sq / ((float)P.S * (float)m.per) + P.eps);
+            P.mean[at] = v.mean;
+            P.rstd[at] = 1.0f / sqrtf(v.far / ((float)P.S * (float)m.per) + P.eps);
         }
         __syncthreads();
     }
@@ -619,6 +664,7 @@ __global__ __launch_bounds__(1024) void k_apply_forward(Norm P)
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     if (!p.n) return;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
+    const int beyond = rows_before_the_end<V>(P, b, p.c);
     T *y = (T *)P.y + (long long)b * P.S * P.ldy + p.c;
     float a[V], beta[V], mean[V];
     parameters<T, V>(a, P.gamma, p.c, p.n, 1.0f);
@@ -635,7 +681,7 @@ __global__ __launch_bounds__(1024) void k_apply_forward(Norm P)
         for (int k = 0; k < kStep; ++k) {
             const int row = r0 + k * m.lanes;
             w[k] = u32x4{0, 0, 0, 0};
-            if (row < s1) w[k] = get<T, V>(x + (long long)row * P.ldx, p.n);
+            if (row < s1) w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond);
         }
 #pragma unroll
         for (int k = 0; k < kStep; ++k) {
@@ -664,6 +710,7 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
     const int b = blockIdx.x / P.chunks, chunk = blockIdx.x - b * P.chunks;
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
+    const int beyond = rows_before_the_end<V>(P, b, p.c);
     const T *dy = (const T *)P.dy + (long long)b * P.S * P.lddy + p.c;
     float *groups = norm_lds + reduce_floats(blockDim.x, V);
     float gamma[V], beta[V], mean[V], rstd[V], scale[V], s[2][V] = {};
@@ -683,8 +730,8 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
             const int row = r0 + k * m.lanes;
             w[k] = d[k] = u32x4{0, 0, 0, 0};
             if (row < s1) {
-                w[k] = get<T, V>(x + (long long)row * P.ldx, p.n);
-                d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n);
+                w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond);
+                d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n, row < beyond);
             }
         }
 #pragma unroll
@@ -706,17 +753,21 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
     group_sums<V, 2>(m, p, s, norm_lds, groups);
     float *mine = P.stat + ((long long)b * P.chunks + chunk) * P.G * 2;
     for (int g = threadIdx.x; g < P.G; g += blockDim.x) {
-        leave(mine + g * 2, groups[g]);
-        leave(mine + g * 2 + 1, groups[m.groups + g]);
+        leave(mine + g * 2, groups[g], groups[m.groups + g]);
     }
     if (!last_of(P, b)) return;
     const float *stat = P.stat + (long long)b * P.chunks * P.G * 2;
     const float inv = 1.0f / ((float)P.S * (float)m.per);
-    const int all = P.G * 2;   // both sums of a group
-    for (int g0 = 0; g0 < all; g0 += blockDim.x) {
-        const int n = all - g0 < (int)blockDim.x ? all - g0 : (int)blockDim.x;
-        const float sum = over_chunks(P, n, norm_lds, [&](int i, int g) { return fetch(stat + (long long)i * all + g0 + g); });
-        if ((int)threadIdx.x < n) P.group[(long long)b * all + g0 + threadIdx.x] = sum * inv;
+    for (int g0 = 0; g0 < P.G; g0 += blockDim.x) {
+        const int n = P.G - g0 < (int)blockDim.x ? P.G - g0 : (int)blockDim.x;
+        const f32x2 v = over_chunks(
+            P, stat, g0, n, (f32x2 *)norm_lds, [](f32x2 &to, f32x2 pair, int) { to += pair; },
+            [](f32x2 &to, const f32x2 &from) { to += from; });
+        if ((int)threadIdx.x < n) {
+            float *to = P.group + ((long long)b * P.G + g0 + threadIdx.x) * 2;
+            to[0] = v.x * inv, to[1] = v.y * inv;
+        }
+        __syncthreads();
     }
 }
 
@@ -765,6 +816,7 @@ __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
     const int s0 = chunk * P.chunk, s1 = P.S - s0 < P.chunk ? P.S : s0 + P.chunk;
     if (!p.n) return;
     const T *x = (const T *)P.x + (long long)b * P.S * P.ldx + p.c;
+    const int beyond = rows_before_the_end<V>(P, b, p.c);
     const T *dy = (const T *)P.dy + (long long)b * P.S * P.lddy + p.c;
     T *dx = (T *)P.dx + (long long)b * P.S * P.lddx + p.c;
     float gamma[V], beta[V], mean[V], scale[V], one[V], two[V];
@@ -785,8 +837,8 @@ __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
             const int row = r0 + k * m.lanes;
             w[k] = d[k] = u32x4{0, 0, 0, 0};
             if (row < s1) {
-                w[k] = get<T, V>(x + (long long)row * P.ldx, p.n);
-                d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n);
+                w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond);
+                d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n, row < beyond);
             }
         }
 #pragma unroll
@@ -814,6 +866,7 @@ __global__ void k_zero(T *a, T *b, int n)
 
 constexpr int kUnits = 256;          // compute units
 constexpr int kSplitGroups = 1024;   // workgroups that a split call aims at
+constexpr int kSampleChunks = 256;   // chunks of a sample, at most
 constexpr int kResidentMost = 1024;  // workgroups of a span in a resident backward pass
 constexpr int kMinSegment = 64;      // bytes of a row that a span has at least, unless the array is small
 constexpr long long kSmallArray = 1 << 20;
@@ -833,8 +886,13 @@ int split_lanes(int C)
     return split_threads<T>(C) / ceil_div(C, kVec<T>);
 }
 
-// The most positions of a thread: what its registers hold (backward: x, and dz in 32 bits), by the size of the workgroup.
-constexpr int kMostForward = 16, kMostBackward = 8, kMostOf1024 = 4;
+// The most positions of a thread, by the size of the workgroup: what its registers hold (backward: x, and dz in 32 bits) with
+// room for another workgroup's on the compute unit.
+template <typename T>
+constexpr int kMostForward = sizeof(T) == 2 ? 4 : 16;
+template <typename T>
+constexpr int kMostBackward = sizeof(T) == 2 ? 4 : 8;
+constexpr int kMostOf1024 = 4;
 // Threads of the workgroups that small samples share: in the backward pass each leaves sums of all parameters.
 constexpr int kTogetherForward = 256, kTogetherBackward = 1024;
 
@@ -887,6 +945,12 @@ Resident resident(int B, int S, int C, int G, int most, int together)
         if (room >= S) break;
         if (m.width <= least || spans >= G) return r;   // does not fit
     }
+    // Spans beside each other in a second round, or few workgroups with much each, cost more than reading x twice in whole rows
+    // (256 x 196 positions of 512 channels bf16, 768 workgroups: 67 us against 38; 5 x 589 of 172 fp32, 20 of 101 KB: 18.3 against
+    // 13.6; 16 x 1024 of 512 fp32, 256 workgroups: 22 against 37).  Samples of few positions are never split.
+    const long long wgs = (long long)B * r.spans, slab = (long long)S * m.width * (long long)sizeof(T);
+    const bool better = (r.spans == 1 || wgs <= kUnits) && (wgs >= kUnits / 4 || slab <= 65536);
+    if (!better && S > split_lanes<T>(C) * kMostOf1024) return r;
     r.fits = true;
     m.per = per;
     r.rows = ceil_div(S, all);
@@ -899,7 +963,7 @@ Resident resident(int B, int S, int C, int G, int most, int together)
     return r;
 }
 
-Norm common(const NormCall &a)
+Norm common(const NormCall &a, int V)
 {
     Norm P{};
     P.B = a.B, P.S = a.S, P.C = a.C, P.G = a.G;
@@ -908,6 +972,7 @@ Norm common(const NormCall &a)
     P.y = a.y, P.dx = a.dx;
     P.mean = a.mean, P.rstd = a.rstd;
     P.act = a.act, P.eps = a.eps;
+    P.ahead = ceil_div(V, a.C);
     return P;
 }
 
@@ -924,7 +989,9 @@ int cut(Norm &P, const NormWorkspace &ws)
     m.groups = P.G;
     complete<T>(m, split_threads<T>(P.C));
     const long long rows = (long long)P.B * P.S;
-    P.chunk = (int)std::min<long long>(P.S, std::max<long long>(m.lanes * kStep, (rows + kSplitGroups - 1) / kSplitGroups));
+    // kSplitGroups chunks in all, but no more of a sample than its last workgroup joins quickly
+    P.chunk = (int)std::min<long long>(P.S, std::max<long long>({m.lanes * kStep, (rows + kSplitGroups - 1) / kSplitGroups,
+                                                                 ceil_div(P.S, kSampleChunks)}));
     P.chunks = ceil_div(P.S, P.chunk);
     P.stat = ws.part;
     P.group = ws.group;
@@ -953,8 +1020,8 @@ size_t lds_bytes(int threads, int V, int sets) { return (size_t)(reduce_floats(t
 template <typename T>
 hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 {
-    Norm P = common(a);
-    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward, kTogetherForward);
+    Norm P = common(a, kVec<T>);
+    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward<T>, kTogetherForward);
     if (r.fits) {
         P.map = r.map;
         const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), 1 << 20), (unsigned)r.spans);
@@ -962,7 +1029,7 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
         if (r.rows <= 1) k_resident_forward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.threads > 512) k_resident_forward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.rows <= 4) k_resident_forward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
-        else k_resident_forward<T, kMostForward, 512><<<grid, r.threads, lds, s>>>(P);
+        else k_resident_forward<T, kMostForward<T>, 512><<<grid, r.threads, lds, s>>>(P);
         return hipGetLastError();
     }
     const int threads = cut<T>(P, ws);
@@ -979,11 +1046,11 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 template <typename T>
 hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 {
-    Norm P = common(a);
+    Norm P = common(a, kVec<T>);
     P.dgamma = a.dgamma, P.dbeta = a.dbeta;
     const bool parameters = a.dgamma || a.dbeta;
     const int blocks = 2 * ceil_div(a.C, 8);   // of reduce_parameters
-    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward, kTogetherBackward);
+    const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward<T>, kTogetherBackward);
     if (r.fits) {
         P.map = r.map;
         const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), kResidentMost), (unsigned)r.spans);
@@ -996,7 +1063,7 @@ hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
         if (r.rows <= 1) k_resident_backward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.threads > 512) k_resident_backward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.rows <= 4) k_resident_backward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
-        else k_resident_backward<T, kMostBackward, 512><<<grid, r.threads, lds, s>>>(P);
+        else k_resident_backward<T, kMostBackward<T>, 512><<<grid, r.threads, lds, s>>>(P);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || !P.rows) return e;
         k_parameters<T><<<blocks, 512, 0, s>>>(P);
@@ -1023,9 +1090,9 @@ template <typename T>
 hipError_t configure()
 {
     const void *kernels[] = {(const void *)k_resident_forward<T, 1, 1024>,          (const void *)k_resident_forward<T, 4, 512>,
-                             (const void *)k_resident_forward<T, kMostForward, 512>, (const void *)k_resident_forward<T, kMostOf1024, 1024>,
+                             (const void *)k_resident_forward<T, kMostForward<T>, 512>, (const void *)k_resident_forward<T, kMostOf1024, 1024>,
                              (const void *)k_resident_backward<T, 1, 1024>,         (const void *)k_resident_backward<T, 4, 512>,
-                             (const void *)k_resident_backward<T, kMostBackward, 512>,
+                             (const void *)k_resident_backward<T, kMostBackward<T>, 512>,
                              (const void *)k_resident_backward<T, kMostOf1024, 1024>, (const void *)k_stats<T>, (const void *)k_sums<T>};
     for (const void *k : kernels) {
         const hipError_t e = hipFuncSetAttribute(k, hipFuncAttributeMaxDynamicSharedMemorySize, kMostLds);
