@@ -867,7 +867,7 @@ __global__ void k_zero(T *a, T *b, int n)
 constexpr int kUnits = 256;          // compute units
 constexpr int kSplitGroups = 1024;   // workgroups that a split call aims at
 constexpr int kSampleChunks = 256;   // chunks of a sample, at most
-constexpr int kResidentMost = 1024;  // workgroups of a span in a resident backward pass
+constexpr int kResidentMost = 768;   // workgroups of a span in a resident pass, of up to 256 threads; others: a third
 constexpr int kMinSegment = 64;      // bytes of a row that a span has at least, unless the array is small
 constexpr long long kSmallArray = 1 << 20;
 
@@ -939,9 +939,11 @@ Resident resident(int B, int S, int C, int G, int most, int together)
         m.width = each * per;
         m.groups = each;
         m.vecs = ceil_div(m.width, V);
-        const int threads = m.vecs <= 512 ? 512 : 1024;
+        int threads = m.vecs <= 512 ? 512 : 1024;
+        // smaller workgroups where there are many: a compute unit holds more of them, one waiting while another computes
+        if (m.vecs <= 256 && (long long)B * r.spans >= kUnits && (long long)(256 / m.vecs) * most >= S) threads = 256;
         all = threads / m.vecs;
-        const long long room = (long long)all * (threads == 512 ? most : kMostOf1024);
+        const long long room = (long long)all * (threads <= 512 ? most : kMostOf1024);
         if (room >= S) break;
         if (m.width <= least || spans >= G) return r;   // does not fit
     }
@@ -961,6 +963,13 @@ Resident resident(int B, int S, int C, int G, int most, int together)
     r.threads = ceil_div(m.vecs * m.lanes * m.subs, 64) * 64;
     complete<T>(m, r.threads);
     return r;
+}
+
+// Workgroups of a span: what the compute units hold together; each goes on to other samples, with its parameters (and, backward,
+// their sums) in registers.
+int resident_groups(const Resident &r, int B)
+{
+    return std::min(ceil_div(B, r.map.subs), r.threads <= 256 ? kResidentMost : kResidentMost / 3);
 }
 
 Norm common(const NormCall &a, int V)
@@ -1024,7 +1033,7 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
     const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward<T>, kTogetherForward);
     if (r.fits) {
         P.map = r.map;
-        const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), 1 << 20), (unsigned)r.spans);
+        const dim3 grid((unsigned)resident_groups(r, a.B), (unsigned)r.spans);
         const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
         if (r.rows <= 1) k_resident_forward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.threads > 512) k_resident_forward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
@@ -1053,7 +1062,7 @@ hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
     const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward<T>, kTogetherBackward);
     if (r.fits) {
         P.map = r.map;
-        const dim3 grid((unsigned)std::min(ceil_div(a.B, r.map.subs), kResidentMost), (unsigned)r.spans);
+        const dim3 grid((unsigned)resident_groups(r, a.B), (unsigned)r.spans);
         if (parameters && grid.x > 1) {
             P.rows = (int)grid.x;
             P.part = ws.part;
