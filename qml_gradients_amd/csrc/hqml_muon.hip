@@ -942,9 +942,8 @@ hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *t
 }
 
 template <int STAGE, int PLANES>
-hipError_t run_stage(Products &G, const Finish &F, float *part, unsigned *ticket, hipStream_t s)
+hipError_t run_stage(Products &G, const Finish &F, const Plan &plan, float *part, unsigned *ticket, hipStream_t s)
 {
-    const Plan plan = plan_of(G, PLANES);
     if (!plan.main.side) return hipErrorInvalidValue;
     int tiles[kMatrices], skip[kMatrices], left = plan.first;
     for (int i = 0; i < G.count; ++i) {
@@ -1021,36 +1020,43 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     each([](const Matrix &m) { return (unsigned)std::min<long long>(((long long)m.rows * pad8(m.cols) / 8 + 255) / 256, 4096); });
     k_begin<G, PLANES><<<groups, 256, 0, s>>>(b, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
+    Products gram{}, poly{}, apply{};
+    gram.count = poly.count = apply.count = b.count;
+    for (int i = 0; i < b.count; ++i) {
+        const Matrix &m = b.t[i];
+        const bool tall = m.rows > m.cols;
+        const int small = std::min(m.rows, m.cols), ldx = pad8(m.cols), lda = pad8(small);
+        const long long plane_x = (long long)m.rows * ldx, plane_a = (long long)small * lda;
+        Product &A = gram.t[i];
+        A.c = m.a;
+        A.lda = A.ldb = ldx, A.ldc = lda;
+        A.plane_a = A.plane_b = plane_x, A.plane_c = plane_a;
+        A.I = A.J = small, A.K = tall ? m.rows : m.cols, A.cols = tall, A.mirrored = true;
+        Product &B = poly.t[i];
+        B.a = B.b = B.with = m.a, B.c = m.b;
+        B.lda = B.ldb = B.ldc = lda;
+        B.plane_a = B.plane_b = B.plane_c = plane_a;
+        B.I = B.J = B.K = small, B.mirrored = true;
+        Product &X = apply.t[i];
+        X.lda = tall ? ldx : lda, X.ldb = tall ? lda : ldx, X.ldc = ldx;
+        X.plane_a = tall ? plane_x : plane_a, X.plane_b = tall ? plane_a : plane_x, X.plane_c = plane_x;
+        X.I = m.rows, X.J = m.cols, X.K = small, X.cols = !tall;
+        X.p = m.p, X.size = m.size;
+    }
+    const Plan plan_gram = plan_of(gram, PLANES), plan_poly = plan_of(poly, PLANES), plan_apply = plan_of(apply, PLANES);
     for (int step = 0; step < cfg.steps; ++step) {
         const bool last = step + 1 == cfg.steps;
-        Products gram{}, poly{}, apply{};
-        gram.count = poly.count = apply.count = b.count;
-        for (int i = 0; i < b.count; ++i) {
+        for (int i = 0; i < b.count; ++i) {   // X goes from one array to the other
             const Matrix &m = b.t[i];
             const bool tall = m.rows > m.cols;
-            const int small = std::min(m.rows, m.cols), ldx = pad8(m.cols), lda = pad8(small);
-            const long long plane_x = (long long)m.rows * ldx, plane_a = (long long)small * lda;
             const Half *x = m.x[step & 1];
-            Product &A = gram.t[i];
-            A.a = A.b = x, A.c = m.a;
-            A.lda = A.ldb = ldx, A.ldc = lda;
-            A.plane_a = A.plane_b = plane_x, A.plane_c = plane_a;
-            A.I = A.J = small, A.K = tall ? m.rows : m.cols, A.cols = tall, A.mirrored = true;
-            Product &B = poly.t[i];
-            B.a = B.b = B.with = m.a, B.c = m.b;
-            B.lda = B.ldb = B.ldc = lda;
-            B.plane_a = B.plane_b = B.plane_c = plane_a;
-            B.I = B.J = B.K = small, B.mirrored = true;
-            Product &X = apply.t[i];
+            Product &A = gram.t[i], &X = apply.t[i];
+            A.a = A.b = x;
             X.a = tall ? x : m.b, X.b = tall ? m.b : x, X.with = x, X.c = m.x[1 - (step & 1)];
-            X.lda = tall ? ldx : lda, X.ldb = tall ? lda : ldx, X.ldc = ldx;
-            X.plane_a = tall ? plane_x : plane_a, X.plane_b = tall ? plane_a : plane_x, X.plane_c = plane_x;
-            X.I = m.rows, X.J = m.cols, X.K = small, X.cols = !tall;
-            X.p = m.p, X.size = m.size;
         }
-        if ((e = run_stage<GRAM, PLANES>(gram, {kUnscale, 0.0f, 0.0f, 0}, part, ticket, s)) != hipSuccess) return e;
-        if ((e = run_stage<POLY, PLANES>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, part, ticket, s)) != hipSuccess) return e;
-        if ((e = run_stage<APPLY, PLANES>(apply, {kUnscale, k.a, k.decay, last}, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<GRAM, PLANES>(gram, {kUnscale, 0.0f, 0.0f, 0}, plan_gram, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<POLY, PLANES>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, plan_poly, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<APPLY, PLANES>(apply, {kUnscale, k.a, k.decay, last}, plan_apply, part, ticket, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
