@@ -250,11 +250,13 @@ struct Product {
     float size;
 };
 
-struct Products {
+template <int MOST>
+struct ProductsOf {
     int count;
-    unsigned first[kMatrices];   // multiples of eight: the XCD of a tile follows from its number
-    Product t[kMatrices];
+    unsigned first[MOST];   // multiples of eight: the XCD of a tile follows from its number
+    Product t[MOST];
 };
+using Products = ProductsOf<kMatrices>;
 
 struct Finish {
     float one, two;   // C = one sum + two with
@@ -522,8 +524,8 @@ __device__ __forceinline__ void product(const Product &P, const Finish &F, int t
     }
 }
 
-template <int STAGE, int PLANES, int SIDE, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 4 ? 1 : 2) void k_product(Products G, Finish F)
+template <int STAGE, int PLANES, int SIDE, int WAVES, int MOST>
+__global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 4 ? 1 : 2) void k_product(ProductsOf<MOST> G, Finish F)
 {
     constexpr int kBytes = SIDE * 64 * PLANES;
     static_assert(PLANES == 1 || SIDE <= 128, "room for two planes");
@@ -565,7 +567,7 @@ __global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 
 
 constexpr int kSmallSide = 64, kSmallWaves = 16, kTinyWaves = 4;
 constexpr int kSmallLds = 160 * 1024 - 1024;
-constexpr long long kSmallWork = 1 << 20;   // multiply-adds of X X^T
+constexpr long long kSmallWork = 3 << 19;   // multiply-adds of X X^T: 64 x 350 84 us (by tiles 89), 64 x 420 99 (92)
 
 __host__ __device__ inline int pad16(int n) { return (n + 15) & ~15; }
 
@@ -910,6 +912,18 @@ Plan plan_of(const Products &G, int planes)
     return best;
 }
 
+// The arguments of few products are few: a launch of 24 takes the host 4.0 us, one of four 2.7.
+constexpr int kFew = 4;
+
+template <int STAGE, int PLANES, int MOST>
+void launch(const ProductsOf<MOST> &G, const Finish &F, int side, unsigned groups, hipStream_t s)
+{
+    if (side == 64) k_product<STAGE, PLANES, 64, 4, MOST><<<groups, 256, 0, s>>>(G, F);
+    else if (PLANES == 1 && side == 128) k_product<STAGE, 1, 128, 4, MOST><<<groups, 256, 0, s>>>(G, F);
+    else if (PLANES == 2) k_product<STAGE, 2, 128, 8, MOST><<<groups, 512, 0, s>>>(G, F);
+    else k_product<STAGE, 1, 256, 8, MOST><<<groups, 512, 0, s>>>(G, F);
+}
+
 template <int STAGE, int PLANES>
 hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *tiles, const int *skip, float *part, unsigned *ticket,
                    hipStream_t s)
@@ -934,10 +948,15 @@ hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *t
         G.first[i] = at;
         at += ((unsigned)P.tiles * (unsigned)P.parts + 7) & ~7u;
     }
-    if (cut.side == 64) k_product<STAGE, PLANES, 64, 4><<<at, 256, 0, s>>>(G, F);
-    else if (PLANES == 1 && cut.side == 128) k_product<STAGE, 1, 128, 4><<<at, 256, 0, s>>>(G, F);
-    else if (PLANES == 2) k_product<STAGE, 2, 128, 8><<<at, 512, 0, s>>>(G, F);
-    else k_product<STAGE, 1, 256, 8><<<at, 512, 0, s>>>(G, F);
+    if (G.count > kFew) {
+        launch<STAGE, PLANES>(G, F, cut.side, at, s);
+    } else {
+        ProductsOf<kFew> few;
+        few.count = G.count;
+        std::copy_n(G.first, kFew, few.first);
+        std::copy_n(G.t, kFew, few.t);
+        launch<STAGE, PLANES>(few, F, cut.side, at, s);
+    }
     return hipGetLastError();
 }
 
