@@ -77,16 +77,19 @@ struct Sixteen {
             __builtin_memcpy(w, t, sizeof t);
         }
     }
-    // The same through a buffer that ends with the row, or, for an odd number of bf16, with its last value's word, whose other
-    // half is cleared.
-    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t row, int c, int K)
+    // The same through a buffer that ends with the row's last whole word.  The last of an odd number of bf16 comes by itself: its
+    // word's other half may lie past the array.
+    __device__ __forceinline__ void load(__amdgpu_buffer_rsrc_t buffer, const T *row, int c, int K)
     {
 #pragma unroll
-        for (int k = 0; k < kV; ++k) w[k] = __builtin_amdgcn_raw_buffer_load_b128(row, c * (int)sizeof(T) + k * 16, 0, 0);
-        if (sizeof(T) == 2 && (K & 1))
+        for (int k = 0; k < kV; ++k) w[k] = __builtin_amdgcn_raw_buffer_load_b128(buffer, c * (int)sizeof(T) + k * 16, 0, 0);
+        if (sizeof(T) == 2 && (K & 1) && c < K && c + 16 > K) {
+            uint16_t last;
+            __builtin_memcpy(&last, row + K - 1, 2);
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                if (c + 2 * k + 1 == K) w[k / 4][k % 4] &= 0xFFFFu;
+                if (c + 2 * k + 1 == K) w[k / 4][k % 4] = last;
+        }
     }
     __device__ __forceinline__ void values(float (&x)[16]) const
     {
@@ -175,12 +178,13 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
     for (long long r0 = (long long)blockIdx.x * (4 / kWaves); r0 < rows; r0 += step) {
         const long long r = r0 + (kWaves == 4 ? 0 : __builtin_amdgcn_readfirstlane(wave));
         const bool some = r < rows;   // the same in all threads of a row
-        const auto row = __builtin_amdgcn_make_buffer_rsrc((void *)(x + (some ? r : 0) * ldx), 0, (K * (int)sizeof(T) + 3) & ~3, 0x00027000);
+        const T *row = x + (some ? r : 0) * ldx;
+        const auto buffer = __builtin_amdgcn_make_buffer_rsrc((void *)row, 0, K * (int)sizeof(T) & ~3, 0x00027000);
         Sixteen<T> v[kHeld];
         uint32_t b = 0;
         if (some) {
 #pragma unroll
-            for (int h = 0; h < kHeld; ++h) v[h].load(row, (h * kThreads + lane) * 16, K);   // zeros past its end
+            for (int h = 0; h < kHeld; ++h) v[h].load(buffer, row, (h * kThreads + lane) * 16, K);   // zeros past its end
 #pragma unroll
             for (int h = 0; h < kHeld; ++h) {
                 b = max(b, largest16(v[h]));
@@ -188,7 +192,7 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
             }
             for (int c = (kHeld * kThreads + lane) * 16; c < Kp; c += kThreads * 16) {
                 Sixteen<T> t;
-                t.load(row, c, K);
+                t.load(buffer, row, c, K);
                 b = max(b, largest16(t));
             }
         }
@@ -213,7 +217,7 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
         }
         for (int c = (kHeld * kThreads + lane) * 16; c < Kp; c += kThreads * 16) {
             Sixteen<T> t;
-            t.load(row, c, K);
+            t.load(buffer, row, c, K);
             *(u32x4 *)(to + c) = codes16(t, s);
         }
         if (lane == 0) scales[r] = scale;

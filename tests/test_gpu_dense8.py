@@ -36,7 +36,7 @@ def check_codes(x):
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 @pytest.mark.parametrize("rows,K,offset,gap", [(1, 1, 0, 0), (3, 15, 1, 2), (5, 16, 0, 0), (257, 17, 3, 1), (7, 784, 0, 0),
                                                (9, 2047, 1, 5), (4, 2048, 0, 0), (3, 2049, 0, 7), (2, 8191, 1, 0),
-                                               (2, 8193, 0, 0), (1, 70001, 1, 0)])
+                                               (2, 8193, 0, 0), (1, 70001, 1, 0), (1, 2047, 1, 0)])
 def test_codes(rows, K, offset, gap, dtype):
     say(f"[gpu] codes {rows} x {K} {dtype}")
     check_codes(matrix(rows, K, dtype, rows + K, 2.0, offset, gap))
@@ -265,3 +265,63 @@ def test_another_stream_and_a_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(twice, x * 2)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_largest_tiles(dtype):
+    import qml_gradients_amd as hq
+    M, K, N = 4100, 1040, 4090
+    say(f"[gpu] dense8 {M} x {K} -> {N} {dtype}")
+    x = matrix(M, K, dtype, 1)
+    codes, scales = hq.quantise_rows(matrix(N, K, dtype, 2, 0.3) / math.sqrt(K))
+    residual = matrix(M, N, dtype, 3)
+    y = hq.DenseInt8(K, N, M, dtype=dtype, activation="gelu").forward(x, codes, scales, None, residual)
+    assert excess(y, dense8(x, codes, scales, None, residual, "gelu", 1.0, dtype)) <= 0
+
+
+@pytest.mark.parametrize("rows", [3, 2200])
+def test_offsets_past_32_bits(rows):
+    """Rows of 2^20 values: of 2,200 of them the last are past 2^31 values, of x, codes, residual and y."""
+    import qml_gradients_amd as hq
+    K, N, ld = 40, 24, 1 << 20
+    say(f"[gpu] dense8 {rows} rows {ld} apart")
+
+    def wide(cols, dt, value):
+        t = torch.zeros(rows * ld, dtype=dt, device="cuda").view(rows, ld)[:, ld - cols:]
+        return t.copy_(value) if value is not None else t
+
+    x, r = matrix(rows, K, "bf16", 1), matrix(rows, N, "bf16", 2)
+    w = hq.quantise_rows(matrix(N, K, "bf16", 3))
+    layer = hq.DenseInt8(K, N, rows, dtype="bf16", activation="silu")
+    want = layer.forward(x, *w, None, r)
+    assert excess(want, dense8(x, *w, None, r, "silu", 1.0, "bf16")) <= 0
+    wide_x, wide_r = wide(K, torch.bfloat16, x), wide(N, torch.bfloat16, r)
+    y = layer.forward(wide_x, *w, None, wide_r, out=wide_r)
+    assert torch.equal(y, want)
+    c, s = hq.quantise_rows(wide_x)
+    c0, s0 = hq.quantise_rows(x)
+    assert torch.equal(c, c0) and torch.equal(s, s0)
+    # as many output channels, their codes as far apart
+    codes = wide(K + 8, torch.int8, None)[:, :K]
+    codes.copy_(c0)
+    layer = hq.DenseInt8(K, rows, 3, dtype="bf16")
+    x3 = matrix(3, K, "bf16", 4)
+    assert torch.equal(layer.forward(x3, codes, s0), layer.forward(x3, c0, s0))
+
+
+def test_two_handles_at_once():
+    import qml_gradients_amd as hq
+    K, N, M = 2048, 64, 17
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    layers = [hq.DenseInt8(K, N, M, stream=s.cuda_stream) for s in streams]
+    w = [hq.quantise_rows(matrix(N, K, "fp32", n)) for n in (1, 2)]
+    x = [matrix(M, K, "fp32", n) for n in (3, 4)]
+    want = [dense8(x[n], *w[n], None, None, "none", 1.0, "fp32") for n in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for n, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got.append(layers[n].forward(x[n], *w[n]))
+    torch.cuda.synchronize()
+    assert all(excess(y, want[i % 2]) <= 0 for i, y in enumerate(got))
