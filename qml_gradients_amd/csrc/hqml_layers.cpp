@@ -3,9 +3,11 @@
 #include <hip/hip_runtime.h>
 #include <math.h>
 
+#include <algorithm>
 #include <cstdio>
 #include <new>
 #include <string>
+#include <vector>
 
 #include "../../include/hqml.h"
 #include "hqml_entry.hpp"
@@ -362,6 +364,35 @@ int check_muon(const hqml_muon_config *c, int n, const hqml_muon_tensor *t, std:
     return refused(why, err);
 }
 
+// Workgroups update matrices while others still read theirs.
+int check_apart(const hqml_muon_config &c, int n, const hqml_muon_tensor *t, const void *workspace, size_t bytes, std::string *err)
+{
+    struct Span {
+        size_t from, to;
+        bool output;
+    };
+    std::vector<Span> all;
+    all.reserve(3 * (size_t)n + 1);
+    auto add = [&](const void *p, size_t size, bool output) {
+        if (p && size) all.push_back({(size_t)p, (size_t)p + size, output});
+    };
+    add(workspace, bytes, true);
+    for (int i = 0; i < n; ++i) {
+        const size_t k = (size_t)t[i].rows * t[i].cols;
+        add(t[i].param, k * dtype_bytes(c.param_dtype), true);
+        add(t[i].grad, k * dtype_bytes(c.grad_dtype), false);
+        add(t[i].momentum, k * 4, true);
+    }
+    std::sort(all.begin(), all.end(), [](const Span &a, const Span &b) { return a.from < b.from; });
+    size_t end = 0, outputs_end = 0;   // of those so far
+    for (const Span &s : all) {
+        if (s.from < outputs_end || (s.output && s.from < end)) return refused("matrices and workspace must not overlap", err);
+        end = std::max(end, s.to);
+        if (s.output) outputs_end = std::max(outputs_end, s.to);
+    }
+    return HQML_OK;
+}
+
 int muon_step(const hqml_muon_config *c, int n, const hqml_muon_tensor *t, void *workspace, size_t bytes)
 {
     std::string err;
@@ -371,6 +402,8 @@ int muon_step(const hqml_muon_config *c, int n, const hqml_muon_tensor *t, void 
     for (int i = 0; i < n; ++i) some = some || (t[i].rows && t[i].cols);
     if (!some) return HQML_OK;
     const size_t need = muon_workspace(*c, n, t);
+    rc = check_apart(*c, n, t, workspace, need, &err);
+    if (rc != HQML_OK) return thread_error(rc, err);
     const OnDevice on(c->device);
     if (on.error() != hipSuccess) return thread_error(HQML_ERR_HIP, hip_text("device", on.error()));
     if (need) {

@@ -70,6 +70,28 @@ def test_muon_configurations_refused(bad):
     assert e.value.status == hq.HQML_ERR_ARG
 
 
+def test_muon_overlaps_refused():
+    """By addresses alone: nothing is read, and arrays beside each other pass on to the next check."""
+    import qml_gradients_amd as hq
+    base, size = 1 << 30, 100 * 100 * 4
+    P, G, M = base, base + size, base + 2 * size   # beside each other
+    at = lambda n: base + n * size
+
+    def step(*matrices, workspace=1 << 40):
+        t = (hq.hqml_muon_tensor * len(matrices))(*[hq.hqml_muon_tensor(*m, 100, 100, 1.0) for m in matrices])
+        with pytest.raises(hq.HqmlError) as e:
+            hq.hqml_muon_step(_muon(), len(matrices), t, workspace, hq.hqml_muon_workspace_bytes(_muon(), len(matrices), t))
+        return str(e.value)
+
+    for bad in ([(P, P, M)], [(P, G, G)], [(P, G, P)], [(P, G, M), (at(3), at(4), M)], [(P, G, M), (P, at(4), at(5))],
+                [(P, G, M), (at(3), P, at(4))], [(P, G, M - 4)], [(P, G, M), (at(3), at(4), at(5)), (at(5) + size - 4, at(7), at(8))]):
+        assert "overlap" in step(*bad)
+    for workspace in (P, G, M, M + size - 256):
+        assert "overlap" in step((P, G, M), workspace=workspace)
+    for good in ([(P, G, M)], [(P, G, M), (at(3), at(4), at(5))], [(P, G, M), (at(3), G, at(4))]):
+        assert "overlap" not in step(*good)   # there is no such memory: refused for that
+
+
 def test_muon_workspace():
     """Two X and two of the smaller side's square for each matrix, rounds of up to 1 GiB, and 64 MiB and 16 KiB of partial sums
     and counters; nothing for small matrices."""
