@@ -81,6 +81,20 @@ def test_steps_and_coefficients(steps, coefficients):
     check([(48, 90), (150, 60)], "fp32", steps=steps, coefficients=coefficients)
 
 
+@pytest.mark.parametrize("sizes,dtype", [
+    ([(3000, 3000)] * 2, "bf16"),                       # more of the largest tiles than compute units
+    ([(2100, 2300)], "fp32"), ([(2400, 2100)], "fp32"),
+    ([(200, 6000), (6000, 200)], "bf16"), ([(200, 6000), (6000, 200)], "fp32"),   # few tiles, split along k
+    ([(64, 350), (350, 64), (64, 420), (48, 500)], "fp32"), ([(16, 2000), (2500, 16), (33, 600)], "bf16")])   # around the LDS's size
+def test_cuts(sizes, dtype):
+    check(sizes, dtype, seed=3)
+
+
+def test_large_and_small_matrices_in_one_call():
+    check([(70 + n, 90 + 2 * n) if n % 3 else (5 + n, 40) for n in range(45)], "bf16")
+    check([(70 + n, 90 + 2 * n) for n in range(5)], "fp32")
+
+
 def test_more_matrices_than_a_launch_takes():
     check([(3 + n, 70 - n) for n in range(40)], "fp32")
 
@@ -203,6 +217,27 @@ def test_streams_and_graphs():
             torch.cuda.synchronize()
             assert all(torch.equal(p, q) for p, q in zip(a, b))
             assert all(torch.equal(x.state[p]["momentum"], y.state[q]["momentum"]) for p, q in zip(a, b))
+
+
+def test_two_streams_at_once():
+    """Steps of their own parameters do not disturb each other."""
+    from qml_gradients_amd.optim import Muon
+    sizes = [(200, 6000), (300, 200), (20, 30)]
+    both = [matrices(sizes, seed=n) for n in (0, 40)]
+    alone = [matrices(sizes, seed=n) for n in (0, 40)]
+    streams = [torch.cuda.Stream() for _ in both]
+    opts = [Muon(p, lr=0.1) for p in both]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, o in zip(streams, opts):
+            with torch.cuda.stream(s):
+                o.step()
+    torch.cuda.synchronize()
+    for p in alone:
+        o = Muon(p, lr=0.1)
+        for _ in range(4):
+            o.step()
+    assert all(torch.equal(a, b) for x, y in zip(both, alone) for a, b in zip(x, y))
 
 
 def test_parameters_are_marked_changed():

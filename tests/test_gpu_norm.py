@@ -71,6 +71,39 @@ def test_widest_and_longest(B, S, C, G, dtype):
     check(B, S, C, G, dtype, "silu", offset=1, gap=1)
 
 
+@pytest.mark.parametrize("B,S", [(20, 110), (2, 1100)])
+def test_offsets_past_32_bits(B, S):
+    """Positions 2^20 values apart: the last of 2,200 are past 2^31 values."""
+    import qml_gradients_amd as hq
+    C, G, gap = 24, 4, (1 << 20) - 24
+    layer = check(B, S, C, G, "bf16", "silu", gap=gap)
+    x, _, gamma, beta = make(B, S, C, "bf16", 2, gap=gap)
+    want = layer.forward(x.contiguous(), gamma, beta)
+    assert torch.equal(layer.forward(x, gamma, beta, out=x), want) and torch.equal(x, want)
+
+
+def test_two_handles_at_once():
+    import qml_gradients_amd as hq
+    B, S, C, G = 2, 5000, 64, 8
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    layers = [hq.GroupNorm(C, G, B * S, activation="silu", stream=s.cuda_stream) for s in streams]
+    data = [make(B, S, C, "fp32", n) for n in (1, 2)]
+
+    def run(layer, x, dy, gamma, beta):
+        y, mean, rstd = layer.forward_train(x, gamma, beta)
+        return (y, *layer.backward(dy, x, gamma, beta, mean, rstd))
+
+    want = [run(hq.GroupNorm(C, G, B * S, activation="silu"), *d) for d in data]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for layer, d, s in zip(layers, data, streams):
+            with torch.cuda.stream(s):
+                got.append(run(layer, *d))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for i, r in enumerate(got) for a, b in zip(r, want[i % 2]))
+
+
 def test_fewer_rows_than_the_handle_allows():
     """Sizes change from call to call, from one kernel to another and back."""
     import qml_gradients_amd as hq
