@@ -71,7 +71,7 @@ struct Norm {
     int chunk, chunks;      // positions of a chunk, chunks of a sample
     float *stat;            // [B][chunks][G][2]
     float *group;           // [B][G][2]
-    unsigned *ticket;       // [B], 0 between calls
+    unsigned *ticket;       // [B], kTicketStep apart, 0 between calls
 };
 
 // A thread's channels and positions.
@@ -498,6 +498,10 @@ __global__ __launch_bounds__(MOST) void k_resident_backward(Norm P)
 
 // ---- chunks of positions ----
 
+// Tickets lie in cache lines of their own: atomics on one line come one after the other (8 x 4096 positions of 512 channels fp32,
+// statistics: eight tickets beside each other 27 us, apart 19.6; without any joining 13.7).
+constexpr int kTicketStep = 32;
+
 // Takes a ticket of sample b; whether this workgroup is the sample's last.  What it left before, as device-scope atomics, has
 // arrived.
 __device__ __forceinline__ bool last_of(const Norm &P, int b)
@@ -505,10 +509,10 @@ __device__ __forceinline__ bool last_of(const Norm &P, int b)
     __shared__ unsigned taken;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // this wave's stores have arrived
     __syncthreads();                                   // every wave's have
-    if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(P.ticket + b, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) taken = __hip_atomic_fetch_add(P.ticket + b * kTicketStep, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     __syncthreads();
     if (taken != (unsigned)P.chunks - 1) return false;
-    if (threadIdx.x == 0) __hip_atomic_store(P.ticket + b, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) __hip_atomic_store(P.ticket + b * kTicketStep, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return true;
 }
 
@@ -865,9 +869,13 @@ __global__ void k_zero(T *a, T *b, int n)
 // ---- which runs, and how it is cut ----
 
 constexpr int kUnits = 256;          // compute units
-constexpr int kSplitGroups = 1024;   // workgroups that a split call aims at
+// Workgroups that a split call aims at (32 x 4096 x 512 bf16, both passes, 512 / 1024 / 2048: 209 / 214 / 224 us; 8 x 4096 x 512 fp32
+// 106 / 110 / 122).
+constexpr int kSplitGroups = 512;
 constexpr int kSampleChunks = 256;   // chunks of a sample, at most
-constexpr int kResidentMost = 768;   // workgroups of a span in a resident pass, of up to 256 threads; others: a third
+// Workgroups of a span in a resident pass, of up to 256 threads; others: a third.  Backward fewer, since each leaves sums of all
+// parameters (1000 x 784 fp32 forward 768 / 1024: 10.2 / 9.6 us; 3000 x 4 x 96 fp32 backward 12.3 / 15.3).
+constexpr int kResidentForward = 1024, kResidentBackward = 768;
 constexpr int kMinSegment = 64;      // bytes of a row that a span has at least, unless the array is small
 constexpr long long kSmallArray = 1 << 20;
 
@@ -967,9 +975,9 @@ Resident resident(int B, int S, int C, int G, int most, int together)
 
 // Workgroups of a span: what the compute units hold together; each goes on to other samples, with its parameters (and, backward,
 // their sums) in registers.
-int resident_groups(const Resident &r, int B)
+int resident_groups(const Resident &r, int B, int most)
 {
-    return std::min(ceil_div(B, r.map.subs), r.threads <= 256 ? kResidentMost : kResidentMost / 3);
+    return std::min(ceil_div(B, r.map.subs), r.threads <= 256 ? most : most / 3);
 }
 
 Norm common(const NormCall &a, int V)
@@ -997,10 +1005,14 @@ int cut(Norm &P, const NormWorkspace &ws)
     m.per = P.C / P.G;
     m.groups = P.G;
     complete<T>(m, split_threads<T>(P.C));
-    const long long rows = (long long)P.B * P.S;
-    // kSplitGroups chunks in all, but no more of a sample than its last workgroup joins quickly
-    P.chunk = (int)std::min<long long>(P.S, std::max<long long>({m.lanes * kStep, (rows + kSplitGroups - 1) / kSplitGroups,
-                                                                 ceil_div(P.S, kSampleChunks)}));
+    // kSplitGroups chunks in all or, where those leave compute units with one more than others, up to twice as many; of one size,
+    // and no more of a sample than its last workgroup joins quickly
+    int most = std::max(1, kSplitGroups / P.B);
+    auto rounds = [&](int n) { return (float)ceil_div((long long)P.B * n, kUnits) / (float)n; };
+    for (int n = most + 1; n <= 2 * kSplitGroups / P.B; ++n)
+        if (rounds(n) < 0.9f * rounds(most)) most = n;
+    most = std::min(most, kSampleChunks);
+    P.chunk = std::min(P.S, std::max(m.lanes * kStep, ceil_div(P.S, most)));
     P.chunks = ceil_div(P.S, P.chunk);
     P.stat = ws.part;
     P.group = ws.group;
@@ -1014,14 +1026,14 @@ template <typename T>
 void split_most(long long rows, int C, long long &samples, long long &chunks)
 {
     samples = rows / (split_lanes<T>(C) * kMostOf1024 + 1);
-    chunks = samples ? kSplitGroups + samples : 0;
+    chunks = samples ? std::max<long long>(2 * kSplitGroups, samples) : 0;
 }
 
 bool fits(const Norm &P, const NormWorkspace &ws, bool parameters)
 {
     const size_t chunks = (size_t)P.B * P.chunks;
     return chunks * (2 * P.G + (parameters ? 2 * P.C : 0)) * 4 <= ws.part_bytes && (size_t)P.B * P.G * 8 <= ws.group_bytes &&
-           (size_t)P.B * sizeof(unsigned) <= ws.ticket_bytes;
+           (size_t)P.B * kTicketStep * sizeof(unsigned) <= ws.ticket_bytes;
 }
 
 size_t lds_bytes(int threads, int V, int sets) { return (size_t)(reduce_floats(threads, V) + 2 * sets) * 4; }
@@ -1033,7 +1045,7 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
     const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostForward<T>, kTogetherForward);
     if (r.fits) {
         P.map = r.map;
-        const dim3 grid((unsigned)resident_groups(r, a.B), (unsigned)r.spans);
+        const dim3 grid((unsigned)resident_groups(r, a.B, kResidentForward), (unsigned)r.spans);
         const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
         if (r.rows <= 1) k_resident_forward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
         else if (r.threads > 512) k_resident_forward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
@@ -1062,7 +1074,7 @@ hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
     const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward<T>, kTogetherBackward);
     if (r.fits) {
         P.map = r.map;
-        const dim3 grid((unsigned)resident_groups(r, a.B), (unsigned)r.spans);
+        const dim3 grid((unsigned)resident_groups(r, a.B, kResidentBackward), (unsigned)r.spans);
         if (parameters && grid.x > 1) {
             P.rows = (int)grid.x;
             P.part = ws.part;
@@ -1117,9 +1129,9 @@ NormWorkspace workspace(const hqml_norm_config &c)
     long long samples, chunks;
     split_most<T>(c.max_rows, c.channels, samples, chunks);
     const size_t C = (size_t)c.channels, G = (size_t)c.groups;
-    ws.part_bytes = std::max((size_t)chunks * (2 * G + 2 * C), std::min<size_t>(kResidentMost, (size_t)c.max_rows) * 2 * C) * 4;
+    ws.part_bytes = std::max((size_t)chunks * (2 * G + 2 * C), std::min<size_t>(kResidentBackward, (size_t)c.max_rows) * 2 * C) * 4;
     ws.group_bytes = (size_t)samples * G * 8;
-    ws.ticket_bytes = (size_t)samples * sizeof(unsigned);
+    ws.ticket_bytes = (size_t)samples * kTicketStep * sizeof(unsigned);
     return ws;
 }
 
