@@ -165,7 +165,8 @@ __device__ __forceinline__ u32x4 codes16(const Sixteen<T> &v, const RowScale &s)
 
 constexpr int kHeld = 4;   // sixteens of a thread that stay in registers between the two passes over a row
 
-// kWaves waves a row, 4 / kWaves rows a workgroup; the codes' rows end with zeros.  Bound by memory.
+// kWaves waves a row, 4 / kWaves rows a workgroup; the codes' rows end with zeros.  A row stays in registers between the pass that
+// finds its scale and the one that forms its codes.  Bound by memory: 8192 x 4096 bf16 24 us, 4.2 TB/s.
 template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, long long rows, int K, int8_t *codes, long long ldc,
                                                   float *scales)
@@ -227,7 +228,8 @@ __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, lon
 template <typename T>
 hipError_t quantise(const void *x, long long ldx, long long rows, int K, int8_t *codes, long long ldc, float *scales, hipStream_t s)
 {
-    // a wave a row where its registers hold it and there are rows for all compute units' waves
+    // A wave a row where its registers hold it and there are rows for all compute units' waves; a workgroup a row otherwise, whose
+    // two barriers cost less than a long row's way through one wave.
     if (K <= 64 * 16 * kHeld && (K <= 64 * 16 || rows >= 2048)) {
         const unsigned grid = (unsigned)std::min<long long>((rows + 3) / 4, 1 << 16);
         k_quantise<T, 1><<<grid, 256, 0, s>>>((const T *)x, ldx, rows, K, codes, ldc, scales);
@@ -264,6 +266,9 @@ __device__ __forceinline__ void scaled(f32x4 (&to)[FI][FJ], const i32x4 (&acc)[F
     }
 }
 
+// Larger products: the dense layer's tiles and choice of them (at twice the k of a bf16 tile), split along k where they are few.
+// Bound by the matrix instructions, half of the compute units' busy cycles, and the epilogue's memory, in bursts between them:
+// 8192 x 4096 x 4096 bf16 with gelu and residual 150 to 162 us, 1,700 to 1,830 TOP/s; a library's bare product takes 131.
 template <typename T, int BM, int BN, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product8(Args P, Scales8 q)
 {
@@ -288,7 +293,8 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product8(Args P, Scales8 q)
                                                 [](int, int, const bool (&)[4]) { return f32x4{}; });
 }
 
-// Few rows of x: tiles of 16 FI x 16, codes of w straight from memory as k_small_forward's, x's codes from the workspace.
+// Few rows of x: tiles of 16 FI x 16, codes of w straight from memory as k_small_forward's, x's codes from the workspace.  Bound by
+// latency: 45 x 1531 -> 803 fp32 5.3 us, behind 3.7 for the codes.
 template <typename T, int FI>
 __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small8(Args P, Scales8 q)
 {
@@ -331,7 +337,7 @@ __host__ __device__ inline int own_pitch(int pairs) { return pairs * 2 + 16; }
 __host__ __device__ inline int own_bytes(int rows, int pairs) { return rows * own_pitch(pairs) + 64; }
 
 // As k_small8<T, 1>, and every workgroup rounds its tile's rows of x by itself, while its first codes of w are under way: one launch
-// instead of two.  P.a: x.
+// instead of two.  P.a: x.  784 -> 20 4.3 us, launched by two 12; 4096 -> 4096 8.5 us (16.8 MB of codes), 12.1 by two.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_small8_own(Args P, Scales8 q, int K)
 {
