@@ -426,8 +426,8 @@ size_t hqml_muon_workspace_bytes(const hqml_muon_config *cfg, int n_tensors, con
  *   `steps` times, with A = X X^T:  X = a X + (b A + c A^2) X;  p = p (1 - lr weight_decay) - lr f X
  * m in fp32.  The products take operands in fp16: one for each value where the parameters are bf16 (11
  * bits), two for fp32 parameters (22 bits), sums in fp32; values of X, A or b A + c A^2 beyond 63
- * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Small
- * matrices (a side of up to 64, and what 160 KB hold) are multiplied in fp32 instead.  Matrices and workspace
+ * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Matrices
+ * with a side of up to 64 are multiplied in fp32 or fp64 instead.  Matrices and workspace
  * must not overlap (HQML_ERR_ARG), but gradients may be shared.  The workspace is used until the step has run.
  * Errors: hqml_last_error(NULL). */
 int hqml_muon_step(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors,

@@ -12,10 +12,11 @@
 // X's values are at most a little over 1 and often small, so X, A and B = b A + c A^2 are held times 2^10: fp16's normal range then
 // goes from 2^-24 to 64 of them.
 //
-// All matrices of a call go through each product in one launch, a workgroup a tile (or a part of one along k).  Bound by the
+// All larger matrices of a call go through each product in one launch, a workgroup a tile (or a part of one along k).  Bound by the
 // matrix instructions (two 4096 x 4096 bf16, a step: X X^T 150 us, b A + c A^2 157, X 238, 1,160 TFLOP/s in the last; two
 // 1024 x 4096 fp32: 41, 19 and 57, 900 fp16 TFLOP/s in the last), below some 800 x 800 by the launches and the steps' latency
-// (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all: three 64 x 32 14.5 us for 76.
+// (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all steps (three 64 x 32 14.5 us for 76), thin ones
+// three.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -47,8 +48,8 @@ struct Matrix {
     void *p;
     const void *g;
     float *m;
-    Half *x[2], *a, *b;
-    double *sums;         // of squares, one a chunk
+    Half *x[2], *a, *b;   // thin matrices: x[0] is P, in 64 bits
+    double *sums;         // of squares, one a chunk; thin matrices: of products
     int rows, cols;
     float size;           // lr f
 };
@@ -570,7 +571,10 @@ __global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 
 
 constexpr int kSmallSide = 64, kSmallWaves = 16, kTinyWaves = 4;
 constexpr int kSmallLds = 160 * 1024 - 1024;
-constexpr long long kSmallWork = 3 << 19;   // multiply-adds of X X^T: 64 x 350 84 us (by tiles 89), 64 x 420 99 (92)
+// Up to where: in values, where the rest may be thin (16 x 1000 31 us, as thin ones 28; 48 x 128 27 and 45, 48 x 400 62 and 50;
+// 64 x 200 58 and 72, 64 x 350 84 and 72), in multiply-adds of X X^T otherwise (64 x 350 84 us, by tiles 89; 64 x 420 99 and 92).
+constexpr int kSmallValues = 14 << 10;
+constexpr long long kSmallWork = 3 << 19;
 
 __host__ __device__ inline int pad16(int n) { return (n + 15) & ~15; }
 
@@ -583,10 +587,11 @@ struct SmallSize {
     __host__ __device__ size_t bytes() const { return ((size_t)n * ldx + 2 * (size_t)n * lda + kSmallWaves * 256) * 4; }
 };
 
-bool is_small(int rows, int cols)
+bool is_small(int rows, int cols, bool thin)
 {
     const SmallSize z(rows, cols);
-    return z.n <= kSmallSide && z.bytes() <= (size_t)kSmallLds && (long long)z.n * z.n * z.m <= kSmallWork;
+    return z.n <= kSmallSide && z.bytes() <= (size_t)kSmallLds &&
+           (thin ? z.n * z.m <= kSmallValues : (long long)z.n * z.n * z.m <= kSmallWork);
 }
 
 // Four k of a 16 x 16 block: lane % 16 is the row of either operand, lane / 16 its k.
@@ -769,6 +774,409 @@ __global__ __launch_bounds__(64 * WAVES) void k_small(Batch batch, Scalars k, in
     });
 }
 
+// ---- thin matrices ----
+//
+// All steps together multiply X by a polynomial P of A = X X^T: with Q = a + b A + c A^2, a step makes Q P of P and Q A Q of A, all
+// of the smaller side alone.  So X is read twice, for A and for P X, in three launches, where each step of k_product takes three
+// and reads it twice.  The price: an error of A grows by up to a^2 = 12 a step, and P's values reach a^5 = 485 and cancel in P X,
+// so everything is held in 64 bits (those of 32 would leave errors of 1e-3), and only few steps go this way (thin_steps).
+// 4 x 3664 fp32 23 us, by k_product 101; 48 x 2000 49 and 103; 64 x 5000 73 and 123: 13 for the chunks, 48 for the chain (five
+// times four products of 64^3, by one workgroup at 7 us), 11 for P X.
+
+constexpr int kThinSide = 64, kThinWaves = 4, kChainWaves = 16;
+constexpr int kThinChunks = 64;     // of a matrix: what its workgroup of k_chain adds up
+constexpr float kThinGrowth = 1 << 22;
+
+// Positions of a workgroup along the longer side at once: for A, and for P X.
+__host__ __device__ constexpr int thin_gram_width(int nt) { return nt == 1 ? 512 : nt == 2 ? 256 : 128; }
+__host__ __device__ constexpr int thin_apply_width(int nt) { return nt == 1 ? 256 : nt == 2 ? 128 : 64; }
+// Parts of a chunk: waves beside each other along k, where there is one tile.
+__host__ __device__ constexpr int thin_parts(int nt) { return nt == 1 ? kThinWaves : 1; }
+__host__ __device__ constexpr int thin_tiles(int nt) { return nt * (nt + 1) / 2; }
+// Floats of u that a workgroup holds, of any size.
+template <class F>
+constexpr int most_floats(F width)
+{
+    int most = 0;
+    for (int nt = 1; nt <= kThinSide / 16; ++nt) most = std::max(most, 16 * nt * (width(nt) + 4));
+    return most;
+}
+
+struct ThinSize {
+    int n, nt, m, chunks;   // smaller side, its tiles, larger side
+    __host__ __device__ ThinSize(int rows, int cols)
+        : n(rows < cols ? rows : cols), nt((n + 15) / 16), m(rows < cols ? cols : rows),
+          chunks((m + thin_gram_width(nt) - 1) / thin_gram_width(nt))
+    {
+        if (chunks > kThinChunks) chunks = kThinChunks;
+    }
+    __host__ __device__ int parts() const { return chunks * thin_parts(nt); }
+};
+
+using f64x4 = __attribute__((ext_vector_type(4))) double;
+
+// Four k of a 16 x 16 block: lane % 16 is the row of either operand, lane / 16 its k; of the result lane % 16 is b's row, and
+// 4 e + lane / 16 a's.
+__device__ __forceinline__ f64x4 multiply(double a, double b, f64x4 c)
+{
+    return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
+
+// Positions p0 .. p0 + width of the longer side: u = f(place in the matrix) to U[smaller side][width + 4].
+template <int WIDTH, class F>
+__device__ __forceinline__ void thin_load(const Matrix &t, const ThinSize &z, int p0, float *U, F f)
+{
+    constexpr int kThreads = 64 * kThinWaves, kAt = F::kAt, kPitch = WIDTH + 4;
+    const int here = z.m - p0 < WIDTH ? z.m - p0 : WIDTH;
+    if (t.rows > t.cols) {   // neighbours lie along the smaller side
+        const long long base = (long long)p0 * z.n;
+        const int all = here * z.n, dp = kThreads / z.n, dc = kThreads - dp * z.n;
+        int p = (int)threadIdx.x / z.n, c = (int)threadIdx.x - p * z.n;
+        for (int i0 = threadIdx.x; i0 < all; i0 += kThreads * kAt) {
+            float u[kAt];
+            f.template many<kAt>(u, base + i0, kThreads, (all - i0 + kThreads - 1) / kThreads);
+#pragma unroll
+            for (int a = 0; a < kAt; ++a) {
+                if (i0 + a * kThreads < all) U[c * kPitch + p] = u[a];
+                p += dp, c += dc;
+                if (c >= z.n) c -= z.n, ++p;
+            }
+        }
+    } else {
+        constexpr int kDown = kThreads > WIDTH ? kThreads / WIDTH : 1, kAcross = kThreads < WIDTH ? WIDTH / kThreads : 1;
+#pragma unroll
+        for (int q = 0; q < kAcross; ++q) {
+            const int c = q * kThreads + (int)threadIdx.x % WIDTH, r0 = kDown > 1 ? (int)threadIdx.x / WIDTH : 0;
+            if (c >= here) continue;
+            for (int r = r0; r < z.n; r += kDown * kAt) {
+                float u[kAt];
+                f.template many<kAt>(u, (long long)r * t.cols + p0 + c, (long long)kDown * t.cols, (z.n - r + kDown - 1) / kDown);
+#pragma unroll
+                for (int a = 0; a < kAt; ++a)
+                    if (r + a * kDown < z.n) U[(r + a * kDown) * kPitch + c] = u[a];
+            }
+        }
+    }
+}
+
+// u at `count` places, `step` apart; updating m, or of an m that has been updated.
+template <typename G, bool UPDATE>
+struct ThinUpdate {
+    static constexpr int kAt = UPDATE ? 8 : 16;   // places before the first is used
+    const G *g;
+    float *m;
+    const Scalars &k;
+    template <int N>
+    __device__ __forceinline__ void many(float (&u)[N], long long at, long long step, int count) const
+    {
+        float gv[N], mv[N];
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+            gv[a] = a < count && (UPDATE || k.nesterov) ? widen(g[at + a * step]) : 0.0f;
+            mv[a] = a < count ? m[at + a * step] : 0.0f;
+        }
+#pragma unroll
+        for (int a = 0; a < N; ++a) {
+            if (UPDATE) {
+                mv[a] = mv[a] * k.mu + gv[a] * k.nu;
+                if (a < count) m[at + a * step] = mv[a];
+            }
+            u[a] = update_of(k, mv[a], gv[a]);
+        }
+    }
+};
+
+__device__ __forceinline__ void clear(float *U, int floats)
+{
+    for (int i = threadIdx.x; i < floats; i += blockDim.x) U[i] = 0.0f;
+    __syncthreads();
+}
+
+// Tile t of a lower triangle, in rows, of few.
+__device__ __forceinline__ void small_triangle(int t, int &i, int &j)
+{
+    i = 0, j = t;
+    while (j > i) j -= ++i;
+}
+
+// m, and the products of u with itself over a chunk: lower tiles, as the lanes hold them.
+template <typename G, int NT>
+__device__ __forceinline__ void thin_gram(const Matrix &t, const Scalars &k, int chunk, float *U)
+{
+    constexpr int kWidth = thin_gram_width(NT), kPitch = kWidth + 4, kParts = thin_parts(NT), kTiles = thin_tiles(NT);
+    constexpr int kOwn = (kTiles * kParts + kThinWaves - 1) / kThinWaves;   // tiles of a wave
+    const ThinSize z(t.rows, t.cols);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4;
+    const ThinUpdate<G, true> update{(const G *)t.g, t.m, k};
+    f64x4 s[kOwn] = {};
+    clear(U, 16 * NT * kPitch);
+    for (int p0 = chunk * kWidth; p0 < z.m; p0 += z.chunks * kWidth) {
+        if (z.m - p0 < kWidth) clear(U, 16 * NT * kPitch);   // the last one: what was there before goes
+        thin_load<kWidth>(t, z, p0, U, update);
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int tile = kParts > 1 ? 0 : o * kThinWaves + wave, part = kParts > 1 ? wave : 0;
+            if (tile >= kTiles) continue;
+            int ti, tj;
+            small_triangle(tile, ti, tj);
+            constexpr int kSteps = kWidth / 4 / kParts, kAt = 8;
+            const float *from = U + row * kPitch + part * kSteps * 4 + quad, *a = from + ti * 16 * kPitch, *b = from + tj * 16 * kPitch;
+            for (int f = 0; f < kSteps; f += kAt) {
+                float av[kAt], bv[kAt];
+#pragma unroll
+                for (int e = 0; e < kAt; ++e) av[e] = a[(f + e) * 4], bv[e] = b[(f + e) * 4];
+#pragma unroll
+                for (int e = 0; e < kAt; ++e) s[o] = multiply((double)av[e], (double)bv[e], s[o]);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int o = 0; o < kOwn; ++o) {
+        const int tile = kParts > 1 ? 0 : o * kThinWaves + wave, part = kParts > 1 ? wave : 0;
+        if (tile < kTiles) *(f64x4 *)(t.sums + ((long long)(chunk * kParts + part) * kTiles + tile) * 256 + lane * 4) = s[o];
+    }
+}
+
+template <typename G>
+__global__ __launch_bounds__(64 * kThinWaves) void k_thin_gram(Batch batch, Scalars k)
+{
+    __shared__ float U[most_floats(thin_gram_width)];
+    const int ti = matrix_of(batch.first, batch.count, blockIdx.x), chunk = blockIdx.x - batch.first[ti];
+    const Matrix &t = batch.t[ti];
+    switch (ThinSize(t.rows, t.cols).nt) {
+    case 1: thin_gram<G, 1>(t, k, chunk, U); break;
+    case 2: thin_gram<G, 2>(t, k, chunk, U); break;
+    case 3: thin_gram<G, 3>(t, k, chunk, U); break;
+    default: thin_gram<G, 4>(t, k, chunk, U); break;
+    }
+}
+
+__host__ __device__ constexpr int chain_pitch(int nt) { return 16 * nt + 2; }
+// Sums of the chunks' values by so many threads each.
+__host__ __device__ constexpr int chain_down(int nt)
+{
+    const int down = 64 * kChainWaves / (thin_tiles(nt) * 128);
+    return down > 1 ? down : 1;
+}
+constexpr size_t chain_bytes(int nt)
+{
+    return (4 * (size_t)(16 * nt) * chain_pitch(nt) + (chain_down(nt) > 1 ? chain_down(nt) * thin_tiles(nt) * 256 : 0)) * 8;
+}
+
+// A matrix's P / max(|u|, eps), from the chunks' products: one workgroup, in LDS.
+template <int NT>
+__device__ __forceinline__ void chain(const Matrix &t, const Scalars &k, int steps, double *lds)
+{
+    constexpr int kThreads = 64 * kChainWaves, kTiles = thin_tiles(NT), kValues = kTiles * 256;
+    constexpr int kPitch = chain_pitch(NT), kN = 16 * NT;
+    const ThinSize z(t.rows, t.cols);
+    double *A = lds, *Q = A + kN * kPitch, *R = Q + kN * kPitch, *P = R + kN * kPitch, *held = P + kN * kPitch;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4;
+    // chunks' products, threads across the values and down the chunks
+    constexpr int kPairs = kValues / 2, kDown = chain_down(NT), kAt = 16;
+    using f64x2 = __attribute__((ext_vector_type(2))) double;
+    const int down = kDown > 1 ? (int)threadIdx.x / kPairs : 0, parts = z.parts();
+    auto put_at = [&](double *to, int tile, int l, int e, double v) {   // value e of lane l, to both places
+        int ti, tj;
+        small_triangle(tile, ti, tj);
+        const int i = ti * 16 + 4 * e + (l >> 4), j = tj * 16 + (l & 15);
+        to[i * kPitch + j] = v;
+        if (ti != tj) to[j * kPitch + i] = v;
+    };
+    for (int i = kDown > 1 ? (int)threadIdx.x % kPairs : (int)threadIdx.x; i < kPairs && down < kDown; i += kThreads) {
+        f64x2 s = {};
+        for (int c0 = down; c0 < parts; c0 += kDown * kAt) {
+            f64x2 v[kAt];
+#pragma unroll
+            for (int a = 0; a < kAt; ++a)
+                v[a] = c0 + a * kDown < parts ? *(const f64x2 *)(t.sums + (long long)(c0 + a * kDown) * kValues + 2 * i) : f64x2{};
+#pragma unroll
+            for (int a = 0; a < kAt; ++a) s += v[a];
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int at = 2 * i + e;
+            if (kDown > 1) held[down * kValues + at] = s[e];
+            else put_at(A, at >> 8, (at & 255) >> 2, at & 3, s[e]);
+        }
+    }
+    __syncthreads();
+    if (kDown > 1) {
+        for (int i = threadIdx.x; i < kValues; i += kThreads) {
+            double s = 0.0;
+#pragma unroll
+            for (int d = 0; d < kDown; ++d) s += held[d * kValues + i];
+            put_at(A, i >> 8, (i & 255) >> 2, i & 3, s);
+        }
+        __syncthreads();
+    }
+    double square = 0.0;   // |u|^2, the trace; the same in every wave
+    if (lane < kN) square = A[lane * kPitch + lane];
+    square = wave_sum(square);
+    const double norm = sqrt(square), inv = 1.0 / (norm <= (double)k.eps ? (double)k.eps : norm);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kN * kN; i += kThreads) A[i / kN * kPitch + i % kN] *= inv * inv;
+    __syncthreads();
+    auto tile_product = [&](const double *a, const double *b, int ti, int tj) {
+        a += (ti * 16 + row) * kPitch + quad, b += (tj * 16 + row) * kPitch + quad;
+        double av[NT * 4], bv[NT * 4];
+#pragma unroll
+        for (int f = 0; f < NT * 4; ++f) av[f] = a[f * 4], bv[f] = b[f * 4];
+        f64x4 s = {};
+#pragma unroll
+        for (int f = 0; f < NT * 4; ++f) s = multiply(av[f], bv[f], s);
+        return s;
+    };
+    auto put_tile = [&](double *to, int tile, f64x4 v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) put_at(to, tile, lane, e, v[e]);
+    };
+    for (int step = 0; step < steps; ++step) {
+        const bool last = step + 1 == steps;
+        for (int tile = wave; tile < kTiles; tile += kChainWaves) {   // Q = a + b A + c A^2
+            int ti, tj;
+            small_triangle(tile, ti, tj);
+            f64x4 s = tile_product(A, A, ti, tj);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = ti * 16 + 4 * e + quad, j = tj * 16 + row;
+                s[e] = (double)k.c * s[e] + (double)k.b * A[i * kPitch + j] + (i == j ? (double)k.a : 0.0);
+            }
+            put_tile(Q, tile, s);
+            if (step == 0) put_tile(P, tile, s);
+        }
+        __syncthreads();
+        // R = Q A, and Q P; P is read by all before any of it is replaced
+        constexpr int kOwn = (2 * kTiles + kChainWaves - 1) / kChainWaves;
+        f64x4 s[kOwn];
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int at = o * kChainWaves + wave, tile = at % kTiles;
+            if (at >= 2 * kTiles || (at < kTiles ? last : step == 0)) continue;
+            int ti, tj;
+            small_triangle(tile, ti, tj);
+            s[o] = tile_product(Q, at < kTiles ? A : P, ti, tj);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int o = 0; o < kOwn; ++o) {
+            const int at = o * kChainWaves + wave, tile = at % kTiles;
+            if (at >= 2 * kTiles || (at < kTiles ? last : step == 0)) continue;
+            put_tile(at < kTiles ? R : P, tile, s[o]);
+        }
+        __syncthreads();
+        if (last) break;
+        for (int tile = wave; tile < kTiles; tile += kChainWaves) {   // A = Q (Q A)
+            int ti, tj;
+            small_triangle(tile, ti, tj);
+            put_tile(A, tile, tile_product(Q, R, ti, tj));
+        }
+        __syncthreads();
+    }
+    double *to = (double *)t.x[0];
+    for (int i = threadIdx.x; i < kN * kN; i += kThreads) to[i] = P[i / kN * kPitch + i % kN] * inv;
+}
+
+__global__ __launch_bounds__(64 * kChainWaves) void k_chain(Batch batch, Scalars k, int steps)
+{
+    extern __shared__ double chain_lds[];
+    const Matrix &t = batch.t[blockIdx.x];
+    switch (ThinSize(t.rows, t.cols).nt) {
+    case 1: chain<1>(t, k, steps, chain_lds); break;
+    case 2: chain<2>(t, k, steps, chain_lds); break;
+    case 3: chain<3>(t, k, steps, chain_lds); break;
+    default: chain<4>(t, k, steps, chain_lds); break;
+    }
+}
+
+// P X, and the parameter.
+template <typename T, typename G, int NT>
+__device__ __forceinline__ void thin_apply(const Matrix &t, const Scalars &k, int wg, float *U, double *P)
+{
+    constexpr int kWidth = thin_apply_width(NT), kPitch = kWidth + 4, kN = 16 * NT, kPitchP = chain_pitch(NT);
+    const ThinSize z(t.rows, t.cols);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, row = lane & 15, quad = lane >> 4, p0 = wg * kWidth;
+    const bool tall = t.rows > t.cols;
+    const double *from = (const double *)t.x[0];
+    double q[NT * NT];   // on its way while u is loaded
+#pragma unroll
+    for (int i = 0; i < NT * NT; ++i) q[i] = from[i * 64 * kThinWaves + threadIdx.x];
+    clear(U, kN * kPitch);
+    thin_load<kWidth>(t, z, p0, U, ThinUpdate<G, false>{(const G *)t.g, t.m, k});
+#pragma unroll
+    for (int i = 0; i < NT * NT; ++i) {
+        const int at = i * 64 * kThinWaves + (int)threadIdx.x;
+        P[at / kN * kPitchP + at % kN] = q[i];
+    }
+    __syncthreads();
+    T *p = (T *)t.p;
+    for (int c = wave; c < kWidth / 16; c += kThinWaves) {
+        if (p0 + c * 16 >= z.m) break;
+        double u[NT * 4];
+        float y[NT][4];
+        auto at = [&](int it, int e, long long &place) {
+            const int own = it * 16 + (tall ? row : 4 * e + quad), along = p0 + c * 16 + (tall ? 4 * e + quad : row);
+            place = tall ? (long long)along * t.cols + own : (long long)own * t.cols + along;
+            return own < z.n && along < z.m;
+        };
+#pragma unroll
+        for (int it = 0; it < NT; ++it)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                long long place;
+                y[it][e] = at(it, e, place) ? widen(p[place]) : 0.0f;
+            }
+#pragma unroll
+        for (int f = 0; f < NT * 4; ++f) u[f] = (double)U[(f * 4 + quad) * kPitch + c * 16 + row];
+#pragma unroll
+        for (int it = 0; it < NT; ++it) {
+            f64x4 s = {};
+#pragma unroll
+            for (int f = 0; f < NT * 4; ++f) {
+                const double v = P[(it * 16 + row) * kPitchP + f * 4 + quad];
+                s = tall ? multiply(u[f], v, s) : multiply(v, u[f], s);   // neighbours of the matrix in neighbouring lanes
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                long long place;
+                if (at(it, e, place)) narrow(__builtin_fmaf(y[it][e], -k.decay, y[it][e]) - t.size * (float)s[e], p[place]);
+            }
+        }
+    }
+}
+
+template <typename T, typename G>
+__global__ __launch_bounds__(64 * kThinWaves) void k_thin_apply(Batch batch, Scalars k)
+{
+    __shared__ float U[most_floats(thin_apply_width)];
+    __shared__ double P[kThinSide * chain_pitch(kThinSide / 16)];
+    const int ti = matrix_of(batch.first, batch.count, blockIdx.x), wg = blockIdx.x - batch.first[ti];
+    const Matrix &t = batch.t[ti];
+    switch (ThinSize(t.rows, t.cols).nt) {
+    case 1: thin_apply<T, G, 1>(t, k, wg, U, P); break;
+    case 2: thin_apply<T, G, 2>(t, k, wg, U, P); break;
+    case 3: thin_apply<T, G, 3>(t, k, wg, U, P); break;
+    default: thin_apply<T, G, 4>(t, k, wg, U, P); break;
+    }
+}
+
+// Whether errors of A stay small over the steps: how much one grows, for any singular value.
+bool thin_steps(const hqml_muon_config &c)
+{
+    for (int i = 0; i <= 64; ++i) {
+        double x = i ? exp2(-(i - 1) * 0.5) : 0.0, grown = 1.0;   // an eigenvalue of A
+        for (int step = 0; step < c.steps; ++step) {
+            const double q = c.a + c.b * x + c.c * x * x, slope = q * (q + 2 * x * (c.b + 2 * c.c * x));
+            grown *= std::max({1.0, q * q, fabs(slope)});
+            x *= q * q;
+            if (!(grown <= kThinGrowth)) return false;
+        }
+    }
+    return true;
+}
+
 // ---- a call ----
 
 struct Bytes {
@@ -788,6 +1196,17 @@ Bytes bytes_of(const hqml_muon_tensor &t, int planes)
     return b;
 }
 
+struct ThinBytes {
+    size_t p, sums;   // P, the chunks' products
+    size_t all() const { return p + sums; }
+};
+
+ThinBytes thin_bytes(const hqml_muon_tensor &t)
+{
+    const ThinSize z(t.rows, t.cols);
+    return {up256((size_t)256 * z.nt * z.nt * 8), up256((size_t)z.parts() * thin_tiles(z.nt) * 256 * 8)};
+}
+
 // Partial sums of a launch: at most this much, in tiles that at most so many tickets count.
 constexpr size_t kPartBytes = 64ull << 20;
 constexpr int kTickets = 4096;
@@ -795,25 +1214,44 @@ constexpr size_t kJoinBytes = kPartBytes + kTickets * sizeof(unsigned);
 
 int planes_of(const hqml_muon_config &cfg) { return cfg.param_dtype == HQML_DTYPE_FP32 ? 2 : 1; }
 
+enum Kind { SMALL, THIN, LARGE };
+
+// Which way a call's matrices go.
+class KindOf {
+public:
+    explicit KindOf(const hqml_muon_config &cfg) : cfg_(cfg) {}
+    Kind operator()(const hqml_muon_tensor &t)
+    {
+        if (std::min(t.rows, t.cols) > kThinSide) return LARGE;
+        if (is_small(t.rows, t.cols, true)) return SMALL;
+        if (few_ < 0) few_ = thin_steps(cfg_);
+        return few_ ? THIN : is_small(t.rows, t.cols, false) ? SMALL : LARGE;
+    }
+
+private:
+    const hqml_muon_config &cfg_;
+    int few_ = -1;
+};
+
 // Calls f(first, last, bytes) for each round of matrices that go together.
 template <typename F>
 void rounds(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, F f)
 {
+    KindOf kind_of(cfg);
     for (int i = 0; i < n;) {
         size_t bytes = 0;
-        int last = i, large = 0, small = 0;
-        for (; last < n && large < kMatrices && small < kMatrices; ++last) {
+        int last = i, count[3] = {};
+        for (; last < n && *std::max_element(count, count + 3) < kMatrices; ++last) {
             if (!t[last].rows || !t[last].cols) continue;
-            if (is_small(t[last].rows, t[last].cols)) {
-                ++small;
-                continue;
-            }
-            const size_t here = bytes_of(t[last], planes_of(cfg)).all();
-            if (large && bytes + here > kBatchBytes) break;
+            const Kind kind = kind_of(t[last]);
+            const size_t here = kind == LARGE  ? bytes_of(t[last], planes_of(cfg)).all()
+                                : kind == THIN ? thin_bytes(t[last]).all()
+                                               : 0;
+            if (bytes && bytes + here > kBatchBytes) break;
             bytes += here;
-            ++large;
+            ++count[kind];
         }
-        if (large || small) f(i, last, large ? bytes + kJoinBytes : 0);
+        if (count[SMALL] || count[THIN] || count[LARGE]) f(i, last, count[LARGE] ? bytes + kJoinBytes : bytes);
         i = last;
     }
 }
@@ -989,9 +1427,10 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     k.eps = (float)cfg.eps;
     k.decay = (float)(cfg.lr * cfg.weight_decay);
     k.a = (float)cfg.a, k.b = (float)cfg.b, k.c = (float)cfg.c;
-    Batch b{}, few{};   // large matrices, small ones
+    Batch b{}, thin{}, few{};   // large matrices, thin ones, small ones
+    KindOf kind_of(cfg);
     unsigned groups = 0;
-    auto each = [&](auto count_of) {   // first workgroups
+    auto each = [&](Batch &b, auto count_of) {   // first workgroups
         groups = 0;
         for (int i = 0; i < b.count; ++i) {
             b.first[i] = groups;
@@ -1000,25 +1439,32 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
     };
     for (int i = 0; i < n; ++i) {
         if (!t[i].rows || !t[i].cols) continue;
-        const bool small = is_small(t[i].rows, t[i].cols);
-        const Bytes z = bytes_of(t[i], PLANES);
-        Matrix &m = small ? few.t[few.count++] : b.t[b.count++];
+        const Kind kind = kind_of(t[i]);
+        Batch &to = kind == SMALL ? few : kind == THIN ? thin : b;
+        Matrix &m = to.t[to.count++];
         m.p = t[i].param, m.g = t[i].grad, m.m = t[i].momentum;
         m.rows = t[i].rows, m.cols = t[i].cols;
         m.size = (float)(cfg.lr * t[i].scale);
-        if (small) continue;
+        if (kind == SMALL) continue;
         auto take = [&](size_t bytes) {
             char *here = work;
             work += bytes;
             return here;
         };
+        if (kind == THIN) {
+            const ThinBytes z = thin_bytes(t[i]);
+            m.x[0] = (Half *)take(z.p);
+            m.sums = (double *)take(z.sums);
+            continue;
+        }
+        const Bytes z = bytes_of(t[i], PLANES);
         m.x[0] = (Half *)take(z.x), m.x[1] = (Half *)take(z.x);
         m.a = (Half *)take(z.gram), m.b = (Half *)take(z.gram);
         m.sums = (double *)take(z.sums);
     }
     hipError_t e = hipSuccess;
+    using T = std::conditional_t<PLANES == 2, float, bf16>;
     if (few.count) {
-        using T = std::conditional_t<PLANES == 2, float, bf16>;
         size_t lds = 0;
         bool tiny = true;
         for (int i = 0; i < few.count; ++i) {
@@ -1032,14 +1478,35 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
         }
         if (tiny) k_small<T, G, kTinyWaves><<<few.count, 64 * kTinyWaves, lds, s>>>(few, k, cfg.steps);
         else k_small<T, G, kSmallWaves><<<few.count, 64 * kSmallWaves, lds, s>>>(few, k, cfg.steps);
-        if ((e = hipGetLastError()) != hipSuccess || !b.count) return e;
+        if ((e = hipGetLastError()) != hipSuccess) return e;
     }
+    if (thin.count) {
+        int nt = 0;
+        for (int i = 0; i < thin.count; ++i) nt = std::max(nt, ThinSize(thin.t[i].rows, thin.t[i].cols).nt);
+        if (chain_bytes(nt) > 64 * 1024) {
+            e = hipFuncSetAttribute((const void *)k_chain, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)chain_bytes(kThinSide / 16));
+            if (e != hipSuccess) return e;
+        }
+        each(thin, [](const Matrix &m) { return (unsigned)ThinSize(m.rows, m.cols).chunks; });
+        k_thin_gram<G><<<groups, 64 * kThinWaves, 0, s>>>(thin, k);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        k_chain<<<thin.count, 64 * kChainWaves, chain_bytes(nt), s>>>(thin, k, cfg.steps);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        each(thin, [](const Matrix &m) {
+            const ThinSize z(m.rows, m.cols);
+            return (unsigned)ceil_div(z.m, thin_apply_width(z.nt));
+        });
+        k_thin_apply<T, G><<<groups, 64 * kThinWaves, 0, s>>>(thin, k);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!b.count) return hipSuccess;
     float *const part = (float *)work;
     unsigned *const ticket = (unsigned *)(work + kPartBytes);
-    each([](const Matrix &m) { return (unsigned)(((long long)m.rows * m.cols + kChunk - 1) / kChunk); });
+    each(b, [](const Matrix &m) { return (unsigned)(((long long)m.rows * m.cols + kChunk - 1) / kChunk); });
     k_momentum<G><<<groups, 256, 0, s>>>(b, k, ticket, kTickets);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    each([](const Matrix &m) { return (unsigned)std::min<long long>(((long long)m.rows * pad8(m.cols) / 8 + 255) / 256, 4096); });
+    each(b, [](const Matrix &m) { return (unsigned)std::min<long long>(((long long)m.rows * pad8(m.cols) / 8 + 255) / 256, 4096); });
     k_begin<G, PLANES><<<groups, 256, 0, s>>>(b, k);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     Products gram{}, poly{}, apply{};

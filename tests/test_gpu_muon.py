@@ -90,6 +90,39 @@ def test_cuts(sizes, dtype):
     check(sizes, dtype, seed=3)
 
 
+THIN = [[(1, 30000)], [(64, 5000), (5000, 64)], [(7, 4099), (4099, 16), (17, 3000), (2049, 33)], [(48, 1300), (1300, 49)],
+        [(64, 40000), (3, 65536)], [(62, 1175), (100, 90), (8, 8), (1175, 62)]]
+
+
+@pytest.mark.parametrize("dtype,grad", [("fp32", "fp32"), ("bf16", "bf16"), ("fp32", "bf16"), ("bf16", "fp32")])
+@pytest.mark.parametrize("n", range(len(THIN)))
+def test_thin_matrices(n, dtype, grad):
+    check(THIN[n], dtype, grad, nesterov=n % 2 == 0, seed=n)
+
+
+@pytest.mark.parametrize("sizes", [(40, 3000), (5000, 64), (30, 40), (300, 200)])
+def test_gradients_of_few_directions(sizes):
+    """Two directions, and, of the roundings, all others 1e-8 as large: what comes of those is as large as in 64 bits."""
+    from qml_gradients_amd.optim import Muon
+    r, c = sizes
+    g = torch.Generator(device="cuda").manual_seed(1)
+    p = torch.nn.Parameter(torch.zeros(r, c, device="cuda"))
+    p.grad = torch.randn(r, 2, generator=g, device="cuda") @ torch.randn(2, c, generator=g, device="cuda")
+    opt = Muon([p], lr=1.0, adjust="none")
+    opt.step()
+    _, u = muon(p, p.grad, torch.zeros_like(p), 1.0, 0.95, 0.0, True, 1.0)
+    x, norm_bound, most = orthogonal_bound(u, "fp32", 5, COEFFICIENTS)
+    off = -p.detach().double() - x
+    assert float(torch.linalg.vector_norm(off)) <= norm_bound + 2.0 ** -24 * float(torch.linalg.vector_norm(x))
+    assert float((off.abs() - 2.0 ** -24 * x.abs()).max()) <= most
+
+
+@pytest.mark.parametrize("steps,coefficients", [(1, COEFFICIENTS), (2, COEFFICIENTS), (6, COEFFICIENTS), (9, COEFFICIENTS),
+                                                (12, (1.5, -0.5, 0.0)), (3, (2.0, -1.5, 0.5))])
+def test_steps_of_thin_matrices(steps, coefficients):
+    check([(50, 1500), (3000, 10)], "fp32", steps=steps, coefficients=coefficients)
+
+
 def test_large_and_small_matrices_in_one_call():
     check([(70 + n, 90 + 2 * n) if n % 3 else (5 + n, 40) for n in range(45)], "bf16")
     check([(70 + n, 90 + 2 * n) for n in range(5)], "fp32")
@@ -152,7 +185,7 @@ def test_sizes_of_gradients_do_not_count():
     assert torch.allclose(-p[0], torch.full_like(p[0], 3.4445e-5), rtol=1e-3)
 
 
-@pytest.mark.parametrize("sizes", [[(20, 30)], [(300, 200)]])
+@pytest.mark.parametrize("sizes", [[(20, 30)], [(300, 200)], [(20, 3000)]])
 def test_gradients_of_zero_and_nan(sizes):
     """Zeros: only the decay.  A NaN or an infinity: the whole matrix, and none beside it."""
     from qml_gradients_amd.optim import Muon
