@@ -231,7 +231,7 @@ def test_same_result_whatever_else_is_in_the_call():
 def test_streams_and_graphs():
     """A captured step repeats the step, with what the gradients then hold; eager ones on another stream come between."""
     from qml_gradients_amd.optim import Muon
-    for sizes in ([(40, 30)], [(300, 420), (128, 200)]):
+    for sizes in ([(40, 30)], [(300, 420), (128, 200)], [(2000, 40), (10, 4000)], [(64, 2000), (20, 30), (100, 90)]):
         a, b = matrices(sizes), matrices(sizes)
         x, y = Muon(a), Muon(b)
         x.step(), y.step()
@@ -255,7 +255,7 @@ def test_streams_and_graphs():
 def test_two_streams_at_once():
     """Steps of their own parameters do not disturb each other."""
     from qml_gradients_amd.optim import Muon
-    sizes = [(200, 6000), (300, 200), (20, 30)]
+    sizes = [(200, 6000), (300, 200), (20, 30), (3000, 33)]
     both = [matrices(sizes, seed=n) for n in (0, 40)]
     alone = [matrices(sizes, seed=n) for n in (0, 40)]
     streams = [torch.cuda.Stream() for _ in both]
