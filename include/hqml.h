@@ -415,6 +415,7 @@ typedef struct {
     double a, b, c;    /* coefficients of the polynomial, magnitudes up to 16 */
     int device;
     void *stream;
+    int precise;       /* nonzero: bf16 parameters' products of two fp16 values an operand, as fp32 ones' */
 } hqml_muon_config;
 
 /* Device bytes that hqml_muon_step needs at `workspace` (256-byte aligned).  Host-only; looks at the
@@ -424,8 +425,9 @@ size_t hqml_muon_workspace_bytes(const hqml_muon_config *cfg, int n_tensors, con
 /* One step over n_tensors matrices (mu = momentum):
  *   m = mu m + (1 - mu) g,  u = nesterov ? mu m + (1 - mu) g : m,  X = u / max(|u|, eps) (Frobenius norm);
  *   `steps` times, with A = X X^T:  X = a X + (b A + c A^2) X;  p = p (1 - lr weight_decay) - lr f X
- * m in fp32.  The products take operands in fp16: one for each value where the parameters are bf16 (11
- * bits), two for fp32 parameters (22 bits), sums in fp32; values of X, A or b A + c A^2 beyond 63
+ * m in fp32.  The products take operands in fp16, sums in fp32: two for each value (22 bits), X then off by
+ * some 2e-6 of its size, or, for bf16 parameters with precise == 0, one (11 bits): a third of the time and half of the workspace,
+ * and X off by 1.5e-3, where a gradient has few directions by up to 4e-2; values of X, A or b A + c A^2 beyond 63
  * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Matrices
  * with a side of up to 64 are multiplied in fp32 or fp64 instead.  Matrices and workspace
  * must not overlap (HQML_ERR_ARG), but gradients may be shared.  The workspace is used until the step has run.

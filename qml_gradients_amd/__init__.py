@@ -142,6 +142,7 @@ class hqml_muon_config(ctypes.Structure):
         ("c", ctypes.c_double),
         ("device", ctypes.c_int),
         ("stream", ctypes.c_void_p),
+        ("precise", ctypes.c_int),
     ]
 
 

@@ -7,14 +7,17 @@
 // The polynomial acts on the singular values alone, so a matrix with more rows than columns takes A = X^T X and
 // X <- a X + X (b A + c A^2): A is as small as it can be, and no matrix is transposed.  Three products a step, on the matrix
 // cores, of operands in fp16 (products exact, sums in fp32):
-//   bf16 parameters  one fp16 value for each: 11 bits, where the parameter keeps 8
-//   fp32 parameters  two, x = hi + lo, 22 bits; of their four products the three that count, one after the other along k
+//   two values for each, x = hi + lo, 22 bits; of their four products the three that count, one after the other along k
+//   one value for each, 11 bits, where the caller of bf16 parameters (`precise` 0) takes that: a third of the products
+// With two, X is as exact as fp32 sums leave it (1e-6 to 2e-6 of its size after five steps).  With one it is off by 1.5e-3, and by 4e-2
+// where a gradient has few directions: roundings fill the others, and each step lifts those by a = 3.4.  A bf16 parameter's own
+// rounding hides such errors in one step, but not in the sum of many.
 // X's values are at most a little over 1 and often small, so X, A and B = b A + c A^2 are held times 2^10: fp16's normal range then
 // goes from 2^-24 to 64 of them.
 //
 // All larger matrices of a call go through each product in one launch, a workgroup a tile (or a part of one along k).  Bound by the
-// matrix instructions (two 4096 x 4096 bf16, a step: X X^T 150 us, b A + c A^2 157, X 238, 1,160 TFLOP/s in the last; two
-// 1024 x 4096 fp32: 41, 19 and 57, 900 fp16 TFLOP/s in the last), below some 800 x 800 by the launches and the steps' latency
+// matrix instructions (two 4096 x 4096 of one value, a step: X X^T 150 us, b A + c A^2 157, X 238, 1,160 TFLOP/s in the last; of
+// two, 8.3 ms for 2.8 in all; two 1024 x 4096 of two: 41, 19 and 57, 900 fp16 TFLOP/s in the last), below some 800 x 800 by the launches and the steps' latency
 // (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all steps (three 64 x 32 14.5 us for 76), thin ones
 // three.
 #include <hip/hip_runtime.h>
@@ -431,7 +434,8 @@ __device__ __forceinline__ void write_planes(Half *to, long long plane, const fl
     if (PLANES == 2) *(u32x4 *)(to + plane) = __builtin_bit_cast(u32x4, lo);
 }
 
-template <int STAGE, int LA, int LB, int PLANES, int BM, int BN, int WI, int WJ>
+// T: the parameter's type.
+template <int STAGE, int LA, int LB, int PLANES, typename T, int BM, int BN, int WI, int WJ>
 __device__ __forceinline__ void product(const Product &P, const Finish &F, int ti, int tj, int tile, int part, char *a0, char *a1,
                                         char *a2, char *a3, char *b0, char *b1, char *b2, char *b3)
 {
@@ -488,7 +492,6 @@ __device__ __forceinline__ void product(const Product &P, const Finish &F, int t
                 }
                 continue;
             }
-            using T = std::conditional_t<PLANES == 2, float, bf16>;
             T *p = (T *)P.p + (long long)i * P.J + j, t[8];
             const float size = P.size * kUnscale;
             if (j + 8 <= P.J) {
@@ -528,7 +531,7 @@ __device__ __forceinline__ void product(const Product &P, const Finish &F, int t
     }
 }
 
-template <int STAGE, int PLANES, int SIDE, int WAVES, int MOST>
+template <int STAGE, int PLANES, typename T, int SIDE, int WAVES, int MOST>
 __global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 4 ? 1 : 2) void k_product(ProductsOf<MOST> G, Finish F)
 {
     constexpr int kBytes = SIDE * 64 * PLANES;
@@ -556,11 +559,11 @@ __global__ __launch_bounds__(64 * WAVES, PLANES == 2 && SIDE == 128 && WAVES == 
     // 256 x 256: waves of 64 x 128 where both operands lie along k, of 128 x 64 elsewhere, as the dense layer's
     constexpr int WI = 2, WJ = WAVES / 2, WIR = WAVES / 2, WJR = 2;
     if (STAGE == POLY || !P.cols)
-        product<STAGE, K_ROWS, K_ROWS, PLANES, SIDE, SIDE, WIR, WJR>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+        product<STAGE, K_ROWS, K_ROWS, PLANES, T, SIDE, SIDE, WIR, WJR>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
     else if (STAGE == GRAM)
-        product<STAGE, K_COLS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+        product<STAGE, K_COLS, K_COLS, PLANES, T, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
     else
-        product<STAGE, K_ROWS, K_COLS, PLANES, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
+        product<STAGE, K_ROWS, K_COLS, PLANES, T, SIDE, SIDE, WI, WJ>(P, F, ti, tj, tile, part, a0, a1, a2, a3, b0, b1, b2, b3);
 }
 
 // ---- small matrices ----
@@ -1212,7 +1215,7 @@ constexpr size_t kPartBytes = 64ull << 20;
 constexpr int kTickets = 4096;
 constexpr size_t kJoinBytes = kPartBytes + kTickets * sizeof(unsigned);
 
-int planes_of(const hqml_muon_config &cfg) { return cfg.param_dtype == HQML_DTYPE_FP32 ? 2 : 1; }
+int planes_of(const hqml_muon_config &cfg) { return cfg.param_dtype == HQML_DTYPE_FP32 || cfg.precise ? 2 : 1; }
 
 enum Kind { SMALL, THIN, LARGE };
 
@@ -1356,16 +1359,20 @@ Plan plan_of(const Products &G, int planes)
 // The arguments of few products are few: three 100 x 120, 17 launches, take 95 us a step so, 100 with room for 24 in each.
 constexpr int kFew = 4;
 
-template <int STAGE, int PLANES, int MOST>
+template <int STAGE, int PLANES, typename T, int MOST>
 void launch(const ProductsOf<MOST> &G, const Finish &F, int side, unsigned groups, hipStream_t s)
 {
-    if (side == 64) k_product<STAGE, PLANES, 64, 4, MOST><<<groups, 256, 0, s>>>(G, F);
-    else if (PLANES == 1 && side == 128) k_product<STAGE, 1, 128, 4, MOST><<<groups, 256, 0, s>>>(G, F);
-    else if (PLANES == 2) k_product<STAGE, 2, 128, 8, MOST><<<groups, 512, 0, s>>>(G, F);
-    else k_product<STAGE, 1, 256, 8, MOST><<<groups, 512, 0, s>>>(G, F);
+    if (side == 64) {
+        k_product<STAGE, PLANES, T, 64, 4, MOST><<<groups, 256, 0, s>>>(G, F);
+    } else if constexpr (PLANES == 2) {
+        k_product<STAGE, 2, T, 128, 8, MOST><<<groups, 512, 0, s>>>(G, F);
+    } else {
+        if (side == 128) k_product<STAGE, 1, T, 128, 4, MOST><<<groups, 256, 0, s>>>(G, F);
+        else k_product<STAGE, 1, T, 256, 8, MOST><<<groups, 512, 0, s>>>(G, F);
+    }
 }
 
-template <int STAGE, int PLANES>
+template <int STAGE, int PLANES, typename T>
 hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *tiles, const int *skip, float *part, unsigned *ticket,
                    hipStream_t s)
 {
@@ -1390,18 +1397,18 @@ hipError_t run_cut(Products &G, const Finish &F, const Pieces &cut, const int *t
         at += ((unsigned)P.tiles * (unsigned)P.parts + 7) & ~7u;
     }
     if (G.count > kFew) {
-        launch<STAGE, PLANES>(G, F, cut.side, at, s);
+        launch<STAGE, PLANES, T>(G, F, cut.side, at, s);
     } else {
         ProductsOf<kFew> few;
         few.count = G.count;
         std::copy_n(G.first, kFew, few.first);
         std::copy_n(G.t, kFew, few.t);
-        launch<STAGE, PLANES>(few, F, cut.side, at, s);
+        launch<STAGE, PLANES, T>(few, F, cut.side, at, s);
     }
     return hipGetLastError();
 }
 
-template <int STAGE, int PLANES>
+template <int STAGE, int PLANES, typename T>
 hipError_t run_stage(Products &G, const Finish &F, const Plan &plan, float *part, unsigned *ticket, hipStream_t s)
 {
     if (!plan.main.side) return hipErrorInvalidValue;
@@ -1412,13 +1419,13 @@ hipError_t run_stage(Products &G, const Finish &F, const Plan &plan, float *part
         left -= tiles[i];
         skip[i] = tiles[i];
     }
-    hipError_t e = run_cut<STAGE, PLANES>(G, F, plan.main, tiles, nullptr, part, ticket, s);
+    hipError_t e = run_cut<STAGE, PLANES, T>(G, F, plan.main, tiles, nullptr, part, ticket, s);
     if (e != hipSuccess || !plan.rest.side) return e;
     for (int i = 0; i < G.count; ++i) tiles[i] = tiles_of(G.t[i], plan.main.side) - skip[i];
-    return run_cut<STAGE, PLANES>(G, F, plan.rest, tiles, skip, part, ticket, s);
+    return run_cut<STAGE, PLANES, T>(G, F, plan.rest, tiles, skip, part, ticket, s);
 }
 
-template <typename G, int PLANES>
+template <typename T, typename G, int PLANES>
 hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, char *work, hipStream_t s)
 {
     Scalars k;
@@ -1463,7 +1470,6 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
         m.sums = (double *)take(z.sums);
     }
     hipError_t e = hipSuccess;
-    using T = std::conditional_t<PLANES == 2, float, bf16>;
     if (few.count) {
         size_t lds = 0;
         bool tiny = true;
@@ -1543,9 +1549,9 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
             A.a = A.b = x;
             X.a = tall ? x : m.b, X.b = tall ? m.b : x, X.with = x, X.c = m.x[1 - (step & 1)];
         }
-        if ((e = run_stage<GRAM, PLANES>(gram, {kUnscale, 0.0f, 0.0f, 0}, plan_gram, part, ticket, s)) != hipSuccess) return e;
-        if ((e = run_stage<POLY, PLANES>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, plan_poly, part, ticket, s)) != hipSuccess) return e;
-        if ((e = run_stage<APPLY, PLANES>(apply, {kUnscale, k.a, k.decay, last}, plan_apply, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<GRAM, PLANES, float>(gram, {kUnscale, 0.0f, 0.0f, 0}, plan_gram, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<POLY, PLANES, float>(poly, {k.c * kUnscale, k.b, 0.0f, 0}, plan_poly, part, ticket, s)) != hipSuccess) return e;
+        if ((e = run_stage<APPLY, PLANES, T>(apply, {kUnscale, k.a, k.decay, last}, plan_apply, part, ticket, s)) != hipSuccess) return e;
     }
     return hipSuccess;
 }
@@ -1564,12 +1570,17 @@ hipError_t launch_muon(const hqml_muon_config &cfg, int n, const hqml_muon_tenso
     hipError_t e = hipSuccess;
     rounds(cfg, n, t, [&](int first, int last, size_t) {
         if (e != hipSuccess) return;
+        auto run_all = [&](auto of_param, auto of_grad) {
+            using T = decltype(of_param);
+            using G = decltype(of_grad);
+            char *work = (char *)workspace;
+            if constexpr (sizeof(T) == 2)
+                if (planes_of(cfg) == 1) return run<T, G, 1>(cfg, last - first, t + first, work, s);
+            return run<T, G, 2>(cfg, last - first, t + first, work, s);
+        };
         const bool gb = cfg.grad_dtype == HQML_DTYPE_BF16;
-        char *work = (char *)workspace;
-        if (cfg.param_dtype == HQML_DTYPE_BF16)
-            e = gb ? run<bf16, 1>(cfg, last - first, t + first, work, s) : run<float, 1>(cfg, last - first, t + first, work, s);
-        else
-            e = gb ? run<bf16, 2>(cfg, last - first, t + first, work, s) : run<float, 2>(cfg, last - first, t + first, work, s);
+        if (cfg.param_dtype == HQML_DTYPE_BF16) e = gb ? run_all(bf16{}, bf16{}) : run_all(bf16{}, 0.0f);
+        else e = gb ? run_all(0.0f, bf16{}) : run_all(0.0f, 0.0f);
     });
     return e;
 }

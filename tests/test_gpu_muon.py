@@ -328,3 +328,106 @@ def test_refusals():
     opt.state[p]["momentum"] = torch.zeros(80, 160, device="cuda")
     with pytest.raises(ValueError):
         opt.step()
+
+
+def beyond_rounding(p, x):
+    """How far p is from -x beyond its own type's rounding, of each element."""
+    u = 2.0 ** -8 if p.dtype is torch.bfloat16 else 2.0 ** -24
+    return ((-p.detach().double() - x).abs() - u * x.abs()).clamp_min(0.0)
+
+
+def check_tight(grads, dtype, steps=5, **how):
+    """As check, but what is left beyond the parameter's own rounding is held to the bounds of two fp16 values for each
+    operand, or fp32, whatever the parameter's type."""
+    from qml_gradients_amd.optim import Muon
+    params = []
+    for g in grads:
+        params.append(torch.nn.Parameter(torch.zeros(g.shape, dtype=TYPES[dtype][0], device="cuda")))
+        params[-1].grad_dtype = None
+        params[-1].grad = g
+    Muon(params, lr=1.0, adjust="none", steps=steps, **how).step()
+    for p, g in zip(params, grads):
+        _, u = muon(p, g, torch.zeros(g.shape, device="cuda"), 1.0, 0.95, 0.0, True, 1.0)
+        x, norm_bound, most = orthogonal_bound(u, "fp32", steps)
+        off = beyond_rounding(p, x)
+        say(f"[gpu] muon {tuple(g.shape)} {g.dtype} for {dtype}: off {float(torch.linalg.vector_norm(off)):.2e} ({norm_bound:.2e}), "
+            f"largest {float(off.max()):.2e} ({most:.2e})")
+        assert float(torch.linalg.vector_norm(off)) <= norm_bound and float(off.max()) <= most
+
+
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+@pytest.mark.parametrize("sizes", [[(300, 200), (100, 700)], [(640, 2100), (2100, 640)], [(1500, 1400)], [(200, 6000)]])
+def test_updates_of_bf16_parameters(sizes, grad):
+    check_tight([gradient(r, c, n, grad) for n, (r, c) in enumerate(sizes)], "bf16")
+
+
+@pytest.mark.parametrize("sizes", [(512, 2048), (300, 200), (2048, 512), (64, 5000)])
+def test_updates_of_bf16_parameters_from_few_directions(sizes):
+    """Eight directions, as a batch of eight gives: roundings of operands would be lifted in all the others."""
+    r, c = sizes
+    g = torch.Generator(device="cuda").manual_seed(1)
+    check_tight([torch.randn(r, 8, generator=g, device="cuda") @ torch.randn(8, c, generator=g, device="cuda")], "bf16")
+
+
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+@pytest.mark.parametrize("sizes", [[(300, 200), (8, 16), (64, 2000)], [(517, 803)], [(1000, 1030)], [(640, 2100), (2100, 640)],
+                                   [(3000, 3000)] * 2, [(200, 6000), (6000, 200)], [(70 + n, 90 + 2 * n) for n in range(30)]])
+def test_half(sizes, grad, monkeypatch):
+    """One fp16 value an operand, within the bounds of that; the largest tiles, their leftovers and parts along k."""
+    from qml_gradients_amd import optim
+
+    class Half(optim.Muon):
+        def __init__(self, params, **how):
+            super().__init__(params, half=True, **how)
+
+    monkeypatch.setattr(optim, "Muon", Half)
+    check(sizes, "bf16", grad, seed=3)
+
+
+def test_half_is_of_bf16_parameters():
+    """Parameters in 32 bits do not know it; a group has it or not."""
+    from qml_gradients_amd.optim import Muon
+    a, b = matrices([(100, 90)]), matrices([(100, 90)])
+    Muon(a, half=True).step(), Muon(b).step()
+    assert torch.equal(a[0], b[0])
+    c, d, e = (matrices([(100, 90)], "bf16", "fp32", zero=True) for _ in range(3))
+    Muon([dict(params=c, half=True), dict(params=d)], lr=1.0).step()
+    Muon(e, lr=1.0).step()
+    assert torch.equal(d[0], e[0]) and not torch.equal(c[0], e[0])
+
+
+def test_states_saved_without_half():
+    from qml_gradients_amd.optim import Muon
+    a, b = matrices([(30, 20)], "bf16"), matrices([(30, 20)], "bf16")
+    x, y = Muon(a), Muon(b, half=True)
+    x.step()
+    state = x.state_dict()
+    for group in state["param_groups"]:
+        del group["half"]
+    y.load_state_dict(state)
+    assert y.param_groups[0]["half"] is False
+    y.step()
+
+
+def test_graph_and_streams_of_bf16_parameters():
+    """Both precisions: a captured step repeats the step, eager ones on another stream between its replays."""
+    from qml_gradients_amd.optim import Muon
+    for half in (False, True):
+        sizes = [(300, 420), (128, 200), (2100, 2200)]
+        a, b = matrices(sizes, "bf16"), matrices(sizes, "bf16")
+        x, y = Muon(a, half=half), Muon(b, half=half)
+        x.step(), y.step()
+        torch.cuda.synchronize()
+        graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        with torch.cuda.graph(graph, stream=side):
+            x.step()
+        for seed in (1, 2, 3):
+            for n, (p, q) in enumerate(zip(a, b)):
+                new = gradient(*p.shape, 30 * seed + n, "bf16")
+                p.grad.copy_(new), q.grad.copy_(new)
+            graph.replay()
+            torch.cuda.synchronize()
+            with torch.cuda.stream(side):
+                y.step()
+            torch.cuda.synchronize()
+            assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -285,3 +285,15 @@ def test_muon_states_that_do_not_fit_are_refused(calls):
     opt.state[p]["momentum"] = torch.zeros(4, 6)
     opt.step()
     assert not calls
+
+
+def test_muon_workspace_of_precise_products():
+    """Two fp16 values for each operand of bf16 parameters take the workspace of fp32 parameters."""
+    _lib()
+    t = (hq.hqml_muon_tensor * 1)(hq.hqml_muon_tensor(None, None, None, 1024, 4096, 1.0))
+    joins = (64 << 20) + (16 << 10)
+    wide = hq.hqml_muon_workspace_bytes(_muon(), 1, t)
+    precise = _muon(param_dtype=1)
+    precise.precise = 1
+    assert hq.hqml_muon_workspace_bytes(precise, 1, t) == wide
+    assert hq.hqml_muon_workspace_bytes(_muon(param_dtype=1), 1, t) - joins < 0.6 * (wide - joins)
