@@ -187,8 +187,8 @@ __device__ __forceinline__ void to_planes(float v, Half &hi, Half &lo)
 
 __device__ __forceinline__ float from_half(Half h) { return (float)__builtin_bit_cast(_Float16, h.u); }
 
-// 1 / max(|u|, eps); NaN where |u| is.
-__device__ __forceinline__ float inverse_norm(const Matrix &t, float eps)
+// 1 / max(|u|, eps), in 64 bits: 32 do not hold it for the least eps.  NaN where |u| is.
+__device__ __forceinline__ double inverse_norm(const Matrix &t, float eps)
 {
     __shared__ double part[4];
     const int chunks = (int)(((long long)t.rows * t.cols + kChunk - 1) / kChunk);
@@ -198,7 +198,7 @@ __device__ __forceinline__ float inverse_norm(const Matrix &t, float eps)
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
     __syncthreads();
     const double norm = sqrt(part[0] + part[1] + part[2] + part[3]);
-    return (float)(1.0 / (norm <= (double)eps ? (double)eps : norm));
+    return 1.0 / (norm <= (double)eps ? (double)eps : norm);
 }
 
 // X, normalised, in rows of a multiple of eight that end with zeros.
@@ -207,7 +207,7 @@ __global__ __launch_bounds__(256) void k_begin(Batch batch, Scalars k)
 {
     const int ti = matrix_of(batch.first, batch.count, blockIdx.x);
     const Matrix &t = batch.t[ti];
-    const float inv = inverse_norm(t, k.eps) * kScale;
+    const double inv = inverse_norm(t, k.eps) * kScale;
     const int ld = (t.cols + 7) & ~7, eights = ld / 8;
     const long long n = (long long)t.rows * eights, plane = (long long)t.rows * ld;
     const unsigned groups = (ti + 1 < batch.count ? batch.first[ti + 1] : gridDim.x) - batch.first[ti];
@@ -227,7 +227,8 @@ __global__ __launch_bounds__(256) void k_begin(Batch batch, Scalars k)
                 if (c + e < t.cols) mv[e] = t.m[at + e], gv[e] = g[at + e];
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) to_planes(c + e < t.cols ? update_of(k, mv[e], widen(gv[e])) * inv : 0.0f, hi[e], lo[e]);
+        for (int e = 0; e < 8; ++e)
+            to_planes(c + e < t.cols ? (float)(update_of(k, mv[e], widen(gv[e])) * inv) : 0.0f, hi[e], lo[e]);
         *(u32x4 *)(t.x[0] + (long long)row * ld + c) = __builtin_bit_cast(u32x4, hi);
         if (PLANES == 2) *(u32x4 *)(t.x[0] + plane + (long long)row * ld + c) = __builtin_bit_cast(u32x4, lo);
     }
@@ -762,8 +763,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_small(Batch batch, Scalars k, in
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) sum += part[w];
     const double norm = sqrt(sum);
-    const float inv = (float)(1.0 / (norm <= (double)k.eps ? (double)k.eps : norm));
-    for (int i = threadIdx.x; i < z.n * z.ldx; i += kThreads) X[i] *= inv;
+    const double inv = 1.0 / (norm <= (double)k.eps ? (double)k.eps : norm);   // beyond 32 bits for the least eps
+    for (int i = threadIdx.x; i < z.n * z.ldx; i += kThreads) X[i] = (float)(X[i] * inv);
     __syncthreads();
     switch (z.n / 16) {
     case 1: small_steps<1, WAVES>(z, k, steps, X, A, B, P); break;

@@ -431,3 +431,21 @@ def test_graph_and_streams_of_bf16_parameters():
                 y.step()
             torch.cuda.synchronize()
             assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("sizes", [[(20, 30)], [(300, 200)], [(20, 3000)]])
+def test_least_eps(sizes, dtype):
+    """The least eps there is: zeros only decay, and gradients whose norm is around 2^-118 give the update of their direction."""
+    from qml_gradients_amd.optim import Muon
+    params = matrices(sizes * 2, dtype)
+    before = [p.detach().clone() for p in params]
+    params[0].grad.zero_()
+    with torch.no_grad():
+        params[1].zero_()
+    params[1].grad.copy_(gradient(*sizes[0], 3, dtype).double() * 2.0 ** -118)
+    Muon(params, lr=1.0, momentum=0.0, weight_decay=0.125, adjust="none", eps=2.0 ** -149).step()
+    assert torch.equal(params[0], before[0] * 0.875)
+    x, norm_bound, most = orthogonal_bound(params[1].grad, dtype, eps=2.0 ** -149)
+    off = beyond_rounding(params[1], x)
+    assert float(torch.linalg.vector_norm(off)) <= norm_bound and float(off.max()) <= most
