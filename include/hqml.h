@@ -342,7 +342,8 @@ const char *hqml_dense8_last_error(const hqml_dense8 *h);
 
 /* y = alpha act(x w^T + bias) + residual with x rounded to codes for each row and w given as
  * codes [N][K] with row stride ldw as hqml_quantise_rows takes it (what its rows hold past K does
- * not count, up to the next multiple of 16 it is read) and scales [N].  Everything else as
+ * not count, up to the next multiple of 16 it is read) and scales [N] (at least 2^-100, as it gives them;
+ * below, results lose bits).  A product of scales may leave fp32's range where a result does not.  Everything else as
  * hqml_dense_forward; there is no gradient.  Sums of products of codes are exact.  A row of
  * x that is not finite gives a row of NaN. */
 int hqml_dense8_forward(hqml_dense8 *h, int M, const void *x, long long ldx, const signed char *codes,

@@ -242,16 +242,35 @@ hipError_t quantise(const void *x, long long ldx, long long rows, int K, int8_t 
 
 // ---- the product ----
 
+// The scale of a row of x, as a value and a power of two.  The product of two scales may leave fp32's range where its product with
+// a sum (or a sum of 0) does not.  Scales lie between 2^-100 and 2^121.1, so this one's fraction times 2^-25, from 2^-26 on, with
+// one of w's is normal (2^-126 to 2^96.1) and, times a sum below 2^31, finite; the power goes into the result at once: the same bits
+// where nothing overflows, one rounding below the normal range.
+struct Scale {
+    float part;
+    int power;
+};
+
+__device__ __forceinline__ Scale split(float scale)
+{
+    return {__builtin_amdgcn_frexp_mantf(scale) * 0x1p-25f, __builtin_amdgcn_frexp_expf(scale) + 25};
+}
+
+__device__ __forceinline__ float scaled(int sum, const Scale &x, float w)
+{
+    return __builtin_amdgcn_ldexpf((float)sum * (x.part * w), x.power);
+}
+
 // Sums of codes' products as fp32 values: scaled by their row and column.
 template <int FI, int FJ>
 __device__ __forceinline__ void scaled(f32x4 (&to)[FI][FJ], const i32x4 (&acc)[FI][FJ], const Args &P, const Scales8 &q, int i0, int j0)
 {
     const int lane = threadIdx.x & 63;
-    float sx[FI];
+    Scale sx[FI];
 #pragma unroll
     for (int f = 0; f < FI; ++f) {
         const int i = i0 + f * 16 + (lane & 15);
-        sx[f] = i < P.I ? q.x[i] : 0.0f;
+        sx[f] = split(i < P.I ? q.x[i] : 0.0f);
     }
 #pragma unroll
     for (int g = 0; g < FJ; ++g) {
@@ -262,7 +281,7 @@ __device__ __forceinline__ void scaled(f32x4 (&to)[FI][FJ], const i32x4 (&acc)[F
 #pragma unroll
         for (int f = 0; f < FI; ++f)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) to[f][g][k] = (float)acc[f][g][k] * (sx[f] * sw[k]);
+            for (int k = 0; k < 4; ++k) to[f][g][k] = scaled(acc[f][g][k], sx[f], sw[k]);
     }
 }
 
@@ -325,7 +344,7 @@ __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small8(Args P, Scales8
             }
     }
     small_finish<T, FI, true>(P, acc, blockIdx.x, i0, j0, small_lds,
-                              [&](int sum, int i, int j) { return (float)sum * (q.x[i] * q.w[j]); });
+                              [&](int sum, int i, int j) { return scaled(sum, split(q.x[i]), q.w[j]); });
 }
 
 constexpr int kOwnHeld = 2;   // sixteens of a thread's
@@ -410,7 +429,7 @@ __global__ __launch_bounds__(1024) void k_small8_own(Args P, Scales8 q, int K)
     small_finish<T, 1, true>(P, acc, blockIdx.x, i0, j0, sums, [&](int sum, int i, int j) {
         float scale;
         (void)row_scale(largest[i - i0], scale);
-        return (float)sum * (scale * q.w[j]);
+        return scaled(sum, split(scale), q.w[j]);
     });
 }
 

@@ -325,3 +325,30 @@ def test_two_handles_at_once():
                 got.append(layers[n].forward(x[n], *w[n]))
     torch.cuda.synchronize()
     assert all(excess(y, want[i % 2]) <= 0 for i, y in enumerate(got))
+
+
+def scaled_rows(rows, cols, size, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return (torch.randn(rows, cols, generator=g, device="cuda").double() * size).float()
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 784, 20), (3, 1000, 70), (45, 1531, 803), (300, 1021, 517), (2100, 640, 2060)])
+@pytest.mark.parametrize("sx,sw", [(1e-20, 1e-20), (1e22, 1e22), (1e-25, 1e28), (1e30, 1e-28), (1e35, 1e-29), (1e-29, 1e35), (1e37, 1e20)])
+def test_scales_of_any_size(M, K, N, sx, sw):
+    """The scales' product may leave fp32's range where the result does not, or where the sum is 0.  Bounds as ever, with half a
+    unit of the smallest numbers, 2^-150, for results below the normal range; infinite where the value rounded to fp32 is."""
+    import qml_gradients_amd as hq
+    x, w = scaled_rows(M, K, sx, 1), scaled_rows(N, K, sw, 2)
+    w[0] = 0.0
+    w[1] = 0.0
+    w[1, 0] = 1000 * sw   # and x's first values are zero: a sum of 0 of rows that are not
+    x[:, 0] = 0.0
+    codes, scales = hq.quantise_rows(w)
+    y = hq.DenseInt8(K, N, M).forward(x, codes, scales)
+    value, bound = dense8(x, codes, scales, None, None, "none", 1.0, "fp32")
+    top = torch.finfo(torch.float32).max
+    above, below = value.abs() > 1.001 * top, value.abs() < 0.999 * top
+    assert (y[:, :2] == 0).all() and not y.isnan().any()
+    assert y[above].isinf().all() and (torch.sign(y[above]) == torch.sign(value[above])).all()
+    off = (y.double() - value).abs() - bound - 2.0 ** -150
+    assert float(off[below].max()) <= 0
