@@ -14,6 +14,7 @@ from __future__ import annotations
 import math
 
 import torch
+from torch.autograd.forward_ad import unpack_dual
 
 from . import Context, Dense, DenseInt8, GroupNorm, quantise_rows
 
@@ -119,7 +120,8 @@ class DenseLayer(torch.nn.Module):
 class DenseInt8Layer(torch.nn.Module):
     """A dense layer served in 8-bit integers: y = alpha act(x w^T + bias) + residual over the last axis of x, with the
     weights held as int8 codes [out_features][in_features] and a scale for each output channel.  `of` makes one of a
-    trained DenseLayer; codes, scales and bias are buffers.  There is no gradient: an input that wants one is refused."""
+    trained DenseLayer; codes, scales and bias are buffers.  There is no gradient: an input that wants one, or has a tangent, is
+    refused."""
 
     def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0, bias=True,
                  device=None):
@@ -146,8 +148,11 @@ class DenseInt8Layer(torch.nn.Module):
         return made
 
     def forward(self, x, residual=None):
-        if torch.is_grad_enabled() and (x.requires_grad or (residual is not None and residual.requires_grad)):
+        given = [t for t in (x, residual, self.scales, self.bias) if t is not None]
+        if torch.is_grad_enabled() and any(t.requires_grad for t in given):
             raise RuntimeError("a dense layer in 8-bit integers has no gradient: call it under torch.no_grad()")
+        if any(unpack_dual(t).tangent is not None for t in given):
+            raise RuntimeError("a dense layer in 8-bit integers has no forward-mode derivative")
         lead = x.shape[:-1]
         x = x.reshape(-1, x.shape[-1])
         if residual is not None:

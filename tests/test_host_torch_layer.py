@@ -90,3 +90,37 @@ def test_a_trace_holds_the_call(layer):
     x = torch.randn(4, 5)
     assert "DenseFunction" in str(traced.graph) or "PythonOp" in str(traced.graph)
     assert torch.allclose(traced(x), plain(layer, x), atol=1e-6)
+
+
+class PlainInt8:
+    """Stands in for DenseInt8, as PlainDense does for Dense."""
+
+    def __init__(self, in_features, out_features, max_batch, dtype="fp32", activation="none", alpha=1.0, device=None):
+        self.device, self.dtype = torch.device("cpu"), torch.float32
+
+    def forward(self, x, codes, scales, bias=None, residual=None):
+        y = (x.detach() @ codes.float().t()) * scales.detach() + (0.0 if bias is None else bias.detach())
+        return y if residual is None else y + residual.detach()
+
+
+def test_8_bit_layer_refuses_what_wants_a_derivative(monkeypatch):
+    """Of any argument, backward or forward mode; a tangent also where gradients are off."""
+    from torch.autograd import forward_ad
+    monkeypatch.setattr(torch_layer, "DenseInt8", PlainInt8)
+    monkeypatch.setattr(torch_layer, "quantise_rows", lambda w: (w.to(torch.int8), torch.ones(w.shape[0])))
+    layer = torch_layer.DenseInt8Layer(5, 3, 16)
+    x, r = torch.randn(2, 4, 5), torch.randn(2, 4, 3)
+    want = layer(x, r)
+    with forward_ad.dual_level():
+        assert torch.equal(layer(x, r), want)
+        for a, b in ((forward_ad.make_dual(x, x), r), (x, forward_ad.make_dual(r, r)), (forward_ad.make_dual(x, x), None)):
+            for on in (True, False):
+                with torch.set_grad_enabled(on), pytest.raises(RuntimeError, match="forward-mode"):
+                    layer(a, b)
+    for t in (x, r, layer.bias, layer.scales):
+        t.requires_grad_(True)
+        with pytest.raises(RuntimeError, match="no gradient"):
+            layer(x, r)
+        with torch.no_grad():
+            assert torch.equal(layer(x, r), want)
+        t.requires_grad_(False)
