@@ -68,6 +68,7 @@ struct Norm {
     float eps;
     float *part;        // backward: partial sums [rows][2][C] of dbeta and dgamma; null: the only workgroup of a span writes those
     void *dgamma, *dbeta;
+    int add;            // whether they are added to what an earlier launch left there
     int rows, extra;
     int ahead;          // rows that hold a thread's channels at least
     Map map;
@@ -412,9 +413,14 @@ __device__ __forceinline__ void parameter_sums(const Norm &P, const Place &p, co
         for (int l = lane; l < down; l += each) sum += lds[q * T_ * V + l * pitch + c];
         sum = lanes_sum(sum, each);
         if (lane) continue;
-        if (P.part) P.part[(row * 2 + q) * P.C + c0 + c] = sum;
-        else if (q && P.dgamma) narrow(sum, ((T *)P.dgamma)[c0 + c]);
-        else if (!q && P.dbeta) narrow(sum, ((T *)P.dbeta)[c0 + c]);
+        if (P.part) {
+            float *to = P.part + (row * 2 + q) * P.C + c0 + c;
+            *to = P.add ? *to + sum : sum;
+        } else if (q && P.dgamma) {
+            narrow(sum, ((T *)P.dgamma)[c0 + c]);
+        } else if (!q && P.dbeta) {
+            narrow(sum, ((T *)P.dbeta)[c0 + c]);
+        }
     }
 }
 
@@ -877,6 +883,11 @@ constexpr int kUnits = 256;          // compute units
 // 106 / 110 / 122).
 constexpr int kSplitGroups = 512;
 constexpr int kSampleChunks = 256;   // chunks of a sample, at most
+// Workspace of the samples that are split at once, and how many they are at least; more go in rounds, whose ends leave compute units
+// idle: rounds of 2,000 samples, 82 MB of x, cost 6 to 10 % (4000 x 5 x 4096 bf16 forward 134 / 144 us, backward 339 / 360), of 1,334
+// 24 % (166) and 11 % (377).  Without rounds that call's workspace is 0.8 of x, with one channel a group 2.4.
+constexpr size_t kRoundBytes = 64ull << 20;
+constexpr int kRoundSamples = 2048;
 // Workgroups of a span in a resident pass, of up to 256 threads; others: a third.  Backward fewer, since each leaves sums of all
 // parameters (1000 x 784 fp32 forward 768 / 1024: 10.2 / 9.6 us; 3000 x 4 x 96 fp32 backward 12.3 / 15.3).
 constexpr int kResidentForward = 1024, kResidentBackward = 768;
@@ -997,9 +1008,9 @@ Norm common(const NormCall &a, int V)
     return P;
 }
 
-// Cuts a split call; the threads of its workgroups.
+// Cuts a split call whose rounds have up to `samples`; the threads of its workgroups.
 template <typename T>
-int cut(Norm &P, const NormWorkspace &ws)
+int cut(Norm &P, const NormWorkspace &ws, int samples)
 {
     Map &m = P.map;
     m.width = P.C;
@@ -1011,9 +1022,9 @@ int cut(Norm &P, const NormWorkspace &ws)
     complete<T>(m, split_threads<T>(P.C));
     // kSplitGroups chunks in all or, where those leave compute units with one more than others, up to twice as many; of one size,
     // and no more of a sample than its last workgroup joins quickly
-    int most = std::max(1, kSplitGroups / P.B);
-    auto rounds = [&](int n) { return (float)ceil_div((long long)P.B * n, kUnits) / (float)n; };
-    for (int n = most + 1; n <= 2 * kSplitGroups / P.B; ++n)
+    int most = std::max(1, kSplitGroups / samples);
+    auto rounds = [&](int n) { return (float)ceil_div((long long)samples * n, kUnits) / (float)n; };
+    for (int n = most + 1; n <= 2 * kSplitGroups / samples; ++n)
         if (rounds(n) < 0.9f * rounds(most)) most = n;
     most = std::min(most, kSampleChunks);
     P.chunk = std::min(P.S, std::max(m.lanes * kStep, ceil_div(P.S, most)));
@@ -1024,13 +1035,48 @@ int cut(Norm &P, const NormWorkspace &ws)
     return split_threads<T>(P.C);
 }
 
-// What a split call of up to `rows` positions in all takes at most: samples, and chunks of all of them.  A sample that is
-// split has more positions than any resident workgroup holds across all channels.
-template <typename T>
-void split_most(long long rows, int C, long long &samples, long long &chunks)
+// The most samples of a round: each has two sums a channel, two values a group of its own and of a chunk's, and a ticket.
+int round_samples(int C, int G)
 {
-    samples = rows / (split_lanes<T>(C) * kMostOf1024 + 1);
+    const size_t each = (2 * (size_t)C + 4 * (size_t)G + kTicketStep) * 4;
+    return std::max((int)(kRoundBytes / each), kRoundSamples);
+}
+
+// What a round of a split call of up to `rows` positions in all takes at most: samples, and chunks of all of them.  A sample that
+// is split has more positions than any resident workgroup holds across all channels.
+template <typename T>
+void split_most(long long rows, int C, int G, long long &samples, long long &chunks)
+{
+    samples = std::min<long long>(rows / (split_lanes<T>(C) * kMostOf1024 + 1), round_samples(C, G));
     chunks = samples ? std::max<long long>(2 * kSplitGroups, samples) : 0;
+}
+
+// The samples of a call from b on, n of them.
+template <typename T>
+NormCall samples_of(const NormCall &a, int b, int n)
+{
+    NormCall c = a;
+    const long long at = (long long)b * a.S, g = (long long)b * a.G;
+    auto from = [&](const void *p, long long ld) { return p ? (void *)((T *)p + at * ld) : nullptr; };
+    c.B = n;
+    c.x = from(a.x, a.ldx), c.dy = from(a.dy, a.lddy);
+    c.y = from(a.y, a.ldy), c.dx = from(a.dx, a.lddx);
+    if (a.mean) c.mean += g, c.rstd += g;
+    return c;
+}
+
+// Calls f(samples, first, last) for the rounds of a call, which are of one size up to the last.
+template <typename T, typename F>
+hipError_t in_rounds(const NormCall &a, F f)
+{
+    const int each = ceil_div(a.B, ceil_div(a.B, round_samples(a.C, a.G)));
+    for (int b = 0; b < a.B;) {
+        const int n = std::min(each, a.B - b);
+        const hipError_t e = f(samples_of<T>(a, b, n), b == 0, b + n == a.B);
+        if (e != hipSuccess) return e;
+        b += n;
+    }
+    return hipSuccess;
 }
 
 bool fits(const Norm &P, const NormWorkspace &ws, bool parameters)
@@ -1057,15 +1103,20 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
         else k_resident_forward<T, kMostForward<T>, 512><<<grid, r.threads, lds, s>>>(P);
         return hipGetLastError();
     }
-    const int threads = cut<T>(P, ws);
-    if (!fits(P, ws, false)) return hipErrorInvalidValue;
-    if (!P.mean) P.mean = ws.group, P.rstd = ws.group + (size_t)a.B * a.G;
-    const unsigned grid = (unsigned)a.B * (unsigned)P.chunks;
-    k_stats<T><<<grid, threads, lds_bytes(threads, kVec<T>, a.G), s>>>(P);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    k_apply_forward<T><<<grid, threads, 0, s>>>(P);
-    return hipGetLastError();
+    int most = 0;   // samples of a round
+    return in_rounds<T>(a, [&](const NormCall &c, bool first, bool) {
+        if (first) most = c.B;
+        Norm P = common(c, kVec<T>);
+        const int threads = cut<T>(P, ws, most);
+        if (!fits(P, ws, false)) return hipErrorInvalidValue;
+        if (!P.mean) P.mean = ws.group, P.rstd = ws.group + (size_t)c.B * c.G;
+        const unsigned grid = (unsigned)c.B * (unsigned)P.chunks;
+        k_stats<T><<<grid, threads, lds_bytes(threads, kVec<T>, c.G), s>>>(P);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        k_apply_forward<T><<<grid, threads, 0, s>>>(P);
+        return hipGetLastError();
+    });
 }
 
 template <typename T>
@@ -1094,20 +1145,28 @@ hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
         k_parameters<T><<<blocks, 512, 0, s>>>(P);
         return hipGetLastError();
     }
-    const int threads = cut<T>(P, ws);
-    if (!fits(P, ws, parameters)) return hipErrorInvalidValue;
-    const unsigned grid = (unsigned)a.B * (unsigned)P.chunks;
-    if (parameters) P.rows = (int)grid, P.part = ws.part + (size_t)grid * 2 * a.G;
-    k_sums<T><<<grid, threads, lds_bytes(threads, kVec<T>, a.G), s>>>(P);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if (a.dx) {
-        P.extra = parameters ? blocks : 0;
-        k_apply_backward<T><<<grid + P.extra, threads, 0, s>>>(P);
-    } else {   // as many threads: the sums' order, and so their last bit, is the same
-        k_parameters<T><<<blocks, threads, 0, s>>>(P);
-    }
-    return hipGetLastError();
+    int most = 0, rows = 0;   // samples of a round, its partial sums of parameters
+    return in_rounds<T>(a, [&](const NormCall &c, bool first, bool last) {
+        if (first) most = c.B;
+        Norm P = common(c, kVec<T>);
+        P.dgamma = a.dgamma, P.dbeta = a.dbeta;
+        const int threads = cut<T>(P, ws, most);
+        if (!fits(P, ws, parameters)) return hipErrorInvalidValue;
+        const unsigned grid = (unsigned)c.B * (unsigned)P.chunks;
+        if (first) rows = (int)grid;   // no later round has more
+        if (parameters) P.rows = rows, P.part = ws.part + (size_t)rows * 2 * a.G, P.add = !first;
+        k_sums<T><<<grid, threads, lds_bytes(threads, kVec<T>, c.G), s>>>(P);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const bool reduce = parameters && last;
+        if (c.dx) {
+            P.extra = reduce ? blocks : 0;
+            k_apply_backward<T><<<grid + P.extra, threads, 0, s>>>(P);
+        } else if (reduce) {   // as many threads: the sums' order, and so their last bit, is the same
+            k_parameters<T><<<blocks, threads, 0, s>>>(P);
+        }
+        return hipGetLastError();
+    });
 }
 
 // More dynamic LDS than 64 KB has to be allowed.
@@ -1131,7 +1190,7 @@ NormWorkspace workspace(const hqml_norm_config &c)
 {
     NormWorkspace ws;
     long long samples, chunks;
-    split_most<T>(c.max_rows, c.channels, samples, chunks);
+    split_most<T>(c.max_rows, c.channels, c.groups, samples, chunks);
     const size_t C = (size_t)c.channels, G = (size_t)c.groups;
     ws.part_bytes = std::max((size_t)chunks * (2 * G + 2 * C), std::min<size_t>(kResidentBackward, (size_t)c.max_rows) * 2 * C) * 4;
     ws.group_bytes = (size_t)samples * G * 8;

@@ -322,3 +322,10 @@ def test_refusals():
         with pytest.raises(hq.HqmlError) as e:
             backward(**bad)
         assert e.value.status == hq.HQML_ERR_ARG, bad
+
+
+@pytest.mark.parametrize("B,S,C,G,dtype", [(2500, 5, 4096, 64, "bf16"), (4200, 6, 2100, 2100, "bf16"), (1100, 20, 2048, 4, "fp32"),
+                                           (2300, 700, 24, 3, "bf16"), (600, 2100, 16, 4, "fp32")])
+def test_many_samples_that_are_split(B, S, C, G, dtype):
+    """More samples than go together, on a handle made for exactly so many positions."""
+    check(B, S, C, G, dtype, "silu")

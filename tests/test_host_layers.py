@@ -297,3 +297,15 @@ def test_muon_workspace_of_precise_products():
     precise.precise = 1
     assert hq.hqml_muon_workspace_bytes(precise, 1, t) == wide
     assert hq.hqml_muon_workspace_bytes(_muon(param_dtype=1), 1, t) - joins < 0.6 * (wide - joins)
+
+
+@pytest.mark.parametrize("C,G,dtype", [(4096, 32, "bf16"), (4096, 4096, "bf16"), (2048, 32, "bf16"), (1024, 1, "fp32"), (784, 16, "fp32"),
+                                       (24, 3, "bf16"), (1, 1, "fp32")])
+def test_norm_workspace_does_not_grow_with_samples(C, G, dtype):
+    """Each sample that goes with others has two sums a channel, two values a group of its own and two of its chunks', and a
+    counter's cache line: 2,048 samples, or more in up to 64 MiB; 2^30 positions take no more.  The kernels of small samples
+    leave up to 768 rows of two sums a channel."""
+    _lib()
+    sizes = [hq.hqml_norm_workspace_bytes(hq.make_norm_config(C, G, rows, dtype=dtype)) for rows in (1 << 10, 1 << 20, 1 << 30)]
+    most = max(2048 * (4 * (2 * C + 4 * G) + 128), 64 << 20) + 768
+    assert 0 < sizes[0] <= sizes[1] <= sizes[2] <= most
