@@ -713,6 +713,21 @@ __global__ __launch_bounds__(1024) void k_apply_forward(Norm P)
 
 constexpr int kStepBack = 4;
 
+// Sums of a thread: after so many steps they go to LDS and begin anew, so that no chain of additions grows with the sample (2^28
+// positions of one channel, 4,096 of a thread: equal values off by 6.1e-5, so by 1e-6).
+constexpr int kSegment = 32;
+
+// What a thread has put into LDS, if any, is added to its sums.
+template <int V>
+__device__ __forceinline__ void add_held(float (&s)[2][V], const float *lds, bool held)
+{
+    if (!held) return;
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[q][e] += lds[(q * V + e) * blockDim.x + threadIdx.x];
+}
+
 // The sums behind a chunk's gradients: by channel to `part`, by group, with gamma, joined by the sample's last workgroup.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_sums(Norm P)
@@ -737,26 +752,38 @@ __global__ __launch_bounds__(1024) void k_sums(Norm P)
         rstd[e] = e < p.n ? P.rstd[g] : 0.0f;
         scale[e] = rstd[e] * gamma[e];
     }
-    for (int r0 = s0 + p.row; r0 < s1 && p.n; r0 += kStepBack * m.lanes) {
-        u32x4 w[kStepBack], d[kStepBack];
+    bool held = false;
+    for (int r0 = s0 + p.row; p.n;) {
+        const int end = s1 - r0 < kSegment * kStepBack * m.lanes ? s1 : r0 + kSegment * kStepBack * m.lanes;
+        for (; r0 < end; r0 += kStepBack * m.lanes) {
+            u32x4 w[kStepBack], d[kStepBack];
 #pragma unroll
-        for (int k = 0; k < kStepBack; ++k) {
-            const int row = r0 + k * m.lanes;
-            w[k] = d[k] = u32x4{0, 0, 0, 0};
-            if (row < s1) {
-                w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond);
-                d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n, row < beyond);
+            for (int k = 0; k < kStepBack; ++k) {
+                const int row = r0 + k * m.lanes;
+                w[k] = d[k] = u32x4{0, 0, 0, 0};
+                if (row < s1) {
+                    w[k] = get<T, V>(x + (long long)row * P.ldx, p.n, row < beyond);
+                    d[k] = get<T, V>(dy + (long long)row * P.lddy, p.n, row < beyond);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kStepBack; ++k) {
+                if (r0 + k * m.lanes >= s1) continue;
+                float dz[V], far[V];
+                gradient_at<T, V>(dz, far, w[k], d[k], mean, scale, beta, P.act);
+#pragma unroll
+                for (int e = 0; e < V; ++e) s[0][e] += dz[e], s[1][e] = __builtin_fmaf(dz[e], far[e], s[1][e]);
             }
         }
+        if (r0 >= s1) break;
+        add_held<V>(s, norm_lds, held);
+        held = true;
 #pragma unroll
-        for (int k = 0; k < kStepBack; ++k) {
-            if (r0 + k * m.lanes >= s1) continue;
-            float dz[V], far[V];
-            gradient_at<T, V>(dz, far, w[k], d[k], mean, scale, beta, P.act);
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int e = 0; e < V; ++e) s[0][e] += dz[e], s[1][e] = __builtin_fmaf(dz[e], far[e], s[1][e]);
-        }
+            for (int e = 0; e < V; ++e) norm_lds[(q * V + e) * blockDim.x + threadIdx.x] = s[q][e], s[q][e] = 0.0f;
     }
+    add_held<V>(s, norm_lds, held);
 #pragma unroll
     for (int e = 0; e < V; ++e) s[1][e] *= rstd[e];
     if (P.part) parameter_sums<T, V>(P, p, s, 0, P.C, (long long)b * P.chunks + chunk, norm_lds);
@@ -891,6 +918,9 @@ constexpr int kRoundSamples = 2048;
 // Workgroups of a span in a resident pass, of up to 256 threads; others: a third.  Backward fewer, since each leaves sums of all
 // parameters (1000 x 784 fp32 forward 768 / 1024: 10.2 / 9.6 us; 3000 x 4 x 96 fp32 backward 12.3 / 15.3).
 constexpr int kResidentForward = 1024, kResidentBackward = 768;
+// Samples of a workgroup's sums in one launch, so that no chain of additions grows with the batch (2^20 x 2048 fp32, 2,048 samples of a
+// workgroup in one: equal values off by 2.9e-5, so by 1.6e-6).
+constexpr int kRun = 256;
 constexpr int kMinSegment = 64;      // bytes of a row that a span has at least, unless the array is small
 constexpr long long kSmallArray = 1 << 20;
 
@@ -1065,11 +1095,11 @@ NormCall samples_of(const NormCall &a, int b, int n)
     return c;
 }
 
-// Calls f(samples, first, last) for the rounds of a call, which are of one size up to the last.
+// Calls f(samples, first, last) for the rounds of a call, of at most `most` samples, of one size up to the last.
 template <typename T, typename F>
-hipError_t in_rounds(const NormCall &a, F f)
+hipError_t in_rounds(const NormCall &a, long long most, F f)
 {
-    const int each = ceil_div(a.B, ceil_div(a.B, round_samples(a.C, a.G)));
+    const int each = ceil_div(a.B, ceil_div(a.B, most));
     for (int b = 0; b < a.B;) {
         const int n = std::min(each, a.B - b);
         const hipError_t e = f(samples_of<T>(a, b, n), b == 0, b + n == a.B);
@@ -1104,7 +1134,7 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
         return hipGetLastError();
     }
     int most = 0;   // samples of a round
-    return in_rounds<T>(a, [&](const NormCall &c, bool first, bool) {
+    return in_rounds<T>(a, round_samples(a.C, a.G), [&](const NormCall &c, bool first, bool) {
         if (first) most = c.B;
         Norm P = common(c, kVec<T>);
         const int threads = cut<T>(P, ws, most);
@@ -1122,31 +1152,34 @@ hipError_t forward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 template <typename T>
 hipError_t backward(const NormCall &a, const NormWorkspace &ws, hipStream_t s)
 {
-    Norm P = common(a, kVec<T>);
-    P.dgamma = a.dgamma, P.dbeta = a.dbeta;
     const bool parameters = a.dgamma || a.dbeta;
     const int blocks = 2 * ceil_div(a.C, 8);   // of reduce_parameters
     const Resident r = resident<T>(a.B, a.S, a.C, a.G, kMostBackward<T>, kTogetherBackward);
     if (r.fits) {
-        P.map = r.map;
         const dim3 grid((unsigned)resident_groups(r, a.B, kResidentBackward), (unsigned)r.spans);
-        if (parameters && grid.x > 1) {
-            P.rows = (int)grid.x;
-            P.part = ws.part;
-            if ((size_t)P.rows * 2 * a.C * 4 > ws.part_bytes) return hipErrorInvalidValue;
-        }
-        const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
-        if (r.rows <= 1) k_resident_backward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
-        else if (r.threads > 512) k_resident_backward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
-        else if (r.rows <= 4) k_resident_backward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
-        else k_resident_backward<T, kMostBackward<T>, 512><<<grid, r.threads, lds, s>>>(P);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || !P.rows) return e;
-        k_parameters<T><<<blocks, 512, 0, s>>>(P);
-        return hipGetLastError();
+        return in_rounds<T>(a, (long long)kRun * grid.x * r.map.subs, [&](const NormCall &c, bool first, bool last) {
+            Norm P = common(c, kVec<T>);
+            P.dgamma = a.dgamma, P.dbeta = a.dbeta;
+            P.map = r.map;
+            if (parameters && grid.x > 1) {
+                P.rows = (int)grid.x;
+                P.part = ws.part;
+                P.add = !first;
+                if ((size_t)P.rows * 2 * a.C * 4 > ws.part_bytes) return hipErrorInvalidValue;
+            }
+            const size_t lds = lds_bytes(r.threads, kVec<T>, r.map.subs * r.map.groups);
+            if (r.rows <= 1) k_resident_backward<T, 1, 1024><<<grid, r.threads, lds, s>>>(P);
+            else if (r.threads > 512) k_resident_backward<T, kMostOf1024, 1024><<<grid, r.threads, lds, s>>>(P);
+            else if (r.rows <= 4) k_resident_backward<T, 4, 512><<<grid, r.threads, lds, s>>>(P);
+            else k_resident_backward<T, kMostBackward<T>, 512><<<grid, r.threads, lds, s>>>(P);
+            const hipError_t e = hipGetLastError();
+            if (e != hipSuccess || !P.rows || !last) return e;
+            k_parameters<T><<<blocks, 512, 0, s>>>(P);
+            return hipGetLastError();
+        });
     }
     int most = 0, rows = 0;   // samples of a round, its partial sums of parameters
-    return in_rounds<T>(a, [&](const NormCall &c, bool first, bool last) {
+    return in_rounds<T>(a, round_samples(a.C, a.G), [&](const NormCall &c, bool first, bool last) {
         if (first) most = c.B;
         Norm P = common(c, kVec<T>);
         P.dgamma = a.dgamma, P.dbeta = a.dbeta;

@@ -329,3 +329,18 @@ def test_refusals():
 def test_many_samples_that_are_split(B, S, C, G, dtype):
     """More samples than go together, on a handle made for exactly so many positions."""
     check(B, S, C, G, dtype, "silu")
+
+
+@pytest.mark.parametrize("B,S,C,value", [(1, 1 << 28, 1, 1.8811031579971313), (1 << 20, 1, 2048, 1.0028703212738037)])
+def test_long_sums(B, S, C, value):
+    """Sums of 2^28 positions, and of 2^20 samples, of equal values: chains of additions stay below 400, each off by at
+    most E of the sum.  One chain of a thread's 4,096 or 2,048 such values is off by 1,018 E or 485 E."""
+    import qml_gradients_amd as hq
+    x, dy = torch.ones(B, S, C, device="cuda"), torch.full((B, S, C), value, device="cuda")
+    mean, rstd = torch.zeros(B, 1, device="cuda"), torch.ones(B, 1, device="cuda")
+    layer = hq.GroupNorm(C, 1, B * S)
+    _, dw, db = layer.backward(dy, x, None, None, mean, rstd, input=False)
+    for t in (dw, db):
+        off = float((t.double() / (value * B * S) - 1).abs().max())
+        say(f"[gpu] long sums {B} x {S} x {C}: off {off:.2e}")
+        assert off < 400 * 2.0 ** -24
