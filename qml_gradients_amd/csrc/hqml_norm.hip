@@ -869,7 +869,7 @@ __global__ __launch_bounds__(1024) void k_apply_backward(Norm P)
         mean[e] = P.mean[g];
         const float rstd = P.rstd[g];
         scale[e] = rstd * gamma[e];   // dx = scale dz - one - (x - mean) two
-        one[e] = rstd * P.group[g * 2], two[e] = rstd * rstd * P.group[g * 2 + 1];
+        one[e] = rstd * P.group[g * 2], two[e] = rstd * (rstd * P.group[g * 2 + 1]);   // rstd^2 may overflow
     }
     for (int r0 = s0 + p.row; r0 < s1; r0 += kStepBack * m.lanes) {
         u32x4 w[kStepBack], d[kStepBack];

@@ -344,3 +344,24 @@ def test_long_sums(B, S, C, value):
         off = float((t.double() / (value * B * S) - 1).abs().max())
         say(f"[gpu] long sums {B} x {S} x {C}: off {off:.2e}")
         assert off < 400 * 2.0 ** -24
+
+
+@pytest.mark.parametrize("S", [5, 5000])
+def test_least_eps_of_constant_groups(S):
+    """rstd is up to 1 / sqrt(2^-149), whose square 32 bits do not hold: dx = rstd (dy - mean dy) all the same.  mean and rstd are
+    given, exactly: a forward pass's variance has the square of its mean's rounding in it, (2.5 2^-24)^2 = 2.2e-14 for one
+    rounding, beside which an eps of 2^-149 = 1.4e-45 does not show."""
+    import qml_gradients_amd as hq
+    layer = hq.GroupNorm(8, 2, S, eps=2.0 ** -149)
+    x = torch.full((1, S, 8), 2.5, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    dy = torch.randn(1, S, 8, generator=g, device="cuda")
+    rstd = torch.full((1, 2), 2.0 ** 74.5, device="cuda")
+    size = float(rstd[0, 0].double())
+    assert not layer.forward(x).any()
+    dx, dw, db = layer.backward(dy, x, None, None, torch.full_like(rstd, 2.5), rstd)
+    d = dy.double().view(1, S, 2, 4)
+    want = size * (d - d.mean((1, 3), keepdim=True)).view(1, S, 8)
+    # the mean's sum, 708 E of the magnitudes' mean, and 8 E of the terms
+    assert float((dx.double() - want).abs().max()) <= size * 2.0 ** -24 * (708 + 8 * 6) and not dw.any()
+    assert float((db.double() - dy.double().sum((0, 1))).abs().max()) <= 708 * 2.0 ** -24 * float(dy.abs().sum((0, 1)).max())
