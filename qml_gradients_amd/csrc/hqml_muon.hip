@@ -580,6 +580,12 @@ constexpr int kSmallLds = 160 * 1024 - 1024;
 constexpr int kSmallValues = 14 << 10;
 constexpr long long kSmallWork = 3 << 19;
 
+// Four waves a matrix where all of a launch have up to so many padded values, sixteen otherwise: barriers and joins of four cost less,
+// products of sixteen (us by four and sixteen: 16 x 16 7.8 and 8.5, 16 x 64 9.2 and 11.6, 32 x 32 10.8 and 13.3, 16 x 128 12.0 and 12.5,
+// 32 x 64 14.2 and 14.3, 32 x 128 22.3 and 17.7).  Matrices run beside each other, so the largest decides.
+constexpr int kTinyValues = 2048;
+static_assert(48 * 48 > kTinyValues, "matrices of three tiles of sixteen rows take sixteen waves");
+
 __host__ __device__ inline int pad16(int n) { return (n + 15) & ~15; }
 
 struct SmallSize {
@@ -769,8 +775,11 @@ __global__ __launch_bounds__(64 * WAVES) void k_small(Batch batch, Scalars k, in
     switch (z.n / 16) {
     case 1: small_steps<1, WAVES>(z, k, steps, X, A, B, P); break;
     case 2: small_steps<2, WAVES>(z, k, steps, X, A, B, P); break;
-    case 3: small_steps<3, WAVES>(z, k, steps, X, A, B, P); break;
-    default: small_steps<4, WAVES>(z, k, steps, X, A, B, P); break;
+    default:
+        if constexpr (WAVES == kSmallWaves) {   // those of three tiles have more than kTinyValues
+            if (z.n == 48) small_steps<3, WAVES>(z, k, steps, X, A, B, P);
+            else small_steps<4, WAVES>(z, k, steps, X, A, B, P);
+        }
     }
     each([&](int i, const float *x) {
         const float y = widen(p[i]);
@@ -1477,7 +1486,7 @@ hipError_t run(const hqml_muon_config &cfg, int n, const hqml_muon_tensor *t, ch
         for (int i = 0; i < few.count; ++i) {
             const SmallSize z(few.t[i].rows, few.t[i].cols);
             lds = std::max(lds, z.bytes());
-            tiny = tiny && z.n <= 32 && z.m <= 128;
+            tiny = tiny && z.n * z.m <= kTinyValues;
         }
         if (lds > 32 * 1024) {   // with what the kernel holds besides, more than a launch may take unasked
             e = hipFuncSetAttribute((const void *)k_small<T, G, kSmallWaves>, hipFuncAttributeMaxDynamicSharedMemorySize, kSmallLds);

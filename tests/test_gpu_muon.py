@@ -449,3 +449,9 @@ def test_least_eps(sizes, dtype):
     x, norm_bound, most = orthogonal_bound(params[1].grad, dtype, eps=2.0 ** -149)
     off = beyond_rounding(params[1], x)
     assert float(torch.linalg.vector_norm(off)) <= norm_bound and float(off.max()) <= most
+
+
+@pytest.mark.parametrize("sizes", [[(16, 128), (32, 64), (64, 17)], [(16, 129)], [(32, 65)], [(33, 33)], [(128, 20), (8, 8)], [(17, 64), (96, 32)]])
+def test_small_matrices_by_few_and_many_waves(sizes):
+    check(sizes, "fp32")
+    check(sizes, "bf16", "fp32", nesterov=False)
