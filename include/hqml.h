@@ -430,7 +430,9 @@ size_t hqml_muon_workspace_bytes(const hqml_muon_config *cfg, int n_tensors, con
  * some 2e-6 of its size, or, for bf16 parameters with precise == 0, one (11 bits): a third of the time and half of the workspace,
  * and X off by 1.5e-3, where a gradient has few directions by up to 4e-2; values of X, A or b A + c A^2 beyond 63
  * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Matrices
- * with a side of up to 64 are multiplied in fp32 or fp64 instead.  Matrices and workspace
+ * with a side of up to 64 are multiplied in fp32 or fp64 instead: those of up to 14,336 values always, longer ones
+ * as far as an error of A grows by less than 2^22 over the steps (six of the usual ones); with more steps only those that a
+ * compute unit holds, the others as larger matrices.  Matrices and workspace
  * must not overlap (HQML_ERR_ARG), but gradients may be shared.  The workspace is used until the step has run.
  * Errors: hqml_last_error(NULL). */
 int hqml_muon_step(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors,

@@ -455,3 +455,18 @@ def test_least_eps(sizes, dtype):
 def test_small_matrices_by_few_and_many_waves(sizes):
     check(sizes, "fp32")
     check(sizes, "bf16", "fp32", nesterov=False)
+
+
+@pytest.mark.parametrize("steps", [6, 7, 9])
+def test_long_matrices_of_bf16_parameters_with_many_steps(steps):
+    """Up to six steps by a polynomial in 64 bits, more by the large matrices' products; a matrix that a compute unit holds, in 32
+    bits, whatever the steps.  half takes 11 bits in the second case alone."""
+    sizes = [(64, 5000), (5000, 50), (40, 300)]
+    grads = [gradient(r, c, n, "bf16") for n, (r, c) in enumerate(sizes)]
+    check_tight(grads, "bf16", steps)
+    if steps == 6:
+        check_tight(grads, "bf16", steps, half=True)
+    else:
+        check_tight(grads[2:], "bf16", steps, half=True)
+        with pytest.raises(AssertionError):
+            check_tight(grads[:1], "bf16", steps, half=True)

@@ -309,3 +309,20 @@ def test_norm_workspace_does_not_grow_with_samples(C, G, dtype):
     sizes = [hq.hqml_norm_workspace_bytes(hq.make_norm_config(C, G, rows, dtype=dtype)) for rows in (1 << 10, 1 << 20, 1 << 30)]
     most = max(2048 * (4 * (2 * C + 4 * G) + 128), 64 << 20) + 768
     assert 0 < sizes[0] <= sizes[1] <= sizes[2] <= most
+
+
+def test_muon_border_of_long_matrices():
+    """As the header has it: 14,336 values take no workspace with any number of steps, longer matrices of up to 64 on one side
+    little with up to six of the usual steps, and a larger matrix's with more, unless a compute unit holds them."""
+    _lib()
+
+    def need(rows, cols, steps):
+        t = (hq.hqml_muon_tensor * 1)(hq.hqml_muon_tensor(None, None, None, rows, cols, 1.0))
+        return hq.hqml_muon_workspace_bytes(_muon(param_dtype=1, steps=steps), 1, t)
+
+    for steps in (1, 6, 7, 100):
+        assert need(64, 224, steps) == 0 and need(224, 64, steps) == 0
+    for rows, cols in ((64, 5000), (5000, 50), (16, 16384)):
+        assert 0 < need(rows, cols, 1) == need(rows, cols, 6) < 4 << 20
+        assert need(rows, cols, 7) > 64 << 20
+    assert need(40, 300, 6) > 0 and need(40, 300, 7) == 0
