@@ -342,10 +342,10 @@ const char *hqml_dense8_last_error(const hqml_dense8 *h);
 
 /* y = alpha act(x w^T + bias) + residual with x rounded to codes for each row and w given as
  * codes [N][K] with row stride ldw as hqml_quantise_rows takes it (what its rows hold past K does
- * not count, up to the next multiple of 16 it is read) and scales [N] (at least 2^-100, as it gives them;
- * below, results lose bits).  A product of scales may leave fp32's range where a result does not.  Everything else as
- * hqml_dense_forward; there is no gradient.  Sums of products of codes are exact.  A row of
- * x that is not finite gives a row of NaN. */
+ * not count, up to the next multiple of 16 it is read) and scales [N] (at least 2^-100, as it gives
+ * them; below, results lose bits).  Everything else as hqml_dense_forward; there is no gradient.
+ * Sums of products of codes are exact, and a product of two scales may leave fp32's range where the
+ * result does not.  A row of x that is not finite gives a row of NaN. */
 int hqml_dense8_forward(hqml_dense8 *h, int M, const void *x, long long ldx, const signed char *codes,
                         long long ldw, const float *scales, const void *bias, const void *residual,
                         long long ldr, void *y, long long ldy);
@@ -419,22 +419,21 @@ typedef struct {
     int precise;       /* nonzero: bf16 parameters' products of two fp16 values an operand, as fp32 ones' */
 } hqml_muon_config;
 
-/* Device bytes that hqml_muon_step needs at `workspace` (256-byte aligned).  Host-only; looks at the
- * matrices' sizes alone.  Returns 0 for invalid arguments and where nothing is needed. */
+/* Device bytes that hqml_muon_step needs at `workspace` (256-byte aligned).  Host-only; of the matrices it
+ * looks at their sizes alone.  Returns 0 for invalid arguments and where nothing is needed. */
 size_t hqml_muon_workspace_bytes(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors);
 
 /* One step over n_tensors matrices (mu = momentum):
  *   m = mu m + (1 - mu) g,  u = nesterov ? mu m + (1 - mu) g : m,  X = u / max(|u|, eps) (Frobenius norm);
  *   `steps` times, with A = X X^T:  X = a X + (b A + c A^2) X;  p = p (1 - lr weight_decay) - lr f X
  * m in fp32.  The products take operands in fp16, sums in fp32: two for each value (22 bits), X then off by
- * some 2e-6 of its size, or, for bf16 parameters with precise == 0, one (11 bits): a third of the time and half of the workspace,
- * and X off by 1.5e-3, where a gradient has few directions by up to 4e-2; values of X, A or b A + c A^2 beyond 63
- * become infinite (with coefficients that bring singular values near 1 they stay below 4).  Matrices
- * with a side of up to 64 are multiplied in fp32 or fp64 instead: those of up to 14,336 values always, longer ones
+ * some 2e-6 of its size, 3e-5 where a gradient has few directions (as in 32 bits throughout); or, for bf16 parameters
+ * with precise == 0, one (11 bits): a third of the time and half of the workspace, and X off by 1.5e-3 and 4e-2.  Values of
+ * X, A or b A + c A^2 beyond 63 become infinite (with coefficients that bring singular values near 1 they stay below 4).
+ * Matrices with a side of up to 64 are multiplied in fp32 or fp64 instead: those of up to 14,336 values always, longer ones
  * as far as an error of A grows by less than 2^22 over the steps (six of the usual ones); with more steps only those that a
- * compute unit holds, the others as larger matrices.  Matrices and workspace
- * must not overlap (HQML_ERR_ARG), but gradients may be shared.  The workspace is used until the step has run.
- * Errors: hqml_last_error(NULL). */
+ * compute unit holds, the others as larger matrices.  Matrices and workspace must not overlap (HQML_ERR_ARG), but gradients
+ * may be shared.  The workspace is used until the step has run.  Errors: hqml_last_error(NULL). */
 int hqml_muon_step(const hqml_muon_config *cfg, int n_tensors, const hqml_muon_tensor *tensors,
                    void *workspace, size_t workspace_bytes);
 

@@ -166,7 +166,8 @@ __device__ __forceinline__ u32x4 codes16(const Sixteen<T> &v, const RowScale &s)
 constexpr int kHeld = 4;   // sixteens of a thread that stay in registers between the two passes over a row
 
 // kWaves waves a row, 4 / kWaves rows a workgroup; the codes' rows end with zeros.  A row stays in registers between the pass that
-// finds its scale and the one that forms its codes.  Bound by memory: 8192 x 4096 bf16 24 us, 4.2 TB/s.
+// finds its scale and the one that forms its codes.  Bound by memory: 8192 x 4096 fp32 31 us, 5.5 TB/s; bf16 24 us, 4.2 TB/s, with
+// arithmetic nearly as long.
 template <typename T, int kWaves>
 __global__ __launch_bounds__(256) void k_quantise(const T *x, long long ldx, long long rows, int K, int8_t *codes, long long ldc,
                                                   float *scales)
@@ -287,7 +288,7 @@ __device__ __forceinline__ void scaled(f32x4 (&to)[FI][FJ], const i32x4 (&acc)[F
 
 // Larger products: the dense layer's tiles and choice of them (at twice the k of a bf16 tile), split along k where they are few.
 // Bound by the matrix instructions, half of the compute units' busy cycles, and the epilogue's memory, in bursts between them:
-// 8192 x 4096 x 4096 bf16 with gelu and residual 150 to 162 us, 1,700 to 1,830 TOP/s; a library's bare product takes 131.
+// 8192 x 4096 x 4096 bf16 with gelu and residual 149 to 162 us, 1,700 to 1,840 TOP/s; a library's bare product takes 131.
 template <typename T, int BM, int BN, int WI, int WJ>
 __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product8(Args P, Scales8 q)
 {
@@ -313,7 +314,7 @@ __global__ __launch_bounds__(64 * WI *WJ, 2) void k_product8(Args P, Scales8 q)
 }
 
 // Few rows of x: tiles of 16 FI x 16, codes of w straight from memory as k_small_forward's, x's codes from the workspace.  Bound by
-// latency: 45 x 1531 -> 803 fp32 5.3 us, behind 3.7 for the codes.
+// latency: 45 x 1531 -> 803 fp32 5.4 us, behind 3.8 for the codes.
 template <typename T, int FI>
 __global__ __launch_bounds__(FI == 1 ? 1024 : 512) void k_small8(Args P, Scales8 q)
 {
@@ -356,7 +357,7 @@ __host__ __device__ inline int own_pitch(int pairs) { return pairs * 2 + 16; }
 __host__ __device__ inline int own_bytes(int rows, int pairs) { return rows * own_pitch(pairs) + 64; }
 
 // As k_small8<T, 1>, and every workgroup rounds its tile's rows of x by itself, while its first codes of w are under way: one launch
-// instead of two.  P.a: x.  784 -> 20 4.3 us, launched by two 12; 4096 -> 4096 8.5 us (16.8 MB of codes), 12.1 by two.
+// instead of two.  P.a: x.  784 -> 20 4.2 us, launched by two 12; 4096 -> 4096 8.6 us (16.8 MB of codes), 12.1 by two.
 template <typename T>
 __global__ __launch_bounds__(1024) void k_small8_own(Args P, Scales8 q, int K)
 {

@@ -9,17 +9,18 @@
 // cores, of operands in fp16 (products exact, sums in fp32):
 //   two values for each, x = hi + lo, 22 bits; of their four products the three that count, one after the other along k
 //   one value for each, 11 bits, where the caller of bf16 parameters (`precise` 0) takes that: a third of the products
-// With two, X is as exact as fp32 sums leave it (1e-6 to 2e-6 of its size after five steps).  With one it is off by 1.5e-3, and by 4e-2
-// where a gradient has few directions: roundings fill the others, and each step lifts those by a = 3.4.  A bf16 parameter's own
-// rounding hides such errors in one step, but not in the sum of many.
+// With two, X is as exact as 32 bits make it: off by 1e-6 to 2e-6 of its size after five steps, and by 2e-5 to 3e-5 where a gradient
+// has few directions (8 in 512 x 2048; the steps in fp32 throughout 4e-6 and 3e-5 to 5e-5): roundings fill the others, and each step
+// lifts those by a = 3.4.  With one it is off by 1.5e-3 and 4e-2.  A bf16 parameter's own rounding hides such errors in one step, but
+// not in the sum of many.
 // X's values are at most a little over 1 and often small, so X, A and B = b A + c A^2 are held times 2^10: fp16's normal range then
 // goes from 2^-24 to 64 of them.
 //
 // All larger matrices of a call go through each product in one launch, a workgroup a tile (or a part of one along k).  Bound by the
-// matrix instructions (two 4096 x 4096 of one value, a step: X X^T 150 us, b A + c A^2 157, X 238, 1,160 TFLOP/s in the last; of
-// two, 8.3 ms for 2.8 in all; two 1024 x 4096 of two: 41, 19 and 57, 900 fp16 TFLOP/s in the last), below some 800 x 800 by the launches and the steps' latency
-// (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all steps (three 64 x 32 14.5 us for 76), thin ones
-// three.
+// matrix instructions (two 4096 x 4096 bf16, a step, of two values: X X^T 452 us, b A + c A^2 452, X 742, 1,110 fp16 TFLOP/s in the
+// last; of one: 150, 157 and 238, 1,160; two 1024 x 4096 fp32: 41, 19 and 58, 890 in the last), below some 800 x 800 by the launches
+// and the steps' latency (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all steps (three 64 x 32 14.2 us
+// for 76), thin ones three.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

@@ -9,12 +9,12 @@
 // stays by channel, and groups of any size are put together from channels in LDS.
 //   k_resident_*  a workgroup holds all positions of a sample and some whole groups in registers: x is read once, and the
 //                 variance is formed of what is left after the mean.  Small samples share a workgroup.  Bound by latency
-//                 (a load, two reductions with barriers, a store): 784 x 32 fp32 6.6 us, 1000 x 784 fp32 9.6 forward and
-//                 10 + 4 backward.
+//                 (a load, two reductions with barriers, a store): 784 x 32 fp32 7.7 us (6.6 at least), 1000 x 784 fp32 9.5
+//                 forward and 10.2 + 3.9 backward.
 //   k_stats, k_sums with k_apply_*  larger samples: workgroups take chunks of positions; the last one of a sample to finish puts
 //                 the chunks' statistics together (in their order, so no result depends on timing), and a second kernel reads
 //                 x again, in the opposite order, to find its end still in the last-level cache.  32 x 4096 x 512 bf16,
-//                 silu: statistics 30 us (4.5 TB/s), forward 46 (5.8), sums 62 (4.3; arithmetic takes 59 % of their
+//                 silu: statistics 30 us (4.5 TB/s), forward 47 (5.7), sums 64 (4.2; arithmetic takes 59 % of their
 //                 busy cycles), backward 70 (5.7).
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -213,11 +213,11 @@ class Muon(torch.optim.Optimizer):
     with (a, b, c) = coefficients.  f by `adjust`: "spectral", sqrt(max(1, rows / cols)); "rms", 0.2 sqrt(max(rows,
     cols)), which gives updates the size of AdamW's; "none", 1.  Parameters: contiguous CUDA matrices in fp32 or bf16
     (vectors, angles and the like are AdamW's); a gradient may be bf16 for an fp32 parameter and the other way round.
-    state[p]["momentum"] is m, in fp32.  X is as exact as sums in 32 bits leave it, some 2e-6 of its size.  half=True: the
-    products of bf16 parameters take operands of 11 bits instead of 22, in a third of the time; X is then off by 1.5e-3 of its
-    size, by up to 4e-2 where a gradient has few directions (a small batch's).  Matrices of up to 64 on one side take 24 bits or
-    more either way, long ones of them with up to six steps of these coefficients.  The step runs on each device's current stream and can be captured into a graph,
-    which then repeats it with the lr it was captured with."""
+    state[p]["momentum"] is m, in fp32.  X is as exact as 32 bits make it: off by some 2e-6 of its size, by 3e-5 where a gradient
+    has few directions (a small batch's).  half=True: the products of bf16 parameters take operands of 11 bits instead of 22, in a
+    third of the time; X is then off by 1.5e-3 and 4e-2.  Matrices of up to 64 on one side take 24 bits or more either way, long
+    ones of them with up to six steps of these coefficients.  The step runs on each device's current stream and can be captured
+    into a graph, which then repeats it with the lr it was captured with."""
 
     def __init__(self, params, lr=0.02, momentum=0.95, weight_decay=0.0, nesterov=True,
                  coefficients=(3.4445, -4.7750, 2.0315), steps=5, eps=1e-7, adjust="spectral", half=False):

@@ -352,3 +352,24 @@ def test_scales_of_any_size(M, K, N, sx, sw):
     assert y[above].isinf().all() and (torch.sign(y[above]) == torch.sign(value[above])).all()
     off = (y.double() - value).abs() - bound - 2.0 ** -150
     assert float(off[below].max()) <= 0
+
+
+@pytest.mark.parametrize("M,K,N", [(1, 784, 20), (45, 1531, 803), (2100, 640, 2060)])
+@pytest.mark.parametrize("sx,sw", [(1e-20, 1e-20), (1e30, 1e-28), (1e22, 1e15)])
+def test_scales_of_any_size_in_bf16(M, K, N, sx, sw):
+    """With bias, activation and residual.  Half a unit of bf16's smallest numbers is 2^-134; results above the largest, 3.39e38, are
+    infinite (1e37 times the square root of 784 is 2.8e38: some of the last sizes'), and so is, in 32 bits, a sum or a z above it
+    whose residual would bring it back: where act(z) is above 0.85 of it (a bias is up to 0.13 of it here), either may be."""
+    import qml_gradients_amd as hq
+    x, w = scaled_rows(M, K, sx, 1).bfloat16(), scaled_rows(N, K, sw, 2)
+    bias, residual = (scaled_rows(1, N, sx * sw, 3)[0]).bfloat16(), scaled_rows(M, N, sx * sw, 4).bfloat16()
+    codes, scales = hq.quantise_rows(w)
+    for act in ("none", "relu"):
+        y = hq.DenseInt8(K, N, M, dtype="bf16", activation=act).forward(x, codes, scales, bias, residual)
+        value, bound = dense8(x, codes, scales, bias, residual, act, 1.0, "bf16")
+        top = torch.finfo(torch.bfloat16).max
+        above, below = value.abs() > 1.01 * top, value.abs() < 0.99 * top
+        assert y[above].isinf().all() and (torch.sign(y[above]) == torch.sign(value[above])).all()
+        below &= (value - residual.double()).abs() < 0.85 * top
+        off = (y.double() - value).abs() - bound - 2.0 ** -134
+        assert float(off[below].max()) <= 0 and float(bias.abs().max()) < 0.13 * top

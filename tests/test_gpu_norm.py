@@ -365,3 +365,34 @@ def test_least_eps_of_constant_groups(S):
     # the mean's sum, 708 E of the magnitudes' mean, and 8 E of the terms
     assert float((dx.double() - want).abs().max()) <= size * 2.0 ** -24 * (708 + 8 * 6) and not dw.any()
     assert float((db.double() - dy.double().sum((0, 1))).abs().max()) <= 708 * 2.0 ** -24 * float(dy.abs().sum((0, 1)).max())
+
+
+def test_more_samples_than_a_launch_takes():
+    """Small samples whose sums of parameters take two launches."""
+    check(66000, 1, 3000, 10, "fp32", "tanh")
+
+
+def test_rounds_in_place_and_captured():
+    """Samples in rounds: in place, and in a graph that is replayed with other data."""
+    import qml_gradients_amd as hq
+    B, S, C, G = 2100, 5, 4096, 8
+    own, side = torch.cuda.Stream(), torch.cuda.Stream()
+    layer = hq.GroupNorm(C, G, B * S, dtype="bf16", activation="gelu", stream=own.cuda_stream)
+    x, dy, gamma, beta = make(B, S, C, "bf16", 1)
+    y = layer.forward(x, gamma, beta)
+    same = x.clone()
+    assert layer.forward(same, gamma, beta, out=same) is same and torch.equal(same, y)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        y, mean, rstd = layer.forward_train(x, gamma, beta)
+        held = (y, *layer.backward(dy, x, gamma, beta, mean, rstd))
+    for seed in (2, 3, 4):
+        for t, new in zip((x, dy, gamma, beta), make(B, S, C, "bf16", seed)):
+            t.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        now = [t.clone() for t in held]
+        y, mean, rstd = layer.forward_train(x, gamma, beta)
+        assert all(torch.equal(a, b) for a, b in zip(now, (y, *layer.backward(dy, x, gamma, beta, mean, rstd))))
+        torch.cuda.synchronize()
