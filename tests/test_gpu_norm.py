@@ -396,3 +396,17 @@ def test_rounds_in_place_and_captured():
         y, mean, rstd = layer.forward_train(x, gamma, beta)
         assert all(torch.equal(a, b) for a, b in zip(now, (y, *layer.backward(dy, x, gamma, beta, mean, rstd))))
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("value", [1.8811031579971313, 1.0028703212738037, 1.5920419692993164])
+def test_sums_of_many_samples_that_are_split(value):
+    """As test_long_sums, of 180,000 samples: what they leave is added in chains below 400 too."""
+    import qml_gradients_amd as hq
+    B, S, C = 180000, 700, 24
+    x, dy = torch.ones(B, S, C, device="cuda"), torch.full((B, S, C), value, device="cuda")
+    mean, rstd = torch.zeros(B, 1, device="cuda"), torch.ones(B, 1, device="cuda")
+    _, dw, db = hq.GroupNorm(C, 1, B * S).backward(dy, x, None, None, mean, rstd, input=False)
+    for t in (dw, db):
+        off = float((t.double() / (value * B * S) - 1).abs().max())
+        say(f"[gpu] sums of {B} x {S} x {C}: off {off:.2e}")
+        assert off < 400 * 2.0 ** -24
