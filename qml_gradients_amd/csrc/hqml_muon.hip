@@ -17,8 +17,8 @@
 // goes from 2^-24 to 64 of them.
 //
 // All larger matrices of a call go through each product in one launch, a workgroup a tile (or a part of one along k).  Bound by the
-// matrix instructions (two 4096 x 4096 bf16, a step, of two values: X X^T 452 us, b A + c A^2 452, X 742, 1,110 fp16 TFLOP/s in the
-// last; of one: 150, 157 and 238, 1,160; two 1024 x 4096 fp32: 41, 19 and 58, 890 in the last), below some 800 x 800 by the launches
+// matrix instructions (two 4096 x 4096 bf16, a step, of two values: X X^T 452 us, b A + c A^2 453, X 750, 1,100 fp16 TFLOP/s in the
+// last; of one: 154, 160 and 243, 1,130; two 1024 x 4096 fp32: 41, 19 and 58, 890 in the last), below some 800 x 800 by the launches
 // and the steps' latency (four 803 x 517 fp32: 16, 12 and 20).  Small matrices take one launch for all steps (three 64 x 32 14.2 us
 // for 76), thin ones three.
 #include <hip/hip_runtime.h>
